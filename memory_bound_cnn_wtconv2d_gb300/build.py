@@ -20,7 +20,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
 SOURCES = ("wtconv_api.cu", "wtconv_fwd.cu", "wtconv_fwd_win.cu", "wtconv_bwd_weight.cu", "wtconv_bwd_weight_win.cu",
-           "wtconv_bwd_fused.cu", "wtconv_noalloc.cu", "wtconv_split.cu")
+           "wtconv_bwd_fused.cu", "wtconv_noalloc.cu", "wtconv_split.cu",
+           # the operators around the layer (include/wtconv_block.h)
+           "block/block_api.cu", "block/gn.cu", "block/ns.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 
@@ -34,7 +36,8 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    for d in (CSRC, os.path.join(CSRC, "block")):
+        files += glob.glob(os.path.join(d, "*.h")) + glob.glob(os.path.join(d, "*.cuh"))
     files += glob.glob(os.path.join(INCLUDE, "*.h"))
     return files
 
@@ -53,7 +56,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     cc = nvcc()
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
         cmd = [cc, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:

@@ -1,0 +1,46 @@
+// Internal launchers of the operators around the layer (host side).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "../../../include/wtconv_block.h"
+
+namespace wtb {
+
+struct GnPlan {
+  int vec;        // elements of one access (a divisor of C; 16 bytes where alignment allows)
+  int tx, ty;     // threads over channel vectors and over rows
+  int splits;     // row ranges of one sample, one CTA each
+  int rows;       // rows of one range
+  size_t ws_bytes;
+};
+
+// Plan of one call; `align` is the number of elements that every pointer and
+// stride involved is a multiple of (capped at 16 bytes).
+GnPlan gn_plan(const wtconv_gn_desc_t& d, int op, int align);
+cudaError_t gn_launch_fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const float* w, const float* b,
+                          void* y, float* mean, float* rstd, void* ws, cudaStream_t s);
+cudaError_t gn_launch_bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, const void* x,
+                          const float* mean, const float* rstd, const float* w, const float* b, void* dx, float* dw,
+                          float* db, void* ws, cudaStream_t s);
+
+// Host pointer arrays of one Newton-Schulz call, passed to kernels by value.
+struct NsPointers {
+  const void* grad[WTCONV_NS_MAX_COUNT];
+  void* out[WTCONV_NS_MAX_COUNT];      // orthogonalize: the result; optimiser step: the weight
+  float* momentum[WTCONV_NS_MAX_COUNT];
+};
+
+struct NsCall {
+  long long g_ld, out_ld, m_ld;
+  float mu, decay, rate;
+  int nesterov;
+  int muon;  // 1: optimiser step, 0: orthogonalize
+};
+
+size_t ns_workspace(const wtconv_ns_desc_t& d);
+cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& c, const NsPointers& p, void* ws, cudaStream_t s);
+unsigned int ns_take_faults();
+
+}  // namespace wtb

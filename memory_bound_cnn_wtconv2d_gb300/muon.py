@@ -1,0 +1,72 @@
+"""An optimiser for the matrices of a block: momentum, then an orthogonalised
+direction (Newton-Schulz), then a decayed weight update, in one call per shape.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import blockops as _b
+
+
+def shape_scale(m: int, n: int, rule: str = "spectral") -> float:
+    """Factor on the learning rate of an m x n matrix: "spectral" keeps the size
+    of the change that the matrix makes to its output, max(1, m / n) ** 0.5;
+    "rms" gives every update the root mean square 0.2, 0.2 * max(m, n) ** 0.5."""
+    if rule == "spectral":
+        return math.sqrt(max(1.0, m / n))
+    if rule == "rms":
+        return 0.2 * math.sqrt(max(m, n))
+    raise ValueError(f"scale rule must be spectral or rms, got {rule!r}")
+
+
+class Muon(torch.optim.Optimizer):
+    """Momentum with orthogonalised updates, for parameters that are matrices.
+
+    A parameter of more than two axes (a pointwise convolution's [O, I, 1, 1])
+    is taken as a matrix of its first axis by all the others.  Parameters of
+    one shape and type take their step in one call.  Other parameters (norms,
+    biases, depthwise kernels) belong to another optimiser.
+    """
+
+    def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, steps: int = 5, coefficients=_b.NS_COEFFICIENTS, eps: float = 1e-7,
+                 scale: str = "spectral"):
+        if not (lr >= 0 and 0 <= momentum < 1 and weight_decay >= 0):
+            raise ValueError("lr and weight_decay must not be negative, momentum must be in [0, 1)")
+        shape_scale(1, 1, scale)
+        super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay,
+                                      steps=steps, coefficients=tuple(coefficients), eps=eps, scale=scale))
+        for group in self.param_groups:
+            for p in group["params"]:
+                if p.dim() < 2:
+                    raise ValueError(f"Muon takes matrices, got a parameter of shape {tuple(p.shape)}")
+                if not p.is_contiguous():
+                    raise ValueError("Muon takes contiguous parameters")
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            stacks = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                state = self.state[p]
+                if not state:
+                    state["buffer"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                rows = p.shape[0]
+                w, b = p.view(rows, -1), state["buffer"].view(rows, -1)
+                g = p.grad.reshape(rows, -1)
+                g = (g if g.is_contiguous() else g.contiguous()).to(p.dtype)
+                stacks.setdefault((tuple(w.shape), p.dtype, p.device), []).append((w, g, b))
+            for (shape, _, _), entries in stacks.items():
+                w, g, b = zip(*entries)
+                _b.wtconv_muon_step(w, g, b, lr=group["lr"], momentum=group["momentum"], nesterov=group["nesterov"],
+                                    weight_decay=group["weight_decay"], scale=shape_scale(*shape, group["scale"]),
+                                    steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
+        return loss

@@ -95,9 +95,9 @@ size_t wtconv_ns_workspace_size(const wtconv_ns_desc_t* desc);
  * m > n, then `steps` times
  *     A = X X^T,  X <- a X + (b A + c A A) X,
  * written to out (transposed back) in desc->dtype.  g and out are HOST arrays
- * of count device pointers, read during the call.  float16 and bfloat16
- * stacks are computed with operands rounded to 11 significand bits and
- * float32 accumulation, float32 stacks with operands of 22 bits. */
+ * of count device pointers, read during the call.  The products take operands
+ * of 11 significand bits for bfloat16 stacks and of 22 bits for float16 and
+ * float32 stacks, with float32 accumulation. */
 wtconv_status_t wtconv_orthogonalize(const wtconv_ns_desc_t* desc, const void* const* g, long long g_ld,
                                      void* const* out, long long out_ld, void* ws, size_t ws_bytes,
                                      void* stream);

@@ -1,18 +1,78 @@
-// Newton-Schulz orthogonalisation and the optimiser step around it, in plain
-// float32 products.
+// Newton-Schulz orthogonalisation and the optimiser step around it.
+//
+//   X = g / (|g| + eps)  (r x c, r <= c);  steps times:
+//     A = X X^T,  B = b A + c A A,  X <- a X + B X
+//
+// Two launches: ns_norm updates the momentum and adds up squares, then one
+// cooperative kernel runs everything else, its CTAs meeting at a barrier
+// between the products (a launch per product costs the host more than the
+// small products take).  The products run on tcgen05 with float32
+// accumulators in TMEM.
+//
+// Number formats.  Operands are float16 with power-of-two scales that put
+// their entries near 1: 11 significand bits instead of bfloat16's 8, and
+// nothing is lost to the range because |X| <= 1.3 is known.  X itself is kept
+// as a pair hi + lo (22 bits): the term a X carries the small singular values,
+// which five steps amplify up to 485 times, and rounding X to 11 bits each
+// step leaves several per cent on them; the products only see hi.  The
+// diagonals of A and of a I + B never enter an operand: they are kept in
+// float32 (da, db) and multiplied in the epilogues, so that the operands'
+// rounding counts relative to the spread of the singular values only (0.4e-3
+// instead of 1.7e-3 on the result of a random 96 x 384 matrix).  That serves
+// bfloat16 stacks.  Types of more bits, and matrices of fewer than 16 rows,
+// whose few roundings do not average out, keep pairs for A and B too and add
+// the products lo hi + hi lo + hi hi (`split`).  The tensor core's additions
+// truncate, some 2^-22 of the sum each; `split` spreads the sum over kSegments
+// accumulators, which the epilogue adds, to keep that below 1e-5.
+//
+// Layout.  Every matrix lies in the workspace as 64 x 64 sub-blocks whose 8 KB
+// are the 128-byte-swizzled image that the tensor core reads, so that an
+// operand tile is one or a few contiguous bulk copies, results leave by the
+// same route, and padding needs no bounds (rows to 128, columns to 64, zero).
+// A and B are symmetric: only sub-blocks on and below the diagonal blocks are
+// computed and stored, and a tile above is read from its mirror image with
+// the other operand order (MN-major), which costs nothing.
 #include "block_device.cuh"
 #include "block_launch.h"
+#include "tc_device.cuh"
 #include "../wtconv_launch.h"
 
 namespace wtb {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kNormCtas = 64;  // partial sums of squares per matrix
+constexpr int kNormThreads = 256;
+constexpr int kNormCtas = 64;      // partial sums of squares per matrix
+constexpr int kThreads = 256;      // 0: copies, 1: MMAs, 4-7: epilogue
+constexpr int kSub = 8192;         // bytes of a 64 x 64 sub-block
+constexpr int kStages = 3;
+constexpr int kMaxNb = 4;          // sub-blocks across a tile
+constexpr int kSegments = 4;       // accumulators of one tile when split
+constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
+constexpr int kStageBytes = (2 + kMaxNb) * kSub;
+constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
+constexpr int kSmem = kStages * kStageBytes + 2 * kEpiBytes + 1024;
+constexpr long long kWaitCycles = 1ll << 31;  // about a second
+
+static __device__ unsigned int g_ns_faults;
 
 struct NsShape {
   int m, n, r, c, tall, count;
   float eps;
+};
+
+struct NsMain {
+  NsShape s;
+  int rb, cb, rk;            // sub-blocks: rows (even), columns, rows that hold data
+  int steps, split;
+  int nb1, nb2, nb3, gsh;    // tile widths of the three products; log2 of the stored diagonal block
+  int t1, t2, t3;            // tiles of one matrix in each product
+  float ca, cb_, cc;         // coefficients
+  float sx, sa;              // scales of X and of A, B
+  unsigned char *xh[2], *xl[2], *ah, *al, *bh, *bl;
+  float *da, *db;            // diagonals of A and a I + B, in the images' scale
+  long long xbytes, abytes;  // of one matrix
+  unsigned int* sync;        // barrier count, abort flag
+  const float* part;
 };
 
 template <typename T>
@@ -29,14 +89,16 @@ __device__ __forceinline__ float direction(const NsCall& k, const NsPointers& p,
   return k.nesterov ? fmaf(k.mu, mo, (1.f - k.mu) * g) : mo;
 }
 
-// Updates the momentum and adds up squares of the direction.
+// Updates the momentum, adds up squares of the direction, clears the barrier.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) ns_norm(NsShape s, NsCall k, NsPointers p, float* __restrict__ part) {
-  __shared__ float sh[kThreads / 32];
+__global__ void __launch_bounds__(kNormThreads)
+ns_norm(NsShape s, NsCall k, const __grid_constant__ NsPointers p, float* __restrict__ part, unsigned int* sync) {
+  __shared__ float sh[kNormThreads / 32];
   const int i = blockIdx.y;
+  if (i == 0 && blockIdx.x == 0 && threadIdx.x < 2) sync[threadIdx.x] = 0;
   const long long total = (long long)s.m * s.n;
   float q = 0.f;
-  for (long long j = blockIdx.x * kThreads + threadIdx.x; j < total; j += (long long)kNormCtas * kThreads) {
+  for (long long j = blockIdx.x * kNormThreads + threadIdx.x; j < total; j += (long long)kNormCtas * kNormThreads) {
     const float u = direction<T>(k, p, i, j / s.n, (int)(j % s.n), true);
     q = fmaf(u, u, q);
   }
@@ -45,112 +107,599 @@ __global__ void __launch_bounds__(kThreads) ns_norm(NsShape s, NsCall k, NsPoint
   __syncthreads();
   if (threadIdx.x == 0) {
     float t = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
+    for (int w = 0; w < kNormThreads / 32; ++w) t += sh[w];
     part[i * kNormCtas + blockIdx.x] = t;
   }
 }
 
-// X = direction / (norm + eps), wide orientation
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-ns_init(NsShape s, NsCall k, NsPointers p, const float* __restrict__ part, float* __restrict__ X) {
-  const int i = blockIdx.y;
-  float q = 0.f;
-  for (int j = 0; j < kNormCtas; ++j) q += part[i * kNormCtas + j];
-  const float norm = sqrtf(q) + s.eps;
-  const long long total = (long long)s.m * s.n;
-  for (long long j = (long long)blockIdx.x * kThreads + threadIdx.x; j < total; j += (long long)gridDim.x * kThreads) {
-    const long long row = j / s.n;
-    const int col = (int)(j % s.n);
-    const float v = direction<T>(k, p, i, row, col, false) / norm;
-    X[(long long)i * total + (s.tall ? (long long)col * s.c + row : row * s.c + col)] = v;
+// ---------------------------------------------------------------------------
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], epi[2], drain;
+  float dcol[kMaxNb * 64];  // product 2: A's diagonal at the tile's columns
+  uint32_t tmem;
+  volatile int dead;  // a wait gave up: every role leaves
+};
+
+// Waits for a phase of an mbarrier; false when it gave up.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_addr(bar);
+  if (mbar_try(a, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(a, parity)) {
+    if (sh.dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      sh.dead = 1;
+      atomicAdd(&g_ns_faults, 1u);
+      return false;
+    }
   }
+  return true;
 }
 
-// out = alpha P Q + beta R: P [M,K], Q read as Q[k * qk + col * qc], out and R [M,Nc]
-__global__ void __launch_bounds__(kThreads)
-ns_gemm(int M, int Nc, int K, const float* __restrict__ P, long long pb, const float* __restrict__ Q, long long qb,
-        long long qk, long long qc, const float* __restrict__ R, float* __restrict__ out, float alpha, float beta) {
-  __shared__ float ps[16][65], qs[16][65];
-  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64, tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
-  P += blockIdx.z * pb;
-  Q += blockIdx.z * qb;
-  const long long ob = (long long)blockIdx.z * M * Nc;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int j = tid; j < 1024; j += kThreads) {
-      const int r = j / 16, kk = j % 16;
-      ps[kk][r] = row0 + r < M && k0 + kk < K ? P[(long long)(row0 + r) * K + k0 + kk] : 0.f;
-      const int cq = qk == 1 ? j / 16 : j % 64, kq = qk == 1 ? j % 16 : j / 64;
-      qs[kq][cq] = col0 + cq < Nc && k0 + kq < K ? Q[(k0 + kq) * qk + (col0 + cq) * qc] : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(ps[kk][tr * 4 + a], qs[kk][tc * 4 + b], acc[a][b]);
-    __syncthreads();
-  }
-  for (int a = 0; a < 4; ++a)
-    for (int b = 0; b < 4; ++b) {
-      const int r = row0 + tr * 4 + a, c = col0 + tc * 4 + b;
-      if (r < M && c < Nc) {
-        const long long o = ob + (long long)r * Nc + c;
-        out[o] = alpha * acc[a][b] + (R ? beta * R[o] : 0.f);
+// All CTAs of the launch (co-resident by the cooperative launch) meet here.
+// `round` counts the barriers.  Everything written before is visible after,
+// to bulk copies too.
+__device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, unsigned int round) {
+  fence_async();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (sh.dead) atomicExch(sync + 1, 1u);
+    unsigned int v;
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(sync) : "memory");
+    const long long t0 = clock64();
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(sync) : "memory");
+      if (v >= round * gridDim.x) break;
+      if (clock64() - t0 > kWaitCycles) {
+        sh.dead = 1;
+        atomicAdd(&g_ns_faults, 1u);
+        atomicExch(sync + 1, 1u);
+        break;
       }
     }
+    unsigned int stop;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(sync + 1) : "memory");
+    if (stop) sh.dead = 1;
+  }
+  const bool stop_all = __syncthreads_or(threadIdx.x == 0 ? sh.dead : 0) != 0;
+  fence_async();
+  return !stop_all;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-ns_finish(NsShape s, NsCall k, NsPointers p, const float* __restrict__ X) {
-  const int i = blockIdx.y;
-  const long long total = (long long)s.m * s.n;
-  for (long long j = (long long)blockIdx.x * kThreads + threadIdx.x; j < total; j += (long long)gridDim.x * kThreads) {
-    const long long row = j / s.n;
-    const int col = (int)(j % s.n);
-    const float v = X[(long long)i * total + (s.tall ? (long long)col * s.c + row : row * s.c + col)];
-    T* o = (T*)p.out[i] + row * k.out_ld + col;
-    *o = round_to<T>(k.muon ? fmaf(k.decay, to_float<T>(*o), -k.rate * v) : v);
+struct Tile {
+  int mat, i, j, nb;  // matrix, 128-row block, first column sub-block, column sub-blocks
+};
+
+// Product 1 and 2: tiles of the stored triangle; product 3: all.
+__device__ __forceinline__ Tile tile_of(const NsMain& a, int phase, int t) {
+  Tile x;
+  const int per = phase == 0 ? a.t1 : phase == 1 ? a.t2 : a.t3;
+  const int nb = phase == 0 ? a.nb1 : phase == 1 ? a.nb2 : a.nb3;
+  x.mat = t / per;
+  t -= x.mat * per;
+  int wide;
+  if (phase == 2) {
+    const int nj = (a.cb + nb - 1) / nb;
+    x.i = t / nj;
+    x.j = t % nj * nb;
+    wide = a.cb;
+  } else {
+    x.i = 0;
+    while (true) {
+      wide = min(a.rb, (((2 * x.i) >> a.gsh) + 1) << a.gsh);
+      const int nj = (wide + nb - 1) / nb;
+      if (t < nj) break;
+      t -= nj;
+      ++x.i;
+    }
+    x.j = t * nb;
+  }
+  x.nb = min(nb, wide - x.j);
+  return x;
+}
+
+// Whether rows i.. (sub-block index) of a symmetric matrix at column sub-block
+// k are stored as such (K-major), or as their mirror image.
+__device__ __forceinline__ bool stored(const NsMain& a, int i, int k) { return (i >> a.gsh) >= (k >> a.gsh); }
+
+__device__ __forceinline__ void load_rows(uint32_t dst, const unsigned char* base, int ncols, int i, int n, int k,
+                                          uint32_t bar) {
+  for (int s = 0; s < n; ++s) bulk_load(dst + s * kSub, base + ((long long)(i + s) * ncols + k) * kSub, kSub, bar);
+}
+// n consecutive sub-blocks of one sub-block row: contiguous
+__device__ __forceinline__ void load_across(uint32_t dst, const unsigned char* base, int ncols, int k, int j, int n,
+                                            uint32_t bar) {
+  bulk_load(dst, base + ((long long)k * ncols + j) * kSub, n * kSub, bar);
+}
+__device__ __forceinline__ void load_symmetric(const NsMain& a, uint32_t dst, const unsigned char* base, int i, int n,
+                                               int k, uint32_t bar) {
+  if (stored(a, i, k)) load_rows(dst, base, a.rb, i, n, k, bar);
+  else load_across(dst, base, a.rb, k, i, n, bar);
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint4 u;
+  __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  return u;
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 
 template <typename T>
-cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
-  NsShape s;
+__global__ void __launch_bounds__(kThreads, 1)
+ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, const __grid_constant__ NsPointers ptrs) {
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  unsigned char* gen = raw + (base - smem_addr(raw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.acc_full[i]), 1);
+      mbar_init(smem_addr(&sh.acc_empty[i]), 128);
+      mbar_init(smem_addr(&sh.epi[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.drain), 1);
+    sh.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&sh.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // X = direction / (norm + eps), as sub-blocks.  Reads run along the rows of
+  // the caller's matrix, whichever way round it is; the turn is in shared memory.
+  {
+    float* tile = reinterpret_cast<float*>(gen);  // [64][65]
+    const int per = a.rb * a.cb;
+    int mat_known = -1;
+    float mul = 0.f;
+    for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
+      const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
+      if (mat != mat_known) {
+        float q = 0.f;
+        for (int j = 0; j < kNormCtas; ++j) q += a.part[mat * kNormCtas + j];
+        mul = a.sx / (sqrtf(q) + a.s.eps);
+        if (q == 0.f) mul = 0.f;
+        mat_known = mat;
+      }
+      const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
+      for (int e = tid; e < 4096; e += kThreads) {
+        const int y = e >> 6, x = e & 63;
+        float v = 0.f;
+        if (row0 + y < a.s.m && col0 + x < a.s.n) v = direction<T>(call, ptrs, mat, row0 + y, col0 + x, false) * mul;
+        tile[a.s.tall ? x * 65 + y : y * 65 + x] = v;
+      }
+      __syncthreads();
+      unsigned char* ph = a.xh[0] + mat * a.xbytes + (long long)u * kSub;
+      unsigned char* pl = a.xl[0] + mat * a.xbytes + (long long)u * kSub;
+      for (int e = tid; e < 512; e += kThreads) {
+        const int y = e >> 3, ch = e & 7;
+        float v[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = tile[y * 65 + ch * 8 + i];
+        const uint4 hi = pack8(v);
+        unpack8(hi, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[i] - w[i];
+        const int at = y * 128 + ((ch ^ (y & 7)) << 4);
+        *reinterpret_cast<uint4*>(ph + at) = hi;
+        *reinterpret_cast<uint4*>(pl + at) = pack8(w);
+      }
+      __syncthreads();
+    }
+  }
+  unsigned int round = 1;
+  bool ok = grid_barrier(sh, a.sync, round);
+
+  int stage = 0, cur = 0;
+  uint32_t ph = 0;          // copies and MMAs: parity of the stage ring
+  uint32_t accph = 0;       // accumulator sets: one parity bit each
+  uint32_t epiph = 0, nth = 0;  // epilogue: parity of each buffer's loads, sub-tiles seen
+  uint32_t fetched[2] = {0, 0};  // loads into each buffer
+  const int passes = a.split ? 3 : 1;
+  for (int step = 0; ok && step < a.steps; ++step, cur ^= 1) {
+    for (int phase = 0; ok && phase < 3; ++phase) {
+      const int tiles = a.s.count * (phase == 0 ? a.t1 : phase == 1 ? a.t2 : a.t3);
+      const int nk = phase == 0 ? a.cb : a.rk;
+      // accumulators: two sets of up to 256 columns, or one of 4 x 128
+      const int nbw = phase == 0 ? a.nb1 : phase == 1 ? a.nb2 : a.nb3;
+      const int segs = a.split ? min(kSegments, nk) : 1;
+      const uint32_t seg_cols = nbw * 64, sets = a.split && nbw == 2 ? 1 : 2;
+      uint32_t acc = 0;
+      if (warp == 0 && lane == 0) {
+        for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
+          const Tile x = tile_of(a, phase, t);
+          const long long xo = x.mat * a.xbytes, ao = x.mat * a.abytes;
+          for (int pass = 0; pass < passes && !sh.dead; ++pass) {
+            const bool alo = a.split && pass == 0, blo = a.split && pass == 1;
+            for (int k = 0; k < nk; ++k) {
+              if (!wait(sh, &sh.empty[stage], ph ^ 1)) break;
+              const uint32_t bar = smem_addr(&sh.full[stage]), da = base + stage * kStageBytes, db = da + 2 * kSub;
+              mbar_expect(bar, (2 + x.nb) * kSub);
+              if (phase == 0) {
+                load_rows(da, (alo ? a.xl : a.xh)[cur] + xo, a.cb, 2 * x.i, 2, k, bar);
+                load_rows(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, x.j, x.nb, k, bar);
+              } else if (phase == 1) {
+                load_symmetric(a, da, (alo ? a.al : a.ah) + ao, 2 * x.i, 2, k, bar);
+                load_symmetric(a, db, (blo ? a.al : a.ah) + ao, x.j, x.nb, k, bar);
+              } else {
+                load_symmetric(a, da, (alo ? a.bl : a.bh) + ao, 2 * x.i, 2, k, bar);
+                load_across(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, k, x.j, x.nb, bar);
+              }
+              if (++stage == kStages) { stage = 0; ph ^= 1; }
+            }
+          }
+        }
+      } else if (warp == 1 && lane == 0) {
+        for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
+          const Tile x = tile_of(a, phase, t);
+          if (!wait(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1)) break;
+          tc_fence_after();
+          uint32_t begun = 0;  // segments that hold a sum
+          for (int pass = 0; pass < passes && !sh.dead; ++pass) {
+            for (int k = 0; k < nk; ++k) {
+              const bool akm = phase == 0 || stored(a, 2 * x.i, k);
+              const bool bkm = phase == 0 || (phase == 1 && stored(a, x.j, k));
+              if (!wait(sh, &sh.full[stage], ph)) break;
+              tc_fence_after();
+              const uint32_t sa = base + stage * kStageBytes, sb = sa + 2 * kSub;
+              const uint32_t idesc = instr_desc(x.nb * 64, akm, bkm);
+              const uint32_t seg = pass + 1 < passes ? 0 : (uint32_t)(k * segs / nk);
+              const uint32_t d = tmem + acc * 256 + seg * seg_cols;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                mma_f16(d, operand_desc(sa + q * (akm ? 32 : 2048), akm), operand_desc(sb + q * (bkm ? 32 : 2048), bkm),
+                        idesc, begun >> seg & 1);
+                begun |= 1u << seg;
+              }
+              mma_commit(smem_addr(&sh.empty[stage]));
+              if (++stage == kStages) { stage = 0; ph ^= 1; }
+            }
+          }
+          mma_commit(smem_addr(&sh.acc_full[acc]));
+          accph ^= 1u << acc;
+          if (++acc == sets) acc = 0;
+        }
+      } else if (warp >= 4) {
+        const int row = tid - 128, sub = row >> 6, y = row & 63;
+        const bool leader = row == 0;
+        const uint32_t ebase = base + kStages * kStageBytes;
+        // what the result is added to, and where it goes
+        const unsigned char *ih, *il;
+        unsigned char *oh, *ol;
+        float fin, facc;
+        bool in, lo;
+        if (phase == 0) {
+          in = false, lo = a.split, ih = il = nullptr, oh = a.ah, ol = a.al;
+          fin = 0.f, facc = a.sa / (a.sx * a.sx);
+        } else if (phase == 1) {
+          in = true, lo = a.split, ih = a.ah, il = a.al, oh = a.bh, ol = a.bl;
+          fin = a.cb_, facc = a.cc / a.sa;
+        } else {
+          in = true, lo = true, ih = a.xh[cur], il = a.xl[cur], oh = a.xh[cur ^ 1], ol = a.xl[cur ^ 1];
+          fin = 0.f, facc = 1.f / a.sa;
+        }
+        const int ncols = phase == 2 ? a.cb : a.rb;
+        const long long obytes = phase == 2 ? a.xbytes : a.abytes;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+          if (named_or<128>(1, sh.dead != 0)) break;  // one decision for the four warps
+          const Tile x = tile_of(a, phase, t);
+          const long long mo = x.mat * obytes;
+          auto offset = [&](int s, int half) {
+            return mo + ((long long)(2 * x.i + half) * ncols + x.j + s) * kSub;
+          };
+          auto fetch = [&](int s, uint32_t b) {  // leader: the addend's sub-tile into buffer b
+            ++fetched[b];
+            const uint32_t bar = smem_addr(&sh.epi[b]), dst = ebase + b * kEpiBytes;
+            mbar_expect(bar, (lo ? 4 : 2) * kSub);
+            for (int half = 0; half < 2; ++half) {
+              bulk_load(dst + half * kSub, ih + offset(s, half), kSub, bar);
+              if (lo) bulk_load(dst + (2 + half) * kSub, il + offset(s, half), kSub, bar);
+            }
+          };
+          if (in && leader) {
+            bulk_wait_read();
+            fetch(0, nth & 1);
+          }
+          const int grow = x.i * 128 + row;  // row of the matrix
+          float diag = 0.f;
+          if (phase == 1) {
+            for (int j = row; j < x.nb * 64; j += 128) sh.dcol[j] = __ldcg(a.da + x.mat * a.rb * 64 + x.j * 64 + j);
+            diag = __ldcg(a.da + x.mat * a.rb * 64 + grow);
+          } else if (phase == 2) {
+            diag = __ldcg(a.db + x.mat * a.rb * 64 + grow);
+          }
+          const bool got = wait(sh, &sh.acc_full[acc], accph >> acc & 1);
+          __syncwarp();
+          tc_fence_after();
+          for (int s = 0; s < x.nb; ++s, ++nth) {
+            const uint32_t b = nth & 1;
+            if (leader) {
+              bulk_wait_read();  // the other buffer's last store has left it
+              if (in && s + 1 < x.nb) fetch(s + 1, b ^ 1);
+            }
+            if (in) {
+              wait(sh, &sh.epi[b], (epiph >> b) & 1);
+              epiph ^= 1u << b;
+            }
+            named_sync<128>(1);
+            unsigned char* buf = gen + kStages * kStageBytes + b * kEpiBytes + sub * kSub + y * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              const uint32_t from = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + acc * 256 + s * 64 + h * 32;
+              tmem_load32(from, v);
+              for (int g = 1; g < segs; ++g) {
+                float w[32];
+                tmem_load32(from + g * seg_cols, w);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += w[i];
+              }
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) {
+                unsigned char* p = buf + (((h * 4 + ch) ^ (y & 7)) << 4);
+                float u[8];
+                if (in) {
+                  unpack8(*reinterpret_cast<uint4*>(p), u);
+                  if (lo) {
+                    float w[8];
+                    unpack8(*reinterpret_cast<uint4*>(p + 2 * kSub), w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] += w[i];
+                  }
+                }
+                if (phase == 0) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) u[i] = facc * v[ch * 8 + i];
+                } else if (phase == 1) {
+                  // (D + A)^2 = A A + D A + A D + D D, A without its diagonal D
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    u[i] = fmaf(fin, u[i], facc * fmaf(diag + sh.dcol[s * 64 + h * 32 + ch * 8 + i], u[i], v[ch * 8 + i]));
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[ch * 8 + i]);
+                }
+                if (phase < 2 && 2 * x.i + sub == x.j + s) {  // the diagonal leaves the operand
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (h * 32 + ch * 8 + i == y) {
+                      float* d = (phase == 0 ? a.da : a.db) + x.mat * a.rb * 64 + grow;
+                      *d = phase == 0 ? u[i] : fmaf(diag, fmaf(facc, diag, fin), u[i]) + a.ca * a.sa;
+                      u[i] = 0.f;
+                    }
+                }
+                const uint4 hi = pack8(u);
+                *reinterpret_cast<uint4*>(p) = hi;
+                if (lo) {
+                  float w[8];
+                  unpack8(hi, w);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) w[i] = u[i] - w[i];
+                  *reinterpret_cast<uint4*>(p + 2 * kSub) = pack8(w);
+                }
+              }
+            }
+            fence_async_shared();
+            named_sync<128>(1);
+            if (leader && got) {
+              const uint32_t src = ebase + b * kEpiBytes;
+              for (int half = 0; half < 2; ++half) {
+                bulk_store(oh + offset(s, half), src + half * kSub, kSub);
+                if (lo) bulk_store(ol + offset(s, half), src + (2 + half) * kSub, kSub);
+              }
+              bulk_commit();
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sh.acc_empty[acc]));
+          accph ^= 1u << acc;
+          if (++acc == sets) acc = 0;
+        }
+        if (leader) bulk_wait();
+      }
+      __syncwarp();
+      ok = grid_barrier(sh, a.sync, ++round);
+    }
+  }
+  // Copies of a role that gave up: nothing may be in flight when the CTA leaves.
+  if (!ok && warp == 1 && lane == 0) {
+    mma_commit(smem_addr(&sh.drain));
+    const long long t0 = clock64();
+    while (!mbar_try(smem_addr(&sh.drain), 0) && clock64() - t0 < kWaitCycles) {
+    }
+  }
+  if (!ok && tid == 128) {
+    const long long t0 = clock64();
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t n = fetched[b];
+      while (n && !mbar_try(smem_addr(&sh.epi[b]), (n - 1) & 1) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+  }
+  if (!ok && warp == 0 && lane == 0) {
+    const long long t0 = clock64();
+    for (int i = 0; i < kStages; ++i) {
+      // stages before `stage` were filled in this turn of the ring, the others in the last
+      const uint32_t parity = i < stage ? ph : ph ^ 1;
+      while (!mbar_try(smem_addr(&sh.full[i]), parity) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+  }
+  // Back to the caller's layout.
+  if (ok) {
+    float* tile = reinterpret_cast<float*>(gen);  // [64][65]
+    const int per = a.rk * a.cb;
+    const float inv = 1.f / a.sx;
+    for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
+      const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
+      const unsigned char* ph_ = a.xh[cur] + mat * a.xbytes + (long long)u * kSub;
+      const unsigned char* pl_ = a.xl[cur] + mat * a.xbytes + (long long)u * kSub;
+      for (int e = tid; e < 512; e += kThreads) {
+        const int y = e >> 3, ch = e & 7, at = y * 128 + ((ch ^ (y & 7)) << 4);
+        float v[8], w[8];
+        unpack8(__ldcg(reinterpret_cast<const uint4*>(ph_ + at)), v);
+        unpack8(__ldcg(reinterpret_cast<const uint4*>(pl_ + at)), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = ch * 8 + i;
+          tile[a.s.tall ? q * 65 + y : y * 65 + q] = (v[i] + w[i]) * inv;
+        }
+      }
+      __syncthreads();
+      const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
+      for (int e = tid; e < 4096; e += kThreads) {
+        const int y = e >> 6, x = e & 63;
+        if (row0 + y < a.s.m && col0 + x < a.s.n) {
+          const float v = tile[y * 65 + x];
+          T* o = (T*)ptrs.out[mat] + (long long)(row0 + y) * call.out_ld + col0 + x;
+          *o = round_to<T>(call.muon ? fmaf(call.decay, to_float<T>(*o), -call.rate * v) : v);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_free(tmem, 512);
+}
+
+int ceil_log2(double v) {
+  int e = 0;
+  while ((double)(1ll << e) < v) ++e;
+  return e;
+}
+
+int sym_tiles(int rb, int nb, int gsh) {
+  int n = 0;
+  for (int i = 0; i < rb / 2; ++i) {
+    const int wide = (((2 * i) >> gsh) + 1) << gsh;
+    n += ((wide < rb ? wide : rb) + nb - 1) / nb;
+  }
+  return n;
+}
+
+// Tile widths: the least number of rounds times the cost of a tile, in cycles:
+// a K step of 64 is bound by its copies ((2 + nb) sub-blocks at 64 bytes a
+// cycle), a tile adds its start and its epilogue.
+double tile_cost(long long tiles, int sms, int nb, int nk, int passes) {
+  const double rounds = (double)((tiles + sms - 1) / sms);
+  return rounds * ((2 + nb) * 128.0 * nk * passes + 1500 + 400.0 * nb);
+}
+
+NsMain plan(const wtconv_ns_desc_t& d) {
+  NsMain a = {};
+  NsShape& s = a.s;
   s.m = d.m; s.n = d.n; s.count = d.count; s.eps = d.eps;
   s.tall = d.m > d.n;
   s.r = s.tall ? d.n : d.m;
   s.c = s.tall ? d.m : d.n;
-  const long long xx = (long long)s.r * s.c, aa = (long long)s.r * s.r;
-  float* part = (float*)ws;
-  float* X0 = part + (size_t)d.count * kNormCtas;
-  float* X1 = X0 + d.count * xx;
-  float* A = X1 + d.count * xx;
-  float* B = A + d.count * aa;
-  const dim3 g(kNormCtas, d.count);
-  ns_norm<T><<<g, kThreads, 0, st>>>(s, k, p, part);
-  ns_init<T><<<g, kThreads, 0, st>>>(s, k, p, part, X0);
-  const dim3 ga((s.r + 63) / 64, (s.r + 63) / 64, d.count), gx((s.c + 63) / 64, (s.r + 63) / 64, d.count);
-  for (int i = 0; i < d.steps; ++i) {
-    ns_gemm<<<ga, kThreads, 0, st>>>(s.r, s.r, s.c, X0, xx, X0, xx, 1, s.c, nullptr, A, 1.f, 0.f);
-    ns_gemm<<<ga, kThreads, 0, st>>>(s.r, s.r, s.r, A, aa, A, aa, 1, s.r, A, B, d.c, d.b);
-    ns_gemm<<<gx, kThreads, 0, st>>>(s.r, s.c, s.r, B, aa, X0, xx, s.c, 1, X0, X1, 1.f, d.a);
-    float* t = X0;
-    X0 = X1;
-    X1 = t;
+  a.rk = (s.r + 63) / 64;
+  a.rb = (a.rk + 1) & ~1;
+  a.cb = (s.c + 63) / 64;
+  a.steps = d.steps;
+  a.split = d.dtype != WTCONV_BF16 || s.r < 16;
+  a.ca = d.a; a.cb_ = d.b; a.cc = d.c;
+  // entries of X near 1: |X|_F is about 1 at first; those of A, B near 1 on
+  // the diagonal.  Both capped so that no entry passes float16's range.
+  int ex = (ceil_log2(s.r) + ceil_log2(s.c)) / 2, ea = ceil_log2(s.r);
+  if (ex > 12) ex = 12;
+  if (ea > 11) ea = 11;
+  a.sx = (float)(1 << ex);
+  a.sa = (float)(1 << ea);
+  a.xbytes = (long long)a.rb * a.cb * kSub;
+  a.abytes = (long long)a.rb * a.rb * kSub;
+  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
+  const int passes = a.split ? 3 : 1, most = a.split ? kSplitNb : kMaxNb;
+  double best = -1;
+  for (int gsh = 1; gsh <= 2; ++gsh) {
+    int pick[2] = {1, 1};
+    double cost = 0;
+    for (int ph = 0; ph < 2; ++ph) {
+      double b = -1;
+      for (int nb = 1; nb <= (1 << gsh) && nb <= most; nb *= 2) {
+        const double c = tile_cost((long long)d.count * sym_tiles(a.rb, nb, gsh), sms, nb, ph ? a.rk : a.cb, passes);
+        if (b < 0 || c < b) b = c, pick[ph] = nb;
+      }
+      cost += b;
+    }
+    if (best < 0 || cost < best) best = cost, a.gsh = gsh, a.nb1 = pick[0], a.nb2 = pick[1];
   }
-  ns_finish<T><<<g, kThreads, 0, st>>>(s, k, p, X0);
-  return cudaGetLastError();
+  best = -1;
+  for (int nb = 1; nb <= most; ++nb) {
+    const double c = tile_cost((long long)d.count * (a.rb / 2) * ((a.cb + nb - 1) / nb), sms, nb, a.rk, passes);
+    if (best < 0 || c < best) best = c, a.nb3 = nb;
+  }
+  a.t1 = sym_tiles(a.rb, a.nb1, a.gsh);
+  a.t2 = sym_tiles(a.rb, a.nb2, a.gsh);
+  a.t3 = (a.rb / 2) * ((a.cb + a.nb3 - 1) / a.nb3);
+  return a;
+}
+
+constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormCtas * 4;  // barrier, partial sums
+
+template <typename T>
+cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
+  NsMain a = plan(d);
+  unsigned char* w = (unsigned char*)ws;
+  a.sync = (unsigned int*)w;
+  float* part = (float*)(w + 256);
+  a.part = part;
+  w += kHead;
+  a.da = (float*)w, w += (size_t)d.count * a.rb * 256;
+  a.db = (float*)w, w += (size_t)d.count * a.rb * 256;
+  const long long xx = a.xbytes * d.count, aa = a.abytes * d.count;
+  for (int i = 0; i < 2; ++i) {
+    a.xh[i] = w, w += xx;
+    a.xl[i] = w, w += xx;
+  }
+  a.ah = w, w += aa;
+  a.bh = w, w += aa;
+  if (a.split) {
+    a.al = w, w += aa;
+    a.bl = w;
+  }
+  ns_norm<T><<<dim3(kNormCtas, d.count), kNormThreads, 0, st>>>(a.s, k, p, part, a.sync);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const void* f = (const void*)ns_main<T>;
+  e = wt::ensure_smem(f, kSmem);
+  if (e != cudaSuccess) return e;
+  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
+  long long grid = (long long)d.count * a.t3;
+  const long long others[3] = {(long long)d.count * a.t1, (long long)d.count * a.t2, (long long)d.count * a.rb * a.cb};
+  for (long long o : others) grid = o > grid ? o : grid;
+  if (grid > sms) grid = sms;
+  NsCall kc = k;
+  NsPointers pc = p;
+  void* args[3] = {&a, &kc, &pc};
+  return cudaLaunchCooperativeKernel(f, dim3((unsigned)grid), dim3(kThreads), args, kSmem, st);
 }
 
 }  // namespace
 
 size_t ns_workspace(const wtconv_ns_desc_t& d) {
-  const size_t r = d.m < d.n ? d.m : d.n, c = d.m < d.n ? d.n : d.m;
-  return (((size_t)d.count * (kNormCtas + 2 * r * c + 2 * r * r)) * 4 + 255) & ~(size_t)255;
+  const NsMain a = plan(d);
+  const size_t x = (size_t)a.xbytes * d.count, m = (size_t)a.abytes * d.count;
+  return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.split ? 4 : 2) * m;
 }
 
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t s) {
@@ -159,6 +708,11 @@ cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointe
   return launch_t<__nv_bfloat16>(d, k, p, ws, s);
 }
 
-unsigned int ns_take_faults() { return 0; }
+unsigned int ns_take_faults() {
+  unsigned int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_ns_faults, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_ns_faults, &z, sizeof(z));
+  return v;
+}
 
 }  // namespace wtb

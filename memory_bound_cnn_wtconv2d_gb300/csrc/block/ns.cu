@@ -41,22 +41,25 @@ namespace wtb {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormCtas = 64;      // partial sums of squares per matrix
-constexpr int kThreads = 256;      // 0: copies, 1: MMAs, 4-7: epilogue
+constexpr int kNormMax = 256;      // partial sums of squares per matrix, at most
+constexpr int kEpiThreads = 256;   // warps 2-9
+constexpr int kThreads = 64 + kEpiThreads;  // warp 0: copies, warp 1: MMAs
 constexpr int kSub = 8192;         // bytes of a 64 x 64 sub-block
-constexpr int kStages = 3;
+constexpr int kRing = 20;          // sub-blocks of operands in flight
+constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
 constexpr int kSegments = 4;       // accumulators of one tile when split
 constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
-constexpr int kStageBytes = (2 + kMaxNb) * kSub;
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
-constexpr int kSmem = kStages * kStageBytes + 2 * kEpiBytes + 1024;
+constexpr int kSmem = kRing * kSub + 2 * kEpiBytes + 1024;
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
 static __device__ unsigned int g_ns_faults;
 
 struct NsShape {
   int m, n, r, c, tall, count;
+  int parts;  // partial sums of squares per matrix
+  int wide;   // rows of the caller's matrices start on 16-byte boundaries
   float eps;
 };
 
@@ -75,32 +78,79 @@ struct NsMain {
   const float* part;
 };
 
+// Eight consecutive elements of a row, of which the first n exist.
 template <typename T>
-__device__ __forceinline__ float direction(const NsCall& k, const NsPointers& p, int i, long long row, int col,
-                                           bool update) {
-  const float g = to_float<T>(((const T*)p.grad[i])[row * k.g_ld + col]);
-  if (!k.muon) return g;
-  float* mp = p.momentum[i] + row * k.m_ld + col;
-  float mo = *mp;
-  if (update) {
-    mo = fmaf(k.mu, mo, (1.f - k.mu) * g);
-    *mp = mo;
+__device__ __forceinline__ void load8(const T* p, int n, bool wide, float (&v)[8]) {
+  if (wide && n >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      Vec<T, 4> a, b;
+      a.load(p), b.load(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a.e[i], v[4 + i] = b.e[i];
+    } else {
+      Vec<T, 8> a;
+      a.load(p);
+      a.widen(v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_float<T>(p[i]) : 0.f;
   }
-  return k.nesterov ? fmaf(k.mu, mo, (1.f - k.mu) * g) : mo;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, bool wide, const float (&v)[8]) {
+  if (wide && n >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      Vec<T, 8> a;
+      a.round(v);
+      a.store(p);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = round_to<T>(v[i]);
+  }
+}
+
+// Eight elements of the matrix to orthogonalise; `update` moves the momentum first.
+template <typename T>
+__device__ __forceinline__ void direction8(const NsCall& k, const NsPointers& p, bool wide, int i, long long row,
+                                           int col, int n, bool update, float (&v)[8]) {
+  load8<T>((const T*)p.grad[i] + row * k.g_ld + col, n, wide, v);
+  if (!k.muon) return;
+  float* mp = p.momentum[i] + row * k.m_ld + col;
+  float mo[8];
+  load8<float>(mp, n, wide, mo);
+  if (update) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mo[j] = fmaf(k.mu, mo[j], (1.f - k.mu) * v[j]);
+    store8<float>(mp, n, wide, mo);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = k.nesterov ? fmaf(k.mu, mo[j], (1.f - k.mu) * v[j]) : mo[j];
 }
 
 // Updates the momentum, adds up squares of the direction, clears the barrier.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads)
-ns_norm(NsShape s, NsCall k, const __grid_constant__ NsPointers p, float* __restrict__ part, unsigned int* sync) {
+ns_norm(const __grid_constant__ NsShape s, const __grid_constant__ NsCall k, const __grid_constant__ NsPointers p,
+        float* __restrict__ part, unsigned int* sync) {
   __shared__ float sh[kNormThreads / 32];
   const int i = blockIdx.y;
-  if (i == 0 && blockIdx.x == 0 && threadIdx.x < 2) sync[threadIdx.x] = 0;
-  const long long total = (long long)s.m * s.n;
+  if (i == 0 && blockIdx.x == 0 && threadIdx.x == 0) *sync = 0;
+  const unsigned int across = (s.n + 7) / 8, total = across * s.m;  // at most 2^27
   float q = 0.f;
-  for (long long j = blockIdx.x * kNormThreads + threadIdx.x; j < total; j += (long long)kNormCtas * kNormThreads) {
-    const float u = direction<T>(k, p, i, j / s.n, (int)(j % s.n), true);
-    q = fmaf(u, u, q);
+#pragma unroll 2
+  for (unsigned int j = blockIdx.x * kNormThreads + threadIdx.x; j < total; j += s.parts * kNormThreads) {
+    const unsigned int row = j / across;
+    const int col = (int)(j - row * across) * 8;
+    float v[8];
+    direction8<T>(k, p, s.wide, i, row, col, s.n - col, true, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
   }
   for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = q;
@@ -108,7 +158,7 @@ ns_norm(NsShape s, NsCall k, const __grid_constant__ NsPointers p, float* __rest
   if (threadIdx.x == 0) {
     float t = 0.f;
     for (int w = 0; w < kNormThreads / 32; ++w) t += sh[w];
-    part[i * kNormCtas + blockIdx.x] = t;
+    part[i * kNormMax + blockIdx.x] = t;
   }
 }
 
@@ -138,15 +188,16 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
 }
 
 // All CTAs of the launch (co-resident by the cooperative launch) meet here.
-// `round` counts the barriers.  Everything written before is visible after,
-// to bulk copies too.
+// `round` counts the barriers; a CTA that gave up sets the count's top bit, and
+// all leave.  Everything written before is visible after, to bulk copies too.
 __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, unsigned int round) {
+  constexpr unsigned int kStop = 1u << 31;
   fence_async();
   __syncthreads();
+  bool stop = false;
   if (threadIdx.x == 0) {
-    if (sh.dead) atomicExch(sync + 1, 1u);
+    if (sh.dead) atomicOr(sync, kStop);
     unsigned int v;
-    __threadfence();
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(sync) : "memory");
     const long long t0 = clock64();
     while (true) {
@@ -155,17 +206,16 @@ __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, uns
       if (clock64() - t0 > kWaitCycles) {
         sh.dead = 1;
         atomicAdd(&g_ns_faults, 1u);
-        atomicExch(sync + 1, 1u);
+        v = atomicOr(sync, kStop) | kStop;
         break;
       }
     }
-    unsigned int stop;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(sync + 1) : "memory");
+    stop = (v & kStop) != 0;
     if (stop) sh.dead = 1;
   }
-  const bool stop_all = __syncthreads_or(threadIdx.x == 0 ? sh.dead : 0) != 0;
-  fence_async();
-  return !stop_all;
+  stop = __syncthreads_or(stop) != 0;
+  if (threadIdx.x == 0 || threadIdx.x == 64) fence_async();  // the threads that issue bulk copies
+  return !stop;
 }
 
 struct Tile {
@@ -251,7 +301,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.acc_full[i]), 1);
-      mbar_init(smem_addr(&sh.acc_empty[i]), 128);
+      mbar_init(smem_addr(&sh.acc_empty[i]), kEpiThreads);
       mbar_init(smem_addr(&sh.epi[i]), 1);
     }
     mbar_init(smem_addr(&sh.drain), 1);
@@ -264,8 +314,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  // X = direction / (norm + eps), as sub-blocks.  Reads run along the rows of
-  // the caller's matrix, whichever way round it is; the turn is in shared memory.
+  // X = direction / (norm + eps), as sub-blocks
   {
     float* tile = reinterpret_cast<float*>(gen);  // [64][65]
     const int per = a.rb * a.cb;
@@ -273,44 +322,63 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     float mul = 0.f;
     for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
       const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
-      if (mat != mat_known) {
+      if (mat != mat_known) {  // every warp adds the partial sums in the same order
         float q = 0.f;
-        for (int j = 0; j < kNormCtas; ++j) q += a.part[mat * kNormCtas + j];
-        mul = a.sx / (sqrtf(q) + a.s.eps);
-        if (q == 0.f) mul = 0.f;
+        for (int j = lane; j < a.s.parts; j += 32) q += a.part[mat * kNormMax + j];
+        for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
+        mul = q == 0.f ? 0.f : a.sx / (sqrtf(q) + a.s.eps);
         mat_known = mat;
       }
-      const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
-      for (int e = tid; e < 4096; e += kThreads) {
-        const int y = e >> 6, x = e & 63;
-        float v = 0.f;
-        if (row0 + y < a.s.m && col0 + x < a.s.n) v = direction<T>(call, ptrs, mat, row0 + y, col0 + x, false) * mul;
-        tile[a.s.tall ? x * 65 + y : y * 65 + x] = v;
-      }
-      __syncthreads();
-      unsigned char* ph = a.xh[0] + mat * a.xbytes + (long long)u * kSub;
-      unsigned char* pl = a.xl[0] + mat * a.xbytes + (long long)u * kSub;
-      for (int e = tid; e < 512; e += kThreads) {
-        const int y = e >> 3, ch = e & 7;
-        float v[8], w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = tile[y * 65 + ch * 8 + i];
+      unsigned char* xh = a.xh[0] + mat * a.xbytes + (long long)u * kSub;
+      unsigned char* xl = a.xl[0] + mat * a.xbytes + (long long)u * kSub;
+      auto put = [&](int y, int ch, const float (&v)[8]) {
+        float w[8];
         const uint4 hi = pack8(v);
         unpack8(hi, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = v[i] - w[i];
         const int at = y * 128 + ((ch ^ (y & 7)) << 4);
-        *reinterpret_cast<uint4*>(ph + at) = hi;
-        *reinterpret_cast<uint4*>(pl + at) = pack8(w);
+        *reinterpret_cast<uint4*>(xh + at) = hi;
+        *reinterpret_cast<uint4*>(xl + at) = pack8(w);
+      };
+      // Reads run along the rows of the caller's matrix; a tall one is turned in shared memory.
+      const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
+#pragma unroll
+      for (int e0 = 0; e0 < 512; e0 += kThreads) {
+        const int e = e0 + tid;
+        if (e < 512) {
+          const int y = e >> 3, ch = e & 7, n = row0 + y < a.s.m ? a.s.n - col0 - ch * 8 : 0;
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (n > 0) direction8<T>(call, ptrs, a.s.wide, mat, row0 + y, col0 + ch * 8, n, false, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= mul;
+          if (!a.s.tall) {
+            put(y, ch, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tile[y * 65 + ch * 8 + i] = v[i];
+          }
+        }
       }
-      __syncthreads();
+      if (a.s.tall) {
+        __syncthreads();
+        for (int e = tid; e < 512; e += kThreads) {
+          const int y = e & 63, ch = e >> 6;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = tile[(ch * 8 + i) * 65 + y];
+          put(y, ch, v);
+        }
+        __syncthreads();
+      }
     }
   }
   unsigned int round = 1;
   bool ok = grid_barrier(sh, a.sync, round);
 
-  int stage = 0, cur = 0;
-  uint32_t ph = 0;          // copies and MMAs: parity of the stage ring
+  int cur = 0;
+  uint32_t ph = 0;          // copies and MMAs: one parity bit for each stage
+  uint32_t filled = 0;      // copies: stages that were ever filled
   uint32_t accph = 0;       // accumulator sets: one parity bit each
   uint32_t epiph = 0, nth = 0;  // epilogue: parity of each buffer's loads, sub-tiles seen
   uint32_t fetched[2] = {0, 0};  // loads into each buffer
@@ -324,6 +392,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       const int segs = a.split ? min(kSegments, nk) : 1;
       const uint32_t seg_cols = nbw * 64, sets = a.split && nbw == 2 ? 1 : 2;
       uint32_t acc = 0;
+      const int stage_bytes = (2 + nbw) * kSub, stages = min(kStages, kRing / (2 + nbw));
+      int stage = 0;
       if (warp == 0 && lane == 0) {
         for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
@@ -331,9 +401,10 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           for (int pass = 0; pass < passes && !sh.dead; ++pass) {
             const bool alo = a.split && pass == 0, blo = a.split && pass == 1;
             for (int k = 0; k < nk; ++k) {
-              if (!wait(sh, &sh.empty[stage], ph ^ 1)) break;
-              const uint32_t bar = smem_addr(&sh.full[stage]), da = base + stage * kStageBytes, db = da + 2 * kSub;
+              if (!wait(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1)) break;
+              const uint32_t bar = smem_addr(&sh.full[stage]), da = base + stage * stage_bytes, db = da + 2 * kSub;
               mbar_expect(bar, (2 + x.nb) * kSub);
+              filled |= 1u << stage;
               if (phase == 0) {
                 load_rows(da, (alo ? a.xl : a.xh)[cur] + xo, a.cb, 2 * x.i, 2, k, bar);
                 load_rows(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, x.j, x.nb, k, bar);
@@ -344,7 +415,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                 load_symmetric(a, da, (alo ? a.bl : a.bh) + ao, 2 * x.i, 2, k, bar);
                 load_across(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, k, x.j, x.nb, bar);
               }
-              if (++stage == kStages) { stage = 0; ph ^= 1; }
+              ph ^= 1u << stage;
+              if (++stage == stages) stage = 0;
             }
           }
         }
@@ -354,15 +426,22 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           if (!wait(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1)) break;
           tc_fence_after();
           uint32_t begun = 0;  // segments that hold a sum
+          int next = 0;        // the last pass moves to the next segment here
+          uint32_t seg = 0;
           for (int pass = 0; pass < passes && !sh.dead; ++pass) {
+            const bool last = pass + 1 == passes;
+            if (last) next = (nk + segs - 1) / segs;
             for (int k = 0; k < nk; ++k) {
+              if (last && k == next) {
+                ++seg;
+                next = ((seg + 1) * nk + segs - 1) / segs;
+              }
               const bool akm = phase == 0 || stored(a, 2 * x.i, k);
               const bool bkm = phase == 0 || (phase == 1 && stored(a, x.j, k));
-              if (!wait(sh, &sh.full[stage], ph)) break;
+              if (!wait(sh, &sh.full[stage], ph >> stage & 1)) break;
               tc_fence_after();
-              const uint32_t sa = base + stage * kStageBytes, sb = sa + 2 * kSub;
+              const uint32_t sa = base + stage * stage_bytes, sb = sa + 2 * kSub;
               const uint32_t idesc = instr_desc(x.nb * 64, akm, bkm);
-              const uint32_t seg = pass + 1 < passes ? 0 : (uint32_t)(k * segs / nk);
               const uint32_t d = tmem + acc * 256 + seg * seg_cols;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -371,61 +450,56 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                 begun |= 1u << seg;
               }
               mma_commit(smem_addr(&sh.empty[stage]));
-              if (++stage == kStages) { stage = 0; ph ^= 1; }
+              ph ^= 1u << stage;
+              if (++stage == stages) stage = 0;
             }
           }
           mma_commit(smem_addr(&sh.acc_full[acc]));
           accph ^= 1u << acc;
           if (++acc == sets) acc = 0;
         }
-      } else if (warp >= 4) {
-        const int row = tid - 128, sub = row >> 6, y = row & 63;
-        const bool leader = row == 0;
-        const uint32_t ebase = base + kStages * kStageBytes;
-        // what the result is added to, and where it goes
-        const unsigned char *ih, *il;
-        unsigned char *oh, *ol;
-        float fin, facc;
-        bool in, lo;
-        if (phase == 0) {
-          in = false, lo = a.split, ih = il = nullptr, oh = a.ah, ol = a.al;
-          fin = 0.f, facc = a.sa / (a.sx * a.sx);
-        } else if (phase == 1) {
-          in = true, lo = a.split, ih = a.ah, il = a.al, oh = a.bh, ol = a.bl;
-          fin = a.cb_, facc = a.cc / a.sa;
-        } else {
-          in = true, lo = true, ih = a.xh[cur], il = a.xl[cur], oh = a.xh[cur ^ 1], ol = a.xl[cur ^ 1];
-          fin = 0.f, facc = 1.f / a.sa;
-        }
+      } else if (warp >= 2) {
+        // row `row` of the tile and half of the columns of each sub-tile
+        const int row = (warp & 3) * 32 + lane, col_half = (warp - 2) >> 2, sub = row >> 6, y = row & 63;
+        const bool leader = tid == 64;
+        const uint32_t ebase = base + kRing * kSub;
+        // what the result is made from besides the product, and where it goes
+        const bool in = phase != 0, lo = phase == 2 || a.split;
+        const unsigned char* ih = phase == 1 ? a.ah : a.xh[cur];
+        const unsigned char* il = phase == 1 ? a.al : a.xl[cur];
+        unsigned char* oh = phase == 0 ? a.ah : phase == 1 ? a.bh : a.xh[cur ^ 1];
+        unsigned char* ol = phase == 0 ? a.al : phase == 1 ? a.bl : a.xl[cur ^ 1];
+        const float facc = phase == 0 ? a.sa / (a.sx * a.sx) : phase == 1 ? a.cc / a.sa : 1.f / a.sa;
         const int ncols = phase == 2 ? a.cb : a.rb;
         const long long obytes = phase == 2 ? a.xbytes : a.abytes;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-          if (named_or<128>(1, sh.dead != 0)) break;  // one decision for the four warps
+          if (named_or<kEpiThreads>(1, sh.dead != 0)) break;  // one decision for all its warps
           const Tile x = tile_of(a, phase, t);
-          const long long mo = x.mat * obytes;
-          auto offset = [&](int s, int half) {
-            return mo + ((long long)(2 * x.i + half) * ncols + x.j + s) * kSub;
-          };
-          auto fetch = [&](int s, uint32_t b) {  // leader: the addend's sub-tile into buffer b
+          const long long at0 = x.mat * obytes + ((long long)(2 * x.i) * ncols + x.j) * kSub;
+          const long long at1 = at0 + (long long)ncols * kSub;  // the lower 64 rows
+          auto fetch = [&](int s, uint32_t b) {  // leader: what sub-tile s is made from, into buffer b
             ++fetched[b];
             const uint32_t bar = smem_addr(&sh.epi[b]), dst = ebase + b * kEpiBytes;
             mbar_expect(bar, (lo ? 4 : 2) * kSub);
-            for (int half = 0; half < 2; ++half) {
-              bulk_load(dst + half * kSub, ih + offset(s, half), kSub, bar);
-              if (lo) bulk_load(dst + (2 + half) * kSub, il + offset(s, half), kSub, bar);
+            bulk_load(dst, ih + at0 + s * kSub, kSub, bar);
+            bulk_load(dst + kSub, ih + at1 + s * kSub, kSub, bar);
+            if (lo) {
+              bulk_load(dst + 2 * kSub, il + at0 + s * kSub, kSub, bar);
+              bulk_load(dst + 3 * kSub, il + at1 + s * kSub, kSub, bar);
             }
           };
           if (in && leader) {
             bulk_wait_read();
             fetch(0, nth & 1);
           }
-          const int grow = x.i * 128 + row;  // row of the matrix
+          const int grow = (x.mat * a.rb + 2 * x.i) * 64 + row;  // row in the diagonals
           float diag = 0.f;
           if (phase == 1) {
-            for (int j = row; j < x.nb * 64; j += 128) sh.dcol[j] = __ldcg(a.da + x.mat * a.rb * 64 + x.j * 64 + j);
-            diag = __ldcg(a.da + x.mat * a.rb * 64 + grow);
+            for (int j = tid - 64; j < x.nb * 64; j += kEpiThreads)
+              sh.dcol[j] = __ldcg(a.da + (x.mat * a.rb + x.j) * 64 + j);
+            diag = __ldcg(a.da + grow);
           } else if (phase == 2) {
-            diag = __ldcg(a.db + x.mat * a.rb * 64 + grow);
+            diag = __ldcg(a.db + grow);
           }
           const bool got = wait(sh, &sh.acc_full[acc], accph >> acc & 1);
           __syncwarp();
@@ -440,77 +514,93 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               wait(sh, &sh.epi[b], (epiph >> b) & 1);
               epiph ^= 1u << b;
             }
-            named_sync<128>(1);
-            unsigned char* buf = gen + kStages * kStageBytes + b * kEpiBytes + sub * kSub + y * 128;
+            named_sync<kEpiThreads>(1);
+            unsigned char* buf = gen + kRing * kSub + b * kEpiBytes + sub * kSub + y * 128;
+            const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc * 256 + s * 64 + col_half * 32;
+            const bool on_diagonal = phase < 2 && 2 * x.i + sub == x.j + s;
+            // rolled: each tile runs this once, and unrolled it is bound by fetching instructions
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              const int ch = col_half * 4 + q;
+              unsigned char* p = buf + ((ch ^ (y & 7)) << 4);
+              float v[8], u[8];
+              if (segs == 1) {
+                tmem_load8(from + q * 8, v);
+                tmem_wait_load();
+                tmem_loaded(v);
+              } else {
+                float w[kSegments][8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v[32];
-              const uint32_t from = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + acc * 256 + s * 64 + h * 32;
-              tmem_load32(from, v);
-              for (int g = 1; g < segs; ++g) {
-                float w[32];
-                tmem_load32(from + g * seg_cols, w);
+                for (int g = 0; g < kSegments; ++g)
+                  if (g < segs) tmem_load8(from + q * 8 + g * seg_cols, w[g]);
+                tmem_wait_load();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += w[i];
+                for (int g = 0; g < kSegments; ++g) tmem_loaded(w[g]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = w[0][i] + w[1][i];
+#pragma unroll
+                for (int g = 2; g < kSegments; ++g)
+                  if (g < segs)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += w[g][i];
               }
-#pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                unsigned char* p = buf + (((h * 4 + ch) ^ (y & 7)) << 4);
-                float u[8];
-                if (in) {
-                  unpack8(*reinterpret_cast<uint4*>(p), u);
-                  if (lo) {
-                    float w[8];
-                    unpack8(*reinterpret_cast<uint4*>(p + 2 * kSub), w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] += w[i];
-                  }
-                }
-                if (phase == 0) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) u[i] = facc * v[ch * 8 + i];
-                } else if (phase == 1) {
-                  // (D + A)^2 = A A + D A + A D + D D, A without its diagonal D
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    u[i] = fmaf(fin, u[i], facc * fmaf(diag + sh.dcol[s * 64 + h * 32 + ch * 8 + i], u[i], v[ch * 8 + i]));
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[ch * 8 + i]);
-                }
-                if (phase < 2 && 2 * x.i + sub == x.j + s) {  // the diagonal leaves the operand
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (h * 32 + ch * 8 + i == y) {
-                      float* d = (phase == 0 ? a.da : a.db) + x.mat * a.rb * 64 + grow;
-                      *d = phase == 0 ? u[i] : fmaf(diag, fmaf(facc, diag, fin), u[i]) + a.ca * a.sa;
-                      u[i] = 0.f;
-                    }
-                }
-                const uint4 hi = pack8(u);
-                *reinterpret_cast<uint4*>(p) = hi;
+              if (in) {
+                unpack8(*reinterpret_cast<uint4*>(p), u);
                 if (lo) {
                   float w[8];
-                  unpack8(hi, w);
+                  unpack8(*reinterpret_cast<uint4*>(p + 2 * kSub), w);
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) w[i] = u[i] - w[i];
-                  *reinterpret_cast<uint4*>(p + 2 * kSub) = pack8(w);
+                  for (int i = 0; i < 8; ++i) u[i] += w[i];
                 }
+              }
+              if (phase == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = facc * v[i];
+              } else if (phase == 1) {
+                // (D + A)^2 = A A + D A + A D + D D, A without its diagonal D
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  u[i] = fmaf(a.cb_, u[i], facc * fmaf(diag + sh.dcol[s * 64 + ch * 8 + i], u[i], v[i]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[i]);
+              }
+              if (on_diagonal && y >> 3 == ch) {  // the diagonal leaves the operand
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if ((y & 7) == i) {
+                    if (phase == 0) a.da[grow] = u[i];
+                    else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.cb_), u[i]) + a.ca * a.sa;
+                    u[i] = 0.f;
+                  }
+              }
+              const uint4 hi = pack8(u);
+              *reinterpret_cast<uint4*>(p) = hi;
+              if (lo) {
+                float w[8];
+                unpack8(hi, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = u[i] - w[i];
+                *reinterpret_cast<uint4*>(p + 2 * kSub) = pack8(w);
               }
             }
             fence_async_shared();
-            named_sync<128>(1);
+            if (s + 1 == x.nb) {
+              tc_fence_before();
+              mbar_arrive(smem_addr(&sh.acc_empty[acc]));
+            }
+            named_sync<kEpiThreads>(1);
             if (leader && got) {
               const uint32_t src = ebase + b * kEpiBytes;
-              for (int half = 0; half < 2; ++half) {
-                bulk_store(oh + offset(s, half), src + half * kSub, kSub);
-                if (lo) bulk_store(ol + offset(s, half), src + (2 + half) * kSub, kSub);
+              bulk_store(oh + at0 + s * kSub, src, kSub);
+              bulk_store(oh + at1 + s * kSub, src + kSub, kSub);
+              if (lo) {
+                bulk_store(ol + at0 + s * kSub, src + 2 * kSub, kSub);
+                bulk_store(ol + at1 + s * kSub, src + 3 * kSub, kSub);
               }
               bulk_commit();
             }
           }
-          tc_fence_before();
-          mbar_arrive(smem_addr(&sh.acc_empty[acc]));
           accph ^= 1u << acc;
           if (++acc == sets) acc = 0;
         }
@@ -527,7 +617,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     while (!mbar_try(smem_addr(&sh.drain), 0) && clock64() - t0 < kWaitCycles) {
     }
   }
-  if (!ok && tid == 128) {
+  if (!ok && tid == 64) {
     const long long t0 = clock64();
     for (int b = 0; b < 2; ++b) {
       const uint32_t n = fetched[b];
@@ -538,43 +628,61 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   if (!ok && warp == 0 && lane == 0) {
     const long long t0 = clock64();
     for (int i = 0; i < kStages; ++i) {
-      // stages before `stage` were filled in this turn of the ring, the others in the last
-      const uint32_t parity = i < stage ? ph : ph ^ 1;
+      if (!(filled >> i & 1)) continue;
+      const uint32_t parity = (ph >> i & 1) ^ 1;  // of its last fill
       while (!mbar_try(smem_addr(&sh.full[i]), parity) && clock64() - t0 < kWaitCycles) {
       }
     }
   }
-  // Back to the caller's layout.
+  // Back to the caller's layout
   if (ok) {
     float* tile = reinterpret_cast<float*>(gen);  // [64][65]
     const int per = a.rk * a.cb;
     const float inv = 1.f / a.sx;
+    auto put = [&](int mat, int row, int col, float (&v)[8]) {
+      if (row >= a.s.m || col >= a.s.n) return;
+      T* o = (T*)ptrs.out[mat] + (long long)row * call.out_ld + col;
+      if (call.muon) {
+        float w[8];
+        load8<T>(o, a.s.n - col, a.s.wide, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(call.decay, w[i], -call.rate * v[i]);
+      }
+      store8<T>(o, a.s.n - col, a.s.wide, v);
+    };
     for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
       const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
-      const unsigned char* ph_ = a.xh[cur] + mat * a.xbytes + (long long)u * kSub;
-      const unsigned char* pl_ = a.xl[cur] + mat * a.xbytes + (long long)u * kSub;
-      for (int e = tid; e < 512; e += kThreads) {
-        const int y = e >> 3, ch = e & 7, at = y * 128 + ((ch ^ (y & 7)) << 4);
-        float v[8], w[8];
-        unpack8(__ldcg(reinterpret_cast<const uint4*>(ph_ + at)), v);
-        unpack8(__ldcg(reinterpret_cast<const uint4*>(pl_ + at)), w);
+      const unsigned char* xh = a.xh[cur] + mat * a.xbytes + (long long)u * kSub;
+      const unsigned char* xl = a.xl[cur] + mat * a.xbytes + (long long)u * kSub;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int q = ch * 8 + i;
-          tile[a.s.tall ? q * 65 + y : y * 65 + q] = (v[i] + w[i]) * inv;
+      for (int e0 = 0; e0 < 512; e0 += kThreads) {
+        const int e = e0 + tid;
+        if (e < 512) {
+          const int y = e >> 3, ch = e & 7, at = y * 128 + ((ch ^ (y & 7)) << 4);
+          float v[8], w[8];
+          unpack8(__ldcg(reinterpret_cast<const uint4*>(xh + at)), v);
+          unpack8(__ldcg(reinterpret_cast<const uint4*>(xl + at)), w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = (v[i] + w[i]) * inv;
+          if (!a.s.tall) {
+            put(mat, bi * 64 + y, bj * 64 + ch * 8, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tile[y * 65 + ch * 8 + i] = v[i];
+          }
         }
       }
-      __syncthreads();
-      const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
-      for (int e = tid; e < 4096; e += kThreads) {
-        const int y = e >> 6, x = e & 63;
-        if (row0 + y < a.s.m && col0 + x < a.s.n) {
-          const float v = tile[y * 65 + x];
-          T* o = (T*)ptrs.out[mat] + (long long)(row0 + y) * call.out_ld + col0 + x;
-          *o = round_to<T>(call.muon ? fmaf(call.decay, to_float<T>(*o), -call.rate * v) : v);
+      if (a.s.tall) {
+        __syncthreads();
+        for (int e = tid; e < 512; e += kThreads) {
+          const int y = e >> 3, ch = e & 7;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = tile[(ch * 8 + i) * 65 + y];
+          put(mat, bj * 64 + y, bi * 64 + ch * 8, v);
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
   tc_fence_before();
@@ -654,7 +762,7 @@ NsMain plan(const wtconv_ns_desc_t& d) {
   return a;
 }
 
-constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormCtas * 4;  // barrier, partial sums
+constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormMax * 4;  // barrier, partial sums
 
 template <typename T>
 cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
@@ -677,13 +785,23 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
     a.al = w, w += aa;
     a.bl = w;
   }
-  ns_norm<T><<<dim3(kNormCtas, d.count), kNormThreads, 0, st>>>(a.s, k, p, part, a.sync);
+  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
+  // one pass of 8 elements for each thread of a small matrix, four CTAs per SM over a large stack
+  const long long chunks = (long long)d.m * ((d.n + 7) / 8);
+  long long parts = (chunks + kNormThreads - 1) / kNormThreads;
+  const long long most = (4 * sms + d.count - 1) / d.count;
+  if (parts > most) parts = most;
+  a.s.parts = (int)(parts > kNormMax ? kNormMax : parts);
+  const int es = sizeof(T);
+  a.s.wide = k.g_ld * es % 16 == 0 && k.out_ld * es % 16 == 0 && (!k.muon || k.m_ld % 4 == 0);
+  for (int i = 0; i < d.count; ++i)
+    if ((uintptr_t)p.grad[i] % 16 || (uintptr_t)p.out[i] % 16 || (uintptr_t)p.momentum[i] % 16) a.s.wide = 0;
+  ns_norm<T><<<dim3(a.s.parts, d.count), kNormThreads, 0, st>>>(a.s, k, p, part, a.sync);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const void* f = (const void*)ns_main<T>;
   e = wt::ensure_smem(f, kSmem);
   if (e != cudaSuccess) return e;
-  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   long long grid = (long long)d.count * a.t3;
   const long long others[3] = {(long long)d.count * a.t1, (long long)d.count * a.t2, (long long)d.count * a.rb * a.cb};
   for (long long o : others) grid = o > grid ? o : grid;

@@ -29,6 +29,9 @@
 // are the 128-byte-swizzled image that the tensor core reads, so that an
 // operand tile is one or a few contiguous bulk copies, results leave by the
 // same route, and padding needs no bounds (rows to 128, columns to 64, zero).
+// The two sub-blocks of a 128-row block lie next to each other: a copy costs
+// the issuing thread 40 ns and a K step 175 ns beside (measured), so the two
+// operands are also issued by a thread each.
 // A and B are symmetric: only sub-blocks on and below the diagonal blocks are
 // computed and stored, and a tile above is read from its mirror image with
 // the other operand order (MN-major), which costs nothing.
@@ -43,7 +46,7 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kNormMax = 256;      // partial sums of squares per matrix, at most
 constexpr int kEpiThreads = 256;   // warps 2-9
-constexpr int kThreads = 64 + kEpiThreads;  // warp 0: copies, warp 1: MMAs
+constexpr int kThreads = 96 + kEpiThreads;  // warps 0 and 10: copies of the two operands, warp 1: MMAs
 constexpr int kSub = 8192;         // bytes of a 64 x 64 sub-block
 constexpr int kRing = 20;          // sub-blocks of operands in flight
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
@@ -214,7 +217,7 @@ __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, uns
     if (stop) sh.dead = 1;
   }
   stop = __syncthreads_or(stop) != 0;
-  if (threadIdx.x == 0 || threadIdx.x == 64) fence_async();  // the threads that issue bulk copies
+  if (threadIdx.x == 0 || threadIdx.x == 64 || threadIdx.x == 320) fence_async();  // the threads that issue bulk copies
   return !stop;
 }
 
@@ -254,14 +257,21 @@ __device__ __forceinline__ Tile tile_of(const NsMain& a, int phase, int t) {
 // k are stored as such (K-major), or as their mirror image.
 __device__ __forceinline__ bool stored(const NsMain& a, int i, int k) { return (i >> a.gsh) >= (k >> a.gsh); }
 
+// Where sub-block (i, j) of a matrix with ncols sub-blocks across lies: the
+// two of a 128-row block next to each other.
+__device__ __forceinline__ long long at_sub(int i, int j, int ncols) {
+  return ((((long long)(i >> 1) * ncols + j) << 1) + (i & 1)) * kSub;
+}
+// n sub-blocks of column k from row i on (i even or n = 1)
 __device__ __forceinline__ void load_rows(uint32_t dst, const unsigned char* base, int ncols, int i, int n, int k,
                                           uint32_t bar) {
-  for (int s = 0; s < n; ++s) bulk_load(dst + s * kSub, base + ((long long)(i + s) * ncols + k) * kSub, kSub, bar);
+  for (int s = 0; s < n; s += 2)
+    bulk_load(dst + s * kSub, base + at_sub(i + s, k, ncols), n - s > 1 ? 2 * kSub : kSub, bar);
 }
-// n consecutive sub-blocks of one sub-block row: contiguous
+// n sub-blocks of row k from column j on
 __device__ __forceinline__ void load_across(uint32_t dst, const unsigned char* base, int ncols, int k, int j, int n,
                                             uint32_t bar) {
-  bulk_load(dst, base + ((long long)k * ncols + j) * kSub, n * kSub, bar);
+  for (int s = 0; s < n; ++s) bulk_load(dst + s * kSub, base + at_sub(k, j + s, ncols), kSub, bar);
 }
 __device__ __forceinline__ void load_symmetric(const NsMain& a, uint32_t dst, const unsigned char* base, int i, int n,
                                                int k, uint32_t bar) {
@@ -296,7 +306,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.full[i]), 2);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -329,8 +339,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         mul = q == 0.f ? 0.f : a.sx / (sqrtf(q) + a.s.eps);
         mat_known = mat;
       }
-      unsigned char* xh = a.xh[0] + mat * a.xbytes + (long long)u * kSub;
-      unsigned char* xl = a.xl[0] + mat * a.xbytes + (long long)u * kSub;
+      unsigned char* xh = a.xh[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
+      unsigned char* xl = a.xl[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
       auto put = [&](int y, int ch, const float (&v)[8]) {
         float w[8];
         const uint4 hi = pack8(v);
@@ -394,27 +404,26 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       uint32_t acc = 0;
       const int stage_bytes = (2 + nbw) * kSub, stages = min(kStages, kRing / (2 + nbw));
       int stage = 0;
-      if (warp == 0 && lane == 0) {
+      if ((warp == 0 || warp == 10) && lane == 0) {
+        const bool first = warp == 0;  // the operand whose rows are the tile's rows
+        const unsigned char* hi = first ? (phase == 0 ? a.xh[cur] : phase == 1 ? a.ah : a.bh)
+                                        : (phase == 1 ? a.ah : a.xh[cur]);
+        const unsigned char* lo = first ? (phase == 0 ? a.xl[cur] : phase == 1 ? a.al : a.bl)
+                                        : (phase == 1 ? a.al : a.xl[cur]);
+        const bool of_x = phase == 0 || (phase == 2 && !first);
         for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
-          const long long xo = x.mat * a.xbytes, ao = x.mat * a.abytes;
+          const int i = first ? 2 * x.i : x.j, n = first ? 2 : x.nb;
           for (int pass = 0; pass < passes && !sh.dead; ++pass) {
-            const bool alo = a.split && pass == 0, blo = a.split && pass == 1;
+            const unsigned char* src = (a.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
             for (int k = 0; k < nk; ++k) {
               if (!wait(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1)) break;
-              const uint32_t bar = smem_addr(&sh.full[stage]), da = base + stage * stage_bytes, db = da + 2 * kSub;
-              mbar_expect(bar, (2 + x.nb) * kSub);
+              const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
+              mbar_expect(bar, n * kSub);
               filled |= 1u << stage;
-              if (phase == 0) {
-                load_rows(da, (alo ? a.xl : a.xh)[cur] + xo, a.cb, 2 * x.i, 2, k, bar);
-                load_rows(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, x.j, x.nb, k, bar);
-              } else if (phase == 1) {
-                load_symmetric(a, da, (alo ? a.al : a.ah) + ao, 2 * x.i, 2, k, bar);
-                load_symmetric(a, db, (blo ? a.al : a.ah) + ao, x.j, x.nb, k, bar);
-              } else {
-                load_symmetric(a, da, (alo ? a.bl : a.bh) + ao, 2 * x.i, 2, k, bar);
-                load_across(db, (blo ? a.xl : a.xh)[cur] + xo, a.cb, k, x.j, x.nb, bar);
-              }
+              if (phase == 0) load_rows(dst, src, a.cb, i, n, k, bar);
+              else if (of_x) load_across(dst, src, a.cb, k, i, n, bar);
+              else load_symmetric(a, dst, src, i, n, k, bar);
               ph ^= 1u << stage;
               if (++stage == stages) stage = 0;
             }
@@ -458,7 +467,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           accph ^= 1u << acc;
           if (++acc == sets) acc = 0;
         }
-      } else if (warp >= 2) {
+      } else if (warp >= 2 && warp < 10) {
         // row `row` of the tile and half of the columns of each sub-tile
         const int row = (warp & 3) * 32 + lane, col_half = (warp - 2) >> 2, sub = row >> 6, y = row & 63;
         const bool leader = tid == 64;
@@ -475,18 +484,14 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
           if (named_or<kEpiThreads>(1, sh.dead != 0)) break;  // one decision for all its warps
           const Tile x = tile_of(a, phase, t);
-          const long long at0 = x.mat * obytes + ((long long)(2 * x.i) * ncols + x.j) * kSub;
-          const long long at1 = at0 + (long long)ncols * kSub;  // the lower 64 rows
+          // a sub-tile (128 rows, 64 columns) is two sub-blocks next to each other
+          const long long at0 = x.mat * obytes + at_sub(2 * x.i, x.j, ncols);
           auto fetch = [&](int s, uint32_t b) {  // leader: what sub-tile s is made from, into buffer b
             ++fetched[b];
             const uint32_t bar = smem_addr(&sh.epi[b]), dst = ebase + b * kEpiBytes;
             mbar_expect(bar, (lo ? 4 : 2) * kSub);
-            bulk_load(dst, ih + at0 + s * kSub, kSub, bar);
-            bulk_load(dst + kSub, ih + at1 + s * kSub, kSub, bar);
-            if (lo) {
-              bulk_load(dst + 2 * kSub, il + at0 + s * kSub, kSub, bar);
-              bulk_load(dst + 3 * kSub, il + at1 + s * kSub, kSub, bar);
-            }
+            bulk_load(dst, ih + at0 + s * 2 * kSub, 2 * kSub, bar);
+            if (lo) bulk_load(dst + 2 * kSub, il + at0 + s * 2 * kSub, 2 * kSub, bar);
           };
           if (in && leader) {
             bulk_wait_read();
@@ -592,12 +597,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             named_sync<kEpiThreads>(1);
             if (leader && got) {
               const uint32_t src = ebase + b * kEpiBytes;
-              bulk_store(oh + at0 + s * kSub, src, kSub);
-              bulk_store(oh + at1 + s * kSub, src + kSub, kSub);
-              if (lo) {
-                bulk_store(ol + at0 + s * kSub, src + 2 * kSub, kSub);
-                bulk_store(ol + at1 + s * kSub, src + 3 * kSub, kSub);
-              }
+              bulk_store(oh + at0 + s * 2 * kSub, src, 2 * kSub);
+              if (lo) bulk_store(ol + at0 + s * 2 * kSub, src + 2 * kSub, 2 * kSub);
               bulk_commit();
             }
           }
@@ -625,7 +626,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       }
     }
   }
-  if (!ok && warp == 0 && lane == 0) {
+  if (!ok && (warp == 0 || warp == 10) && lane == 0) {
     const long long t0 = clock64();
     for (int i = 0; i < kStages; ++i) {
       if (!(filled >> i & 1)) continue;
@@ -652,8 +653,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     };
     for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
       const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
-      const unsigned char* xh = a.xh[cur] + mat * a.xbytes + (long long)u * kSub;
-      const unsigned char* xl = a.xl[cur] + mat * a.xbytes + (long long)u * kSub;
+      const unsigned char* xh = a.xh[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
+      const unsigned char* xl = a.xl[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
 #pragma unroll
       for (int e0 = 0; e0 < 512; e0 += kThreads) {
         const int e = e0 + tid;

@@ -109,7 +109,7 @@ extern "C" {
 size_t wtconv_gn_workspace_size(const wtconv_gn_desc_t* d, int op) {
   try {
     if (check_gn(d, op) != WTCONV_OK || d->N == 0 || d->S == 0) return 0;
-    return wtb::gn_plan(*d, op, 16 / esize(d->dtype)).ws_bytes;
+    return wtb::gn_workspace(*d, op);
   } catch (...) {
     return 0;
   }
@@ -243,7 +243,7 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* d, void* const* weight,
 
 unsigned int wtconv_block_device_faults(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return 0;
-  return wtb::ns_take_faults();
+  return wtb::ns_take_faults() + wtb::gn_take_faults();
 }
 
 }  // extern "C"

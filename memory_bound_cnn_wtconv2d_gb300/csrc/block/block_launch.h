@@ -9,16 +9,22 @@
 namespace wtb {
 
 struct GnPlan {
-  int vec;        // elements of one access (a divisor of C; 16 bytes where alignment allows)
-  int tx, ty;     // threads over channel vectors and over rows
-  int splits;     // row ranges of one sample, one CTA each
-  int rows;       // rows of one range
+  int vec;         // elements of one access (a divisor of C; 16 bytes where alignment allows)
+  int tx, ty;      // threads over channel vectors and over rows
+  int rows;        // rows of one CTA
+  int cluster;     // resident form: CTAs of a cluster (0: streamed)
+  int ch;          // resident form: channels of a CTA
+  int splits;      // streamed form: row ranges of one sample, one CTA each
+  int lag;         // streamed form: samples read ahead
+  size_t part_at;  // streamed form: where the ranges' sums lie in the workspace
   size_t ws_bytes;
 };
 
 // Plan of one call; `align` is the number of elements that every pointer and
 // stride involved is a multiple of (capped at 16 bytes).
 GnPlan gn_plan(const wtconv_gn_desc_t& d, int op, int align);
+// Workspace that suffices whatever the pointers' alignment.
+size_t gn_workspace(const wtconv_gn_desc_t& d, int op);
 cudaError_t gn_launch_fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const float* w, const float* b,
                           void* y, float* mean, float* rstd, void* ws, cudaStream_t s);
 cudaError_t gn_launch_bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, const void* x,
@@ -42,5 +48,6 @@ struct NsCall {
 size_t ns_workspace(const wtconv_ns_desc_t& d);
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& c, const NsPointers& p, void* ws, cudaStream_t s);
 unsigned int ns_take_faults();
+unsigned int gn_take_faults();
 
 }  // namespace wtb

@@ -406,5 +406,5 @@ def test_refusals(ops):
         f(x, 4, w, eps=-1.0)
     assert e.value.status == wtconv.WTCONV_ERR_INVALID_ARG
     with pytest.raises(wtconv.WtconvError) as e:
-        f(x, 4, w, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+        g(x, x, mean, rstd, 4, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert e.value.status == wtconv.WTCONV_ERR_WORKSPACE

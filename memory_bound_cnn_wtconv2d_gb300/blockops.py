@@ -78,14 +78,13 @@ def _on(device):
     return _HERE if device.index is None or torch.cuda.current_device() == device.index else _c._device_ctx(device)
 
 
-def _float32(t, name, shape, device):
+def _float32(t, name, numel, device):
     if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and _c._on_cuda(t) and t.dtype == torch.float32 and t.is_contiguous()):
+        return
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and _c._on_cuda(t) and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
-    if t.device != device or t.numel() != math.prod(shape):
-        raise ValueError(f"{name} must hold {math.prod(shape)} elements on {device}, got {t.numel()} on {t.device}")
-    return t
+    if t.numel() != numel or t.device != device:
+        raise ValueError(f"{name} must hold {numel} elements on {device}, got {t.numel()} on {t.device}")
 
 
 def _rows(t, name):
@@ -116,31 +115,66 @@ def _rows(t, name):
     return st[0], C if row is None else row
 
 
-def _gn_desc(x, num_groups, eps, activation, xs, ds=(0, 0)):
-    if activation not in ACT_CODES:
-        raise ValueError(f"activation must be one of none, silu, gelu, got {activation!r}")
-    shape = x.shape
-    C = shape[-1]
-    if not (isinstance(num_groups, int) and num_groups >= 1 and C >= 1 and C % num_groups == 0):
-        raise ValueError(f"num_groups = {num_groups} must be a positive divisor of the {C} channels")
-    return GnDesc(shape[0], math.prod(shape[1:-1]), C, num_groups, _c.DTYPE_CODES[x.dtype], ACT_CODES[activation],
-                  eps, xs[0], xs[1], ds[0], ds[1])
+class _GnLayout:
+    """What a call needs to know of its layout: built once for each."""
+
+    __slots__ = ("desc", "ref", "N", "C", "G", "device", "index", "ws", "contiguous")
+
+    def __init__(self, x, dy, num_groups, eps, activation):
+        xs = _rows(x, "x")
+        ds = (0, 0)
+        if dy is not None:
+            ds = _rows(dy, "dy")
+            if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+                raise ValueError(f"dy must be {tuple(x.shape)} {x.dtype} on {x.device}, "
+                                 f"got {tuple(dy.shape)} {dy.dtype} on {dy.device}")
+        if activation not in ACT_CODES:
+            raise ValueError(f"activation must be one of none, silu, gelu, got {activation!r}")
+        shape = x.shape
+        C = shape[-1]
+        if not (isinstance(num_groups, int) and num_groups >= 1 and C >= 1 and C % num_groups == 0):
+            raise ValueError(f"num_groups = {num_groups} must be a positive divisor of the {C} channels")
+        self.desc = GnDesc(shape[0], math.prod(shape[1:-1]), C, num_groups, _c.DTYPE_CODES[x.dtype],
+                           ACT_CODES[activation], eps, xs[0], xs[1], ds[0], ds[1])
+        self.ref = ctypes.byref(self.desc)
+        self.N, self.C, self.G = shape[0], C, num_groups
+        self.device, self.index = x.device, x.device.index
+        self.contiguous = x.is_contiguous()
+        with _on(x.device):  # the size follows the device
+            self.ws = lib().wtconv_gn_workspace_size(self.ref, OP_GN_FWD if dy is None else OP_GN_BWD)
 
 
-# Workspace bytes per call kind and layout; they depend on nothing else.
-_SIZES = {}
+# Layouts by shapes, strides, types, devices and options: a step calls the
+# same few again and again, and checking and describing one costs more than
+# launching it.  Bounded, for processes that meet many shapes.
+_MAX_LAYOUTS = 1024
+_LAYOUTS = {}
 
 
-def _scratch(key, query, device, workspace):
-    """The caller's workspace, else a new one of the size the call needs."""
-    if workspace is not None:
-        return workspace, _c._workspace_bytes(workspace, device)
-    need = _SIZES.get(key)
-    if need is None:
-        if len(_SIZES) > 4096:
-            _SIZES.clear()
-        need = _SIZES[key] = query()
-    return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+def _gn_layout(x, dy, num_groups, eps, activation):
+    try:
+        key = (x.shape, x.stride(), x.dtype, x.device, num_groups, eps, activation,
+               None if dy is None else (dy.shape, dy.stride(), dy.dtype, dy.device))
+        lay = _LAYOUTS.get(key)
+    except (AttributeError, TypeError):  # not tensors, or options no call takes: the checks say which
+        key = lay = None
+    if lay is None:
+        lay = _GnLayout(x, dy, num_groups, eps, activation)
+        if len(_LAYOUTS) >= _MAX_LAYOUTS:
+            _LAYOUTS.clear()
+        if key is not None:
+            _LAYOUTS[key] = lay
+    return lay
+
+
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, device):
+    """The stream handle of a call: the given stream's, else the device's current one's."""
+    if stream is None:
+        return _RAW_STREAM(device.index) if _RAW_STREAM is not None else torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _span(t):
@@ -177,33 +211,31 @@ def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activatio
     a wider tensor as long as a pixel's channels are contiguous and the pixels
     of a sample lie one stride apart.
     """
-    xs = _rows(x, "x")
-    device = x.device
-    desc = _gn_desc(x, num_groups, eps, activation, xs)
-    C = desc.C
-    _float32(weight, "weight", (C,), device)
-    _float32(bias, "bias", (C,), device)
-    given = [("y", y), ("mean", mean), ("rstd", rstd), ("workspace", workspace)]
-    if any(t is not None for _, t in given):
+    lay = _gn_layout(x, None, num_groups, eps, activation)
+    device, C = lay.device, lay.C
+    _float32(weight, "weight", C, device)
+    _float32(bias, "bias", C, device)
+    if y is not None or mean is not None or rstd is not None or workspace is not None:
         if y is not None:
             _given(y, "y", x)
-        for n, t in given[1:3]:
-            _float32(t, n, (desc.N, num_groups), device)
-        _disjoint(given, [("x", x), ("weight", weight), ("bias", bias)])
+        _float32(mean, "mean", lay.N * lay.G, device)
+        _float32(rstd, "rstd", lay.N * lay.G, device)
+        _disjoint([("y", y), ("mean", mean), ("rstd", rstd), ("workspace", workspace)],
+                  [("x", x), ("weight", weight), ("bias", bias)])
     with _on(device):
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=device)
+            y = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
         if mean is None:
-            mean = torch.empty((desc.N, num_groups), dtype=torch.float32, device=device)
+            mean = torch.empty((lay.N, lay.G), dtype=torch.float32, device=device)
         if rstd is None:
-            rstd = torch.empty((desc.N, num_groups), dtype=torch.float32, device=device)
-        L = lib()
-        ws, n = _scratch((OP_GN_FWD, desc.N, desc.S, C, num_groups, desc.dtype),
-                         lambda: L.wtconv_gn_workspace_size(ctypes.byref(desc), OP_GN_FWD), device, workspace)
-        _c._check(L.wtconv_gn_act_fwd(
-            ctypes.byref(desc), x.data_ptr(), None if weight is None else weight.data_ptr(),
+            rstd = torch.empty((lay.N, lay.G), dtype=torch.float32, device=device)
+        ws, n = _scratch(lay.ws, device, workspace)
+        status = lib().wtconv_gn_act_fwd(
+            lay.ref, x.data_ptr(), None if weight is None else weight.data_ptr(),
             None if bias is None else bias.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            None if ws is None else ws.data_ptr(), n, _c._stream(stream, device)))
+            None if ws is None else ws.data_ptr(), n, _stream_of(stream, device))
+        if status:
+            _c._check(status)
     return y, mean, rstd
 
 
@@ -212,43 +244,44 @@ def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, act
     """Gradients of ``wtconv_gn_act_fwd``: (dx, dweight, dbias), dx contiguous in
     x's type, the parameter gradients float32 [C] (of a None weight or bias
     too: what ones and zeros in their place would get)."""
-    xs = _rows(x, "x")
-    ds = _rows(dy, "dy")
-    device = x.device
-    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != device:
-        raise ValueError(f"dy must be {tuple(x.shape)} {x.dtype} on {device}, "
-                         f"got {tuple(dy.shape)} {dy.dtype} on {dy.device}")
-    desc = _gn_desc(x, num_groups, 0.0, activation, xs, ds)
-    C = desc.C
-    _float32(weight, "weight", (C,), device)
-    _float32(bias, "bias", (C,), device)
-    for n, t in (("mean", mean), ("rstd", rstd)):
-        if t is None:
-            raise ValueError(f"{n} is required")
-        _float32(t, n, (desc.N, num_groups), device)
-    given = [("dx", dx), ("dweight", dweight), ("dbias", dbias), ("workspace", workspace)]
-    if any(t is not None for _, t in given):
+    lay = _gn_layout(x, dy, num_groups, 0.0, activation)
+    device, C = lay.device, lay.C
+    _float32(weight, "weight", C, device)
+    _float32(bias, "bias", C, device)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are required")
+    _float32(mean, "mean", lay.N * lay.G, device)
+    _float32(rstd, "rstd", lay.N * lay.G, device)
+    if dx is not None or dweight is not None or dbias is not None or workspace is not None:
         if dx is not None:
             _given(dx, "dx", x)
-        for n, t in given[1:3]:
-            _float32(t, n, (C,), device)
-        _disjoint(given, [("dy", dy), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight), ("bias", bias)])
+        _float32(dweight, "dweight", C, device)
+        _float32(dbias, "dbias", C, device)
+        _disjoint([("dx", dx), ("dweight", dweight), ("dbias", dbias), ("workspace", workspace)],
+                  [("dy", dy), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight), ("bias", bias)])
     with _on(device):
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+            dx = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
         if dweight is None:
             dweight = torch.empty(C, dtype=torch.float32, device=device)
         if dbias is None:
             dbias = torch.empty(C, dtype=torch.float32, device=device)
-        L = lib()
-        ws, n = _scratch((OP_GN_BWD, desc.N, desc.S, C, num_groups, desc.dtype),
-                         lambda: L.wtconv_gn_workspace_size(ctypes.byref(desc), OP_GN_BWD), device, workspace)
-        _c._check(L.wtconv_gn_act_bwd(
-            ctypes.byref(desc), dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        ws, n = _scratch(lay.ws, device, workspace)
+        status = lib().wtconv_gn_act_bwd(
+            lay.ref, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), dx.data_ptr(),
             dweight.data_ptr(), dbias.data_ptr(), None if ws is None else ws.data_ptr(), n,
-            _c._stream(stream, device)))
+            _stream_of(stream, device))
+        if status:
+            _c._check(status)
     return dx, dweight, dbias
+
+
+def _scratch(need, device, workspace):
+    """The caller's workspace, else a new one of the size the call needs."""
+    if workspace is not None:
+        return workspace, _c._workspace_bytes(workspace, device)
+    return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
 
 
 class _Stack:
@@ -265,30 +298,32 @@ class _Stack:
         for q in ts:
             if not (isinstance(q, torch.Tensor) and _c._on_cuda(q)):
                 raise ValueError(f"{name} must be CUDA tensors")
-            if q.dim() < 2:
-                raise ValueError(f"{name} must be matrices [..., m, n], got {tuple(q.shape)}")
-            if q.shape[-2:] != first.shape[-2:] or q.dtype != first.dtype or q.device != first.device:
+            shape = q.shape
+            if len(shape) < 2:
+                raise ValueError(f"{name} must be matrices [..., m, n], got {tuple(shape)}")
+            m, n = shape[-2:]
+            if q is first:
+                self.m, self.n, self.dtype, self.device = m, n, q.dtype, q.device
+            elif m != self.m or n != self.n or q.dtype != self.dtype or q.device != self.device:
                 raise ValueError(f"{name}: one shape, type and device for all matrices")
-            m, n = q.shape[-2:]
-            sm, sn = q.stride()[-2:]
+            strides = q.stride()
+            sm, sn = strides[-2:]
             if n > 1 and sn != 1:
                 raise ValueError(f"{name}: the elements of a row must be contiguous (stride {sn})")
             sm = n if m <= 1 else sm
             if sm < n or (ld is not None and sm != ld):
                 raise ValueError(f"{name}: rows must not overlap, and lie the same distance apart in all matrices")
             ld = sm
-            if q.dim() == 2:
+            if len(shape) == 2:
                 ptrs.append(q.data_ptr())
             else:
                 e, offsets = q.element_size(), [0]
-                for size, stride in zip(q.shape[:-2], q.stride()[:-2]):
+                for size, stride in zip(shape[:-2], strides[:-2]):
                     offsets = [o + i * stride for o in offsets for i in range(size)]
                 p = q.data_ptr()
                 ptrs += [p + o * e for o in offsets]
         self.tensors = ts
         self.pointers, self.ld, self.count = ptrs, max(ld, 1), len(ptrs)
-        self.m, self.n = first.shape[-2:]
-        self.dtype, self.device = first.dtype, first.device
         if dtype is not None and self.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {self.dtype}")
         if self.dtype not in _c.DTYPE_CODES:
@@ -329,17 +364,29 @@ def _disjoint_stacks(w, g, b, workspace):
         reach[name] = max(hi, reach.get(name, 0))
 
 
+# Descriptors and workspace sizes by shape and options.
+_NS_DESCS = {}
+
+
 def _ns_desc(s, count, steps, coefficients, eps):
-    if not (isinstance(steps, int) and 0 <= steps <= 64):
-        raise ValueError(f"steps must be an int in [0, 64], got {steps!r}")
-    if len(coefficients) != 3 or not all(math.isfinite(v) and abs(v) <= 16 for v in coefficients):
-        raise ValueError(f"coefficients must be three numbers of at most 16 in size, got {coefficients!r}")
-    return NsDesc(count, s.m, s.n, _c.DTYPE_CODES[s.dtype], steps, *coefficients, eps)
-
-
-def _ns_scratch(desc, device, workspace):
-    return _scratch((2, desc.count, desc.m, desc.n, desc.dtype),
-                    lambda: lib().wtconv_ns_workspace_size(ctypes.byref(desc)), device, workspace)
+    try:
+        key = (count, s.m, s.n, s.dtype, s.device, steps, tuple(coefficients), eps)
+        got = _NS_DESCS.get(key)
+    except TypeError:
+        key = got = None
+    if got is None:
+        if not (isinstance(steps, int) and 0 <= steps <= 64):
+            raise ValueError(f"steps must be an int in [0, 64], got {steps!r}")
+        if len(coefficients) != 3 or not all(math.isfinite(v) and abs(v) <= 16 for v in coefficients):
+            raise ValueError(f"coefficients must be three numbers of at most 16 in size, got {coefficients!r}")
+        desc = NsDesc(count, s.m, s.n, _c.DTYPE_CODES[s.dtype], steps, *coefficients, eps)
+        ref = ctypes.byref(desc)
+        got = (ref, lib().wtconv_ns_workspace_size(ref))
+        if len(_NS_DESCS) >= _MAX_LAYOUTS:
+            _NS_DESCS.clear()
+        if key is not None:
+            _NS_DESCS[key] = got
+    return got
 
 
 def wtconv_orthogonalize(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out=None, workspace=None, stream=None):
@@ -357,17 +404,20 @@ def wtconv_orthogonalize(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out
     elif workspace is not None:
         _disjoint([("workspace", workspace)], [("g", g)])
     with _on(s.device):
-        if out is None:
+        fresh = out is None
+        if fresh:
             out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
         o = _Stack(out, "out", like=s)
-        o.separate("out")
+        if not fresh:
+            o.separate("out")
         for i in range(0, s.count, NS_MAX_COUNT):
             k = min(NS_MAX_COUNT, s.count - i)
-            desc = _ns_desc(s, k, steps, coefficients, eps)
-            ws, n = _ns_scratch(desc, s.device, workspace)
-            _c._check(lib().wtconv_orthogonalize(ctypes.byref(desc), s.chunk(i, k), s.ld, o.chunk(i, k), o.ld,
-                                                 None if ws is None else ws.data_ptr(), n,
-                                                 _c._stream(stream, s.device)))
+            ref, need = _ns_desc(s, k, steps, coefficients, eps)
+            ws, n = _scratch(need, s.device, workspace)
+            status = lib().wtconv_orthogonalize(ref, s.chunk(i, k), s.ld, o.chunk(i, k), o.ld,
+                                                None if ws is None else ws.data_ptr(), n, _stream_of(stream, s.device))
+            if status:
+                _c._check(status)
     return out
 
 
@@ -393,12 +443,14 @@ def wtconv_muon_step(weight, grad, buffer, lr, momentum=0.95, nesterov=True, wei
     with _on(w.device):
         for i in range(0, w.count, NS_MAX_COUNT):
             k = min(NS_MAX_COUNT, w.count - i)
-            desc = _ns_desc(w, k, steps, coefficients, eps)
-            ws, n = _ns_scratch(desc, w.device, workspace)
-            _c._check(lib().wtconv_muon_step(
-                ctypes.byref(desc), w.chunk(i, k), w.ld, g.chunk(i, k), g.ld, b.chunk(i, k), b.ld, momentum,
+            ref, need = _ns_desc(w, k, steps, coefficients, eps)
+            ws, n = _scratch(need, w.device, workspace)
+            status = lib().wtconv_muon_step(
+                ref, w.chunk(i, k), w.ld, g.chunk(i, k), g.ld, b.chunk(i, k), b.ld, momentum,
                 int(bool(nesterov)), 1.0 - lr * weight_decay, lr * scale, None if ws is None else ws.data_ptr(), n,
-                _c._stream(stream, w.device)))
+                _stream_of(stream, w.device))
+            if status:
+                _c._check(status)
     return weight
 
 

@@ -14,9 +14,10 @@ struct GnPlan {
   int rows;        // rows of one CTA
   int cluster;     // resident form: CTAs of a cluster (0: streamed)
   int ch;          // resident form: channels of a CTA
-  int splits;      // streamed form: row ranges of one sample, one CTA each
+  int spread;      // spread form
+  int splits;      // spread and streamed form: row ranges of one sample
   int lag;         // streamed form: samples read ahead
-  size_t part_at;  // streamed form: where the ranges' sums lie in the workspace
+  size_t part_at;  // both: where the ranges' sums lie in the workspace
   size_t ws_bytes;
 };
 

@@ -15,6 +15,7 @@ WTB_DECLARE(f16)
 WTB_DECLARE(bf16)
 #undef WTB_DECLARE
 long long gn_resident_smem(int op, int ch, int ty, long long rows, int groups, int es);
+long long gn_spread_smem(int op, int C, int G, int ty, long long rows, int es);
 
 namespace {
 
@@ -63,6 +64,32 @@ void plan_resident(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& 
   }
 }
 
+// The spread form: ranges of as many rows as two to four CTAs an SM have room
+// for; false where the GPU does not hold a sample.
+bool plan_spread(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& p) {
+  const int es = d.dtype == WTCONV_F32 ? 4 : 2;
+  if (d.C / vec > kThreads) return false;
+  p.tx = d.C / vec;
+  p.ty = kThreads / p.tx;
+  for (int occ = op == WTCONV_OP_GN_FWD ? 4 : 3; occ >= 2; --occ) {
+    const long long room = kSmemSm / occ - 1024 - gn_spread_smem(op, d.C, d.G, p.ty, 0, es);
+    const long long row = (long long)d.C * (op == WTCONV_OP_GN_FWD ? es : es + 4);
+    long long fit = room / row;
+    if (fit < p.ty) continue;
+    fit -= fit % p.ty;  // whole passes
+    long long splits = (d.S + fit - 1) / fit;
+    // half of the CTAs at most, so that a second sample is under way
+    if (2 * splits > (long long)occ * sms) continue;
+    // small samples: enough ranges to fill the GPU
+    const long long want = ((long long)occ * sms + d.N - 1) / d.N, most = (d.S + 4LL * p.ty - 1) / (4LL * p.ty);
+    if (splits < want) splits = want < most ? want : most > splits ? most : splits;
+    p.rows = (int)((d.S + splits - 1) / splits);
+    p.splits = (int)((d.S + p.rows - 1) / p.rows);
+    return true;
+  }
+  return false;
+}
+
 GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   GnPlan p = {};
   const int widest = d.dtype == WTCONV_F32 ? 4 : 8;
@@ -72,23 +99,28 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   plan_resident(d, op, vec, sms, p);
   const size_t n = (size_t)d.N;
-  if (!p.cluster && vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
+  if (!p.cluster) p.spread = plan_spread(d, op, vec, sms, p);
+  if (!p.cluster && !p.spread && vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
   if (p.cluster) {
     p.ws_bytes = op == WTCONV_OP_GN_FWD ? 0 : n * p.cluster * 2 * d.C * 4;
+  } else if (p.spread) {
+    p.part_at = ((n + 1) * 4 + (n + 1) * 4 + 255) & ~(size_t)255;  // the queue and the samples' counters first
+    p.ws_bytes = p.part_at + (op == WTCONV_OP_GN_FWD ? n * p.splits * d.G * 8
+                                                     : n * (p.splits + 1) * 2 * d.C * 4 + n * p.splits * 2 * d.G * 4);
   } else {
     p.tx = d.C / vec < kThreads ? d.C / vec : kThreads;
     p.ty = kThreads / p.tx;
-    // Samples are read 40 MB ahead of their second reading: far enough for the
-    // statistics to be there, near enough for the L2 (129 MB).  Ranges of 64 KB
-    // of x, at least 16 rows a thread.
+    // Samples are read 16 MB ahead of their second reading, and some 20 MB are
+    // being read or applied: near enough for the L2, whose halves may each hold
+    // a line.  Ranges of 32 KB of x, at least 8 rows a thread.
     const int es = d.dtype == WTCONV_F32 ? 4 : 2;
     const long long bytes = d.S * d.C * es, all = bytes * (op == WTCONV_OP_GN_FWD ? 1 : 2);
-    long long lag = (40LL << 20) / all;
+    long long lag = (16LL << 20) / all;
     if (lag < 1) lag = 1;
     if (lag > d.N) lag = d.N;
     p.lag = (int)lag;
-    long long want = bytes >> 16;
-    const long long most = (d.S + 16LL * p.ty - 1) / (16LL * p.ty);
+    long long want = bytes >> 15;
+    const long long most = (d.S + 8LL * p.ty - 1) / (8LL * p.ty);
     if (want > most) want = most;
     if (want > 4096) want = 4096;
     if (want < 1) want = 1;

@@ -1,8 +1,11 @@
 // Group norm with an activation, channels last.
 //
-// Two forms.  Resident: a cluster of up to eight CTAs holds one sample's rows
+// Three forms.  Resident: a cluster of up to eight CTAs holds one sample's rows
 // of a range of channels (whole groups) in shared memory, so that x (and dy)
 // cross the memory once: read, statistics, cluster exchange, written.
+// Spread: the same over the whole GPU; CTAs take row ranges off a queue, hold
+// them in shared memory and exchange statistics through memory, two to four
+// samples being under way at once.
 // Streamed, for samples that no cluster holds: one pass for the statistics and
 // one that applies them, in one launch whose CTAs take row ranges off a queue
 // that applies a sample some 40 MB after it was read, so that the second read
@@ -484,8 +487,9 @@ bwd_reduce(int C, long long blocks, const float* __restrict__ part, float* __res
   }
 }
 
-// ---------------------------------------------------------------- streamed
+// ---------------------------------------------------------------- queues
 
+// Of both the spread and the streamed form.
 struct Streamed {
   int tx, ty;        // threads across channel vectors, rows side by side
   int splits, rows;  // row ranges of a sample: the queue's items
@@ -515,26 +519,33 @@ __device__ __forceinline__ Item item_at(const Args& a, const Streamed& p, unsign
   return t;
 }
 
-// The CTA's next item; also the barrier between two items.
-__device__ __forceinline__ Item next_item(const Args& a, const Streamed& p) {
-  __shared__ unsigned int at;
-  __syncthreads();
-  if (threadIdx.x == 0) at = atomicAdd(p.sync, 1u);
-  __syncthreads();
-  return item_at(a, p, at);
-}
+// Takes items off the queue, one fetched ahead.
+struct Queue {
+  unsigned int next, turn;  // of thread 0: the item after this one
+  __device__ __forceinline__ Queue(const Streamed& p) : next(0), turn(0) { fetch(p); }
+  __device__ __forceinline__ void fetch(const Streamed& p) {
+    if (threadIdx.x == 0) next = atomicAdd(p.sync, 1u);
+  }
+  // also the barrier between two items
+  __device__ __forceinline__ unsigned int take() {
+    __shared__ unsigned int at[2];
+    turn ^= 1;
+    if (threadIdx.x == 0) at[turn] = next;
+    __syncthreads();
+    return at[turn];
+  }
+};
 
-// Waits until a sample's statistics are there.  The CTAs that read it took
-// their items earlier and wait for nothing, so this ends; false: it gave up.
-__device__ __forceinline__ bool wait_sample(const Args& a, const Streamed& p, long long n) {
+// Waits until *flag is `least` or more; false: it gave up.  The CTAs that it
+// waits for took their items earlier (see the callers), so this ends.
+__device__ __forceinline__ bool wait_for(const unsigned int* flag, unsigned int least) {
   bool ok = true;
   if (threadIdx.x == 0) {
-    const unsigned int* flag = p.sync + 1 + a.N + n;
     const long long t0 = clock64();
     unsigned int v;
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-      if (v) break;
+      if (v >= least) break;
       if (clock64() - t0 > kWaitCycles) {
         atomicAdd(&g_gn_faults, 1u);
         ok = false;
@@ -564,6 +575,270 @@ __device__ __forceinline__ void raise_sample(const Args& a, const Streamed& p, l
     asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(p.sync + 1 + a.N + n) : "memory");
   }
 }
+
+// ---------------------------------------------------------------- spread
+
+// The queue holds the samples' ranges in order.  A CTA keeps its range until
+// all ranges of the sample are read.  The launch is cooperative, so that all
+// its CTAs run, and no sample has more ranges than there are CTAs; a later
+// sample's are taken after an earlier one's, so the earliest unfinished sample
+// always has all its ranges at work.
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads, 4)
+fwd_spread(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
+           const float* __restrict__ w, const float* __restrict__ b, float2* part, T* __restrict__ y,
+           float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int P = kPairs<VEC>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31, c = tx * VEC;
+  const bool on = ty < p.ty, whole = a.Cg % VEC == 0;
+  T* data = reinterpret_cast<T*>(raw);  // [rows][C]; a thread only touches what it copied
+  T* pd = data + ty * a.C + c;
+  float* st = reinterpret_cast<float*>(raw + (((long long)p.rows * a.C * sizeof(T) + 15) & ~15LL));  // [2][ty][C]
+  float* g_all = st + 2 * p.ty * a.C;  // [2][G]
+  const int step = p.ty * a.C;
+  const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
+  int g[VEC];
+  groups_of<VEC>(c, a.Cg, g);
+  Queue queue(p);
+  while (true) {
+    const unsigned int it = queue.take();
+    const int n = (int)(it / (unsigned)p.splits), split = (int)(it - (unsigned)n * (unsigned)p.splits);
+    if (n >= (int)a.N) return;
+    const long long r0 = (long long)split * p.rows;
+    const int rows = (int)min((long long)p.rows, a.S - r0), stop = on ? rows : 0;
+    {
+      const T* from = x + n * a.xs + (r0 + ty) * a.xr + c;
+      T* to = pd;
+#pragma unroll 4
+      for (int r = ty; r < stop; r += p.ty, from += p.ty * a.xr, to += step) copy_async<VEC * sizeof(T)>(to, from);
+    }
+    copy_wait();
+    if (on) {
+      float2 f[P], m[P], q[P];
+      const int mine = ty < rows ? (rows - ty + p.ty - 1) / p.ty : 0;
+      if (mine) {
+        Running<VEC> run;
+        const T* at = pd;
+        load_pairs<T, VEC>(at, f);
+        run.begin(f);
+#pragma unroll 2
+        for (int i = 1; i < mine; ++i) {
+          at += step;
+          load_pairs<T, VEC>(at, f);
+          run.add(f);
+        }
+        run.end(mine, m, q);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) m[i] = q[i] = make_float2(0.f, 0.f);
+      }
+      put_statistics<VEC>(st, p.ty, whole ? p.tx : a.C, whole, ty, tx, mine, m, q);
+    }
+    __syncthreads();
+    float2* all = part + (long long)n * p.splits * a.G;
+    group_statistics(st, p.ty, whole ? p.tx : a.C, whole ? a.Cg / VEC : a.Cg, whole ? VEC : 1, a.G, rows,
+                     [&](int k, float m, float q) { all[split * a.G + k] = make_float2(m, q); });
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) atomicAdd(p.sync + 1 + n, 1u);
+    if (!wait_for(p.sync + 1 + n, p.splits)) return;
+    queue.fetch(p);  // not before: the next range may be of this sample
+    for (int k = tid >> 5; k < a.G; k += kThreads / 32) {  // one warp per group
+      float t = 0.f;
+      for (int s = lane; s < p.splits; s += 32)
+        t = fmaf(s + 1 < p.splits ? (float)p.rows : last, __ldcg(all + s * a.G + k).x, t);
+      const float mean = warp_sum(t) / (float)a.S;
+      t = 0.f;
+      for (int s = lane; s < p.splits; s += 32) {
+        const float2 v = __ldcg(all + s * a.G + k);
+        const float d = v.x - mean;
+        t += fmaf((s + 1 < p.splits ? (float)p.rows : last) * (float)a.Cg * d, d, v.y);
+      }
+      const float rs = rsqrtf(warp_sum(t) / ((float)a.S * (float)a.Cg) + a.eps);
+      if (lane == 0) {
+        g_all[k] = mean;
+        g_all[a.G + k] = rs;
+        if (split == 0) {
+          mean_out[(long long)n * a.G + k] = mean;
+          rstd_out[(long long)n * a.G + k] = rs;
+        }
+      }
+    }
+    __syncthreads();
+    if (on) {
+      float2 mu[P], sc[P], sh[P];
+      per_channel<VEC>(mu, [&](int e) { return -g_all[g[e]]; });
+      per_channel<VEC>(sc, [&](int e) { return g_all[a.G + g[e]] * (w ? w[c + e] : 1.f); });
+      per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
+      T* py = y + (n * a.S + r0 + ty) * a.C + c;
+      const T* at = pd;
+      const long long ystep = (long long)p.ty * a.C;
+#pragma unroll 2
+      for (int r = ty; r < rows; r += p.ty, at += step, py += ystep) {
+        float2 f[P];
+        load_pairs<T, VEC>(at, f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = act2<ACT>(fma2(add2(f[i], mu[i]), sc[i], sh[i]));
+        store_pairs<T, VEC>(py, f);
+      }
+    }
+  }
+}
+
+// part[n][split][2][C]: sums of dz and of dz * xhat over the range; gpart
+// [n][split][2][G]: the groups' weighted sums.  The CTA that read a sample's
+// last range adds the parts up into sums[n][2][C].
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads, 3)
+bwd_spread(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
+           const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+           const float* __restrict__ w, const float* __restrict__ b, float* part, float* gpart, float* sums,
+           T* __restrict__ dx) {
+  constexpr int P = kPairs<VEC>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ int is_last;
+  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31, c = tx * VEC;
+  const bool on = ty < p.ty;
+  const int step = p.ty * a.C;
+  // [rows][C] each; a thread only touches what it copied.  dy lands in the
+  // first bytes of its dz slots.
+  float* dz = reinterpret_cast<float*>(raw);
+  T* data = reinterpret_cast<T*>(dz + (((long long)p.rows * a.C + 3) & ~3LL));
+  T* pd = data + ty * a.C + c;
+  float* pz = dz + ty * a.C + c;
+  float* st = reinterpret_cast<float*>(  // [2][ty][C]
+      raw + (((((long long)p.rows * a.C + 3) & ~3LL) * 4 + (long long)p.rows * a.C * sizeof(T) + 15) & ~15LL));
+  float* ch = st + 2 * p.ty * a.C;  // [2][C]
+  float* g_all = ch + 2 * a.C;      // [2][G]
+  float* tmp = g_all + 2 * a.G;
+  int g[VEC];
+  groups_of<VEC>(c, a.Cg, g);
+  const float inv = 1.f / ((float)a.S * (float)a.Cg);
+  Queue queue(p);
+  while (true) {
+    const unsigned int it = queue.take();
+    const int n = (int)(it / (unsigned)p.splits), split = (int)(it - (unsigned)n * (unsigned)p.splits);
+    if (n >= (int)a.N) return;
+    const long long r0 = (long long)split * p.rows;
+    const int rows = (int)min((long long)p.rows, a.S - r0), stop = on ? rows : 0;
+    {
+      const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
+      const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
+      int at = 0;
+#pragma unroll 4
+      for (int r = ty; r < stop; r += p.ty, at += step, px += p.ty * a.xr, py += p.ty * a.dr) {
+        copy_async<VEC * sizeof(T)>(pd + at, px);
+        copy_async<VEC * sizeof(T)>(pz + at, py);
+      }
+    }
+    float2 mu[P], rs[P], sc[P];
+    if (on) {
+      float2 bb[P], t0[P], t1[P];
+      const float* pm = mean + (long long)n * a.G;
+      const float* pr = rstd + (long long)n * a.G;
+      per_channel<VEC>(mu, [&](int e) { return -pm[g[e]]; });
+      per_channel<VEC>(rs, [&](int e) { return pr[g[e]]; });
+      per_channel<VEC>(sc, [&](int e) { return w ? w[c + e] : 1.f; });
+      per_channel<VEC>(bb, [&](int e) { return b ? b[c + e] : 0.f; });
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        sc[i] = mul2(sc[i], rs[i]);
+        t0[i] = t1[i] = make_float2(0.f, 0.f);
+      }
+      copy_wait();
+      int at = 0;
+#pragma unroll 2
+      for (int r = ty; r < rows; r += p.ty, at += step) {
+        float2 f[P], d[P];
+        load_pairs<T, VEC>(pd + at, f);
+        load_pairs<T, VEC>(reinterpret_cast<T*>(pz + at), d);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 xm = add2(f[i], mu[i]);
+          d[i] = through2<ACT>(d[i], fma2(xm, sc[i], bb[i]));
+          t0[i] = add2(t0[i], d[i]);
+          t1[i] = fma2(d[i], xm, t1[i]);
+        }
+        if constexpr (ACT != ACT_NONE || sizeof(T) == 2) store_floats<VEC>(pz + at, d);
+      }
+      float* s = st + ty * a.C + c;
+#pragma unroll
+      for (int i = 0; i < P; ++i) t1[i] = mul2(t1[i], rs[i]);
+      each_channel<VEC>(t0, [&](int e, float v) { s[e] = v; });
+      each_channel<VEC>(t1, [&](int e, float v) { s[p.ty * a.C + e] = v; });
+    }
+    __syncthreads();
+    float* mine = part + ((long long)n * p.splits + split) * 2 * a.C;
+    lane_sums(st, p.ty, a.C, tmp, [&](int j, float t) {
+      mine[j] = t;
+      ch[j] = t * (w ? w[j >= a.C ? j - a.C : j] : 1.f);
+    });
+    __syncthreads();
+    float* all = gpart + (long long)n * p.splits * 2 * a.G;
+    for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
+      const int k = j >= a.G, gg = j - k * a.G;
+      float t = 0.f;
+      for (int i = lane; i < a.Cg; i += 32) t += ch[k * a.C + gg * a.Cg + i];
+      t = warp_sum(t);
+      if (lane == 0) all[split * 2 * a.G + j] = t;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) is_last = atomicAdd(p.sync + 1 + n, 1u) + 1 == (unsigned)p.splits;
+    if (!wait_for(p.sync + 1 + n, p.splits)) return;
+    queue.fetch(p);  // not before: the next range may be of this sample
+    const bool adds = is_last != 0;
+    for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
+      float t = 0.f;
+      for (int s = lane; s < p.splits; s += 32) t += __ldcg(all + s * 2 * a.G + j);
+      t = warp_sum(t);
+      if (lane == 0) g_all[j] = t * inv;
+    }
+    __syncthreads();
+    if (on) {
+      // dx = rstd (w dz - s1 - xhat s2)
+      float2 k0[P], k1[P];
+      per_channel<VEC>(k0, [&](int e) { return -g_all[g[e]]; });
+      per_channel<VEC>(k1, [&](int e) { return -g_all[a.G + g[e]]; });
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        k0[i] = mul2(k0[i], rs[i]);
+        k1[i] = mul2(mul2(k1[i], rs[i]), rs[i]);
+      }
+      T* po = dx + (n * a.S + r0 + ty) * a.C + c;
+      const long long ostep = (long long)p.ty * a.C;
+      int at = 0;
+#pragma unroll 2
+      for (int r = ty; r < rows; r += p.ty, at += step, po += ostep) {
+        float2 f[P], d[P];
+        load_pairs<T, VEC>(pd + at, f);
+        load_floats<VEC>(pz + at, d);
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = fma2(sc[i], d[i], fma2(add2(f[i], mu[i]), k1[i], k0[i]));
+        store_pairs<T, VEC>(po, f);
+      }
+    }
+    if (adds) {
+      const float* from = part + (long long)n * p.splits * 2 * a.C;
+      for (int j = tid; j < 2 * a.C; j += kThreads) {
+        float t = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < p.splits; ++s) t += __ldcg(from + (long long)s * 2 * a.C + j);
+        sums[(long long)n * 2 * a.C + j] = t;
+      }
+    }
+  }
+}
+
+// Shared memory of one CTA of the spread forms.
+inline long long spread_smem(int op, int C, int G, int ty, long long rows, int es) {
+  return op == WTCONV_OP_GN_FWD ? rows * C * es + 16 + 4LL * (2 * ty * C + 2 * G)
+                                : rows * C * (es + 4) + 32 + 4LL * (2 * ty * C + 2 * C + 2 * G + kThreads);
+}
+
+// ---------------------------------------------------------------- streamed
 
 // part[n][split][G] = (mean, m2) over the split's rows; the last CTA of a
 // sample writes its mean and rstd.
@@ -673,15 +948,20 @@ fwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p,
   constexpr int P = kPairs<VEC>;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  Queue queue(p);
   while (true) {
-    const Item it = next_item(a, p);
+    // The next item is fetched while this one is worked on.  An item held back
+    // is later in the queue than the one its CTA works on, so whoever waits for
+    // it still waits for the front of the queue, which nothing holds up.
+    const Item it = item_at(a, p, queue.take());
+    queue.fetch(p);
     if (!it.some) return;
     const long long n = it.n;
     if (!it.apply) {
       fwd_read<T, VEC>(a, p, n, it.split, x, part, mean, rstd, sm);
       continue;
     }
-    if (!wait_sample(a, p, n)) return;
+    if (!wait_for(p.sync + 1 + a.N + n, 1)) return;
     if (ty >= p.ty) continue;
     const long long r0 = (long long)it.split * p.rows, r1 = min(r0 + p.rows, a.S);
     const int rows = (int)(r1 - r0);
@@ -698,10 +978,10 @@ fwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p,
 #pragma unroll 4
       for (int r = ty; r < rows; r += p.ty, px += xstep, py += ystep) {
         float2 f[P];
-        load_pairs<T, VEC>(px, f);
+        load_pairs<T, VEC, true>(px, f);
 #pragma unroll
         for (int i = 0; i < P; ++i) f[i] = act2<ACT>(fma2(add2(f[i], mu[i]), sc[i], sh[i]));
-        store_pairs<T, VEC>(py, f);
+        store_pairs<T, VEC, true>(py, f);
       }
     }
   }
@@ -798,15 +1078,20 @@ bwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p,
   constexpr int P = kPairs<VEC>;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  Queue queue(p);
   while (true) {
-    const Item it = next_item(a, p);
+    // The next item is fetched while this one is worked on.  An item held back
+    // is later in the queue than the one its CTA works on, so whoever waits for
+    // it still waits for the front of the queue, which nothing holds up.
+    const Item it = item_at(a, p, queue.take());
+    queue.fetch(p);
     if (!it.some) return;
     const long long n = it.n;
     if (!it.apply) {
       bwd_read<T, VEC, ACT>(a, p, n, it.split, dy, x, mean, rstd, w, b, part, sums, means, sm);
       continue;
     }
-    if (!wait_sample(a, p, n)) return;
+    if (!wait_for(p.sync + 1 + a.N + n, 1)) return;
     if (ty >= p.ty) continue;
     const long long r0 = (long long)it.split * p.rows, r1 = min(r0 + p.rows, a.S);
     const int rows = (int)(r1 - r0);
@@ -830,15 +1115,15 @@ bwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p,
 #pragma unroll 2
       for (int r = ty; r < rows; r += p.ty, px += xstep, py += dstep, po += ostep) {
         float2 f[P], d[P];
-        load_pairs<T, VEC>(px, f);
-        load_pairs<T, VEC>(py, d);
+        load_pairs<T, VEC, true>(px, f);
+        load_pairs<T, VEC, true>(py, d);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const float2 xm = add2(f[i], mu[i]);
           const float2 z = through2<ACT>(d[i], fma2(xm, sc[i], bb[i]));
           f[i] = fma2(sc[i], z, fma2(xm, k1[i], k0[i]));
         }
-        store_pairs<T, VEC>(po, f);
+        store_pairs<T, VEC, true>(po, f);
       }
     }
   }
@@ -881,9 +1166,10 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int cluster, int smem, cudaStrea
 }
 
 // One launch of a streamed kernel: as many CTAs as the GPU holds at once.
+// `jobs`: queue entries of a sample's range.
 template <typename K, typename... A>
-cudaError_t launch_streamed(K kernel, const wtconv_gn_desc_t& d, const GnPlan& p, int smem, void* ws, cudaStream_t s,
-                            A... args) {
+cudaError_t launch_streamed(K kernel, int jobs, const wtconv_gn_desc_t& d, const GnPlan& p, int smem, void* ws,
+                            cudaStream_t s, A... args) {
   cudaError_t e = wt::ensure_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   e = cudaMemsetAsync(ws, 0, (size_t)(1 + 2 * d.N) * 4, s);
@@ -891,11 +1177,21 @@ cudaError_t launch_streamed(K kernel, const wtconv_gn_desc_t& d, const GnPlan& p
   int per_sm = wt::occupancy((const void*)kernel, kThreads, smem), sms = wt::sm_count();
   if (per_sm < 1) per_sm = 1;
   if (sms < 1) sms = 152;
-  const long long items = 2 * d.N * p.splits;
-  const long long grid = items < (long long)per_sm * sms ? items : (long long)per_sm * sms;
+  const long long items = jobs * d.N * p.splits, slots = (long long)per_sm * sms;
+  const long long grid = items < slots ? items : slots;
+  if (jobs == 1 && p.splits > slots) return cudaErrorInvalidConfiguration;  // the plan sees to it
   const Streamed q = {p.tx, p.ty, p.splits, p.rows, p.lag, (unsigned int*)ws};
-  kernel<<<(unsigned)grid, kThreads, smem, s>>>(args_of(d), q, args...);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = jobs == 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args_of(d), q, args...);
 }
 
 // bwd_reduce, its launch overlapping the end of the kernel before it
@@ -925,11 +1221,16 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
     return launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)x, w, b,
                           (T*)y, mean, rstd);
   }
+  if (p.spread) {
+    const int smem = (int)spread_smem(WTCONV_OP_GN_FWD, d.C, d.G, p.ty, p.rows, sizeof(T));
+    return launch_streamed(fwd_spread<T, VEC, ACT>, 1, d, p, smem, ws, s, (const T*)x, w, b,
+                           (float2*)((char*)ws + p.part_at), (T*)y, mean, rstd);
+  }
   if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
     const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
-    return launch_streamed(fwd_streamed<T, VEC, ACT>, d, p, smem, ws, s, (const T*)x, w, b,
+    return launch_streamed(fwd_streamed<T, VEC, ACT>, 2, d, p, smem, ws, s, (const T*)x, w, b,
                            (float2*)((char*)ws + p.part_at), (T*)y, mean, rstd);
   }
 }
@@ -953,6 +1254,14 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
     if (e != cudaSuccess) return e;
     e = launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)dy,
                        (const T*)x, mean, rstd, w, b, (T*)dx, part);
+  } else if (p.spread) {
+    float* part = (float*)((char*)ws + p.part_at);
+    float* sum = part + (size_t)d.N * p.splits * 2 * d.C;
+    float* gpart = sum + (size_t)d.N * 2 * d.C;
+    sums = sum;
+    const int smem = (int)spread_smem(WTCONV_OP_GN_BWD, d.C, d.G, p.ty, p.rows, sizeof(T));
+    e = launch_streamed(bwd_spread<T, VEC, ACT>, 1, d, p, smem, ws, s, (const T*)dy, (const T*)x, mean, rstd, w, b,
+                        part, gpart, sum, (T*)dx);
   } else if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
@@ -962,7 +1271,7 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
     float* sum = part + (size_t)d.N * p.splits * 2 * d.C;
     float* means = sum + (size_t)d.N * 2 * d.C;
     sums = sum;
-    e = launch_streamed(bwd_streamed<T, VEC, ACT>, d, p, smem, ws, s, (const T*)dy, (const T*)x, mean, rstd, w, b, part,
+    e = launch_streamed(bwd_streamed<T, VEC, ACT>, 2, d, p, smem, ws, s, (const T*)dy, (const T*)x, mean, rstd, w, b, part,
                         sum, means, (T*)dx);
   }
   if (e != cudaSuccess || (!dw && !db)) return e;

@@ -103,13 +103,15 @@ __device__ __forceinline__ void widen_pairs(const Vec<T, VEC>& a, float2 (&v)[kP
     }
   }
 }
-template <typename T, int VEC>
+// LAST: nothing will read the line again, the L2 may drop it first.
+template <typename T, int VEC, bool LAST = false>
 __device__ __forceinline__ void load_pairs(const T* p, float2 (&v)[kPairs<VEC>]) {
   Vec<T, VEC> a;
-  a.load(p);
+  if constexpr (LAST) a.r = __ldcs(reinterpret_cast<const typename Vec<T, VEC>::raw*>(p));
+  else a.load(p);
   widen_pairs<T, VEC>(a, v);
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool LAST = false>
 __device__ __forceinline__ void store_pairs(T* p, const float2 (&v)[kPairs<VEC>]) {
   Vec<T, VEC> a;
   if constexpr (VEC == 1) {
@@ -128,7 +130,8 @@ __device__ __forceinline__ void store_pairs(T* p, const float2 (&v)[kPairs<VEC>]
       }
     }
   }
-  a.store(p);
+  if constexpr (LAST) __stcs(reinterpret_cast<typename Vec<T, VEC>::raw*>(p), a.r);
+  else a.store(p);
 }
 
 // The same for float32 in shared memory, 16 bytes at a time.

@@ -243,7 +243,7 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* d, void* const* weight,
 
 unsigned int wtconv_block_device_faults(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return 0;
-  return wtb::ns_take_faults() + wtb::gn_take_faults();
+  return wtb::ns_take_faults();
 }
 
 }  // extern "C"

@@ -8,16 +8,19 @@
 
 namespace wtb {
 
+// Channel sums of up to kReduceOnce blocks are added up by one launch, those of
+// more by two, the first over this many ranges of them.
+constexpr int kReduceOnce = 512, kReduceRanges = 32;
+
 struct GnPlan {
   int vec;         // elements of one access (a divisor of C; 16 bytes where alignment allows)
   int tx, ty;      // threads over channel vectors and over rows
   int rows;        // rows of one CTA
   int cluster;     // resident form: CTAs of a cluster (0: streamed)
   int ch;          // resident form: channels of a CTA
-  int spread;      // spread form
-  int splits;      // spread and streamed form: row ranges of one sample
-  int lag;         // streamed form: samples read ahead
-  size_t part_at;  // both: where the ranges' sums lie in the workspace
+  int splits;      // streamed form: row ranges of one sample, one CTA each
+  int batch;       // streamed form: samples of one launch
+  size_t tmp_at;   // backward: where the first of two reductions writes
   size_t ws_bytes;
 };
 
@@ -49,6 +52,5 @@ struct NsCall {
 size_t ns_workspace(const wtconv_ns_desc_t& d);
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& c, const NsPointers& p, void* ws, cudaStream_t s);
 unsigned int ns_take_faults();
-unsigned int gn_take_faults();
 
 }  // namespace wtb

@@ -8,18 +8,19 @@ namespace wtb {
   cudaError_t gn_fwd_##n(const wtconv_gn_desc_t&, const GnPlan&, const void*, const float*, const float*, void*,   \
                          float*, float*, void*, cudaStream_t);                                                     \
   cudaError_t gn_bwd_##n(const wtconv_gn_desc_t&, const GnPlan&, const void*, const void*, const float*,           \
-                         const float*, const float*, const float*, void*, float*, float*, void*, cudaStream_t);    \
-  unsigned int gn_faults_##n();
+                         const float*, const float*, const float*, void*, float*, float*, void*, cudaStream_t);
 WTB_DECLARE(f32)
 WTB_DECLARE(f16)
 WTB_DECLARE(bf16)
 #undef WTB_DECLARE
 long long gn_resident_smem(int op, int ch, int ty, long long rows, int groups, int es);
-long long gn_spread_smem(int op, int C, int G, int ty, long long rows, int es);
 
 namespace {
 
 constexpr int kThreads = 256;
+// Samples of one launch of the streamed form: what its second reading still
+// finds in the L2 (129 MB, of which each half may hold a copy).
+constexpr long long kBatchBytes = 1000LL << 20;
 constexpr long long kSmemCta = 113 * 1024, kSmemSm = 228 * 1024;  // two CTAs an SM at least
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -64,32 +65,6 @@ void plan_resident(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& 
   }
 }
 
-// The spread form: ranges of as many rows as two to four CTAs an SM have room
-// for; false where the GPU does not hold a sample.
-bool plan_spread(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& p) {
-  const int es = d.dtype == WTCONV_F32 ? 4 : 2;
-  if (d.C / vec > kThreads) return false;
-  p.tx = d.C / vec;
-  p.ty = kThreads / p.tx;
-  for (int occ = op == WTCONV_OP_GN_FWD ? 4 : 3; occ >= 2; --occ) {
-    const long long room = kSmemSm / occ - 1024 - gn_spread_smem(op, d.C, d.G, p.ty, 0, es);
-    const long long row = (long long)d.C * (op == WTCONV_OP_GN_FWD ? es : es + 4);
-    long long fit = room / row;
-    if (fit < p.ty) continue;
-    fit -= fit % p.ty;  // whole passes
-    long long splits = (d.S + fit - 1) / fit;
-    // half of the CTAs at most, so that a second sample is under way
-    if (2 * splits > (long long)occ * sms) continue;
-    // small samples: enough ranges to fill the GPU
-    const long long want = ((long long)occ * sms + d.N - 1) / d.N, most = (d.S + 4LL * p.ty - 1) / (4LL * p.ty);
-    if (splits < want) splits = want < most ? want : most > splits ? most : splits;
-    p.rows = (int)((d.S + splits - 1) / splits);
-    p.splits = (int)((d.S + p.rows - 1) / p.rows);
-    return true;
-  }
-  return false;
-}
-
 GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   GnPlan p = {};
   const int widest = d.dtype == WTCONV_F32 ? 4 : 8;
@@ -99,37 +74,33 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   plan_resident(d, op, vec, sms, p);
   const size_t n = (size_t)d.N;
-  if (!p.cluster) p.spread = plan_spread(d, op, vec, sms, p);
-  if (!p.cluster && !p.spread && vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
+  size_t blocks = 0;  // of channel sums
   if (p.cluster) {
-    p.ws_bytes = op == WTCONV_OP_GN_FWD ? 0 : n * p.cluster * 2 * d.C * 4;
-  } else if (p.spread) {
-    p.part_at = ((n + 1) * 4 + (n + 1) * 4 + 255) & ~(size_t)255;  // the queue and the samples' counters first
-    p.ws_bytes = p.part_at + (op == WTCONV_OP_GN_FWD ? n * p.splits * d.G * 8
-                                                     : n * (p.splits + 1) * 2 * d.C * 4 + n * p.splits * 2 * d.G * 4);
+    if (op == WTCONV_OP_GN_BWD) blocks = n * p.cluster;
   } else {
+    if (vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
     p.tx = d.C / vec < kThreads ? d.C / vec : kThreads;
     p.ty = kThreads / p.tx;
-    // Samples are read 16 MB ahead of their second reading, and some 20 MB are
-    // being read or applied: near enough for the L2, whose halves may each hold
-    // a line.  Ranges of 32 KB of x, at least 8 rows a thread.
     const int es = d.dtype == WTCONV_F32 ? 4 : 2;
-    const long long bytes = d.S * d.C * es, all = bytes * (op == WTCONV_OP_GN_FWD ? 1 : 2);
-    long long lag = (16LL << 20) / all;
-    if (lag < 1) lag = 1;
-    if (lag > d.N) lag = d.N;
-    p.lag = (int)lag;
-    long long want = bytes >> 15;
+    const long long sample = d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2), slots = 4LL * sms;
+    long long batch = kBatchBytes / sample;
+    if (batch < 1) batch = 1;
+    if (batch > d.N) batch = d.N;
+    const long long launches = (d.N + batch - 1) / batch;
+    p.batch = (int)((d.N + launches - 1) / launches);
+    // one wave of CTAs a launch, at least 8 rows a thread
+    long long want = slots / p.batch;
     const long long most = (d.S + 8LL * p.ty - 1) / (8LL * p.ty);
     if (want > most) want = most;
-    if (want > 4096) want = 4096;
     if (want < 1) want = 1;
     p.rows = (int)((d.S + want - 1) / want);
     p.splits = (int)((d.S + p.rows - 1) / p.rows);
-    p.part_at = ((2 * n + 1) * 4 + 255) & ~(size_t)255;  // the queue and the samples' counters first
-    p.ws_bytes = p.part_at + (op == WTCONV_OP_GN_FWD ? n * p.splits * d.G * 8
-                                                     : n * (p.splits + 1) * 2 * d.C * 4 + n * 2 * d.G * 4);
+    p.ws_bytes = n * p.splits * d.G * 8;
+    if (op == WTCONV_OP_GN_BWD) blocks = n * p.splits;
   }
+  p.ws_bytes += blocks * 2 * d.C * 4;
+  p.tmp_at = p.ws_bytes;
+  if (blocks) p.ws_bytes += kReduceRanges * 2 * (size_t)d.C * 4;
   p.ws_bytes = (p.ws_bytes + 255) & ~(size_t)255;
   return p;
 }
@@ -174,7 +145,5 @@ cudaError_t gn_launch_bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void
   const auto f = d.dtype == WTCONV_F32 ? gn_bwd_f32 : d.dtype == WTCONV_F16 ? gn_bwd_f16 : gn_bwd_bf16;
   return f(d, p, dy, x, mean, rstd, w, b, dx, dw, db, ws, s);
 }
-
-unsigned int gn_take_faults() { return gn_faults_f32() + gn_faults_f16() + gn_faults_bf16(); }
 
 }  // namespace wtb

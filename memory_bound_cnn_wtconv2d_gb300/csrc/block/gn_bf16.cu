@@ -11,5 +11,4 @@ cudaError_t gn_bwd_bf16(const wtconv_gn_desc_t& d, const GnPlan& p, const void* 
                       cudaStream_t s) {
   return gn::bwd_typed<__nv_bfloat16>(d, p, dy, x, mean, rstd, w, b, dx, dw, db, ws, s);
 }
-unsigned int gn_faults_bf16() { return gn::take_faults(); }
 }  // namespace wtb

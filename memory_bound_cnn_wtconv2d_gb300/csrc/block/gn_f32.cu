@@ -14,8 +14,4 @@ cudaError_t gn_bwd_f32(const wtconv_gn_desc_t& d, const GnPlan& p, const void* d
 long long gn_resident_smem(int op, int ch, int ty, long long rows, int groups, int es) {
   return gn::resident_smem(op, ch, ty, rows, groups, es);
 }
-unsigned int gn_faults_f32() { return gn::take_faults(); }
-long long gn_spread_smem(int op, int C, int G, int ty, long long rows, int es) {
-  return gn::spread_smem(op, C, G, ty, rows, es);
-}
 }  // namespace wtb

@@ -1,15 +1,12 @@
 // Group norm with an activation, channels last.
 //
-// Three forms.  Resident: a cluster of up to eight CTAs holds one sample's rows
+// Two forms.  Resident: a cluster of up to eight CTAs holds one sample's rows
 // of a range of channels (whole groups) in shared memory, so that x (and dy)
 // cross the memory once: read, statistics, cluster exchange, written.
-// Spread: the same over the whole GPU; CTAs take row ranges off a queue, hold
-// them in shared memory and exchange statistics through memory, two to four
-// samples being under way at once.
-// Streamed, for samples that no cluster holds: one pass for the statistics and
-// one that applies them, in one launch whose CTAs take row ranges off a queue
-// that applies a sample some 40 MB after it was read, so that the second read
-// hits the L2 and both passes overlap to the end.
+// Streamed: one launch for the statistics and one that applies them, over
+// batches of samples small enough for the second reading to hit the L2, each
+// launch one wave of CTAs; a launch's CTAs move in as those of the one before
+// leave.
 //
 // A thread owns VEC consecutive channels (16 bytes where alignment allows) and
 // walks down rows, so that a warp reads whole lines of consecutive pixels and
@@ -460,17 +457,20 @@ bwd_resident(const __grid_constant__ Args a, const __grid_constant__ Resident p,
   if (p.cluster > 1) cluster_wait();
 }
 
-// dweight, dbias: part[blocks][2][C] over its blocks.  A CTA of 32 channels x
-// 32 lanes; lane l adds blocks l, l + 32, ..., the lanes are added in order.
+// dweight, dbias: part[blocks][2][C] over its blocks, or, of several CTAs
+// along y, each a range of the blocks into out[y][2][C] (the second launch adds
+// those).  A CTA of 32 channels x 32 lanes; lane l adds blocks l, l + 32, ...,
+// the lanes are added in order.
 static __global__ void __launch_bounds__(1024)
-bwd_reduce(int C, long long blocks, const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db) {
+bwd_reduce(int C, long long blocks, long long per, const float* part, float* out, float* dw, float* db) {
   __shared__ float sh[2][32][33];
   const int cc = threadIdx.x & 31, lane = threadIdx.x >> 5, c = blockIdx.x * 32 + cc;
+  const long long first = blockIdx.y * per, stop = min(blocks, first + per);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float t0 = 0.f, t1 = 0.f;
   if (c < C) {
 #pragma unroll 4
-    for (long long k = lane; k < blocks; k += 32) {
+    for (long long k = first + lane; k < stop; k += 32) {
       t0 += part[(k * 2) * C + c];
       t1 += part[(k * 2 + 1) * C + c];
     }
@@ -482,372 +482,32 @@ bwd_reduce(int C, long long blocks, const float* __restrict__ part, float* __res
     float t = 0.f;
 #pragma unroll
     for (int l = 0; l < 32; ++l) t += sh[lane][l][cc];
-    float* out = lane ? dw : db;
-    if (out && c < C) out[c] = t;
+    float* to = out ? out + (blockIdx.y * 2 + lane) * (long long)C : lane ? dw : db;
+    if (to && c < C) to[c] = t;
   }
-}
-
-// ---------------------------------------------------------------- queues
-
-// Of both the spread and the streamed form.
-struct Streamed {
-  int tx, ty;        // threads across channel vectors, rows side by side
-  int splits, rows;  // row ranges of a sample: the queue's items
-  int lag;           // samples that are read ahead of the one applied
-  unsigned int* sync;  // [0] the queue; [1 + n] ranges of sample n that are read; [1 + N + n] its statistics are there
-};
-
-// Waits of this type's kernels that gave up.
-static __device__ unsigned int g_gn_faults;
-constexpr long long kWaitCycles = 1ll << 31;  // about a second
-
-// The queue: `lag` samples to read, then one to apply and one to read in
-// turn, then the rest to apply, `splits` items each.
-struct Item {
-  bool some, apply;
-  long long n;
-  int split;
-};
-__device__ __forceinline__ Item item_at(const Args& a, const Streamed& p, unsigned int i) {
-  Item t;
-  const int job = (int)(i / (unsigned)p.splits), N = (int)a.N;
-  t.some = job < 2 * N;
-  t.split = (int)(i - (unsigned)job * (unsigned)p.splits);
-  const int k = job - p.lag, both = 2 * (N - p.lag);
-  t.apply = k >= 0 && (k >= both || !(k & 1));
-  t.n = k < 0 ? job : k >= both ? N - p.lag + (k - both) : t.apply ? k >> 1 : p.lag + (k >> 1);
-  return t;
-}
-
-// Takes items off the queue, one fetched ahead.
-struct Queue {
-  unsigned int next, turn;  // of thread 0: the item after this one
-  __device__ __forceinline__ Queue(const Streamed& p) : next(0), turn(0) { fetch(p); }
-  __device__ __forceinline__ void fetch(const Streamed& p) {
-    if (threadIdx.x == 0) next = atomicAdd(p.sync, 1u);
-  }
-  // also the barrier between two items
-  __device__ __forceinline__ unsigned int take() {
-    __shared__ unsigned int at[2];
-    turn ^= 1;
-    if (threadIdx.x == 0) at[turn] = next;
-    __syncthreads();
-    return at[turn];
-  }
-};
-
-// Waits until *flag is `least` or more; false: it gave up.  The CTAs that it
-// waits for took their items earlier (see the callers), so this ends.
-__device__ __forceinline__ bool wait_for(const unsigned int* flag, unsigned int least) {
-  bool ok = true;
-  if (threadIdx.x == 0) {
-    const long long t0 = clock64();
-    unsigned int v;
-    while (true) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-      if (v >= least) break;
-      if (clock64() - t0 > kWaitCycles) {
-        atomicAdd(&g_gn_faults, 1u);
-        ok = false;
-        break;
-      }
-    }
-  }
-  return __syncthreads_and(ok);
-}
-
-// Whether this CTA is the sample's last to arrive here, having written its
-// part: it then adds the parts up (in their order, whichever CTA it is) and
-// raises the sample's flag.
-__device__ __forceinline__ bool last_of_sample(const Streamed& p, long long n) {
-  __shared__ int is_last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) is_last = atomicAdd(p.sync + 1 + n, 1u) + 1 == (unsigned)p.splits;
-  __syncthreads();
-  if (is_last) __threadfence();
-  return is_last;
-}
-__device__ __forceinline__ void raise_sample(const Args& a, const Streamed& p, long long n) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(p.sync + 1 + a.N + n) : "memory");
-  }
-}
-
-// ---------------------------------------------------------------- spread
-
-// The queue holds the samples' ranges in order.  A CTA keeps its range until
-// all ranges of the sample are read.  The launch is cooperative, so that all
-// its CTAs run, and no sample has more ranges than there are CTAs; a later
-// sample's are taken after an earlier one's, so the earliest unfinished sample
-// always has all its ranges at work.
-
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 4)
-fwd_spread(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
-           const float* __restrict__ w, const float* __restrict__ b, float2* part, T* __restrict__ y,
-           float* __restrict__ mean_out, float* __restrict__ rstd_out) {
-  constexpr int P = kPairs<VEC>;
-  extern __shared__ __align__(16) unsigned char raw[];
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31, c = tx * VEC;
-  const bool on = ty < p.ty, whole = a.Cg % VEC == 0;
-  T* data = reinterpret_cast<T*>(raw);  // [rows][C]; a thread only touches what it copied
-  T* pd = data + ty * a.C + c;
-  float* st = reinterpret_cast<float*>(raw + (((long long)p.rows * a.C * sizeof(T) + 15) & ~15LL));  // [2][ty][C]
-  float* g_all = st + 2 * p.ty * a.C;  // [2][G]
-  const int step = p.ty * a.C;
-  const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
-  int g[VEC];
-  groups_of<VEC>(c, a.Cg, g);
-  Queue queue(p);
-  while (true) {
-    const unsigned int it = queue.take();
-    const int n = (int)(it / (unsigned)p.splits), split = (int)(it - (unsigned)n * (unsigned)p.splits);
-    if (n >= (int)a.N) return;
-    const long long r0 = (long long)split * p.rows;
-    const int rows = (int)min((long long)p.rows, a.S - r0), stop = on ? rows : 0;
-    {
-      const T* from = x + n * a.xs + (r0 + ty) * a.xr + c;
-      T* to = pd;
-#pragma unroll 4
-      for (int r = ty; r < stop; r += p.ty, from += p.ty * a.xr, to += step) copy_async<VEC * sizeof(T)>(to, from);
-    }
-    copy_wait();
-    if (on) {
-      float2 f[P], m[P], q[P];
-      const int mine = ty < rows ? (rows - ty + p.ty - 1) / p.ty : 0;
-      if (mine) {
-        Running<VEC> run;
-        const T* at = pd;
-        load_pairs<T, VEC>(at, f);
-        run.begin(f);
-#pragma unroll 2
-        for (int i = 1; i < mine; ++i) {
-          at += step;
-          load_pairs<T, VEC>(at, f);
-          run.add(f);
-        }
-        run.end(mine, m, q);
-      } else {
-#pragma unroll
-        for (int i = 0; i < P; ++i) m[i] = q[i] = make_float2(0.f, 0.f);
-      }
-      put_statistics<VEC>(st, p.ty, whole ? p.tx : a.C, whole, ty, tx, mine, m, q);
-    }
-    __syncthreads();
-    float2* all = part + (long long)n * p.splits * a.G;
-    group_statistics(st, p.ty, whole ? p.tx : a.C, whole ? a.Cg / VEC : a.Cg, whole ? VEC : 1, a.G, rows,
-                     [&](int k, float m, float q) { all[split * a.G + k] = make_float2(m, q); });
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) atomicAdd(p.sync + 1 + n, 1u);
-    if (!wait_for(p.sync + 1 + n, p.splits)) return;
-    queue.fetch(p);  // not before: the next range may be of this sample
-    for (int k = tid >> 5; k < a.G; k += kThreads / 32) {  // one warp per group
-      float t = 0.f;
-      for (int s = lane; s < p.splits; s += 32)
-        t = fmaf(s + 1 < p.splits ? (float)p.rows : last, __ldcg(all + s * a.G + k).x, t);
-      const float mean = warp_sum(t) / (float)a.S;
-      t = 0.f;
-      for (int s = lane; s < p.splits; s += 32) {
-        const float2 v = __ldcg(all + s * a.G + k);
-        const float d = v.x - mean;
-        t += fmaf((s + 1 < p.splits ? (float)p.rows : last) * (float)a.Cg * d, d, v.y);
-      }
-      const float rs = rsqrtf(warp_sum(t) / ((float)a.S * (float)a.Cg) + a.eps);
-      if (lane == 0) {
-        g_all[k] = mean;
-        g_all[a.G + k] = rs;
-        if (split == 0) {
-          mean_out[(long long)n * a.G + k] = mean;
-          rstd_out[(long long)n * a.G + k] = rs;
-        }
-      }
-    }
-    __syncthreads();
-    if (on) {
-      float2 mu[P], sc[P], sh[P];
-      per_channel<VEC>(mu, [&](int e) { return -g_all[g[e]]; });
-      per_channel<VEC>(sc, [&](int e) { return g_all[a.G + g[e]] * (w ? w[c + e] : 1.f); });
-      per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
-      T* py = y + (n * a.S + r0 + ty) * a.C + c;
-      const T* at = pd;
-      const long long ystep = (long long)p.ty * a.C;
-#pragma unroll 2
-      for (int r = ty; r < rows; r += p.ty, at += step, py += ystep) {
-        float2 f[P];
-        load_pairs<T, VEC>(at, f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = act2<ACT>(fma2(add2(f[i], mu[i]), sc[i], sh[i]));
-        store_pairs<T, VEC>(py, f);
-      }
-    }
-  }
-}
-
-// part[n][split][2][C]: sums of dz and of dz * xhat over the range; gpart
-// [n][split][2][G]: the groups' weighted sums.  The CTA that read a sample's
-// last range adds the parts up into sums[n][2][C].
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 3)
-bwd_spread(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
-           const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
-           const float* __restrict__ w, const float* __restrict__ b, float* part, float* gpart, float* sums,
-           T* __restrict__ dx) {
-  constexpr int P = kPairs<VEC>;
-  extern __shared__ __align__(16) unsigned char raw[];
-  __shared__ int is_last;
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31, c = tx * VEC;
-  const bool on = ty < p.ty;
-  const int step = p.ty * a.C;
-  // [rows][C] each; a thread only touches what it copied.  dy lands in the
-  // first bytes of its dz slots.
-  float* dz = reinterpret_cast<float*>(raw);
-  T* data = reinterpret_cast<T*>(dz + (((long long)p.rows * a.C + 3) & ~3LL));
-  T* pd = data + ty * a.C + c;
-  float* pz = dz + ty * a.C + c;
-  float* st = reinterpret_cast<float*>(  // [2][ty][C]
-      raw + (((((long long)p.rows * a.C + 3) & ~3LL) * 4 + (long long)p.rows * a.C * sizeof(T) + 15) & ~15LL));
-  float* ch = st + 2 * p.ty * a.C;  // [2][C]
-  float* g_all = ch + 2 * a.C;      // [2][G]
-  float* tmp = g_all + 2 * a.G;
-  int g[VEC];
-  groups_of<VEC>(c, a.Cg, g);
-  const float inv = 1.f / ((float)a.S * (float)a.Cg);
-  Queue queue(p);
-  while (true) {
-    const unsigned int it = queue.take();
-    const int n = (int)(it / (unsigned)p.splits), split = (int)(it - (unsigned)n * (unsigned)p.splits);
-    if (n >= (int)a.N) return;
-    const long long r0 = (long long)split * p.rows;
-    const int rows = (int)min((long long)p.rows, a.S - r0), stop = on ? rows : 0;
-    {
-      const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
-      const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
-      int at = 0;
-#pragma unroll 4
-      for (int r = ty; r < stop; r += p.ty, at += step, px += p.ty * a.xr, py += p.ty * a.dr) {
-        copy_async<VEC * sizeof(T)>(pd + at, px);
-        copy_async<VEC * sizeof(T)>(pz + at, py);
-      }
-    }
-    float2 mu[P], rs[P], sc[P];
-    if (on) {
-      float2 bb[P], t0[P], t1[P];
-      const float* pm = mean + (long long)n * a.G;
-      const float* pr = rstd + (long long)n * a.G;
-      per_channel<VEC>(mu, [&](int e) { return -pm[g[e]]; });
-      per_channel<VEC>(rs, [&](int e) { return pr[g[e]]; });
-      per_channel<VEC>(sc, [&](int e) { return w ? w[c + e] : 1.f; });
-      per_channel<VEC>(bb, [&](int e) { return b ? b[c + e] : 0.f; });
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        sc[i] = mul2(sc[i], rs[i]);
-        t0[i] = t1[i] = make_float2(0.f, 0.f);
-      }
-      copy_wait();
-      int at = 0;
-#pragma unroll 2
-      for (int r = ty; r < rows; r += p.ty, at += step) {
-        float2 f[P], d[P];
-        load_pairs<T, VEC>(pd + at, f);
-        load_pairs<T, VEC>(reinterpret_cast<T*>(pz + at), d);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 xm = add2(f[i], mu[i]);
-          d[i] = through2<ACT>(d[i], fma2(xm, sc[i], bb[i]));
-          t0[i] = add2(t0[i], d[i]);
-          t1[i] = fma2(d[i], xm, t1[i]);
-        }
-        if constexpr (ACT != ACT_NONE || sizeof(T) == 2) store_floats<VEC>(pz + at, d);
-      }
-      float* s = st + ty * a.C + c;
-#pragma unroll
-      for (int i = 0; i < P; ++i) t1[i] = mul2(t1[i], rs[i]);
-      each_channel<VEC>(t0, [&](int e, float v) { s[e] = v; });
-      each_channel<VEC>(t1, [&](int e, float v) { s[p.ty * a.C + e] = v; });
-    }
-    __syncthreads();
-    float* mine = part + ((long long)n * p.splits + split) * 2 * a.C;
-    lane_sums(st, p.ty, a.C, tmp, [&](int j, float t) {
-      mine[j] = t;
-      ch[j] = t * (w ? w[j >= a.C ? j - a.C : j] : 1.f);
-    });
-    __syncthreads();
-    float* all = gpart + (long long)n * p.splits * 2 * a.G;
-    for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
-      const int k = j >= a.G, gg = j - k * a.G;
-      float t = 0.f;
-      for (int i = lane; i < a.Cg; i += 32) t += ch[k * a.C + gg * a.Cg + i];
-      t = warp_sum(t);
-      if (lane == 0) all[split * 2 * a.G + j] = t;
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) is_last = atomicAdd(p.sync + 1 + n, 1u) + 1 == (unsigned)p.splits;
-    if (!wait_for(p.sync + 1 + n, p.splits)) return;
-    queue.fetch(p);  // not before: the next range may be of this sample
-    const bool adds = is_last != 0;
-    for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
-      float t = 0.f;
-      for (int s = lane; s < p.splits; s += 32) t += __ldcg(all + s * 2 * a.G + j);
-      t = warp_sum(t);
-      if (lane == 0) g_all[j] = t * inv;
-    }
-    __syncthreads();
-    if (on) {
-      // dx = rstd (w dz - s1 - xhat s2)
-      float2 k0[P], k1[P];
-      per_channel<VEC>(k0, [&](int e) { return -g_all[g[e]]; });
-      per_channel<VEC>(k1, [&](int e) { return -g_all[a.G + g[e]]; });
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        k0[i] = mul2(k0[i], rs[i]);
-        k1[i] = mul2(mul2(k1[i], rs[i]), rs[i]);
-      }
-      T* po = dx + (n * a.S + r0 + ty) * a.C + c;
-      const long long ostep = (long long)p.ty * a.C;
-      int at = 0;
-#pragma unroll 2
-      for (int r = ty; r < rows; r += p.ty, at += step, po += ostep) {
-        float2 f[P], d[P];
-        load_pairs<T, VEC>(pd + at, f);
-        load_floats<VEC>(pz + at, d);
-#pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = fma2(sc[i], d[i], fma2(add2(f[i], mu[i]), k1[i], k0[i]));
-        store_pairs<T, VEC>(po, f);
-      }
-    }
-    if (adds) {
-      const float* from = part + (long long)n * p.splits * 2 * a.C;
-      for (int j = tid; j < 2 * a.C; j += kThreads) {
-        float t = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < p.splits; ++s) t += __ldcg(from + (long long)s * 2 * a.C + j);
-        sums[(long long)n * 2 * a.C + j] = t;
-      }
-    }
-  }
-}
-
-// Shared memory of one CTA of the spread forms.
-inline long long spread_smem(int op, int C, int G, int ty, long long rows, int es) {
-  return op == WTCONV_OP_GN_FWD ? rows * C * es + 16 + 4LL * (2 * ty * C + 2 * G)
-                                : rows * C * (es + 4) + 32 + 4LL * (2 * ty * C + 2 * C + 2 * G + kThreads);
 }
 
 // ---------------------------------------------------------------- streamed
 
-// part[n][split][G] = (mean, m2) over the split's rows; the last CTA of a
-// sample writes its mean and rstd.
+struct Streamed {
+  int tx, ty;        // threads across channel vectors, rows side by side
+  int splits, rows;  // row ranges of a sample, one CTA each
+  int n0;            // the batch's first sample
+};
+
+// Lets the next launch's CTAs in as this one's leave / waits for the launch before.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// part[n][split][G] = (mean, m2) over the split's rows
 template <typename T, int VEC>
-__device__ __forceinline__ void fwd_read(const Args& a, const Streamed& p, long long n, int split,
-                                         const T* __restrict__ x, float2* part, float* mean_out, float* rstd_out,
-                                         float* sm) {
+__global__ void __launch_bounds__(kThreads, 4)
+fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
+         float2* __restrict__ part) {
   constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+  extern __shared__ __align__(16) float sm[];
+  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  const long long n = p.n0 + (int)blockIdx.y;
   const int W = p.tx * VEC;
   float* ch = sm;            // [2][C]
   float* st = sm + 2 * a.C;  // [2][ty][W]
@@ -855,6 +515,7 @@ __device__ __forceinline__ void fwd_read(const Args& a, const Streamed& p, long 
   const int rows = (int)(r1 - r0);
   const T* base = x + n * a.xs + r0 * a.xr;
   const bool whole = a.Cg % VEC == 0 && W >= a.C;  // a thread's channels count as one
+  let_next_in();
   for (int c0 = 0; c0 < a.C; c0 += W) {
     const int c = c0 + tx * VEC;
     if (ty < p.ty) {
@@ -917,91 +578,96 @@ __device__ __forceinline__ void fwd_read(const Args& a, const Streamed& p, long 
   if (whole) group_statistics(st, p.ty, p.tx, a.Cg / VEC, VEC, a.G, rows, put);
   else if (W >= a.C) group_statistics(st, p.ty, W, a.Cg, 1, a.G, rows, put);
   else group_statistics(ch, 1, a.C, a.Cg, 1, a.G, rows, put);
-  if (!last_of_sample(p, n)) return;
-  const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
-  for (int g = tid >> 5; g < a.G; g += kThreads / 32) {
-    const float2* q = part + n * p.splits * a.G + g;
-    float t = 0.f;
-    for (int s = lane; s < p.splits; s += 32)
-      t = fmaf(s + 1 < p.splits ? (float)p.rows : last, __ldcg(q + (long long)s * a.G).x, t);
-    const float mean = warp_sum(t) / (float)a.S;
-    t = 0.f;
-    for (int s = lane; s < p.splits; s += 32) {
-      const float2 v = __ldcg(q + (long long)s * a.G);
-      const float d = v.x - mean;
-      t += fmaf((s + 1 < p.splits ? (float)p.rows : last) * (float)a.Cg * d, d, v.y);
-    }
-    t = warp_sum(t);
-    if (lane == 0) {
-      mean_out[n * a.G + g] = mean;
-      rstd_out[n * a.G + g] = rsqrtf(t / ((float)a.S * (float)a.Cg) + a.eps);
-    }
-  }
-  raise_sample(a, p, n);
+  wait_previous();  // so that a launch never ends before the one before it
 }
 
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, 4)
-fwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
-             const float* __restrict__ w, const float* __restrict__ b, float2* part, T* __restrict__ y, float* mean,
-             float* rstd) {
-  constexpr int P = kPairs<VEC>;
-  extern __shared__ __align__(16) float sm[];
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
-  Queue queue(p);
-  while (true) {
-    // The next item is fetched while this one is worked on.  An item held back
-    // is later in the queue than the one its CTA works on, so whoever waits for
-    // it still waits for the front of the queue, which nothing holds up.
-    const Item it = item_at(a, p, queue.take());
-    queue.fetch(p);
-    if (!it.some) return;
-    const long long n = it.n;
-    if (!it.apply) {
-      fwd_read<T, VEC>(a, p, n, it.split, x, part, mean, rstd, sm);
-      continue;
-    }
-    if (!wait_for(p.sync + 1 + a.N + n, 1)) return;
-    if (ty >= p.ty) continue;
-    const long long r0 = (long long)it.split * p.rows, r1 = min(r0 + p.rows, a.S);
-    const int rows = (int)(r1 - r0);
-    for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
-      float2 mu[P], sc[P], sh[P];
-      int g[VEC];
-      groups_of<VEC>(c, a.Cg, g);
-      per_channel<VEC>(mu, [&](int e) { return -__ldcg(mean + n * a.G + g[e]); });
-      per_channel<VEC>(sc, [&](int e) { return __ldcg(rstd + n * a.G + g[e]) * (w ? w[c + e] : 1.f); });
-      per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
-      const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
-      T* py = y + (n * a.S + r0 + ty) * a.C + c;
-      const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
+fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
+          const float* __restrict__ w, const float* __restrict__ b, const float2* part, T* __restrict__ y,
+          float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
+  extern __shared__ __align__(16) float sm[];  // [2][G]
+  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+  const long long n = p.n0 + (int)blockIdx.y;
+  let_next_in();
+  wait_previous();
+  const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
+  for (int g = tid >> 5; g < a.G; g += kThreads / 32) {                  // one warp per group
+    const float2* q = part + n * p.splits * a.G + g;
+    float t = 0.f;
 #pragma unroll 4
-      for (int r = ty; r < rows; r += p.ty, px += xstep, py += ystep) {
-        float2 f[P];
-        load_pairs<T, VEC, true>(px, f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = act2<ACT>(fma2(add2(f[i], mu[i]), sc[i], sh[i]));
-        store_pairs<T, VEC, true>(py, f);
+    for (int s = lane; s < p.splits; s += 32) t = fmaf(s + 1 < p.splits ? (float)p.rows : last, q[(long long)s * a.G].x, t);
+    const float mean = warp_sum(t) / (float)a.S;
+    t = 0.f;
+#pragma unroll 4
+    for (int s = lane; s < p.splits; s += 32) {
+      const float2 v = q[(long long)s * a.G];
+      const float d = v.x - mean;
+      t += fmaf((s + 1 < p.splits ? (float)p.rows : last) * (float)a.Cg * d, d, v.y);
+    }
+    const float rs = rsqrtf(warp_sum(t) / ((float)a.S * (float)a.Cg) + a.eps);
+    if (lane == 0) {
+      sm[g] = mean;
+      sm[a.G + g] = rs;
+      if (split == 0) {
+        mean_out[n * a.G + g] = mean;
+        rstd_out[n * a.G + g] = rs;
       }
+    }
+  }
+  __syncthreads();
+  if (ty >= p.ty) return;
+  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
+  const int rows = (int)(r1 - r0);
+  for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
+    float2 mu[P], sc[P], sh[P];
+    int g[VEC];
+    groups_of<VEC>(c, a.Cg, g);
+    per_channel<VEC>(mu, [&](int e) { return -sm[g[e]]; });
+    per_channel<VEC>(sc, [&](int e) { return sm[a.G + g[e]] * (w ? w[c + e] : 1.f); });
+    per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
+    const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
+    T* py = y + (n * a.S + r0 + ty) * a.C + c;
+    const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
+    const int left = rows - ty;
+    for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * ystep) {
+      Vec<T, VEC> v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (r + i * p.ty < left) v[i].load_last(px + i * xstep);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (r + i * p.ty < left) {
+          float2 f[P];
+          widen_pairs<T, VEC>(v[i], f);
+#pragma unroll
+          for (int j = 0; j < P; ++j) f[j] = act2<ACT>(fma2(add2(f[j], mu[j]), sc[j], sh[j]));
+          store_pairs<T, VEC, true>(py + i * ystep, f);
+        }
     }
   }
 }
 
-// part[n][split][2][C]: sums of dz and of dz * xhat over the split's rows; the
-// last CTA of a sample writes sums[n][2][C] and means[n][2][G], the groups'
-// weighted means of both.
+// part[n][split][2][C]: sums of dz and of dz * xhat over the split's rows;
+// gpart[n][split][2][G]: the groups' weighted sums.
 template <typename T, int VEC, int ACT>
-__device__ __forceinline__ void bwd_read(const Args& a, const Streamed& p, long long n, int split,
-                                         const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
-                                         const float* __restrict__ rstd, const float* __restrict__ w,
-                                         const float* __restrict__ b, float* part, float* sums, float* means,
-                                         float* sm) {
-  constexpr int P = kPairs<VEC>;
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+__global__ void __launch_bounds__(kThreads, 4)
+bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
+         const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+         const float* __restrict__ w, const float* __restrict__ b, float* __restrict__ part,
+         float* __restrict__ gpart) {
+  constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
+  extern __shared__ __align__(16) float sm[];
+  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+  const long long n = p.n0 + (int)blockIdx.y;
   const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
   const int rows = (int)(r1 - r0), W = p.tx * VEC;
-  float* tmp = sm;            // kThreads
-  float* st = sm + kThreads;  // [2][ty][W]
+  float* ch = sm;               // [2][C], weighted
+  float* tmp = sm + 2 * a.C;    // kThreads
+  float* st = tmp + kThreads;   // [2][ty][W]
+  float* mine = part + (n * p.splits + split) * 2 * a.C;
+  let_next_in();
   for (int c0 = 0; c0 < a.C; c0 += W) {
     const int c = c0 + tx * VEC;
     if (ty < p.ty) {
@@ -1018,18 +684,29 @@ __device__ __forceinline__ void bwd_read(const Args& a, const Streamed& p, long 
         const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
         const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
         const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr;
-#pragma unroll 4
-        for (int r = ty; r < rows; r += p.ty, px += xstep, py += dstep) {
-          float2 f[P], d[P];
-          load_pairs<T, VEC>(px, f);
-          load_pairs<T, VEC>(py, d);
+        const int left = rows - ty;
+        for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * dstep) {
+          Vec<T, VEC> vx[kBatch], vd[kBatch];
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float2 xm = add2(f[i], mu[i]);
-            const float2 z = through2<ACT>(d[i], fma2(xm, sc[i], bb[i]));
-            t0[i] = add2(t0[i], z);
-            t1[i] = fma2(z, xm, t1[i]);
-          }
+          for (int i = 0; i < kBatch; ++i)
+            if (r + i * p.ty < left) {
+              vx[i].load(px + i * xstep);
+              vd[i].load(py + i * dstep);
+            }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (r + i * p.ty < left) {
+              float2 f[P], d[P];
+              widen_pairs<T, VEC>(vx[i], f);
+              widen_pairs<T, VEC>(vd[i], d);
+#pragma unroll
+              for (int j = 0; j < P; ++j) {
+                const float2 xm = add2(f[j], mu[j]);
+                const float2 z = through2<ACT>(d[j], fma2(xm, sc[j], bb[j]));
+                t0[j] = add2(t0[j], z);
+                t1[j] = fma2(z, xm, t1[j]);
+              }
+            }
         }
         float2 rs[P];
         per_channel<VEC>(rs, [&](int e) { return rstd[n * a.G + g[e]]; });
@@ -1041,102 +718,93 @@ __device__ __forceinline__ void bwd_read(const Args& a, const Streamed& p, long 
       each_channel<VEC>(t1, [&](int e, float v) { s[p.ty * W + e] = v; });
     }
     __syncthreads();
-    float* mine = part + (n * p.splits + split) * 2 * a.C + c0;
     lane_sums(st, p.ty, W, tmp, [&](int j, float t) {
-      const int k = j >= W, cc = j - k * W;
-      if (c0 + cc < a.C) mine[k * a.C + cc] = t;
+      const int k = j >= W, cc = c0 + j - k * W;
+      if (cc < a.C) {
+        mine[k * a.C + cc] = t;
+        ch[k * a.C + cc] = t * (w ? w[cc] : 1.f);
+      }
     });
     __syncthreads();
   }
-  if (!last_of_sample(p, n)) return;
-  float* ch = sm;  // [2][C]
-  for (int j = tid; j < 2 * a.C; j += kThreads) {
-    float t = 0.f;
-#pragma unroll 16
-    for (int s = 0; s < p.splits; ++s) t += __ldcg(part + (n * p.splits + s) * 2 * a.C + j);
-    sums[n * 2 * a.C + j] = t;
-    ch[j] = t * (w ? w[j >= a.C ? j - a.C : j] : 1.f);
-  }
-  __syncthreads();
-  const float inv = 1.f / ((float)a.S * (float)a.Cg);
   for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
     const int k = j >= a.G, g = j - k * a.G;
     float t = 0.f;
     for (int i = lane; i < a.Cg; i += 32) t += ch[k * a.C + g * a.Cg + i];
     t = warp_sum(t);
-    if (lane == 0) means[n * 2 * a.G + j] = t * inv;
+    if (lane == 0) gpart[(n * p.splits + split) * 2 * a.G + j] = t;
   }
-  raise_sample(a, p, n);
+  wait_previous();  // so that a launch never ends before the one before it
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 3)
-bwd_streamed(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
-             const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
-             const float* __restrict__ w, const float* __restrict__ b, float* part, float* sums, float* means,
-             T* __restrict__ dx) {
-  constexpr int P = kPairs<VEC>;
-  extern __shared__ __align__(16) float sm[];
-  const int tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
-  Queue queue(p);
-  while (true) {
-    // The next item is fetched while this one is worked on.  An item held back
-    // is later in the queue than the one its CTA works on, so whoever waits for
-    // it still waits for the front of the queue, which nothing holds up.
-    const Item it = item_at(a, p, queue.take());
-    queue.fetch(p);
-    if (!it.some) return;
-    const long long n = it.n;
-    if (!it.apply) {
-      bwd_read<T, VEC, ACT>(a, p, n, it.split, dy, x, mean, rstd, w, b, part, sums, means, sm);
-      continue;
-    }
-    if (!wait_for(p.sync + 1 + a.N + n, 1)) return;
-    if (ty >= p.ty) continue;
-    const long long r0 = (long long)it.split * p.rows, r1 = min(r0 + p.rows, a.S);
-    const int rows = (int)(r1 - r0);
-    for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
-      // dx = rstd (w dz - s1 - xhat s2)
-      float2 mu[P], sc[P], bb[P], k0[P], k1[P];
-      int g[VEC];
-      groups_of<VEC>(c, a.Cg, g);
-      per_channel<VEC>(mu, [&](int e) { return -mean[n * a.G + g[e]]; });
-      per_channel<VEC>(sc, [&](int e) { return rstd[n * a.G + g[e]] * (w ? w[c + e] : 1.f); });
-      per_channel<VEC>(bb, [&](int e) { return b ? b[c + e] : 0.f; });
-      per_channel<VEC>(k0, [&](int e) { return -rstd[n * a.G + g[e]] * __ldcg(means + n * 2 * a.G + g[e]); });
-      per_channel<VEC>(k1, [&](int e) {
-        const float r = rstd[n * a.G + g[e]];
-        return -r * r * __ldcg(means + (n * 2 + 1) * a.G + g[e]);
-      });
-      const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
-      const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
-      T* po = dx + (n * a.S + r0 + ty) * a.C + c;
-      const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
-#pragma unroll 2
-      for (int r = ty; r < rows; r += p.ty, px += xstep, py += dstep, po += ostep) {
-        float2 f[P], d[P];
-        load_pairs<T, VEC, true>(px, f);
-        load_pairs<T, VEC, true>(py, d);
+__global__ void __launch_bounds__(kThreads, 4)
+bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
+          const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+          const float* __restrict__ w, const float* __restrict__ b, const float* gpart, T* __restrict__ dx) {
+  constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
+  extern __shared__ __align__(16) float sm[];  // [2][G]
+  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+  const long long n = p.n0 + (int)blockIdx.y;
+  let_next_in();
+  wait_previous();
+  const float inv = 1.f / ((float)a.S * (float)a.Cg);
+  for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
+    float t = 0.f;
+#pragma unroll 4
+    for (int s = lane; s < p.splits; s += 32) t += gpart[(n * p.splits + s) * 2 * a.G + j];
+    t = warp_sum(t);
+    if (lane == 0) sm[j] = t * inv;
+  }
+  __syncthreads();
+  if (ty >= p.ty) return;
+  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
+  const int rows = (int)(r1 - r0);
+  for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
+    // dx = rstd (w dz - s1 - xhat s2)
+    float2 mu[P], sc[P], bb[P], k0[P], k1[P];
+    int g[VEC];
+    groups_of<VEC>(c, a.Cg, g);
+    per_channel<VEC>(mu, [&](int e) { return -mean[n * a.G + g[e]]; });
+    per_channel<VEC>(sc, [&](int e) { return rstd[n * a.G + g[e]] * (w ? w[c + e] : 1.f); });
+    per_channel<VEC>(bb, [&](int e) { return b ? b[c + e] : 0.f; });
+    per_channel<VEC>(k0, [&](int e) { return -rstd[n * a.G + g[e]] * sm[g[e]]; });
+    per_channel<VEC>(k1, [&](int e) {
+      const float r = rstd[n * a.G + g[e]];
+      return -r * r * sm[a.G + g[e]];
+    });
+    const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
+    const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
+    T* po = dx + (n * a.S + r0 + ty) * a.C + c;
+    const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
+    const int left = rows - ty;
+    for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * dstep, po += kBatch * ostep) {
+      Vec<T, VEC> vx[kBatch], vd[kBatch];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 xm = add2(f[i], mu[i]);
-          const float2 z = through2<ACT>(d[i], fma2(xm, sc[i], bb[i]));
-          f[i] = fma2(sc[i], z, fma2(xm, k1[i], k0[i]));
+      for (int i = 0; i < kBatch; ++i)
+        if (r + i * p.ty < left) {
+          vx[i].load_last(px + i * xstep);
+          vd[i].load_last(py + i * dstep);
         }
-        store_pairs<T, VEC, true>(po, f);
-      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (r + i * p.ty < left) {
+          float2 f[P], d[P];
+          widen_pairs<T, VEC>(vx[i], f);
+          widen_pairs<T, VEC>(vd[i], d);
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            const float2 xm = add2(f[j], mu[j]);
+            const float2 z = through2<ACT>(d[j], fma2(xm, sc[j], bb[j]));
+            f[j] = fma2(sc[j], z, fma2(xm, k1[j], k0[j]));
+          }
+          store_pairs<T, VEC, true>(po + i * ostep, f);
+        }
     }
   }
 }
 
 // ---------------------------------------------------------------- launches
-
-inline unsigned int take_faults() {
-  unsigned int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_gn_faults, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_gn_faults, &z, sizeof(z));
-  return v;
-}
 
 inline Args args_of(const wtconv_gn_desc_t& d) {
   Args a;
@@ -1166,46 +834,36 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int cluster, int smem, cudaStrea
 }
 
 // One launch of a streamed kernel: as many CTAs as the GPU holds at once.
-// `jobs`: queue entries of a sample's range.
+// A launch whose CTAs may move in before the one before it has ended.
 template <typename K, typename... A>
-cudaError_t launch_streamed(K kernel, int jobs, const wtconv_gn_desc_t& d, const GnPlan& p, int smem, void* ws,
-                            cudaStream_t s, A... args) {
+cudaError_t launch_next(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
   cudaError_t e = wt::ensure_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(ws, 0, (size_t)(1 + 2 * d.N) * 4, s);
-  if (e != cudaSuccess) return e;
-  int per_sm = wt::occupancy((const void*)kernel, kThreads, smem), sms = wt::sm_count();
-  if (per_sm < 1) per_sm = 1;
-  if (sms < 1) sms = 152;
-  const long long items = jobs * d.N * p.splits, slots = (long long)per_sm * sms;
-  const long long grid = items < slots ? items : slots;
-  if (jobs == 1 && p.splits > slots) return cudaErrorInvalidConfiguration;  // the plan sees to it
-  const Streamed q = {p.tx, p.ty, p.splits, p.rows, p.lag, (unsigned int*)ws};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;
-  at[0].val.cooperative = jobs == 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args_of(d), q, args...);
-}
-
-// bwd_reduce, its launch overlapping the end of the kernel before it
-inline cudaError_t launch_reduce(int C, long long blocks, const float* part, float* dw, float* db, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((C + 31) / 32);
-  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bwd_reduce, C, blocks, part, dw, db);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+inline cudaError_t launch_reduce(int C, long long blocks, const float* part, float* tmp, float* dw, float* db,
+                                 cudaStream_t s) {
+  const unsigned cx = (C + 31) / 32;
+  if (blocks > kReduceOnce) {
+    const long long per = (blocks + kReduceRanges - 1) / kReduceRanges, ranges = (blocks + per - 1) / per;
+    const cudaError_t e = launch_next(bwd_reduce, dim3(cx, (unsigned)ranges), 1024, 0, s, C, blocks, per, part, tmp,
+                                      (float*)nullptr, (float*)nullptr);
+    if (e != cudaSuccess) return e;
+    part = tmp;
+    blocks = ranges;
+  }
+  return launch_next(bwd_reduce, dim3(cx), 1024, 0, s, C, blocks, blocks, part, (float*)nullptr, dw, db);
 }
 
 template <typename T, int VEC, int ACT>
@@ -1221,17 +879,25 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
     return launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)x, w, b,
                           (T*)y, mean, rstd);
   }
-  if (p.spread) {
-    const int smem = (int)spread_smem(WTCONV_OP_GN_FWD, d.C, d.G, p.ty, p.rows, sizeof(T));
-    return launch_streamed(fwd_spread<T, VEC, ACT>, 1, d, p, smem, ws, s, (const T*)x, w, b,
-                           (float2*)((char*)ws + p.part_at), (T*)y, mean, rstd);
-  }
   if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
+    cudaError_t e = cudaSuccess;
+    float2* part = (float2*)ws;
+    Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
     const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
-    return launch_streamed(fwd_streamed<T, VEC, ACT>, 2, d, p, smem, ws, s, (const T*)x, w, b,
-                           (float2*)((char*)ws + p.part_at), (T*)y, mean, rstd);
+    for (long long n0 = 0; n0 < d.N && e == cudaSuccess; n0 += p.batch) {
+      const dim3 grid(p.splits, (unsigned)(d.N - n0 < p.batch ? d.N - n0 : p.batch));
+      q.n0 = (int)n0;
+      // the first launch reads what the caller's last one wrote: it waits for it
+      e = n0 == 0 ? (wt::ensure_smem((const void*)fwd_read<T, VEC>, smem),
+                     fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part), cudaGetLastError())
+                  : launch_next(fwd_read<T, VEC>, grid, kThreads, smem, s, a, q, (const T*)x, part);
+      if (e == cudaSuccess)
+        e = launch_next(fwd_apply<T, VEC, ACT>, grid, kThreads, 8 * d.G, s, a, q, (const T*)x, w, b,
+                        (const float2*)part, (T*)y, mean, rstd);
+    }
+    return e;
   }
 }
 
@@ -1254,28 +920,32 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
     if (e != cudaSuccess) return e;
     e = launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)dy,
                        (const T*)x, mean, rstd, w, b, (T*)dx, part);
-  } else if (p.spread) {
-    float* part = (float*)((char*)ws + p.part_at);
-    float* sum = part + (size_t)d.N * p.splits * 2 * d.C;
-    float* gpart = sum + (size_t)d.N * 2 * d.C;
-    sums = sum;
-    const int smem = (int)spread_smem(WTCONV_OP_GN_BWD, d.C, d.G, p.ty, p.rows, sizeof(T));
-    e = launch_streamed(bwd_spread<T, VEC, ACT>, 1, d, p, smem, ws, s, (const T*)dy, (const T*)x, mean, rstd, w, b,
-                        part, gpart, sum, (T*)dx);
   } else if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
-    int smem = 4 * (kThreads + 2 * p.ty * p.tx * VEC);
-    if (smem < 8 * d.C) smem = 8 * d.C;
-    float* part = (float*)((char*)ws + p.part_at);
-    float* sum = part + (size_t)d.N * p.splits * 2 * d.C;
-    float* means = sum + (size_t)d.N * 2 * d.C;
-    sums = sum;
-    e = launch_streamed(bwd_streamed<T, VEC, ACT>, 2, d, p, smem, ws, s, (const T*)dy, (const T*)x, mean, rstd, w, b, part,
-                        sum, means, (T*)dx);
+    sums = (float*)ws;
+    blocks *= p.splits;
+    float* part = (float*)ws;
+    float* gpart = part + (size_t)blocks * 2 * d.C;
+    Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+    const int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
+    e = cudaSuccess;
+    for (long long n0 = 0; n0 < d.N && e == cudaSuccess; n0 += p.batch) {
+      const dim3 grid(p.splits, (unsigned)(d.N - n0 < p.batch ? d.N - n0 : p.batch));
+      q.n0 = (int)n0;
+      e = n0 == 0 ? (wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem),
+                     bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w,
+                                                                        b, part, gpart),
+                     cudaGetLastError())
+                  : launch_next(bwd_read<T, VEC, ACT>, grid, kThreads, smem, s, a, q, (const T*)dy, (const T*)x, mean,
+                                rstd, w, b, part, gpart);
+      if (e == cudaSuccess)
+        e = launch_next(bwd_apply<T, VEC, ACT>, grid, kThreads, 8 * d.G, s, a, q, (const T*)dy, (const T*)x, mean, rstd,
+                        w, b, (const float*)gpart, (T*)dx);
+    }
   }
   if (e != cudaSuccess || (!dw && !db)) return e;
-  return launch_reduce(d.C, blocks, sums, dw, db, s);
+  return launch_reduce(d.C, blocks, sums, (float*)((char*)ws + p.tmp_at), dw, db, s);
 }
 
 #define WTB_ACTS(T, V, CALL)                                  \

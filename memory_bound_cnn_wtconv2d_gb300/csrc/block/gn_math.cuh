@@ -103,14 +103,13 @@ __device__ __forceinline__ void widen_pairs(const Vec<T, VEC>& a, float2 (&v)[kP
     }
   }
 }
-// LAST: nothing will read the line again, the L2 may drop it first.
-template <typename T, int VEC, bool LAST = false>
+template <typename T, int VEC>
 __device__ __forceinline__ void load_pairs(const T* p, float2 (&v)[kPairs<VEC>]) {
   Vec<T, VEC> a;
-  if constexpr (LAST) a.r = __ldcs(reinterpret_cast<const typename Vec<T, VEC>::raw*>(p));
-  else a.load(p);
+  a.load(p);
   widen_pairs<T, VEC>(a, v);
 }
+// LAST: the L2 may drop the line first.
 template <typename T, int VEC, bool LAST = false>
 __device__ __forceinline__ void store_pairs(T* p, const float2 (&v)[kPairs<VEC>]) {
   Vec<T, VEC> a;

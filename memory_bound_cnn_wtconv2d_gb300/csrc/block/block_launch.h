@@ -8,9 +8,8 @@
 
 namespace wtb {
 
-// Channel sums of up to kReduceOnce blocks are added up by one launch, those of
-// more by two, the first over this many ranges of them.
-constexpr int kReduceOnce = 512, kReduceRanges = 32;
+// Streamed group norm backward: at most this many CTAs add up channel sums.
+constexpr int kExtraCtas = 24;
 
 struct GnPlan {
   int vec;         // elements of one access (a divisor of C; 16 bytes where alignment allows)
@@ -19,8 +18,6 @@ struct GnPlan {
   int cluster;     // resident form: CTAs of a cluster (0: streamed)
   int ch;          // resident form: channels of a CTA
   int splits;      // streamed form: row ranges of one sample, one CTA each
-  int batch;       // streamed form: samples of one launch
-  size_t tmp_at;   // backward: where the first of two reductions writes
   size_t ws_bytes;
 };
 

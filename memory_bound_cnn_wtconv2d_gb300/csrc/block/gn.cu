@@ -18,9 +18,6 @@ long long gn_resident_smem(int op, int ch, int ty, long long rows, int groups, i
 namespace {
 
 constexpr int kThreads = 256;
-// Samples of one launch of the streamed form: what its second reading still
-// finds in the L2 (129 MB, of which each half may hold a copy).
-constexpr long long kBatchBytes = 1000LL << 20;
 constexpr long long kSmemCta = 113 * 1024, kSmemSm = 228 * 1024;  // two CTAs an SM at least
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -52,7 +49,7 @@ void plan_resident(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& 
       const double passes = (double)((rows + ty - 1) / ty) * 256 / (tx * ty);
       const double line = ch * es % 32 ? 1.25 : ch * es < 64 ? 1.1 : 1.0;
       const double pass = (op == WTCONV_OP_GN_FWD ? 0.2 : 0.4) * (beside > 3.0 ? beside / 3.0 : 1.0);
-      const double t = (ctas > slots ? ctas / slots : 1.0) * (3.0 + (cl > 1 ? 1.5 : 0.0) + passes * line * pass);
+      const double t = (ctas > slots ? ctas / slots : 1.0) * (3.0 + (cl > 1 ? 4.0 : 0.0) + passes * line * pass);
       if (p.cluster == 0 || t < best) {
         best = t;
         p.cluster = cl;
@@ -74,33 +71,29 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   plan_resident(d, op, vec, sms, p);
   const size_t n = (size_t)d.N;
-  size_t blocks = 0;  // of channel sums
+  if (p.cluster > 1) {
+    // Clusters only while latency counts; they measured slower than the
+    // streamed form on larger tensors, the more so the narrower the lines.
+    const int es = d.dtype == WTCONV_F32 ? 4 : 2, line = p.ch * es;
+    const long long read = d.N * d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2);
+    if (!((line >= 48 && read <= 12LL << 20) || (line >= 64 && read <= 24LL << 20))) p.cluster = 0;
+  }
   if (p.cluster) {
-    if (op == WTCONV_OP_GN_BWD) blocks = n * p.cluster;
+    if (op == WTCONV_OP_GN_BWD) p.ws_bytes = n * p.cluster * 2 * d.C * 4;
   } else {
     if (vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
     p.tx = d.C / vec < kThreads ? d.C / vec : kThreads;
     p.ty = kThreads / p.tx;
-    const int es = d.dtype == WTCONV_F32 ? 4 : 2;
-    const long long sample = d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2), slots = 4LL * sms;
-    long long batch = kBatchBytes / sample;
-    if (batch < 1) batch = 1;
-    if (batch > d.N) batch = d.N;
-    const long long launches = (d.N + batch - 1) / batch;
-    p.batch = (int)((d.N + launches - 1) / launches);
-    // one wave of CTAs a launch, at least 8 rows a thread
-    long long want = slots / p.batch;
+    // one wave of CTAs, at least 8 rows a thread
+    long long want = (4LL * sms - (op == WTCONV_OP_GN_BWD ? kExtraCtas : 0)) / d.N;
     const long long most = (d.S + 8LL * p.ty - 1) / (8LL * p.ty);
     if (want > most) want = most;
     if (want < 1) want = 1;
     p.rows = (int)((d.S + want - 1) / want);
     p.splits = (int)((d.S + p.rows - 1) / p.rows);
     p.ws_bytes = n * p.splits * d.G * 8;
-    if (op == WTCONV_OP_GN_BWD) blocks = n * p.splits;
+    if (op == WTCONV_OP_GN_BWD) p.ws_bytes += n * p.splits * 2 * d.C * 4;
   }
-  p.ws_bytes += blocks * 2 * d.C * 4;
-  p.tmp_at = p.ws_bytes;
-  if (blocks) p.ws_bytes += kReduceRanges * 2 * (size_t)d.C * 4;
   p.ws_bytes = (p.ws_bytes + 255) & ~(size_t)255;
   return p;
 }

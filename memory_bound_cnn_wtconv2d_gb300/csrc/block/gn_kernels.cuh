@@ -3,10 +3,9 @@
 // Two forms.  Resident: a cluster of up to eight CTAs holds one sample's rows
 // of a range of channels (whole groups) in shared memory, so that x (and dy)
 // cross the memory once: read, statistics, cluster exchange, written.
-// Streamed: one launch for the statistics and one that applies them, over
-// batches of samples small enough for the second reading to hit the L2, each
-// launch one wave of CTAs; a launch's CTAs move in as those of the one before
-// leave.
+// Streamed: one launch for the statistics and one that applies them, each one
+// wave of CTAs.  The second walks each range from its end, which the L2 still
+// holds.
 //
 // A thread owns VEC consecutive channels (16 bytes where alignment allows) and
 // walks down rows, so that a warp reads whole lines of consecutive pixels and
@@ -457,20 +456,46 @@ bwd_resident(const __grid_constant__ Args a, const __grid_constant__ Resident p,
   if (p.cluster > 1) cluster_wait();
 }
 
-// dweight, dbias: part[blocks][2][C] over its blocks, or, of several CTAs
-// along y, each a range of the blocks into out[y][2][C] (the second launch adds
-// those).  A CTA of 32 channels x 32 lanes; lane l adds blocks l, l + 32, ...,
-// the lanes are added in order.
+// dweight, dbias: the sums of part[blocks][2][C] over its blocks, by the first
+// `ctas` CTAs, 32 channels at a time.  Lane l of 8 adds blocks
+// l, l + 8, ..., the lanes are added in order.  sh: 2 kThreads floats.
+__device__ __forceinline__ void add_channels(int C, long long blocks, const float* part, float* dw, float* db, float* sh,
+                                             int ctas) {
+  const int cc = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  for (int cb = blockIdx.x * 32; cb < C; cb += ctas * 32) {
+    const int c = cb + cc;
+    float t0 = 0.f, t1 = 0.f;
+    if (c < C) {
+#pragma unroll 8
+      for (long long k = lane; k < blocks; k += kThreads / 32) {
+        t0 += part[(k * 2) * C + c];
+        t1 += part[(k * 2 + 1) * C + c];
+      }
+    }
+    __syncthreads();
+    sh[threadIdx.x] = t0;
+    sh[kThreads + threadIdx.x] = t1;
+    __syncthreads();
+    if (lane < 2) {
+      float t = 0.f;
+#pragma unroll
+      for (int l = 0; l < kThreads / 32; ++l) t += sh[lane * kThreads + l * 32 + cc];
+      float* to = lane ? dw : db;
+      if (to && c < C) to[c] = t;
+    }
+  }
+}
+
+// The same as a launch of its own, of 32 lanes.
 static __global__ void __launch_bounds__(1024)
-bwd_reduce(int C, long long blocks, long long per, const float* part, float* out, float* dw, float* db) {
+bwd_reduce(int C, long long blocks, const float* part, float* dw, float* db) {
   __shared__ float sh[2][32][33];
   const int cc = threadIdx.x & 31, lane = threadIdx.x >> 5, c = blockIdx.x * 32 + cc;
-  const long long first = blockIdx.y * per, stop = min(blocks, first + per);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float t0 = 0.f, t1 = 0.f;
   if (c < C) {
-#pragma unroll 4
-    for (long long k = first + lane; k < stop; k += 32) {
+#pragma unroll 8
+    for (long long k = lane; k < blocks; k += 32) {
       t0 += part[(k * 2) * C + c];
       t1 += part[(k * 2 + 1) * C + c];
     }
@@ -482,7 +507,7 @@ bwd_reduce(int C, long long blocks, long long per, const float* part, float* out
     float t = 0.f;
 #pragma unroll
     for (int l = 0; l < 32; ++l) t += sh[lane][l][cc];
-    float* to = out ? out + (blockIdx.y * 2 + lane) * (long long)C : lane ? dw : db;
+    float* to = lane ? dw : db;
     if (to && c < C) to[c] = t;
   }
 }
@@ -492,8 +517,38 @@ bwd_reduce(int C, long long blocks, long long per, const float* part, float* out
 struct Streamed {
   int tx, ty;        // threads across channel vectors, rows side by side
   int splits, rows;  // row ranges of a sample, one CTA each
-  int n0;            // the batch's first sample
+  int extra;         // backward: the second launch's first CTAs, which add up the channel sums
 };
+
+// Sums over a sample's ranges of f(range, j) for j < count, by all warps:
+// lanes side by side over j (coalesced), then over ranges.  out(j, sum) by one
+// thread each; sh: kThreads floats.  Ends with a barrier.
+template <typename F, typename O>
+__device__ __forceinline__ void range_sums(int splits, int count, float* sh, const F& f, const O& out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int across = 32;
+  while (across / 2 >= count) across >>= 1;
+  const int down = 32 / across, j0 = lane & (across - 1), sub = warp * down + lane / across;
+  const int step = kThreads / 32 * down;
+  for (int jb = 0; jb < count; jb += across) {
+    const int j = jb + j0;
+    float t = 0.f;
+    if (j < count) {
+#pragma unroll 4
+      for (int s = sub; s < splits; s += step) t += f(s, j);
+    }
+    for (int o = across; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
+    if (lane < across) sh[warp * across + lane] = t;
+    __syncthreads();
+    if (threadIdx.x < across && jb + (int)threadIdx.x < count) {
+      float u = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) u += sh[w * across + threadIdx.x];
+      out(jb + (int)threadIdx.x, u);
+    }
+    __syncthreads();
+  }
+}
 
 // Lets the next launch's CTAs in as this one's leave / waits for the launch before.
 __device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -506,8 +561,8 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
          float2* __restrict__ part) {
   constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
   extern __shared__ __align__(16) float sm[];
-  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
-  const long long n = p.n0 + (int)blockIdx.y;
+  const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  const long long n = blockIdx.x / p.splits;
   const int W = p.tx * VEC;
   float* ch = sm;            // [2][C]
   float* st = sm + 2 * a.C;  // [2][ty][W]
@@ -578,7 +633,6 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
   if (whole) group_statistics(st, p.ty, p.tx, a.Cg / VEC, VEC, a.G, rows, put);
   else if (W >= a.C) group_statistics(st, p.ty, W, a.Cg, 1, a.G, rows, put);
   else group_statistics(ch, 1, a.C, a.Cg, 1, a.G, rows, put);
-  wait_previous();  // so that a launch never ends before the one before it
 }
 
 template <typename T, int VEC, int ACT>
@@ -587,36 +641,33 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
           const float* __restrict__ w, const float* __restrict__ b, const float2* part, T* __restrict__ y,
           float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];  // [2][G]
-  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
-  const long long n = p.n0 + (int)blockIdx.y;
-  let_next_in();
+  extern __shared__ __align__(16) float sm[];  // [2][G], kThreads
+  const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  const long long n = blockIdx.x / p.splits;
   wait_previous();
-  const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
-  for (int g = tid >> 5; g < a.G; g += kThreads / 32) {                  // one warp per group
-    const float2* q = part + n * p.splits * a.G + g;
-    float t = 0.f;
-#pragma unroll 4
-    for (int s = lane; s < p.splits; s += 32) t = fmaf(s + 1 < p.splits ? (float)p.rows : last, q[(long long)s * a.G].x, t);
-    const float mean = warp_sum(t) / (float)a.S;
-    t = 0.f;
-#pragma unroll 4
-    for (int s = lane; s < p.splits; s += 32) {
-      const float2 v = q[(long long)s * a.G];
-      const float d = v.x - mean;
-      t += fmaf((s + 1 < p.splits ? (float)p.rows : last) * (float)a.Cg * d, d, v.y);
-    }
-    const float rs = rsqrtf(warp_sum(t) / ((float)a.S * (float)a.Cg) + a.eps);
-    if (lane == 0) {
-      sm[g] = mean;
-      sm[a.G + g] = rs;
-      if (split == 0) {
-        mean_out[n * a.G + g] = mean;
-        rstd_out[n * a.G + g] = rs;
-      }
-    }
+  {
+    const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
+    const float2* q = part + n * p.splits * a.G;
+    float* tmp = sm + 2 * a.G;
+    const auto weight = [&](int s) { return s + 1 < p.splits ? (float)p.rows : last; };
+    range_sums(p.splits, a.G, tmp, [&](int s, int g) { return weight(s) * q[(long long)s * a.G + g].x; },
+               [&](int g, float t) { sm[g] = t / (float)a.S; });
+    range_sums(
+        p.splits, a.G, tmp,
+        [&](int s, int g) {
+          const float2 v = q[(long long)s * a.G + g];
+          const float d = v.x - sm[g];
+          return fmaf(weight(s) * (float)a.Cg * d, d, v.y);
+        },
+        [&](int g, float t) {
+          const float rs = rsqrtf(t / ((float)a.S * (float)a.Cg) + a.eps);
+          sm[a.G + g] = rs;
+          if (split == 0) {
+            mean_out[n * a.G + g] = sm[g];
+            rstd_out[n * a.G + g] = rs;
+          }
+        });
   }
-  __syncthreads();
   if (ty >= p.ty) return;
   const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
   const int rows = (int)(r1 - r0);
@@ -627,11 +678,11 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
     per_channel<VEC>(mu, [&](int e) { return -sm[g[e]]; });
     per_channel<VEC>(sc, [&](int e) { return sm[a.G + g[e]] * (w ? w[c + e] : 1.f); });
     per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
-    const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
-    T* py = y + (n * a.S + r0 + ty) * a.C + c;
     const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
-    const int left = rows - ty;
-    for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * ystep) {
+    const int left = rows - ty, first = left > 0 ? (left - 1) / (kBatch * p.ty) * (kBatch * p.ty) : -1;
+    const T* px = x + n * a.xs + (r0 + ty + first) * a.xr + c;
+    T* py = y + (n * a.S + r0 + ty + first) * a.C + c;
+    for (int r = first; r >= 0; r -= kBatch * p.ty, px -= kBatch * xstep, py -= kBatch * ystep) {
       Vec<T, VEC> v[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
@@ -659,8 +710,8 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
          float* __restrict__ gpart) {
   constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
   extern __shared__ __align__(16) float sm[];
-  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
-  const long long n = p.n0 + (int)blockIdx.y;
+  const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
+  const long long n = blockIdx.x / p.splits;
   const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
   const int rows = (int)(r1 - r0), W = p.tx * VEC;
   float* ch = sm;               // [2][C], weighted
@@ -734,29 +785,30 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
     t = warp_sum(t);
     if (lane == 0) gpart[(n * p.splits + split) * 2 * a.G + j] = t;
   }
-  wait_previous();  // so that a launch never ends before the one before it
 }
 
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, 4)
 bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
           const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
-          const float* __restrict__ w, const float* __restrict__ b, const float* gpart, T* __restrict__ dx) {
+          const float* __restrict__ w, const float* __restrict__ b, const float* part, const float* gpart,
+          T* __restrict__ dx, float* __restrict__ dw, float* __restrict__ db) {
   constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];  // [2][G]
-  const int split = blockIdx.x, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
-  const long long n = p.n0 + (int)blockIdx.y;
-  let_next_in();
-  wait_previous();
-  const float inv = 1.f / ((float)a.S * (float)a.Cg);
-  for (int j = tid >> 5; j < 2 * a.G; j += kThreads / 32) {
-    float t = 0.f;
-#pragma unroll 4
-    for (int s = lane; s < p.splits; s += 32) t += gpart[(n * p.splits + s) * 2 * a.G + j];
-    t = warp_sum(t);
-    if (lane == 0) sm[j] = t * inv;
+  extern __shared__ __align__(16) float sm[];  // [2][G], kThreads; or 2 kThreads
+  if ((int)blockIdx.x < p.extra) {
+    wait_previous();
+    add_channels(a.C, a.N * p.splits, part, dw, db, sm, p.extra);
+    return;
   }
-  __syncthreads();
+  const int at = blockIdx.x - p.extra, split = at % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
+  const long long n = at / p.splits;
+  wait_previous();
+  {
+    const float inv = 1.f / ((float)a.S * (float)a.Cg);
+    const float* q = gpart + n * p.splits * 2 * a.G;
+    range_sums(p.splits, 2 * a.G, sm + 2 * a.G, [&](int s, int j) { return q[(long long)s * 2 * a.G + j]; },
+               [&](int j, float t) { sm[j] = t * inv; });
+  }
   if (ty >= p.ty) return;
   const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
   const int rows = (int)(r1 - r0);
@@ -773,12 +825,12 @@ bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
       const float r = rstd[n * a.G + g[e]];
       return -r * r * sm[a.G + g[e]];
     });
-    const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
-    const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
-    T* po = dx + (n * a.S + r0 + ty) * a.C + c;
     const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
-    const int left = rows - ty;
-    for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * dstep, po += kBatch * ostep) {
+    const int left = rows - ty, first = left > 0 ? (left - 1) / (kBatch * p.ty) * (kBatch * p.ty) : -1;
+    const T* px = x + n * a.xs + (r0 + ty + first) * a.xr + c;
+    const T* py = dy + n * a.ds + (r0 + ty + first) * a.dr + c;
+    T* po = dx + (n * a.S + r0 + ty + first) * a.C + c;
+    for (int r = first; r >= 0; r -= kBatch * p.ty, px -= kBatch * xstep, py -= kBatch * dstep, po -= kBatch * ostep) {
       Vec<T, VEC> vx[kBatch], vd[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
@@ -852,20 +904,6 @@ cudaError_t launch_next(K kernel, dim3 grid, int threads, int smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-inline cudaError_t launch_reduce(int C, long long blocks, const float* part, float* tmp, float* dw, float* db,
-                                 cudaStream_t s) {
-  const unsigned cx = (C + 31) / 32;
-  if (blocks > kReduceOnce) {
-    const long long per = (blocks + kReduceRanges - 1) / kReduceRanges, ranges = (blocks + per - 1) / per;
-    const cudaError_t e = launch_next(bwd_reduce, dim3(cx, (unsigned)ranges), 1024, 0, s, C, blocks, per, part, tmp,
-                                      (float*)nullptr, (float*)nullptr);
-    if (e != cudaSuccess) return e;
-    part = tmp;
-    blocks = ranges;
-  }
-  return launch_next(bwd_reduce, dim3(cx), 1024, 0, s, C, blocks, blocks, part, (float*)nullptr, dw, db);
-}
-
 template <typename T, int VEC, int ACT>
 cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const float* w, const float* b, void* y,
                 float* mean, float* rstd, void* ws, cudaStream_t s) {
@@ -882,22 +920,17 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
   if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
-    cudaError_t e = cudaSuccess;
     float2* part = (float2*)ws;
-    Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+    const Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+    const unsigned grid = (unsigned)(d.N * p.splits);
     const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
-    for (long long n0 = 0; n0 < d.N && e == cudaSuccess; n0 += p.batch) {
-      const dim3 grid(p.splits, (unsigned)(d.N - n0 < p.batch ? d.N - n0 : p.batch));
-      q.n0 = (int)n0;
-      // the first launch reads what the caller's last one wrote: it waits for it
-      e = n0 == 0 ? (wt::ensure_smem((const void*)fwd_read<T, VEC>, smem),
-                     fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part), cudaGetLastError())
-                  : launch_next(fwd_read<T, VEC>, grid, kThreads, smem, s, a, q, (const T*)x, part);
-      if (e == cudaSuccess)
-        e = launch_next(fwd_apply<T, VEC, ACT>, grid, kThreads, 8 * d.G, s, a, q, (const T*)x, w, b,
-                        (const float2*)part, (T*)y, mean, rstd);
-    }
-    return e;
+    cudaError_t e = wt::ensure_smem((const void*)fwd_read<T, VEC>, smem);
+    if (e != cudaSuccess) return e;
+    fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_next(fwd_apply<T, VEC, ACT>, dim3(grid), kThreads, 4 * (2 * d.G + kThreads), s, a, q, (const T*)x, w, b,
+                       (const float2*)part, (T*)y, mean, rstd);
   }
 }
 
@@ -906,46 +939,36 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
                 const float* rstd, const float* w, const float* b, void* dx, float* dw, float* db, void* ws,
                 cudaStream_t s) {
   const Args a = args_of(d);
-  cudaError_t e;
-  const float* sums;
-  long long blocks = d.N;
   if (p.cluster) {
     float* part = (float*)ws;
-    sums = part;
-    blocks *= p.cluster;
     const Resident r = {p.ch, p.tx, p.ty, p.rows, p.cluster};
     const int smem = (int)resident_smem(WTCONV_OP_GN_BWD, p.ch, p.ty, p.rows, p.ch / a.Cg, sizeof(T));
     const auto k = bwd_resident<T, VEC, ACT>;
-    e = wt::ensure_smem((const void*)k, smem);
+    cudaError_t e = wt::ensure_smem((const void*)k, smem);
     if (e != cudaSuccess) return e;
     e = launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)dy,
                        (const T*)x, mean, rstd, w, b, (T*)dx, part);
-  } else if constexpr (VEC == 8) {
+    if (e != cudaSuccess || (!dw && !db)) return e;
+    return launch_next(bwd_reduce, dim3((d.C + 31) / 32), 1024, 0, s, d.C, d.N * p.cluster, (const float*)part, dw, db);
+  }
+  if constexpr (VEC == 8) {
     return cudaErrorInvalidValue;  // never planned
   } else {
-    sums = (float*)ws;
-    blocks *= p.splits;
     float* part = (float*)ws;
-    float* gpart = part + (size_t)blocks * 2 * d.C;
+    float* gpart = part + (size_t)d.N * p.splits * 2 * d.C;
     Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
-    const int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
-    e = cudaSuccess;
-    for (long long n0 = 0; n0 < d.N && e == cudaSuccess; n0 += p.batch) {
-      const dim3 grid(p.splits, (unsigned)(d.N - n0 < p.batch ? d.N - n0 : p.batch));
-      q.n0 = (int)n0;
-      e = n0 == 0 ? (wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem),
-                     bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w,
-                                                                        b, part, gpart),
-                     cudaGetLastError())
-                  : launch_next(bwd_read<T, VEC, ACT>, grid, kThreads, smem, s, a, q, (const T*)dy, (const T*)x, mean,
-                                rstd, w, b, part, gpart);
-      if (e == cudaSuccess)
-        e = launch_next(bwd_apply<T, VEC, ACT>, grid, kThreads, 8 * d.G, s, a, q, (const T*)dy, (const T*)x, mean, rstd,
-                        w, b, (const float*)gpart, (T*)dx);
-    }
+    if (dw || db) q.extra = (d.C + 31) / 32 < kExtraCtas ? (d.C + 31) / 32 : kExtraCtas;
+    const unsigned grid = (unsigned)(d.N * p.splits);
+    int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
+    cudaError_t e = wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem);
+    if (e != cudaSuccess) return e;
+    bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w, b, part, gpart);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    smem = 4 * (2 * d.G + 2 * kThreads);
+    return launch_next(bwd_apply<T, VEC, ACT>, dim3(grid + q.extra), kThreads, smem, s, a, q, (const T*)dy, (const T*)x,
+                       mean, rstd, w, b, (const float*)part, (const float*)gpart, (T*)dx, dw, db);
   }
-  if (e != cudaSuccess || (!dw && !db)) return e;
-  return launch_reduce(d.C, blocks, sums, (float*)((char*)ws + p.tmp_at), dw, db, s);
 }
 
 #define WTB_ACTS(T, V, CALL)                                  \

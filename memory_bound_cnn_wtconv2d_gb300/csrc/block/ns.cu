@@ -257,27 +257,12 @@ __device__ __forceinline__ Tile tile_of(const NsMain& a, int phase, int t) {
 // k are stored as such (K-major), or as their mirror image.
 __device__ __forceinline__ bool stored(const NsMain& a, int i, int k) { return (i >> a.gsh) >= (k >> a.gsh); }
 
-// Where sub-block (i, j) of a matrix with ncols sub-blocks across lies: the
-// two of a 128-row block next to each other.
-__device__ __forceinline__ long long at_sub(int i, int j, int ncols) {
-  return ((((long long)(i >> 1) * ncols + j) << 1) + (i & 1)) * kSub;
+// Where sub-block (i, j) of a matrix with ncols sub-blocks across lies (in
+// sub-blocks): the two of a 128-row block next to each other.
+__device__ __forceinline__ uint32_t sub_index(int i, int j, int ncols) {
+  return ((((uint32_t)(i >> 1) * ncols + j) << 1) + (i & 1));
 }
-// n sub-blocks of column k from row i on (i even or n = 1)
-__device__ __forceinline__ void load_rows(uint32_t dst, const unsigned char* base, int ncols, int i, int n, int k,
-                                          uint32_t bar) {
-  for (int s = 0; s < n; s += 2)
-    bulk_load(dst + s * kSub, base + at_sub(i + s, k, ncols), n - s > 1 ? 2 * kSub : kSub, bar);
-}
-// n sub-blocks of row k from column j on
-__device__ __forceinline__ void load_across(uint32_t dst, const unsigned char* base, int ncols, int k, int j, int n,
-                                            uint32_t bar) {
-  for (int s = 0; s < n; ++s) bulk_load(dst + s * kSub, base + at_sub(k, j + s, ncols), kSub, bar);
-}
-__device__ __forceinline__ void load_symmetric(const NsMain& a, uint32_t dst, const unsigned char* base, int i, int n,
-                                               int k, uint32_t bar) {
-  if (stored(a, i, k)) load_rows(dst, base, a.rb, i, n, k, bar);
-  else load_across(dst, base, a.rb, k, i, n, bar);
-}
+__device__ __forceinline__ long long at_sub(int i, int j, int ncols) { return (long long)sub_index(i, j, ncols) * kSub; }
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   uint4 u;
@@ -416,14 +401,26 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           const int i = first ? 2 * x.i : x.j, n = first ? 2 : x.nb;
           for (int pass = 0; pass < passes && !sh.dead; ++pass) {
             const unsigned char* src = (a.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
-            for (int k = 0; k < nk; ++k) {
-              if (!wait(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1)) break;
+            const unsigned char* along = src + at_sub(i, 0, of_x ? a.cb : a.rb);   // rows i.. of column k
+            const unsigned char* across = src + at_sub(0, i, of_x ? a.cb : a.rb);  // row k, columns i..
+            const uint32_t row_pair = 2u * (of_x ? a.cb : a.rb) * kSub;
+            const uint32_t bytes = n * kSub;
+            for (int k = 0; k < nk; ++k, along += 2 * kSub) {
               const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
-              mbar_expect(bar, n * kSub);
+              const bool km = phase == 0 || (!of_x && stored(a, i, k));
+              if (!wait(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1)) break;
+              mbar_expect(bar, bytes);
               filled |= 1u << stage;
-              if (phase == 0) load_rows(dst, src, a.cb, i, n, k, bar);
-              else if (of_x) load_across(dst, src, a.cb, k, i, n, bar);
-              else load_symmetric(a, dst, src, i, n, k, bar);
+              if (km) {  // pairs of rows lie row_pair apart (i even or n = 1)
+                bulk_load(dst, along, n > 1 ? 2 * kSub : kSub, bar);
+                if (n > 2) bulk_load(dst + 2 * kSub, along + row_pair, bytes - 2 * kSub, bar);
+              } else {
+                const unsigned char* from = across + (uint64_t)(k >> 1) * row_pair + (k & 1) * kSub;
+                bulk_load(dst, from, kSub, bar);
+#pragma unroll
+                for (int c = 1; c < kMaxNb; ++c)
+                  if (c < n) bulk_load(dst + c * kSub, from + c * 2 * kSub, kSub, bar);
+              }
               ph ^= 1u << stage;
               if (++stage == stages) stage = 0;
             }
@@ -435,6 +432,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           if (!wait(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1)) break;
           tc_fence_after();
           uint32_t begun = 0;  // segments that hold a sum
+          const uint32_t idesc0 = instr_desc(x.nb * 64, true, true);
           int next = 0;        // the last pass moves to the next segment here
           uint32_t seg = 0;
           for (int pass = 0; pass < passes && !sh.dead; ++pass) {
@@ -447,16 +445,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               }
               const bool akm = phase == 0 || stored(a, 2 * x.i, k);
               const bool bkm = phase == 0 || (phase == 1 && stored(a, x.j, k));
+              const uint32_t sa = base + stage * stage_bytes, idesc = idesc0 | (akm ? 0u : 1u << 15) | (bkm ? 0u : 1u << 16);
+              uint32_t da = desc_low(sa, akm), db = desc_low(sa + 2 * kSub, bkm);
+              const uint32_t ka = desc_step(akm), kb = desc_step(bkm);
+              const uint32_t d = tmem + acc * 256 + seg * seg_cols;
               if (!wait(sh, &sh.full[stage], ph >> stage & 1)) break;
               tc_fence_after();
-              const uint32_t sa = base + stage * stage_bytes, sb = sa + 2 * kSub;
-              const uint32_t idesc = instr_desc(x.nb * 64, akm, bkm);
-              const uint32_t d = tmem + acc * 256 + seg * seg_cols;
+              mma_f16(d, da, db, kDescHigh, idesc, begun >> seg & 1);
+              begun |= 1u << seg;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                mma_f16(d, operand_desc(sa + q * (akm ? 32 : 2048), akm), operand_desc(sb + q * (bkm ? 32 : 2048), bkm),
-                        idesc, begun >> seg & 1);
-                begun |= 1u << seg;
+              for (int q = 1; q < 4; ++q) {
+                da += ka, db += kb;
+                mma_f16(d, da, db, kDescHigh, idesc, 1);
               }
               mma_commit(smem_addr(&sh.empty[stage]));
               ph ^= 1u << stage;

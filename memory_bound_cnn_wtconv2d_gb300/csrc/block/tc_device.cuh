@@ -70,10 +70,14 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // D[tmem] (+)= A B for one K = 16 step, float16 operands, float32 accumulator.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Descriptors come as their low words and one high word.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{ .reg .pred p; .reg .b64 x, y;\n"
+      "mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3}; setp.ne.b32 p, %5, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "r"(high), "r"(idesc),
+      "r"(accumulate)
       : "memory");
 }
 // The barrier completes when every MMA issued so far has.
@@ -99,10 +103,14 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[8]) {
 //   along K:  rows are the operand's M or N index; 8-row groups lie 1024 bytes apart
 //   along MN: rows are the K index; 8-row groups 1024 bytes apart, and the
 //             next 64 of M or N one sub-block (8192 bytes) on
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool k_major) {
-  const uint64_t lbo = k_major ? 1 : 8192 >> 4, sbo = 1024 >> 4;
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+// The descriptor's low word: the address and the MN stride; its high word: the
+// 8-row stride, the version and the swizzle, the same for all.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool k_major) {
+  return (addr >> 4) | ((k_major ? 1u : 8192u >> 4) << 16);
 }
+// What a K = 16 step adds to it: 32 bytes along K, or 16 rows of 128 bytes.
+__device__ __forceinline__ uint32_t desc_step(bool k_major) { return k_major ? 32u >> 4 : 2048u >> 4; }
 // M = 128, N columns, float16 operands, float32 accumulator.
 __device__ __forceinline__ uint32_t instr_desc(int n, bool a_k_major, bool b_k_major) {
   return (1u << 4) | ((a_k_major ? 0u : 1u) << 15) | ((b_k_major ? 0u : 1u) << 16) | ((uint32_t)(n >> 3) << 17) |

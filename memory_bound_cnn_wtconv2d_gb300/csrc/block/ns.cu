@@ -190,6 +190,24 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
   return true;
 }
 
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_addr(bar);
+  if (__all_sync(~0u, mbar_try(a, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(~0u, mbar_try(a, parity))) {
+    const bool late = clock64() - t0 > kWaitCycles;
+    if (__any_sync(~0u, late || sh.dead)) {
+      if (late && !sh.dead) {
+        sh.dead = 1;
+        if ((threadIdx.x & 31) == 0) atomicAdd(&g_ns_faults, 1u);
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
 // All CTAs of the launch (co-resident by the cooperative launch) meet here.
 // `round` counts the barriers; a CTA that gave up sets the count's top bit, and
 // all leave.  Everything written before is visible after, to bulk copies too.
@@ -288,7 +306,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   __shared__ Shared sh;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   unsigned char* gen = raw + (base - smem_addr(raw));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 2);
@@ -307,7 +325,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
 
   // X = direction / (norm + eps), as sub-blocks
   {
@@ -389,17 +407,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       uint32_t acc = 0;
       const int stage_bytes = (2 + nbw) * kSub, stages = min(kStages, kRing / (2 + nbw));
       int stage = 0;
-      if ((warp == 0 || warp == 10) && lane == 0) {
+      if (warp == 0 || warp == 10) {
         const bool first = warp == 0;  // the operand whose rows are the tile's rows
         const unsigned char* hi = first ? (phase == 0 ? a.xh[cur] : phase == 1 ? a.ah : a.bh)
                                         : (phase == 1 ? a.ah : a.xh[cur]);
         const unsigned char* lo = first ? (phase == 0 ? a.xl[cur] : phase == 1 ? a.al : a.bl)
                                         : (phase == 1 ? a.al : a.xl[cur]);
         const bool of_x = phase == 0 || (phase == 2 && !first);
-        for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
+        bool go = true;
+        for (int t = blockIdx.x; t < tiles && go; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
           const int i = first ? 2 * x.i : x.j, n = first ? 2 : x.nb;
-          for (int pass = 0; pass < passes && !sh.dead; ++pass) {
+          for (int pass = 0; pass < passes && go; ++pass) {
             const unsigned char* src = (a.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
             const unsigned char* along = src + at_sub(i, 0, of_x ? a.cb : a.rb);   // rows i.. of column k
             const unsigned char* across = src + at_sub(0, i, of_x ? a.cb : a.rb);  // row k, columns i..
@@ -408,34 +427,40 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             for (int k = 0; k < nk; ++k, along += 2 * kSub) {
               const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
               const bool km = phase == 0 || (!of_x && stored(a, i, k));
-              if (!wait(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1)) break;
-              mbar_expect(bar, bytes);
+              go = wait_warp(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1);
+              if (!go) break;
               filled |= 1u << stage;
-              if (km) {  // pairs of rows lie row_pair apart (i even or n = 1)
-                bulk_load(dst, along, n > 1 ? 2 * kSub : kSub, bar);
-                if (n > 2) bulk_load(dst + 2 * kSub, along + row_pair, bytes - 2 * kSub, bar);
-              } else {
-                const unsigned char* from = across + (uint64_t)(k >> 1) * row_pair + (k & 1) * kSub;
-                bulk_load(dst, from, kSub, bar);
+              if (elect_one()) {
+                mbar_expect(bar, bytes);
+                if (km) {  // pairs of rows lie row_pair apart (i even or n = 1)
+                  bulk_load(dst, along, n > 1 ? 2 * kSub : kSub, bar);
+                  if (n > 2) bulk_load(dst + 2 * kSub, along + row_pair, bytes - 2 * kSub, bar);
+                } else {
+                  const unsigned char* from = across + (uint64_t)(k >> 1) * row_pair + (k & 1) * kSub;
+                  bulk_load(dst, from, kSub, bar);
 #pragma unroll
-                for (int c = 1; c < kMaxNb; ++c)
-                  if (c < n) bulk_load(dst + c * kSub, from + c * 2 * kSub, kSub, bar);
+                  for (int c = 1; c < kMaxNb; ++c)
+                    if (c < n) bulk_load(dst + c * kSub, from + c * 2 * kSub, kSub, bar);
+                }
               }
+              __syncwarp();
               ph ^= 1u << stage;
               if (++stage == stages) stage = 0;
             }
           }
         }
-      } else if (warp == 1 && lane == 0) {
-        for (int t = blockIdx.x; t < tiles && !sh.dead; t += gridDim.x) {
+      } else if (warp == 1) {
+        bool go = true;
+        for (int t = blockIdx.x; t < tiles && go; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
-          if (!wait(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1)) break;
+          go = wait_warp(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1);
+          if (!go) break;
           tc_fence_after();
           uint32_t begun = 0;  // segments that hold a sum
           const uint32_t idesc0 = instr_desc(x.nb * 64, true, true);
           int next = 0;        // the last pass moves to the next segment here
           uint32_t seg = 0;
-          for (int pass = 0; pass < passes && !sh.dead; ++pass) {
+          for (int pass = 0; pass < passes && go; ++pass) {
             const bool last = pass + 1 == passes;
             if (last) next = (nk + segs - 1) / segs;
             for (int k = 0; k < nk; ++k) {
@@ -449,21 +474,23 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               uint32_t da = desc_low(sa, akm), db = desc_low(sa + 2 * kSub, bkm);
               const uint32_t ka = desc_step(akm), kb = desc_step(bkm);
               const uint32_t d = tmem + acc * 256 + seg * seg_cols;
-              if (!wait(sh, &sh.full[stage], ph >> stage & 1)) break;
+              go = wait_warp(sh, &sh.full[stage], ph >> stage & 1);
+              if (!go) break;
               tc_fence_after();
-              mma_f16(d, da, db, kDescHigh, idesc, begun >> seg & 1);
-              begun |= 1u << seg;
+              if (elect_one()) {
+                mma_f16(d, da, db, kDescHigh, idesc, begun >> seg & 1);
 #pragma unroll
-              for (int q = 1; q < 4; ++q) {
-                da += ka, db += kb;
-                mma_f16(d, da, db, kDescHigh, idesc, 1);
+                for (int q = 1; q < 4; ++q) mma_f16(d, da + q * ka, db + q * kb, kDescHigh, idesc, 1);
+                mma_commit(smem_addr(&sh.empty[stage]));
               }
-              mma_commit(smem_addr(&sh.empty[stage]));
+              __syncwarp();
+              begun |= 1u << seg;
               ph ^= 1u << stage;
               if (++stage == stages) stage = 0;
             }
           }
-          mma_commit(smem_addr(&sh.acc_full[acc]));
+          if (elect_one()) mma_commit(smem_addr(&sh.acc_full[acc]));
+          __syncwarp();
           accph ^= 1u << acc;
           if (++acc == sets) acc = 0;
         }

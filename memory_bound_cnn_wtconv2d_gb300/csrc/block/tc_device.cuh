@@ -25,6 +25,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One lane of a converged warp.  The loops that issue copies and MMAs run on
+// whole warps with only the issue itself elected: what they compute is then
+// uniform and stays in uniform registers, where these instructions want it (in
+// code of a single thread each operand is moved there first, 60 cycles an MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
 // Global -> shared, completing on an mbarrier; sizes and addresses are multiples of 16.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),

@@ -55,6 +55,7 @@ constexpr int kSegments = 4;       // accumulators of one tile when split
 constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
 constexpr int kSmem = kRing * kSub + 2 * kEpiBytes + 1024;
+static_assert(kThreads / 32 * 64 * 65 * 4 <= kRing * kSub + 2 * kEpiBytes, "the first and last pass's tiles");
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
 static __device__ unsigned int g_ns_faults;
@@ -213,7 +214,9 @@ __device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t pa
 // all leave.  Everything written before is visible after, to bulk copies too.
 __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, unsigned int round) {
   constexpr unsigned int kStop = 1u << 31;
-  fence_async();
+  // what bulk copies read after this was written by plain stores in the first
+  // pass, and by the epilogue leader's bulk stores from then on
+  if (round == 1 || threadIdx.x == 64) fence_async();
   __syncthreads();
   bool stop = false;
   if (threadIdx.x == 0) {
@@ -327,14 +330,19 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
 
-  // X = direction / (norm + eps), as sub-blocks
+  // X = direction / (norm + eps).  A warp takes a sub-block, or where there are
+  // few of them 64 / share of its rows in the caller's order (8 at least).
+  float* tile = reinterpret_cast<float*>(gen) + warp * 64 * 65;  // the warp's own, [64][65]
+  const int warps = gridDim.x * (kThreads / 32), first = warp * gridDim.x + blockIdx.x;
+  int share = 1;
+  while (share < 8 && a.s.count * a.rb * a.cb * share < warps) share *= 2;
+  const int slice = 64 / share, lnch = 31 - __clz(slice / 8);
   {
-    float* tile = reinterpret_cast<float*>(gen);  // [64][65]
-    const int per = a.rb * a.cb;
+    const int per = a.rb * a.cb * share;
     int mat_known = -1;
     float mul = 0.f;
-    for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
-      const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
+    for (int t = first; t < per * a.s.count; t += warps) {
+      const int mat = t / per, u = t % per / share, y0 = (t % share) * slice, bi = u / a.cb, bj = u % a.cb;
       if (mat != mat_known) {  // every warp adds the partial sums in the same order
         float q = 0.f;
         for (int j = lane; j < a.s.parts; j += 32) q += a.part[mat * kNormMax + j];
@@ -356,33 +364,31 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       };
       // Reads run along the rows of the caller's matrix; a tall one is turned in shared memory.
       const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
+      const int ch = lane & 7, n = a.s.n - col0 - ch * 8;
+#pragma unroll 4
+      for (int y = y0 + (lane >> 3); y < y0 + slice; y += 4) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (n > 0 && row0 + y < a.s.m) direction8<T>(call, ptrs, a.s.wide, mat, row0 + y, col0 + ch * 8, n, false, v);
 #pragma unroll
-      for (int e0 = 0; e0 < 512; e0 += kThreads) {
-        const int e = e0 + tid;
-        if (e < 512) {
-          const int y = e >> 3, ch = e & 7, n = row0 + y < a.s.m ? a.s.n - col0 - ch * 8 : 0;
-          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (n > 0) direction8<T>(call, ptrs, a.s.wide, mat, row0 + y, col0 + ch * 8, n, false, v);
+        for (int i = 0; i < 8; ++i) v[i] *= mul;
+        if (!a.s.tall) {
+          put(y, ch, v);
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= mul;
-          if (!a.s.tall) {
-            put(y, ch, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tile[y * 65 + ch * 8 + i] = v[i];
-          }
+          for (int i = 0; i < 8; ++i) tile[y * 65 + ch * 8 + i] = v[i];
         }
       }
       if (a.s.tall) {
-        __syncthreads();
-        for (int e = tid; e < 512; e += kThreads) {
-          const int y = e & 63, ch = e >> 6;
+        __syncwarp();
+#pragma unroll 4
+        for (int e = lane; e < 8 * slice; e += 32) {
+          const int y = e >> lnch, c8 = y0 / 8 + (e & (slice / 8 - 1));  // of X: row, chunk of 8 columns
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = tile[(ch * 8 + i) * 65 + y];
-          put(y, ch, v);
+          for (int i = 0; i < 8; ++i) v[i] = tile[(c8 * 8 + i) * 65 + y];
+          put(y, c8, v);
         }
-        __syncthreads();
+        __syncwarp();
       }
     }
   }
@@ -551,7 +557,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc * 256 + s * 64 + col_half * 32;
             const bool on_diagonal = phase < 2 && 2 * x.i + sub == x.j + s;
             // rolled: each tile runs this once, and unrolled it is bound by fetching instructions
-#pragma unroll 1
+#pragma unroll 2
             for (int q = 0; q < 4; ++q) {
               const int ch = col_half * 4 + q;
               unsigned char* p = buf + ((ch ^ (y & 7)) << 4);
@@ -662,10 +668,10 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       }
     }
   }
-  // Back to the caller's layout
+  // Back to the caller's layout, shared out in the same way; a slice is of X's
+  // rows, or of its columns where the caller's matrix is tall.
   if (ok) {
-    float* tile = reinterpret_cast<float*>(gen);  // [64][65]
-    const int per = a.rk * a.cb;
+    const int per = a.rk * a.cb * share;
     const float inv = 1.f / a.sx;
     auto put = [&](int mat, int row, int col, float (&v)[8]) {
       if (row >= a.s.m || col >= a.s.n) return;
@@ -678,38 +684,38 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       }
       store8<T>(o, a.s.n - col, a.s.wide, v);
     };
-    for (int t = blockIdx.x; t < per * a.s.count; t += gridDim.x) {
-      const int mat = t / per, u = t % per, bi = u / a.cb, bj = u % a.cb;
+    for (int t = first; t < per * a.s.count; t += warps) {
+      const int mat = t / per, u = t % per / share, y0 = (t % share) * slice, bi = u / a.cb, bj = u % a.cb;
       const unsigned char* xh = a.xh[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
       const unsigned char* xl = a.xl[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
+#pragma unroll 4
+      for (int e = lane; e < 8 * slice; e += 32) {
+        // row and chunk of 8 columns of X
+        const int y = a.s.tall ? e >> lnch : y0 + (e >> 3), ch = a.s.tall ? y0 / 8 + (e & (slice / 8 - 1)) : e & 7;
+        const int at = y * 128 + ((ch ^ (y & 7)) << 4);
+        float v[8], w[8];
+        unpack8(__ldcg(reinterpret_cast<const uint4*>(xh + at)), v);
+        unpack8(__ldcg(reinterpret_cast<const uint4*>(xl + at)), w);
 #pragma unroll
-      for (int e0 = 0; e0 < 512; e0 += kThreads) {
-        const int e = e0 + tid;
-        if (e < 512) {
-          const int y = e >> 3, ch = e & 7, at = y * 128 + ((ch ^ (y & 7)) << 4);
-          float v[8], w[8];
-          unpack8(__ldcg(reinterpret_cast<const uint4*>(xh + at)), v);
-          unpack8(__ldcg(reinterpret_cast<const uint4*>(xl + at)), w);
+        for (int i = 0; i < 8; ++i) v[i] = (v[i] + w[i]) * inv;
+        if (!a.s.tall) {
+          put(mat, bi * 64 + y, bj * 64 + ch * 8, v);
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = (v[i] + w[i]) * inv;
-          if (!a.s.tall) {
-            put(mat, bi * 64 + y, bj * 64 + ch * 8, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tile[y * 65 + ch * 8 + i] = v[i];
-          }
+          for (int i = 0; i < 8; ++i) tile[(ch * 8 + i) * 65 + y] = v[i];
         }
       }
       if (a.s.tall) {
-        __syncthreads();
-        for (int e = tid; e < 512; e += kThreads) {
-          const int y = e >> 3, ch = e & 7;
+        __syncwarp();
+#pragma unroll 4
+        for (int e = lane; e < 8 * slice; e += 32) {
+          const int y = y0 + (e >> 3), ch = e & 7;
           float v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = tile[(ch * 8 + i) * 65 + y];
+          for (int i = 0; i < 8; ++i) v[i] = tile[y * 65 + ch * 8 + i];
           put(mat, bj * 64 + y, bi * 64 + ch * 8, v);
         }
-        __syncthreads();
+        __syncwarp();
       }
     }
   }

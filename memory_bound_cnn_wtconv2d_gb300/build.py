@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libwtconv.so")
 SOURCES = ("wtconv_api.cu", "wtconv_fwd.cu", "wtconv_fwd_win.cu", "wtconv_bwd_weight.cu", "wtconv_bwd_weight_win.cu",
            "wtconv_bwd_fused.cu", "wtconv_noalloc.cu", "wtconv_split.cu",
            # the operators around the layer (include/wtconv_block.h)
-           "block/block_api.cu", "block/gn.cu", "block/gn_f32.cu", "block/gn_f16.cu", "block/gn_bf16.cu", "block/ns.cu")
+           "block/block_api.cu", "block/gn.cu", "block/gn_f32.cu", "block/gn_f16.cu", "block/gn_bf16.cu", "block/ns.cu",
+           "block/ns_small.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

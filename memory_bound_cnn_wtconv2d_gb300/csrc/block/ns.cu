@@ -35,19 +35,24 @@
 // A and B are symmetric: only sub-blocks on and below the diagonal blocks are
 // computed and stored, and a tile above is read from its mirror image with
 // the other operand order (MN-major), which costs nothing.
-#include "block_device.cuh"
-#include "block_launch.h"
-#include "tc_device.cuh"
+#include "ns_common.cuh"
 #include "../wtconv_launch.h"
 
 namespace wtb {
+
+// The form for short matrices (ns_small.cu): whether it takes this call.
+bool ns_small_takes(const wtconv_ns_desc_t& d);
+cudaError_t ns_small_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, cudaStream_t s);
+unsigned int ns_small_take_faults();
+
 namespace {
+
+using namespace ns;
 
 constexpr int kNormThreads = 256;
 constexpr int kNormMax = 256;      // partial sums of squares per matrix, at most
 constexpr int kEpiThreads = 256;   // warps 2-9
 constexpr int kThreads = 96 + kEpiThreads;  // warps 0 and 10: copies of the two operands, warp 1: MMAs
-constexpr int kSub = 8192;         // bytes of a 64 x 64 sub-block
 constexpr int kRing = 20;          // sub-blocks of operands in flight
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
@@ -56,86 +61,21 @@ constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
 constexpr int kSmem = kRing * kSub + 2 * kEpiBytes + 1024;
 static_assert(kThreads / 32 * 64 * 65 * 4 <= kRing * kSub + 2 * kEpiBytes, "the first and last pass's tiles");
-constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
 static __device__ unsigned int g_ns_faults;
-
-struct NsShape {
-  int m, n, r, c, tall, count;
-  int parts;  // partial sums of squares per matrix
-  int wide;   // rows of the caller's matrices start on 16-byte boundaries
-  float eps;
-};
 
 struct NsMain {
   NsShape s;
   int rb, cb, rk;            // sub-blocks: rows (even), columns, rows that hold data
-  int steps, split;
+  NsPoly p;
   int nb1, nb2, nb3, gsh;    // tile widths of the three products; log2 of the stored diagonal block
   int t1, t2, t3;            // tiles of one matrix in each product
-  float ca, cb_, cc;         // coefficients
-  float sx, sa;              // scales of X and of A, B
   unsigned char *xh[2], *xl[2], *ah, *al, *bh, *bl;
   float *da, *db;            // diagonals of A and a I + B, in the images' scale
   long long xbytes, abytes;  // of one matrix
   unsigned int* sync;        // barrier count, abort flag
   const float* part;
 };
-
-// Eight consecutive elements of a row, of which the first n exist.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool wide, float (&v)[8]) {
-  if (wide && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      Vec<T, 4> a, b;
-      a.load(p), b.load(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = a.e[i], v[4 + i] = b.e[i];
-    } else {
-      Vec<T, 8> a;
-      a.load(p);
-      a.widen(v);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_float<T>(p[i]) : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, bool wide, const float (&v)[8]) {
-  if (wide && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      Vec<T, 8> a;
-      a.round(v);
-      a.store(p);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = round_to<T>(v[i]);
-  }
-}
-
-// Eight elements of the matrix to orthogonalise; `update` moves the momentum first.
-template <typename T>
-__device__ __forceinline__ void direction8(const NsCall& k, const NsPointers& p, bool wide, int i, long long row,
-                                           int col, int n, bool update, float (&v)[8]) {
-  load8<T>((const T*)p.grad[i] + row * k.g_ld + col, n, wide, v);
-  if (!k.muon) return;
-  float* mp = p.momentum[i] + row * k.m_ld + col;
-  float mo[8];
-  load8<float>(mp, n, wide, mo);
-  if (update) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mo[j] = fmaf(k.mu, mo[j], (1.f - k.mu) * v[j]);
-    store8<float>(mp, n, wide, mo);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = k.nesterov ? fmaf(k.mu, mo[j], (1.f - k.mu) * v[j]) : mo[j];
-}
 
 // Updates the momentum, adds up squares of the direction, clears the barrier.
 template <typename T>
@@ -285,23 +225,6 @@ __device__ __forceinline__ uint32_t sub_index(int i, int j, int ncols) {
 }
 __device__ __forceinline__ long long at_sub(int i, int j, int ncols) { return (long long)sub_index(i, j, ncols) * kSub; }
 
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  uint4 u;
-  __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-  return u;
-}
-__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
-  const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, const __grid_constant__ NsPointers ptrs) {
@@ -347,7 +270,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         float q = 0.f;
         for (int j = lane; j < a.s.parts; j += 32) q += a.part[mat * kNormMax + j];
         for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-        mul = q == 0.f ? 0.f : a.sx / (sqrtf(q) + a.s.eps);
+        mul = q == 0.f ? 0.f : a.p.sx / (sqrtf(q) + a.s.eps);
         mat_known = mat;
       }
       unsigned char* xh = a.xh[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
@@ -401,15 +324,15 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   uint32_t accph = 0;       // accumulator sets: one parity bit each
   uint32_t epiph = 0, nth = 0;  // epilogue: parity of each buffer's loads, sub-tiles seen
   uint32_t fetched[2] = {0, 0};  // loads into each buffer
-  const int passes = a.split ? 3 : 1;
-  for (int step = 0; ok && step < a.steps; ++step, cur ^= 1) {
+  const int passes = a.p.split ? 3 : 1;
+  for (int step = 0; ok && step < a.p.steps; ++step, cur ^= 1) {
     for (int phase = 0; ok && phase < 3; ++phase) {
       const int tiles = a.s.count * (phase == 0 ? a.t1 : phase == 1 ? a.t2 : a.t3);
       const int nk = phase == 0 ? a.cb : a.rk;
       // accumulators: two sets of up to 256 columns, or one of 4 x 128
       const int nbw = phase == 0 ? a.nb1 : phase == 1 ? a.nb2 : a.nb3;
-      const int segs = a.split ? min(kSegments, nk) : 1;
-      const uint32_t seg_cols = nbw * 64, sets = a.split && nbw == 2 ? 1 : 2;
+      const int segs = a.p.split ? min(kSegments, nk) : 1;
+      const uint32_t seg_cols = nbw * 64, sets = a.p.split && nbw == 2 ? 1 : 2;
       uint32_t acc = 0;
       const int stage_bytes = (2 + nbw) * kSub, stages = min(kStages, kRing / (2 + nbw));
       int stage = 0;
@@ -425,7 +348,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           const Tile x = tile_of(a, phase, t);
           const int i = first ? 2 * x.i : x.j, n = first ? 2 : x.nb;
           for (int pass = 0; pass < passes && go; ++pass) {
-            const unsigned char* src = (a.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
+            const unsigned char* src = (a.p.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
             const unsigned char* along = src + at_sub(i, 0, of_x ? a.cb : a.rb);   // rows i.. of column k
             const unsigned char* across = src + at_sub(0, i, of_x ? a.cb : a.rb);  // row k, columns i..
             const uint32_t row_pair = 2u * (of_x ? a.cb : a.rb) * kSub;
@@ -506,12 +429,12 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         const bool leader = tid == 64;
         const uint32_t ebase = base + kRing * kSub;
         // what the result is made from besides the product, and where it goes
-        const bool in = phase != 0, lo = phase == 2 || a.split;
+        const bool in = phase != 0, lo = phase == 2 || a.p.split;
         const unsigned char* ih = phase == 1 ? a.ah : a.xh[cur];
         const unsigned char* il = phase == 1 ? a.al : a.xl[cur];
         unsigned char* oh = phase == 0 ? a.ah : phase == 1 ? a.bh : a.xh[cur ^ 1];
         unsigned char* ol = phase == 0 ? a.al : phase == 1 ? a.bl : a.xl[cur ^ 1];
-        const float facc = phase == 0 ? a.sa / (a.sx * a.sx) : phase == 1 ? a.cc / a.sa : 1.f / a.sa;
+        const float facc = phase == 0 ? a.p.sa / (a.p.sx * a.p.sx) : phase == 1 ? a.p.cc / a.p.sa : 1.f / a.p.sa;
         const int ncols = phase == 2 ? a.cb : a.rb;
         const long long obytes = phase == 2 ? a.xbytes : a.abytes;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -598,7 +521,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                 // (D + A)^2 = A A + D A + A D + D D, A without its diagonal D
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  u[i] = fmaf(a.cb_, u[i], facc * fmaf(diag + sh.dcol[s * 64 + ch * 8 + i], u[i], v[i]));
+                  u[i] = fmaf(a.p.cb, u[i], facc * fmaf(diag + sh.dcol[s * 64 + ch * 8 + i], u[i], v[i]));
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[i]);
@@ -608,7 +531,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                 for (int i = 0; i < 8; ++i)
                   if ((y & 7) == i) {
                     if (phase == 0) a.da[grow] = u[i];
-                    else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.cb_), u[i]) + a.ca * a.sa;
+                    else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.p.cb), u[i]) + a.p.ca * a.p.sa;
                     u[i] = 0.f;
                   }
               }
@@ -672,7 +595,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   // rows, or of its columns where the caller's matrix is tall.
   if (ok) {
     const int per = a.rk * a.cb * share;
-    const float inv = 1.f / a.sx;
+    const float inv = 1.f / a.p.sx;
     auto put = [&](int mat, int row, int col, float (&v)[8]) {
       if (row >= a.s.m || col >= a.s.n) return;
       T* o = (T*)ptrs.out[mat] + (long long)row * call.out_ld + col;
@@ -724,12 +647,6 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   if (warp == 1) tmem_free(tmem, 512);
 }
 
-int ceil_log2(double v) {
-  int e = 0;
-  while ((double)(1ll << e) < v) ++e;
-  return e;
-}
-
 int sym_tiles(int rb, int nb, int gsh) {
   int n = 0;
   for (int i = 0; i < rb / 2; ++i) {
@@ -749,28 +666,16 @@ double tile_cost(long long tiles, int sms, int nb, int nk, int passes) {
 
 NsMain plan(const wtconv_ns_desc_t& d) {
   NsMain a = {};
-  NsShape& s = a.s;
-  s.m = d.m; s.n = d.n; s.count = d.count; s.eps = d.eps;
-  s.tall = d.m > d.n;
-  s.r = s.tall ? d.n : d.m;
-  s.c = s.tall ? d.m : d.n;
+  a.s = shape_of(d);
+  const NsShape& s = a.s;
+  a.p = poly_of(d, s);
   a.rk = (s.r + 63) / 64;
   a.rb = (a.rk + 1) & ~1;
   a.cb = (s.c + 63) / 64;
-  a.steps = d.steps;
-  a.split = d.dtype != WTCONV_BF16 || s.r < 16;
-  a.ca = d.a; a.cb_ = d.b; a.cc = d.c;
-  // entries of X near 1: |X|_F is about 1 at first; those of A, B near 1 on
-  // the diagonal.  Both capped so that no entry passes float16's range.
-  int ex = (ceil_log2(s.r) + ceil_log2(s.c)) / 2, ea = ceil_log2(s.r);
-  if (ex > 12) ex = 12;
-  if (ea > 11) ea = 11;
-  a.sx = (float)(1 << ex);
-  a.sa = (float)(1 << ea);
   a.xbytes = (long long)a.rb * a.cb * kSub;
   a.abytes = (long long)a.rb * a.rb * kSub;
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
-  const int passes = a.split ? 3 : 1, most = a.split ? kSplitNb : kMaxNb;
+  const int passes = a.p.split ? 3 : 1, most = a.p.split ? kSplitNb : kMaxNb;
   double best = -1;
   for (int gsh = 1; gsh <= 2; ++gsh) {
     int pick[2] = {1, 1};
@@ -815,7 +720,7 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
   }
   a.ah = w, w += aa;
   a.bh = w, w += aa;
-  if (a.split) {
+  if (a.p.split) {
     a.al = w, w += aa;
     a.bl = w;
   }
@@ -826,10 +731,7 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
   const long long most = (4 * sms + d.count - 1) / d.count;
   if (parts > most) parts = most;
   a.s.parts = (int)(parts > kNormMax ? kNormMax : parts);
-  const int es = sizeof(T);
-  a.s.wide = k.g_ld * es % 16 == 0 && k.out_ld * es % 16 == 0 && (!k.muon || k.m_ld % 4 == 0);
-  for (int i = 0; i < d.count; ++i)
-    if ((uintptr_t)p.grad[i] % 16 || (uintptr_t)p.out[i] % 16 || (uintptr_t)p.momentum[i] % 16) a.s.wide = 0;
+  a.s.wide = is_wide(d, k, p);
   ns_norm<T><<<dim3(a.s.parts, d.count), kNormThreads, 0, st>>>(a.s, k, p, part, a.sync);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -849,12 +751,14 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
 }  // namespace
 
 size_t ns_workspace(const wtconv_ns_desc_t& d) {
+  if (ns_small_takes(d)) return 0;
   const NsMain a = plan(d);
   const size_t x = (size_t)a.xbytes * d.count, m = (size_t)a.abytes * d.count;
-  return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.split ? 4 : 2) * m;
+  return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.p.split ? 4 : 2) * m;
 }
 
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t s) {
+  if (ns_small_takes(d)) return ns_small_launch(d, k, p, s);
   if (d.dtype == WTCONV_F32) return launch_t<float>(d, k, p, ws, s);
   if (d.dtype == WTCONV_F16) return launch_t<__half>(d, k, p, ws, s);
   return launch_t<__nv_bfloat16>(d, k, p, ws, s);
@@ -864,7 +768,7 @@ unsigned int ns_take_faults() {
   unsigned int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, g_ns_faults, sizeof(v)) != cudaSuccess) return 0;
   cudaMemcpyToSymbol(g_ns_faults, &z, sizeof(z));
-  return v;
+  return v + ns_small_take_faults();
 }
 
 }  // namespace wtb

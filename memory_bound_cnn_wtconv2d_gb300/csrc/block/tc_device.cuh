@@ -112,12 +112,12 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[8]) {
 // sub-blocks of 16-bit values (64 rows of 128 bytes, 8 KB, 1024-aligned).
 //   along K:  rows are the operand's M or N index; 8-row groups lie 1024 bytes apart
 //   along MN: rows are the K index; 8-row groups 1024 bytes apart, and the
-//             next 64 of M or N one sub-block (8192 bytes) on
+//             next 64 of M or N mn_stride bytes on
 // The descriptor's low word: the address and the MN stride; its high word: the
 // 8-row stride, the version and the swizzle, the same for all.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool k_major) {
-  return (addr >> 4) | ((k_major ? 1u : 8192u >> 4) << 16);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool k_major, uint32_t mn_stride = 8192) {
+  return (addr >> 4) | ((k_major ? 1u : mn_stride >> 4) << 16);
 }
 // What a K = 16 step adds to it: 32 bytes along K, or 16 rows of 128 bytes.
 __device__ __forceinline__ uint32_t desc_step(bool k_major) { return k_major ? 32u >> 4 : 2048u >> 4; }

@@ -91,14 +91,14 @@ def test_group_norm_pointers_refused(L):
     assert L.wtconv_gn_act_fwd(None, p, None, None, p, p, p, p, need, None) == wtconv.WTCONV_ERR_INVALID_ARG
 
 
-def ns(count=2, m=8, n=12, dtype=0, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7):
+def ns(count=2, m=200, n=300, dtype=0, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7):
     return blockops.NsDesc(count, m, n, dtype, steps, a, b, c, eps)
 
 
-def call_orth(L, d, ld=12, ptrs=(FAKE, FAKE), out=(FAKE, FAKE), ws=FAKE, n=None):
+def call_orth(L, d, ld=300, ptrs=(FAKE, FAKE), out=(FAKE, FAKE), ws=FAKE, n=None):
     arr = lambda v: (ctypes.c_void_p * len(v))(*v)  # noqa: E731
     n = L.wtconv_ns_workspace_size(ctypes.byref(d)) if n is None else n
-    return L.wtconv_orthogonalize(ctypes.byref(d), arr(ptrs), ld, arr(out), 12, ctypes.c_void_p(ws) if ws else None, n, None)
+    return L.wtconv_orthogonalize(ctypes.byref(d), arr(ptrs), ld, arr(out), 300, ctypes.c_void_p(ws) if ws else None, n, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -113,7 +113,7 @@ def test_matrix_descriptors_refused(L, over, status):
 
 def test_matrix_pointers_refused(L):
     d = ns()
-    assert call_orth(L, d, ld=11) == wtconv.WTCONV_ERR_INVALID_ARG
+    assert call_orth(L, d, ld=299) == wtconv.WTCONV_ERR_INVALID_ARG
     assert call_orth(L, d, ptrs=(FAKE, 0)) == wtconv.WTCONV_ERR_INVALID_ARG
     assert call_orth(L, d, out=(FAKE, FAKE + 2)) == wtconv.WTCONV_ERR_MISALIGNED
     assert call_orth(L, d, ws=0) == wtconv.WTCONV_ERR_WORKSPACE
@@ -122,10 +122,10 @@ def test_matrix_pointers_refused(L):
     arr = (ctypes.c_void_p * 2)(FAKE, FAKE)
     need = L.wtconv_ns_workspace_size(ctypes.byref(d))
     p = ctypes.c_void_p(FAKE)
-    step = lambda mu, rate: L.wtconv_muon_step(ctypes.byref(d), arr, 12, arr, 12, arr, 12, mu, 1, 1.0, rate, p, need, None)  # noqa: E731
+    step = lambda mu, rate: L.wtconv_muon_step(ctypes.byref(d), arr, 300, arr, 300, arr, 300, mu, 1, 1.0, rate, p, need, None)  # noqa: E731
     assert step(float("nan"), 0.1) == wtconv.WTCONV_ERR_INVALID_ARG
     assert step(0.9, float("inf")) == wtconv.WTCONV_ERR_INVALID_ARG
-    assert L.wtconv_muon_step(ctypes.byref(d), None, 12, arr, 12, arr, 12, 0.9, 1, 1.0, 0.1, p, need, None) == \
+    assert L.wtconv_muon_step(ctypes.byref(d), None, 300, arr, 300, arr, 300, 0.9, 1, 1.0, 0.1, p, need, None) == \
         wtconv.WTCONV_ERR_INVALID_ARG
 
 

@@ -295,7 +295,7 @@ def test_refusals(ops):
     from memory_bound_cnn_wtconv2d_gb300 import wtconv
     from memory_bound_cnn_wtconv2d_gb300.muon import Muon
     with pytest.raises(wtconv.WtconvError) as e:
-        f(g, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        f(matrices(2, 200, 300), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == wtconv.WTCONV_ERR_WORKSPACE
     with pytest.raises(wtconv.WtconvError) as e:
         f(g, eps=-1.0)

@@ -526,14 +526,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[i]);
               }
-              if (on_diagonal && y >> 3 == ch) {  // the diagonal leaves the operand
+              if (on_diagonal) {  // the diagonal leaves the operand; selects, as the lanes' places differ
+                const int on = y >> 3 == ch ? y & 7 : 8;
+                float d = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if ((y & 7) == i) {
-                    if (phase == 0) a.da[grow] = u[i];
-                    else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.p.cb), u[i]) + a.p.ca * a.p.sa;
-                    u[i] = 0.f;
-                  }
+                for (int i = 0; i < 8; ++i) {
+                  d = on == i ? u[i] : d;
+                  u[i] = on == i ? 0.f : u[i];
+                }
+                if (on < 8) {
+                  if (phase == 0) a.da[grow] = d;
+                  else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.p.cb), d) + a.p.ca * a.p.sa;
+                }
               }
               const uint4 hi = pack8(u);
               *reinterpret_cast<uint4*>(p) = hi;

@@ -104,11 +104,14 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   // momentum), then again, scaled; a thread meets the same elements twice.
   const int row_lo = a.s.tall ? c0 : 0, row_hi = a.s.tall ? min(c0 + cs, a.s.m) : a.s.m;
   const int col_lo = a.s.tall ? 0 : c0, col_hi = a.s.tall ? a.s.n : min(c0 + cs, a.s.n);
-  const int across = max(0, (col_hi - col_lo + 7) / 8), chunks = max(0, row_hi - row_lo) * across;
+  // Lanes go along the caller's rows, or, where it is tall, down them: then
+  // they go along the rows of X, whose elements lie apart in shared memory.
+  const int across = max(0, (col_hi - col_lo + 7) / 8), down = max(0, row_hi - row_lo), chunks = down * across;
+  const int side = max(1, a.s.tall ? down : across);
   float q = 0.f;
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
-    const int y = e / across, x = (e - y * across) * 8;
+    const int e1 = e / side, e0 = e - e1 * side, y = a.s.tall ? e0 : e1, x = (a.s.tall ? e1 : e0) * 8;
     float v[8];
     direction8<T>(call, ptrs, a.s.wide, mat, row_lo + y, col_lo + x, col_hi - col_lo - x, true, v);
 #pragma unroll
@@ -134,7 +137,7 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   }
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
-    const int y = e / across, x = (e - y * across) * 8;
+    const int e1 = e / side, e0 = e - e1 * side, y = a.s.tall ? e0 : e1, x = (a.s.tall ? e1 : e0) * 8;
     float v[8];
     direction8<T>(call, ptrs, a.s.wide, mat, row_lo + y, col_lo + x, col_hi - col_lo - x, false, v);
 #pragma unroll
@@ -213,33 +216,31 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
         }
       }
     });
-    // its rows to the CTAs that add them up; 16-byte units of a row are turned
-    // by the row, so that the lanes' rows do not meet in one bank
+    // Its rows to the CTAs that add them up, as [sender][4 columns][row]: lanes
+    // are rows and write side by side, some 4 times faster than rows apart.  The
+    // rows are turned by the column, for the reader's banks.
     if (live) {
-      const int owner = row / per;
-      const uint32_t to = remote(uex + ((rank * per + row - owner * per) * a.rw) * 4, owner);
-      const int units = a.rw / 4 - 1;
-#pragma unroll 1
+      const int owner = row / per, mine = row - owner * per;
+      const uint32_t to = remote(uex + rank * per * a.rw * 4, owner);
+#pragma unroll 2
       for (int ch = half * (a.rw / 16); ch < (half + 1) * (a.rw / 16); ++ch) {
         float v[8];
         tmem_load8(lanes + ch * 8, v);
         tmem_wait_load();
         tmem_loaded(v);
-        const uint32_t u = ch * 2, t = row & units & ~1;
-        store_remote(to + ((u ^ t) << 4), make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                     __float_as_uint(v[3])));
-        store_remote(to + (((u ^ t) + 1) << 4), make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                                           __float_as_uint(v[6]), __float_as_uint(v[7])));
+        const uint32_t at = to + ((ch * 2 * per + ((mine + ch) & (per - 1))) << 4);
+        store_remote(at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        store_remote(at + (per << 4),
+                     make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
       }
     }
     cluster_sync();
     for (int e = tid; e < per * a.rw / 8; e += kThreads) {
       const int mine = e / (a.rw / 8), ch = e - mine * (a.rw / 8), r = rank * per + mine;
-      const uint32_t u = (ch * 2) ^ (r & (a.rw / 4 - 1) & ~1);
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < a.cluster; ++k) {
-        const float4* from = reinterpret_cast<const float4*>(ex + ((k * per + mine) * a.rw) * 4 + (u << 4));
-        const float4 x = from[0], y = from[1];
+        const float4* from = reinterpret_cast<const float4*>(ex + k * per * a.rw * 4) + ch * 2 * per + ((mine + ch) & (per - 1));
+        const float4 x = from[0], y = from[per];
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
       }
       float d = 0.f;
@@ -289,14 +290,14 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
         tmem_loaded(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = fmaf(a.p.cb, u[i], f1 * fmaf(diag + da[ch * 8 + i], u[i], v[i]));
-        if (row >> 3 == ch) {
+        const int on = row >> 3 == ch ? row & 7 : 8;  // selects: a branch for each lane's place takes 400 cycles
+        float d = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((row & 7) == i) {
-              db[row] = fmaf(diag, fmaf(f1, diag, a.p.cb), u[i]) + a.p.ca * a.p.sa;
-              u[i] = 0.f;
-            }
+        for (int i = 0; i < 8; ++i) {
+          d = on == i ? u[i] : d;
+          u[i] = on == i ? 0.f : u[i];
         }
+        if (on < 8) db[row] = fmaf(diag, fmaf(f1, diag, a.p.cb), d) + a.p.ca * a.p.sa;
         uint4 hi, lo;
         split8(u, hi, lo);
         *reinterpret_cast<uint4*>(ah + at) = hi;
@@ -348,7 +349,7 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   const float inv = 1.f / a.p.sx;
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
-    const int y = e / across, x = (e - y * across) * 8;
+    const int e1 = e / side, e0 = e - e1 * side, y = a.s.tall ? e0 : e1, x = (a.s.tall ? e1 : e0) * 8;
     float v[8], w[8];
     if (!a.s.tall) {
       const int at = image_at(y, x >> 3);

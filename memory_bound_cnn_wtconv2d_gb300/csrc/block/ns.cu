@@ -23,7 +23,8 @@
 // whose few roundings do not average out, keep pairs for A and B too and add
 // the products lo hi + hi lo + hi hi (`split`).  The tensor core's additions
 // truncate, some 2^-22 of the sum each; `split` spreads the sum over kSegments
-// accumulators, which the epilogue adds, to keep that below 1e-5.
+// accumulators (one for the small products), which the epilogue adds, to keep
+// that below 1e-5.
 //
 // Layout.  Every matrix lies in the workspace as 64 x 64 sub-blocks whose 8 KB
 // are the 128-byte-swizzled image that the tensor core reads, so that an
@@ -324,17 +325,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   uint32_t accph = 0;       // accumulator sets: one parity bit each
   uint32_t epiph = 0, nth = 0;  // epilogue: parity of each buffer's loads, sub-tiles seen
   uint32_t fetched[2] = {0, 0};  // loads into each buffer
-  const int passes = a.p.split ? 3 : 1;
+  const int planes = a.p.split ? 2 : 1;  // hi, or hi and lo
   for (int step = 0; ok && step < a.p.steps; ++step, cur ^= 1) {
     for (int phase = 0; ok && phase < 3; ++phase) {
       const int tiles = a.s.count * (phase == 0 ? a.t1 : phase == 1 ? a.t2 : a.t3);
       const int nk = phase == 0 ? a.cb : a.rk;
       // accumulators: two sets of up to 256 columns, or one of 4 x 128
       const int nbw = phase == 0 ? a.nb1 : phase == 1 ? a.nb2 : a.nb3;
-      const int segs = a.p.split ? min(kSegments, nk) : 1;
+      // of which, split, the first takes the products with a lo and the others share the sum of hi hi
+      const int segs = a.p.split ? 1 + min(kSegments - 1, nk) : 1;
       const uint32_t seg_cols = nbw * 64, sets = a.p.split && nbw == 2 ? 1 : 2;
       uint32_t acc = 0;
-      const int stage_bytes = (2 + nbw) * kSub, stages = min(kStages, kRing / (2 + nbw));
+      const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, stages = min(kStages, kRing / (planes * (2 + nbw)));
       int stage = 0;
       if (warp == 0 || warp == 10) {
         const bool first = warp == 0;  // the operand whose rows are the tile's rows
@@ -347,35 +349,37 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         for (int t = blockIdx.x; t < tiles && go; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
           const int i = first ? 2 * x.i : x.j, n = first ? 2 : x.nb;
-          for (int pass = 0; pass < passes && go; ++pass) {
-            const unsigned char* src = (a.p.split && pass == (first ? 0 : 1) ? lo : hi) + x.mat * (of_x ? a.xbytes : a.abytes);
-            const unsigned char* along = src + at_sub(i, 0, of_x ? a.cb : a.rb);   // rows i.. of column k
-            const unsigned char* across = src + at_sub(0, i, of_x ? a.cb : a.rb);  // row k, columns i..
-            const uint32_t row_pair = 2u * (of_x ? a.cb : a.rb) * kSub;
-            const uint32_t bytes = n * kSub;
-            for (int k = 0; k < nk; ++k, along += 2 * kSub) {
-              const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
-              const bool km = phase == 0 || (!of_x && stored(a, i, k));
-              go = wait_warp(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1);
-              if (!go) break;
-              filled |= 1u << stage;
-              if (elect_one()) {
-                mbar_expect(bar, bytes);
+          const long long at = x.mat * (of_x ? a.xbytes : a.abytes);
+          const int ncols = of_x ? a.cb : a.rb;
+          const uint32_t row_pair = 2u * ncols * kSub, bytes = n * kSub;
+          uint64_t along = at + at_sub(i, 0, ncols);           // rows i.. of column k
+          const uint64_t across = at + at_sub(0, i, ncols);    // row k, columns i..
+          for (int k = 0; k < nk; ++k, along += 2 * kSub) {
+            const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
+            const bool km = phase == 0 || (!of_x && stored(a, i, k));
+            go = wait_warp(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1);
+            if (!go) break;
+            filled |= 1u << stage;
+            if (elect_one()) {
+              mbar_expect(bar, planes * bytes);
+              for (int p = 0; p < planes; ++p) {
+                const unsigned char* src = p ? lo : hi;
+                const uint32_t to = dst + p * lo_at;
                 if (km) {  // pairs of rows lie row_pair apart (i even or n = 1)
-                  bulk_load(dst, along, n > 1 ? 2 * kSub : kSub, bar);
-                  if (n > 2) bulk_load(dst + 2 * kSub, along + row_pair, bytes - 2 * kSub, bar);
+                  bulk_load(to, src + along, n > 1 ? 2 * kSub : kSub, bar);
+                  if (n > 2) bulk_load(to + 2 * kSub, src + along + row_pair, bytes - 2 * kSub, bar);
                 } else {
-                  const unsigned char* from = across + (uint64_t)(k >> 1) * row_pair + (k & 1) * kSub;
-                  bulk_load(dst, from, kSub, bar);
+                  const unsigned char* from = src + across + (uint64_t)(k >> 1) * row_pair + (k & 1) * kSub;
+                  bulk_load(to, from, kSub, bar);
 #pragma unroll
                   for (int c = 1; c < kMaxNb; ++c)
-                    if (c < n) bulk_load(dst + c * kSub, from + c * 2 * kSub, kSub, bar);
+                    if (c < n) bulk_load(to + c * kSub, from + c * 2 * kSub, kSub, bar);
                 }
               }
-              __syncwarp();
-              ph ^= 1u << stage;
-              if (++stage == stages) stage = 0;
             }
+            __syncwarp();
+            ph ^= 1u << stage;
+            if (++stage == stages) stage = 0;
           }
         }
       } else if (warp == 1) {
@@ -387,36 +391,40 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           tc_fence_after();
           uint32_t begun = 0;  // segments that hold a sum
           const uint32_t idesc0 = instr_desc(x.nb * 64, true, true);
-          int next = 0;        // the last pass moves to the next segment here
-          uint32_t seg = 0;
-          for (int pass = 0; pass < passes && go; ++pass) {
-            const bool last = pass + 1 == passes;
-            if (last) next = (nk + segs - 1) / segs;
-            for (int k = 0; k < nk; ++k) {
-              if (last && k == next) {
-                ++seg;
-                next = ((seg + 1) * nk + segs - 1) / segs;
-              }
-              const bool akm = phase == 0 || stored(a, 2 * x.i, k);
-              const bool bkm = phase == 0 || (phase == 1 && stored(a, x.j, k));
-              const uint32_t sa = base + stage * stage_bytes, idesc = idesc0 | (akm ? 0u : 1u << 15) | (bkm ? 0u : 1u << 16);
-              uint32_t da = desc_low(sa, akm), db = desc_low(sa + 2 * kSub, bkm);
-              const uint32_t ka = desc_step(akm), kb = desc_step(bkm);
-              const uint32_t d = tmem + acc * 256 + seg * seg_cols;
-              go = wait_warp(sh, &sh.full[stage], ph >> stage & 1);
-              if (!go) break;
-              tc_fence_after();
-              if (elect_one()) {
-                mma_f16(d, da, db, kDescHigh, idesc, begun >> seg & 1);
-#pragma unroll
-                for (int q = 1; q < 4; ++q) mma_f16(d, da + q * ka, db + q * kb, kDescHigh, idesc, 1);
-                mma_commit(smem_addr(&sh.empty[stage]));
-              }
-              __syncwarp();
-              begun |= 1u << seg;
-              ph ^= 1u << stage;
-              if (++stage == stages) stage = 0;
+          const uint32_t d0 = tmem + acc * 256;
+          // split: chunk k of hi hi goes to segment 1 + k * (segs - 1) / nk
+          uint32_t seg = a.p.split ? 1 : 0;
+          int next = a.p.split ? (nk + segs - 2) / (segs - 1) : nk;
+          for (int k = 0; k < nk; ++k) {
+            if (k == next) {
+              ++seg;
+              next = (seg * nk + segs - 2) / (segs - 1);
             }
+            const bool akm = phase == 0 || stored(a, 2 * x.i, k);
+            const bool bkm = phase == 0 || (phase == 1 && stored(a, x.j, k));
+            const uint32_t sa = base + stage * stage_bytes, idesc = idesc0 | (akm ? 0u : 1u << 15) | (bkm ? 0u : 1u << 16);
+            const uint32_t da = desc_low(sa, akm), db = desc_low(sa + 2 * kSub, bkm);
+            const uint32_t ka = desc_step(akm), kb = desc_step(bkm), d = d0 + seg * seg_cols, lo = lo_at >> 4;
+            go = wait_warp(sh, &sh.full[stage], ph >> stage & 1);
+            if (!go) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if (a.p.split) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  mma_f16(d0, da + lo + q * ka, db + q * kb, kDescHigh, idesc, k | q);
+                  mma_f16(d0, da + q * ka, db + lo + q * kb, kDescHigh, idesc, 1);
+                }
+              }
+              mma_f16(d, da, db, kDescHigh, idesc, begun >> seg & 1);
+#pragma unroll
+              for (int q = 1; q < 4; ++q) mma_f16(d, da + q * ka, db + q * kb, kDescHigh, idesc, 1);
+              mma_commit(smem_addr(&sh.empty[stage]));
+            }
+            __syncwarp();
+            begun |= 1u << seg;
+            ph ^= 1u << stage;
+            if (++stage == stages) stage = 0;
           }
           if (elect_one()) mma_commit(smem_addr(&sh.acc_full[acc]));
           __syncwarp();
@@ -662,10 +670,10 @@ int sym_tiles(int rb, int nb, int gsh) {
 
 // Tile widths: the least number of rounds times the cost of a tile, in cycles:
 // a K step of 64 is bound by its copies ((2 + nb) sub-blocks at 64 bytes a
-// cycle), a tile adds its start and its epilogue.
-double tile_cost(long long tiles, int sms, int nb, int nk, int passes) {
+// cycle, twice when split), a tile adds its start and its epilogue.
+double tile_cost(long long tiles, int sms, int nb, int nk, int planes) {
   const double rounds = (double)((tiles + sms - 1) / sms);
-  return rounds * ((2 + nb) * 128.0 * nk * passes + 1500 + 400.0 * nb);
+  return rounds * ((2 + nb) * 128.0 * nk * planes + 1500 + 400.0 * nb);
 }
 
 NsMain plan(const wtconv_ns_desc_t& d) {
@@ -679,7 +687,7 @@ NsMain plan(const wtconv_ns_desc_t& d) {
   a.xbytes = (long long)a.rb * a.cb * kSub;
   a.abytes = (long long)a.rb * a.rb * kSub;
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
-  const int passes = a.p.split ? 3 : 1, most = a.p.split ? kSplitNb : kMaxNb;
+  const int planes = a.p.split ? 2 : 1, most = a.p.split ? kSplitNb : kMaxNb;
   double best = -1;
   for (int gsh = 1; gsh <= 2; ++gsh) {
     int pick[2] = {1, 1};
@@ -687,7 +695,7 @@ NsMain plan(const wtconv_ns_desc_t& d) {
     for (int ph = 0; ph < 2; ++ph) {
       double b = -1;
       for (int nb = 1; nb <= (1 << gsh) && nb <= most; nb *= 2) {
-        const double c = tile_cost((long long)d.count * sym_tiles(a.rb, nb, gsh), sms, nb, ph ? a.rk : a.cb, passes);
+        const double c = tile_cost((long long)d.count * sym_tiles(a.rb, nb, gsh), sms, nb, ph ? a.rk : a.cb, planes);
         if (b < 0 || c < b) b = c, pick[ph] = nb;
       }
       cost += b;
@@ -696,7 +704,7 @@ NsMain plan(const wtconv_ns_desc_t& d) {
   }
   best = -1;
   for (int nb = 1; nb <= most; ++nb) {
-    const double c = tile_cost((long long)d.count * (a.rb / 2) * ((a.cb + nb - 1) / nb), sms, nb, a.rk, passes);
+    const double c = tile_cost((long long)d.count * (a.rb / 2) * ((a.cb + nb - 1) / nb), sms, nb, a.rk, planes);
     if (best < 0 || c < best) best = c, a.nb3 = nb;
   }
   a.t1 = sym_tiles(a.rb, a.nb1, a.gsh);

@@ -54,13 +54,18 @@ constexpr int kNormThreads = 256;
 constexpr int kNormMax = 256;      // partial sums of squares per matrix, at most
 constexpr int kEpiThreads = 256;   // warps 2-9
 constexpr int kThreads = 96 + kEpiThreads;  // warps 0 and 10: copies of the two operands, warp 1: MMAs
-constexpr int kRing = 20;          // sub-blocks of operands in flight
+// Sub-blocks of operands in flight, beside two epilogue buffers.  Where tiles
+// are widest and long (32 K steps hide an epilogue without a second buffer),
+// beside one: three stages are a latency short of keeping the MMAs fed
+// (4096^2 1217 -> 1119 us with four; 2048 x 1024, 16 steps, 283 -> 302).
+constexpr int kRing = 20, kRingWide = 24;
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
 constexpr int kSegments = 4;       // accumulators of one tile when split
 constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
-constexpr int kSmem = kRing * kSub + 2 * kEpiBytes + 1024;
+constexpr int kSmem = kRingWide * kSub + kEpiBytes + 1024;
+static_assert(kRing * kSub + 2 * kEpiBytes == kRingWide * kSub + kEpiBytes, "one layout for both");
 static_assert(kThreads / 32 * 64 * 65 * 4 <= kRing * kSub + 2 * kEpiBytes, "the first and last pass's tiles");
 
 static __device__ unsigned int g_ns_faults;
@@ -336,7 +341,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       const int segs = a.p.split ? 1 + min(kSegments - 1, nk) : 1;
       const uint32_t seg_cols = nbw * 64, sets = a.p.split && nbw == 2 ? 1 : 2;
       uint32_t acc = 0;
-      const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, stages = min(kStages, kRing / (planes * (2 + nbw)));
+      const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, ebufs = nbw == kMaxNb && nk >= 32 ? 1 : 2;
+      const int stages = min(kStages, (ebufs == 1 ? kRingWide : kRing) / (planes * (2 + nbw)));
       int stage = 0;
       if (warp == 0 || warp == 10) {
         const bool first = warp == 0;  // the operand whose rows are the tile's rows
@@ -435,7 +441,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         // row `row` of the tile and half of the columns of each sub-tile
         const int row = (warp & 3) * 32 + lane, col_half = (warp - 2) >> 2, sub = row >> 6, y = row & 63;
         const bool leader = tid == 64;
-        const uint32_t ebase = base + kRing * kSub;
+        const uint32_t ebase = base + kRingWide * kSub;  // buffer 1 lies before buffer 0
         // what the result is made from besides the product, and where it goes
         const bool in = phase != 0, lo = phase == 2 || a.p.split;
         const unsigned char* ih = phase == 1 ? a.ah : a.xh[cur];
@@ -452,14 +458,14 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           const long long at0 = x.mat * obytes + at_sub(2 * x.i, x.j, ncols);
           auto fetch = [&](int s, uint32_t b) {  // leader: what sub-tile s is made from, into buffer b
             ++fetched[b];
-            const uint32_t bar = smem_addr(&sh.epi[b]), dst = ebase + b * kEpiBytes;
+            const uint32_t bar = smem_addr(&sh.epi[b]), dst = ebase - b * kEpiBytes;
             mbar_expect(bar, (lo ? 4 : 2) * kSub);
             bulk_load(dst, ih + at0 + s * 2 * kSub, 2 * kSub, bar);
             if (lo) bulk_load(dst + 2 * kSub, il + at0 + s * 2 * kSub, 2 * kSub, bar);
           };
           if (in && leader) {
             bulk_wait_read();
-            fetch(0, nth & 1);
+            fetch(0, nth & (ebufs - 1));
           }
           const int grow = (x.mat * a.rb + 2 * x.i) * 64 + row;  // row in the diagonals
           float diag = 0.f;
@@ -474,17 +480,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           __syncwarp();
           tc_fence_after();
           for (int s = 0; s < x.nb; ++s, ++nth) {
-            const uint32_t b = nth & 1;
+            const uint32_t b = nth & (ebufs - 1);
             if (leader) {
-              bulk_wait_read();  // the other buffer's last store has left it
-              if (in && s + 1 < x.nb) fetch(s + 1, b ^ 1);
+              bulk_wait_read();  // the last store has left its buffer
+              if (in && ebufs == 2 && s + 1 < x.nb) fetch(s + 1, b ^ 1);
+              if (in && ebufs == 1 && s > 0) fetch(s, 0);
             }
             if (in) {
               wait(sh, &sh.epi[b], (epiph >> b) & 1);
               epiph ^= 1u << b;
             }
             named_sync<kEpiThreads>(1);
-            unsigned char* buf = gen + kRing * kSub + b * kEpiBytes + sub * kSub + y * 128;
+            unsigned char* buf = gen + kRingWide * kSub - b * kEpiBytes + sub * kSub + y * 128;
             const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc * 256 + s * 64 + col_half * 32;
             const bool on_diagonal = phase < 2 && 2 * x.i + sub == x.j + s;
             // rolled: each tile runs this once, and unrolled it is bound by fetching instructions
@@ -564,7 +571,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             }
             named_sync<kEpiThreads>(1);
             if (leader && got) {
-              const uint32_t src = ebase + b * kEpiBytes;
+              const uint32_t src = ebase - b * kEpiBytes;
               bulk_store(oh + at0 + s * 2 * kSub, src, 2 * kSub);
               if (lo) bulk_store(ol + at0 + s * 2 * kSub, src + 2 * kSub, 2 * kSub);
               bulk_commit();

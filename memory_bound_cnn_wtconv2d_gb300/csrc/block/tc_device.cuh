@@ -117,7 +117,8 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[8]) {
 // 8-row stride, the version and the swizzle, the same for all.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool k_major, uint32_t mn_stride = 8192) {
-  return (addr >> 4) | ((k_major ? 1u : mn_stride >> 4) << 16);
+  // in a cluster the address also holds the CTA's rank, above these bits
+  return ((addr & 0x3FFFF) >> 4) | ((k_major ? 1u : mn_stride >> 4) << 16);
 }
 // What a K = 16 step adds to it: 32 bytes along K, or 16 rows of 128 bytes.
 __device__ __forceinline__ uint32_t desc_step(bool k_major) { return k_major ? 32u >> 4 : 2048u >> 4; }

@@ -55,7 +55,8 @@ def matrices(*shape, dtype=F32, seed=0, size=1e-3):
 
 
 SHAPES = [(1, 1), (1, 7), (9, 1), (3, 5), (16, 16), (64, 64), (65, 63), (96, 384), (384, 96), (127, 129), (128, 128),
-          (129, 130), (192, 768), (200, 1000), (257, 255), (333, 1201), (512, 512), (1000, 130), (640, 1030), (5, 4000)]
+          (129, 130), (192, 768), (200, 1000), (257, 255), (333, 1201), (512, 512), (1000, 130), (640, 1030), (5, 4000), (128, 1024),
+          (100, 1500), (2048, 60), (128, 2048), (700, 700), (1100, 1030), (900, 2300), (2100, 2050)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])

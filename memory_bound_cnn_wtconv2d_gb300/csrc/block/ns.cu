@@ -55,9 +55,11 @@ constexpr int kNormMax = 256;      // partial sums of squares per matrix, at mos
 constexpr int kEpiThreads = 256;   // warps 2-9
 constexpr int kThreads = 96 + kEpiThreads;  // warps 0 and 10: copies of the two operands, warp 1: MMAs
 // Sub-blocks of operands in flight, beside two epilogue buffers.  Where tiles
-// are widest and long (32 K steps hide an epilogue without a second buffer),
-// beside one: three stages are a latency short of keeping the MMAs fed
-// (4096^2 1217 -> 1119 us with four; 2048 x 1024, 16 steps, 283 -> 302).
+// are widest and long (32 K steps, or 16 of three products each, hide an
+// epilogue without a second buffer), beside one: with a stage less the copies'
+// latency leaves the MMAs waiting (4096^2 1217 -> 1119 us, float32 3650 -> 3130,
+// 4 x 2048 x 1024 float32 569 -> 539; bfloat16 of 16 steps 283 -> 302).  A third
+// buffer for short products cost them 4 %.
 constexpr int kRing = 20, kRingWide = 24;
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
@@ -341,7 +343,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       const int segs = a.p.split ? 1 + min(kSegments - 1, nk) : 1;
       const uint32_t seg_cols = nbw * 64, sets = a.p.split && nbw == 2 ? 1 : 2;
       uint32_t acc = 0;
-      const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, ebufs = nbw == kMaxNb && nk >= 32 ? 1 : 2;
+      const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, ebufs = nbw == (a.p.split ? kSplitNb : kMaxNb) && nk >= (a.p.split ? 16 : 32) ? 1 : 2;
       const int stages = min(kStages, (ebufs == 1 ? kRingWide : kRing) / (planes * (2 + nbw)));
       int stage = 0;
       if (warp == 0 || warp == 10) {

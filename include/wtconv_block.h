@@ -97,7 +97,8 @@ size_t wtconv_ns_workspace_size(const wtconv_ns_desc_t* desc);
  * written to out (transposed back) in desc->dtype.  g and out are HOST arrays
  * of count device pointers, read during the call.  The products take operands
  * of 11 significand bits for bfloat16 stacks and of 22 bits for float16 and
- * float32 stacks, with float32 accumulation. */
+ * float32 stacks and for matrices of fewer than 16 rows or columns, with
+ * float32 accumulation. */
 wtconv_status_t wtconv_orthogonalize(const wtconv_ns_desc_t* desc, const void* const* g, long long g_ld,
                                      void* const* out, long long out_ld, void* ws, size_t ws_bytes,
                                      void* stream);
@@ -107,7 +108,8 @@ wtconv_status_t wtconv_orthogonalize(const wtconv_ns_desc_t* desc, const void* c
  *     u = nesterov ? mu momentum + (1 - mu) grad : momentum
  *     weight <- decay weight - rate orthogonalize(u)
  * weight and grad in desc->dtype (row strides w_ld, g_ld), momentum float32
- * (row stride m_ld).  decay is 1 - learning rate * weight decay and rate the
+ * (row stride m_ld).  Operands of 22 bits for float32 weights, of 11 for
+ * 16-bit ones, whose rounding is far above what that leaves on a step.  decay is 1 - learning rate * weight decay and rate the
  * learning rate times the shape's scale. */
 wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* desc, void* const* weight, long long w_ld,
                                  const void* const* grad, long long g_ld, float* const* momentum,

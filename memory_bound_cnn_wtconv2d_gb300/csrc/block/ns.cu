@@ -685,11 +685,11 @@ double tile_cost(long long tiles, int sms, int nb, int nk, int planes) {
   return rounds * ((2 + nb) * 128.0 * nk * planes + 1500 + 400.0 * nb);
 }
 
-NsMain plan(const wtconv_ns_desc_t& d) {
+NsMain plan(const wtconv_ns_desc_t& d, bool muon) {
   NsMain a = {};
   a.s = shape_of(d);
   const NsShape& s = a.s;
-  a.p = poly_of(d, s);
+  a.p = poly_of(d, s, muon);
   a.rk = (s.r + 63) / 64;
   a.rb = (a.rk + 1) & ~1;
   a.cb = (s.c + 63) / 64;
@@ -726,7 +726,7 @@ constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormMax * 4;  // b
 
 template <typename T>
 cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
-  NsMain a = plan(d);
+  NsMain a = plan(d, k.muon);
   unsigned char* w = (unsigned char*)ws;
   a.sync = (unsigned int*)w;
   float* part = (float*)(w + 256);
@@ -773,7 +773,7 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
 
 size_t ns_workspace(const wtconv_ns_desc_t& d) {
   if (ns_small_takes(d)) return 0;
-  const NsMain a = plan(d);
+  const NsMain a = plan(d, false);  // of the two uses the one that needs more
   const size_t x = (size_t)a.xbytes * d.count, m = (size_t)a.abytes * d.count;
   return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.p.split ? 4 : 2) * m;
 }

@@ -115,10 +115,12 @@ inline NsShape shape_of(const wtconv_ns_desc_t& d) {
 
 // Entries of X near 1: |X|_F is about 1 at first; those of A, B near 1 on the
 // diagonal.  Both capped so that no entry passes float16's range.
-inline NsPoly poly_of(const wtconv_ns_desc_t& d, const NsShape& s) {
+// Pairs where the result shows more than 11 bits: not where a float16 weight
+// takes a step of a few per cent of its size.
+inline NsPoly poly_of(const wtconv_ns_desc_t& d, const NsShape& s, bool muon) {
   NsPoly p = {};
   p.steps = d.steps;
-  p.split = d.dtype != WTCONV_BF16 || s.r < 16;
+  p.split = d.dtype == WTCONV_F32 || (d.dtype == WTCONV_F16 && !muon) || s.r < 16;
   p.ca = d.a; p.cb = d.b; p.cc = d.c;
   int ex = (ceil_log2(s.r) + ceil_log2(s.c)) / 2, ea = ceil_log2(s.r);
   if (ex > 12) ex = 12;

@@ -387,7 +387,7 @@ int smem_of(const NsSmall& a) {
 
 bool plan(const wtconv_ns_desc_t& d, NsSmall& a) {
   a.s = shape_of(d);
-  a.p = poly_of(d, a.s);
+  a.p = poly_of(d, a.s, false);  // of the two uses the one that needs more shared memory
   if (a.s.r > kRows || a.s.r < 1) return false;
   a.rw = a.s.r <= 64 ? 64 : 128;
   const int cb = (a.s.c + 63) / 64;
@@ -427,6 +427,7 @@ bool ns_small_takes(const wtconv_ns_desc_t& d) {
 cudaError_t ns_small_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, cudaStream_t s) {
   NsSmall a = {};
   plan(d, a);
+  a.p.split = poly_of(d, a.s, k.muon).split;
   a.s.wide = is_wide(d, k, p);
   if (d.dtype == WTCONV_F32) return launch_t<float>(a, k, p, s);
   if (d.dtype == WTCONV_F16) return launch_t<__half>(a, k, p, s);

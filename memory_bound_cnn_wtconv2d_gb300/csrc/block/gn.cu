@@ -81,11 +81,11 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   if (p.cluster) {
     if (op == WTCONV_OP_GN_BWD) p.ws_bytes = n * p.cluster * 2 * d.C * 4;
   } else {
-    if (vec == 8) p.vec = vec = 4;  // eight channels' values do not fit the streamed kernels' registers
     p.tx = d.C / vec < kThreads ? d.C / vec : kThreads;
     p.ty = kThreads / p.tx;
     // one wave of CTAs, at least 8 rows a thread
-    long long want = (4LL * sms - (op == WTCONV_OP_GN_BWD ? kExtraCtas : 0)) / d.N;
+    const int slots = sms * streamed_ctas(op, vec) - (op == WTCONV_OP_GN_BWD ? extra_ctas(d.C) : 0);
+    long long want = slots / d.N;
     const long long most = (d.S + 8LL * p.ty - 1) / (8LL * p.ty);
     if (want > most) want = most;
     if (want < 1) want = 1;

@@ -514,6 +514,15 @@ bwd_reduce(int C, long long blocks, const float* part, float* dw, float* db) {
 
 // ---------------------------------------------------------------- streamed
 
+// CTAs an SM: 128 registers for the forward of eight channels a thread and the
+// backward, 80 otherwise; a wave of fewer CTAs, each with more rows, spends less
+// on its start and its sums.  Of four (64 registers, no more than four channels
+// a thread): 16 x 112 x 112 x 64 bf16 17.9 -> 15.7 us forward and 30.7 -> 25.8
+// backward, 4 x 128 x 128 x 96 15.4 -> 13.9 and 21.9 -> 17.1, 32 x 128 x 128 x 96
+// the same and 107 -> 101.
+template <int VEC> constexpr int kFwdCtas = streamed_ctas(WTCONV_OP_GN_FWD, VEC);
+constexpr int kBwdCtas = streamed_ctas(WTCONV_OP_GN_BWD, 1);
+
 struct Streamed {
   int tx, ty;        // threads across channel vectors, rows side by side
   int splits, rows;  // row ranges of a sample, one CTA each
@@ -556,7 +565,7 @@ __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.w
 
 // part[n][split][G] = (mean, m2) over the split's rows
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kFwdCtas<VEC>)
 fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
          float2* __restrict__ part) {
   constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
@@ -636,7 +645,7 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kFwdCtas<VEC>)
 fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
           const float* __restrict__ w, const float* __restrict__ b, const float2* part, T* __restrict__ y,
           float* __restrict__ mean_out, float* __restrict__ rstd_out) {
@@ -703,12 +712,12 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
 // part[n][split][2][C]: sums of dz and of dz * xhat over the split's rows;
 // gpart[n][split][2][G]: the groups' weighted sums.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
 bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
          const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
          const float* __restrict__ w, const float* __restrict__ b, float* __restrict__ part,
          float* __restrict__ gpart) {
-  constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
+  constexpr int P = kPairs<VEC>, kBatch = VEC == 8 ? 4 : 8;  // rows loaded together
   extern __shared__ __align__(16) float sm[];
   const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
   const long long n = blockIdx.x / p.splits;
@@ -788,12 +797,12 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
 bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
           const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
           const float* __restrict__ w, const float* __restrict__ b, const float* part, const float* gpart,
           T* __restrict__ dx, float* __restrict__ dw, float* __restrict__ db) {
-  constexpr int P = kPairs<VEC>, kBatch = VEC * sizeof(T) == 16 ? 2 : 4;  // rows loaded together
+  constexpr int P = kPairs<VEC>, kBatch = VEC == 8 ? 4 : 8;  // rows loaded together
   extern __shared__ __align__(16) float sm[];  // [2][G], kThreads; or 2 kThreads
   if ((int)blockIdx.x < p.extra) {
     wait_previous();
@@ -917,21 +926,17 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
     return launch_cluster(k, dim3((unsigned)d.N * p.cluster, d.C / p.ch), p.cluster, smem, s, a, r, (const T*)x, w, b,
                           (T*)y, mean, rstd);
   }
-  if constexpr (VEC == 8) {
-    return cudaErrorInvalidValue;  // never planned
-  } else {
-    float2* part = (float2*)ws;
-    const Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
-    const unsigned grid = (unsigned)(d.N * p.splits);
-    const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
-    cudaError_t e = wt::ensure_smem((const void*)fwd_read<T, VEC>, smem);
-    if (e != cudaSuccess) return e;
-    fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_next(fwd_apply<T, VEC, ACT>, dim3(grid), kThreads, 4 * (2 * d.G + kThreads), s, a, q, (const T*)x, w, b,
-                       (const float2*)part, (T*)y, mean, rstd);
-  }
+  float2* part = (float2*)ws;
+  const Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+  const unsigned grid = (unsigned)(d.N * p.splits);
+  const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
+  cudaError_t e = wt::ensure_smem((const void*)fwd_read<T, VEC>, smem);
+  if (e != cudaSuccess) return e;
+  fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_next(fwd_apply<T, VEC, ACT>, dim3(grid), kThreads, 4 * (2 * d.G + kThreads), s, a, q, (const T*)x, w, b,
+                     (const float2*)part, (T*)y, mean, rstd);
 }
 
 template <typename T, int VEC, int ACT>
@@ -951,24 +956,20 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
     if (e != cudaSuccess || (!dw && !db)) return e;
     return launch_next(bwd_reduce, dim3((d.C + 31) / 32), 1024, 0, s, d.C, d.N * p.cluster, (const float*)part, dw, db);
   }
-  if constexpr (VEC == 8) {
-    return cudaErrorInvalidValue;  // never planned
-  } else {
-    float* part = (float*)ws;
-    float* gpart = part + (size_t)d.N * p.splits * 2 * d.C;
-    Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
-    if (dw || db) q.extra = (d.C + 31) / 32 < kExtraCtas ? (d.C + 31) / 32 : kExtraCtas;
-    const unsigned grid = (unsigned)(d.N * p.splits);
-    int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
-    cudaError_t e = wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem);
-    if (e != cudaSuccess) return e;
-    bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w, b, part, gpart);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    smem = 4 * (2 * d.G + 2 * kThreads);
-    return launch_next(bwd_apply<T, VEC, ACT>, dim3(grid + q.extra), kThreads, smem, s, a, q, (const T*)dy, (const T*)x,
-                       mean, rstd, w, b, (const float*)part, (const float*)gpart, (T*)dx, dw, db);
-  }
+  float* part = (float*)ws;
+  float* gpart = part + (size_t)d.N * p.splits * 2 * d.C;
+  Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+  if (dw || db) q.extra = extra_ctas(d.C);
+  const unsigned grid = (unsigned)(d.N * p.splits);
+  int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
+  cudaError_t e = wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem);
+  if (e != cudaSuccess) return e;
+  bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w, b, part, gpart);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  smem = 4 * (2 * d.G + 2 * kThreads);
+  return launch_next(bwd_apply<T, VEC, ACT>, dim3(grid + q.extra), kThreads, smem, s, a, q, (const T*)dy, (const T*)x,
+                     mean, rstd, w, b, (const float*)part, (const float*)gpart, (T*)dx, dw, db);
 }
 
 #define WTB_ACTS(T, V, CALL)                                  \

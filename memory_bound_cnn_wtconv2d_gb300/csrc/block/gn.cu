@@ -71,12 +71,15 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   plan_resident(d, op, vec, sms, p);
   const size_t n = (size_t)d.N;
-  if (p.cluster > 1) {
-    // Clusters only while latency counts; they measured slower than the
-    // streamed form on larger tensors, the more so the narrower the lines.
+  if (p.cluster) {
+    // Narrow lines cost the more the larger the tensor: resident CTAs of lines
+    // below 64 bytes take 25.8 us where the streamed form takes 18.7 (64 x 28 x 28
+    // x 192 f32, forward) and 32 where it takes 20 (64 x 32 x 32 x 128 bf16,
+    // backward); at 16 MB 11.6 and 13.3.  Clusters only while latency counts.
     const int es = d.dtype == WTCONV_F32 ? 4 : 2, line = p.ch * es;
-    const long long read = d.N * d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2);
-    if (!((line >= 48 && read <= 12LL << 20) || (line >= 64 && read <= 24LL << 20))) p.cluster = 0;
+    const long long read = (d.N * d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2)) >> 20;
+    if (p.cluster == 1 ? line < 64 && read > 20 : !((line >= 48 && read <= 12) || (line >= 64 && read <= 24)))
+      p.cluster = 0;
   }
   if (p.cluster) {
     if (op == WTCONV_OP_GN_BWD) p.ws_bytes = n * p.cluster * 2 * d.C * 4;

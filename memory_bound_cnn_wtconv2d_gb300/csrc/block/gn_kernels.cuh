@@ -64,21 +64,21 @@ __device__ __forceinline__ void group_statistics(const float* st, int ty, int wi
   // lanes side by side over a group's entries, then over row lanes
   const int across = min(Cu, 32), down = 32 / across, t0 = lane / across, k0 = lane - t0 * across;
   const bool in = t0 < down;
+  const int lanes = min(ty, rows);  // that hold a row
   for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
+    const float *sg = st + g * Cu, *qg = q + g * Cu;
     float s = 0.f;
-    for (int t = in ? t0 : ty; t < ty; t += down) {
-      const float cnt = (float)(full + (t < extra));
-      for (int k = k0; k < Cu; k += across) s = fmaf(cnt, st[t * width + g * Cu + k], s);
+    for (int k = k0; k < Cu; k += across) {
+#pragma unroll 4
+      for (int t = in ? t0 : ty; t < lanes; t += down) s = fmaf((float)(full + (t < extra)), sg[t * width + k], s);
     }
     const float mean = rows > 0 ? warp_sum(s) / ((float)rows * (float)Cu) : 0.f;
     s = 0.f;
-    for (int t = in ? t0 : ty; t < ty; t += down) {
-      const int n = full + (t < extra);
-      if (n == 0) break;
-      const float cnt = (float)(n * unit);
-      for (int k = k0; k < Cu; k += across) {
-        const float d = st[t * width + g * Cu + k] - mean;
-        s += fmaf(cnt * d, d, q[t * width + g * Cu + k]);
+    for (int k = k0; k < Cu; k += across) {
+#pragma unroll 4
+      for (int t = in ? t0 : ty; t < lanes; t += down) {
+        const float d = sg[t * width + k] - mean;
+        s += fmaf((float)((full + (t < extra)) * unit) * d, d, qg[t * width + k]);
       }
     }
     s = warp_sum(s);

@@ -5,7 +5,8 @@ backward), Newton-Schulz orthogonalisation, and the optimiser step built on
 it.  As in ``wtconv``: argument checks and marshalling only, the C names, work
 on the current torch stream unless ``stream`` is given, outputs and workspaces
 may be passed in, a mismatch raises ``ValueError`` before anything is
-launched, and there is no CPU fallback.
+launched, and there is no CPU fallback.  What a call allocates belongs to the
+stream that it works on.
 """
 from __future__ import annotations
 
@@ -73,8 +74,17 @@ class _Here:
 _HERE = _Here()
 
 
-def _on(device):
-    """Makes `device` current for a call; nothing to do where it already is."""
+def _on(device, stream=None):
+    """Makes `device`, and a given stream, current for a call, so that what it
+    allocates belongs to the stream that uses it; nothing to do for the current
+    ones."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
     return _HERE if device.index is None or torch.cuda.current_device() == device.index else _c._device_ctx(device)
 
 
@@ -170,11 +180,9 @@ def _gn_layout(x, dy, num_groups, eps, activation):
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_of(stream, device):
-    """The stream handle of a call: the given stream's, else the device's current one's."""
-    if stream is None:
-        return _RAW_STREAM(device.index) if _RAW_STREAM is not None else torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream_of(device):
+    """The handle of the device's current stream."""
+    return _RAW_STREAM(device.index) if _RAW_STREAM is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _span(t):
@@ -222,7 +230,7 @@ def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activatio
         _float32(rstd, "rstd", lay.N * lay.G, device)
         _disjoint([("y", y), ("mean", mean), ("rstd", rstd), ("workspace", workspace)],
                   [("x", x), ("weight", weight), ("bias", bias)])
-    with _on(device):
+    with _on(device, stream):
         if y is None:
             y = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
         if mean is None:
@@ -233,7 +241,7 @@ def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activatio
         status = lib().wtconv_gn_act_fwd(
             lay.ref, x.data_ptr(), None if weight is None else weight.data_ptr(),
             None if bias is None else bias.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            None if ws is None else ws.data_ptr(), n, _stream_of(stream, device))
+            None if ws is None else ws.data_ptr(), n, _stream_of(device))
         if status:
             _c._check(status)
     return y, mean, rstd
@@ -259,7 +267,7 @@ def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, act
         _float32(dbias, "dbias", C, device)
         _disjoint([("dx", dx), ("dweight", dweight), ("dbias", dbias), ("workspace", workspace)],
                   [("dy", dy), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight), ("bias", bias)])
-    with _on(device):
+    with _on(device, stream):
         if dx is None:
             dx = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
         if dweight is None:
@@ -271,7 +279,7 @@ def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, act
             lay.ref, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), dx.data_ptr(),
             dweight.data_ptr(), dbias.data_ptr(), None if ws is None else ws.data_ptr(), n,
-            _stream_of(stream, device))
+            _stream_of(device))
         if status:
             _c._check(status)
     return dx, dweight, dbias
@@ -403,7 +411,7 @@ def wtconv_orthogonalize(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out
         _disjoint([("out", out), ("workspace", workspace)], [("g", g)])
     elif workspace is not None:
         _disjoint([("workspace", workspace)], [("g", g)])
-    with _on(s.device):
+    with _on(s.device, stream):
         fresh = out is None
         if fresh:
             out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
@@ -415,7 +423,7 @@ def wtconv_orthogonalize(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out
             ref, need = _ns_desc(s, k, steps, coefficients, eps)
             ws, n = _scratch(need, s.device, workspace)
             status = lib().wtconv_orthogonalize(ref, s.chunk(i, k), s.ld, o.chunk(i, k), o.ld,
-                                                None if ws is None else ws.data_ptr(), n, _stream_of(stream, s.device))
+                                                None if ws is None else ws.data_ptr(), n, _stream_of(s.device))
             if status:
                 _c._check(status)
     return out
@@ -440,7 +448,7 @@ def wtconv_muon_step(weight, grad, buffer, lr, momentum=0.95, nesterov=True, wei
     w.separate("weight")
     b.separate("buffer")
     _disjoint_stacks(w, g, b, workspace)
-    with _on(w.device):
+    with _on(w.device, stream):
         for i in range(0, w.count, NS_MAX_COUNT):
             k = min(NS_MAX_COUNT, w.count - i)
             ref, need = _ns_desc(w, k, steps, coefficients, eps)
@@ -448,7 +456,7 @@ def wtconv_muon_step(weight, grad, buffer, lr, momentum=0.95, nesterov=True, wei
             status = lib().wtconv_muon_step(
                 ref, w.chunk(i, k), w.ld, g.chunk(i, k), g.ld, b.chunk(i, k), b.ld, momentum,
                 int(bool(nesterov)), 1.0 - lr * weight_decay, lr * scale, None if ws is None else ws.data_ptr(), n,
-                _stream_of(stream, w.device))
+                _stream_of(w.device))
             if status:
                 _c._check(status)
     return weight

@@ -305,3 +305,21 @@ def test_refusals(ops):
         Muon([torch.nn.Parameter(torch.zeros(3))])
     with pytest.raises(ValueError):
         Muon([torch.nn.Parameter(torch.zeros(3, 3))], momentum=1.0)
+
+
+def test_workspace_belongs_to_the_given_stream(ops):
+    # the stream is held up while the caller's stream reuses all memory that is free to it
+    g = matrices(2, 300, 200, dtype=BF16, seed=31)
+    want = ops.wtconv_orthogonalize(g)
+    need = ops._ns_desc(ops._Stack(g, "g"), 2, 5, ops.NS_COEFFICIENTS, 1e-7)[1]
+    assert need > 0
+    for handle in (False, True):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = ops.wtconv_orthogonalize(g, stream=s.cuda_stream if handle else s)
+        for _ in range(50):
+            torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        s.synchronize()
+        assert torch.equal(want, got)

@@ -408,3 +408,22 @@ def test_refusals(ops):
     with pytest.raises(wtconv.WtconvError) as e:
         g(x, x, mean, rstd, 4, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert e.value.status == wtconv.WTCONV_ERR_WORKSPACE
+
+
+def test_allocations_belong_to_the_given_stream(ops):
+    # the stream is held up while the caller's stream reuses all memory that is free to it
+    x, dy, w, b = inputs((8, 64, 64, 64), BF16, seed=21)
+    y, mean, rstd = ops.wtconv_gn_act_fwd(x, 8, w, b, activation="silu")
+    want = ops.wtconv_gn_act_bwd(dy, x, mean, rstd, 8, w, b, activation="silu")
+    need = ops._gn_layout(x, dy, 8, 0.0, "silu").ws
+    assert need > 0
+    for handle in (False, True):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = ops.wtconv_gn_act_bwd(dy, x, mean, rstd, 8, w, b, activation="silu", stream=s.cuda_stream if handle else s)
+        for _ in range(50):
+            torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        s.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, got))

@@ -35,8 +35,6 @@ struct Vec {
   };
   __device__ __forceinline__ Vec() {}
   __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const raw*>(p); }
-  // nothing will read the line again, the L2 may drop it first
-  __device__ __forceinline__ void load_last(const T* p) { r = __ldcs(reinterpret_cast<const raw*>(p)); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<raw*>(p) = r; }
   __device__ __forceinline__ void widen(float (&v)[VEC]) const {
 #pragma unroll

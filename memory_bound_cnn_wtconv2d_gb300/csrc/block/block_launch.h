@@ -10,8 +10,8 @@ namespace wtb {
 
 // Streamed group norm backward: at most this many CTAs add up channel sums.
 constexpr int extra_ctas(int C) { return (C + 31) / 32 < 24 ? (C + 31) / 32 : 24; }
-// Group norm, streamed form: CTAs an SM (by registers), of which one wave is launched.
-constexpr int streamed_ctas(int op, int vec) { return op == WTCONV_OP_GN_FWD && vec < 8 ? 3 : 2; }
+// Group norm, streamed form: CTAs an SM, of which one wave is launched.
+constexpr int kStreamedCtas = 2;
 
 struct GnPlan {
   int vec;         // elements of one access (a divisor of C; 16 bytes where alignment allows)

@@ -87,7 +87,7 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
     p.tx = d.C / vec < kThreads ? d.C / vec : kThreads;
     p.ty = kThreads / p.tx;
     // one wave of CTAs, at least 8 rows a thread
-    const int slots = sms * streamed_ctas(op, vec) - (op == WTCONV_OP_GN_BWD ? extra_ctas(d.C) : 0);
+    const int slots = sms * kStreamedCtas - (op == WTCONV_OP_GN_BWD ? extra_ctas(d.C) : 0);
     long long want = slots / d.N;
     const long long most = (d.S + 8LL * p.ty - 1) / (8LL * p.ty);
     if (want > most) want = most;

@@ -12,6 +12,17 @@
 // every per-channel value stays in registers, whatever the group size: groups
 // of 3 channels are narrower than any vector.
 //
+// What bounds it, on one GB300.  Streamed, large: the second pass over x (and dy)
+// comes from memory again, so that 3 (5) transfers are made of the 2 (3) that
+// count: 16 x 224 x 224 x 64 float32 98 us forward, 6.3 TB/s of those three, of
+// 6.8 that a copy reaches; 32 x 128 x 128 x 96 bfloat16 backward 94 us, 5.3 TB/s of
+// the five.  Streamed, within the L2 (64 x 56 x 56 x 96 bfloat16 with GELU 30 us):
+// instructions, 14 an element to read and 22 to apply, and the start and the
+// sums of two launches.  Resident (128 x 14 x 14 x 384 float16 backward with GELU
+// 29 us): instructions, 49 an element, half of them the same however long the
+// columns.  One small image (1 x 7 x 7 x 768, 4 us): a chain of load, two
+// reductions and store.
+//
 // Statistics are kept as (count, mean, sum of squared deviations) and merged;
 // a thread's own come from sums around its first value, which loses no more
 // than its row count in units of 2^-24, however far the mean is from zero.
@@ -193,6 +204,9 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   }
 }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
 
 // A value of another CTA of the cluster.
 __device__ __forceinline__ float cluster_read(const float* p, int rank) {
@@ -514,19 +528,29 @@ bwd_reduce(int C, long long blocks, const float* part, float* dw, float* db) {
 
 // ---------------------------------------------------------------- streamed
 
-// CTAs an SM: 128 registers for the forward of eight channels a thread and the
-// backward, 80 otherwise; a wave of fewer CTAs, each with more rows, spends less
-// on its start and its sums.  Of four (64 registers, no more than four channels
-// a thread): 16 x 112 x 112 x 64 bf16 17.9 -> 15.7 us forward and 30.7 -> 25.8
-// backward, 4 x 128 x 128 x 96 15.4 -> 13.9 and 21.9 -> 17.1, 32 x 128 x 128 x 96
-// the same and 107 -> 101.
-template <int VEC> constexpr int kFwdCtas = streamed_ctas(WTCONV_OP_GN_FWD, VEC);
-constexpr int kBwdCtas = streamed_ctas(WTCONV_OP_GN_BWD, 1);
-
 struct Streamed {
   int tx, ty;        // threads across channel vectors, rows side by side
   int splits, rows;  // row ranges of a sample, one CTA each
   int extra;         // backward: the second launch's first CTAs, which add up the channel sums
+};
+
+// A thread's rows on their way through shared memory: kAhead batches of rows,
+// in slots that only this thread uses, 64 KB a CTA.  Loads are in flight while
+// earlier batches are worked on, and none of them holds a register (loaded into
+// registers in batches: 32 x 128 x 128 x 96 bf16 backward 95 -> 84 us, 64 x 56 x
+// 56 x 96 forward 26.5 -> 24, f32 backward 62 -> 56).  Two CTAs an SM: a wave of
+// fewer CTAs, each with more rows, spends less on its start and its sums, and
+// threads can hold eight channels (three of 80 registers: backward 84 -> 101; one:
+// 86, forward the same).
+constexpr int kAhead = 4, kFwdRows = 4, kBwdRows = 2;
+template <typename T, int VEC, int ROWS>
+struct Ring {
+  static constexpr int kBytes = VEC * (int)sizeof(T), kSize = kAhead * ROWS * kThreads * kBytes;
+  unsigned char* mine;
+  __device__ __forceinline__ Ring(void* smem) : mine((unsigned char*)smem + threadIdx.x * kBytes) {}
+  __device__ __forceinline__ T* at(int batch, int row) const {
+    return reinterpret_cast<T*>(mine + ((batch & (kAhead - 1)) * ROWS + row) * (kThreads * kBytes));
+  }
 };
 
 // Sums over a sample's ranges of f(range, j) for j < count, by all warps:
@@ -565,11 +589,14 @@ __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.w
 
 // part[n][split][G] = (mean, m2) over the split's rows
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads, kFwdCtas<VEC>)
+__global__ void __launch_bounds__(kThreads, kStreamedCtas)
 fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
          float2* __restrict__ part) {
-  constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];
+  constexpr int P = kPairs<VEC>, kRows = kFwdRows, kChunk = 32;  // rows of a batch, and around one pivot
+  using Slots = Ring<T, VEC, kRows>;
+  extern __shared__ __align__(16) float smem[];
+  float* sm = smem + Slots::kSize / 4;
+  const Slots ring(smem);
   const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
   const long long n = blockIdx.x / p.splits;
   const int W = p.tx * VEC;
@@ -587,36 +614,54 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
       float2 mean[P], m2[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) mean[i] = m2[i] = make_float2(0.f, 0.f);
-      if (c < a.C) {
-        const T* px = base + ty * a.xr + c;
-        const long long step = p.ty * a.xr;
-        for (int r = ty; r < rows; r += kBatch * p.ty, px += kBatch * step) {
-          // a batch around its first row, merged into the running statistics
-          const int k = min(kBatch, (rows - r + p.ty - 1) / p.ty);
-          Vec<T, VEC> v[kBatch];
-          float2 f[P], mb[P], qb[P];
+      const int mine = c < a.C && rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0, batches = (mine + kRows - 1) / kRows;
+      const T* px = base + ty * a.xr + c;
+      const long long step = p.ty * a.xr;
+      int asked = 0;
+      const auto ask = [&] {
+        const int m = mine - asked * kRows;
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (i < k) v[i].load(px + i * step);
-          Running<VEC> run;
-          widen_pairs<T, VEC>(v[0], f);
-          run.begin(f);
+        for (int i = 0; i < kRows; ++i)
+          if (i < m) {
+            copy_async<Slots::kBytes>(ring.at(asked, i), px);
+            px += step;
+          }
+        ++asked;
+        copy_commit();
+      };
 #pragma unroll
-          for (int i = 1; i < kBatch; ++i)
-            if (i < k) {
-              widen_pairs<T, VEC>(v[i], f);
+      for (int i = 0; i < kAhead - 1; ++i) ask();
+      for (int j = 0; j < batches;) {
+        // up to kChunk rows around their first, merged into the running statistics
+        Running<VEC> run;
+        float2 f[P], mb[P], qb[P];
+        int k = 0;
+        do {
+          copy_wait_but<kAhead - 2>();
+          ask();
+          const int m = min(kRows, mine - j * kRows);
+          if (k == 0) {
+            load_pairs<T, VEC>(ring.at(j, 0), f);
+            run.begin(f);
+          }
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (i < m) {
+              load_pairs<T, VEC>(ring.at(j, i), f);
               run.add(f);
             }
-          run.end(k, mb, qb);
-          const float tot = cnt + (float)k, fr = (float)k / tot;
+          k += m;
+          ++j;
+        } while (j < batches && k < kChunk);
+        run.end(k, mb, qb);
+        const float tot = cnt + (float)k, fr = (float)k / tot;
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float2 d = add2(mb[i], make_float2(-mean[i].x, -mean[i].y));
-            mean[i] = fma2(d, splat(fr), mean[i]);
-            m2[i] = add2(m2[i], fma2(mul2(d, splat(cnt * fr)), d, qb[i]));
-          }
-          cnt = tot;
+        for (int i = 0; i < P; ++i) {
+          const float2 d = add2(mb[i], make_float2(-mean[i].x, -mean[i].y));
+          mean[i] = fma2(d, splat(fr), mean[i]);
+          m2[i] = add2(m2[i], fma2(mul2(d, splat(cnt * fr)), d, qb[i]));
         }
+        cnt = tot;
       }
       put_statistics<VEC>(st, p.ty, whole ? p.tx : W, whole, ty, tx, (int)cnt, mean, m2);
     }
@@ -645,14 +690,39 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, kFwdCtas<VEC>)
+__global__ void __launch_bounds__(kThreads, kStreamedCtas)
 fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ x,
           const float* __restrict__ w, const float* __restrict__ b, const float2* part, T* __restrict__ y,
           float* __restrict__ mean_out, float* __restrict__ rstd_out) {
-  constexpr int P = kPairs<VEC>, kBatch = 8;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];  // [2][G], kThreads
+  constexpr int P = kPairs<VEC>, kRows = kFwdRows;  // rows of a batch
+  using Slots = Ring<T, VEC, kRows>;
+  extern __shared__ __align__(16) float smem[];
+  float* sm = smem + Slots::kSize / 4;  // [2][G], kThreads
+  const Slots ring(smem);
   const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
   const long long n = blockIdx.x / p.splits;
+  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
+  const int rows = (int)(r1 - r0), mine = ty < p.ty && rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0;
+  const int batches = (mine + kRows - 1) / kRows, first = (batches - 1) * kRows;
+  const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
+  const T* px;
+  int asked;
+  const auto ask = [&] {  // the last rows first
+    const int m = asked >= batches ? 0 : asked ? kRows : mine - first;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i < m) copy_async<Slots::kBytes>(ring.at(asked, i), px + i * xstep);
+    px -= kRows * xstep;
+    ++asked;
+    copy_commit();
+  };
+  const auto begin = [&](int c) {
+    px = x + n * a.xs + (r0 + ty + (long long)first * p.ty) * a.xr + c;
+    asked = 0;
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) ask();
+  };
+  begin(tx * VEC);  // x is not the previous launch's
   wait_previous();
   {
     const float last = (float)(a.S - (long long)(p.splits - 1) * p.rows);  // rows of the last range
@@ -677,32 +747,26 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
           }
         });
   }
-  if (ty >= p.ty) return;
-  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
-  const int rows = (int)(r1 - r0);
-  for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
+  for (int c = tx * VEC; c < a.C && mine; c += p.tx * VEC) {
     float2 mu[P], sc[P], sh[P];
     int g[VEC];
     groups_of<VEC>(c, a.Cg, g);
     per_channel<VEC>(mu, [&](int e) { return -sm[g[e]]; });
     per_channel<VEC>(sc, [&](int e) { return sm[a.G + g[e]] * (w ? w[c + e] : 1.f); });
     per_channel<VEC>(sh, [&](int e) { return b ? b[c + e] : 0.f; });
-    const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
-    const int left = rows - ty, first = left > 0 ? (left - 1) / (kBatch * p.ty) * (kBatch * p.ty) : -1;
-    const T* px = x + n * a.xs + (r0 + ty + first) * a.xr + c;
-    T* py = y + (n * a.S + r0 + ty + first) * a.C + c;
-    for (int r = first; r >= 0; r -= kBatch * p.ty, px -= kBatch * xstep, py -= kBatch * ystep) {
-      Vec<T, VEC> v[kBatch];
+    if (c != tx * VEC) begin(c);
+    T* py = y + (n * a.S + r0 + ty + (long long)first * p.ty) * a.C + c;
+    for (int j = 0; j < batches; ++j, py -= kRows * ystep) {
+      copy_wait_but<kAhead - 2>();
+      ask();
+      const int m = j ? kRows : mine - first;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (r + i * p.ty < left) v[i].load_last(px + i * xstep);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (r + i * p.ty < left) {
+      for (int i = 0; i < kRows; ++i)
+        if (i < m) {
           float2 f[P];
-          widen_pairs<T, VEC>(v[i], f);
+          load_pairs<T, VEC>(ring.at(j, i), f);
 #pragma unroll
-          for (int j = 0; j < P; ++j) f[j] = act2<ACT>(fma2(add2(f[j], mu[j]), sc[j], sh[j]));
+          for (int q = 0; q < P; ++q) f[q] = act2<ACT>(fma2(add2(f[q], mu[q]), sc[q], sh[q]));
           store_pairs<T, VEC, true>(py + i * ystep, f);
         }
     }
@@ -712,13 +776,16 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
 // part[n][split][2][C]: sums of dz and of dz * xhat over the split's rows;
 // gpart[n][split][2][G]: the groups' weighted sums.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, kBwdCtas)
+__global__ void __launch_bounds__(kThreads, kStreamedCtas)
 bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
          const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
          const float* __restrict__ w, const float* __restrict__ b, float* __restrict__ part,
          float* __restrict__ gpart) {
-  constexpr int P = kPairs<VEC>, kBatch = VEC == 8 ? 4 : 8;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];
+  constexpr int P = kPairs<VEC>, kRows = kBwdRows;  // rows of a batch
+  using Slots = Ring<T, VEC, kRows>;
+  extern __shared__ __align__(16) float smem[];
+  float* sm = smem + 2 * Slots::kSize / 4;
+  const Slots ring_x(smem), ring_d((unsigned char*)smem + Slots::kSize);
   const int split = blockIdx.x % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx, lane = tid & 31;
   const long long n = blockIdx.x / p.splits;
   const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
@@ -744,21 +811,33 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
         const T* px = x + n * a.xs + (r0 + ty) * a.xr + c;
         const T* py = dy + n * a.ds + (r0 + ty) * a.dr + c;
         const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr;
-        const int left = rows - ty;
-        for (int r = 0; r < left; r += kBatch * p.ty, px += kBatch * xstep, py += kBatch * dstep) {
-          Vec<T, VEC> vx[kBatch], vd[kBatch];
+        const int mine_rows = rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0, batches = (mine_rows + kRows - 1) / kRows;
+        int asked = 0;
+        const auto ask = [&] {
+          const int m = mine_rows - asked * kRows;
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (r + i * p.ty < left) {
-              vx[i].load(px + i * xstep);
-              vd[i].load(py + i * dstep);
+          for (int i = 0; i < kRows; ++i)
+            if (i < m) {
+              copy_async<Slots::kBytes>(ring_x.at(asked, i), px);
+              copy_async<Slots::kBytes>(ring_d.at(asked, i), py);
+              px += xstep;
+              py += dstep;
             }
+          ++asked;
+          copy_commit();
+        };
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (r + i * p.ty < left) {
+        for (int i = 0; i < kAhead - 1; ++i) ask();
+        for (int q = 0; q < batches; ++q) {
+          copy_wait_but<kAhead - 2>();
+          ask();
+          const int m = mine_rows - q * kRows;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (i < m) {
               float2 f[P], d[P];
-              widen_pairs<T, VEC>(vx[i], f);
-              widen_pairs<T, VEC>(vd[i], d);
+              load_pairs<T, VEC>(ring_x.at(q, i), f);
+              load_pairs<T, VEC>(ring_d.at(q, i), d);
 #pragma unroll
               for (int j = 0; j < P; ++j) {
                 const float2 xm = add2(f[j], mu[j]);
@@ -797,13 +876,16 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, kBwdCtas)
+__global__ void __launch_bounds__(kThreads, kStreamedCtas)
 bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, const T* __restrict__ dy,
           const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
           const float* __restrict__ w, const float* __restrict__ b, const float* part, const float* gpart,
           T* __restrict__ dx, float* __restrict__ dw, float* __restrict__ db) {
-  constexpr int P = kPairs<VEC>, kBatch = VEC == 8 ? 4 : 8;  // rows loaded together
-  extern __shared__ __align__(16) float sm[];  // [2][G], kThreads; or 2 kThreads
+  constexpr int P = kPairs<VEC>, kRows = kBwdRows;  // rows of a batch
+  using Slots = Ring<T, VEC, kRows>;
+  extern __shared__ __align__(16) float smem[];
+  float* sm = smem + 2 * Slots::kSize / 4;  // [2][G], kThreads; or 2 kThreads
+  const Slots ring_x(smem), ring_d((unsigned char*)smem + Slots::kSize);
   if ((int)blockIdx.x < p.extra) {
     wait_previous();
     add_channels(a.C, a.N * p.splits, part, dw, db, sm, p.extra);
@@ -811,6 +893,34 @@ bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
   }
   const int at = blockIdx.x - p.extra, split = at % p.splits, tid = threadIdx.x, tx = tid % p.tx, ty = tid / p.tx;
   const long long n = at / p.splits;
+  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
+  const int rows = (int)(r1 - r0), mine = ty < p.ty && rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0;
+  const int batches = (mine + kRows - 1) / kRows, first = (batches - 1) * kRows;
+  const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
+  const long long row = r0 + ty + (long long)first * p.ty;
+  const T *px, *py;
+  int asked;
+  const auto ask = [&] {  // the last rows first
+    const int m = asked >= batches ? 0 : asked ? kRows : mine - first;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i < m) {
+        copy_async<Slots::kBytes>(ring_x.at(asked, i), px + i * xstep);
+        copy_async<Slots::kBytes>(ring_d.at(asked, i), py + i * dstep);
+      }
+    px -= kRows * xstep;
+    py -= kRows * dstep;
+    ++asked;
+    copy_commit();
+  };
+  const auto begin = [&](int c) {
+    px = x + n * a.xs + row * a.xr + c;
+    py = dy + n * a.ds + row * a.dr + c;
+    asked = 0;
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) ask();
+  };
+  begin(tx * VEC);  // x and dy are not the previous launch's
   wait_previous();
   {
     const float inv = 1.f / ((float)a.S * (float)a.Cg);
@@ -818,10 +928,7 @@ bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
     range_sums(p.splits, 2 * a.G, sm + 2 * a.G, [&](int s, int j) { return q[(long long)s * 2 * a.G + j]; },
                [&](int j, float t) { sm[j] = t * inv; });
   }
-  if (ty >= p.ty) return;
-  const long long r0 = (long long)split * p.rows, r1 = min(r0 + p.rows, a.S);
-  const int rows = (int)(r1 - r0);
-  for (int c = tx * VEC; c < a.C; c += p.tx * VEC) {
+  for (int c = tx * VEC; c < a.C && mine; c += p.tx * VEC) {
     // dx = rstd (w dz - s1 - xhat s2)
     float2 mu[P], sc[P], bb[P], k0[P], k1[P];
     int g[VEC];
@@ -834,30 +941,23 @@ bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
       const float r = rstd[n * a.G + g[e]];
       return -r * r * sm[a.G + g[e]];
     });
-    const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
-    const int left = rows - ty, first = left > 0 ? (left - 1) / (kBatch * p.ty) * (kBatch * p.ty) : -1;
-    const T* px = x + n * a.xs + (r0 + ty + first) * a.xr + c;
-    const T* py = dy + n * a.ds + (r0 + ty + first) * a.dr + c;
-    T* po = dx + (n * a.S + r0 + ty + first) * a.C + c;
-    for (int r = first; r >= 0; r -= kBatch * p.ty, px -= kBatch * xstep, py -= kBatch * dstep, po -= kBatch * ostep) {
-      Vec<T, VEC> vx[kBatch], vd[kBatch];
+    if (c != tx * VEC) begin(c);
+    T* po = dx + (n * a.S + row) * a.C + c;
+    for (int j = 0; j < batches; ++j, po -= kRows * ostep) {
+      copy_wait_but<kAhead - 2>();
+      ask();
+      const int m = j ? kRows : mine - first;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (r + i * p.ty < left) {
-          vx[i].load_last(px + i * xstep);
-          vd[i].load_last(py + i * dstep);
-        }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (r + i * p.ty < left) {
+      for (int i = 0; i < kRows; ++i)
+        if (i < m) {
           float2 f[P], d[P];
-          widen_pairs<T, VEC>(vx[i], f);
-          widen_pairs<T, VEC>(vd[i], d);
+          load_pairs<T, VEC>(ring_x.at(j, i), f);
+          load_pairs<T, VEC>(ring_d.at(j, i), d);
 #pragma unroll
-          for (int j = 0; j < P; ++j) {
-            const float2 xm = add2(f[j], mu[j]);
-            const float2 z = through2<ACT>(d[j], fma2(xm, sc[j], bb[j]));
-            f[j] = fma2(sc[j], z, fma2(xm, k1[j], k0[j]));
+          for (int q = 0; q < P; ++q) {
+            const float2 xm = add2(f[q], mu[q]);
+            const float2 z = through2<ACT>(d[q], fma2(xm, sc[q], bb[q]));
+            f[q] = fma2(sc[q], z, fma2(xm, k1[q], k0[q]));
           }
           store_pairs<T, VEC, true>(po + i * ostep, f);
         }
@@ -929,13 +1029,15 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
   float2* part = (float2*)ws;
   const Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
   const unsigned grid = (unsigned)(d.N * p.splits);
-  const int smem = 4 * (2 * d.C + 2 * p.ty * p.tx * VEC);
+  constexpr int ring = Ring<T, VEC, kFwdRows>::kSize;
+  const int smem = ring + 4 * (2 * d.C + 2 * p.ty * p.tx * VEC), smem_apply = ring + 4 * (2 * d.G + kThreads);
   cudaError_t e = wt::ensure_smem((const void*)fwd_read<T, VEC>, smem);
+  if (e == cudaSuccess) e = wt::ensure_smem((const void*)fwd_apply<T, VEC, ACT>, smem_apply);
   if (e != cudaSuccess) return e;
   fwd_read<T, VEC><<<grid, kThreads, smem, s>>>(a, q, (const T*)x, part);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_next(fwd_apply<T, VEC, ACT>, dim3(grid), kThreads, 4 * (2 * d.G + kThreads), s, a, q, (const T*)x, w, b,
+  return launch_next(fwd_apply<T, VEC, ACT>, dim3(grid), kThreads, smem_apply, s, a, q, (const T*)x, w, b,
                      (const float2*)part, (T*)y, mean, rstd);
 }
 
@@ -961,14 +1063,15 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
   Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
   if (dw || db) q.extra = extra_ctas(d.C);
   const unsigned grid = (unsigned)(d.N * p.splits);
-  int smem = 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC);
+  constexpr int ring = 2 * Ring<T, VEC, kBwdRows>::kSize;
+  const int smem = ring + 4 * (2 * d.C + kThreads + 2 * p.ty * p.tx * VEC), smem_apply = ring + 4 * (2 * d.G + 2 * kThreads);
   cudaError_t e = wt::ensure_smem((const void*)bwd_read<T, VEC, ACT>, smem);
+  if (e == cudaSuccess) e = wt::ensure_smem((const void*)bwd_apply<T, VEC, ACT>, smem_apply);
   if (e != cudaSuccess) return e;
   bwd_read<T, VEC, ACT><<<grid, kThreads, smem, s>>>(a, q, (const T*)dy, (const T*)x, mean, rstd, w, b, part, gpart);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  smem = 4 * (2 * d.G + 2 * kThreads);
-  return launch_next(bwd_apply<T, VEC, ACT>, dim3(grid + q.extra), kThreads, smem, s, a, q, (const T*)dy, (const T*)x,
+  return launch_next(bwd_apply<T, VEC, ACT>, dim3(grid + q.extra), kThreads, smem_apply, s, a, q, (const T*)dy, (const T*)x,
                      mean, rstd, w, b, (const float*)part, (const float*)gpart, (T*)dx, dw, db);
 }
 

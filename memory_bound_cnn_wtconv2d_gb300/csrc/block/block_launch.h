@@ -20,6 +20,7 @@ struct GnPlan {
   int cluster;     // resident form: CTAs of a cluster (0: streamed)
   int ch;          // resident form: channels of a CTA
   int splits;      // streamed form: row ranges of one sample, one CTA each
+  int keep;        // streamed form: first row of a range that the L2 is to hold for the second launch
   size_t ws_bytes;
 };
 

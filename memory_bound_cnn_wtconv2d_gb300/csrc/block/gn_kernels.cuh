@@ -13,12 +13,13 @@
 // of 3 channels are narrower than any vector.
 //
 // What bounds it, on one GB300.  Streamed, large: the second pass over x (and dy)
-// comes from memory again, so that 3 (5) transfers are made of the 2 (3) that
-// count: 16 x 224 x 224 x 64 float32 98 us forward, 6.3 TB/s of those three, of
-// 6.8 that a copy reaches; 32 x 128 x 128 x 96 bfloat16 backward 94 us, 5.3 TB/s of
-// the five.  Streamed, within the L2 (64 x 56 x 56 x 96 bfloat16 with GELU 30 us):
-// instructions, 14 an element to read and 22 to apply, and the start and the
-// sums of two launches.  Resident (128 x 14 x 14 x 384 float16 backward with GELU
+// comes from memory again but for what the L2 could hold, so that nearly 3 (5)
+// transfers are made of the 2 (3) that count: 16 x 224 x 224 x 64 float32 93 us
+// forward, 5.7 TB/s of the 535 MB left, of 6.8 that a copy reaches; 32 x 128 x 128 x
+// 96 bfloat16 backward 78 us, 5.4 TB/s of 423 MB.  Streamed, within the L2 (64 x 56 x
+// 56 x 96 bfloat16 with GELU 29 us): latency of two launches, each its start, the
+// sums over ranges and columns of 37 rows a thread, and one wave of 256 CTAs in
+// 304 places.  Resident (128 x 14 x 14 x 384 float16 backward with GELU
 // 29 us): instructions, 49 an element, half of them the same however long the
 // columns.  One small image (1 x 7 x 7 x 768, 4 us): a chain of load, two
 // reductions and store.
@@ -202,6 +203,29 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   } else {
     *reinterpret_cast<unsigned short*>(dst) = *reinterpret_cast<const unsigned short*>(src);
   }
+}
+// The same with a word to the L2 on how long to keep the lines.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, uint64_t policy) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "l"(policy) : "memory");
+  } else if constexpr (BYTES >= 4) {
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "l"(policy)
+                 : "memory");
+  } else {
+    copy_async<BYTES>(dst, src);
+  }
+}
+__device__ __forceinline__ uint64_t drop_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t drop_usual() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_unchanged.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -531,6 +555,7 @@ bwd_reduce(int C, long long blocks, const float* part, float* dw, float* db) {
 struct Streamed {
   int tx, ty;        // threads across channel vectors, rows side by side
   int splits, rows;  // row ranges of a sample, one CTA each
+  int keep;          // first row of a range that the L2 is to hold for the second launch
   int extra;         // backward: the second launch's first CTAs, which add up the channel sums
 };
 
@@ -618,12 +643,14 @@ fwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
       const T* px = base + ty * a.xr + c;
       const long long step = p.ty * a.xr;
       int asked = 0;
+      const uint64_t soon = drop_first(), late = drop_usual();
       const auto ask = [&] {
         const int m = mine - asked * kRows;
+        const uint64_t policy = asked * kRows * p.ty >= p.keep ? late : soon;
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
           if (i < m) {
-            copy_async<Slots::kBytes>(ring.at(asked, i), px);
+            copy_async<Slots::kBytes>(ring.at(asked, i), px, policy);
             px += step;
           }
         ++asked;
@@ -705,13 +732,14 @@ fwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
   const int rows = (int)(r1 - r0), mine = ty < p.ty && rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0;
   const int batches = (mine + kRows - 1) / kRows, first = (batches - 1) * kRows;
   const long long xstep = p.ty * a.xr, ystep = (long long)p.ty * a.C;
-  const T* px;
+  const T* px = x;
   int asked;
+  const uint64_t soon = drop_first();
   const auto ask = [&] {  // the last rows first
     const int m = asked >= batches ? 0 : asked ? kRows : mine - first;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (i < m) copy_async<Slots::kBytes>(ring.at(asked, i), px + i * xstep);
+      if (i < m) copy_async<Slots::kBytes>(ring.at(asked, i), px + i * xstep, soon);
     px -= kRows * xstep;
     ++asked;
     copy_commit();
@@ -813,13 +841,15 @@ bwd_read(const __grid_constant__ Args a, const __grid_constant__ Streamed p, con
         const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr;
         const int mine_rows = rows > ty ? (rows - ty + p.ty - 1) / p.ty : 0, batches = (mine_rows + kRows - 1) / kRows;
         int asked = 0;
+        const uint64_t soon = drop_first(), late = drop_usual();
         const auto ask = [&] {
           const int m = mine_rows - asked * kRows;
+          const uint64_t policy = asked * kRows * p.ty >= p.keep ? late : soon;
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
             if (i < m) {
-              copy_async<Slots::kBytes>(ring_x.at(asked, i), px);
-              copy_async<Slots::kBytes>(ring_d.at(asked, i), py);
+              copy_async<Slots::kBytes>(ring_x.at(asked, i), px, policy);
+              copy_async<Slots::kBytes>(ring_d.at(asked, i), py, policy);
               px += xstep;
               py += dstep;
             }
@@ -898,15 +928,16 @@ bwd_apply(const __grid_constant__ Args a, const __grid_constant__ Streamed p, co
   const int batches = (mine + kRows - 1) / kRows, first = (batches - 1) * kRows;
   const long long xstep = p.ty * a.xr, dstep = p.ty * a.dr, ostep = (long long)p.ty * a.C;
   const long long row = r0 + ty + (long long)first * p.ty;
-  const T *px, *py;
+  const T *px = x, *py = dy;
   int asked;
+  const uint64_t soon = drop_first();
   const auto ask = [&] {  // the last rows first
     const int m = asked >= batches ? 0 : asked ? kRows : mine - first;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
       if (i < m) {
-        copy_async<Slots::kBytes>(ring_x.at(asked, i), px + i * xstep);
-        copy_async<Slots::kBytes>(ring_d.at(asked, i), py + i * dstep);
+        copy_async<Slots::kBytes>(ring_x.at(asked, i), px + i * xstep, soon);
+        copy_async<Slots::kBytes>(ring_d.at(asked, i), py + i * dstep, soon);
       }
     px -= kRows * xstep;
     py -= kRows * dstep;
@@ -1027,7 +1058,7 @@ cudaError_t fwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* x, const
                           (T*)y, mean, rstd);
   }
   float2* part = (float2*)ws;
-  const Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+  const Streamed q = {p.tx, p.ty, p.splits, p.rows, p.keep, 0};
   const unsigned grid = (unsigned)(d.N * p.splits);
   constexpr int ring = Ring<T, VEC, kFwdRows>::kSize;
   const int smem = ring + 4 * (2 * d.C + 2 * p.ty * p.tx * VEC), smem_apply = ring + 4 * (2 * d.G + kThreads);
@@ -1060,7 +1091,7 @@ cudaError_t bwd(const wtconv_gn_desc_t& d, const GnPlan& p, const void* dy, cons
   }
   float* part = (float*)ws;
   float* gpart = part + (size_t)d.N * p.splits * 2 * d.C;
-  Streamed q = {p.tx, p.ty, p.splits, p.rows, 0};
+  Streamed q = {p.tx, p.ty, p.splits, p.rows, p.keep, 0};
   if (dw || db) q.extra = extra_ctas(d.C);
   const unsigned grid = (unsigned)(d.N * p.splits);
   constexpr int ring = 2 * Ring<T, VEC, kBwdRows>::kSize;

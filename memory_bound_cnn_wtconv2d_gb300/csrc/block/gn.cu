@@ -44,11 +44,13 @@ void plan_resident(const wtconv_gn_desc_t& d, int op, int vec, int sms, GnPlan& 
       long long occ = kSmemSm / smem;
       const int most = op == WTCONV_OP_GN_FWD ? 4 : 3;  // by registers
       if (occ > most) occ = most;
+      // Not all places can be filled by clusters (16 x 28 x 28 x 192 bf16
+      // backward 18.7 -> 14.4 us since a fifth is counted off).
       // Microseconds: rounds of resident CTAs, each its latency (a cluster's
       // exchange more) and the passes of its threads over the rows.  A CTA
       // alone on its SM is bound by latency; from about three on, passes share
       // the SM's issue rate.
-      const double ctas = (double)d.N * (d.C / ch) * cl, slots = (double)sms * occ;
+      const double ctas = (double)d.N * (d.C / ch) * cl, slots = (double)sms * occ * (cl > 1 ? 0.8 : 1.0);
       const double beside = ctas >= slots ? (double)occ : ctas > sms ? ctas / sms : 1.0;
       const double passes = (double)((rows + ty - 1) / ty) * 256 / (tx * ty);
       const double line = ch * es % 32 ? 1.25 : ch * es < 64 ? 1.1 : 1.0;
@@ -77,12 +79,14 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
   const size_t n = (size_t)d.N;
   if (p.cluster) {
     // Narrow lines cost the more the larger the tensor: resident CTAs of lines
-    // below 64 bytes take 25.8 us where the streamed form takes 18.7 (64 x 28 x 28
-    // x 192 f32, forward) and 32 where it takes 20 (64 x 32 x 32 x 128 bf16,
-    // backward); at 16 MB 11.6 and 13.3.  Clusters only while latency counts.
+    // below 64 bytes take 25.8 us where the streamed form takes 18.2 (64 x 28 x 28
+    // x 192 f32, forward) and 32 where it takes 19 (64 x 32 x 32 x 128 bf16,
+    // backward); at 16 MB 11.8 and 13.2.  A resident backward pays for its start
+    // and its sums with every 37 KB (256 x 14 x 14 x 384 bf16, 77 MB: 52 and 38; at
+    // 38 MB f16 with GELU 29.5 and 30.3).  Clusters only while latency counts.
     const int es = d.dtype == WTCONV_F32 ? 4 : 2, line = p.ch * es;
     const long long read = (d.N * d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2)) >> 20;
-    if (p.cluster == 1 ? line < 64 && read > 20 : !((line >= 48 && read <= 12) || (line >= 64 && read <= 24)))
+    if (p.cluster == 1 ? read > (line < 64 ? 20 : op == WTCONV_OP_GN_BWD ? 48 : 1 << 20) : !((line >= 48 && read <= 12) || (line >= 64 && read <= 24)))
       p.cluster = 0;
   }
   if (p.cluster) {

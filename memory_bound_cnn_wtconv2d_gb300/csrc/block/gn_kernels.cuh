@@ -13,10 +13,10 @@
 // of 3 channels are narrower than any vector.
 //
 // What bounds it, on one GB300.  Streamed, large: the second pass over x (and dy)
-// comes from memory again but for what the L2 could hold, so that nearly 3 (5)
-// transfers are made of the 2 (3) that count: 16 x 224 x 224 x 64 float32 93 us
-// forward, 5.7 TB/s of the 535 MB left, of 6.8 that a copy reaches; 32 x 128 x 128 x
-// 96 bfloat16 backward 78 us, 5.4 TB/s of 423 MB.  Streamed, within the L2 (64 x 56 x
+// comes from memory again but for what the L2 could hold: 16 x 224 x 224 x 64
+// float32 forward 93 us, 524 MB of DRAM traffic for the 411 that count, at 5.6 TB/s
+// (a copy reaches 6.8); 32 x 128 x 128 x 96 bfloat16 backward 78 us, 414 MB for 302,
+// at 5.3 TB/s.  Streamed, within the L2 (64 x 56 x
 // 56 x 96 bfloat16 with GELU 29 us): latency of two launches, each its start, the
 // sums over ranges and columns of 37 rows a thread, and one wave of 256 CTAs in
 // 304 places.  Resident (128 x 14 x 14 x 384 float16 backward with GELU

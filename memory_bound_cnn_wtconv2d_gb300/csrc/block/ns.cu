@@ -24,7 +24,10 @@
 // the products lo hi + hi lo + hi hi (`split`).  The tensor core's additions
 // truncate, some 2^-22 of the sum each; `split` spreads the sum over kSegments
 // accumulators (one for the small products), which the epilogue adds, to keep
-// that below 1e-5.
+// that below 1e-5.  It shows on the diagonal of A, whose sums only grow; long
+// ones of an orthogonalised stack are spread over kDeepSegments (275 x 3176
+// float32: error 4.5e-6 -> 1.7e-6, that of float32 sums 2.0e-6; 223 -> 225 us, 4 x
+// 2048 x 1024 540 -> 594; of 19 steps 1.4e-6 and 2.2e-6 without).
 //
 // Layout.  Every matrix lies in the workspace as 64 x 64 sub-blocks whose 8 KB
 // are the 128-byte-swizzled image that the tensor core reads, so that an
@@ -73,6 +76,8 @@ constexpr int kRing = 20, kRingWide = 24;
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
 constexpr int kSegments = 4;       // accumulators of one tile when split
+constexpr int kDeepSegments = 8;   // of the first product, 64 columns wide, over more than kDeepSteps K steps
+constexpr int kDeepSteps = 24;
 constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
 constexpr int kSmem = kRingWide * kSub + kEpiBytes + 1024;
@@ -85,6 +90,7 @@ struct NsMain {
   NsShape s;
   int rb, cb, rk;            // sub-blocks: rows (even), columns, rows that hold data
   NsPoly p;
+  int deep;                  // the first product in more accumulators
   int nb1, nb2, nb3, gsh;    // tile widths of the three products; log2 of the stored diagonal block
   int t1, t2, t3;            // tiles of one matrix in each product
   unsigned char *xh[2], *xl[2], *ah, *al, *bh, *bl;
@@ -346,11 +352,12 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     for (int phase = 0; ok && phase < 3; ++phase) {
       const int tiles = a.s.count * (phase == 0 ? a.t1 : phase == 1 ? a.t2 : a.t3);
       const int nk = phase == 0 ? a.cb : a.rk;
-      // accumulators: two sets of up to 256 columns, or one of 4 x 128
+      // accumulators: two sets of up to 256 columns, or one of 4 x 128 or 8 x 64
       const int nbw = phase == 0 ? a.nb1 : phase == 1 ? a.nb2 : a.nb3;
       // of which, split, the first takes the products with a lo and the others share the sum of hi hi
-      const int segs = a.p.split ? 1 + min(kSegments - 1, nk) : 1;
-      const uint32_t seg_cols = nbw * 64, sets = a.p.split && nbw == 2 ? 1 : 2;
+      const bool deep = phase == 0 && a.deep;
+      const int segs = a.p.split ? 1 + min((deep ? kDeepSegments : kSegments) - 1, nk) : 1;
+      const uint32_t seg_cols = nbw * 64, sets = a.p.split && (nbw == 2 || deep) ? 1 : 2;
       uint32_t acc = 0;
       const int lo_at = (2 + nbw) * kSub, stage_bytes = planes * lo_at, ebufs = nbw == (a.p.split ? kSplitNb : kMaxNb) && nk >= (a.p.split ? 16 : 32) ? 1 : 2;
       const int stages = min(kStages, (ebufs == 1 ? kRingWide : kRing) / (planes * (2 + nbw)));
@@ -530,6 +537,18 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                   if (g < segs)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] += w[g][i];
+                if (deep) {
+                  static_assert(kDeepSegments == 2 * kSegments && kDeepSteps >= kDeepSegments, "a second round, all in use");
+#pragma unroll
+                  for (int g = 0; g < kSegments; ++g) tmem_load8(from + q * 8 + (kSegments + g) * seg_cols, w[g]);
+                  tmem_wait_load();
+#pragma unroll
+                  for (int g = 0; g < kSegments; ++g) {
+                    tmem_loaded(w[g]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += w[g][i];
+                  }
+                }
               }
               if (in) {
                 unpack8(*reinterpret_cast<uint4*>(p), u);
@@ -702,6 +721,7 @@ NsMain plan(const wtconv_ns_desc_t& d, bool muon) {
   a.rk = (s.r + 63) / 64;
   a.rb = (a.rk + 1) & ~1;
   a.cb = (s.c + 63) / 64;
+  a.deep = a.p.split && !muon && a.cb > kDeepSteps;
   a.xbytes = (long long)a.rb * a.cb * kSub;
   a.abytes = (long long)a.rb * a.rb * kSub;
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
@@ -712,7 +732,7 @@ NsMain plan(const wtconv_ns_desc_t& d, bool muon) {
     double cost = 0;
     for (int ph = 0; ph < 2; ++ph) {
       double b = -1;
-      for (int nb = 1; nb <= (1 << gsh) && nb <= most; nb *= 2) {
+      for (int nb = 1; nb <= (1 << gsh) && nb <= (ph == 0 && a.deep ? 1 : most); nb *= 2) {
         const double c = tile_cost((long long)d.count * sym_tiles(a.rb, nb, gsh), sms, nb, ph ? a.rk : a.cb, planes);
         if (b < 0 || c < b) b = c, pick[ph] = nb;
       }

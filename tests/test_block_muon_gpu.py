@@ -323,3 +323,10 @@ def test_workspace_belongs_to_the_given_stream(ops):
             torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
         s.synchronize()
         assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("m,n", [(275, 3176), (3176, 275), (300, 9000), (520, 1601)])
+def test_long_rows(ops, m, n):
+    # the diagonal of X X^T is a sum of n squares, of which every addition loses a little
+    g = matrices(m, n, seed=m + n)
+    assert rel(ops.wtconv_orthogonalize(g), ns64(g)) <= TOL[F32]

@@ -237,8 +237,16 @@ __device__ __forceinline__ float cluster_read(const float* p, int rank) {
   namespace cg = cooperative_groups;
   return *cg::this_cluster().map_shared_rank(p, rank);
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The aligned forms are for converged warps; their callers' warps may have
+// parted (threads across that do not divide 32, lanes without a row).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Shared memory of the resident forms, in bytes: the forward's data, then
 // [2][ty][ch] floats and [4][groups]; the backward's x, then dz in float32

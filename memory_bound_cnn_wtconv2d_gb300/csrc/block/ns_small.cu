@@ -39,6 +39,7 @@ __device__ __forceinline__ int image_at(int row, int chunk) {
 }
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {

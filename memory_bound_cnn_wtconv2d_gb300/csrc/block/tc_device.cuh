@@ -1,5 +1,7 @@
 // Thin wrappers of the sm_103a instructions that the matrix kernels use:
-// mbarriers, bulk copies, tcgen05.
+// mbarriers, bulk copies, tcgen05.  Those with an aligned instruction bring the
+// warp together first: lanes may have parted before (a lane that leads, one
+// that sees its wait end later).
 #pragma once
 
 #include <stdint.h>
@@ -56,6 +58,7 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;
 
 template <int THREADS>
 __device__ __forceinline__ void named_sync(int id) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
 
@@ -70,10 +73,12 @@ __device__ __forceinline__ bool named_or(int id, bool p) {
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(columns) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -97,11 +102,15 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 
 // 8 consecutive columns of this warp's 32 lanes; valid after tmem_wait_load().
 __device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
+  __syncwarp();
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_load() {
+  __syncwarp();
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 
 // Keeps uses of v behind the wait.
 __device__ __forceinline__ void tmem_loaded(float (&v)[8]) {

@@ -351,10 +351,13 @@ class _Stack:
         e = self.tensors[0].element_size()
         size = ((self.m - 1) * self.ld + self.n) * e if self.m and self.n else 0
         p = sorted(self.pointers)
-        for a, b in zip(p, p[1:]):
-            column = (b - a) // e % self.ld  # side by side in wider rows: apart when neither reaches the other
-            if b - a < size and (column < self.n or column + self.n > self.ld):
-                raise ValueError(f"{name}: the matrices overlap")
+        for i, a in enumerate(p):
+            for b in p[i + 1:]:  # every one that begins before this one ends, not the next alone
+                if b - a >= size:
+                    break
+                column = (b - a) // e % self.ld  # side by side in wider rows: apart when neither reaches the other
+                if column < self.n or column + self.n > self.ld:
+                    raise ValueError(f"{name}: the matrices overlap")
 
 
 def _disjoint_stacks(w, g, b, workspace):

@@ -1,0 +1,50 @@
+"""The binding's checks of the block operators' arguments, on CPU tensors."""
+import itertools
+
+import pytest
+import torch
+
+from memory_bound_cnn_wtconv2d_gb300 import blockops
+
+
+def stack(ts):
+    """The binding's view of a list of matrices, without its check of the device."""
+    s = blockops._Stack.__new__(blockops._Stack)
+    s.tensors = list(ts)
+    s.m, s.n = ts[0].shape
+    s.ld = ts[0].stride(0)
+    s.pointers = [t.data_ptr() for t in ts]
+    return s
+
+
+def elements(t):
+    m, n = t.shape
+    return {t.storage_offset() + i * t.stride(0) + j for i in range(m) for j in range(n)}
+
+
+def refused(ts):
+    try:
+        stack(ts).separate("w")
+    except ValueError:
+        return True
+    return False
+
+
+def test_matrices_that_share_elements_with_one_further_on():
+    # side by side with the second, which begins between the first and the third
+    flat = torch.zeros(64)
+    at = lambda o: flat[o:].as_strided((2, 4), (10, 1), o)  # noqa: E731
+    ts = [at(0), at(4), at(10)]
+    assert elements(ts[0]) & elements(ts[2])
+    assert refused(ts)
+    assert not refused([at(0), at(4), at(20)])
+
+
+def test_overlap_of_lists_agrees_with_the_elements():
+    flat = torch.zeros(400)
+    for m, n, ld in ((2, 4, 10), (3, 3, 9), (1, 5, 12), (3, 4, 4), (4, 1, 3)):
+        for offsets in itertools.combinations(range(0, 34, 2 if n > 2 else 1), 3):
+            ts = [flat.as_strided((m, n), (ld, 1), o) for o in offsets]
+            sets = [elements(t) for t in ts]
+            share = any(a & b for a, b in itertools.combinations(sets, 2))
+            assert refused(ts) == share, (m, n, ld, offsets)

@@ -201,7 +201,9 @@ __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, uns
     if (stop) sh.dead = 1;
   }
   stop = __syncthreads_or(stop) != 0;
-  if (threadIdx.x == 0 || threadIdx.x == 64 || threadIdx.x == 320) fence_async();  // the threads that issue bulk copies
+  // whoever issues bulk copies: an elected lane of the copy warps, the epilogue's leader
+  const int warp = threadIdx.x >> 5;
+  if (warp == 0 || warp == 10 || threadIdx.x == 64) fence_async();
   return !stop;
 }
 
@@ -617,7 +619,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     }
   }
   // Copies of a role that gave up: nothing may be in flight when the CTA leaves.
-  if (!ok && warp == 1 && lane == 0) {
+  if (!ok && warp == 1 && elect_one()) {  // the lane whose MMAs a commit covers
     mma_commit(smem_addr(&sh.drain));
     const long long t0 = clock64();
     while (!mbar_try(smem_addr(&sh.drain), 0) && clock64() - t0 < kWaitCycles) {

@@ -35,3 +35,16 @@ def test_the_rule_sees_the_helpers():
         found |= {n for n, _ in functions_with(src, r'"[^"\n]*(?:\.aligned|bar\.sync)[^"\n]*"')}
     assert {"cluster_arrive", "cluster_wait", "cluster_sync", "named_sync", "tmem_alloc", "tmem_free", "tmem_load8",
             "tmem_wait_load"} <= found
+
+
+def test_fences_and_commits_cover_the_elected_lane():
+    # which lane elect.sync picks is not promised: what it issues is committed by
+    # an elected lane too, and fenced by every lane of its warp
+    src = re.sub(r"//[^\n]*", "", open([p for p in FILES if p.endswith("/ns.cu")][0]).read())
+    for m in re.finditer(r"mma_commit\(", src):
+        guard = src[:m.start()].rsplit("if (", 2)[-1]
+        assert "elect_one()" in src[:m.start()][-900:] and "lane == 0" not in guard.split("{")[0]
+    barrier = src[src.index("bool grid_barrier"):]
+    barrier = barrier[:barrier.index("return !stop")]
+    after = barrier[barrier.index("__syncthreads_or"):]
+    assert re.search(r"warp == 0 \|\| warp == 10", after) and "threadIdx.x == 0" not in after

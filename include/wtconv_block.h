@@ -116,9 +116,14 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* desc, void* const* weig
                                  long long m_ld, float mu, int nesterov, float decay, float rate, void* ws,
                                  size_t ws_bytes, void* stream);
 
-/* In-kernel waits of these operators that gave up since the previous call on
- * the current device (0 in normal operation), then resets the count; see
- * wtconv_device_faults.  Synchronises the current device. */
+/* In-kernel waits of the matrix operators that gave up (after about a second)
+ * since the previous call on the current device (0 in normal operation), then
+ * resets the count; see wtconv_device_faults.  Synchronises the current
+ * device.  After such a wait the kernel leaves early, the device stays
+ * usable, and no matrix of that call gets a result: wtconv_orthogonalize
+ * writes NaN, wtconv_muon_step leaves the weights as they are (the momentum
+ * has been moved).  In stacks of at most 128 rows this holds matrix by
+ * matrix.  wtconv_test_copy_timeout makes a wait of every call run out. */
 unsigned int wtconv_block_device_faults(void);
 
 #ifdef __cplusplus

@@ -49,7 +49,6 @@
 // arithmetic alone is 1 us or less.  float32 stacks take three products and twice
 // the operand bytes (4 x 2048 x 1024 582 us where bfloat16 takes 286).
 #include "ns_common.cuh"
-#include "../wtconv_launch.h"
 
 namespace wtb {
 
@@ -90,6 +89,7 @@ struct NsMain {
   NsShape s;
   int rb, cb, rk;            // sub-blocks: rows (even), columns, rows that hold data
   NsPoly p;
+  NsWaits w;
   int deep;                  // the first product in more accumulators
   int nb1, nb2, nb3, gsh;    // tile widths of the three products; log2 of the stored diagonal block
   int t1, t2, t3;            // tiles of one matrix in each product
@@ -139,13 +139,13 @@ struct Shared {
 };
 
 // Waits for a phase of an mbarrier; false when it gave up.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait(Shared& sh, long long limit, uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
   if (mbar_try(a, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try(a, parity)) {
     if (sh.dead) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > limit) {
       sh.dead = 1;
       atomicAdd(&g_ns_faults, 1u);
       return false;
@@ -155,12 +155,12 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
 }
 
 // The same by a whole warp, with one answer.
-__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_warp(Shared& sh, long long limit, uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
   if (__all_sync(~0u, mbar_try(a, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(~0u, mbar_try(a, parity))) {
-    const bool late = clock64() - t0 > kWaitCycles;
+    const bool late = clock64() - t0 > limit;
     if (__any_sync(~0u, late || sh.dead)) {
       if (late && !sh.dead) {
         sh.dead = 1;
@@ -173,9 +173,12 @@ __device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t pa
 }
 
 // All CTAs of the launch (co-resident by the cooperative launch) meet here.
-// `round` counts the barriers; a CTA that gave up sets the count's top bit, and
-// all leave.  Everything written before is visible after, to bulk copies too.
-__device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, unsigned int round) {
+// `round` counts the barriers; a CTA that gave up sets the count's top bit
+// before the count is full, so that all leave or none does.  The first barrier
+// also waits for CTAs that still wait for another kernel's TMEM: it has 16
+// times as long.  Everything written before is visible after, to bulk copies
+// too.
+__device__ __forceinline__ bool grid_barrier(Shared& sh, long long limit, unsigned int* sync, unsigned int round) {
   constexpr unsigned int kStop = 1u << 31;
   // what bulk copies read after this was written by plain stores in the first
   // pass, and by the epilogue leader's bulk stores from then on
@@ -190,10 +193,9 @@ __device__ __forceinline__ bool grid_barrier(Shared& sh, unsigned int* sync, uns
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(sync) : "memory");
       if (v >= round * gridDim.x) break;
-      if (clock64() - t0 > kWaitCycles) {
-        sh.dead = 1;
+      if (clock64() - t0 > (round == 1 ? limit * 16 : limit) && atomicCAS(sync, v, v | kStop) == v) {
         atomicAdd(&g_ns_faults, 1u);
-        v = atomicOr(sync, kStop) | kStop;
+        v |= kStop;
         break;
       }
     }
@@ -341,7 +343,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
     }
   }
   unsigned int round = 1;
-  bool ok = grid_barrier(sh, a.sync, round);
+  bool ok = grid_barrier(sh, a.w.limit, a.sync, round);
 
   int cur = 0;
   uint32_t ph = 0;          // copies and MMAs: one parity bit for each stage
@@ -383,11 +385,11 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           for (int k = 0; k < nk; ++k, along += 2 * kSub) {
             const uint32_t bar = smem_addr(&sh.full[stage]), dst = base + stage * stage_bytes + (first ? 0 : 2 * kSub);
             const bool km = phase == 0 || (!of_x && stored(a, i, k));
-            go = wait_warp(sh, &sh.empty[stage], (ph >> stage & 1) ^ 1);
+            go = wait_warp(sh, a.w.limit, &sh.empty[stage], (ph >> stage & 1) ^ 1);
             if (!go) break;
             filled |= 1u << stage;
             if (elect_one()) {
-              mbar_expect(bar, planes * bytes);
+              mbar_expect(bar, planes * bytes + (a.w.hold && first ? 16 : 0));
               for (int p = 0; p < planes; ++p) {
                 const unsigned char* src = p ? lo : hi;
                 const uint32_t to = dst + p * lo_at;
@@ -412,7 +414,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         bool go = true;
         for (int t = blockIdx.x; t < tiles && go; t += gridDim.x) {
           const Tile x = tile_of(a, phase, t);
-          go = wait_warp(sh, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1);
+          go = wait_warp(sh, a.w.limit, &sh.acc_empty[acc], (accph >> acc & 1) ^ 1);
           if (!go) break;
           tc_fence_after();
           uint32_t begun = 0;  // segments that hold a sum
@@ -431,7 +433,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             const uint32_t sa = base + stage * stage_bytes, idesc = idesc0 | (akm ? 0u : 1u << 15) | (bkm ? 0u : 1u << 16);
             const uint32_t da = desc_low(sa, akm), db = desc_low(sa + 2 * kSub, bkm);
             const uint32_t ka = desc_step(akm), kb = desc_step(bkm), d = d0 + seg * seg_cols, lo = lo_at >> 4;
-            go = wait_warp(sh, &sh.full[stage], ph >> stage & 1);
+            go = wait_warp(sh, a.w.limit, &sh.full[stage], ph >> stage & 1);
             if (!go) break;
             tc_fence_after();
             if (elect_one()) {
@@ -496,7 +498,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
           } else if (phase == 2) {
             diag = __ldcg(a.db + grow);
           }
-          const bool got = wait(sh, &sh.acc_full[acc], accph >> acc & 1);
+          const bool got = wait(sh, a.w.limit, &sh.acc_full[acc], accph >> acc & 1);
           __syncwarp();
           tc_fence_after();
           for (int s = 0; s < x.nb; ++s, ++nth) {
@@ -507,7 +509,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               if (in && ebufs == 1 && s > 0) fetch(s, 0);
             }
             if (in) {
-              wait(sh, &sh.epi[b], (epiph >> b) & 1);
+              wait(sh, a.w.limit, &sh.epi[b], (epiph >> b) & 1);
               epiph ^= 1u << b;
             }
             named_sync<kEpiThreads>(1);
@@ -615,7 +617,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         if (leader) bulk_wait();
       }
       __syncwarp();
-      ok = grid_barrier(sh, a.sync, ++round);
+      ok = grid_barrier(sh, a.w.limit, a.sync, ++round);
     }
   }
   // Copies of a role that gave up: nothing may be in flight when the CTA leaves.
@@ -642,11 +644,13 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       }
     }
   }
+  if (!ok) __syncthreads();  // the copies that were in flight have landed
   // Back to the caller's layout, shared out in the same way; a slice is of X's
-  // rows, or of its columns where the caller's matrix is tall.
-  if (ok) {
+  // rows, or of its columns where the caller's matrix is tall.  After a wait
+  // that gave up a result is NaN, and weights stay as they are.
+  if (ok || !call.muon) {
     const int per = a.rk * a.cb * share;
-    const float inv = 1.f / a.p.sx;
+    const float inv = ok ? 1.f / a.p.sx : __int_as_float(0x7FC00000);
     auto put = [&](int mat, int row, int col, float (&v)[8]) {
       if (row >= a.s.m || col >= a.s.n) return;
       T* o = (T*)ptrs.out[mat] + (long long)row * call.out_ld + col;
@@ -758,6 +762,7 @@ constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormMax * 4;  // b
 template <typename T>
 cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
   NsMain a = plan(d, k.muon);
+  a.w = waits();
   unsigned char* w = (unsigned char*)ws;
   a.sync = (unsigned int*)w;
   float* part = (float*)(w + 256);

@@ -5,12 +5,24 @@
 #include "block_device.cuh"
 #include "block_launch.h"
 #include "tc_device.cuh"
+#include "../wtconv_launch.h"
 
 namespace wtb {
 namespace ns {
 
 constexpr int kSub = 8192;                    // bytes of a 64 x 64 sub-block
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
+
+// Limit of the kernels' waits, and whether one of them is made to run out
+// (wtconv_test_copy_timeout).
+struct NsWaits {
+  long long limit;
+  int hold;
+};
+inline NsWaits waits() {
+  const bool hook = wt::wait_hook_on();
+  return {hook ? 1ll << 20 : kWaitCycles, hook ? 1 : 0};
+}
 
 struct NsShape {
   int m, n, r, c, tall, count;

@@ -12,7 +12,6 @@
 // Bound by latency: five steps of three dependent products and an exchange, 8 us
 // a step (3 x 384 x 96 bfloat16 48 us, in the general form 85; 1 x 64 x 256 29 us).
 #include "ns_common.cuh"
-#include "../wtconv_launch.h"
 
 namespace wtb {
 namespace {
@@ -28,6 +27,7 @@ static __device__ unsigned int g_small_faults;
 struct NsSmall {
   NsShape s;
   NsPoly p;
+  NsWaits w;
   int cluster, blocks;  // CTAs of a matrix, 64-column blocks of each
   int rw;               // 64 or 128: rows and columns of A that are not all zero
 };
@@ -78,7 +78,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call, const __grid_constant__ NsPointers ptrs) {
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, drain;
+  __shared__ int gave_up[8];  // of each CTA of the cluster
   __shared__ uint32_t tmem_at;
   __shared__ float da[kRows], db[kRows], warp_sum[kThreads / 32], norms[8];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -96,6 +97,7 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
 
   if (tid == 0) {
     mbar_init(smem_addr(&bar), 1);
+    mbar_init(smem_addr(&drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc(smem_addr(&tmem_at), 512);
@@ -171,25 +173,30 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const bool live = row < a.rw;  // whole warps
   uint32_t parity = 0;
+  bool late = false, gone = false;  // a wait of this thread, of any of the CTA's, gave up
   // All threads: what was written to shared memory is there for the products
   // that `issue` (one lane of warp 0) enqueues; returns when they are done.
+  // After a wait that gave up no more are issued: the CTA goes on with what is
+  // there, as the others of the cluster wait for it at the barriers, and none of
+  // them hands out a result.
   auto products = [&](auto&& issue) {
     fence_async_shared();
     tc_fence_before();
-    __syncthreads();
+    gone = __syncthreads_or(late) != 0;
+    if (gone) return;
     if (warp == 0) {
       tc_fence_after();
       fence_async_shared();
       if (elect_one()) {
         issue();
-        mma_commit(smem_addr(&bar));
+        if (!a.w.hold) mma_commit(smem_addr(&bar));
       }
       __syncwarp();
     }
     const long long t0 = clock64();
     while (!mbar_try(smem_addr(&bar), parity)) {
-      if (clock64() - t0 > kWaitCycles) {
-        if (tid == 0) atomicAdd(&g_small_faults, 1u);
+      if (clock64() - t0 > a.w.limit) {
+        late = true;
         break;
       }
     }
@@ -346,11 +353,28 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
     }
   }
   tc_fence_before();
-  __syncthreads();
+  gone = __syncthreads_or(late) != 0;
+  if (gone && warp == 0) {
+    if (elect_one()) {  // its products may not have ended
+      atomicAdd(&g_small_faults, 1u);
+      mma_commit(smem_addr(&drain));
+      const long long t0 = clock64();
+      while (!mbar_try(smem_addr(&drain), 0) && clock64() - t0 < kWaitCycles) {
+      }
+      while (!a.w.hold && !mbar_try(smem_addr(&bar), parity ^ 1) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+    __syncwarp();
+  }
   if (warp == 0) tmem_free(tmem, 512);
+  if (tid < a.cluster) store_remote(remote(smem_addr(&gave_up[rank]), tid), __int_as_float(gone));
+  cluster_sync();  // the last access to another CTA's shared memory: each may leave from here
+  bool stop = false;
+  for (int k = 0; k < a.cluster; ++k) stop |= gave_up[k] != 0;
+  if (stop && call.muon) return;  // the weights stay as they are
 
   // back to the caller's layout
-  const float inv = 1.f / a.p.sx;
+  const float inv = stop ? __int_as_float(0x7FC00000) : 1.f / a.p.sx;
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
     const int e1 = e / side, e0 = e - e1 * side, y = a.s.tall ? e0 : e1, x = (a.s.tall ? e1 : e0) * 8;
@@ -377,7 +401,6 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
     }
     store8<T>(o, n, a.s.wide, v);
   }
-  cluster_sync();  // nobody leaves while another may still write to its shared memory
 }
 
 // Shared memory of a CTA.  At least a little over half of an SM's, so that one
@@ -432,6 +455,7 @@ cudaError_t ns_small_launch(const wtconv_ns_desc_t& d, const NsCall& k, const Ns
   NsSmall a = {};
   plan(d, a);
   a.p.split = poly_of(d, a.s, k.muon).split;
+  a.w = waits();
   a.s.wide = is_wide(d, k, p);
   if (d.dtype == WTCONV_F32) return launch_t<float>(a, k, p, s);
   if (d.dtype == WTCONV_F16) return launch_t<__half>(a, k, p, s);

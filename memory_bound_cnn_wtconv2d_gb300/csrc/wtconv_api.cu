@@ -240,6 +240,15 @@ wtconv_status_t plan_bw_win(const wtconv_desc_t* d, WtBwPlan& pl, int load) {
 std::mutex g_hook_mu;
 bool g_hook_on = false;
 
+}  // namespace
+
+bool wt::wait_hook_on() {
+  std::lock_guard<std::mutex> lock(g_hook_mu);
+  return g_hook_on;
+}
+
+namespace {
+
 template <typename Plan>
 void apply_wait_hook(Plan& pl) {
   std::lock_guard<std::mutex> lock(g_hook_mu);

@@ -86,6 +86,9 @@ cudaError_t launch_scale(const float* in, float* out, int n, float f, cudaStream
 // Sets the thread-local message returned by wtconv_last_error().
 void set_last_error(const char* msg);
 
+// Whether wtconv_test_copy_timeout has the test hook on.
+bool wait_hook_on();
+
 // Host-side caches, per device, of what every call would otherwise ask the
 // runtime again (each a few microseconds):
 //   ensure_smem: raises kernel f's opt-in dynamic shared-memory limit to at

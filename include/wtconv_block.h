@@ -81,7 +81,11 @@ typedef struct {
   int count, m, n;
   int dtype;          /* wtconv_dtype_t of the matrices               */
   int steps;          /* Newton-Schulz steps, 0..64                   */
-  float a, b, c;      /* coefficients, finite, at most 16 in size     */
+  float a, b, c;      /* coefficients, finite, at most 16 in size; p(s) =
+                         a s + b s^3 + c s^5, applied `steps` times, keeps
+                         [0, 1] within [-64, 64] at every step (otherwise
+                         WTCONV_ERR_UNSUPPORTED): the products' operands
+                         have float16's range                         */
   float eps;          /* added to the Frobenius norm, finite, >= 0    */
 } wtconv_ns_desc_t;
 

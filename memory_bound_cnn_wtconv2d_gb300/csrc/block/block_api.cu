@@ -88,6 +88,10 @@ wtconv_status_t check_ns(const wtconv_ns_desc_t* d) {
   for (float v : q)
     if (!(fabsf(v) <= 16.f)) return fail(WTCONV_ERR_INVALID_ARG, "coefficients must be finite and at most 16 in size");
   if (!(isfinite(d->eps) && d->eps >= 0.f)) return fail(WTCONV_ERR_INVALID_ARG, "eps must be finite and not negative");
+  const double reach = wtb::ns_bounds(*d).x;
+  if (!(reach <= wtb::kNsMostGrowth))
+    return fail(WTCONV_ERR_UNSUPPORTED, "%d steps of (%g, %g, %g) can take a norm of 1 beyond %g", d->steps, d->a, d->b, d->c,
+                wtb::kNsMostGrowth);
   if (d->count > WTCONV_NS_MAX_COUNT)
     return fail(WTCONV_ERR_UNSUPPORTED, "%d matrices in one call (at most %d)", d->count, WTCONV_NS_MAX_COUNT);
   if (d->m > 32768 || d->n > 32768) return fail(WTCONV_ERR_UNSUPPORTED, "%d x %d: at most 32768 rows and columns", d->m, d->n);

@@ -49,6 +49,16 @@ struct NsCall {
   int muon;  // 1: optimiser step, 0: orthogonalize
 };
 
+// What the iterates of a call can reach from |X| = 1, in the spectral norm:
+// bounds on every X, and on the entries of A and B off the diagonal.
+struct NsBounds {
+  double x, ab;
+};
+NsBounds ns_bounds(const wtconv_ns_desc_t& d);
+// The most that x may be: float16 operands with fixed scales keep 22 bits of
+// what polynomials make that stay below it.
+constexpr double kNsMostGrowth = 64;
+
 size_t ns_workspace(const wtconv_ns_desc_t& d);
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& c, const NsPointers& p, void* ws, cudaStream_t s);
 unsigned int ns_take_faults();

@@ -10,24 +10,26 @@
 // accumulators in TMEM.
 //
 // Number formats.  Operands are float16 with power-of-two scales that put
-// their entries near 1: 11 significand bits instead of bfloat16's 8, and
-// nothing is lost to the range because |X| <= 1.3 is known.  X itself is kept
-// as a pair hi + lo (22 bits): the term a X carries the small singular values,
-// which five steps amplify up to 485 times, and rounding X to 11 bits each
-// step leaves several per cent on them; the products only see hi.  The
-// diagonals of A and of a I + B never enter an operand: they are kept in
-// float32 (da, db) and multiplied in the epilogues, so that the operands'
-// rounding counts relative to the spread of the singular values only (0.4e-3
-// instead of 1.7e-3 on the result of a random 96 x 384 matrix).  That serves
-// bfloat16 stacks, and the step of float16 weights.  Types of more bits, and matrices of fewer than 16 rows,
-// whose few roundings do not average out, keep pairs for A and B too and add
-// the products lo hi + hi lo + hi hi (`split`).  The tensor core's additions
-// truncate, some 2^-22 of the sum each; `split` spreads the sum over kSegments
-// accumulators (one for the small products), which the epilogue adds, to keep
-// that below 1e-5.  It shows on the diagonal of A, whose sums only grow; long
-// ones of an orthogonalised stack are spread over kDeepSegments (275 x 3176
-// float32: error 4.5e-6 -> 1.7e-6, that of float32 sums 2.0e-6; 223 -> 225 us, 4 x
-// 2048 x 1024 540 -> 594; of 19 steps 1.4e-6 and 2.2e-6 without).
+// their entries near 1: 11 significand bits instead of bfloat16's 8.  The
+// scales leave room for what the polynomial can make of a norm of 1 in all its
+// steps (ns_bounds; the default set stays below 1.3), and one that can pass 64
+// is refused.  X itself is kept as a pair hi + lo (22 bits): the term a X
+// carries the small singular values, which five steps amplify up to 485 times,
+// and rounding X to 11 bits each step leaves several per cent on them; the
+// products only see hi.  The diagonals of A and of a I + B never enter an
+// operand: they are kept in float32 (da, db) and multiplied in the epilogues,
+// so that the operands' rounding counts relative to the spread of the singular
+// values only (0.4e-3 instead of 1.7e-3 on the result of a random 96 x 384
+// matrix).  That serves bfloat16 stacks, and the step of 16-bit weights.
+// Types of more bits, and matrices of fewer than 16 rows, whose few roundings
+// do not average out, keep pairs for A and B too and add the products lo hi +
+// hi lo + hi hi (`split`).  The tensor core's additions truncate, some 2^-22
+// of the sum each; `split` spreads the sum over kSegments accumulators (one
+// for the small products), which the epilogue adds, to keep that below 1e-5.
+// It shows on the diagonal of A, whose sums only grow; long ones of an
+// orthogonalised stack are spread over kDeepSegments (275 x 3176 float32:
+// error 4.5e-6 -> 1.7e-6, that of float32 sums 2.0e-6; 223 -> 225 us, 4 x 2048
+// x 1024 540 -> 594; of 19 steps 1.4e-6 and 2.2e-6 without).
 //
 // Layout.  Every matrix lies in the workspace as 64 x 64 sub-blocks whose 8 KB
 // are the 128-byte-swizzled image that the tensor core reads, so that an
@@ -806,6 +808,42 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
 }
 
 }  // namespace
+
+// Every singular value s of X becomes p(s) = a s + b s^3 + c s^5, and A's
+// eigenvalues t = s^2 become b t + c t^2.  An entry off the diagonal of a
+// symmetric matrix is at most half the width of its spectrum.
+NsBounds ns_bounds(const wtconv_ns_desc_t& d) {
+  const double a = d.a, b = d.b, c = d.c;
+  const auto most = [&](double s) {  // of |p| on [0, s]
+    const auto p = [&](double v) { return fabs(v * (a + v * v * (b + v * v * c))); };
+    double m = p(s);
+    const auto inner = [&](double t) {  // a root of p' in s^2
+      if (t > 0 && t < s * s && p(sqrt(t)) > m) m = p(sqrt(t));
+    };
+    const double disc = 9 * b * b - 20 * a * c;
+    if (c != 0 && disc >= 0) {
+      inner((-3 * b + sqrt(disc)) / (10 * c));
+      inner((-3 * b - sqrt(disc)) / (10 * c));
+    } else if (c == 0 && b != 0) {
+      inner(-a / (3 * b));
+    }
+    return m;
+  };
+  double s = 1 + 1.0 / 256;  // room for the products' rounding
+  NsBounds r = {s, 0.5 * s * s};
+  for (int i = 0; i < d.steps && r.x <= kNsMostGrowth; ++i) {
+    const double t = s * s, q = t * (b + t * c);
+    double lo = q < 0 ? q : 0, hi = q > 0 ? q : 0;
+    if (c != 0) {
+      const double at = -b / (2 * c), v = at * (b + at * c);
+      if (at > 0 && at < t) lo = v < lo ? v : lo, hi = v > hi ? v : hi;
+    }
+    r.ab = fmax(r.ab, 0.5 * fmax(t, hi - lo));
+    s = most(s);
+    r.x = fmax(r.x, s);
+  }
+  return r;
+}
 
 size_t ns_workspace(const wtconv_ns_desc_t& d) {
   if (ns_small_takes(d)) return 0;

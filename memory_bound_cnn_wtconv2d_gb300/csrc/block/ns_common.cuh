@@ -2,6 +2,8 @@
 // and float16 pairs.
 #pragma once
 
+#include <math.h>
+
 #include "block_device.cuh"
 #include "block_launch.h"
 #include "tc_device.cuh"
@@ -116,6 +118,12 @@ inline int ceil_log2(double v) {
   return e;
 }
 
+// Largest e <= most with 2^e v <= 2^15, half of float16's range.
+inline int room(double v, int most) {
+  while (ldexp(v, most) > 32768.0) --most;
+  return most;
+}
+
 inline NsShape shape_of(const wtconv_ns_desc_t& d) {
   NsShape s = {};
   s.m = d.m; s.n = d.n; s.count = d.count; s.eps = d.eps;
@@ -126,7 +134,8 @@ inline NsShape shape_of(const wtconv_ns_desc_t& d) {
 }
 
 // Entries of X near 1: |X|_F is about 1 at first; those of A, B near 1 on the
-// diagonal.  Both capped so that no entry passes float16's range.
+// diagonal.  Both lower where what the polynomial can make of a norm of 1 would
+// bring an entry past float16's range.
 // Pairs where the result shows more than 11 bits: not where a float16 weight
 // takes a step of a few per cent of its size.
 inline NsPoly poly_of(const wtconv_ns_desc_t& d, const NsShape& s, bool muon) {
@@ -135,10 +144,9 @@ inline NsPoly poly_of(const wtconv_ns_desc_t& d, const NsShape& s, bool muon) {
   p.split = d.dtype == WTCONV_F32 || (d.dtype == WTCONV_F16 && !muon) || s.r < 16;
   p.ca = d.a; p.cb = d.b; p.cc = d.c;
   int ex = (ceil_log2(s.r) + ceil_log2(s.c)) / 2, ea = ceil_log2(s.r);
-  if (ex > 12) ex = 12;
-  if (ea > 11) ea = 11;
-  p.sx = (float)(1 << ex);
-  p.sa = (float)(1 << ea);
+  const NsBounds b = ns_bounds(d);
+  p.sx = (float)ldexp(1.0, room(b.x, ex < 12 ? ex : 12));
+  p.sa = (float)ldexp(1.0, room(b.ab, ea < 11 ? ea : 11));
   return p;
 }
 

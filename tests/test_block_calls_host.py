@@ -48,3 +48,18 @@ def test_overlap_of_lists_agrees_with_the_elements():
             sets = [elements(t) for t in ts]
             share = any(a & b for a, b in itertools.combinations(sets, 2))
             assert refused(ts) == share, (m, n, ld, offsets)
+
+
+def test_polynomials_beyond_the_range_have_no_workspace():
+    from memory_bound_cnn_wtconv2d_gb300 import build
+    import ctypes
+    build.build()
+    L = blockops.lib()
+    size = lambda abc, steps: L.wtconv_ns_workspace_size(  # noqa: E731
+        ctypes.byref(blockops.NsDesc(2, 300, 400, 0, steps, *abc, 1e-7)))
+    for abc, steps in (((16.0, 0.0, 0.0), 1), ((2.0, 0.0, 0.0), 5), ((16.0, 16.0, 16.0), 1), (blockops.NS_COEFFICIENTS, 64),
+                       ((1.5, -0.5, 0.0), 64), ((1.875, -1.25, 0.375), 64), ((2.0, -1.5, 0.5), 64), ((-1.0, 0.0, 0.0), 64)):
+        assert size(abc, steps) > 0, (abc, steps)
+    for abc, steps in (((2.0, 0.0, 0.0), 6), ((16.0, 16.0, 16.0), 2), ((1.1, 0.0, 0.0), 64), ((0.0, 0.0, 16.0), 3),
+                       ((-16.0, 16.0, -16.0), 2)):
+        assert size(abc, steps) == 0, (abc, steps)

@@ -102,7 +102,10 @@ size_t wtconv_ns_workspace_size(const wtconv_ns_desc_t* desc);
  * of count device pointers, read during the call.  The products take operands
  * of 11 significand bits for bfloat16 stacks and of 22 bits for float16 and
  * float32 stacks and for matrices of fewer than 16 rows or columns, with
- * float32 accumulation. */
+ * float32 accumulation; where |g| lies below eps, or the polynomial shrinks
+ * what it is given, these are bits of the small matrix that results.  |g| is
+ * the root of a float32 sum of squares: entries below 1e-19 do not count in
+ * it, and one above 1e19 makes it infinite and the result 0. */
 wtconv_status_t wtconv_orthogonalize(const wtconv_ns_desc_t* desc, const void* const* g, long long g_ld,
                                      void* const* out, long long out_ld, void* ws, size_t ws_bytes,
                                      void* stream);

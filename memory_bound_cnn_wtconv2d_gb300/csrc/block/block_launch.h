@@ -50,9 +50,10 @@ struct NsCall {
 };
 
 // What the iterates of a call can reach from |X| = 1, in the spectral norm:
-// bounds on every X, and on the entries of A and B off the diagonal.
+// bounds on every X, on the entries of A and B off the diagonal, and on
+// |p(s)| / s, the factor of a step.
 struct NsBounds {
-  double x, ab;
+  double x, ab, slope;
 };
 NsBounds ns_bounds(const wtconv_ns_desc_t& d);
 // The most that x may be: float16 operands with fixed scales keep 22 bits of

@@ -13,7 +13,8 @@
 // their entries near 1: 11 significand bits instead of bfloat16's 8.  The
 // scales leave room for what the polynomial can make of a norm of 1 in all its
 // steps (ns_bounds; the default set stays below 1.3), and one that can pass 64
-// is refused.  X itself is kept as a pair hi + lo (22 bits): the term a X
+// is refused; a matrix whose norm lies far below eps is kept times a power of
+// two more, step by step (shift_of).  X itself is kept as a pair hi + lo (22 bits): the term a X
 // carries the small singular values, which five steps amplify up to 485 times,
 // and rounding X to 11 bits each step leaves several per cent on them; the
 // products only see hi.  The diagonals of A and of a I + B never enter an
@@ -97,6 +98,7 @@ struct NsMain {
   int t1, t2, t3;            // tiles of one matrix in each product
   unsigned char *xh[2], *xl[2], *ah, *al, *bh, *bl;
   float *da, *db;            // diagonals of A and a I + B, in the images' scale
+  float* lead;               // of each matrix, see shift_of
   long long xbytes, abytes;  // of one matrix
   unsigned int* sync;        // barrier count, abort flag
   const float* part;
@@ -299,8 +301,10 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         float q = 0.f;
         for (int j = lane; j < a.s.parts; j += 32) q += a.part[mat * kNormMax + j];
         for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-        mul = q == 0.f ? 0.f : a.p.sx / (sqrtf(q) + a.s.eps);
+        const float norm = sqrtf(q), inv = 1.f / (norm + a.s.eps), lead = lead_of(norm, inv);
+        mul = q == 0.f ? 0.f : a.p.sx * pow2(shift_of(lead, a.p.grow, 0)) * inv;
         mat_known = mat;
+        if (lane == 0) a.lead[mat] = lead;  // by every warp that meets the matrix, the same value
       }
       unsigned char* xh = a.xh[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
       unsigned char* xl = a.xl[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
@@ -472,7 +476,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         const unsigned char* il = phase == 1 ? a.al : a.xl[cur];
         unsigned char* oh = phase == 0 ? a.ah : phase == 1 ? a.bh : a.xh[cur ^ 1];
         unsigned char* ol = phase == 0 ? a.al : phase == 1 ? a.bl : a.xl[cur ^ 1];
-        const float facc = phase == 0 ? a.p.sa / (a.p.sx * a.p.sx) : phase == 1 ? a.p.cc / a.p.sa : 1.f / a.p.sa;
+        const float fphase = phase == 0 ? a.p.sa / (a.p.sx * a.p.sx) : phase == 1 ? a.p.cc / a.p.sa : 1.f / a.p.sa;
         const int ncols = phase == 2 ? a.cb : a.rb;
         const long long obytes = phase == 2 ? a.xbytes : a.abytes;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -492,7 +496,12 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             fetch(0, nth & (ebufs - 1));
           }
           const int grow = (x.mat * a.rb + 2 * x.i) * 64 + row;  // row in the diagonals
-          float diag = 0.f;
+          float diag = 0.f, facc = fphase;
+          if (phase != 1) {
+            const float lead = __ldcg(a.lead + x.mat);
+            const int now = shift_of(lead, a.p.grow, step);
+            facc *= pow2(phase == 0 ? -2 * now : shift_of(lead, a.p.grow, step + 1) - now);
+          }
           if (phase == 1) {
             for (int j = tid - 64; j < x.nb * 64; j += kEpiThreads)
               sh.dcol[j] = __ldcg(a.da + (x.mat * a.rb + x.j) * 64 + j);
@@ -652,7 +661,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   // that gave up a result is NaN, and weights stay as they are.
   if (ok || !call.muon) {
     const int per = a.rk * a.cb * share;
-    const float inv = ok ? 1.f / a.p.sx : __int_as_float(0x7FC00000);
+    int mat_known = -1;
+    float inv = 0.f;
     auto put = [&](int mat, int row, int col, float (&v)[8]) {
       if (row >= a.s.m || col >= a.s.n) return;
       T* o = (T*)ptrs.out[mat] + (long long)row * call.out_ld + col;
@@ -668,6 +678,10 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       const int mat = t / per, u = t % per / share, y0 = (t % share) * slice, bi = u / a.cb, bj = u % a.cb;
       const unsigned char* xh = a.xh[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
       const unsigned char* xl = a.xl[cur] + mat * a.xbytes + at_sub(bi, bj, a.cb);
+      if (mat != mat_known) {
+        inv = ok ? pow2(-shift_of(__ldcg(a.lead + mat), a.p.grow, a.p.steps)) / a.p.sx : __int_as_float(0x7FC00000);
+        mat_known = mat;
+      }
 #pragma unroll 4
       for (int e = lane; e < 8 * slice; e += 32) {
         // row and chunk of 8 columns of X
@@ -759,7 +773,9 @@ NsMain plan(const wtconv_ns_desc_t& d, bool muon) {
   return a;
 }
 
-constexpr size_t kHead = 256 + (size_t)WTCONV_NS_MAX_COUNT * kNormMax * 4;  // barrier, partial sums
+constexpr size_t kLead = 256;  // WTCONV_NS_MAX_COUNT floats
+constexpr size_t kHead = 256 + kLead + (size_t)WTCONV_NS_MAX_COUNT * kNormMax * 4;  // barrier, leads, partial sums
+static_assert(kLead >= WTCONV_NS_MAX_COUNT * 4, "");
 
 template <typename T>
 cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t st) {
@@ -767,7 +783,8 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
   a.w = waits();
   unsigned char* w = (unsigned char*)ws;
   a.sync = (unsigned int*)w;
-  float* part = (float*)(w + 256);
+  a.lead = (float*)(w + 256);
+  float* part = (float*)(w + 256 + kLead);
   a.part = part;
   w += kHead;
   a.da = (float*)w, w += (size_t)d.count * a.rb * 256;
@@ -830,15 +847,16 @@ NsBounds ns_bounds(const wtconv_ns_desc_t& d) {
     return m;
   };
   double s = 1 + 1.0 / 256;  // room for the products' rounding
-  NsBounds r = {s, 0.5 * s * s};
+  NsBounds r = {s, 0.5 * s * s, fabs(a)};
   for (int i = 0; i < d.steps && r.x <= kNsMostGrowth; ++i) {
     const double t = s * s, q = t * (b + t * c);
-    double lo = q < 0 ? q : 0, hi = q > 0 ? q : 0;
+    double lo = q < 0 ? q : 0, hi = q > 0 ? q : 0;  // b t + c t^2 over [0, s^2]
     if (c != 0) {
       const double at = -b / (2 * c), v = at * (b + at * c);
       if (at > 0 && at < t) lo = v < lo ? v : lo, hi = v > hi ? v : hi;
     }
     r.ab = fmax(r.ab, 0.5 * fmax(t, hi - lo));
+    r.slope = fmax(r.slope, fmax(fabs(a + lo), fabs(a + hi)));
     s = most(s);
     r.x = fmax(r.x, s);
   }

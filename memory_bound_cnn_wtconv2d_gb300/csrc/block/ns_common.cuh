@@ -110,7 +110,24 @@ struct NsPoly {
   int steps, split;
   float ca, cb, cc;  // coefficients
   float sx, sa;      // scales of X and of A, B
+  float grow;        // log2 of the most that a step makes of a singular value's size
 };
+
+// A matrix whose norm lies below eps (or that the polynomial shrinks) would
+// leave float16's range at the lower end, and lose its low halves first.  X is
+// kept times 2^shift more while what its norm can have become after k steps is
+// below 1/2; lead: log2 of |g| / (|g| + eps).  Powers of two: a matrix that
+// needs none keeps its bits.  A and B need none: what they add to a X is
+// smaller by the square of X.
+constexpr int kMostShift = 60;
+__device__ __forceinline__ int shift_of(float lead, float grow, int k) {
+  const float f = -fmaf((float)k, grow, lead);
+  return f >= 1.f ? min((int)f, kMostShift) : 0;  // 0 for a NaN
+}
+// inv: 1 / (norm + eps)
+__device__ __forceinline__ float lead_of(float norm, float inv) { return norm > 0.f ? log2f(norm * inv) : 0.f; }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
 inline int ceil_log2(double v) {
   int e = 0;
@@ -147,6 +164,7 @@ inline NsPoly poly_of(const wtconv_ns_desc_t& d, const NsShape& s, bool muon) {
   const NsBounds b = ns_bounds(d);
   p.sx = (float)ldexp(1.0, room(b.x, ex < 12 ? ex : 12));
   p.sa = (float)ldexp(1.0, room(b.ab, ea < 11 ? ea : 11));
+  p.grow = (float)log2(b.slope > 1e-3 ? b.slope : 1e-3);
   return p;
 }
 

@@ -135,11 +135,13 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
     store_remote(remote(smem_addr(&norms[rank]), tid), t);
   }
   cluster_sync();
-  float mul;
+  float mul, lead;
   {
     float t = 0.f;
     for (int k = 0; k < a.cluster; ++k) t += norms[k];
-    mul = t == 0.f ? 0.f : a.p.sx / (sqrtf(t) + a.s.eps);
+    const float norm = sqrtf(t), inv = 1.f / (norm + a.s.eps);
+    lead = lead_of(norm, inv);
+    mul = t == 0.f ? 0.f : a.p.sx * pow2(shift_of(lead, a.p.grow, 0)) * inv;
   }
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
@@ -207,10 +209,17 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   // Adds the products of two operands along 64 columns at a time: K-major a,
   // and b of either order.
   const int passes = split ? 3 : 1;
-  const float f0 = a.p.sa / (a.p.sx * a.p.sx), f1 = a.p.cc / a.p.sa, f2 = 1.f / a.p.sa;
+  const float f1 = a.p.cc / a.p.sa;
+  const bool shifts = lead <= -1.f || a.p.grow < 0.f;  // at any step
   const int per = a.rw / a.cluster;  // rows of A that a CTA adds up
 
   for (int step = 0; step < a.p.steps; ++step) {
+    float f0 = a.p.sa / (a.p.sx * a.p.sx), f2 = 1.f / a.p.sa;
+    if (shifts) {
+      const int now = shift_of(lead, a.p.grow, step);
+      f0 *= pow2(-2 * now);
+      f2 *= pow2(shift_of(lead, a.p.grow, step + 1) - now);
+    }
     // A's share of this CTA's columns
     products([&]() {
       const uint32_t idesc = instr_desc(a.rw, true, true);
@@ -374,7 +383,7 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   if (stop && call.muon) return;  // the weights stay as they are
 
   // back to the caller's layout
-  const float inv = stop ? __int_as_float(0x7FC00000) : 1.f / a.p.sx;
+  const float inv = stop ? __int_as_float(0x7FC00000) : pow2(-shift_of(lead, a.p.grow, a.p.steps)) / a.p.sx;
 #pragma unroll 2
   for (int e = tid; e < chunks; e += kThreads) {
     const int e1 = e / side, e0 = e - e1 * side, y = a.s.tall ? e0 : e1, x = (a.s.tall ? e1 : e0) * 8;

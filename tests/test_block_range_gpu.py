@@ -80,3 +80,44 @@ def test_polynomials_that_leave_the_range_are_refused(ops):
             ops.wtconv_orthogonalize(g, steps=steps, coefficients=abc, out=out)
         assert e.value.status == wtconv.WTCONV_ERR_UNSUPPORTED
     assert float((out - 7).abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n", [(300, 700), (700, 90), (5, 9), (1030, 640)])
+@pytest.mark.parametrize("norm", [3e-8, 1e-10, 1e-12, 1e-15, 1e-17])
+def test_norms_far_below_eps(ops, norm, m, n, dtype):
+    # X = g / (|g| + eps) is tiny, and so is the result; its bits are asked for all the same
+    g = random(2, m, n, seed=n, size=1.0)
+    g[1] *= 1e6  # beside a matrix further up
+    g = (g * (norm / float(g[0].norm()))).to(dtype)
+    out = ops.wtconv_orthogonalize(g)
+    for i in range(2):
+        assert rel(out[i], ns64(g[i])) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("m,n", [(100, 300), (420, 300)])
+def test_a_tiny_matrix_grows_to_an_orthogonal_one(ops, m, n):
+    # 64 cubic steps from a norm of 1e-10 / 1e-7: 17 to come to 1, the rest converges.
+    # Each rounds by 2^-22 of the result at most: 64 of them stay below 2e-5.
+    g = random(m, n, seed=3, size=1.0)
+    g *= 1e-10 / float(g.norm())
+    out = ops.wtconv_orthogonalize(g, steps=64, coefficients=(1.5, -0.5, 0.0))
+    want = ns64(g, 64, (1.5, -0.5, 0.0))
+    assert abs(float(want.norm()) - min(m, n) ** 0.5) < 1e-6
+    assert rel(out, want) <= 2e-5
+
+
+@pytest.mark.parametrize("abc,steps", [((0.5, 0.0, 0.0), 20), ((0.25, 0.1, 0.0), 15), ((-0.75, 0.0, -0.1), 9)])
+@pytest.mark.parametrize("m,n", [(90, 700), (600, 500)])
+def test_shrinking_polynomials(ops, m, n, abc, steps):
+    g = random(m, n, seed=5)
+    # 20 roundings of 2^-22 at most
+    assert rel(ops.wtconv_orthogonalize(g, steps=steps, coefficients=abc), ns64(g, steps, abc)) <= 1e-5
+
+
+@pytest.mark.parametrize("m,n", [(60, 90), (300, 200)])
+def test_optimizer_step_on_a_tiny_gradient(ops, m, n):
+    w, g, b = torch.zeros(m, n, device="cuda"), random(m, n, seed=6, size=1e-14), torch.zeros(m, n, device="cuda")
+    m64 = 0.05 * g.double()
+    ops.wtconv_muon_step(w, g, b, lr=1.0, momentum=0.95, nesterov=False)
+    assert rel(w, -ns64(m64)) <= 1e-5

@@ -45,6 +45,17 @@ class Muon(torch.optim.Optimizer):
                 if not p.is_contiguous():
                     raise ValueError("Muon takes contiguous parameters")
 
+    def load_state_dict(self, state_dict):
+        """As every optimiser's, but the buffers stay float32: the base class casts
+        the state of 16-bit parameters to their type."""
+        super().load_state_dict(state_dict)
+        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
+        params = [p for group in self.param_groups for p in group["params"]]
+        for i, p in zip(saved, params):
+            entry = state_dict["state"].get(i)
+            if entry and "buffer" in entry:
+                self.state[p]["buffer"] = entry["buffer"].detach().to(p.device, torch.float32, copy=True).contiguous()
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None

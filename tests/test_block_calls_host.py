@@ -63,3 +63,24 @@ def test_polynomials_beyond_the_range_have_no_workspace():
     for abc, steps in (((2.0, 0.0, 0.0), 6), ((16.0, 16.0, 16.0), 2), ((1.1, 0.0, 0.0), 64), ((0.0, 0.0, 16.0), 3),
                        ((-16.0, 16.0, -16.0), 2)):
         assert size(abc, steps) == 0, (abc, steps)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_a_resumed_optimiser_has_its_buffers_in_float32(dtype):
+    from memory_bound_cnn_wtconv2d_gb300.muon import Muon
+    shapes = [(6, 4), (4, 6), (3, 5, 1, 1), (2, 2)]
+    new = lambda: [torch.nn.Parameter(torch.randn(s).to(dtype)) for s in shapes]  # noqa: E731
+    ps = new()
+    opt = Muon([{"params": ps[:2]}, {"params": ps[2:], "lr": 0.5}], lr=0.1)
+    for p in ps[:3]:  # the last has not had a gradient
+        opt.state[p]["buffer"] = torch.randn(p.shape)
+    saved = opt.state_dict()
+    qs = new()
+    again = Muon([{"params": qs[:2]}, {"params": qs[2:]}], lr=0.3)
+    again.load_state_dict(saved)
+    assert [g["lr"] for g in again.param_groups] == [0.1, 0.5]
+    for p, q in zip(ps[:3], qs):
+        b = again.state[q]["buffer"]
+        assert b.dtype is torch.float32 and torch.equal(b, opt.state[p]["buffer"])
+        assert b.data_ptr() != opt.state[p]["buffer"].data_ptr()
+    assert not again.state[qs[3]]

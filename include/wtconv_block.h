@@ -133,6 +133,11 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* desc, void* const* weig
  * matrix.  wtconv_test_copy_timeout makes a wait of every call run out. */
 unsigned int wtconv_block_device_faults(void);
 
+/* The same count without a wait and without a reset: enqueues a copy of it, as
+ * it is when `stream` gets there, to *count, host memory that stays valid until
+ * then (page-locked, or the copy may synchronise). */
+wtconv_status_t wtconv_block_device_faults_async(unsigned int* count, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

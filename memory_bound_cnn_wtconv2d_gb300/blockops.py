@@ -24,7 +24,8 @@ NS_MAX_COUNT = 64
 
 # entry points declared in include/wtconv_block.h
 EXPORTS = ("wtconv_gn_workspace_size", "wtconv_gn_act_fwd", "wtconv_gn_act_bwd", "wtconv_ns_workspace_size",
-           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_block_device_faults")
+           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_block_device_faults",
+           "wtconv_block_device_faults_async")
 
 
 class GnDesc(ctypes.Structure):
@@ -56,7 +57,8 @@ def lib() -> ctypes.CDLL:
                 ("wtconv_ns_workspace_size", sz, [nd]),
                 ("wtconv_orthogonalize", i, [nd, vp, ll, vp, ll, vp, sz, vp]),
                 ("wtconv_muon_step", i, [nd, vp, ll, vp, ll, vp, ll, f, i, f, f, vp, sz, vp]),
-                ("wtconv_block_device_faults", ctypes.c_uint, [])):
+                ("wtconv_block_device_faults", ctypes.c_uint, []),
+                ("wtconv_block_device_faults_async", i, [vp, vp])):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         _LIB = L
@@ -469,3 +471,17 @@ def wtconv_block_device_faults() -> int:
     """In-kernel waits of these operators that gave up since the previous call
     (0 in normal operation); synchronises the device and resets the count."""
     return int(lib().wtconv_block_device_faults())
+
+
+def wtconv_block_device_faults_async(count, device, stream=None) -> None:
+    """Enqueues a copy of that count, not reset, to `count`: a pinned int32 CPU
+    tensor of one element that stays alive until the copy is done.  No wait."""
+    if not (isinstance(count, torch.Tensor) and count.dtype is torch.int32 and count.numel() == 1
+            and count.device.type == "cpu" and count.is_pinned()):
+        raise ValueError("count must be a pinned int32 CPU tensor of one element")
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {device}")
+    device = torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
+    with _on(device, stream):
+        _c._check(lib().wtconv_block_device_faults_async(count.data_ptr(), _stream_of(device)))

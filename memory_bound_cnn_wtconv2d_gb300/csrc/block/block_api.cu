@@ -245,6 +245,14 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* d, void* const* weight,
   }
 }
 
+wtconv_status_t wtconv_block_device_faults_async(unsigned int* count, void* stream) {
+  TRY(pointer(count, "count", 4));
+  const unsigned int* from = wtb::ns_fault_count();
+  if (!from) return cuda_status(cudaGetLastError(), "wtconv_block_device_faults_async");
+  return cuda_status(cudaMemcpyAsync(count, from, sizeof(*count), cudaMemcpyDeviceToHost, (cudaStream_t)stream),
+                     "wtconv_block_device_faults_async");
+}
+
 unsigned int wtconv_block_device_faults(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return 0;
   return wtb::ns_take_faults();

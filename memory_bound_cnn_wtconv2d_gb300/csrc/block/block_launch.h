@@ -63,5 +63,6 @@ constexpr double kNsMostGrowth = 64;
 size_t ns_workspace(const wtconv_ns_desc_t& d);
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& c, const NsPointers& p, void* ws, cudaStream_t s);
 unsigned int ns_take_faults();
+unsigned int* ns_fault_count();  // on the current device; NULL where the runtime has none
 
 }  // namespace wtb

@@ -58,7 +58,6 @@ namespace wtb {
 // The form for short matrices (ns_small.cu): whether it takes this call.
 bool ns_small_takes(const wtconv_ns_desc_t& d);
 cudaError_t ns_small_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, cudaStream_t s);
-unsigned int ns_small_take_faults();
 
 namespace {
 
@@ -86,7 +85,7 @@ constexpr int kSmem = kRingWide * kSub + kEpiBytes + 1024;
 static_assert(kRing * kSub + 2 * kEpiBytes == kRingWide * kSub + kEpiBytes, "one layout for both");
 static_assert(kThreads / 32 * 64 * 65 * 4 <= kRing * kSub + 2 * kEpiBytes, "the first and last pass's tiles");
 
-static __device__ unsigned int g_ns_faults;
+static __device__ unsigned int g_ns_faults;  // of both forms
 
 struct NsMain {
   NsShape s;
@@ -166,9 +165,9 @@ __device__ __forceinline__ bool wait_warp(Shared& sh, long long limit, uint64_t*
   while (!__all_sync(~0u, mbar_try(a, parity))) {
     const bool late = clock64() - t0 > limit;
     if (__any_sync(~0u, late || sh.dead)) {
-      if (late && !sh.dead) {
+      if (__any_sync(~0u, late) && (threadIdx.x & 31) == 0) {
         sh.dead = 1;
-        if ((threadIdx.x & 31) == 0) atomicAdd(&g_ns_faults, 1u);
+        atomicAdd(&g_ns_faults, 1u);
       }
       return false;
     }
@@ -877,11 +876,16 @@ cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointe
   return launch_t<__nv_bfloat16>(d, k, p, ws, s);
 }
 
+unsigned int* ns_fault_count() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_ns_faults) == cudaSuccess ? (unsigned int*)p : nullptr;
+}
+
 unsigned int ns_take_faults() {
   unsigned int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, g_ns_faults, sizeof(v)) != cudaSuccess) return 0;
   cudaMemcpyToSymbol(g_ns_faults, &z, sizeof(z));
-  return v + ns_small_take_faults();
+  return v;
 }
 
 }  // namespace wtb

@@ -22,12 +22,11 @@ constexpr int kThreads = 256;
 constexpr int kRows = 128;            // rows of every operand: M of the products
 constexpr int kBlock = 2 * kSub;      // 128 rows x 64 columns
 
-static __device__ unsigned int g_small_faults;
-
 struct NsSmall {
   NsShape s;
   NsPoly p;
   NsWaits w;
+  unsigned int* faults;
   int cluster, blocks;  // CTAs of a matrix, 64-column blocks of each
   int rw;               // 64 or 128: rows and columns of A that are not all zero
 };
@@ -365,7 +364,7 @@ ns_small(const __grid_constant__ NsSmall a, const __grid_constant__ NsCall call,
   gone = __syncthreads_or(late) != 0;
   if (gone && warp == 0) {
     if (elect_one()) {  // its products may not have ended
-      atomicAdd(&g_small_faults, 1u);
+      atomicAdd(a.faults, 1u);
       mma_commit(smem_addr(&drain));
       const long long t0 = clock64();
       while (!mbar_try(smem_addr(&drain), 0) && clock64() - t0 < kWaitCycles) {
@@ -465,17 +464,12 @@ cudaError_t ns_small_launch(const wtconv_ns_desc_t& d, const NsCall& k, const Ns
   plan(d, a);
   a.p.split = poly_of(d, a.s, k.muon).split;
   a.w = waits();
+  a.faults = ns_fault_count();
+  if (!a.faults) return cudaGetLastError();
   a.s.wide = is_wide(d, k, p);
   if (d.dtype == WTCONV_F32) return launch_t<float>(a, k, p, s);
   if (d.dtype == WTCONV_F16) return launch_t<__half>(a, k, p, s);
   return launch_t<__nv_bfloat16>(a, k, p, s);
-}
-
-unsigned int ns_small_take_faults() {
-  unsigned int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_small_faults, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_small_faults, &z, sizeof(z));
-  return v;
 }
 
 }  // namespace wtb

@@ -21,6 +21,28 @@ def shape_scale(m: int, n: int, rule: str = "spectral") -> float:
     raise ValueError(f"scale rule must be spectral or rms, got {rule!r}")
 
 
+class _FaultWatch:
+    """The count of in-kernel waits that gave up on one device, copied behind every
+    step and looked at before the next one, without a wait for the GPU."""
+
+    def __init__(self, device):
+        self.device = device
+        self.count = torch.zeros(1, dtype=torch.int32, pin_memory=True)
+        self.copy()
+        torch.cuda.current_stream(device).synchronize()  # once: what others left in the count
+        self.seen = int(self.count)
+
+    def copy(self):
+        _b.wtconv_block_device_faults_async(self.count, self.device)
+
+    def check(self):
+        now, before = int(self.count), self.seen
+        self.seen = now
+        if now > before:  # it only falls when someone reads and resets it
+            raise RuntimeError("a wait inside the optimiser's kernels gave up in an earlier step on "
+                               f"{self.device}: weights of that step were left as they were")
+
+
 class Muon(torch.optim.Optimizer):
     """Momentum with orthogonalised updates, for parameters that are matrices.
 
@@ -28,6 +50,10 @@ class Muon(torch.optim.Optimizer):
     is taken as a matrix of its first axis by all the others.  Parameters of
     one shape and type take their step in one call.  Other parameters (norms,
     biases, depthwise kernels) belong to another optimiser.
+
+    The kernels' waits are bounded; where one gave up, weights were left as they
+    were, and a later ``step`` raises RuntimeError (the first one that starts
+    after the GPU got there).
     """
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
@@ -59,9 +85,13 @@ class Muon(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
+        watches = self.__dict__.setdefault("_watches", {})
+        for watch in watches.values():
+            watch.check()
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        devices = set()
         for group in self.param_groups:
             stacks = {}
             for p in group["params"]:
@@ -75,9 +105,14 @@ class Muon(torch.optim.Optimizer):
                 g = p.grad.reshape(rows, -1)
                 g = (g if g.is_contiguous() else g.contiguous()).to(p.dtype)
                 stacks.setdefault((tuple(w.shape), p.dtype, p.device), []).append((w, g, b))
-            for (shape, _, _), entries in stacks.items():
+                devices.add(p.device)
+            for (shape, _, device), entries in stacks.items():
+                if device not in watches and device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+                    watches[device] = _FaultWatch(device)
                 w, g, b = zip(*entries)
                 _b.wtconv_muon_step(w, g, b, lr=group["lr"], momentum=group["momentum"], nesterov=group["nesterov"],
                                     weight_decay=group["weight_decay"], scale=shape_scale(*shape, group["scale"]),
                                     steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
+        for device in devices & watches.keys():
+            watches[device].copy()
         return loss

@@ -64,3 +64,59 @@ def test_a_step_leaves_the_weights(ops, count, m, n, dtype):
     ops.wtconv_muon_step(good, g, gb, lr=0.1)
     assert not torch.equal(good, before) and torch.isfinite(good).all()
     assert ops.wtconv_block_device_faults() == 0
+
+
+@pytest.mark.parametrize("m,n", [(40, 60), (300, 200)])
+def test_the_optimiser_says_so_at_a_later_step(ops, m, n):
+    from memory_bound_cnn_wtconv2d_gb300.muon import Muon
+    p = torch.nn.Parameter(torch.randn(m, n, device="cuda"))
+    opt = Muon([p], lr=0.1)
+    p.grad = torch.randn(m, n, device="cuda")
+    for first in (True, False):  # the first step's faults count too
+        before = p.detach().clone()
+        held(opt.step)
+        assert torch.equal(p, before)
+        with pytest.raises(RuntimeError, match="gave up"):
+            opt.step()
+        assert torch.equal(p, before)
+        opt.step()
+        opt.step()
+        assert not torch.equal(p, before)
+        if first:
+            assert ops.wtconv_block_device_faults() > 0  # a reset between steps is no fault
+            opt.step()
+            opt.step()
+    assert ops.wtconv_block_device_faults() > 0
+
+
+def test_an_optimiser_does_not_answer_for_earlier_faults(ops):
+    from memory_bound_cnn_wtconv2d_gb300.muon import Muon
+    g = torch.randn(2, 48, 60, device="cuda")
+    held(lambda: ops.wtconv_orthogonalize(g))
+    p = torch.nn.Parameter(torch.randn(40, 60, device="cuda"))
+    opt = Muon([p], lr=0.1)
+    p.grad = torch.randn(40, 60, device="cuda")
+    for _ in range(3):
+        opt.step()
+        torch.cuda.synchronize()
+    assert ops.wtconv_block_device_faults() > 0
+
+
+def test_the_count_in_a_captured_step(ops):
+    from memory_bound_cnn_wtconv2d_gb300.muon import Muon
+    p = torch.nn.Parameter(torch.randn(40, 60, device="cuda"))
+    opt = Muon([p], lr=0.1)
+    p.grad = torch.randn(40, 60, device="cuda")
+    opt.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    before = p.detach().clone()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(p, before)
+    opt.step()
+    with pytest.raises(ValueError):
+        ops.wtconv_block_device_faults_async(torch.zeros(1, dtype=torch.int32), "cuda")
+    assert ops.wtconv_block_device_faults() == 0

@@ -165,7 +165,8 @@ _LAYOUTS = {}
 
 def _gn_layout(x, dy, num_groups, eps, activation):
     try:
-        key = (x.shape, x.stride(), x.dtype, x.device, num_groups, eps, activation,
+        # with the type: 4.0 and 4 are equal, but only one of them is taken
+        key = (x.shape, x.stride(), x.dtype, x.device, num_groups, type(num_groups), eps, activation,
                None if dy is None else (dy.shape, dy.stride(), dy.dtype, dy.device))
         lay = _LAYOUTS.get(key)
     except (AttributeError, TypeError):  # not tensors, or options no call takes: the checks say which
@@ -383,7 +384,7 @@ _NS_DESCS = {}
 
 def _ns_desc(s, count, steps, coefficients, eps):
     try:
-        key = (count, s.m, s.n, s.dtype, s.device, steps, tuple(coefficients), eps)
+        key = (count, s.m, s.n, s.dtype, s.device, steps, type(steps), tuple(coefficients), eps)
         got = _NS_DESCS.get(key)
     except TypeError:
         key = got = None

@@ -84,3 +84,25 @@ def test_a_resumed_optimiser_has_its_buffers_in_float32(dtype):
         assert b.dtype is torch.float32 and torch.equal(b, opt.state[p]["buffer"])
         assert b.data_ptr() != opt.state[p]["buffer"].data_ptr()
     assert not again.state[qs[3]]
+
+
+def refuses(call):
+    try:
+        call()
+    except ValueError:
+        return True
+    return False
+
+
+def test_refusals_do_not_depend_on_earlier_calls(monkeypatch):
+    from memory_bound_cnn_wtconv2d_gb300 import build
+    build.build()
+    monkeypatch.setattr(blockops._c, "_on_cuda", lambda t: True)
+    x = torch.zeros(2, 3, 8)
+    s = stack([torch.zeros(20, 30)])
+    s.dtype, s.device = torch.float32, torch.device("cpu")
+    layout = lambda groups: blockops._gn_layout(x, None, groups, 1e-5, "none")  # noqa: E731
+    desc = lambda steps: blockops._ns_desc(s, 1, steps, blockops.NS_COEFFICIENTS, 1e-7)  # noqa: E731
+    assert refuses(lambda: layout(4.0)) and refuses(lambda: desc(5.0))
+    assert layout(4) is layout(4) and desc(5) is desc(5)
+    assert refuses(lambda: layout(4.0)) and refuses(lambda: desc(5.0))

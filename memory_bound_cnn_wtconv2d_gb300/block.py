@@ -36,8 +36,8 @@ class WTConvBlock(torch.nn.Module):
 
 def block_optimizers(module: torch.nn.Module, lr: float = 0.02, other_lr: float = 1e-3, weight_decay: float = 0.0):
     """(Muon over the matrices of the module's linear layers, AdamW over every
-    other parameter)."""
+    other parameter).  weight_decay is that of both."""
     matrices = [m.weight for m in module.modules() if isinstance(m, torch.nn.Linear)]
     taken = {id(p) for p in matrices}
     others = [p for p in module.parameters() if id(p) not in taken]
-    return Muon(matrices, lr=lr, weight_decay=weight_decay), torch.optim.AdamW(others, lr=other_lr)
+    return Muon(matrices, lr=lr, weight_decay=weight_decay), torch.optim.AdamW(others, lr=other_lr, weight_decay=weight_decay)

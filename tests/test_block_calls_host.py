@@ -106,3 +106,10 @@ def test_refusals_do_not_depend_on_earlier_calls(monkeypatch):
     assert refuses(lambda: layout(4.0)) and refuses(lambda: desc(5.0))
     assert layout(4) is layout(4) and desc(5) is desc(5)
     assert refuses(lambda: layout(4.0)) and refuses(lambda: desc(5.0))
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.05])
+def test_the_weight_decay_asked_for_is_that_of_every_parameter(decay):
+    from memory_bound_cnn_wtconv2d_gb300.block import WTConvBlock, block_optimizers
+    for opt in block_optimizers(WTConvBlock(16, num_groups=4), weight_decay=decay):
+        assert [g["weight_decay"] for g in opt.param_groups] == [decay]

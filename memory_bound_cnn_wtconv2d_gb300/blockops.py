@@ -251,10 +251,12 @@ def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activatio
 
 
 def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, activation="none", dx=None,
-                      dweight=None, dbias=None, workspace=None, stream=None):
+                      dweight=None, dbias=None, workspace=None, stream=None, need_dweight=True, need_dbias=True):
     """Gradients of ``wtconv_gn_act_fwd``: (dx, dweight, dbias), dx contiguous in
     x's type, the parameter gradients float32 [C] (of a None weight or bias
-    too: what ones and zeros in their place would get)."""
+    too: what ones and zeros in their place would get).  Without need_dweight
+    or need_dbias None in its place; without both, the sums over the batch are
+    not made."""
     lay = _gn_layout(x, dy, num_groups, 0.0, activation)
     device, C = lay.device, lay.C
     _float32(weight, "weight", C, device)
@@ -273,16 +275,16 @@ def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, act
     with _on(device, stream):
         if dx is None:
             dx = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
-        if dweight is None:
+        if dweight is None and need_dweight:
             dweight = torch.empty(C, dtype=torch.float32, device=device)
-        if dbias is None:
+        if dbias is None and need_dbias:
             dbias = torch.empty(C, dtype=torch.float32, device=device)
         ws, n = _scratch(lay.ws, device, workspace)
         status = lib().wtconv_gn_act_bwd(
             lay.ref, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), dx.data_ptr(),
-            dweight.data_ptr(), dbias.data_ptr(), None if ws is None else ws.data_ptr(), n,
-            _stream_of(device))
+            None if dweight is None else dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+            None if ws is None else ws.data_ptr(), n, _stream_of(device))
         if status:
             _c._check(status)
     return dx, dweight, dbias

@@ -24,10 +24,10 @@ class GroupNormActFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, mean, rstd = ctx.saved_tensors
         # an upstream gradient may come broadcast (stride 0) or in another order of axes
-        dx, dw, db = _b.wtconv_gn_act_bwd(dy.contiguous().to(x.dtype), x, mean, rstd, ctx.num_groups, weight, bias,
-                                          activation=ctx.activation)
         need = ctx.needs_input_grad
-        return (dx if need[0] else None, dw if need[1] else None, db if need[2] else None, None, None, None)
+        dx, dw, db = _b.wtconv_gn_act_bwd(dy.contiguous().to(x.dtype), x, mean, rstd, ctx.num_groups, weight, bias,
+                                          activation=ctx.activation, need_dweight=need[1], need_dbias=need[2])
+        return (dx if need[0] else None, dw, db, None, None, None)
 
 
 def group_norm_act(x, num_groups, weight=None, bias=None, eps=1e-5, activation="none"):

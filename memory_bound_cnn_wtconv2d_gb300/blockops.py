@@ -212,6 +212,12 @@ def _given(t, name, like, contiguous=True):
     return t
 
 
+def _written(*tensors):
+    """Tells autograd that a call has written the caller's tensors: a graph that
+    saved one of them before must not be used any more."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activation="none", y=None, mean=None,
                       rstd=None, workspace=None, stream=None):
     """y = act(group_norm(x) * weight + bias) on channels-last x [N, ..., C].
@@ -233,6 +239,7 @@ def wtconv_gn_act_fwd(x, num_groups, weight=None, bias=None, eps=1e-5, activatio
         _float32(rstd, "rstd", lay.N * lay.G, device)
         _disjoint([("y", y), ("mean", mean), ("rstd", rstd), ("workspace", workspace)],
                   [("x", x), ("weight", weight), ("bias", bias)])
+        _written(y, mean, rstd)
     with _on(device, stream):
         if y is None:
             y = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
@@ -272,6 +279,7 @@ def wtconv_gn_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, act
         _float32(dbias, "dbias", C, device)
         _disjoint([("dx", dx), ("dweight", dweight), ("dbias", dbias), ("workspace", workspace)],
                   [("dy", dy), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight), ("bias", bias)])
+        _written(dx, dweight, dbias)
     with _on(device, stream):
         if dx is None:
             dx = torch.empty_like(x) if lay.contiguous else torch.empty(x.shape, dtype=x.dtype, device=device)
@@ -434,6 +442,8 @@ def wtconv_orthogonalize(g, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, out
                                                 None if ws is None else ws.data_ptr(), n, _stream_of(s.device))
             if status:
                 _c._check(status)
+    if not fresh:
+        _written(out)
     return out
 
 
@@ -467,6 +477,7 @@ def wtconv_muon_step(weight, grad, buffer, lr, momentum=0.95, nesterov=True, wei
                 _stream_of(w.device))
             if status:
                 _c._check(status)
+    _written(*w.tensors, *b.tensors)
     return weight
 
 

@@ -11,12 +11,14 @@ from . import blockops as _b
 
 
 class GroupNormActFunction(torch.autograd.Function):
+    """One backward, by the kernels.  No second derivative, no forward mode, no
+    vmap or torch.func: torch raises where one is asked for."""
+
     @staticmethod
     def forward(ctx, x, weight, bias, num_groups, eps, activation):
         y, mean, rstd = _b.wtconv_gn_act_fwd(x, num_groups, weight, bias, eps=eps, activation=activation)
         ctx.save_for_backward(x, weight, bias, mean, rstd)
         ctx.num_groups, ctx.activation = num_groups, activation
-        ctx.mark_non_differentiable(mean, rstd)
         return y
 
     @staticmethod

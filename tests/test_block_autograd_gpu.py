@@ -83,3 +83,49 @@ def test_given_outputs_count_as_written(ops):
     with torch.inference_mode():  # tensors without a version
         w = torch.randn(30, 40, device="cuda")
         ops.wtconv_muon_step(w, g, torch.zeros(30, 40, device="cuda"), lr=0.1)
+
+
+def test_what_the_function_does_not_have_raises(ops):
+    from memory_bound_cnn_wtconv2d_gb300.norm import group_norm_act
+    x = torch.randn(2, 5, 16, device="cuda", requires_grad=True)
+    f = lambda t: group_norm_act(t, 4, activation="silu")  # noqa: E731
+    grad, = torch.autograd.grad(f(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        grad.sum().backward()
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises(NotImplementedError):
+            f(torch.autograd.forward_ad.make_dual(x.detach(), torch.ones_like(x)))
+    for wrong in (lambda: torch.func.vmap(f)(x[None].detach()), lambda: torch.func.grad(lambda t: f(t).sum())(x.detach())):
+        with pytest.raises(RuntimeError):
+            wrong()
+
+
+def amp_block(dtype):
+    from memory_bound_cnn_wtconv2d_gb300.block import WTConvBlock
+    torch.manual_seed(0)
+    block = WTConvBlock(24, levels=2, num_groups=4, device="cuda")
+    x, t = torch.randn(3, 24, 20, 22, device="cuda"), torch.randn(3, 24, 20, 22, device="cuda")
+
+    def run(x, dtype):
+        x = x.detach().clone().requires_grad_()
+        with torch.autocast("cuda", dtype=dtype or torch.float16, enabled=dtype is not None):
+            y = block(x)
+        return (y, *torch.autograd.grad((y.float() * t).sum(), [x, *block.parameters()]))
+
+    return [n for n, _ in block.named_parameters()], run(x, None), run(x, dtype), run(x.to(dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_the_block_in_16_bits(ops, dtype):
+    # Under autocast the pointwise products run in 16 bits; with a 16-bit input the
+    # layer and the norms too.  Six roundings of 2^-11 (2^-8) on the way forward and
+    # as many back, some of them amplified by the norms (weights near 1) and by sums
+    # over 1320 pixels that partly cancel: 16 roundings are allowed.
+    names, full, mixed, low = amp_block(dtype)
+    tol = 16 * (2.0 ** -11 if dtype is torch.float16 else 2.0 ** -8)
+    assert low[0].dtype is dtype and low[1].dtype is dtype and mixed[0].dtype is torch.float32
+    for got in (mixed, low):
+        for name, a, b in zip(["y", "x", *names], got, full):
+            assert a.shape == b.shape and torch.isfinite(a).all()
+            a, b = a.detach().double(), b.detach().double()
+            assert float((a - b).norm() / b.norm()) <= tol, name

@@ -32,11 +32,21 @@ __device__ __forceinline__ float2 rcp2(float2 a) {
 
 // 1 / (1 + exp(-z)).  Below -41 the exponent is held: the result, 1e-18, is
 // far below a rounding of anything it is added to.  fminf returns the bound
-// for a NaN; callers multiply by z and get it back.
+// for a NaN; callers multiply by held2(z) and get it back.
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   const float2 t = mul2(z, splat(-1.44269504f));
   const float2 e = make_float2(exp2_approx(fminf(t.x, 60.f)), exp2_approx(fminf(t.y, 60.f)));
   return rcp2(add2(e, splat(1.f)));
+}
+
+// z for a product with sigmoid2(z): held where the exponent is, as a z of -1e38
+// (a channel masked by its bias) times 1e-18 would be far from the 0 that it
+// stands for.  A NaN stays.
+__device__ __forceinline__ float2 held2(float2 z) {
+  float2 r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(z.x), "f"(-41.5888308f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(z.y), "f"(-41.5888308f));
+  return r;
 }
 
 // Phi(z), and exp(-z^2 / 2).  erfc by the rational form 7.1.26 of Abramowitz
@@ -58,7 +68,7 @@ __device__ __forceinline__ float2 normal_cdf2(float2 z, float2& bell) {
 
 template <int ACT>
 __device__ __forceinline__ float2 act2(float2 z) {
-  if constexpr (ACT == ACT_SILU) return mul2(z, sigmoid2(z));
+  if constexpr (ACT == ACT_SILU) return mul2(held2(z), sigmoid2(z));
   if constexpr (ACT == ACT_GELU) {
     float2 bell;
     return mul2(z, normal_cdf2(z, bell));
@@ -71,7 +81,7 @@ template <int ACT>
 __device__ __forceinline__ float2 through2(float2 d, float2 z) {
   if constexpr (ACT == ACT_SILU) {
     const float2 s = sigmoid2(z);
-    return mul2(d, mul2(s, fma2(z, fma2(s, splat(-1.f), splat(1.f)), splat(1.f))));
+    return mul2(d, mul2(s, fma2(held2(z), fma2(s, splat(-1.f), splat(1.f)), splat(1.f))));
   }
   if constexpr (ACT == ACT_GELU) {
     float2 bell;

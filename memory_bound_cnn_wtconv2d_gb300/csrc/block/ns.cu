@@ -25,12 +25,21 @@
 // Types of more bits, and matrices of fewer than 16 rows, whose few roundings
 // do not average out, keep pairs for A and B too and add the products lo hi +
 // hi lo + hi hi (`split`).  The tensor core's additions truncate, some 2^-22
-// of the sum each; `split` spreads the sum over kSegments accumulators (one
-// for the small products), which the epilogue adds, to keep that below 1e-5.
-// It shows on the diagonal of A, whose sums only grow; long ones of an
-// orthogonalised stack are spread over kDeepSegments (275 x 3176 float32:
-// error 4.5e-6 -> 1.7e-6, that of float32 sums 2.0e-6; 223 -> 225 us, 4 x 2048
-// x 1024 540 -> 594; of 19 steps 1.4e-6 and 2.2e-6 without).
+// of the sum each; `split` spreads the sum over kSegments accumulators, which
+// the epilogue adds, and that of a long first product over kDeepSegments.  That
+// serves sums whose terms have either sign.  Those of A's diagonal only grow,
+// and what they lose grows with the number of columns, so they are made
+// outside (`exact`): sums of squares in float32 where X is written, added by
+// the first product's diagonal tiles while these wait for their accumulators.
+// Errors of float32 matrices without and with (that of float32 sums): 130 x
+// 32768 4.0e-5, 1.7e-6 (1.4e-6); 150 x 4000 3.5e-6, 0.5e-6 (1.3e-6); a step's
+// direction, 1024 x 2048 5.5e-6, 2.6e-6 (3.4e-6).  Not where a long first
+// product has eight accumulators and the others are as long: what those lose
+// then has the other sign (2048^2 1.2e-6, 2.2e-6 (3.6e-6)).  Eight accumulators
+// halve the width of the first product's tiles, which costs nothing where the
+// rows are long and few; a step takes them only there, an orthogonalised stack
+// always (2048^2 570 us for 518 with four, whose error is 2.6e-6; 4 x 2048 x
+// 1024 601 for 550; 4096^2 3430 for 3140).
 //
 // Layout.  Every matrix lies in the workspace as 64 x 64 sub-blocks whose 8 KB
 // are the 128-byte-swizzled image that the tensor core reads, so that an
@@ -70,19 +79,22 @@ constexpr int kThreads = 96 + kEpiThreads;  // warps 0 and 10: copies of the two
 // Sub-blocks of operands in flight, beside two epilogue buffers.  Where tiles
 // are widest and long (32 K steps, or 16 of three products each, hide an
 // epilogue without a second buffer), beside one: with a stage less the copies'
-// latency leaves the MMAs waiting (4096^2 1217 -> 1119 us, float32 3650 -> 3130,
-// 4 x 2048 x 1024 float32 569 -> 539; bfloat16 of 16 steps 283 -> 302).  A third
-// buffer for short products cost them 4 %.
+// latency leaves the MMAs waiting (4096^2 1217 -> 1119 us; float32 with four
+// accumulators in the first product 3650 -> 3130, 4 x 2048 x 1024 569 -> 539;
+// bfloat16 of 16 steps 283 -> 302).  A third buffer for short products cost
+// them 4 %.
 constexpr int kRing = 20, kRingWide = 24;
 constexpr int kStages = 6;         // at most; a stage is 2 + nb sub-blocks
 constexpr int kMaxNb = 4;          // sub-blocks across a tile
 constexpr int kSegments = 4;       // accumulators of one tile when split
 constexpr int kDeepSegments = 8;   // of the first product, 64 columns wide, over more than kDeepSteps K steps
 constexpr int kDeepSteps = 24;
+constexpr int kSqParts = 8;        // sums of squares of a row of a sub-block, at most
 constexpr int kSplitNb = 2;        // 4 segments x 128 columns: all of TMEM
 constexpr int kEpiBytes = 4 * kSub;  // 128 rows x 64 columns, hi and lo
 constexpr int kSmem = kRingWide * kSub + kEpiBytes + 1024;
 static_assert(kRing * kSub + 2 * kEpiBytes == kRingWide * kSub + kEpiBytes, "one layout for both");
+static_assert(kMaxNb * 64 == 2 * 128, "two halves of 128 rows");
 static_assert(kThreads / 32 * 64 * 65 * 4 <= kRing * kSub + 2 * kEpiBytes, "the first and last pass's tiles");
 
 static __device__ unsigned int g_ns_faults;  // of both forms
@@ -92,12 +104,13 @@ struct NsMain {
   int rb, cb, rk;            // sub-blocks: rows (even), columns, rows that hold data
   NsPoly p;
   NsWaits w;
-  int deep;                  // the first product in more accumulators
+  int deep, exact;           // the first product in more accumulators, A's diagonal from sums of squares
   int nb1, nb2, nb3, gsh;    // tile widths of the three products; log2 of the stored diagonal block
   int t1, t2, t3;            // tiles of one matrix in each product
   unsigned char *xh[2], *xl[2], *ah, *al, *bh, *bl;
   float *da, *db;            // diagonals of A and a I + B, in the images' scale
   float* lead;               // of each matrix, see shift_of
+  float* sq;                 // exact: [column sub-block][kSqParts][row] sums of X's squares
   long long xbytes, abytes;  // of one matrix
   unsigned int* sync;        // barrier count, abort flag
   const float* part;
@@ -136,7 +149,9 @@ ns_norm(const __grid_constant__ NsShape s, const __grid_constant__ NsCall k, con
 
 struct Shared {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], epi[2], drain;
-  float dcol[kMaxNb * 64];  // product 2: A's diagonal at the tile's columns
+  // A's diagonal: in product 2 at the tile's columns; in product 1, exact, two
+  // halves of it at the tile's 128 rows
+  float dcol[kMaxNb * 64];
   uint32_t tmem;
   volatile int dead;  // a wait gave up: every role leaves
 };
@@ -290,6 +305,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   int share = 1;
   while (share < 8 && a.s.count * a.rb * a.cb * share < warps) share *= 2;
   const int slice = 64 / share, lnch = 31 - __clz(slice / 8);
+  const int sq_rows = a.s.count * a.rb * 64, group = a.s.tall ? min(4, slice / 8) : 4;  // chunks of one sum of squares
   {
     const int per = a.rb * a.cb * share;
     int mat_known = -1;
@@ -316,6 +332,14 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         const int at = y * 128 + ((ch ^ (y & 7)) << 4);
         *reinterpret_cast<uint4*>(xh + at) = hi;
         *reinterpret_cast<uint4*>(xl + at) = pack8(w);
+        if (a.exact) {  // neighbouring lanes have neighbouring chunks
+          float q = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q = fmaf(v[i], v[i], q);
+          for (int o = 1; o < group; o <<= 1) q += __shfl_xor_sync(~0u, q, o);
+          if ((lane & (group - 1)) == 0)
+            a.sq[(long long)(bj * kSqParts + ch / group) * sq_rows + (mat * a.rb + bi) * 64 + y] = q;
+        }
       };
       // Reads run along the rows of the caller's matrix; a tall one is turned in shared memory.
       const int row0 = (a.s.tall ? bj : bi) * 64, col0 = (a.s.tall ? bi : bj) * 64;
@@ -501,6 +525,21 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             const int now = shift_of(lead, a.p.grow, step);
             facc *= pow2(phase == 0 ? -2 * now : shift_of(lead, a.p.grow, step + 1) - now);
           }
+          if (phase == 0 && a.exact && x.j < 2 * x.i + 2 && x.j + x.nb > 2 * x.i) {  // on the diagonal
+            const int parts = step == 0 ? 8 / group : 2;
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int q = col_half; q < parts; q += 2) {
+              const float* from = a.sq + (long long)q * sq_rows + grow;
+              const long long next = (long long)kSqParts * sq_rows;
+              int j = 0;
+#pragma unroll 2
+              for (; j + 4 <= a.cb; j += 4, from += 4 * next)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] += __ldcg(from + i * next);
+              for (; j < a.cb; ++j, from += next) t[0] += __ldcg(from);
+            }
+            sh.dcol[col_half * 128 + row] = (t[0] + t[1]) + (t[2] + t[3]);
+          }
           if (phase == 1) {
             for (int j = tid - 64; j < x.nb * 64; j += kEpiThreads)
               sh.dcol[j] = __ldcg(a.da + (x.mat * a.rb + x.j) * 64 + j);
@@ -526,6 +565,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             unsigned char* buf = gen + kRingWide * kSub - b * kEpiBytes + sub * kSub + y * 128;
             const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc * 256 + s * 64 + col_half * 32;
             const bool on_diagonal = phase < 2 && 2 * x.i + sub == x.j + s;
+            float squares = 0.f;  // of the row's half of X's sub-block
             // rolled: each tile runs this once, and unrolled it is bound by fetching instructions
 #pragma unroll 2
             for (int q = 0; q < 4; ++q) {
@@ -584,6 +624,12 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[i] = facc * fmaf(diag, u[i], v[i]);
+                if (a.exact) {  // a tree: the sum is on the way of every sub-tile
+                  float t[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) t[i] = fmaf(u[i], u[i], u[i + 4] * u[i + 4]);
+                  squares += (t[0] + t[1]) + (t[2] + t[3]);
+                }
               }
               if (on_diagonal) {  // the diagonal leaves the operand; selects, as the lanes' places differ
                 const int on = y >> 3 == ch ? y & 7 : 8;
@@ -594,7 +640,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
                   u[i] = on == i ? 0.f : u[i];
                 }
                 if (on < 8) {
-                  if (phase == 0) a.da[grow] = d;
+                  if (phase == 0) a.da[grow] = a.exact ? facc * (sh.dcol[row] + sh.dcol[128 + row]) : d;
                   else a.db[grow] = fmaf(diag, fmaf(facc, diag, a.p.cb), d) + a.p.ca * a.p.sa;
                 }
               }
@@ -614,6 +660,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               mbar_arrive(smem_addr(&sh.acc_empty[acc]));
             }
             named_sync<kEpiThreads>(1);
+            if (phase == 2 && a.exact) a.sq[(long long)((x.j + s) * kSqParts + col_half) * sq_rows + grow] = squares;
             if (leader && got) {
               const uint32_t src = ebase - b * kEpiBytes;
               bulk_store(oh + at0 + s * 2 * kSub, src, 2 * kSub);
@@ -742,7 +789,8 @@ NsMain plan(const wtconv_ns_desc_t& d, bool muon) {
   a.rk = (s.r + 63) / 64;
   a.rb = (a.rk + 1) & ~1;
   a.cb = (s.c + 63) / 64;
-  a.deep = a.p.split && !muon && a.cb > kDeepSteps;
+  a.deep = a.p.split && a.cb > kDeepSteps && (!muon || a.cb >= 4 * a.rk);
+  a.exact = a.p.split && (!a.deep || a.cb > 2 * a.rk);
   a.xbytes = (long long)a.rb * a.cb * kSub;
   a.abytes = (long long)a.rb * a.rb * kSub;
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
@@ -797,7 +845,8 @@ cudaError_t launch_t(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointer
   a.bh = w, w += aa;
   if (a.p.split) {
     a.al = w, w += aa;
-    a.bl = w;
+    a.bl = w, w += aa;
+    a.sq = (float*)w;
   }
   const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;
   // one pass of 8 elements for each thread of a small matrix, four CTAs per SM over a large stack
@@ -866,7 +915,8 @@ size_t ns_workspace(const wtconv_ns_desc_t& d) {
   if (ns_small_takes(d)) return 0;
   const NsMain a = plan(d, false);  // of the two uses the one that needs more
   const size_t x = (size_t)a.xbytes * d.count, m = (size_t)a.abytes * d.count;
-  return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.p.split ? 4 : 2) * m;
+  const size_t sq = a.p.split ? (size_t)kSqParts * a.cb * d.count * a.rb * 64 * sizeof(float) : 0;
+  return kHead + 2 * (size_t)d.count * a.rb * 256 + 4 * x + (a.p.split ? 4 : 2) * m + sq;
 }
 
 cudaError_t ns_launch(const wtconv_ns_desc_t& d, const NsCall& k, const NsPointers& p, void* ws, cudaStream_t s) {

@@ -121,3 +121,30 @@ def test_optimizer_step_on_a_tiny_gradient(ops, m, n):
     m64 = 0.05 * g.double()
     ops.wtconv_muon_step(w, g, b, lr=1.0, momentum=0.95, nesterov=False)
     assert rel(w, -ns64(m64)) <= 1e-5
+
+
+@pytest.mark.parametrize("m,n", [(150, 4000), (4000, 150), (140, 12000), (130, 32768), (32768, 130), (700, 9000)])
+def test_very_long_rows(ops, m, n):
+    # the diagonal of X X^T is a sum of n squares
+    g = random(m, n, seed=m)
+    assert rel(ops.wtconv_orthogonalize(g), ns64(g)) <= 1e-5
+    # an orthogonal matrix stays one: every step starts from the largest sums there are
+    q = ops.wtconv_orthogonalize(g, steps=20, coefficients=(1.5, -0.5, 0.0))
+    assert rel(q, ns64(g, 20, (1.5, -0.5, 0.0))) <= 1e-5
+
+
+def step64(w, g, b, lr, mu, wd, scale):
+    b = mu * b.double() + (1 - mu) * g.double()
+    return (1 - lr * wd) * w.double() - lr * scale * ns64(mu * b + (1 - mu) * g.double()), b
+
+
+@pytest.mark.parametrize("count,m,n", [(2, 1024, 2048), (1, 2048, 1024), (1, 300, 9000), (1, 9000, 300), (1, 1500, 1500),
+                                       (3, 520, 1601)])
+def test_optimizer_step_of_large_float32_matrices(ops, count, m, n):
+    # weights of 0: what comes out is the direction, to the bits of a float32 stack
+    w = torch.zeros(count, m, n, device="cuda")
+    g, b = random(count, m, n, seed=n), random(count, m, n, seed=n + 1)
+    want = [step64(w[i], g[i], b[i], 0.5, 0.9, 0.1, 1.5) for i in range(count)]
+    ops.wtconv_muon_step(w, g, b, lr=0.5, momentum=0.9, weight_decay=0.1, scale=1.5)
+    for i in range(count):
+        assert rel(w[i], want[i][0]) <= 1e-5 and rel(b[i], want[i][1]) <= 1e-6

@@ -82,12 +82,16 @@ GnPlan make_plan(const wtconv_gn_desc_t& d, int op, int align) {
     // below 64 bytes take 25.8 us where the streamed form takes 18.2 (64 x 28 x 28
     // x 192 f32, forward) and 32 where it takes 19 (64 x 32 x 32 x 128 bf16,
     // backward); at 16 MB 11.8 and 13.2.  A resident backward pays for its start
-    // and its sums with every 37 KB (256 x 14 x 14 x 384 bf16, 77 MB: 52 and 38; at
-    // 38 MB f16 with GELU 29.5 and 30.3).  Clusters only while latency counts.
+    // and its sums with every 37 KB (256 x 14 x 14 x 384 bf16, 77 MB: 48 and 26; at
+    // 38 MB f16 with GELU 29.5 and 30.3), but not as much as the streamed form for
+    // its second pass over float32 where the resident lines are 128 bytes or more
+    // (512 x 7 x 7 x 768 56 and 65, 1024 x 7 x 7 x 512 74 and 92, 400 x 14 x 14 x 256
+    // 52 and 62, but 2048 x 7 x 7 x 192 78 and 69; of 96 bytes 256 x 14 x 14 x 384 60
+    // and 55).  Clusters only while latency counts.
     const int es = d.dtype == WTCONV_F32 ? 4 : 2, line = p.ch * es;
     const long long read = (d.N * d.S * d.C * es * (op == WTCONV_OP_GN_FWD ? 1 : 2)) >> 20;
-    if (p.cluster == 1 ? read > (line < 64 ? 20 : op == WTCONV_OP_GN_BWD ? 48 : 1 << 20) : !((line >= 48 && read <= 12) || (line >= 64 && read <= 24)))
-      p.cluster = 0;
+    const long long most = line < 64 ? 20 : op == WTCONV_OP_GN_BWD && (es == 2 || line < 128) ? 48 : 1 << 20;  // MB
+    if (p.cluster == 1 ? read > most : !((line >= 48 && read <= 12) || (line >= 64 && read <= 24))) p.cluster = 0;
   }
   if (p.cluster) {
     if (op == WTCONV_OP_GN_BWD) p.ws_bytes = n * p.cluster * 2 * d.C * 4;

@@ -24,7 +24,8 @@ def ops():
 # whole samples that no CTA holds, few rows of many channels, samples just above and far above the places
 @pytest.mark.parametrize("shape,G,dtype,act", [((305, 41, 40, 24), 3, F32, "silu"), ((400, 40, 40, 48), 6, F16, "gelu"),
                                                ((1000, 7, 7, 300), 25, F32, "none"), ((700, 7, 7, 768), 32, BF16, "gelu"),
-                                               ((3000, 5, 5, 260), 4, F16, "silu"), ((310, 90, 1100), 10, BF16, "none")])
+                                               ((3000, 5, 5, 260), 4, F16, "silu"), ((310, 90, 1100), 10, BF16, "none"), ((512, 7, 7, 768), 32, F32, "gelu"),
+                                               ((400, 14, 14, 256), 32, F32, "silu")])
 def test_more_samples_than_places(ops, shape, G, dtype, act):
     x, dy, w, b = inputs(shape, dtype, seed=shape[0])
     check_forward(ops, x, G, w, b, act)

@@ -228,6 +228,7 @@ unsigned int wtconv_device_faults(void);
  * out: the kernel records the fault (see wtconv_device_faults), lets its copy
  * land and leaves early, with its outputs invalid and the device usable.
  * This exercises the give-up path of the bounded waits without a GPU fault.
+ * The matrix operators of wtconv_block.h follow the same switch.
  * enable = 0 restores normal operation. */
 void wtconv_test_copy_timeout(int enable);
 

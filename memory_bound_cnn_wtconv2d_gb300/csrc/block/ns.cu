@@ -305,7 +305,8 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
   int share = 1;
   while (share < 8 && a.s.count * a.rb * a.cb * share < warps) share *= 2;
   const int slice = 64 / share, lnch = 31 - __clz(slice / 8);
-  const int sq_rows = a.s.count * a.rb * 64, group = a.s.tall ? min(4, slice / 8) : 4;  // chunks of one sum of squares
+  const int sq_rows = a.s.count * a.rb * 64;
+  const int group = a.s.tall ? min(2, lnch) : 2;  // log2 of the chunks in one sum of squares
   {
     const int per = a.rb * a.cb * share;
     int mat_known = -1;
@@ -323,6 +324,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
       }
       unsigned char* xh = a.xh[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
       unsigned char* xl = a.xl[0] + mat * a.xbytes + at_sub(bi, bj, a.cb);
+      float* sq = a.sq + (long long)(bj * kSqParts) * sq_rows + (mat * a.rb + bi) * 64;
       auto put = [&](int y, int ch, const float (&v)[8]) {
         float w[8];
         const uint4 hi = pack8(v);
@@ -333,12 +335,11 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
         *reinterpret_cast<uint4*>(xh + at) = hi;
         *reinterpret_cast<uint4*>(xl + at) = pack8(w);
         if (a.exact) {  // neighbouring lanes have neighbouring chunks
-          float q = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q = fmaf(v[i], v[i], q);
-          for (int o = 1; o < group; o <<= 1) q += __shfl_xor_sync(~0u, q, o);
-          if ((lane & (group - 1)) == 0)
-            a.sq[(long long)(bj * kSqParts + ch / group) * sq_rows + (mat * a.rb + bi) * 64 + y] = q;
+          float q = fmaf(v[0], v[0], v[1] * v[1]) + fmaf(v[2], v[2], v[3] * v[3]);
+          q += fmaf(v[4], v[4], v[5] * v[5]) + fmaf(v[6], v[6], v[7] * v[7]);
+          if (group > 0) q += __shfl_xor_sync(~0u, q, 1);
+          if (group > 1) q += __shfl_xor_sync(~0u, q, 2);
+          if ((lane & ((1 << group) - 1)) == 0) sq[(ch >> group) * sq_rows + y] = q;
         }
       };
       // Reads run along the rows of the caller's matrix; a tall one is turned in shared memory.
@@ -519,6 +520,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             fetch(0, nth & (ebufs - 1));
           }
           const int grow = (x.mat * a.rb + 2 * x.i) * 64 + row;  // row in the diagonals
+          float* sq_to = a.sq + (long long)(x.j * kSqParts + col_half) * sq_rows + grow;
           float diag = 0.f, facc = fphase;
           if (phase != 1) {
             const float lead = __ldcg(a.lead + x.mat);
@@ -526,7 +528,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
             facc *= pow2(phase == 0 ? -2 * now : shift_of(lead, a.p.grow, step + 1) - now);
           }
           if (phase == 0 && a.exact && x.j < 2 * x.i + 2 && x.j + x.nb > 2 * x.i) {  // on the diagonal
-            const int parts = step == 0 ? 8 / group : 2;
+            const int parts = step == 0 ? 8 >> group : 2;
             float t[4] = {0.f, 0.f, 0.f, 0.f};
             for (int q = col_half; q < parts; q += 2) {
               const float* from = a.sq + (long long)q * sq_rows + grow;
@@ -660,7 +662,7 @@ ns_main(const __grid_constant__ NsMain a, const __grid_constant__ NsCall call, c
               mbar_arrive(smem_addr(&sh.acc_empty[acc]));
             }
             named_sync<kEpiThreads>(1);
-            if (phase == 2 && a.exact) a.sq[(long long)((x.j + s) * kSqParts + col_half) * sq_rows + grow] = squares;
+            if (phase == 2 && a.exact) sq_to[(long long)(s * kSqParts) * sq_rows] = squares;
             if (leader && got) {
               const uint32_t src = ebase - b * kEpiBytes;
               bulk_store(oh + at0 + s * 2 * kSub, src, 2 * kSub);

@@ -52,14 +52,16 @@
 // computed and stored, and a tile above is read from its mirror image with
 // the other operand order (MN-major), which costs nothing.
 //
-// What bounds it, on one GB300.  Large matrices (4096^2 bfloat16 1111 us, 1.24
-// PFLOP/s of the 1.92 that a large library product reaches alone): the MMAs and
-// the L2, which a CTA's operands leave at 69 bytes a cycle, at the 1.45 GHz that
-// the power limit leaves.  Stacks of middle size (9 x 1536 x 384 181 us, 2 x 333
-// x 1201 float32 158 us): 15 products one after the other, each a barrier, the
-// copies' latency, a short K loop and an epilogue, 8 to 11 us in all, while the
-// arithmetic alone is 1 us or less.  float32 stacks take three products and twice
-// the operand bytes (4 x 2048 x 1024 582 us where bfloat16 takes 286).
+// What bounds it, on one GB300.  Large matrices (4096^2 bfloat16 1130 us, 1.22
+// PFLOP/s; a large library product reaches 1.92 alone and 1.73 under the power
+// limit): the MMAs and the L2, which a CTA's operands leave at 69 bytes a
+// cycle, at the 1.45 GHz that the power limit leaves, and the last round of
+// each product (272, 272 and 512 tiles on 152 SMs: 8 rounds for 6.95).  Stacks
+// of middle size (9 x 1536 x 384 185 us, 2 x 333 x 1201 float32 166 us): 15
+// products one after the other, each a barrier, the copies' latency, a short K
+// loop and an epilogue, 11 to 12 us in all, while the arithmetic alone is 1 us
+// or less.  float32 stacks take three products and twice the operand bytes (4 x
+// 2048 x 1024 604 us where bfloat16 takes 288).
 #include "ns_common.cuh"
 
 namespace wtb {

@@ -10,7 +10,7 @@
 // launch, no workspace; number formats as in the general form.
 //
 // Bound by latency: five steps of three dependent products and an exchange, 8 us
-// a step (3 x 384 x 96 bfloat16 48 us, in the general form 85; 1 x 64 x 256 29 us).
+// a step (3 x 384 x 96 bfloat16 49 us, in the general form 87; 1 x 64 x 256 30 us).
 #include "ns_common.cuh"
 
 namespace wtb {

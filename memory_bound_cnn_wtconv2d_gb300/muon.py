@@ -39,8 +39,8 @@ class _FaultWatch:
         now, before = int(self.count), self.seen
         self.seen = now
         if now > before:  # it only falls when someone reads and resets it
-            raise RuntimeError("a wait inside the optimiser's kernels gave up in an earlier step on "
-                               f"{self.device}: weights of that step were left as they were")
+            raise RuntimeError(f"a wait inside the matrix kernels on {self.device} gave up since the last step: weights of "
+                               "an earlier step, of this optimiser or of another, were left as they were")
 
 
 class Muon(torch.optim.Optimizer):

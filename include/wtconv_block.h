@@ -61,7 +61,8 @@ size_t wtconv_gn_workspace_size(const wtconv_gn_desc_t* desc, int op);
  * (ones, zeros).  Statistics are accumulated in float32 around pivots taken
  * from the data, so a mean far from zero costs few digits (rstd 6e-6 of its
  * value where the mean is 4096 deviations; y as much as rounding the mean to
- * float32 does).  N = 0 or S = 0: nothing is computed (mean and rstd are written as 0 when S = 0).
+ * float32 does).  N = 0 or S = 0: nothing is computed (mean and rstd are
+ * written as 0 when S = 0).
  * Limits: C <= 8192; N <= 65535; S < 2^31. */
 wtconv_status_t wtconv_gn_act_fwd(const wtconv_gn_desc_t* desc, const void* x, const float* weight,
                                   const float* bias, void* y, float* mean, float* rstd, void* ws,

@@ -1,46 +1,13 @@
 // C entry points of include/wtconv_block.h: argument checks, then the launches.
 #include <cuda_runtime.h>
 #include <math.h>
-#include <stdarg.h>
-#include <stdint.h>
-#include <stdio.h>
 
+#include "api_checks.h"
 #include "block_launch.h"
-#include "../wtconv_launch.h"
+
+using namespace wtb::api;
 
 namespace {
-
-wtconv_status_t fail(wtconv_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-wtconv_status_t fail(wtconv_status_t st, const char* fmt, ...) {
-  char msg[400];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(msg, sizeof(msg), fmt, ap);
-  va_end(ap);
-  wt::set_last_error(msg);
-  return st;
-}
-
-int esize(int dtype) { return dtype == WTCONV_F32 ? 4 : 2; }
-
-wtconv_status_t pointer(const void* p, const char* name, int align, bool nullable = false) {
-  if (!p) return nullable ? WTCONV_OK : fail(WTCONV_ERR_INVALID_ARG, "%s is NULL", name);
-  if ((uintptr_t)p % align) return fail(WTCONV_ERR_MISALIGNED, "%s is not %d-byte aligned", name, align);
-  return WTCONV_OK;
-}
-
-wtconv_status_t workspace(const void* ws, size_t given, size_t need) {
-  if (need == 0) return WTCONV_OK;
-  if (!ws || given < need) return fail(WTCONV_ERR_WORKSPACE, "workspace of %zu B given, %zu B needed", ws ? given : 0, need);
-  if ((uintptr_t)ws % 256) return fail(WTCONV_ERR_MISALIGNED, "workspace is not 256-byte aligned");
-  return WTCONV_OK;
-}
-
-#define TRY(e)                                       \
-  do {                                               \
-    const wtconv_status_t st_ = (e);                 \
-    if (st_ != WTCONV_OK) return st_;                \
-  } while (0)
 
 wtconv_status_t strides(const char* name, long long sample, long long row, const wtconv_gn_desc_t* d) {
   if (d->N < 1 || d->S < 1) return WTCONV_OK;
@@ -65,18 +32,6 @@ wtconv_status_t check_gn(const wtconv_gn_desc_t* d, int op) {
   TRY(strides("x", d->x_sample_stride, d->x_row_stride, d));
   if (op == WTCONV_OP_GN_BWD) TRY(strides("dy", d->dy_sample_stride, d->dy_row_stride, d));
   return WTCONV_OK;
-}
-
-// Elements of the widest access (at most 16 bytes) that an address and its
-// strides allow.
-int widest(int es, const void* p, long long sample, long long row, long long n, long long s) {
-  int v = 16 / es;
-  while (v > 1 && ((uintptr_t)p % (v * es) || (s > 1 && row % v) || (n > 1 && sample % v))) v >>= 1;
-  return v;
-}
-
-wtconv_status_t cuda_status(cudaError_t e, const char* name) {
-  return e == cudaSuccess ? WTCONV_OK : fail(WTCONV_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 
 wtconv_status_t check_ns(const wtconv_ns_desc_t* d) {

@@ -1,0 +1,42 @@
+// Internal launchers of the gated channel mixer's operators (host side).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "../../../include/wtconv_mixer.h"
+
+namespace wtb {
+
+// Root-mean-square norm.  `vec` is the number of elements of the widest access
+// that every pointer, stride and C allow (16 bytes at most).
+struct RmsArgs {
+  const void *x, *r, *dy;  // backward: x is t, r is what reaches t by itself
+  const float* weight;
+  void* y;                 // backward: dx
+  unsigned char* q;
+  void* total;
+  float* rstd;             // 8-bit output: the scales
+  float* dweight;
+};
+enum RmsOp { RMS_FWD, RMS_Q8, RMS_QUANTIZE };
+cudaError_t rms_launch(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, int vec, cudaStream_t s);
+size_t rms_bwd_workspace(const wtconv_rms_desc_t& d);
+cudaError_t rms_bwd_launch(const wtconv_rms_desc_t& d, const RmsArgs& a, int vec, void* ws, cudaStream_t s);
+
+// Gated product.
+struct GatedArgs {
+  const void *x, *gate, *up, *dh;
+  const float *x_scale, *gate_scale, *up_scale;  // 8-bit operands
+  void *h, *dx, *dgate, *dup;
+};
+size_t gated_workspace(const wtconv_gated_desc_t& d, int op);
+cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& a, bool q8, void* ws, cudaStream_t s);
+cudaError_t gated_launch_bwd(const wtconv_gated_desc_t& d, const GatedArgs& a, void* ws, cudaStream_t s);
+
+// Gradient norm.
+size_t clip_workspace(int count);
+cudaError_t clip_launch(const wtconv_tensor_t* t, int count, bool clip, float max_norm, float eps, float* norm, void* ws,
+                        cudaStream_t s);
+
+}  // namespace wtb

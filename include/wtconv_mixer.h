@@ -88,13 +88,17 @@ typedef struct {
   int act;   /* wtconv_act_t */
   long long x_stride, gate_stride, up_stride;
   long long dh_stride; /* read by the backward only */
+  int align; /* bytes that the addresses of x, gate and up are all multiples
+                of, as far as the caller knows (0: nothing known).  From 16 on,
+                with strides that are multiples of 16 bytes too, 16-bit
+                operands are read where they lie; others are copied to the
+                workspace first */
 } wtconv_gated_desc_t;
 
 typedef enum { WTCONV_OP_GATED_FWD = 0, WTCONV_OP_GATED_BWD = 1, WTCONV_OP_GATED_Q8 = 2 } wtconv_gated_op_t;
 
-/* Bytes of device workspace (256-byte aligned) of `op` (wtconv_gated_op_t)
- * whatever the pointers' alignment; 0 for an invalid desc, and where none is
- * needed. */
+/* Bytes of device workspace (256-byte aligned) of `op` (wtconv_gated_op_t); 0
+ * for an invalid desc, and where none is needed. */
 size_t wtconv_gated_workspace_size(const wtconv_gated_desc_t* desc, int op);
 
 /* h = act(x gate^T) * (x up^T).  Products of 16-bit operands are exact and

@@ -1,147 +1,434 @@
-// Gated product h = act(x Wg^T) * (x Wu^T) and its gradients, in their plainest
-// form: 16 x 16 threads make a tile of 32 x 32 outputs from tiles in shared
-// memory, in float32.
-#include <cuda_fp8.h>
+// Gated product h = act(x Wg^T) * (x Wu^T) and its gradients: plans and launches
+// of the products in gated_kernels.cuh, and the small kernels around them.
+//
+// The backward keeps nothing of the forward but x: g and u are made again (4 M H
+// C operations of 12 in all), which costs less than writing and reading them
+// where C is below about 560, and no memory.  Three products: P = [dg du] with
+// its epilogue, dx = P [Wg; Wu], dW = P^T x.
+#include "gated_kernels.cuh"
 
-#include "block_device.cuh"
-#include "gn_math.cuh"
-#include "mixer_launch.h"
+#include "block_launch.h"
+#include "../wtconv_launch.h"
 
 namespace wtb {
 namespace {
 
-constexpr int kTile = 32;
+using namespace gated;
 
-__device__ __forceinline__ float value(const __nv_fp8_e4m3* p) { return (float)*p; }
-__device__ __forceinline__ float value(const float* p) { return *p; }
-__device__ __forceinline__ float value(const __half* p) { return to_float(*p); }
-__device__ __forceinline__ float value(const __nv_bfloat16* p) { return to_float(*p); }
+constexpr long long round_up(long long v, long long to) { return (v + to - 1) / to * to; }
+constexpr size_t bytes_up(size_t v) { return (v + 255) / 256 * 256; }
 
-// acc += A B over k of a tile: A(m, k) at a + m * am + k * ak, B(n, k) alike.
-template <typename TA, typename TB>
-__device__ __forceinline__ void product(const TA* a, long long am, long long ak, long long m0, long long M, const TB* b,
-                                        long long bn, long long bk, long long n0, long long N, long long K,
-                                        float (&acc)[2][2]) {
-  __shared__ float sa[kTile][kTile + 1], sb[kTile][kTile + 1];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  for (long long k0 = 0; k0 < K; k0 += kTile) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * kTile; i += 256) {
-      const int r = i / kTile, k = i % kTile;
-      sa[r][k] = m0 + r < M && k0 + k < K ? value(a + (m0 + r) * am + (k0 + k) * ak) : 0.f;
-      sb[r][k] = n0 + r < N && k0 + k < K ? value(b + (n0 + r) * bn + (k0 + k) * bk) : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < kTile; ++k)
+// ---- operands copied to the workspace: as they are, or in three parts --------
+
+struct PackOne {
+  const void* from;
+  void* to;
+  long long rows, ld, part;  // elements from one part to the next
+  int cols, pitch;
+};
+struct PackArgs {
+  PackOne t[3];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) gated_pack(const __grid_constant__ PackArgs a) {
+  const PackOne& p = a.t[blockIdx.y];
+  const int across = p.pitch / 8;
+  const long long total = p.rows * across;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const long long row = i / across;
+    const int col = (int)(i - row * across) * 8;
+    const T* from = (const T*)p.from + row * p.ld + col;
+    T v[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 8; ++j) v[j] = col + j < p.cols ? from[j] : round_to<T>(0.f);
+    if constexpr (sizeof(T) == 2) {
+      Vec<T, 8> o;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = fmaf(sa[ty + 16 * i][k], sb[tx + 16 * j][k], acc[i][j]);
-  }
-}
-
-__device__ __forceinline__ float act_of(int act, float z) {
-  const float2 v = make_float2(z, 0.f);
-  return act == ACT_SILU ? gn::act2<ACT_SILU>(v).x : act == ACT_GELU ? gn::act2<ACT_GELU>(v).x : z;
-}
-__device__ __forceinline__ float through(int act, float d, float z) {
-  const float2 v = make_float2(z, 0.f), e = make_float2(d, 0.f);
-  return act == ACT_SILU ? gn::through2<ACT_SILU>(e, v).x : act == ACT_GELU ? gn::through2<ACT_GELU>(e, v).x : d;
-}
-
-// BWD: dg and du into `g`, `u` (float32); otherwise h.
-template <typename TI, typename T, bool BWD>
-__global__ void __launch_bounds__(256)
-gated_tile(const __grid_constant__ wtconv_gated_desc_t d, const __grid_constant__ GatedArgs a, float* g, float* u) {
-  const long long tiles = (d.H + kTile - 1) / kTile;
-  const long long m0 = blockIdx.x / tiles * kTile, n0 = blockIdx.x % tiles * kTile;
-  float ag[2][2] = {}, au[2][2] = {};
-  product((const TI*)a.x, d.x_stride, 1, m0, d.M, (const TI*)a.gate, d.gate_stride, 1, n0, d.H, d.C, ag);
-  product((const TI*)a.x, d.x_stride, 1, m0, d.M, (const TI*)a.up, d.up_stride, 1, n0, d.H, d.C, au);
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) {
-      const long long m = m0 + threadIdx.x / 16 + 16 * i, n = n0 + threadIdx.x % 16 + 16 * j;
-      if (m >= d.M || n >= d.H) continue;
-      float vg = ag[i][j], vu = au[i][j];
-      if (a.x_scale) vg *= a.x_scale[m] * a.gate_scale[n], vu *= a.x_scale[m] * a.up_scale[n];
-      const float act = act_of(d.act, vg);
-      if constexpr (BWD) {
-        const float dh = to_float(((const T*)a.dh)[m * d.dh_stride + n]);
-        g[m * d.H + n] = through(d.act, dh * vu, vg);
-        u[m * d.H + n] = dh * act;
-      } else {
-        ((T*)a.h)[m * d.H + n] = round_to<T>(act * vu);
+      for (int j = 0; j < 8; ++j) o.e[j] = v[j];
+      o.store((T*)p.to + row * p.pitch + col);
+    } else {
+      for (int part = 0; part < 3; ++part) {
+        Vec<__nv_bfloat16, 8> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.e[j] = take_part(v[j]);
+        o.store((__nv_bfloat16*)p.to + part * p.part + row * p.pitch + col);
       }
     }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-gated_dx(const __grid_constant__ wtconv_gated_desc_t d, const __grid_constant__ GatedArgs a, const float* g, const float* u) {
-  const long long tiles = (d.C + kTile - 1) / kTile;
-  const long long m0 = blockIdx.x / tiles * kTile, n0 = blockIdx.x % tiles * kTile;
-  float acc[2][2] = {};
-  product(g, d.H, 1, m0, d.M, (const T*)a.gate, 1, d.gate_stride, n0, d.C, d.H, acc);
-  product(u, d.H, 1, m0, d.M, (const T*)a.up, 1, d.up_stride, n0, d.C, d.H, acc);
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) {
-      const long long m = m0 + threadIdx.x / 16 + 16 * i, n = n0 + threadIdx.x % 16 + 16 * j;
-      if (m < d.M && n < d.C) ((T*)a.dx)[m * d.C + n] = round_to<T>(acc[i][j]);
-    }
-}
-template <typename T>
-__global__ void __launch_bounds__(256)
-gated_dw(const __grid_constant__ wtconv_gated_desc_t d, const __grid_constant__ GatedArgs a, const float* p, T* out) {
-  const long long tiles = (d.C + kTile - 1) / kTile;
-  const long long m0 = blockIdx.x / tiles * kTile, n0 = blockIdx.x % tiles * kTile;
-  float acc[2][2] = {};
-  product(p, 1, d.H, m0, d.H, (const T*)a.x, 1, d.x_stride, n0, d.C, d.M, acc);
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) {
-      const long long m = m0 + threadIdx.x / 16 + 16 * i, n = n0 + threadIdx.x % 16 + 16 * j;
-      if (m < d.H && n < d.C) out[m * d.C + n] = round_to<T>(acc[i][j]);
-    }
-}
-
-unsigned int tiles_of(long long m, long long n) { return (unsigned int)((m + kTile - 1) / kTile * ((n + kTile - 1) / kTile)); }
-
-template <typename T>
-cudaError_t backward(const wtconv_gated_desc_t& d, const GatedArgs& a, float* ws, cudaStream_t s) {
-  float *g = ws, *u = ws + d.M * d.H;
-  gated_tile<T, T, true><<<tiles_of(d.M, d.H), 256, 0, s>>>(d, a, g, u);
-  if (a.dx) gated_dx<T><<<tiles_of(d.M, d.C), 256, 0, s>>>(d, a, g, u);
-  if (a.dgate) {
-    gated_dw<T><<<tiles_of(d.H, d.C), 256, 0, s>>>(d, a, g, (T*)a.dgate);
-    gated_dw<T><<<tiles_of(d.H, d.C), 256, 0, s>>>(d, a, u, (T*)a.dup);
   }
+}
+
+// ---- sums over the splits of a product, in order --------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+gated_sum(const float* part, int splits, long long part_rows, long long ld, long long rows, int cols, long long second,
+          long long second_at, T* out, T* out2) {
+  const int across = (cols + 3) / 4;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < rows * across; i += gridDim.x * 256ll) {
+    const long long row = i / across;
+    const int col = (int)(i - row * across) * 4;
+    // rows from `second` on are of the second matrix, whose sums begin at row second_at
+    const float* p = part + (row < second ? row : row - second + second_at) * ld + col;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + k * part_rows * ld));
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    T* o = (row < second ? out + row * cols : out2 + (row - second) * cols) + col;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < cols) o[j] = round_to<T>(v[j]);
+  }
+}
+
+// ---- plans -----------------------------------------------------------------------
+
+struct Operand {
+  const void* p;
+  long long ld;    // elements
+  long long part;  // elements from one part to the next
+};
+
+// A product's tiles and its split of k.
+struct Tiles {
+  int n;       // columns of an accumulator (FWD: gate and up)
+  int tiles_n, splits, kblocks;  // k blocks of a split
+  int stages;
+};
+
+// Time of a product in clocks, in round numbers: a k block takes its MMAs (a
+// column each 2 clocks at 64 k) or its bytes at 48 a clock, a tile 1500 until
+// the first operands are there, and its epilogue runs beside the next tile's
+// products, except for the last one's.
+double clocks(long long items, int sms, double iters, int n, double epilogue) {
+  const double mma = 2.0 * n, load = (kABytes + n * 128) / 48.0;
+  const double tile = iters * (mma > load ? mma : load);
+  const double rounds = (double)((items + sms - 1) / sms);
+  return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
+}
+
+int stages_of(int n) {
+  const int s = kRing / (kABytes + n * 128);
+  return s < kMaxStages ? s : kMaxStages;
+}
+
+Tiles plan_forward(long long M, int C, int H, int products, bool q8, bool grad, int sms) {
+  const int kb = q8 ? 128 : 64;
+  Tiles best = {};
+  double least = 0;
+  for (int half = 32; half <= 128; half += 32) {
+    const int tn = (H + half - 1) / half;
+    const double iters = (double)((C + kb - 1) / kb) * products;
+    const double epi = (half + 63) / 64 * (grad ? 2400. : 1200.);
+    const double t = clocks((M + kRows - 1) / kRows * tn, sms, iters, 2 * half, epi);
+    if (!best.n || t <= least) {
+      least = t;
+      best.n = 2 * half;
+      best.tiles_n = tn;
+      best.splits = 1;
+      best.kblocks = (C + kb - 1) / kb;
+      best.stages = stages_of(2 * half);
+    }
+  }
+  return best;
+}
+
+// Sums alone: `tiles_m` row tiles of N columns over k blocks; few tiles share out
+// k, at least four blocks each, and a second launch adds their sums up.
+Tiles plan_sums(long long tiles_m, int N, long long kblocks, int products, int sms) {
+  Tiles best = {};
+  double least = 0;
+  for (int n = 64; n <= kMaxN; n += 64) {
+    const int tn = (N + n - 1) / n;
+    if (n > 64 && n - 64 >= N) break;
+    for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
+      const long long each = (kblocks + want - 1) / want;
+      if (want > 1 && each < 4) break;
+      const int splits = (int)((kblocks + each - 1) / each);
+      double t = clocks(tiles_m * tn * splits, sms, (double)each * products, n, (n + 63) / 64 * 800.);
+      if (splits > 1)  // written and read at about 2500 bytes a clock, and a launch
+        t += 4000 + 8.0 * splits * tiles_m * kRows * N / 2500;
+      if (!best.n || t < least) {
+        least = t;
+        best.n = n;
+        best.tiles_n = tn;
+        best.splits = splits;
+        best.kblocks = (int)each;
+        best.stages = stages_of(n);
+      }
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int parts, products, Hp;
+  bool copy_x, copy_w;        // operands that are copied to the workspace
+  int pitch;                  // of copied rows
+  long long rows;             // M
+  Tiles fwd, dx, dw;
+  size_t x_at, gate_at, up_at, p_at, sum_at, bytes;
+  long long p_part;
+};
+
+Plan plan_of(const wtconv_gated_desc_t& d, int op) {
+  Plan p = {};
+  const int sms = wt::sm_count();
+  const bool f32 = d.dtype == WTCONV_F32 && op != WTCONV_OP_GATED_Q8;
+  p.parts = f32 ? 3 : 1;
+  p.products = f32 ? 6 : 1;
+  p.pitch = (int)round_up(d.C, 8);
+  if (op != WTCONV_OP_GATED_Q8) {
+    const bool at16 = d.align >= 16;
+    p.copy_x = f32 || !at16 || (d.M > 1 && d.x_stride % 8);
+    p.copy_w = f32 || !at16 || (d.H > 1 && (d.gate_stride % 8 || d.up_stride % 8));
+  }
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += bytes_up(bytes);
+    return here;
+  };
+  if (p.copy_x) p.x_at = take((size_t)p.parts * d.M * p.pitch * 2);
+  if (p.copy_w) {
+    p.gate_at = take((size_t)p.parts * d.H * p.pitch * 2);
+    p.up_at = take((size_t)p.parts * d.H * p.pitch * 2);
+  }
+  const bool grad = op == WTCONV_OP_GATED_BWD;
+  p.fwd = plan_forward(d.M, d.C, d.H, p.products, op == WTCONV_OP_GATED_Q8, grad, sms);
+  if (grad) {
+    p.Hp = (int)round_up(d.H, 64);
+    p.p_part = d.M * 2 * p.Hp;
+    p.p_at = take((size_t)p.parts * p.p_part * 2);
+    const long long tm = (d.M + kRows - 1) / kRows, th = 2 * ((d.H + kRows - 1) / kRows);
+    p.dx = plan_sums(tm, d.C, 2 * (p.Hp / 64), p.products, sms);
+    p.dw = plan_sums(th, d.C, (d.M + 63) / 64, p.products, sms);
+    size_t sums = 0;
+    const size_t ld = round_up(d.C, 4);
+    if (p.dx.splits > 1) sums = (size_t)p.dx.splits * tm * kRows * ld * 4;
+    if (p.dw.splits > 1 && (size_t)p.dw.splits * th * kRows * ld * 4 > sums) sums = (size_t)p.dw.splits * th * kRows * ld * 4;
+    p.sum_at = take(sums);
+  }
+  p.bytes = at;
+  return p;
+}
+
+// ---- launches --------------------------------------------------------------------
+
+#define RET(e)                               \
+  do {                                       \
+    const cudaError_t e_ = (e);              \
+    if (e_ != cudaSuccess) return e_;        \
+  } while (0)
+
+// columns x halves x rows x parts; boxes of 128 bytes x `box_rows`
+cudaError_t make_map(CUtensorMap* m, int type, const void* p, long long cols, int halves, long long half_ld, long long rows,
+                     long long ld, int parts, long long part_ld, int box_rows) {
+  wt::EncodeTiledFn fn = wt::encode_tiled();
+  if (!fn) return cudaErrorNotSupported;
+  const int es = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
+  if (halves == 1) half_ld = ld;
+  if (rows == 1) ld = round_up(cols, 16 / es);
+  if (parts == 1) part_ld = ld;
+  const cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)halves, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t strides[3] = {(cuuint64_t)((halves == 1 ? ld : half_ld) * es), (cuuint64_t)(ld * es), (cuuint64_t)(part_ld * es)};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1u, (cuuint32_t)box_rows, 1u};
+  const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+  return fn(m, (CUtensorMapDataType)type, 4, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int EPI, typename T, bool Q8>
+cudaError_t launch_gemm(GemmArgs& a, cudaStream_t s) {
+  const bool hook = wt::wait_hook_on();
+  a.wait = hook ? 1ll << 20 : kWaitCycles;
+  a.hold = hook;
+  a.faults = ns_fault_count();
+  if (!a.faults) return cudaGetLastError();
+  const void* f = (const void*)gated_gemm<EPI, T, Q8>;
+  RET(wt::ensure_smem(f, kSmem));
+  const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
+  const int sms = wt::sm_count();
+  gated_gemm<EPI, T, Q8><<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, s>>>(a);
   return cudaGetLastError();
+}
+
+// What all products of a call share.
+struct Call {
+  const wtconv_gated_desc_t& d;
+  Plan p;
+  Operand x, gate, up;
+  int type;      // of the operands' elements
+  uint32_t kind; // bits of the instruction descriptor
+  unsigned char* ws;
+  cudaStream_t s;
+};
+
+void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_along, bool b_along) {
+  a.tiles_m = tiles_m;
+  a.tiles_n = t.tiles_n;
+  a.splits = t.splits;
+  a.group = 16;
+  a.n = t.n;
+  a.kblocks = t.kblocks;
+  a.parts = c.p.parts;
+  a.stages = t.stages;
+  a.b_bytes = t.n * 128;
+  a.idesc = instr_desc(t.n, a_along, b_along) | c.kind;
+  a.act = c.d.act;
+  a.M = c.d.M;
+  a.H = c.d.H;
+  a.Hp = c.p.Hp;
+  a.p_part = c.p.p_part;
+  a.p = c.ws + c.p.p_at;
+}
+
+template <typename T>
+cudaError_t pack(Call& c, const GatedArgs& g) {
+  const wtconv_gated_desc_t& d = c.d;
+  PackArgs a = {};
+  int n = 0;
+  long long most = 0;
+  auto add = [&](const void* from, size_t at, long long rows, long long ld, Operand& o) {
+    PackOne& t = a.t[n++];
+    t.from = from;
+    t.to = c.ws + at;
+    t.rows = rows;
+    t.ld = ld;
+    t.cols = d.C;
+    t.pitch = c.p.pitch;
+    t.part = rows * c.p.pitch;
+    o = {t.to, t.pitch, t.part};
+    if (rows > most) most = rows;
+  };
+  if (c.p.copy_x) add(g.x, c.p.x_at, d.M, d.x_stride, c.x);
+  if (c.p.copy_w) {
+    add(g.gate, c.p.gate_at, d.H, d.gate_stride, c.gate);
+    add(g.up, c.p.up_at, d.H, d.up_stride, c.up);
+  }
+  if (!n) return cudaSuccess;
+  const long long blocks = (most * (c.p.pitch / 8) + 255) / 256, limit = 16ll * wt::sm_count();
+  gated_pack<T><<<dim3((unsigned)(blocks < limit ? blocks : limit), n), 256, 0, c.s>>>(a);
+  return cudaGetLastError();
+}
+
+bool at16(const void* p, long long ld, int es) { return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0; }
+
+template <int EPI, typename T, bool Q8>
+cudaError_t product_forward(const Call& c, const GatedArgs& g) {
+  const wtconv_gated_desc_t& d = c.d;
+  GemmArgs a = {};
+  set_tiles(a, c, c.p.fwd, (int)((d.M + kRows - 1) / kRows), true, true);
+  a.load = LOAD_FWD;
+  a.half = a.n / 2;
+  a.k = d.C;
+  a.out = g.h;
+  a.ld = d.H;
+  a.dh = g.dh;
+  a.dh_ld = d.dh_stride;
+  const int each = 16 / (int)sizeof(T);
+  a.vec = (g.h && at16(g.h, d.H, sizeof(T)) ? 1 : 0) |
+          (g.dh && d.H % each == 0 && (uintptr_t)g.dh % 16 == 0 && (d.M == 1 || d.dh_stride % each == 0) ? 2 : 0);
+  a.x_scale = g.x_scale;
+  a.gate_scale = g.gate_scale;
+  a.up_scale = g.up_scale;
+  RET(make_map(&a.a, c.type, c.x.p, d.C, 1, 0, d.M, c.x.ld, c.p.parts, c.x.part, kRows));
+  RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, a.half));
+  RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, a.half));
+  return launch_gemm<EPI, T, Q8>(a, c.s);
+}
+
+template <typename T>
+cudaError_t sum_up(const Call& c, const GemmArgs& a, long long rows, long long second, long long second_at) {
+  const long long n = (rows * ((c.d.C + 3) / 4) + 255) / 256, limit = 8ll * wt::sm_count();
+  gated_sum<T><<<(unsigned)(n < limit ? n : limit), 256, 0, c.s>>>(a.partial, a.splits, a.partial_rows, a.ld, rows, c.d.C, second,
+                                                                 second_at, (T*)a.out, (T*)a.out2);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
+  const wtconv_gated_desc_t& d = c.d;
+  GemmArgs a = {};
+  const int tiles = dw ? (d.H + kRows - 1) / kRows : (int)((d.M + kRows - 1) / kRows);
+  const Tiles& t = dw ? c.p.dw : c.p.dx;
+  set_tiles(a, c, t, dw ? 2 * tiles : tiles, !dw, false);
+  a.load = dw ? LOAD_DW : LOAD_DX;
+  a.khalf = dw ? (int)((d.M + 63) / 64) : c.p.Hp / 64;
+  a.k = dw ? (int)d.M : d.H;
+  a.N = d.C;
+  a.out = dw ? g.dgate : g.dx;
+  a.out2 = g.dup;
+  a.ld = d.C;
+  a.vec = at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)));
+  if (t.splits > 1) {
+    a.partial = (float*)(c.ws + c.p.sum_at);
+    a.partial_rows = (long long)a.tiles_m * kRows;
+    a.ld = round_up(d.C, 4);
+  }
+  RET(make_map(&a.a, c.type, a.p, d.H, 2, c.p.Hp, d.M, 2ll * c.p.Hp, c.p.parts, c.p.p_part, dw ? 64 : kRows));
+  if (dw) {
+    RET(make_map(&a.b0, c.type, c.x.p, d.C, 1, 0, d.M, c.x.ld, c.p.parts, c.x.part, 64));
+  } else {
+    RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, 64));
+    RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, 64));
+  }
+  RET((launch_gemm<EPI_OUT, T, false>(a, c.s)));
+  if (t.splits == 1) return cudaSuccess;
+  return dw ? sum_up<T>(c, a, 2ll * d.H, d.H, (long long)tiles * kRows) : sum_up<T>(c, a, d.M, d.M, 0);
+}
+
+Call call_of(const wtconv_gated_desc_t& d, const GatedArgs& g, int op, void* ws, cudaStream_t s) {
+  Call c = {d, plan_of(d, op), {g.x, d.x_stride, 0}, {g.gate, d.gate_stride, 0}, {g.up, d.up_stride, 0}, 0, 0,
+            (unsigned char*)ws, s};
+  if (op == WTCONV_OP_GATED_Q8) {
+    c.type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  } else if (d.dtype == WTCONV_F16) {
+    c.type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  } else {
+    c.type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    c.kind = (1u << 7) | (1u << 10);
+  }
+  return c;
+}
+
+template <typename T>
+cudaError_t forward(Call& c, const GatedArgs& g, bool q8) {
+  if (q8) return product_forward<EPI_H, T, true>(c, g);
+  RET(pack<T>(c, g));
+  return product_forward<EPI_H, T, false>(c, g);
+}
+
+template <typename T>
+cudaError_t backward(Call& c, const GatedArgs& g) {
+  RET(pack<T>(c, g));
+  RET((product_forward<EPI_P, T, false>(c, g)));
+  if (g.dx) RET(product_sums<T>(c, g, false));
+  if (g.dgate) RET(product_sums<T>(c, g, true));
+  return cudaSuccess;
 }
 
 }  // namespace
 
-size_t gated_workspace(const wtconv_gated_desc_t& d, int op) {
-  return op == WTCONV_OP_GATED_BWD ? ((size_t)d.M * d.H * 8 + 255) / 256 * 256 : 0;
+size_t gated_workspace(const wtconv_gated_desc_t& d, int op) { return plan_of(d, op).bytes; }
+
+cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& g, bool q8, void* ws, cudaStream_t s) {
+  Call c = call_of(d, g, q8 ? WTCONV_OP_GATED_Q8 : WTCONV_OP_GATED_FWD, ws, s);
+  if (d.dtype == WTCONV_F32) return forward<float>(c, g, q8);
+  if (d.dtype == WTCONV_F16) return forward<__half>(c, g, q8);
+  return forward<__nv_bfloat16>(c, g, q8);
 }
 
-cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& a, bool q8, void*, cudaStream_t s) {
-  const unsigned int n = tiles_of(d.M, d.H);
-  typedef __nv_fp8_e4m3 Q;
-  if (q8) {
-    if (d.dtype == WTCONV_F32) gated_tile<Q, float, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-    else if (d.dtype == WTCONV_F16) gated_tile<Q, __half, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-    else gated_tile<Q, __nv_bfloat16, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-  } else {
-    if (d.dtype == WTCONV_F32) gated_tile<float, float, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-    else if (d.dtype == WTCONV_F16) gated_tile<__half, __half, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-    else gated_tile<__nv_bfloat16, __nv_bfloat16, false><<<n, 256, 0, s>>>(d, a, nullptr, nullptr);
-  }
-  return cudaGetLastError();
-}
-
-cudaError_t gated_launch_bwd(const wtconv_gated_desc_t& d, const GatedArgs& a, void* ws, cudaStream_t s) {
-  if (d.dtype == WTCONV_F32) return backward<float>(d, a, (float*)ws, s);
-  if (d.dtype == WTCONV_F16) return backward<__half>(d, a, (float*)ws, s);
-  return backward<__nv_bfloat16>(d, a, (float*)ws, s);
+cudaError_t gated_launch_bwd(const wtconv_gated_desc_t& d, const GatedArgs& g, void* ws, cudaStream_t s) {
+  Call c = call_of(d, g, WTCONV_OP_GATED_BWD, ws, s);
+  if (d.dtype == WTCONV_F32) return backward<float>(c, g);
+  if (d.dtype == WTCONV_F16) return backward<__half>(c, g);
+  return backward<__nv_bfloat16>(c, g);
 }
 
 }  // namespace wtb

@@ -94,6 +94,17 @@ wtconv_status_t check_gated(const wtconv_gated_desc_t* d, int op) {
   if (op == WTCONV_OP_GATED_BWD) TRY(rows("dh", d->dh_stride, d->M, d->H));
   if (op == WTCONV_OP_GATED_Q8 && (d->C % 16 || d->x_stride % 16 || d->gate_stride % 16 || d->up_stride % 16))
     return fail(WTCONV_ERR_UNSUPPORTED, "8-bit operands: C=%d and the strides must be multiples of 16", d->C);
+  if (d->align < 0) return fail(WTCONV_ERR_INVALID_ARG, "align=%d is negative", d->align);
+  return WTCONV_OK;
+}
+
+// The operands' addresses, and whether they keep what the desc says of them.
+wtconv_status_t operands(const wtconv_gated_desc_t* d, const void* x, const void* gate, const void* up, int align) {
+  TRY(pointer(x, "x", align));
+  TRY(pointer(gate, "gate", align));
+  TRY(pointer(up, "up", align));
+  if (d->align >= 16 && ((uintptr_t)x | (uintptr_t)gate | (uintptr_t)up) % 16)
+    return fail(WTCONV_ERR_MISALIGNED, "align=%d: x, gate or up is not 16-byte aligned", d->align);
   return WTCONV_OK;
 }
 
@@ -198,9 +209,7 @@ wtconv_status_t wtconv_gated_fwd(const wtconv_gated_desc_t* d, const void* x, co
     TRY(check_gated(d, WTCONV_OP_GATED_FWD));
     if (d->M == 0) return WTCONV_OK;
     const int es = esize(d->dtype);
-    TRY(pointer(x, "x", es));
-    TRY(pointer(gate, "gate", es));
-    TRY(pointer(up, "up", es));
+    TRY(operands(d, x, gate, up, es));
     TRY(pointer(h, "h", es));
     TRY(workspace(ws, ws_bytes, wtb::gated_workspace(*d, WTCONV_OP_GATED_FWD)));
     wtb::GatedArgs a = {};
@@ -217,9 +226,7 @@ wtconv_status_t wtconv_gated_q8(const wtconv_gated_desc_t* d, const void* x, con
   try {
     TRY(check_gated(d, WTCONV_OP_GATED_Q8));
     if (d->M == 0) return WTCONV_OK;
-    TRY(pointer(x, "x", 16));
-    TRY(pointer(gate, "gate", 16));
-    TRY(pointer(up, "up", 16));
+    TRY(operands(d, x, gate, up, 16));
     TRY(pointer(x_scale, "x_scale", 4));
     TRY(pointer(gate_scale, "gate_scale", 4));
     TRY(pointer(up_scale, "up_scale", 4));
@@ -253,9 +260,7 @@ wtconv_status_t wtconv_gated_bwd(const wtconv_gated_desc_t* d, const void* dh, c
     }
     if (!dx && !dgate) return WTCONV_OK;
     TRY(pointer(dh, "dh", es));
-    TRY(pointer(x, "x", es));
-    TRY(pointer(gate, "gate", es));
-    TRY(pointer(up, "up", es));
+    TRY(operands(d, x, gate, up, es));
     TRY(workspace(ws, ws_bytes, wtb::gated_workspace(*d, WTCONV_OP_GATED_BWD)));
     wtb::GatedArgs a = {};
     a.x = x; a.gate = gate; a.up = up; a.dh = dh; a.dx = dx; a.dgate = dgate; a.dup = dup;

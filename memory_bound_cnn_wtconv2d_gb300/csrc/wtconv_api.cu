@@ -1035,26 +1035,6 @@ wtconv_status_t plan_bw_win_compute(const wtconv_desc_t* d, WtBwPlan& pl, int lo
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// cuTensorMapEncodeTiled, fetched from the driver through the runtime so the
-// library does not link libcuda directly.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // Tensor map over a float32 NCHW tensor, dimensions (W, H, C, N) innermost
 // first, with box (box_w, box_h, 1, P): one box is P planes of one channel
 // with a margin, landing in shared memory as P consecutive padded planes.
@@ -1062,7 +1042,7 @@ EncodeTiledFn encode_tiled() {
 bool encode_plane_map(CUtensorMap* m, const void* base, const wtconv_desc_t* d, int box_w, int box_h, int P) {
   if (d->dtype != WTCONV_F32 || (d->W % 4) != 0 || !aligned(base, 16)) return false;
   if (box_w > 256 || box_h > 256 || P > 256 || (box_w % 4) != 0) return false;
-  EncodeTiledFn fn = encode_tiled();
+  wt::EncodeTiledFn fn = wt::encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)d->W, (cuuint64_t)d->H, (cuuint64_t)d->C, (cuuint64_t)d->N};
   const cuuint64_t strides[3] = {4ull * d->W, 4ull * d->W * d->H, 4ull * d->W * d->H * d->C};
@@ -1079,7 +1059,7 @@ bool encode_plane_map(CUtensorMap* m, const void* base, const wtconv_desc_t* d, 
 bool encode_map16(CUtensorMap* m, const void* base, const wtconv_desc_t* d, int box_w, int box_h, int P) {
   if (d->dtype == WTCONV_F32 || (d->W % 8) != 0 || !aligned(base, 16)) return false;
   if (box_w > 256 || box_h > 256 || P > 256 || (box_w % 8) != 0) return false;
-  EncodeTiledFn fn = encode_tiled();
+  wt::EncodeTiledFn fn = wt::encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)d->W, (cuuint64_t)d->H, (cuuint64_t)d->C, (cuuint64_t)d->N};
   const cuuint64_t strides[3] = {2ull * d->W, 2ull * d->W * d->H, 2ull * d->W * d->H * d->C};
@@ -1390,6 +1370,22 @@ wtconv_status_t split_bw(const wtconv_desc_t* d, int s, const void* x, const voi
 }  // namespace
 
 namespace wt {
+// cuTensorMapEncodeTiled, fetched from the driver through the runtime so the
+// library does not link libcuda directly.
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 
 namespace {

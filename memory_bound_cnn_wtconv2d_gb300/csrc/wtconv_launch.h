@@ -86,6 +86,12 @@ cudaError_t launch_scale(const float* in, float* out, int n, float f, cudaStream
 // Sets the thread-local message returned by wtconv_last_error().
 void set_last_error(const char* msg);
 
+// cuTensorMapEncodeTiled, or NULL where the driver has none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
+
 // Whether wtconv_test_copy_timeout has the test hook on.
 bool wait_hook_on();
 

@@ -36,7 +36,7 @@ class RmsDesc(ctypes.Structure):
 class GatedDesc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_longlong), ("C", ctypes.c_int), ("H", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("act", ctypes.c_int), ("x_stride", ctypes.c_longlong), ("gate_stride", ctypes.c_longlong),
-                ("up_stride", ctypes.c_longlong), ("dh_stride", ctypes.c_longlong)]
+                ("up_stride", ctypes.c_longlong), ("dh_stride", ctypes.c_longlong), ("align", ctypes.c_int)]
 
 
 class Tensor(ctypes.Structure):
@@ -286,7 +286,7 @@ def wtconv_rms_norm_bwd(dy, total, rstd, weight=None, dtotal=None, dx=None, dwei
 class _GatedLayout:
     __slots__ = ("desc", "ref", "M", "C", "H", "device", "dtype", "h_shape", "ws")
 
-    def __init__(self, x, gate, up, dh, activation, op, dtype):
+    def __init__(self, x, gate, up, dh, activation, op, dtype, aligned):
         xs = _row_stride(x, "x")
         C = x.shape[-1]
         device = x.device
@@ -319,7 +319,8 @@ class _GatedLayout:
             ds = _row_stride(dh, "dh")
         if op == OP_GATED_Q8 and (C % 16 or any(s % 16 for s in (xs, *strides))):
             raise ValueError(f"8-bit operands: the {C} channels and the rows' strides must be multiples of 16")
-        self.desc = GatedDesc(self.M, C, self.H, _c.DTYPE_CODES[dtype], _b.ACT_CODES[activation], xs, *strides, ds)
+        self.desc = GatedDesc(self.M, C, self.H, _c.DTYPE_CODES[dtype], _b.ACT_CODES[activation], xs, *strides, ds,
+                              16 if aligned else 0)
         self.ref = ctypes.byref(self.desc)
         with _b._on(device):  # the size follows the device
             self.ws = lib().wtconv_gated_workspace_size(self.ref, op)
@@ -327,9 +328,11 @@ class _GatedLayout:
 
 def _gated_layout(x, gate, up, dh, activation, op, dtype=None):
     def make():
-        return _GatedLayout(x, gate, up, dh, activation, op, dtype)
+        return _GatedLayout(x, gate, up, dh, activation, op, dtype, aligned)
+    aligned = False
     try:
-        key = (x.shape, x.stride(), x.dtype, x.device, gate.shape, gate.stride(), gate.dtype, gate.device, up.shape,
+        aligned = (x.data_ptr() | gate.data_ptr() | up.data_ptr()) % 16 == 0
+        key = (aligned, x.shape, x.stride(), x.dtype, x.device, gate.shape, gate.stride(), gate.dtype, gate.device, up.shape,
                up.stride(), up.dtype, up.device, activation, op, dtype,
                None if dh is None else (dh.shape, dh.stride(), dh.dtype, dh.device))
     except AttributeError:  # not tensors: the checks say which

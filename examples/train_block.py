@@ -2,9 +2,11 @@
 
 Each class is a sinusoidal grating of its own orientation and frequency under
 noise; the blocks run WTConv2d, the group norms and the Muon optimiser of this
-package together.  Prints the loss as it goes, and the final accuracy.
+package together; with --gated the RMS norms and gated products, and the
+gradients are clipped by their global norm.  Prints the loss as it goes, and the
+final accuracy.
 
-    python examples/train_block.py [--steps 60] [--channels 32] [--size 32]
+    python examples/train_block.py [--steps 60] [--channels 32] [--size 32] [--gated]
 """
 import argparse
 import math
@@ -15,7 +17,8 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from memory_bound_cnn_wtconv2d_gb300.block import WTConvBlock, block_optimizers  # noqa: E402
+from memory_bound_cnn_wtconv2d_gb300.block import WTConvBlock, WTConvGatedBlock, block_optimizers  # noqa: E402
+from memory_bound_cnn_wtconv2d_gb300.clip import clip_grad_norm_  # noqa: E402
 
 
 def textures(batch, size, classes, generator, device):
@@ -29,12 +32,14 @@ def textures(batch, size, classes, generator, device):
     return image[:, None] + 0.5 * torch.randn(batch, 1, size, size, generator=generator, device=device), label
 
 
-def train(steps=60, channels=32, size=32, batch=64, classes=6, device="cuda", seed=0, log=print):
+def train(steps=60, channels=32, size=32, batch=64, classes=6, device="cuda", seed=0, log=print, gated=False):
     torch.manual_seed(seed)
     generator = torch.Generator(device=device)
     generator.manual_seed(seed)
     stem = torch.nn.Conv2d(1, channels, 3, padding=1, device=device)
-    blocks = torch.nn.Sequential(*[WTConvBlock(channels, levels=2, num_groups=4, device=device) for _ in range(2)])
+    make = ((lambda: WTConvGatedBlock(channels, levels=2, device=device)) if gated else
+            (lambda: WTConvBlock(channels, levels=2, num_groups=4, device=device)))
+    blocks = torch.nn.Sequential(*[make() for _ in range(2)])
     head = torch.nn.Linear(channels, classes, device=device)
     muon, adam = block_optimizers(blocks)
     rest = torch.optim.AdamW([*stem.parameters(), *head.parameters()], lr=3e-3)
@@ -46,6 +51,8 @@ def train(steps=60, channels=32, size=32, batch=64, classes=6, device="cuda", se
         for o in (muon, adam, rest):
             o.zero_grad(set_to_none=True)
         loss.backward()
+        if gated:
+            clip_grad_norm_([*stem.parameters(), *blocks.parameters(), *head.parameters()], 1.0)
         for o in (muon, adam, rest):
             o.step()
         losses.append(float(loss.detach()))
@@ -60,5 +67,6 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--channels", type=int, default=32)
     ap.add_argument("--size", type=int, default=32)
+    ap.add_argument("--gated", action="store_true", help="blocks with a gated channel mixer, gradients clipped")
     a = ap.parse_args()
-    train(a.steps, a.channels, a.size)
+    train(a.steps, a.channels, a.size, gated=a.gated)

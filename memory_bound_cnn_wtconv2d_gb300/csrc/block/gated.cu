@@ -176,7 +176,7 @@ struct Plan {
 
 Plan plan_of(const wtconv_gated_desc_t& d, int op) {
   Plan p = {};
-  const int sms = wt::sm_count();
+  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;  // a size may be asked for without a GPU
   const bool f32 = d.dtype == WTCONV_F32 && op != WTCONV_OP_GATED_Q8;
   p.parts = f32 ? 3 : 1;
   p.products = f32 ? 6 : 1;

@@ -328,10 +328,11 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
   unsigned char* buf = staging + warp * kStaging;
   float* scale = reinterpret_cast<float*>(buf);  // of a chunk's columns, before its rows are staged
   uint32_t acc = 0, phase = 0;
+  bool got = true;
   for (int i = blockIdx.x; i < items; i += gridDim.x) {
     const Item t = item_of(a, i);
     const long long row0 = (long long)t.m * kRows + quadrant * 32;
-    const bool got = wait(sh, a, &sh.acc_full[acc], phase);
+    got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
     tc_fence_after();
     const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * kMaxN;
     const int width = EPI == EPI_OUT ? a.n : a.half;

@@ -3,9 +3,10 @@
 //   n = (sum of all g^2)^1/2, g <- g min(1, limit / (n + eps))
 //
 // Bound by memory: the elements are read, and where the norm is above the
-// limit read and written again.  The list of tensors is cut into chunks of
-// equal length, whose number the CTAs share out; the list itself comes as a
-// kernel argument, so that a call copies nothing and can be captured.
+// limit read and written again.  The list of tensors is cut into chunks of 16 KB,
+// which the CTAs share out; the list itself comes as a kernel argument, so that a
+// call copies nothing and can be captured.  The second launch walks the chunks
+// from the last one back: what the first one read last is still in the L2.
 #include "block_device.cuh"
 #include "mixer_launch.h"
 #include "../wtconv_launch.h"
@@ -14,20 +15,23 @@ namespace wtb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;     // elements
-constexpr int kMaxTensors = 512; // of one launch: 12 KB of arguments
-constexpr int kParts = 608;      // partial sums of one launch, at most
+constexpr int kChunkBytes = 16384;
+constexpr int kMost = 512;   // tensors of one launch
+constexpr int kCtas = 8;     // an SM
+constexpr int kParts = 2048; // partial sums of one launch, at most
 
+// Three sizes: a launch's cost grows with its arguments.
+template <int N>
 struct ClipList {
-  void* data[kMaxTensors];
-  long long numel[kMaxTensors];
-  int start[kMaxTensors + 1];  // first chunk of each tensor
-  unsigned char dtype[kMaxTensors];
+  void* data[N];
+  long long numel[N];
+  int start[N + 1];  // first chunk of each tensor
+  unsigned char dtype[N];
   int count;
 };
 
-// The tensor of a chunk: the last one that starts at or before it.
-__device__ __forceinline__ int find(const ClipList& l, int chunk) {
+template <typename L>
+__device__ __forceinline__ int find(const L& l, int chunk) {  // the last tensor that starts at or before it
   int lo = 0, hi = l.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -35,6 +39,26 @@ __device__ __forceinline__ int find(const ClipList& l, int chunk) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+// Calls f with a chunk's elements, in the tensor's type.
+template <typename L, typename F>
+__device__ __forceinline__ void with_chunk(const L& l, int chunk, const F& f) {
+  const int t = find(l, chunk);
+  auto go = [&](auto* p) {
+    constexpr int kEach = kChunkBytes / (int)sizeof(*p);
+    const long long at = (long long)(chunk - l.start[t]) * kEach;
+    f(p + at, (int)min((long long)kEach, l.numel[t] - at));
+  };
+  if (l.dtype[t] == WTCONV_F32) go((float*)l.data[t]);
+  else if (l.dtype[t] == WTCONV_F16) go((__half*)l.data[t]);
+  else go((__nv_bfloat16*)l.data[t]);
+}
+
+// Elements before the first 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int n) {
+  return min(n, (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T));
 }
 
 // Sum of squares of a few values in float32; of scaled ones where that
@@ -66,38 +90,78 @@ __device__ __forceinline__ double over_cta(double v) {
 
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int n) {
+  constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads;
+  const int head = head_of(p, n), body = (n - head) / kVec;
   double s = 0.;
-  for (int i = threadIdx.x; i < n; i += kThreads * 8) {
-    float v[8];
+  Vec<T, kVec> u[kLoads];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = i + j * kThreads < n ? to_float<T>(p[i + j * kThreads]) : 0.f;
-    s += squares(v);
+  for (int j = 0; j < kLoads; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    if (i < body) u[j].load(p + head + i * kVec);
+    else u[j].r = make_uint4(0, 0, 0, 0);
   }
-  return s;
-}
-template <typename T>
-__device__ __forceinline__ void chunk_scale(T* p, int n, float f) {
-  for (int i = threadIdx.x; i < n; i += kThreads) p[i] = round_to<T>(to_float<T>(p[i]) * f);
+  // what lies before and behind the whole accesses: fewer elements than threads
+  const int edge = n - body * kVec;
+  if (threadIdx.x < edge) {
+    const int i = threadIdx.x < head ? threadIdx.x : threadIdx.x + body * kVec;
+    const float v[1] = {to_float<T>(p[i])};
+    s = squares(v);
+  }
+  // one float64 addition for them all: those run at a 64th of float32's rate
+  float v[kLoads * kVec];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    float w[kVec];
+    u[j].widen(w);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) v[j * kVec + k] = w[k];
+  }
+  return s + squares(v);
 }
 
-__global__ void __launch_bounds__(kThreads)
-clip_squares(const __grid_constant__ ClipList l, double* part) {
-  double s = 0.;
-  for (int chunk = blockIdx.x; chunk < l.start[l.count]; chunk += gridDim.x) {
-    const int t = find(l, chunk);
-    const long long at = (long long)(chunk - l.start[t]) * kChunk;
-    const int n = (int)min((long long)kChunk, l.numel[t] - at);
-    if (l.dtype[t] == WTCONV_F32) s += chunk_squares((const float*)l.data[t] + at, n);
-    else if (l.dtype[t] == WTCONV_F16) s += chunk_squares((const __half*)l.data[t] + at, n);
-    else s += chunk_squares((const __nv_bfloat16*)l.data[t] + at, n);
+template <typename T>
+__device__ __forceinline__ void chunk_scale(T* p, int n, float f) {
+  constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads;
+  const int head = head_of(p, n), body = (n - head) / kVec, edge = n - body * kVec;
+  Vec<T, kVec> u[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    if (i < body) u[j].load(p + head + i * kVec);
   }
+  if (threadIdx.x < edge) {
+    T* e = p + (threadIdx.x < head ? threadIdx.x : threadIdx.x + body * kVec);
+    *e = round_to<T>(to_float<T>(*e) * f);
+  }
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    if (i < body) {
+      float v[kVec];
+      u[j].widen(v);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) v[k] *= f;
+      u[j].round(v);
+      u[j].store(p + head + i * kVec);
+    }
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_squares(const __grid_constant__ ClipList<N> l, double* part) {
+  double s = 0.;
+  const int chunks = l.start[l.count];
+  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x)
+    with_chunk(l, chunk, [&](auto* p, int n) { s += chunk_squares(p, n); });
   s = over_cta(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 __device__ __forceinline__ float norm_of(const double* part, int parts) {
   double s = 0.;
-  for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+#pragma unroll 8
+  for (int i = threadIdx.x; i < parts; i += kThreads) s += __ldcg(part + i);
   return (float)sqrt(over_cta(s));
 }
 
@@ -106,65 +170,71 @@ __global__ void __launch_bounds__(kThreads) clip_norm(const double* part, int pa
   if (threadIdx.x == 0) *norm = n;
 }
 
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-clip_scale(const __grid_constant__ ClipList l, const double* part, int parts, float limit, float eps) {
-  const float f = limit / (norm_of(part, parts) + eps);
+clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float limit, float eps, float* norm) {
+  const float n = norm_of(part, parts);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  const float f = limit / (n + eps);
   if (f >= 1.f) return;
-  for (int chunk = blockIdx.x; chunk < l.start[l.count]; chunk += gridDim.x) {
-    const int t = find(l, chunk);
-    const long long at = (long long)(chunk - l.start[t]) * kChunk;
-    const int n = (int)min((long long)kChunk, l.numel[t] - at);
-    if (l.dtype[t] == WTCONV_F32) chunk_scale((float*)l.data[t] + at, n, f);
-    else if (l.dtype[t] == WTCONV_F16) chunk_scale((__half*)l.data[t] + at, n, f);
-    else chunk_scale((__nv_bfloat16*)l.data[t] + at, n, f);
-  }
-}
-
-// Fills `l` from the tensors from `first` on; returns how many it took.
-int fill(ClipList& l, const wtconv_tensor_t* t, int first, int count) {
-  long long chunks = 0;
-  int i = first;
-  l.count = 0;
-  for (; i < count && l.count < kMaxTensors; ++i) {
-    if (t[i].numel == 0) continue;
-    l.data[l.count] = t[i].data;
-    l.numel[l.count] = t[i].numel;
-    l.dtype[l.count] = (unsigned char)t[i].dtype;
-    l.start[l.count++] = (int)chunks;
-    chunks += (t[i].numel + kChunk - 1) / kChunk;  // below 2^31: the lists hold less than 2^43 elements
-  }
-  l.start[l.count] = (int)chunks;
-  return i - first;
+  for (int chunk = l.start[l.count] - 1 - (int)blockIdx.x; chunk >= 0; chunk -= gridDim.x)
+    with_chunk(l, chunk, [&](auto* p, int m) { chunk_scale(p, m, f); });
 }
 
 int grid_of(int chunks) {
-  const int most = wt::sm_count() * 4 < kParts ? wt::sm_count() * 4 : kParts;
+  const int most = wt::sm_count() * kCtas < kParts ? wt::sm_count() * kCtas : kParts;
   return chunks < most ? chunks : most;
+}
+
+// Walks the tensors that hold something, kMost at a time, and launches on each list.
+template <int N, typename F>
+void with_list(const wtconv_tensor_t* const* t, int n, const F& f) {
+  ClipList<N> l;
+  long long chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    const int each = kChunkBytes / (t[i]->dtype == WTCONV_F32 ? 4 : 2);
+    l.data[i] = t[i]->data;
+    l.numel[i] = t[i]->numel;
+    l.dtype[i] = (unsigned char)t[i]->dtype;
+    l.start[i] = (int)chunks;
+    chunks += (t[i]->numel + each - 1) / each;  // below 2^31: the lists hold less than 2^42 elements
+  }
+  l.start[n] = (int)chunks;
+  l.count = n;
+  f(l);
+}
+template <typename F>
+void with_lists(const wtconv_tensor_t* t, int count, const F& f) {
+  const wtconv_tensor_t* some[kMost];
+  for (int i = 0; i < count;) {
+    int n = 0;
+    for (; i < count && n < kMost; ++i)
+      if (t[i].numel > 0) some[n++] = t + i;
+    if (n == 0) continue;
+    if (n <= 32) with_list<32>(some, n, f);
+    else if (n <= 128) with_list<128>(some, n, f);
+    else with_list<kMost>(some, n, f);
+  }
 }
 
 }  // namespace
 
-// A launch takes kMaxTensors tensors.
-size_t clip_workspace(int count) { return ((size_t)(count / kMaxTensors + 1) * kParts * sizeof(double) + 255) / 256 * 256; }
+size_t clip_workspace(int count) { return ((size_t)(count / kMost + 1) * kParts * sizeof(double) + 255) / 256 * 256; }
 
 cudaError_t clip_launch(const wtconv_tensor_t* t, int count, bool clip, float max_norm, float eps, float* norm, void* ws,
                         cudaStream_t s) {
-  ClipList l;
   double* part = (double*)ws;
   int parts = 0;
-  for (int i = 0; i < count;) {
-    i += fill(l, t, i, count);
-    if (!l.count) continue;
+  with_lists(t, count, [&](const auto& l) {
     const int grid = grid_of(l.start[l.count]);
     clip_squares<<<grid, kThreads, 0, s>>>(l, part + parts);
     parts += grid;
-  }
-  clip_norm<<<1, kThreads, 0, s>>>(part, parts, norm);
-  if (clip)
-    for (int i = 0; i < count;) {
-      i += fill(l, t, i, count);
-      if (l.count) clip_scale<<<grid_of(l.start[l.count]), kThreads, 0, s>>>(l, part, parts, max_norm, eps);
-    }
+  });
+  if (!clip || parts == 0) clip_norm<<<1, kThreads, 0, s>>>(part, parts, norm);
+  else
+    with_lists(t, count, [&](const auto& l) {
+      clip_scale<<<grid_of(l.start[l.count]), kThreads, 0, s>>>(l, part, parts, max_norm, eps, norm);
+    });
   return cudaGetLastError();
 }
 

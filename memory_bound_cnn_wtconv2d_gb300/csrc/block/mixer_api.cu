@@ -116,8 +116,8 @@ wtconv_status_t check_tensors(const wtconv_tensor_t* t, int count) {
     if (t[i].dtype < 0 || t[i].dtype > WTCONV_BF16)
       return fail(WTCONV_ERR_INVALID_ARG, "tensor %d: dtype=%d unknown", i, t[i].dtype);
     if (t[i].numel < 0) return fail(WTCONV_ERR_INVALID_ARG, "tensor %d: numel=%lld is negative", i, t[i].numel);
-    if (t[i].numel >= (1LL << 43) || (total += t[i].numel) >= (1LL << 43))
-      return fail(WTCONV_ERR_UNSUPPORTED, "more than 2^43 elements");
+    if (t[i].numel >= (1LL << 42) || (total += t[i].numel) >= (1LL << 42))
+      return fail(WTCONV_ERR_UNSUPPORTED, "more than 2^42 elements");
     if (t[i].numel) TRY(pointer(t[i].data, "a tensor", esize(t[i].dtype)));
   }
   return WTCONV_OK;

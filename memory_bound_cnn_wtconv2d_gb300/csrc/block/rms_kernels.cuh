@@ -1,0 +1,507 @@
+// Root-mean-square norm over rows of C channels with the residual's addition.
+//
+//   t = x + r, rstd = (sum t^2 / C + eps)^-1/2, y = t rstd w
+//   8 bits: scale = max |y| / 448, q = e4m3(y / scale)
+//   dx = rstd (w dy - xhat mean(w dy xhat)) + dt, xhat = t rstd; dw = sum dy xhat
+//
+// All of them are bound by the bytes they move: 6 to 12 operations an element
+// against 4 to 16 bytes.  So a row is read once and stays in the registers of the
+// lanes that share it: a power of two of lanes with up to 32 values each, a part
+// of a warp for short rows (several rows a warp, no barrier), a CTA of 64 to 256
+// threads for long ones.  Values a lane and lanes are chosen so that few lanes
+// idle (96 channels of 16 bits: 4 lanes of three 16-byte accesses).  Rows that no
+// CTA holds (above 8192 channels, or long ones of odd width) are read twice or
+// three times, the later times from the caches.
+//
+// CTAs stay and take rows in turn: the weight is read once where it fits the
+// registers, and the backward adds up its part of dw on the way, so that dy and t
+// are read once for both results.  A second launch adds the CTAs' parts in order.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gn_math.cuh"
+#include "mixer_launch.h"
+#include "../wtconv_launch.h"
+
+namespace wtb {
+namespace rms {
+
+constexpr int kThreads = 256;      // of a CTA whose rows take a warp at most
+constexpr int kMostLanes = 256;
+constexpr int kMostValues = 32;    // of a lane
+constexpr float kE4m3Most = 448.f;
+constexpr float kLeastScale = 0x1p-120f;
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Sum or maximum over a row's lanes: part of a warp, or the CTA.
+template <bool MAX>
+__device__ __forceinline__ float over_row(float v, int lanes) {
+  __shared__ float part[2][kMostLanes / 32];
+  for (int o = min(lanes, 32) / 2; o; o >>= 1) {
+    const float u = __shfl_xor_sync(~0u, v, o);
+    v = MAX ? max_nan(v, u) : v + u;
+  }
+  if (lanes > 32) {
+    __syncthreads();  // the last row's sums have been read
+    if ((threadIdx.x & 31) == 0) part[MAX][threadIdx.x / 32] = v;
+    __syncthreads();
+    v = part[MAX][0];
+    for (int i = 1; i < lanes / 32; ++i) v = MAX ? max_nan(v, part[MAX][i]) : v + part[MAX][i];
+  }
+  return v;
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_weight(const float* w, int c, float (&v)[VEC]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 1.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = __ldg(w + c + i);
+  }
+}
+
+// VEC values of a row as e4m3.
+template <int VEC>
+__device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    unsigned short h[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    if constexpr (VEC == 2) *reinterpret_cast<unsigned short*>(p) = h[0];
+    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(p) = h[0] | (uint32_t)h[1] << 16;
+    else *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+  }
+}
+
+// ---- rows that stay in registers ------------------------------------------------
+
+template <typename T, int VEC, int ITEMS, bool Q8>
+__global__ void __launch_bounds__(kThreads)
+rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
+  constexpr bool kKeep = VEC * ITEMS <= 24;  // the weight in registers
+  const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
+  const float* weight = a.weight;
+  float w[kKeep ? ITEMS : 1][VEC];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < d.C) load_weight<VEC>(weight, c, w[k]);
+    }
+  }
+  for (long long first = (long long)blockIdx.x * per; first < d.M; first += (long long)gridDim.x * per) {
+    const long long row = first + threadIdx.x / lanes;
+    const int most = row < d.M ? d.C : 0;
+    const T *x = (const T*)a.x + row * d.x_stride, *r = (const T*)a.r + row * d.r_stride;
+    Vec<T, VEC> u[ITEMS], v[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) u[k].load(x + c);
+    }
+    if (a.r) {
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c < most) v[k].load(r + c);
+      }
+    }
+    float t[ITEMS][VEC], s = 0.f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) {
+        u[k].widen(t[k]);
+        if (a.r) {
+          float o[VEC];
+          v[k].widen(o);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) t[k][i] += o[i];
+          if (a.total) {
+            v[k].round(t[k]);
+            v[k].store((T*)a.total + row * d.C + c);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s = fmaf(t[k][i], t[k][i], s);
+      }
+    }
+    float rstd = 1.f, m = 0.f;
+    if (norm) rstd = 1.f / sqrtf(over_row<false>(s, lanes) / d.C + d.eps);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) {
+        if constexpr (!kKeep) load_weight<VEC>(weight, c, w[0]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          t[k][i] = t[k][i] * rstd * w[kKeep ? k : 0][i];
+          if constexpr (Q8) m = max_nan(m, fabsf(t[k][i]));
+        }
+        if constexpr (!Q8) {
+          u[k].round(t[k]);
+          u[k].store((T*)a.y + row * d.C + c);
+        }
+      }
+    }
+    if constexpr (Q8) {
+      m = max_nan(over_row<true>(m, lanes), kLeastScale * kE4m3Most);
+      const float inv = kE4m3Most / m;
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c < most) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) t[k][i] *= inv;
+          store_e4m3<VEC>(a.q + row * d.C + c, t[k]);
+        }
+      }
+    }
+    if (lane == 0 && most) a.rstd[row] = Q8 ? m / kE4m3Most : rstd;
+  }
+}
+
+template <typename T, int VEC, int ITEMS>
+__global__ void __launch_bounds__(kThreads)
+rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part) {
+  extern __shared__ float sums[];  // [rows at a time][lanes * ITEMS * VEC], for dw
+  const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
+  const float* weight = a.weight;
+  float dw[ITEMS][VEC];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) dw[k][i] = 0.f;
+  const float over = 1.f / d.C;
+  for (long long first = (long long)blockIdx.x * per; first < d.M; first += (long long)gridDim.x * per) {
+    const long long row = first + threadIdx.x / lanes;
+    const int most = row < d.M ? d.C : 0;
+    const T *x = (const T*)a.x + row * d.x_stride, *dy = (const T*)a.dy + row * d.d_stride, *r = (const T*)a.r + row * d.r_stride;
+    Vec<T, VEC> u[ITEMS], v[ITEMS], e[ITEMS];
+    const float rstd = most ? a.rstd[row] : 0.f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) {
+        u[k].load(x + c);
+        v[k].load(dy + c);
+        if (a.r) e[k].load(r + c);
+      }
+    }
+    float s = 0.f;
+    float t[ITEMS][VEC], g[ITEMS][VEC];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) {
+        float w[VEC];
+        load_weight<VEC>(weight, c, w);
+        u[k].widen(t[k]);
+        v[k].widen(g[k]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          t[k][i] *= rstd;  // xhat
+          dw[k][i] = fmaf(g[k][i], t[k][i], dw[k][i]);
+          g[k][i] *= w[i];
+          s = fmaf(g[k][i], t[k][i], s);
+        }
+      }
+    }
+    s = -over_row<false>(s, lanes) * over;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c < most) {
+        float o[VEC];
+        if (a.r) e[k].widen(o);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
+          if (a.r) g[k][i] += o[i];
+        }
+        u[k].round(g[k]);
+        u[k].store((T*)a.y + row * d.C + c);
+      }
+    }
+  }
+  if (!a.dweight) return;
+  float* out = part + (long long)blockIdx.x * d.C;
+  if (per == 1) {
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (c < d.C) out[c + i] = dw[k][i];
+    }
+    return;
+  }
+  const int width = lanes * ITEMS * VEC;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sums[threadIdx.x / lanes * width + (k * lanes + lane) * VEC + i] = dw[k][i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < d.C; c += blockDim.x) {
+    float v = 0.f;
+    for (int i = 0; i < per; ++i) v += sums[i * width + c];
+    out[c] = v;
+  }
+}
+
+// dw from the CTAs' parts: 32 columns a CTA, eight ranges of parts side by side.
+static __global__ void __launch_bounds__(256) add_parts(const float* part, int n, int C, float* out) {
+  __shared__ float sh[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x / 32;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < C) {
+    const int each = (n + 7) / 8, end = min(n, (y + 1) * each);
+    int i = y * each;
+    for (; i + 4 <= end; i += 4)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += __ldcg(part + (long long)(i + j) * C + c);
+    for (; i < end; ++i) s[0] += __ldcg(part + (long long)i * C + c);
+  }
+  sh[y][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (y == 0 && c < C) {
+    float v = 0.f;
+    for (int i = 0; i < 8; ++i) v += sh[i][threadIdx.x];
+    out[c] = v;
+  }
+}
+
+// ---- rows that are read again ---------------------------------------------------
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_sum(const RmsArgs& a, long long xo, long long ro, float (&t)[VEC]) {
+  Vec<T, VEC> u;
+  u.load((const T*)a.x + xo);
+  u.widen(t);
+  if (a.r) {
+    float r[VEC];
+    u.load((const T*)a.r + ro);
+    u.widen(r);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) t[i] += r[i];
+  }
+}
+
+template <typename T, int VEC, bool Q8>
+__global__ void __launch_bounds__(kThreads)
+long_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int norm) {
+  for (long long row = blockIdx.x; row < d.M; row += gridDim.x) {
+    const long long xo = row * d.x_stride, ro = row * d.r_stride, yo = row * d.C;
+    float rstd = 1.f, t[VEC], w[VEC];
+    if (norm) {
+      float s = 0.f;
+      for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
+        load_sum<T, VEC>(a, xo + c, ro + c, t);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s = fmaf(t[i], t[i], s);
+      }
+      rstd = 1.f / sqrtf(over_row<false>(s, kThreads) / d.C + d.eps);
+    }
+    float m = 0.f, inv = 0.f;
+    if constexpr (Q8) {
+      for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
+        load_sum<T, VEC>(a, xo + c, ro + c, t);
+        load_weight<VEC>(a.weight, c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m = max_nan(m, fabsf(t[i] * rstd * w[i]));
+      }
+      m = max_nan(over_row<true>(m, kThreads), kLeastScale * kE4m3Most);
+      inv = kE4m3Most / m;
+    }
+    for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
+      load_sum<T, VEC>(a, xo + c, ro + c, t);
+      load_weight<VEC>(a.weight, c, w);
+      Vec<T, VEC> o;
+      if (a.total) {
+        o.round(t);
+        o.store((T*)a.total + yo + c);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) t[i] = t[i] * rstd * w[i] * (Q8 ? inv : 1.f);
+      if constexpr (Q8) {
+        store_e4m3<VEC>(a.q + yo + c, t);
+      } else {
+        o.round(t);
+        o.store((T*)a.y + yo + c);
+      }
+    }
+    if (threadIdx.x == 0) a.rstd[row] = Q8 ? m / kE4m3Most : rstd;
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads)
+long_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a) {
+  for (long long row = blockIdx.x; row < d.M; row += gridDim.x) {
+    const T *x = (const T*)a.x + row * d.x_stride, *dy = (const T*)a.dy + row * d.d_stride, *r = (const T*)a.r + row * d.r_stride;
+    const float rstd = a.rstd[row];
+    float s = 0.f, t[VEC], g[VEC], w[VEC];
+    Vec<T, VEC> u;
+    for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
+      u.load(x + c);
+      u.widen(t);
+      u.load(dy + c);
+      u.widen(g);
+      load_weight<VEC>(a.weight, c, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s = fmaf(g[i] * w[i], t[i] * rstd, s);
+    }
+    s = -over_row<false>(s, kThreads) / d.C;
+    for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
+      u.load(x + c);
+      u.widen(t);
+      u.load(dy + c);
+      u.widen(g);
+      load_weight<VEC>(a.weight, c, w);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) g[i] = rstd * fmaf(s, t[i] * rstd, g[i] * w[i]);
+      if (a.r) {
+        u.load(r + c);
+        u.widen(t);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) g[i] += t[i];
+      }
+      u.round(g);
+      u.store((T*)a.y + row * d.C + c);
+    }
+  }
+}
+
+// Parts of dw over ranges of rows.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+long_dweight(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, float* part, long long rows) {
+  const int c = blockIdx.x * kThreads + threadIdx.x;
+  if (c >= d.C) return;
+  float s = 0.f;
+  const long long end = min(d.M, (blockIdx.y + 1) * rows);
+  for (long long row = blockIdx.y * rows; row < end; ++row)
+    s = fmaf(to_float(((const T*)a.dy)[row * d.d_stride + c]), to_float(((const T*)a.x)[row * d.x_stride + c]) * a.rstd[row], s);
+  part[(long long)blockIdx.y * d.C + c] = s;
+}
+
+// ---- launches --------------------------------------------------------------------
+
+// How a row lies over lanes; items = 0: no CTA holds it.
+struct Shape {
+  int lanes, items, threads;
+};
+inline Shape shape_of(int C, int vec) {
+  const int n = (C + vec - 1) / vec;
+  Shape best = {0, 0, 0};
+  int least = 0;
+  for (int items : {4, 3, 2, 1, 8}) {  // in order of preference where as many lanes idle
+    if (items * vec > kMostValues) continue;
+    int lanes = 1;
+    while (lanes < (n + items - 1) / items) lanes *= 2;
+    if (lanes > kMostLanes) continue;
+    // lanes beyond a warp cost a barrier, worth a quarter of idle lanes
+    const int cost = lanes * items * (lanes > 32 ? 5 : 4);
+    if (!best.items || cost < least) least = cost, best = {lanes, items, lanes > 32 ? lanes : kThreads};
+  }
+  return best;
+}
+
+inline int parts_most(const wtconv_rms_desc_t& d) {
+  // CTAs that add up dw: at most eight an SM, and no more than rows
+  const long long sms = wt::sm_count() > 0 ? wt::sm_count() : 152, most = sms * 8;
+  return (int)(d.M < most ? d.M : most);
+}
+
+inline int grid_of(const void* f, long long M, const Shape& s, int smem) {
+  const long long per = s.threads / s.lanes, n = (M + per - 1) / per;
+  const int fit = wt::occupancy(f, s.threads, smem);
+  const long long most = (long long)wt::sm_count() * (fit < 1 ? 1 : fit);
+  return (int)(n < most ? n : most);
+}
+
+template <typename T, int VEC, int ITEMS>
+cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, const Shape& s, cudaStream_t st) {
+  if (op == RMS_FWD) {
+    const int grid = grid_of((const void*)rows_forward<T, VEC, ITEMS, false>, d.M, s, 0);
+    rows_forward<T, VEC, ITEMS, false><<<grid, s.threads, 0, st>>>(d, a, s.lanes, 1);
+  } else {
+    const int grid = grid_of((const void*)rows_forward<T, VEC, ITEMS, true>, d.M, s, 0);
+    rows_forward<T, VEC, ITEMS, true><<<grid, s.threads, 0, st>>>(d, a, s.lanes, op == RMS_Q8);
+  }
+  return cudaGetLastError();
+}
+template <typename T, int VEC, int ITEMS>
+cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Shape& s, float* part, cudaStream_t st) {
+  const int smem = a.dweight && s.threads > s.lanes ? s.threads * ITEMS * VEC * 4 : 0;
+  int grid = grid_of((const void*)rows_backward<T, VEC, ITEMS>, d.M, s, smem);
+  if (grid > parts_most(d)) grid = parts_most(d);
+  rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part);
+  if (a.dweight) add_parts<<<(d.C + 31) / 32, 256, 0, st>>>(part, grid, d.C, a.dweight);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, cudaStream_t st) {
+  const Shape s = shape_of(d.C, VEC);
+  switch (s.items) {
+    case 1: return forward_rows<T, VEC, 1>(d, op, a, s, st);
+    case 2: return forward_rows<T, VEC, 2>(d, op, a, s, st);
+    case 3: return forward_rows<T, VEC, 3>(d, op, a, s, st);
+    case 4: return forward_rows<T, VEC, 4>(d, op, a, s, st);
+    case 8:
+      if constexpr (VEC * 8 <= kMostValues) return forward_rows<T, VEC, 8>(d, op, a, s, st);
+  }
+  const long long most = (long long)wt::sm_count() * 8;
+  const int grid = (int)(d.M < most ? d.M : most);
+  if (op == RMS_FWD) long_forward<T, VEC, false><<<grid, kThreads, 0, st>>>(d, a, 1);
+  else long_forward<T, VEC, true><<<grid, kThreads, 0, st>>>(d, a, op == RMS_Q8);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* part, cudaStream_t st) {
+  const Shape s = shape_of(d.C, VEC);
+  switch (s.items) {
+    case 1: return backward_rows<T, VEC, 1>(d, a, s, part, st);
+    case 2: return backward_rows<T, VEC, 2>(d, a, s, part, st);
+    case 3: return backward_rows<T, VEC, 3>(d, a, s, part, st);
+    case 4: return backward_rows<T, VEC, 4>(d, a, s, part, st);
+    case 8:
+      if constexpr (VEC * 8 <= kMostValues) return backward_rows<T, VEC, 8>(d, a, s, part, st);
+  }
+  const long long most = (long long)wt::sm_count() * 8;
+  long_backward<T, VEC><<<(int)(d.M < most ? d.M : most), kThreads, 0, st>>>(d, a);
+  if (a.dweight) {
+    const int n = parts_most(d);
+    long_dweight<T><<<dim3((d.C + kThreads - 1) / kThreads, n), kThreads, 0, st>>>(d, a, part, (d.M + n - 1) / n);
+    add_parts<<<(d.C + 31) / 32, 256, 0, st>>>(part, n, d.C, a.dweight);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_typed(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, int vec, cudaStream_t s) {
+  if (vec >= 16 / (int)sizeof(T)) return forward_vec<T, 16 / sizeof(T)>(d, op, a, s);
+  return vec >= 2 ? forward_vec<T, 2>(d, op, a, s) : forward_vec<T, 1>(d, op, a, s);
+}
+template <typename T>
+cudaError_t backward_typed(const wtconv_rms_desc_t& d, const RmsArgs& a, int vec, float* part, cudaStream_t s) {
+  if (vec >= 16 / (int)sizeof(T)) return backward_vec<T, 16 / sizeof(T)>(d, a, part, s);
+  return vec >= 2 ? backward_vec<T, 2>(d, a, part, s) : backward_vec<T, 1>(d, a, part, s);
+}
+
+}  // namespace rms
+}  // namespace wtb

@@ -11,6 +11,7 @@ works on.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -432,26 +433,25 @@ def _dense(t):
 
 
 def _list(tensors, name="tensors"):
+    """The tensors, and their entries for the library: three 64-bit words each."""
     ts = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
     if not ts:
         raise ValueError(f"{name}: no tensors")
-    entries = (Tensor * len(ts))()
-    device = None
-    for i, t in enumerate(ts):
+    words, codes, device = [], _c.DTYPE_CODES, None
+    for t in ts:
         if not (isinstance(t, torch.Tensor) and _c._on_cuda(t)) or t.layout is not torch.strided:
             raise ValueError(f"{name} must be dense CUDA tensors")
-        code = _c.DTYPE_CODES.get(t.dtype)
+        code = codes.get(t.dtype)
         if code is None:
             raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
         if device is None:
             device = t.device
         elif t.device != device:
             raise ValueError(f"{name}: one device for all, got {device} and {t.device}")
-        if not _dense(t):
+        if not (t.is_contiguous() or _dense(t)):
             raise ValueError(f"{name}: the elements of a tensor must fill one stretch of memory, got strides {t.stride()}")
-        e = entries[i]
-        e.data, e.numel, e.dtype = t.data_ptr(), t.numel(), code
-    return ts, entries, device
+        words += (t.data_ptr(), t.numel(), code)
+    return ts, words, (Tensor * len(ts)).from_buffer(array.array("q", words)), device
 
 
 def _apart(spans, name):
@@ -462,15 +462,11 @@ def _apart(spans, name):
             raise ValueError(f"{name}: the tensors overlap")
 
 
-def _spans(entries, ts):
-    return [(e.data, e.data + e.numel * t.element_size()) for e, t in zip(entries, ts) if e.numel]
-
-
 def wtconv_grad_norm(tensors, norm=None, workspace=None, stream=None):
     """The root of the sum of squares of all elements of a list of tensors (of any
     of the three types, mixed if need be): a float32 tensor of no axes, on the
     GPU."""
-    ts, entries, device = _list(tensors)
+    ts, _, entries, device = _list(tensors)
     need = lib().wtconv_clip_workspace_size(len(ts))
     if norm is not None or workspace is not None:
         _check_out(norm, "norm", (), torch.float32, device)
@@ -489,10 +485,10 @@ def wtconv_grad_norm(tensors, norm=None, workspace=None, stream=None):
 def wtconv_clip_grads(tensors, max_norm, eps=1e-6, norm=None, workspace=None, stream=None):
     """Multiplies every tensor of a list in place by min(1, max_norm / (norm + eps)),
     with the norm of ``wtconv_grad_norm``, which it returns."""
-    ts, entries, device = _list(tensors)
+    ts, words, entries, device = _list(tensors)
     if not (max_norm >= 0 and math.isfinite(eps) and eps >= 0):
         raise ValueError("max_norm and eps must not be negative, eps finite")
-    _apart(_spans(entries, ts), "tensors")
+    _apart([(p, p + n * (2 if code else 4)) for p, n, code in zip(*[iter(words)] * 3) if n], "tensors")
     need = lib().wtconv_clip_workspace_size(len(ts))
     if norm is not None or workspace is not None:
         _check_out(norm, "norm", (), torch.float32, device)

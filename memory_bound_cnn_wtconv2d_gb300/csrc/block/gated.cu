@@ -94,73 +94,76 @@ struct Operand {
 
 // A product's tiles and its split of k.
 struct Tiles {
-  int n;       // columns of an accumulator (FWD: gate and up)
+  int pair, rows;  // of a tile: 128 of one CTA, 256 of a pair
+  int n;           // columns (FWD: gate and up)
   int tiles_n, splits, kblocks;  // k blocks of a split
-  int stages;
+  int b_bytes, stages;
 };
 
 // Time of a product in clocks, in round numbers: a k block takes its MMAs (a
-// column each 2 clocks at 64 k) or its bytes at 48 a clock, a tile 1500 until
-// the first operands are there, and its epilogue runs beside the next tile's
-// products, except for the last one's.
-double clocks(long long items, int sms, double iters, int n, double epilogue) {
-  const double mma = 2.0 * n, load = (kABytes + n * 128) / 48.0;
+// column two clocks at 64 k) or its bytes at 55 a clock, and 1500 pass until the
+// first operands are there.  Epilogues run beside the next tile's products where
+// TMEM holds two tiles.
+double clocks(long long items, const Tiles& t, int sms, double iters, double epilogue) {
+  const double mma = 2.0 * t.n, load = (kABytes + t.b_bytes) / 55.0;
   const double tile = iters * (mma > load ? mma : load);
-  const double rounds = (double)((items + sms - 1) / sms);
+  const int workers = t.pair ? sms / 2 : sms;
+  const double rounds = (double)((items + workers - 1) / workers);
+  if (t.n > kAccumulator) return rounds * (tile + epilogue) + 1500;
   return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
 }
 
-int stages_of(int n) {
-  const int s = kRing / (kABytes + n * 128);
-  return s < kMaxStages ? s : kMaxStages;
+Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks) {
+  Tiles t = {};
+  t.pair = pair;
+  t.rows = pair ? 2 * kRows : kRows;
+  t.n = n;
+  t.tiles_n = tiles_n;
+  t.splits = splits;
+  t.kblocks = kblocks;
+  t.b_bytes = n * (pair ? 64 : 128);
+  t.stages = kRing / (kABytes + t.b_bytes);
+  if (t.stages > kMaxStages) t.stages = kMaxStages;
+  return t;
 }
 
-Tiles plan_forward(long long M, int C, int H, int products, bool q8, bool grad, int sms) {
-  const int kb = q8 ? 128 : 64;
+Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool grad, int sms) {
+  const int kb = q8 ? 128 : 64, kblocks = (d.C + kb - 1) / kb;
+  // a warp's stretch of columns, of four side by side: 32 of 16 bits, 16 of float32
+  const int stretch = d.dtype == WTCONV_F32 ? 64 : 128;
   Tiles best = {};
   double least = 0;
-  for (int half = 32; half <= 128; half += 32) {
-    const int tn = (H + half - 1) / half;
-    const double iters = (double)((C + kb - 1) / kb) * products;
-    const double epi = (half + 63) / 64 * (grad ? 2400. : 1200.);
-    const double t = clocks((M + kRows - 1) / kRows * tn, sms, iters, 2 * half, epi);
-    if (!best.n || t <= least) {
-      least = t;
-      best.n = 2 * half;
-      best.tiles_n = tn;
-      best.splits = 1;
-      best.kblocks = (C + kb - 1) / kb;
-      best.stages = stages_of(2 * half);
+  for (int pair = 0; pair < 2; ++pair)
+    for (int half = 32; half <= 128; half += 32) {
+      const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks);
+      const long long items = (d.M + t.rows - 1) / t.rows * t.tiles_n;
+      const double c = clocks(items, t, sms, (double)kblocks * products, (half + stretch - 1) / stretch * (grad ? 3000. : 1500.));
+      if (!best.n || c <= least) least = c, best = t;
     }
-  }
   return best;
 }
 
-// Sums alone: `tiles_m` row tiles of N columns over k blocks; few tiles share out
-// k, at least four blocks each, and a second launch adds their sums up.
-Tiles plan_sums(long long tiles_m, int N, long long kblocks, int products, int sms) {
+// Sums alone: M rows (of each of `halves` matrices) of N columns over k blocks; few
+// tiles share out k, at least four blocks each, and a second launch adds their sums
+// up.
+Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products, int sms) {
   Tiles best = {};
   double least = 0;
-  for (int n = 64; n <= kMaxN; n += 64) {
-    const int tn = (N + n - 1) / n;
-    if (n > 64 && n - 64 >= N) break;
-    for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
-      const long long each = (kblocks + want - 1) / want;
-      if (want > 1 && each < 4) break;
-      const int splits = (int)((kblocks + each - 1) / each);
-      double t = clocks(tiles_m * tn * splits, sms, (double)each * products, n, (n + 63) / 64 * 800.);
-      if (splits > 1)  // written and read at about 2500 bytes a clock, and a launch
-        t += 4000 + 8.0 * splits * tiles_m * kRows * N / 2500;
-      if (!best.n || t < least) {
-        least = t;
-        best.n = n;
-        best.tiles_n = tn;
-        best.splits = splits;
-        best.kblocks = (int)each;
-        best.stages = stages_of(n);
+  for (int pair = 0; pair < 2; ++pair)
+    for (int n = pair ? 128 : 64; n <= (pair ? 512 : 256); n += pair ? 128 : 64) {
+      const int tn = (N + n - 1) / n;
+      if (best.n && best.pair == pair && n - (pair ? 128 : 64) >= N) break;
+      for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
+        const long long each = (kblocks + want - 1) / want;
+        if (want > 1 && each < 4) break;
+        const Tiles t = tiles_of(pair, n, tn, (int)((kblocks + each - 1) / each), (int)each);
+        const long long tm = halves * ((M + t.rows - 1) / t.rows);
+        double c = clocks(tm * tn * t.splits, t, sms, (double)each * products, (n + 127) / 128 * 700.);
+        if (t.splits > 1)  // written and read at about 2500 bytes a clock, and a launch
+          c += 4000 + 8.0 * t.splits * tm * t.rows * N / 2500;
+        if (!best.n || c < least) least = c, best = t;
       }
     }
-  }
   return best;
 }
 
@@ -198,18 +201,21 @@ Plan plan_of(const wtconv_gated_desc_t& d, int op) {
     p.up_at = take((size_t)p.parts * d.H * p.pitch * 2);
   }
   const bool grad = op == WTCONV_OP_GATED_BWD;
-  p.fwd = plan_forward(d.M, d.C, d.H, p.products, op == WTCONV_OP_GATED_Q8, grad, sms);
+  p.fwd = plan_forward(d, p.products, op == WTCONV_OP_GATED_Q8, grad, sms);
   if (grad) {
     p.Hp = (int)round_up(d.H, 64);
     p.p_part = d.M * 2 * p.Hp;
     p.p_at = take((size_t)p.parts * p.p_part * 2);
-    const long long tm = (d.M + kRows - 1) / kRows, th = 2 * ((d.H + kRows - 1) / kRows);
-    p.dx = plan_sums(tm, d.C, 2 * (p.Hp / 64), p.products, sms);
-    p.dw = plan_sums(th, d.C, (d.M + 63) / 64, p.products, sms);
+    p.dx = plan_sums(d.M, 1, d.C, 2 * (p.Hp / 64), p.products, sms);
+    p.dw = plan_sums(d.H, 2, d.C, (d.M + 63) / 64, p.products, sms);
     size_t sums = 0;
     const size_t ld = round_up(d.C, 4);
-    if (p.dx.splits > 1) sums = (size_t)p.dx.splits * tm * kRows * ld * 4;
-    if (p.dw.splits > 1 && (size_t)p.dw.splits * th * kRows * ld * 4 > sums) sums = (size_t)p.dw.splits * th * kRows * ld * 4;
+    auto of = [&](const Tiles& t, long long rows, int halves) {
+      const size_t n = (size_t)t.splits * halves * round_up(rows, t.rows) * ld * 4;
+      if (t.splits > 1 && n > sums) sums = n;
+    };
+    of(p.dx, d.M, 1);
+    of(p.dw, d.H, 2);
     p.sum_at = take(sums);
   }
   p.bytes = at;
@@ -243,19 +249,29 @@ cudaError_t make_map(CUtensorMap* m, int type, const void* p, long long cols, in
              : cudaErrorInvalidValue;
 }
 
-template <int EPI, typename T, bool Q8>
+template <int EPI, typename T, bool Q8, bool PAIR>
 cudaError_t launch_gemm(GemmArgs& a, cudaStream_t s) {
   const bool hook = wt::wait_hook_on();
   a.wait = hook ? 1ll << 20 : kWaitCycles;
   a.hold = hook;
   a.faults = ns_fault_count();
   if (!a.faults) return cudaGetLastError();
-  const void* f = (const void*)gated_gemm<EPI, T, Q8>;
+  const void* f = (const void*)gated_gemm<EPI, T, Q8, PAIR>;
   RET(wt::ensure_smem(f, kSmem));
   const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
-  const int sms = wt::sm_count();
-  gated_gemm<EPI, T, Q8><<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, s>>>(a);
-  return cudaGetLastError();
+  const int workers = PAIR ? wt::sm_count() / 2 : wt::sm_count();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(items < workers ? items : workers) * (PAIR ? 2 : 1));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = kSmem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&c, gated_gemm<EPI, T, Q8, PAIR>, (const GemmArgs)a);
 }
 
 // What all products of a call share.
@@ -275,11 +291,13 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_a
   a.splits = t.splits;
   a.group = 16;
   a.n = t.n;
+  a.rows = t.rows;
   a.kblocks = t.kblocks;
   a.parts = c.p.parts;
   a.stages = t.stages;
-  a.b_bytes = t.n * 128;
-  a.idesc = instr_desc(t.n, a_along, b_along) | c.kind;
+  a.b_bytes = t.b_bytes;
+  a.idesc = instr_desc(t.n < kAccumulator ? t.n : kAccumulator, a_along, b_along, t.rows) | c.kind;
+  a.idesc2 = instr_desc(t.n - kAccumulator, a_along, b_along, t.rows) | c.kind;
   a.act = c.d.act;
   a.M = c.d.M;
   a.H = c.d.H;
@@ -323,7 +341,7 @@ template <int EPI, typename T, bool Q8>
 cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
-  set_tiles(a, c, c.p.fwd, (int)((d.M + kRows - 1) / kRows), true, true);
+  set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows), true, true);
   a.load = LOAD_FWD;
   a.half = a.n / 2;
   a.k = d.C;
@@ -340,7 +358,7 @@ cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   RET(make_map(&a.a, c.type, c.x.p, d.C, 1, 0, d.M, c.x.ld, c.p.parts, c.x.part, kRows));
   RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, a.half));
   RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, a.half));
-  return launch_gemm<EPI, T, Q8>(a, c.s);
+  return c.p.fwd.pair ? launch_gemm<EPI, T, Q8, true>(a, c.s) : launch_gemm<EPI, T, Q8, false>(a, c.s);
 }
 
 template <typename T>
@@ -355,8 +373,8 @@ template <typename T>
 cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
-  const int tiles = dw ? (d.H + kRows - 1) / kRows : (int)((d.M + kRows - 1) / kRows);
   const Tiles& t = dw ? c.p.dw : c.p.dx;
+  const int tiles = (int)(((dw ? d.H : d.M) + t.rows - 1) / t.rows);
   set_tiles(a, c, t, dw ? 2 * tiles : tiles, !dw, false);
   a.load = dw ? LOAD_DW : LOAD_DX;
   a.khalf = dw ? (int)((d.M + 63) / 64) : c.p.Hp / 64;
@@ -368,7 +386,7 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
   a.vec = at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)));
   if (t.splits > 1) {
     a.partial = (float*)(c.ws + c.p.sum_at);
-    a.partial_rows = (long long)a.tiles_m * kRows;
+    a.partial_rows = (long long)a.tiles_m * t.rows;
     a.ld = round_up(d.C, 4);
   }
   RET(make_map(&a.a, c.type, a.p, d.H, 2, c.p.Hp, d.M, 2ll * c.p.Hp, c.p.parts, c.p.p_part, dw ? 64 : kRows));
@@ -378,9 +396,9 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
     RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, 64));
     RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, 64));
   }
-  RET((launch_gemm<EPI_OUT, T, false>(a, c.s)));
+  RET((t.pair ? launch_gemm<EPI_OUT, T, false, true>(a, c.s) : launch_gemm<EPI_OUT, T, false, false>(a, c.s)));
   if (t.splits == 1) return cudaSuccess;
-  return dw ? sum_up<T>(c, a, 2ll * d.H, d.H, (long long)tiles * kRows) : sum_up<T>(c, a, d.M, d.M, 0);
+  return dw ? sum_up<T>(c, a, 2ll * d.H, d.H, (long long)tiles * t.rows) : sum_up<T>(c, a, d.M, d.M, 0);
 }
 
 Call call_of(const wtconv_gated_desc_t& d, const GatedArgs& g, int op, void* ws, cudaStream_t s) {

@@ -1,7 +1,10 @@
 // The products behind the gated operators, on tcgen05.
 //
-// One kernel makes them all: D[128 rows, n columns] = A B over k, for tiles
-// that a CTA per SM takes in turn.  Operands come by TMA through a ring of
+// One kernel makes them all: D[rows, n columns] = A B over k, for tiles that a CTA
+// per SM (128 rows), or a pair of them (256), takes in turn.  A pair's CTAs each
+// hold their own rows of A and half of B's columns, and its MMAs read both: a k
+// block of a 256-column tile then takes 32 KB for each SM in place of 48, and the
+// L2 delivers 50 to 60 bytes a clock to each, while the MMAs take 512 clocks.  Operands come by TMA through a ring of
 // 64-wide k blocks (128-byte rows, 128-byte swizzle), either along k (x and the
 // matrices in the forward: rows of the tile) or across it (the gradients'
 // products: rows are k, and what TMA brings is already the transposed
@@ -28,14 +31,14 @@ namespace wtb {
 namespace gated {
 
 constexpr int kRows = 128;         // of a tile
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;    // four for each quarter of the rows
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRing = 196608;      // bytes of operands in flight
 constexpr int kABytes = 16384;     // 128 rows (or two times 64 k) of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr int kStaging = 4096;     // of an epilogue warp: 32 rows of 32 columns, float32, or two of 16 bits
+constexpr int kStaging = 2048;     // of an epilogue warp: 32 rows of 64 bytes
 constexpr int kSmem = kRing + kEpiWarps * kStaging + 1024;
-constexpr int kMaxN = 256;         // columns of an accumulator
+constexpr int kAccumulator = 256;  // columns; a tile of up to 512 has both
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
 enum Epilogue { EPI_H, EPI_P, EPI_OUT };
@@ -50,12 +53,14 @@ struct GemmArgs {
   int load;
   int tiles_m, tiles_n, splits;
   int group;              // tiles are taken in groups of this many row tiles
-  int n, half;            // columns of an accumulator; FWD: gate columns of them
+  int n, half;            // columns of a tile; FWD: gate columns of them
+  int rows;               // of a tile: 128, a pair's 256
   int kblocks, khalf;     // k blocks (of a split, at most), DX: of one matrix
   int k;                  // valid k: C, H (of each half), M
   int parts;              // 1, or 3 for float32
   int stages;
-  uint32_t idesc, b_bytes;
+  uint32_t idesc, idesc2; // of the first 256 columns and of those beyond
+  uint32_t b_bytes;       // of a k block of B, for one CTA
   int act;
   long long M;            // valid rows and columns of the output
   int N, H;
@@ -98,6 +103,11 @@ __device__ __forceinline__ bool wait(Shared& sh, const GemmArgs& a, uint64_t* ba
   return true;
 }
 
+// The CTA's place among those that share out the tiles, and in its pair.
+struct Worker {
+  int first, step, rank;
+};
+
 struct Item {
   int m, n, split;
 };
@@ -132,15 +142,21 @@ __device__ __forceinline__ void drain(const GemmArgs& a, uint64_t* bar, uint32_t
   }
 }
 
-template <bool Q8>
-__device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t ring, int items) {
+template <bool PAIR>
+__device__ __forceinline__ void load(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  if constexpr (PAIR) box_load_pair(dst, map, c0, c1, c2, c3, bar);
+  else box_load(dst, map, c0, c1, c2, c3, bar);
+}
+
+template <bool PAIR, bool Q8>
+__device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t ring, const Worker& w, int items) {
   constexpr int kBlock = Q8 ? 128 : 64;
   const uint32_t bytes = kABytes + a.b_bytes;
   const int products = a.parts == 1 ? 1 : 6;
   uint32_t stage = 0, phase = 1;
   long long issued = 0;
   bool ok = true;
-  for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+  for (int i = w.first; ok && i < items; i += w.step) {
     const Item t = item_of(a, i);
     const int2 blocks = blocks_of(a, t.split);
     for (int q = 0; ok && q < products; ++q) {
@@ -148,24 +164,38 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
         ok = wait(sh, a, &sh.empty[stage], phase);
         if (!ok) break;
-        const uint32_t full = smem_addr(&sh.full[stage]), to = ring + stage * bytes, tb = to + kABytes;
+        const uint32_t own = smem_addr(&sh.full[stage]), to = ring + stage * bytes, tb = to + kABytes;
+        // a pair's copies complete on its first CTA's barrier
+        const uint32_t full = PAIR ? at_rank(own, 0) : own;
         if (elect_one()) {
-          mbar_expect(full, bytes + (a.hold && issued == 0 ? 16 : 0));  // held: more than comes
+          // held: more than comes
+          if (w.rank == 0) mbar_expect(own, (PAIR ? 2 : 1) * bytes + (a.hold && issued == 0 ? 16 : 0));
           if (a.load == LOAD_FWD) {
             const int c = kb * kBlock;
-            box_load(to, &a.a, c, 0, t.m * kRows, pa, full);
-            box_load(tb, &a.b0, c, 0, t.n * a.half, pb, full);
-            box_load(tb + a.half * 128, &a.b1, c, 0, t.n * a.half, pb, full);
-          } else if (a.load == LOAD_DX) {
-            const int second = kb >= a.khalf, h = (kb - (second ? a.khalf : 0)) * 64;
-            box_load(to, &a.a, h, second, t.m * kRows, pa, full);
-            for (int j = 0; j < a.n; j += 64)
-              box_load(tb + j * 128, second ? &a.b1 : &a.b0, t.n * a.n + j, 0, h, pb, full);
+            load<PAIR>(to, &a.a, c, 0, t.m * a.rows + w.rank * kRows, pa, full);
+            if (!PAIR || w.rank == 0) load<PAIR>(tb, &a.b0, c, 0, t.n * a.half, pb, full);
+            if (!PAIR || w.rank == 1) load<PAIR>(PAIR ? tb : tb + a.half * 128, &a.b1, c, 0, t.n * a.half, pb, full);
           } else {
-            const int tiles = a.tiles_m / 2, second = t.m >= tiles, h = (t.m - (second ? tiles : 0)) * kRows;
-            box_load(to, &a.a, h, second, kb * 64, pa, full);
-            box_load(to + 8192, &a.a, h + 64, second, kb * 64, pa, full);
-            for (int j = 0; j < a.n; j += 64) box_load(tb + j * 128, &a.b0, t.n * a.n + j, 0, kb * 64, pb, full);
+            // B's columns of this CTA: of each accumulator's a pair's half
+            const void* from = &a.b0;
+            int row = kb * 64;
+            if (a.load == LOAD_DX) {
+              const int second = kb >= a.khalf;
+              row -= second ? a.khalf * 64 : 0;
+              if (second) from = &a.b1;
+              load<PAIR>(to, &a.a, row, second, t.m * a.rows + w.rank * kRows, pa, full);
+            } else {
+              const int tiles = a.tiles_m / 2, second = t.m >= tiles;
+              const int h = (t.m - (second ? tiles : 0)) * a.rows + w.rank * kRows;
+              load<PAIR>(to, &a.a, h, second, row, pa, full);
+              load<PAIR>(to + 8192, &a.a, h + 64, second, row, pa, full);
+            }
+            uint32_t b = tb;
+            for (int j = 0; j < a.n; j += kAccumulator) {
+              const int some = min(kAccumulator, a.n - j) / (PAIR ? 2 : 1);
+              for (int k = 0; k < some; k += 64, b += 8192)
+                load<PAIR>(b, from, t.n * a.n + j + w.rank * some + k, 0, row, pb, full);
+            }
           }
         }
         __syncwarp();
@@ -174,24 +204,37 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
       }
     }
   }
+  if (w.rank == 0) {
   for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
+  } else if (!ok || sh.dead) {
+    // The first CTA's barriers say nothing of copies that it did not ask for
+    // itself; they land in a fraction of this time.
+    const long long t0 = clock64();
+    while (clock64() - t0 < a.wait) {
+    }
+  }
 }
 
-template <bool Q8>
-__device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t ring, uint32_t tmem, int items) {
+// The MMAs, by a CTA's second warp; a pair's by its first CTA's.
+template <bool PAIR, bool Q8>
+__device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t ring, uint32_t tmem, const Worker& w, int items) {
   constexpr int kBlock = Q8 ? 128 : 64, kStep = Q8 ? 32 : 16;
   const uint32_t bytes = kABytes + a.b_bytes;
   const bool a_along = a.load != LOAD_DW, b_along = a.load == LOAD_FWD;
   const uint32_t step_a = desc_step(a_along), step_b = desc_step(b_along);
-  const int products = a.parts == 1 ? 1 : 6;
+  const int products = a.parts == 1 ? 1 : 6, buffers = a.n > kAccumulator ? 1 : 2;
+  auto commit = [](uint64_t* bar) {
+    if constexpr (PAIR) mma_commit_pair(smem_addr(bar));
+    else mma_commit(smem_addr(bar));
+  };
   uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
   bool ok = true;
-  for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+  for (int i = w.first; ok && i < items; i += w.step) {
     const int2 blocks = blocks_of(a, item_of(a, i).split);
     ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
     if (!ok) break;
     tc_fence_after();
-    const uint32_t d = tmem + acc * kMaxN;
+    const uint32_t d = tmem + acc * kAccumulator;
     uint32_t accumulate = 0;
     for (int q = 0; ok && q < products; ++q)
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
@@ -204,89 +247,104 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
         const uint32_t la = desc_low(from, a_along), lb = desc_low(from + kABytes, b_along);
         if (elect_one()) {
           for (int s = 0; s < steps; ++s) {
-            if constexpr (Q8) mma_f8(d, la + s * step_a, lb + s * step_b, kDescHigh, a.idesc, accumulate);
-            else mma_f16(d, la + s * step_a, lb + s * step_b, kDescHigh, a.idesc, accumulate);
+            mma_step<PAIR, Q8>(d, la + s * step_a, lb + s * step_b, kDescHigh, a.idesc, accumulate);
+            if (buffers == 1)  // what lies beyond the first 256 columns
+              mma_step<PAIR, Q8>(d + kAccumulator, la + s * step_a, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * step_b, kDescHigh,
+                                 a.idesc2, accumulate);
             accumulate = 1;
           }
-          mma_commit(smem_addr(&sh.empty[stage]));
+          commit(&sh.empty[stage]);
         }
         accumulate = 1;
         __syncwarp();
         if (++stage == (uint32_t)a.stages) stage = 0, phase ^= 1;
       }
-    if (ok && elect_one()) mma_commit(smem_addr(&sh.acc_full[acc]));
+    if (ok && elect_one()) commit(&sh.acc_full[acc]);
     __syncwarp();
-    acc ^= 1;
-    if (acc == 0) acc_phase ^= 1;
+    if (++acc == (uint32_t)buffers) acc = 0, acc_phase ^= 1;
   }
   if (elect_one()) {
-    mma_commit(smem_addr(&sh.drain));
+    commit(&sh.drain);
     drain(a, &sh.drain, 0);
   }
   __syncwarp();
 }
 
-// A warp's staging area: 32 rows of CHUNKS 16-byte chunks, which eight rows in
-// turn spread over all banks.
-template <int CHUNKS>
+// A warp's staging area: 32 rows of four 16-byte chunks, which eight rows in turn
+// spread over all banks.
 __device__ __forceinline__ uint4* staged(unsigned char* buf, int row, int chunk) {
-  const int turn = CHUNKS == 4 ? (row >> 1) & 3 : row & 7;
-  return reinterpret_cast<uint4*>(buf + row * (CHUNKS * 16) + ((chunk ^ turn) << 4));
+  return reinterpret_cast<uint4*>(buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// Copies 32 rows x 32 columns between the staging area and global memory, rows
-// `ld` elements apart, of which `rows` and `cols` exist.
-template <typename T, bool STORE>
-__device__ __forceinline__ void copy_tile(unsigned char* buf, T* p, long long ld, int rows, int cols, bool vec) {
-  constexpr int kEach = 16 / sizeof(T), kChunks = 32 / kEach;
+// Copies 32 rows x 64 bytes from the staging area to global memory, rows `ld`
+// elements apart, of which `rows` and `cols` exist.  `vec`: rows start on 16-byte
+// boundaries, and what is written beyond `cols` up to the next one is padding.
+template <typename T>
+__device__ __forceinline__ void copy_out(unsigned char* buf, T* p, long long ld, int rows, int cols, bool vec) {
+  constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   if (vec) {
+    const int q = lane & 3;
+    p += (lane >> 2) * ld + q * kEach;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int row = i * (32 / kChunks) + lane / kChunks, q = lane % kChunks;
-      if (row < rows && q * kEach < cols) {
-        uint4* g = reinterpret_cast<uint4*>(p + row * ld + q * kEach);
-        if constexpr (STORE) *g = *staged<kChunks>(buf, row, q);
-        else *staged<kChunks>(buf, row, q) = *g;
-      }
-    }
+    for (int i = 0; i < 4; ++i, p += 8 * ld)
+      if (i * 8 + (lane >> 2) < rows && q * kEach < cols)
+        *reinterpret_cast<uint4*>(p) = *staged(buf, i * 8 + (lane >> 2), q);
   } else if (lane < cols) {
-    for (int row = 0; row < rows; ++row) {
-      T* s = reinterpret_cast<T*>(staged<kChunks>(buf, row, lane / kEach)) + lane % kEach;
-      if constexpr (STORE) p[row * ld + lane] = *s;
-      else *s = p[row * ld + lane];
-    }
+    for (int row = 0; row < rows; ++row)
+      p[row * ld + lane] = reinterpret_cast<const T*>(staged(buf, row, lane / kEach))[lane % kEach];
   }
 }
-
+// The same from global memory.  Whole accesses are asynchronous: copied_in() waits.
 template <typename T>
-__device__ __forceinline__ void put_row(unsigned char* buf, const float (&v)[32]) {
-  constexpr int kEach = 16 / sizeof(T), kChunks = 32 / kEach;
+__device__ __forceinline__ void copy_in(unsigned char* buf, const T* p, long long ld, int rows, int cols, bool vec) {
+  constexpr int kEach = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  if (vec) {
+    const int q = lane & 3;
+    p += (lane >> 2) * ld + q * kEach;
 #pragma unroll
-  for (int q = 0; q < kChunks; ++q) {
+    for (int i = 0; i < 4; ++i, p += 8 * ld)
+      if (i * 8 + (lane >> 2) < rows && q * kEach < cols) copy16(smem_addr(staged(buf, i * 8 + (lane >> 2), q)), p);
+  } else if (lane < cols) {
+    for (int row = 0; row < rows; ++row)
+      reinterpret_cast<T*>(staged(buf, row, lane / kEach))[lane % kEach] = p[row * ld + lane];
+  }
+}
+__device__ __forceinline__ void copied_in() {
+  copy16_wait();
+  __syncwarp();
+}
+
+// This lane's row of the staging area: N values of T, from a chunk on.
+template <typename T, int N>
+__device__ __forceinline__ void put_row(unsigned char* buf, const float (&v)[N], int first = 0) {
+  constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+  for (int q = 0; q < N / kEach; ++q) {
     float2 t[kEach / 2];
 #pragma unroll
     for (int i = 0; i < kEach / 2; ++i) t[i] = make_float2(v[q * kEach + 2 * i], v[q * kEach + 2 * i + 1]);
-    gn::store_pairs<T, kEach>(reinterpret_cast<T*>(staged<kChunks>(buf, threadIdx.x & 31, q)), t);
+    gn::store_pairs<T, kEach>(reinterpret_cast<T*>(staged(buf, threadIdx.x & 31, first + q)), t);
   }
 }
-template <typename T>
-__device__ __forceinline__ void get_row(unsigned char* buf, float (&v)[32]) {
-  constexpr int kEach = 16 / sizeof(T), kChunks = 32 / kEach;
+template <typename T, int N>
+__device__ __forceinline__ void get_row(unsigned char* buf, float (&v)[N], int first = 0) {
+  constexpr int kEach = 16 / sizeof(T);
 #pragma unroll
-  for (int q = 0; q < kChunks; ++q) {
+  for (int q = 0; q < N / kEach; ++q) {
     float2 t[kEach / 2];
-    gn::load_pairs<T, kEach>(reinterpret_cast<const T*>(staged<kChunks>(buf, threadIdx.x & 31, q)), t);
+    gn::load_pairs<T, kEach>(reinterpret_cast<const T*>(staged(buf, threadIdx.x & 31, first + q)), t);
 #pragma unroll
     for (int i = 0; i < kEach / 2; ++i) v[q * kEach + 2 * i] = t[i].x, v[q * kEach + 2 * i + 1] = t[i].y;
   }
 }
 
-// h = act(g) u, or dg into g and du into u.
-template <int ACT, bool P>
-__device__ __forceinline__ void gate_act(float (&g)[32], float (&u)[32], const float (&dh)[P ? 32 : 1]) {
+// h = act(g) u into g, or dg into g and du into u.
+template <int ACT, bool P, int N>
+__device__ __forceinline__ void gate_act(float (&g)[N], float (&u)[N], const float (&dh)[P ? N : 1]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     const float2 z = make_float2(g[i], g[i + 1]), v = make_float2(u[i], u[i + 1]);
     if constexpr (P) {
       const float2 d = make_float2(dh[i], dh[i + 1]);
@@ -299,6 +357,12 @@ __device__ __forceinline__ void gate_act(float (&g)[32], float (&u)[32], const f
     }
   }
 }
+template <bool P, int N>
+__device__ __forceinline__ void gate_act(int act, float (&g)[N], float (&u)[N], const float (&dh)[P ? N : 1]) {
+  if (act == ACT_SILU) gate_act<ACT_SILU, P>(g, u, dh);
+  else if (act == ACT_GELU) gate_act<ACT_GELU, P>(g, u, dh);
+  else gate_act<ACT_NONE, P>(g, u, dh);
+}
 
 // The next part of a float32 value: its nearest bfloat16, and what is left.  An
 // infinity or a NaN is its own first part; a value that would round to infinity
@@ -310,135 +374,181 @@ __device__ __forceinline__ __nv_bfloat16 take_part(float& v) {
   v = fabsf(v) <= 3.4028235e38f ? left : 0.f;
   return h;
 }
-__device__ __forceinline__ void put_part(unsigned char* buf, float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void put_part(unsigned char* buf, float (&v)[N]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < N / 8; ++q) {
     Vec<__nv_bfloat16, 8> t;
 #pragma unroll
     for (int i = 0; i < 8; ++i) t.e[i] = take_part(v[q * 8 + i]);
-    *staged<4>(buf, threadIdx.x & 31, q) = t.r;
+    *staged(buf, threadIdx.x & 31, q) = t.r;
   }
 }
 
-template <int EPI, typename T>
-__device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, int items) {
+// Sums of N columns as rows of T, from column n0 on.
+template <typename T, int N>
+__device__ __forceinline__ void store_sums(unsigned char* buf, uint32_t from, bool got, T* p, long long ld, int rows, int cols,
+                                           bool vec) {
+  float v[N];
+  tmem_load<N>(from, v);
+  if (!got) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __int_as_float(0x7FC00000);
+  }
+  put_row<T>(buf, v);
+  __syncwarp();
+  copy_out<T>(buf, p, ld, rows, cols, vec);
+  __syncwarp();
+}
+
+// A hidden unit's scale: of gate for the first sixteen lanes, of up for the others.
+__device__ __forceinline__ float unit_scale(const GemmArgs& a, int n, int lane) {
+  return __ldg((lane < 16 ? a.gate_scale : a.up_scale) + n);
+}
+
+// Sixteen warps, four to each quarter of a tile's rows (TMEM opens its lanes to
+// warps by their number), each with every fourth stretch of 64 bytes of columns: 32
+// of 16 bits, 16 of float32.  What they write goes through a staging area of 2 KB,
+// so that whole 64-byte stretches of a row reach memory at once; dh comes the same
+// way, asked for when the warp is done with the tile before.  With eight warps the
+// epilogue of short contractions was bound by latency (200704 x 96 -> 256 forward
+// 52 us, now WAITING).
+template <int EPI, typename T, bool PAIR>
+__device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
+  constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
-  // TMEM lanes are open to warps by their number in the CTA
   const int quadrant = (warp + 2) & 3, side = warp / 4;
   unsigned char* buf = staging + warp * kStaging;
-  float* scale = reinterpret_cast<float*>(buf);  // of a chunk's columns, before its rows are staged
+  const int width = EPI == EPI_OUT ? a.n : a.half;
+  const int buffers = width > kAccumulator ? 1 : 2;
+  auto row_of = [&](const Item& t) { return (long long)t.m * a.rows + w.rank * kRows + quadrant * 32; };
+  auto rows_of = [&](const Item& t) { return (int)max(0ll, min(32ll, a.M - row_of(t))); };
+  // dh of a stretch of columns, if the tile has it
+  auto fetch = [&](const Item& t, int c) {
+    const int n0 = t.n * a.half + c;
+    const long long m0 = row_of(t);
+    if (c < a.half && n0 < a.H)
+      copy_in<T>(buf, (const T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, rows_of(t), min(kCols, a.H - n0), a.vec & 2);
+  };
   uint32_t acc = 0, phase = 0;
   bool got = true;
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+  if constexpr (EPI == EPI_P)
+    if (w.first < items) fetch(item_of(a, w.first), side * kCols);
+  for (int i = w.first; i < items; i += w.step) {
     const Item t = item_of(a, i);
-    const long long row0 = (long long)t.m * kRows + quadrant * 32;
+    const long long m0 = row_of(t);
+    const int rows = rows_of(t);
     got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
     tc_fence_after();
-    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * kMaxN;
-    const int width = EPI == EPI_OUT ? a.n : a.half;
-    for (int c = side * 32; c < width; c += 64) {
-      const long long m0 = row0;
-      const int rows = (int)max(0ll, min(32ll, a.M - m0));
-      float g[32];
-      tmem_load32(from + c, g);
-      if constexpr (EPI == EPI_OUT) {
-        tmem_wait_load();
-        tmem_loaded(g);
+    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * kAccumulator;
+    if constexpr (EPI == EPI_OUT) {
+      long long m = m0;
+      int left = rows;
+      T* out = (T*)a.out;
+      if (a.load == LOAD_DW) {  // rows are hidden units, of gate in the first half of the tiles, of up in the second
+        const int tiles = a.tiles_m / 2;
+        if (t.m >= tiles) m -= (long long)tiles * a.rows, out = (T*)a.out2;
+        left = (int)max(0ll, min(32ll, a.H - m));
+      }
+      if (a.partial) {
+        float* p = a.partial + (t.split * a.partial_rows + m0) * a.ld;
+        for (int c = side * 16; c < width && t.n * a.n + c < a.N; c += 64)
+          store_sums<float, 16>(buf, from + c, got, p + t.n * a.n + c, a.ld, left, min(16, a.N - t.n * a.n - c), true);
       } else {
-        const int n0 = t.n * a.half + c, cols = min(32, a.H - n0);
-        float u[32], dh[EPI == EPI_P ? 32 : 1];
-        tmem_load32(from + a.half + c, u);
+        out += m * a.ld;
+        for (int c = side * kCols; c < width && t.n * a.n + c < a.N; c += 4 * kCols)
+          store_sums<T, kCols>(buf, from + c, got, out + t.n * a.n + c, a.ld, left, min(kCols, a.N - t.n * a.n - c), a.vec & 1);
+      }
+    } else {
+      for (int c = side * kCols; c < width; c += 4 * kCols) {
+        const int n0 = t.n * a.half + c, cols = min(kCols, a.H - n0);
+        if (cols <= 0) break;
         if constexpr (EPI == EPI_P) {
-          if (cols > 0) copy_tile<T, false>(buf, (T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, rows, cols, a.vec & 2);
-          __syncwarp();
-          get_row<T>(buf, dh);
+          if (c >= 4 * kCols) fetch(t, c);
+          copied_in();
         }
-        tmem_wait_load();
-        tmem_loaded(g);
-        tmem_loaded(u);
-        if (!got) {
+        // sixteen columns at a time: 18 warps leave a thread 96 registers
+        float g[16], u[16], dh[EPI == EPI_P ? 16 : 1];
+        uint4 second[EPI == EPI_P && sizeof(T) == 2 ? kCols / 8 : 1];  // du, until dg has left the staging area
 #pragma unroll
-          for (int j = 0; j < 32; ++j) g[j] = u[j] = __int_as_float(0x7FC00000);
-        }
-        if (cols > 0) {
-          if (a.x_scale) {
-            const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
-            __syncwarp();
-            scale[lane] = lane < cols ? a.gate_scale[n0 + lane] : 0.f;
-            scale[32 + lane] = lane < cols ? a.up_scale[n0 + lane] : 0.f;
-            __syncwarp();
+        for (int h = 0; h < kCols / 16; ++h) {
+          constexpr int kHalf = 16 * sizeof(T) / 16;  // chunks
+          if constexpr (EPI == EPI_P) get_row<T>(buf, dh, h * kHalf);
+          tmem_load2<16>(from + c + h * 16, g, from + a.half + c + h * 16, u);
+          if (!got) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] *= xs * scale[j], u[j] *= xs * scale[32 + j];
+            for (int j = 0; j < 16; ++j) g[j] = u[j] = __int_as_float(0x7FC00000);
           }
-          if (a.act == ACT_SILU) gate_act<ACT_SILU, EPI == EPI_P>(g, u, dh);
-          else if (a.act == ACT_GELU) gate_act<ACT_GELU, EPI == EPI_P>(g, u, dh);
-          else gate_act<ACT_NONE, EPI == EPI_P>(g, u, dh);
-          __syncwarp();
           if constexpr (EPI == EPI_H) {
-            put_row<T>(buf, g);
-            __syncwarp();
-            copy_tile<T, true>(buf, (T*)a.out + m0 * a.ld + n0, a.ld, rows, cols, a.vec & 1);
-          } else if constexpr (sizeof(T) == 2) {
-            T* p = (T*)a.p + m0 * 2 * a.Hp + n0;
-            put_row<T>(buf, g);
-            put_row<T>(buf + 2048, u);
-            __syncwarp();
-            copy_tile<T, true>(buf, p, 2 * a.Hp, rows, cols, true);
-            copy_tile<T, true>(buf + 2048, p + a.Hp, 2 * a.Hp, rows, cols, true);
-          } else {
-            __nv_bfloat16* p = (__nv_bfloat16*)a.p + m0 * 2 * a.Hp + n0;
-            for (int part = 0; part < 3; ++part, p += a.p_part) {
-              put_part(buf, g);
-              put_part(buf + 2048, u);
-              __syncwarp();
-              copy_tile<__nv_bfloat16, true>(buf, p, 2 * a.Hp, rows, cols, true);
-              copy_tile<__nv_bfloat16, true>(buf + 2048, p + a.Hp, 2 * a.Hp, rows, cols, true);
-              __syncwarp();
+            if (a.x_scale) {
+              const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
+              const int n = min(n0 + h * 16 + (lane & 15), a.H - 1);
+              const float w = unit_scale(a, n, lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                g[j] *= xs * __shfl_sync(~0u, w, j);
+                u[j] *= xs * __shfl_sync(~0u, w, 16 + j);
+              }
+            }
+          }
+          gate_act<EPI == EPI_P>(a.act, g, u, dh);
+          if constexpr (EPI == EPI_H || sizeof(T) == 2) put_row<T>(buf, g, h * kHalf);  // a lane's row of dh is its own
+          if constexpr (EPI == EPI_P && sizeof(T) == 2) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              Vec<T, 8> o;
+              float2 pairs[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) pairs[j] = make_float2(u[q * 8 + 2 * j], u[q * 8 + 2 * j + 1]);
+              gn::store_pairs<T, 8>(o.e, pairs);
+              second[h * 2 + q] = o.r;
             }
           }
         }
-        __syncwarp();
-      }
-      if constexpr (EPI == EPI_OUT) {
-        const int n0 = t.n * a.n + c, cols = min(32, a.N - n0);
-        long long m = m0;
-        int left = rows;
-        void* out = a.out;
-        if (a.load == LOAD_DW) {
-          const int tiles = a.tiles_m / 2, second = t.m >= tiles;
-          m -= second ? (long long)tiles * kRows : 0;
-          left = (int)max(0ll, min(32ll, a.H - m));
-          if (second) out = a.out2;
-        }
-        if (!got) {
+        if constexpr (EPI == EPI_H) {
+          __syncwarp();
+          copy_out<T>(buf, (T*)a.out + m0 * a.ld + n0, a.ld, rows, cols, a.vec & 1);
+          __syncwarp();
+        } else if constexpr (sizeof(T) == 2) {
+          T* p = (T*)a.p + m0 * 2 * a.Hp + n0;
+          __syncwarp();
+          copy_out<T>(buf, p, 2 * a.Hp, rows, cols, true);
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) g[j] = __int_as_float(0x7FC00000);
-        }
-        if (cols > 0) {
-          if (a.partial) {
-            // rows of the second half follow the first's tiles
-            float* p = a.partial + (t.split * a.partial_rows + m0) * a.ld + n0;
-            put_row<float>(buf, g);
+          for (int q = 0; q < 4; ++q) *staged(buf, lane, q) = second[q];
+          __syncwarp();
+          copy_out<T>(buf, p + a.Hp, 2 * a.Hp, rows, cols, true);
+          __syncwarp();
+        } else {
+          __nv_bfloat16* p = (__nv_bfloat16*)a.p + m0 * 2 * a.Hp + n0;
+          for (int part = 0; part < 3; ++part, p += a.p_part) {
+            put_part(buf, g);
             __syncwarp();
-            copy_tile<float, true>(buf, p, a.ld, left, cols, true);
-          } else {
-            put_row<T>(buf, g);
+            copy_out<__nv_bfloat16>(buf, p, 2 * a.Hp, rows, cols, true);
             __syncwarp();
-            copy_tile<T, true>(buf, (T*)out + m * a.ld + n0, a.ld, left, cols, a.vec & 1);
+            put_part(buf, u);
+            __syncwarp();
+            copy_out<__nv_bfloat16>(buf, p + a.Hp, 2 * a.Hp, rows, cols, true);
+            __syncwarp();
           }
         }
-        __syncwarp();
       }
+      if constexpr (EPI == EPI_P)
+        if (i + w.step < items) fetch(item_of(a, i + w.step), side * kCols);
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&sh.acc_empty[acc]));
-    acc ^= 1;
-    if (acc == 0) phase ^= 1;
+    if (lane == 0) {
+      const uint32_t bar = smem_addr(&sh.acc_empty[acc]);
+      if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
+      else mbar_arrive(bar);
+    }
+    if (++acc == (uint32_t)buffers) acc = 0, phase ^= 1;
   }
+  copy16_wait();
 }
 
-template <int EPI, typename T, bool Q8>
+template <int EPI, typename T, bool Q8, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant__ GemmArgs a) {
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
@@ -446,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   unsigned char* staging = raw + (base - smem_addr(raw)) + kRing;
   const int warp = threadIdx.x / 32;
   const int items = a.tiles_m * a.tiles_n * a.splits;
+  Worker w = {(int)blockIdx.x, (int)gridDim.x, 0};
+  if constexpr (PAIR) w = {(int)blockIdx.x / 2, (int)gridDim.x / 2, (int)cluster_rank()};
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 1);
@@ -453,23 +565,35 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.acc_full[i]), 1);
-      mbar_init(smem_addr(&sh.acc_empty[i]), kEpiWarps);
+      mbar_init(smem_addr(&sh.acc_empty[i]), kEpiWarps * (PAIR ? 2 : 1));
     }
     mbar_init(smem_addr(&sh.drain), 1);
     sh.dead = 0;
     mbar_init_done();
   }
-  if (warp == 1) tmem_alloc(smem_addr(&sh.tmem), 2 * kMaxN);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(smem_addr(&sh.tmem), 2 * kAccumulator);
+    else tmem_alloc(smem_addr(&sh.tmem), 2 * kAccumulator);
+  }
+  if constexpr (PAIR) cluster_meet();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  if (warp == 0) produce<Q8>(sh, a, base, items);
-  else if (warp == 1) multiply<Q8>(sh, a, base, tmem, items);
-  else epilogue<EPI, T>(sh, a, staging, tmem, items);
+  if (warp == 0) {
+    produce<PAIR, Q8>(sh, a, base, w, items);
+  } else if (warp == 1) {
+    if (w.rank == 0) multiply<PAIR, Q8>(sh, a, base, tmem, w, items);
+  } else {
+    epilogue<EPI, T, PAIR>(sh, a, staging, tmem, w, items);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_meet();  // the other CTA's MMAs, copies and arrivals touch this one
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, 2 * kMaxN);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_free_pair(tmem, 2 * kAccumulator);
+    else tmem_free(tmem, 2 * kAccumulator);
+  }
 }
 
 }  // namespace gated

@@ -53,6 +53,13 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// 16 bytes global -> shared by one lane, asynchronous; copy16_wait() waits for the
+// lane's own.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A box of a tensor map -> shared, completing on an mbarrier.  The innermost
 // coordinate is a multiple of 16 bytes; what lies outside reads as zero and
 // counts among the bytes.
@@ -61,6 +68,35 @@ __device__ __forceinline__ void box_load(uint32_t dst, const void* map, int c0, 
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
+}
+
+// The same by a CTA of a pair, completing on a barrier of either one (`bar` is a
+// cluster address).
+__device__ __forceinline__ void box_load_pair(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// A shared address of this CTA as the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// All threads of the cluster meet; what they wrote to shared memory before is visible.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Orders this thread's generic accesses against bulk copies.
@@ -92,6 +128,16 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
   __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
+// The same by one warp of each CTA of a pair.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t where, uint32_t columns) {
+  __syncwarp();
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t tmem, uint32_t columns) {
+  __syncwarp();
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -106,18 +152,31 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(accumulate)
       : "memory");
 }
-// The same for a K = 32 step of e4m3 operands.
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; .reg .b64 x, y;\n"
-      "mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3}; setp.ne.b32 p, %5, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "r"(high), "r"(idesc),
-      "r"(accumulate)
-      : "memory");
+// A step of 32 bytes along K for one CTA or a pair, float16 or bfloat16 (K = 16) or
+// e4m3 operands (K = 32).
+template <bool PAIR, bool Q8>
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t accumulate) {
+#define WTB_MMA(what)                                                          \
+  asm volatile(                                                                \
+      "{ .reg .pred p; .reg .b64 x, y;\n"                                      \
+      "mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3}; setp.ne.b32 p, %5, 0;\n"      \
+      "tcgen05.mma." what " [%0], x, y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(accumulate) \
+      : "memory")
+  if constexpr (PAIR && Q8) WTB_MMA("cta_group::2.kind::f8f6f4");
+  else if constexpr (PAIR) WTB_MMA("cta_group::2.kind::f16");
+  else if constexpr (Q8) WTB_MMA("cta_group::1.kind::f8f6f4");
+  else WTB_MMA("cta_group::1.kind::f16");
+#undef WTB_MMA
 }
 // The barrier completes when every MMA issued so far has.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same for a pair's MMAs, on that barrier of both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((unsigned short)3)
+               : "memory");
 }
 
 // 8 consecutive columns of this warp's 32 lanes; valid after tmem_wait_load().
@@ -127,15 +186,19 @@ __device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                : "r"(addr));
 }
-// 32 consecutive columns of this warp's 32 lanes.
+// 16 or 32 consecutive columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_wait_load() {
@@ -148,11 +211,33 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[8]) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
 }
 
-__device__ __forceinline__ void tmem_loaded(float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]),
                  "+f"(v[i + 7]));
+}
+// N columns (16 or 32) from one place, or from each of two, ready for use.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t from, float (&v)[N]) {
+  if constexpr (N == 16) tmem_load16(from, v);
+  else tmem_load32(from, v);
+  tmem_wait_load();
+  tmem_loaded<N>(v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_load2(uint32_t from, float (&v)[N], uint32_t from2, float (&w)[N]) {
+  if constexpr (N == 16) {
+    tmem_load16(from, v);
+    tmem_load16(from2, w);
+  } else {
+    tmem_load32(from, v);
+    tmem_load32(from2, w);
+  }
+  tmem_wait_load();
+  tmem_loaded<N>(v);
+  tmem_loaded<N>(w);
 }
 
 // Shared-memory descriptor of a 128-byte-swizzled operand tile made of 64 x 64
@@ -169,10 +254,10 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, bool k_major, uint32
 }
 // What a K = 16 step adds to it: 32 bytes along K, or 16 rows of 128 bytes.
 __device__ __forceinline__ uint32_t desc_step(bool k_major) { return k_major ? 32u >> 4 : 2048u >> 4; }
-// M = 128, N columns, float16 operands, float32 accumulator.
-__host__ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_k_major, bool b_k_major) {
+// M = 128 (a pair: 256), N columns, float16 operands, float32 accumulator.
+__host__ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_k_major, bool b_k_major, int m = 128) {
   return (1u << 4) | ((a_k_major ? 0u : 1u) << 15) | ((b_k_major ? 0u : 1u) << 16) | ((uint32_t)(n >> 3) << 17) |
-         ((128u >> 4) << 24);
+         ((uint32_t)(m >> 4) << 24);
 }
 
 }  // namespace wtb

@@ -113,7 +113,7 @@ double clocks(long long items, const Tiles& t, int sms, double iters, double epi
   return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
 }
 
-Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks) {
+Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, bool p = false) {
   Tiles t = {};
   t.pair = pair;
   t.rows = pair ? 2 * kRows : kRows;
@@ -122,7 +122,7 @@ Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks) {
   t.splits = splits;
   t.kblocks = kblocks;
   t.b_bytes = n * (pair ? 64 : 128);
-  t.stages = kRing / (kABytes + t.b_bytes);
+  t.stages = (p ? kRing<true> : kRing<false>) / (kABytes + t.b_bytes);
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   return t;
 }
@@ -135,7 +135,7 @@ Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool gra
   double least = 0;
   for (int pair = 0; pair < 2; ++pair)
     for (int half = 32; half <= 128; half += 32) {
-      const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks);
+      const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks, grad);
       const long long items = (d.M + t.rows - 1) / t.rows * t.tiles_n;
       const double c = clocks(items, t, sms, (double)kblocks * products, (half + stretch - 1) / stretch * (grad ? 3000. : 1500.));
       if (!best.n || c <= least) least = c, best = t;
@@ -230,23 +230,30 @@ Plan plan_of(const wtconv_gated_desc_t& d, int op) {
     if (e_ != cudaSuccess) return e_;        \
   } while (0)
 
-// columns x halves x rows x parts; boxes of 128 bytes x `box_rows`
+// columns x halves x rows x parts; boxes of 128 or 64 bytes x `box_rows`, swizzled
+// over as many
 cudaError_t make_map(CUtensorMap* m, int type, const void* p, long long cols, int halves, long long half_ld, long long rows,
-                     long long ld, int parts, long long part_ld, int box_rows) {
+                     long long ld, int parts, long long part_ld, int box_rows, int box_bytes = 128) {
   wt::EncodeTiledFn fn = wt::encode_tiled();
   if (!fn) return cudaErrorNotSupported;
-  const int es = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
+  const int es = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   if (halves == 1) half_ld = ld;
   if (rows == 1) ld = round_up(cols, 16 / es);
   if (parts == 1) part_ld = ld;
   const cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)halves, (cuuint64_t)rows, (cuuint64_t)parts};
   const cuuint64_t strides[3] = {(cuuint64_t)((halves == 1 ? ld : half_ld) * es), (cuuint64_t)(ld * es), (cuuint64_t)(part_ld * es)};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1u, (cuuint32_t)box_rows, 1u};
+  const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / es), 1u, (cuuint32_t)box_rows, 1u};
   const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
   return fn(m, (CUtensorMapDataType)type, 4, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
+}
+
+template <typename T>
+int map_type() {
+  return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
 template <int EPI, typename T, bool Q8, bool PAIR>
@@ -290,6 +297,10 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_a
   a.tiles_n = t.tiles_n;
   a.splits = t.splits;
   a.group = 16;
+  a.by_split = divisor(a.tiles_m * a.tiles_n);
+  a.by_group = divisor(a.group * a.tiles_n);
+  a.by_rows = divisor(a.group);
+  a.by_last = divisor(a.tiles_m - (a.tiles_m - 1) / a.group * a.group);
   a.n = t.n;
   a.rows = t.rows;
   a.kblocks = t.kblocks;
@@ -350,8 +361,17 @@ cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   a.dh = g.dh;
   a.dh_ld = d.dh_stride;
   const int each = 16 / (int)sizeof(T);
-  a.vec = (g.h && at16(g.h, d.H, sizeof(T)) ? 1 : 0) |
-          (g.dh && d.H % each == 0 && (uintptr_t)g.dh % 16 == 0 && (d.M == 1 || d.dh_stride % each == 0) ? 2 : 0);
+  const int type = map_type<T>();
+  if (EPI == EPI_H && at16(g.h, d.H, sizeof(T))) {
+    a.boxes = 1;
+    RET(make_map(&a.o0, type, g.h, d.H, 1, 0, d.M, d.H, 1, 0, 32, 64));
+  } else if (EPI == EPI_P) {
+    RET(make_map(&a.o0, c.type, a.p, d.H, 2, c.p.Hp, d.M, 2ll * c.p.Hp, c.p.parts, c.p.p_part, 32, 64));
+    if ((uintptr_t)g.dh % 16 == 0 && (d.M == 1 || d.dh_stride % each == 0)) {
+      a.boxes = 2;
+      RET(make_map(&a.dh_map, type, g.dh, d.H, 1, 0, d.M, d.dh_stride, 1, 0, 32, 64));
+    }
+  }
   a.x_scale = g.x_scale;
   a.gate_scale = g.gate_scale;
   a.up_scale = g.up_scale;
@@ -383,11 +403,16 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
   a.out = dw ? g.dgate : g.dx;
   a.out2 = g.dup;
   a.ld = d.C;
-  a.vec = at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)));
   if (t.splits > 1) {
     a.partial = (float*)(c.ws + c.p.sum_at);
     a.partial_rows = (long long)a.tiles_m * t.rows;
     a.ld = round_up(d.C, 4);
+    RET(make_map(&a.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.partial, d.C, 1, 0, a.splits * a.partial_rows, a.ld, 1, 0, 32, 64));
+  } else if (at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)))) {
+    a.boxes = 1;
+    const long long rows = dw ? d.H : d.M;
+    RET(make_map(&a.o0, map_type<T>(), a.out, d.C, 1, 0, rows, d.C, 1, 0, 32, 64));
+    if (dw) RET(make_map(&a.o1, map_type<T>(), a.out2, d.C, 1, 0, rows, d.C, 1, 0, 32, 64));
   }
   RET(make_map(&a.a, c.type, a.p, d.H, 2, c.p.Hp, d.M, 2ll * c.p.Hp, c.p.parts, c.p.p_part, dw ? 64 : kRows));
   if (dw) {

@@ -33,11 +33,14 @@ namespace gated {
 constexpr int kRows = 128;         // of a tile
 constexpr int kEpiWarps = 16;    // four for each quarter of the rows
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kRing = 196608;      // bytes of operands in flight
 constexpr int kABytes = 16384;     // 128 rows (or two times 64 k) of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr int kStaging = 2048;     // of an epilogue warp: 32 rows of 64 bytes
-constexpr int kSmem = kRing + kEpiWarps * kStaging + 1024;
+constexpr int kTileBytes = 2048;   // an epilogue warp's staging tile: 32 rows of 64 bytes
+// Staging tiles of an epilogue warp (EPI_P: dh, which dg takes the place of, du, and
+// the next dh), and the bytes of operands in flight that they leave.
+template <bool P> constexpr int kTilesStaged = P ? 3 : 2;
+template <bool P> constexpr int kRing = 229376 - kEpiWarps * kTilesStaged<P> * kTileBytes;
+constexpr int kSmem = 229376 + 1024;
 constexpr int kAccumulator = 256;  // columns; a tile of up to 512 has both
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
@@ -48,11 +51,26 @@ enum Load {
   LOAD_DW    // A: P, B: x, both across k = M
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery's method).
+struct Divisor {
+  uint32_t mul, shift;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return {(uint32_t)((((1ull << s) - d) << 32) / d + 1), s};
+}
+__device__ __forceinline__ int divide(int n, const Divisor& d) {
+  return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
+}
+
 struct GemmArgs {
-  CUtensorMap a, b0, b1;  // (column, 0 or which half, row, part)
+  CUtensorMap a, b0, b1;  // operands: (column, 0 or which half, row, part)
+  CUtensorMap o0, o1, dh_map;  // results and dh, in staging tiles
   int load;
   int tiles_m, tiles_n, splits;
   int group;              // tiles are taken in groups of this many row tiles
+  Divisor by_split, by_group, by_rows, by_last;  // a split's tiles, a group's, its rows, the last one's
   int n, half;            // columns of a tile; FWD: gate columns of them
   int rows;               // of a tile: 128, a pair's 256
   int kblocks, khalf;     // k blocks (of a split, at most), DX: of one matrix
@@ -66,7 +84,7 @@ struct GemmArgs {
   int N, H;
   long long ld;           // row distance of out
   long long dh_ld;
-  int vec;                // rows of out start on 16-byte boundaries; dh's too
+  int boxes;              // 1: results go through o0 (o1), 2: dh comes through its map
   void *out, *out2;       // DW: of gate and up
   const void* dh;
   const float *x_scale, *gate_scale, *up_scale;
@@ -82,6 +100,7 @@ struct GemmArgs {
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint64_t dh[kEpiWarps][2];  // a warp's dh has come, of even and odd tiles
   uint32_t tmem;
   volatile int dead;  // a wait gave up: every role leaves, the outputs are NaN
 };
@@ -114,14 +133,13 @@ struct Item {
 // Row tiles in groups, down each group's rows first: the CTAs that run at one
 // time share few rows of A and few of B.
 __device__ __forceinline__ Item item_of(const GemmArgs& a, int i) {
-  const int tiles = a.tiles_m * a.tiles_n;
   Item t;
-  t.split = i / tiles;
-  i -= t.split * tiles;
-  const int per = a.group * a.tiles_n, g = i / per, r = i - g * per;
-  const int rows = min(a.group, a.tiles_m - g * a.group);
-  t.n = r / rows;
-  t.m = g * a.group + r - t.n * rows;
+  t.split = a.splits == 1 ? 0 : divide(i, a.by_split);
+  i -= t.split * a.tiles_m * a.tiles_n;
+  const int per = a.group * a.tiles_n, g = divide(i, a.by_group), r = i - g * per;
+  const bool last = (g + 1) * a.group > a.tiles_m;
+  t.n = divide(r, last ? a.by_last : a.by_rows);
+  t.m = g * a.group + r - t.n * (last ? a.tiles_m - g * a.group : a.group);
   return t;
 }
 // k blocks [first, first + count) of a split
@@ -139,6 +157,13 @@ __device__ __forceinline__ int part_b(int i) { return (0x021010 >> ((5 - i) * 4)
 __device__ __forceinline__ void drain(const GemmArgs& a, uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try(smem_addr(bar), parity) && clock64() - t0 < a.wait) {
+  }
+}
+
+// Copies that nobody waits for after a wait gave up land in a fraction of this time.
+__device__ __forceinline__ void linger(const GemmArgs& a) {
+  const long long t0 = clock64();
+  while (clock64() - t0 < a.wait) {
   }
 }
 
@@ -207,11 +232,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
   if (w.rank == 0) {
   for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
   } else if (!ok || sh.dead) {
-    // The first CTA's barriers say nothing of copies that it did not ask for
-    // itself; they land in a fraction of this time.
-    const long long t0 = clock64();
-    while (clock64() - t0 < a.wait) {
-    }
+    linger(a);  // the first CTA's barriers say nothing of copies that it did not ask for itself
   }
 }
 
@@ -270,20 +291,20 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
   __syncwarp();
 }
 
-// A warp's staging area: 32 rows of four 16-byte chunks, which eight rows in turn
-// spread over all banks.
+// A staging tile: 32 rows of four 16-byte chunks, which eight rows in turn spread
+// over all banks (the 64-byte swizzle of TMA).
 __device__ __forceinline__ uint4* staged(unsigned char* buf, int row, int chunk) {
   return reinterpret_cast<uint4*>(buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// Copies 32 rows x 64 bytes from the staging area to global memory, rows `ld`
-// elements apart, of which `rows` and `cols` exist.  `vec`: rows start on 16-byte
-// boundaries, and what is written beyond `cols` up to the next one is padding.
-template <typename T>
-__device__ __forceinline__ void copy_out(unsigned char* buf, T* p, long long ld, int rows, int cols, bool vec) {
+// Copies a staging tile to or from rows `ld` elements apart, of which `rows` and
+// `cols` exist, element by element: for rows that TMA cannot address.  BY16: rows
+// start on 16-byte boundaries and are padded to the next one.
+template <typename T, bool BY16>
+__device__ __forceinline__ void copy_out(unsigned char* buf, T* p, long long ld, int rows, int cols) {
   constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
-  if (vec) {
+  if constexpr (BY16) {
     const int q = lane & 3;
     p += (lane >> 2) * ld + q * kEach;
 #pragma unroll
@@ -295,25 +316,13 @@ __device__ __forceinline__ void copy_out(unsigned char* buf, T* p, long long ld,
       p[row * ld + lane] = reinterpret_cast<const T*>(staged(buf, row, lane / kEach))[lane % kEach];
   }
 }
-// The same from global memory.  Whole accesses are asynchronous: copied_in() waits.
 template <typename T>
-__device__ __forceinline__ void copy_in(unsigned char* buf, const T* p, long long ld, int rows, int cols, bool vec) {
+__device__ __forceinline__ void copy_in(unsigned char* buf, const T* p, long long ld, int rows, int cols) {
   constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
-  if (vec) {
-    const int q = lane & 3;
-    p += (lane >> 2) * ld + q * kEach;
-#pragma unroll
-    for (int i = 0; i < 4; ++i, p += 8 * ld)
-      if (i * 8 + (lane >> 2) < rows && q * kEach < cols) copy16(smem_addr(staged(buf, i * 8 + (lane >> 2), q)), p);
-  } else if (lane < cols) {
+  if (lane < cols)
     for (int row = 0; row < rows; ++row)
       reinterpret_cast<T*>(staged(buf, row, lane / kEach))[lane % kEach] = p[row * ld + lane];
-  }
-}
-__device__ __forceinline__ void copied_in() {
-  copy16_wait();
-  __syncwarp();
 }
 
 // This lane's row of the staging area: N values of T, from a chunk on.
@@ -385,91 +394,150 @@ __device__ __forceinline__ void put_part(unsigned char* buf, float (&v)[N]) {
   }
 }
 
-// Sums of N columns as rows of T, from column n0 on.
-template <typename T, int N>
-__device__ __forceinline__ void store_sums(unsigned char* buf, uint32_t from, bool got, T* p, long long ld, int rows, int cols,
-                                           bool vec) {
-  float v[N];
-  tmem_load<N>(from, v);
-  if (!got) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = __int_as_float(0x7FC00000);
-  }
-  put_row<T>(buf, v);
-  __syncwarp();
-  copy_out<T>(buf, p, ld, rows, cols, vec);
-  __syncwarp();
-}
-
 // A hidden unit's scale: of gate for the first sixteen lanes, of up for the others.
 __device__ __forceinline__ float unit_scale(const GemmArgs& a, int n, int lane) {
   return __ldg((lane < 16 ? a.gate_scale : a.up_scale) + n);
 }
 
-// Sixteen warps, four to each quarter of a tile's rows (TMEM opens its lanes to
-// warps by their number), each with every fourth stretch of 64 bytes of columns: 32
-// of 16 bits, 16 of float32.  What they write goes through a staging area of 2 KB,
-// so that whole 64-byte stretches of a row reach memory at once; dh comes the same
-// way, asked for when the warp is done with the tile before.  With eight warps the
-// epilogue of short contractions was bound by latency (200704 x 96 -> 256 forward
-// 52 us, now WAITING).
+// Two staging tiles in turn: the one that comes next is free once its last store has
+// been read.  All stores are issued by the first lane, whose groups they are.
+struct Staging {
+  unsigned char* base;
+  int turn;
+  __device__ __forceinline__ unsigned char* next() {
+    if ((threadIdx.x & 31) == 0) bulk_wait_read_but<1>();
+    __syncwarp();
+    turn ^= 1;
+    return base + turn * kTileBytes;
+  }
+};
+
+// Sends a staging tile to columns from c on and rows from `row` on.
+template <typename T>
+__device__ __forceinline__ void send(unsigned char* buf, const void* map, int c, int half, long long row, int part) {
+  fence_async_shared();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    box_store(map, c, half, (int)row, part, smem_addr(buf));
+    bulk_commit();
+  }
+}
+
+// Sixteen warps.  TMEM opens its lanes to warps by their number: four warps, or two
+// groups of two, share a quarter of a tile's rows.  Where TMEM holds two tiles each
+// is one group's of eight warps, so that two tiles' epilogues are under way at a
+// time and what a tile costs each warp (3000 clocks, most of it latency) is paid for
+// two stretches of columns; a tile of both accumulators is all sixteen warps'.  A
+// stretch is 64 bytes of a row, 32 columns of 16 bits or 16 of float32, for each of
+// the warp's 32 rows: they go through a staging tile and TMA, which writes whole
+// stretches; dh comes the same way, one stretch ahead.
 template <int EPI, typename T, bool PAIR>
 __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
   constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
-  const int quadrant = (warp + 2) & 3, side = warp / 4;
-  unsigned char* buf = staging + warp * kStaging;
   const int width = EPI == EPI_OUT ? a.n : a.half;
-  const int buffers = width > kAccumulator ? 1 : 2;
+  const bool both = a.n > kAccumulator;  // one tile at a time
+  const int quadrant = (warp + 2) & 3, sides = both ? 4 : 2, side = (warp / 4) & (sides - 1);
+  const uint32_t acc = both ? 0 : warp / 8;
+  const int first = w.first + (int)acc * w.step, step = both ? w.step : 2 * w.step;
+  Staging st = {staging + warp * kTilesStaged<EPI == EPI_P> * kTileBytes, 0};
   auto row_of = [&](const Item& t) { return (long long)t.m * a.rows + w.rank * kRows + quadrant * 32; };
   auto rows_of = [&](const Item& t) { return (int)max(0ll, min(32ll, a.M - row_of(t))); };
-  // dh of a stretch of columns, if the tile has it
-  auto fetch = [&](const Item& t, int c) {
-    const int n0 = t.n * a.half + c;
-    const long long m0 = row_of(t);
-    if (c < a.half && n0 < a.H)
-      copy_in<T>(buf, (const T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, rows_of(t), min(kCols, a.H - n0), a.vec & 2);
-  };
-  uint32_t acc = 0, phase = 0;
+
+  // dh of the warp's stretches, one after the other, into the tiles of even and odd ones
+  int fi = first, fc = side * kCols;  // the next stretch to ask for
+  uint32_t asked = 0, taken = 0;
   bool got = true;
-  if constexpr (EPI == EPI_P)
-    if (w.first < items) fetch(item_of(a, w.first), side * kCols);
-  for (int i = w.first; i < items; i += w.step) {
+  auto fetch = [&]() {
+    if constexpr (EPI == EPI_P) {
+      // dg and du of the stretch before have left their tiles
+      if (lane == 0) bulk_wait_read_but<0>();
+      __syncwarp();
+      while (got && fi < items) {
+        const Item t = item_of(a, fi);
+        const int n0 = t.n * a.half + fc;
+        if (fc < width && n0 < a.H) {
+          unsigned char* buf = st.base + (asked & 1) * 2 * kTileBytes;
+          if (a.boxes & 2) {
+            if (lane == 0) {
+              const uint32_t bar = smem_addr(&sh.dh[warp][asked & 1]);
+              mbar_expect(bar, kTileBytes);
+              box_load(smem_addr(buf), &a.dh_map, n0, 0, (int)row_of(t), 0, bar);
+            }
+          } else {
+            const long long m0 = row_of(t);
+            copy_in<T>(buf, (const T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, rows_of(t), min(kCols, a.H - n0));
+          }
+          __syncwarp();
+          ++asked;
+          fc += sides * kCols;
+          return;
+        }
+        fi += step;
+        fc = side * kCols;
+      }
+    }
+  };
+  fetch();
+
+  uint32_t phase = 0;
+  for (int i = first; i < items; i += step) {
     const Item t = item_of(a, i);
     const long long m0 = row_of(t);
     const int rows = rows_of(t);
     got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
+    phase ^= 1;
     tc_fence_after();
     const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * kAccumulator;
     if constexpr (EPI == EPI_OUT) {
-      long long m = m0;
-      int left = rows;
-      T* out = (T*)a.out;
-      if (a.load == LOAD_DW) {  // rows are hidden units, of gate in the first half of the tiles, of up in the second
-        const int tiles = a.tiles_m / 2;
-        if (t.m >= tiles) m -= (long long)tiles * a.rows, out = (T*)a.out2;
-        left = (int)max(0ll, min(32ll, a.H - m));
-      }
-      if (a.partial) {
-        float* p = a.partial + (t.split * a.partial_rows + m0) * a.ld;
-        for (int c = side * 16; c < width && t.n * a.n + c < a.N; c += 64)
-          store_sums<float, 16>(buf, from + c, got, p + t.n * a.n + c, a.ld, left, min(16, a.N - t.n * a.n - c), true);
+      const int tiles = a.tiles_m / 2;
+      const bool second = a.load == LOAD_DW && t.m >= tiles;  // rows are hidden units, of up
+      const long long m = second ? m0 - (long long)tiles * a.rows : m0;
+      const int left = a.load == LOAD_DW ? (int)max(0ll, min(32ll, a.H - m)) : rows;
+      const int n0 = t.n * a.n;
+      auto sums = [&](auto zero, int c, auto store) {  // a stretch of TO
+        typedef decltype(zero) TO;
+        float v[64 / sizeof(TO)];
+        tmem_load<64 / sizeof(TO)>(from + c, v);
+        if (!got) {
+#pragma unroll
+          for (int j = 0; j < 64 / (int)sizeof(TO); ++j) v[j] = __int_as_float(0x7FC00000);
+        }
+        unsigned char* buf = st.next();
+        put_row<TO>(buf, v);
+        store(buf);
+      };
+      if (a.partial) {  // rows and columns are padded to whole tiles
+        for (int c = side * 16; c < width && n0 + c < a.N; c += sides * 16)
+          sums(0.f, c, [&](unsigned char* buf) { send<float>(buf, &a.o0, n0 + c, 0, t.split * a.partial_rows + m0, 0); });
       } else {
-        out += m * a.ld;
-        for (int c = side * kCols; c < width && t.n * a.n + c < a.N; c += 4 * kCols)
-          store_sums<T, kCols>(buf, from + c, got, out + t.n * a.n + c, a.ld, left, min(kCols, a.N - t.n * a.n - c), a.vec & 1);
+        for (int c = side * kCols; c < width && n0 + c < a.N; c += sides * kCols)
+          sums(T(), c, [&](unsigned char* buf) {
+            if (a.boxes & 1) {
+              if (left > 0) send<T>(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0);
+            } else {
+              __syncwarp();
+              copy_out<T, false>(buf, (T*)(second ? a.out2 : a.out) + m * a.ld + n0 + c, a.ld, left, min(kCols, a.N - n0 - c));
+              __syncwarp();
+            }
+          });
       }
     } else {
-      for (int c = side * kCols; c < width; c += 4 * kCols) {
+      for (int c = side * kCols; c < width; c += sides * kCols) {
         const int n0 = t.n * a.half + c, cols = min(kCols, a.H - n0);
         if (cols <= 0) break;
+        unsigned char* buf;
         if constexpr (EPI == EPI_P) {
-          if (c >= 4 * kCols) fetch(t, c);
-          copied_in();
+          // the tiles of even and odd stretches' dh, and between them that of du
+          buf = st.base + (taken & 1) * 2 * kTileBytes;
+          if (a.boxes & 2) got = wait(sh, a, &sh.dh[warp][taken & 1], (taken >> 1) & 1) && got;
+          ++taken;
+        } else {
+          buf = st.next();
         }
         // sixteen columns at a time: 18 warps leave a thread 96 registers
         float g[16], u[16], dh[EPI == EPI_P ? 16 : 1];
-        uint4 second[EPI == EPI_P && sizeof(T) == 2 ? kCols / 8 : 1];  // du, until dg has left the staging area
+        uint4 second[EPI == EPI_P && sizeof(T) == 2 ? kCols / 8 : 1];  // du, until its tile is free
 #pragma unroll
         for (int h = 0; h < kCols / 16; ++h) {
           constexpr int kHalf = 16 * sizeof(T) / 16;  // chunks
@@ -482,12 +550,11 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
           if constexpr (EPI == EPI_H) {
             if (a.x_scale) {
               const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
-              const int n = min(n0 + h * 16 + (lane & 15), a.H - 1);
-              const float w = unit_scale(a, n, lane);
+              const float s = unit_scale(a, min(n0 + h * 16 + (lane & 15), a.H - 1), lane);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                g[j] *= xs * __shfl_sync(~0u, w, j);
-                u[j] *= xs * __shfl_sync(~0u, w, 16 + j);
+                g[j] *= xs * __shfl_sync(~0u, s, j);
+                u[j] *= xs * __shfl_sync(~0u, s, 16 + j);
               }
             }
           }
@@ -504,37 +571,38 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
               second[h * 2 + q] = o.r;
             }
           }
+          if (h == 0) fetch();
         }
         if constexpr (EPI == EPI_H) {
-          __syncwarp();
-          copy_out<T>(buf, (T*)a.out + m0 * a.ld + n0, a.ld, rows, cols, a.vec & 1);
-          __syncwarp();
-        } else if constexpr (sizeof(T) == 2) {
-          T* p = (T*)a.p + m0 * 2 * a.Hp + n0;
-          __syncwarp();
-          copy_out<T>(buf, p, 2 * a.Hp, rows, cols, true);
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) *staged(buf, lane, q) = second[q];
-          __syncwarp();
-          copy_out<T>(buf, p + a.Hp, 2 * a.Hp, rows, cols, true);
-          __syncwarp();
-        } else {
-          __nv_bfloat16* p = (__nv_bfloat16*)a.p + m0 * 2 * a.Hp + n0;
-          for (int part = 0; part < 3; ++part, p += a.p_part) {
-            put_part(buf, g);
+          if (a.boxes & 1) {
+            if (rows > 0) send<T>(buf, &a.o0, n0, 0, m0, 0);
+          } else {
             __syncwarp();
-            copy_out<__nv_bfloat16>(buf, p, 2 * a.Hp, rows, cols, true);
-            __syncwarp();
-            put_part(buf, u);
-            __syncwarp();
-            copy_out<__nv_bfloat16>(buf, p + a.Hp, 2 * a.Hp, rows, cols, true);
+            copy_out<T, false>(buf, (T*)a.out + m0 * a.ld + n0, a.ld, rows, cols);
             __syncwarp();
           }
+        } else if constexpr (sizeof(T) == 2) {
+          unsigned char* to = st.base + kTileBytes;
+          if (rows > 0) send<T>(buf, &a.o0, n0, 0, m0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) *staged(to, lane, q) = second[q];
+          if (rows > 0) send<T>(to, &a.o0, n0, 1, m0, 0);
+        } else {
+          __nv_bfloat16* p = (__nv_bfloat16*)a.p + m0 * 2 * a.Hp + n0;
+          unsigned char* to = st.base + kTileBytes;
+          for (int part = 0; part < 3; ++part, p += a.p_part) {
+            __syncwarp();
+            put_part(to, g);
+            __syncwarp();
+            copy_out<__nv_bfloat16, true>(to, p, 2 * a.Hp, rows, cols);
+            __syncwarp();
+            put_part(to, u);
+            __syncwarp();
+            copy_out<__nv_bfloat16, true>(to, p + a.Hp, 2 * a.Hp, rows, cols);
+          }
+          __syncwarp();
         }
       }
-      if constexpr (EPI == EPI_P)
-        if (i + w.step < items) fetch(item_of(a, i + w.step), side * kCols);
     }
     tc_fence_before();
     __syncwarp();
@@ -543,9 +611,9 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
       if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
       else mbar_arrive(bar);
     }
-    if (++acc == (uint32_t)buffers) acc = 0, phase ^= 1;
   }
-  copy16_wait();
+  if (lane == 0) bulk_wait();
+  if (EPI == EPI_P && !got) linger(a);  // dh that was asked for
 }
 
 template <int EPI, typename T, bool Q8, bool PAIR>
@@ -553,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  unsigned char* staging = raw + (base - smem_addr(raw)) + kRing;
+  unsigned char* staging = raw + (base - smem_addr(raw)) + kRing<EPI == EPI_P>;
   const int warp = threadIdx.x / 32;
   const int items = a.tiles_m * a.tiles_n * a.splits;
   Worker w = {(int)blockIdx.x, (int)gridDim.x, 0};
@@ -565,7 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.acc_full[i]), 1);
-      mbar_init(smem_addr(&sh.acc_empty[i]), kEpiWarps * (PAIR ? 2 : 1));
+      // a tile's epilogue warps, of both CTAs of a pair
+      mbar_init(smem_addr(&sh.acc_empty[i]), (a.n > kAccumulator ? kEpiWarps : kEpiWarps / 2) * (PAIR ? 2 : 1));
+      for (int j = 0; j < kEpiWarps; ++j) mbar_init(smem_addr(&sh.dh[j][i]), 1);
     }
     mbar_init(smem_addr(&sh.drain), 1);
     sh.dead = 0;

@@ -53,13 +53,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// 16 bytes global -> shared by one lane, asynchronous; copy16_wait() waits for the
-// lane's own.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // A box of a tensor map -> shared, completing on an mbarrier.  The innermost
 // coordinate is a multiple of 16 bytes; what lies outside reads as zero and
 // counts among the bytes.
@@ -77,6 +70,18 @@ __device__ __forceinline__ void box_load_pair(uint32_t dst, const void* map, int
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
+}
+
+// Shared -> a box of a tensor map, tracked by the issuing thread's bulk groups; what
+// lies outside is not written.
+__device__ __forceinline__ void box_store(const void* map, int c0, int c1, int c2, int c3, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map), "r"(c0),
+               "r"(c1), "r"(c2), "r"(c3), "r"(src)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() {  // all but the last N groups
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // A shared address of this CTA as the same place in CTA `rank` of the cluster.

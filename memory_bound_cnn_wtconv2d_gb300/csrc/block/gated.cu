@@ -109,7 +109,7 @@ double clocks(long long items, const Tiles& t, int sms, double iters, double epi
   const double tile = iters * (mma > load ? mma : load);
   const int workers = t.pair ? sms / 2 : sms;
   const double rounds = (double)((items + workers - 1) / workers);
-  if (t.n > kAccumulator) return rounds * (tile + epilogue) + 1500;
+  if (t.n > kMostN) return rounds * (tile + epilogue) + 1500;
   return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
 }
 
@@ -292,11 +292,14 @@ struct Call {
   cudaStream_t s;
 };
 
-void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_along, bool b_along) {
+// stretches: of 64 bytes across a tile's results
+void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stretches, bool a_along, bool b_along) {
   a.tiles_m = tiles_m;
   a.tiles_n = t.tiles_n;
   a.splits = t.splits;
   a.group = 16;
+  a.buffers = t.n > 256 ? 1 : t.n > 128 ? 2 : t.n > 64 ? 4 : 8;
+  a.groups = stretches > 2 || a.buffers == 1 ? 1 : stretches == 2 ? 2 : 4;
   a.by_split = divisor(a.tiles_m * a.tiles_n);
   a.by_group = divisor(a.group * a.tiles_n);
   a.by_rows = divisor(a.group);
@@ -307,8 +310,8 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_a
   a.parts = c.p.parts;
   a.stages = t.stages;
   a.b_bytes = t.b_bytes;
-  a.idesc = instr_desc(t.n < kAccumulator ? t.n : kAccumulator, a_along, b_along, t.rows) | c.kind;
-  a.idesc2 = instr_desc(t.n - kAccumulator, a_along, b_along, t.rows) | c.kind;
+  a.idesc = instr_desc(t.n < kMostN ? t.n : kMostN, a_along, b_along, t.rows) | c.kind;
+  a.idesc2 = instr_desc(t.n - kMostN, a_along, b_along, t.rows) | c.kind;
   a.act = c.d.act;
   a.M = c.d.M;
   a.H = c.d.H;
@@ -352,7 +355,8 @@ template <int EPI, typename T, bool Q8>
 cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
-  set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows), true, true);
+  set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows),
+            c.p.fwd.n / 2 * (int)sizeof(T) / 64, true, true);
   a.load = LOAD_FWD;
   a.half = a.n / 2;
   a.k = d.C;
@@ -395,7 +399,7 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
   GemmArgs a = {};
   const Tiles& t = dw ? c.p.dw : c.p.dx;
   const int tiles = (int)(((dw ? d.H : d.M) + t.rows - 1) / t.rows);
-  set_tiles(a, c, t, dw ? 2 * tiles : tiles, !dw, false);
+  set_tiles(a, c, t, dw ? 2 * tiles : tiles, t.n * (t.splits > 1 ? 4 : (int)sizeof(T)) / 64, !dw, false);
   a.load = dw ? LOAD_DW : LOAD_DX;
   a.khalf = dw ? (int)((d.M + 63) / 64) : c.p.Hp / 64;
   a.k = dw ? (int)d.M : d.H;

@@ -41,7 +41,9 @@ constexpr int kTileBytes = 2048;   // an epilogue warp's staging tile: 32 rows o
 template <bool P> constexpr int kTilesStaged = P ? 3 : 2;
 template <bool P> constexpr int kRing = 229376 - kEpiWarps * kTilesStaged<P> * kTileBytes;
 constexpr int kSmem = 229376 + 1024;
-constexpr int kAccumulator = 256;  // columns; a tile of up to 512 has both
+constexpr int kColumns = 512;      // of TMEM, all of them
+constexpr int kMostN = 256;        // columns of an MMA; wider tiles take two
+constexpr int kMaxBuffers = 8;
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
 enum Epilogue { EPI_H, EPI_P, EPI_OUT };
@@ -73,6 +75,8 @@ struct GemmArgs {
   Divisor by_split, by_group, by_rows, by_last;  // a split's tiles, a group's, its rows, the last one's
   int n, half;            // columns of a tile; FWD: gate columns of them
   int rows;               // of a tile: 128, a pair's 256
+  int buffers;            // tiles that TMEM holds: a power of two
+  int groups;             // of epilogue warps (1, 2, 4, at most `buffers`): each takes its turn of the tiles
   int kblocks, khalf;     // k blocks (of a split, at most), DX: of one matrix
   int k;                  // valid k: C, H (of each half), M
   int parts;              // 1, or 3 for float32
@@ -99,7 +103,7 @@ struct GemmArgs {
 };
 
 struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kMaxBuffers], acc_empty[kMaxBuffers], drain;
   uint64_t dh[kEpiWarps][2];  // a warp's dh has come, of even and odd tiles
   uint32_t tmem;
   volatile int dead;  // a wait gave up: every role leaves, the outputs are NaN
@@ -216,8 +220,8 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
               load<PAIR>(to + 8192, &a.a, h + 64, second, row, pa, full);
             }
             uint32_t b = tb;
-            for (int j = 0; j < a.n; j += kAccumulator) {
-              const int some = min(kAccumulator, a.n - j) / (PAIR ? 2 : 1);
+            for (int j = 0; j < a.n; j += kMostN) {
+              const int some = min(kMostN, a.n - j) / (PAIR ? 2 : 1);
               for (int k = 0; k < some; k += 64, b += 8192)
                 load<PAIR>(b, from, t.n * a.n + j + w.rank * some + k, 0, row, pb, full);
             }
@@ -243,7 +247,8 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
   const uint32_t bytes = kABytes + a.b_bytes;
   const bool a_along = a.load != LOAD_DW, b_along = a.load == LOAD_FWD;
   const uint32_t step_a = desc_step(a_along), step_b = desc_step(b_along);
-  const int products = a.parts == 1 ? 1 : 6, buffers = a.n > kAccumulator ? 1 : 2;
+  const int products = a.parts == 1 ? 1 : 6;
+  const bool wide = a.n > kMostN;
   auto commit = [](uint64_t* bar) {
     if constexpr (PAIR) mma_commit_pair(smem_addr(bar));
     else mma_commit(smem_addr(bar));
@@ -255,7 +260,7 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
     ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
     if (!ok) break;
     tc_fence_after();
-    const uint32_t d = tmem + acc * kAccumulator;
+    const uint32_t d = tmem + acc * (kColumns / a.buffers);
     uint32_t accumulate = 0;
     for (int q = 0; ok && q < products; ++q)
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
@@ -269,8 +274,8 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
         if (elect_one()) {
           for (int s = 0; s < steps; ++s) {
             mma_step<PAIR, Q8>(d, la + s * step_a, lb + s * step_b, kDescHigh, a.idesc, accumulate);
-            if (buffers == 1)  // what lies beyond the first 256 columns
-              mma_step<PAIR, Q8>(d + kAccumulator, la + s * step_a, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * step_b, kDescHigh,
+            if (wide)  // what lies beyond the first 256 columns
+              mma_step<PAIR, Q8>(d + kMostN, la + s * step_a, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * step_b, kDescHigh,
                                  a.idesc2, accumulate);
             accumulate = 1;
           }
@@ -282,7 +287,7 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
       }
     if (ok && elect_one()) commit(&sh.acc_full[acc]);
     __syncwarp();
-    if (++acc == (uint32_t)buffers) acc = 0, acc_phase ^= 1;
+    if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
   }
   if (elect_one()) {
     commit(&sh.drain);
@@ -423,23 +428,19 @@ __device__ __forceinline__ void send(unsigned char* buf, const void* map, int c,
   }
 }
 
-// Sixteen warps.  TMEM opens its lanes to warps by their number: four warps, or two
-// groups of two, share a quarter of a tile's rows.  Where TMEM holds two tiles each
-// is one group's of eight warps, so that two tiles' epilogues are under way at a
-// time and what a tile costs each warp (3000 clocks, most of it latency) is paid for
-// two stretches of columns; a tile of both accumulators is all sixteen warps'.  A
-// stretch is 64 bytes of a row, 32 columns of 16 bits or 16 of float32, for each of
-// the warp's 32 rows: they go through a staging tile and TMA, which writes whole
-// stretches; dh comes the same way, one stretch ahead.
+// Sixteen warps.  TMEM opens its lanes to warps by their number, so that four share
+// a quarter of a tile's rows: side by side where the tile has as many stretches of
+// columns, else in groups that take turns of the tiles.  A stretch is 64 bytes of a
+// row, 32 columns of 16 bits or 16 of float32, for each of the warp's 32 rows: they
+// go through a staging tile and TMA, which writes whole stretches; dh comes the
+// same way, one stretch ahead.
 template <int EPI, typename T, bool PAIR>
 __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
   constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
   const int width = EPI == EPI_OUT ? a.n : a.half;
-  const bool both = a.n > kAccumulator;  // one tile at a time
-  const int quadrant = (warp + 2) & 3, sides = both ? 4 : 2, side = (warp / 4) & (sides - 1);
-  const uint32_t acc = both ? 0 : warp / 8;
-  const int first = w.first + (int)acc * w.step, step = both ? w.step : 2 * w.step;
+  const int quadrant = (warp + 2) & 3, sides = 4 / a.groups, side = (warp / 4) & (sides - 1), group = warp / 4 / sides;
+  const int first = w.first + group * w.step, step = a.groups * w.step;
   Staging st = {staging + warp * kTilesStaged<EPI == EPI_P> * kTileBytes, 0};
   auto row_of = [&](const Item& t) { return (long long)t.m * a.rows + w.rank * kRows + quadrant * 32; };
   auto rows_of = [&](const Item& t) { return (int)max(0ll, min(32ll, a.M - row_of(t))); };
@@ -480,15 +481,14 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
   };
   fetch();
 
-  uint32_t phase = 0;
+  uint32_t acc = group, phase = 0;
   for (int i = first; i < items; i += step) {
     const Item t = item_of(a, i);
     const long long m0 = row_of(t);
     const int rows = rows_of(t);
     got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
-    phase ^= 1;
     tc_fence_after();
-    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * kAccumulator;
+    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * (kColumns / a.buffers);
     if constexpr (EPI == EPI_OUT) {
       const int tiles = a.tiles_m / 2;
       const bool second = a.load == LOAD_DW && t.m >= tiles;  // rows are hidden units, of up
@@ -611,6 +611,8 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
       if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
       else mbar_arrive(bar);
     }
+    acc += a.groups;
+    if (acc >= (uint32_t)a.buffers) acc -= a.buffers, phase ^= 1;
   }
   if (lane == 0) bulk_wait();
   if (EPI == EPI_P && !got) linger(a);  // dh that was asked for
@@ -631,19 +633,19 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
       mbar_init(smem_addr(&sh.full[i]), 1);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < a.buffers; ++i) {
       mbar_init(smem_addr(&sh.acc_full[i]), 1);
       // a tile's epilogue warps, of both CTAs of a pair
-      mbar_init(smem_addr(&sh.acc_empty[i]), (a.n > kAccumulator ? kEpiWarps : kEpiWarps / 2) * (PAIR ? 2 : 1));
-      for (int j = 0; j < kEpiWarps; ++j) mbar_init(smem_addr(&sh.dh[j][i]), 1);
+      mbar_init(smem_addr(&sh.acc_empty[i]), kEpiWarps / a.groups * (PAIR ? 2 : 1));
     }
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(smem_addr(&sh.dh[i / 2][i % 2]), 1);
     mbar_init(smem_addr(&sh.drain), 1);
     sh.dead = 0;
     mbar_init_done();
   }
   if (warp == 1) {
-    if constexpr (PAIR) tmem_alloc_pair(smem_addr(&sh.tmem), 2 * kAccumulator);
-    else tmem_alloc(smem_addr(&sh.tmem), 2 * kAccumulator);
+    if constexpr (PAIR) tmem_alloc_pair(smem_addr(&sh.tmem), kColumns);
+    else tmem_alloc(smem_addr(&sh.tmem), kColumns);
   }
   if constexpr (PAIR) cluster_meet();
   __syncthreads();
@@ -661,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   if constexpr (PAIR) cluster_meet();  // the other CTA's MMAs, copies and arrivals touch this one
   tc_fence_after();
   if (warp == 1) {
-    if constexpr (PAIR) tmem_free_pair(tmem, 2 * kAccumulator);
-    else tmem_free(tmem, 2 * kAccumulator);
+    if constexpr (PAIR) tmem_free_pair(tmem, kColumns);
+    else tmem_free(tmem, kColumns);
   }
 }
 

@@ -357,7 +357,7 @@ cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   GemmArgs a = {};
   set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows),
             c.p.fwd.n / 2 * (int)sizeof(T) / 64, true, true);
-  a.load = LOAD_FWD;
+  a.total = c.p.fwd.kblocks;
   a.half = a.n / 2;
   a.k = d.C;
   a.out = g.h;
@@ -393,15 +393,16 @@ cudaError_t sum_up(const Call& c, const GemmArgs& a, long long rows, long long s
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
+template <int EPI, typename T>
+cudaError_t product_sums(const Call& c, const GatedArgs& g) {
+  constexpr bool dw = EPI == EPI_DW;
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
   const Tiles& t = dw ? c.p.dw : c.p.dx;
   const int tiles = (int)(((dw ? d.H : d.M) + t.rows - 1) / t.rows);
   set_tiles(a, c, t, dw ? 2 * tiles : tiles, t.n * (t.splits > 1 ? 4 : (int)sizeof(T)) / 64, !dw, false);
-  a.load = dw ? LOAD_DW : LOAD_DX;
   a.khalf = dw ? (int)((d.M + 63) / 64) : c.p.Hp / 64;
+  a.total = dw ? a.khalf : 2 * a.khalf;
   a.k = dw ? (int)d.M : d.H;
   a.N = d.C;
   a.out = dw ? g.dgate : g.dx;
@@ -425,7 +426,7 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, bool dw) {
     RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, 64));
     RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, 64));
   }
-  RET((t.pair ? launch_gemm<EPI_OUT, T, false, true>(a, c.s) : launch_gemm<EPI_OUT, T, false, false>(a, c.s)));
+  RET((t.pair ? launch_gemm<EPI, T, false, true>(a, c.s) : launch_gemm<EPI, T, false, false>(a, c.s)));
   if (t.splits == 1) return cudaSuccess;
   return dw ? sum_up<T>(c, a, 2ll * d.H, d.H, (long long)tiles * t.rows) : sum_up<T>(c, a, d.M, d.M, 0);
 }
@@ -455,8 +456,8 @@ template <typename T>
 cudaError_t backward(Call& c, const GatedArgs& g) {
   RET(pack<T>(c, g));
   RET((product_forward<EPI_P, T, false>(c, g)));
-  if (g.dx) RET(product_sums<T>(c, g, false));
-  if (g.dgate) RET(product_sums<T>(c, g, true));
+  if (g.dx) RET((product_sums<EPI_DX, T>(c, g)));
+  if (g.dgate) RET((product_sums<EPI_DW, T>(c, g)));
   return cudaSuccess;
 }
 

@@ -13,8 +13,8 @@
 //   EPI_H    columns are half gate, half up: act(g) u
 //   EPI_P    the same with dh: dg = dh u act'(g) and du = dh act(g), side by
 //            side in one matrix P[M, 2 Hp], Hp the hidden units to a whole k block
-//   EPI_OUT  the sums themselves (dx = P [Wg; Wu], dW = P^T x), or where k is
-//            split over CTAs, float32 partial sums
+//   EPI_DX, EPI_DW  the sums themselves (dx = P [Wg; Wu], dW = P^T x), or where
+//            k is split over CTAs, float32 partial sums
 // float32 operands come as three bfloat16 parts (24 bits); six of their nine
 // products count (the others lie below 2^-25), least first, since the tensor
 // core's additions truncate.
@@ -46,11 +46,12 @@ constexpr int kMostN = 256;        // columns of an MMA; wider tiles take two
 constexpr int kMaxBuffers = 8;
 constexpr long long kWaitCycles = 1ll << 31;  // about a second
 
-enum Epilogue { EPI_H, EPI_P, EPI_OUT };
-enum Load {
-  LOAD_FWD,  // A: x, B: gate and up, all along k = C
-  LOAD_DX,   // A: P along k = 2 Hp, B: gate, then up, across k
-  LOAD_DW    // A: P, B: x, both across k = M
+// The product, by its epilogue.  Operands along k (A's rows and B's columns of k
+// values) or across it (k rows of as many):
+enum Epilogue {
+  EPI_H, EPI_P,  // A: x, B: gate and up, all along k = C
+  EPI_DX,        // A: P along k = 2 Hp, B: gate, then up, across k
+  EPI_DW         // A: P, B: x, both across k = M
 };
 
 // n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery's method).
@@ -69,7 +70,6 @@ __device__ __forceinline__ int divide(int n, const Divisor& d) {
 struct GemmArgs {
   CUtensorMap a, b0, b1;  // operands: (column, 0 or which half, row, part)
   CUtensorMap o0, o1, dh_map;  // results and dh, in staging tiles
-  int load;
   int tiles_m, tiles_n, splits;
   int group;              // tiles are taken in groups of this many row tiles
   Divisor by_split, by_group, by_rows, by_last;  // a split's tiles, a group's, its rows, the last one's
@@ -77,7 +77,7 @@ struct GemmArgs {
   int rows;               // of a tile: 128, a pair's 256
   int buffers;            // tiles that TMEM holds: a power of two
   int groups;             // of epilogue warps (1, 2, 4, at most `buffers`): each takes its turn of the tiles
-  int kblocks, khalf;     // k blocks (of a split, at most), DX: of one matrix
+  int total, kblocks, khalf;  // k blocks: all, of a split (at most), DX: of one matrix
   int k;                  // valid k: C, H (of each half), M
   int parts;              // 1, or 3 for float32
   int stages;
@@ -148,9 +148,8 @@ __device__ __forceinline__ Item item_of(const GemmArgs& a, int i) {
 }
 // k blocks [first, first + count) of a split
 __device__ __forceinline__ int2 blocks_of(const GemmArgs& a, int split) {
-  const int total = a.load == LOAD_FWD ? a.kblocks : a.load == LOAD_DX ? 2 * a.khalf : a.khalf;
   const int first = split * a.kblocks;
-  return make_int2(first, min(a.kblocks, total - first));
+  return make_int2(first, min(a.kblocks, a.total - first));
 }
 
 // Parts of A and B of the i-th of the six products of float32 operands.
@@ -177,10 +176,15 @@ __device__ __forceinline__ void load(uint32_t dst, const void* map, int c0, int 
   else box_load(dst, map, c0, c1, c2, c3, bar);
 }
 
-template <bool PAIR, bool Q8>
+// The copies, by a CTA's first warp.  A k block costs it and the MMAs' warp a
+// wait, a vote and a few instructions that depend on one another: what can be
+// computed outside of the block of the elected lane is, in uniform registers.
+template <int EPI, bool PAIR, bool Q8>
 __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t ring, const Worker& w, int items) {
   constexpr int kBlock = Q8 ? 128 : 64;
-  const uint32_t bytes = kABytes + a.b_bytes;
+  const uint32_t bytes = kABytes + a.b_bytes, own = smem_addr(&sh.full[0]);
+  // a pair's copies complete on its first CTA's barriers
+  const uint32_t there = PAIR ? at_rank(own, 0) : own;
   const int products = a.parts == 1 ? 1 : 6;
   uint32_t stage = 0, phase = 1;
   long long issued = 0;
@@ -188,42 +192,49 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
   for (int i = w.first; ok && i < items; i += w.step) {
     const Item t = item_of(a, i);
     const int2 blocks = blocks_of(a, t.split);
+    int row = t.m * a.rows + w.rank * kRows, second = 0;  // A's rows
+    if constexpr (EPI == EPI_DW) {  // hidden units, of gate in the first half of the tiles, of up in the second
+      const int tiles = a.tiles_m / 2;
+      if (t.m >= tiles) row -= tiles * a.rows, second = 1;
+    }
+    const int column = EPI == EPI_H || EPI == EPI_P ? t.n * a.half : t.n * a.n;
     for (int q = 0; ok && q < products; ++q) {
       const int pa = products == 1 ? 0 : part_a(q), pb = products == 1 ? 0 : part_b(q);
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
         ok = wait(sh, a, &sh.empty[stage], phase);
         if (!ok) break;
-        const uint32_t own = smem_addr(&sh.full[stage]), to = ring + stage * bytes, tb = to + kABytes;
-        // a pair's copies complete on its first CTA's barrier
-        const uint32_t full = PAIR ? at_rank(own, 0) : own;
-        if (elect_one()) {
-          // held: more than comes
-          if (w.rank == 0) mbar_expect(own, (PAIR ? 2 : 1) * bytes + (a.hold && issued == 0 ? 16 : 0));
-          if (a.load == LOAD_FWD) {
-            const int c = kb * kBlock;
-            load<PAIR>(to, &a.a, c, 0, t.m * a.rows + w.rank * kRows, pa, full);
-            if (!PAIR || w.rank == 0) load<PAIR>(tb, &a.b0, c, 0, t.n * a.half, pb, full);
-            if (!PAIR || w.rank == 1) load<PAIR>(PAIR ? tb : tb + a.half * 128, &a.b1, c, 0, t.n * a.half, pb, full);
-          } else {
-            // B's columns of this CTA: of each accumulator's a pair's half
-            const void* from = &a.b0;
-            int row = kb * 64;
-            if (a.load == LOAD_DX) {
-              const int second = kb >= a.khalf;
-              row -= second ? a.khalf * 64 : 0;
-              if (second) from = &a.b1;
-              load<PAIR>(to, &a.a, row, second, t.m * a.rows + w.rank * kRows, pa, full);
+        const uint32_t full = there + stage * 8, to = ring + stage * bytes, tb = to + kABytes;
+        // held: more than comes
+        const uint32_t expect = (PAIR ? 2 : 1) * bytes + (a.hold && issued == 0 ? 16 : 0);
+        if constexpr (EPI == EPI_H || EPI == EPI_P) {
+          const int c = kb * kBlock;
+          if (elect_one()) {
+            if (!PAIR || w.rank == 0) mbar_expect(own + stage * 8, expect);
+            load<PAIR>(to, &a.a, c, 0, row, pa, full);
+            if constexpr (PAIR) {
+              load<PAIR>(tb, w.rank == 0 ? &a.b0 : &a.b1, c, 0, column, pb, full);
             } else {
-              const int tiles = a.tiles_m / 2, second = t.m >= tiles;
-              const int h = (t.m - (second ? tiles : 0)) * a.rows + w.rank * kRows;
-              load<PAIR>(to, &a.a, h, second, row, pa, full);
-              load<PAIR>(to + 8192, &a.a, h + 64, second, row, pa, full);
+              load<PAIR>(tb, &a.b0, c, 0, column, pb, full);
+              load<PAIR>(tb + a.half * 128, &a.b1, c, 0, column, pb, full);
             }
+          }
+        } else {
+          const bool up = EPI == EPI_DX && kb >= a.khalf;
+          const int k = (up ? kb - a.khalf : kb) * 64;
+          const void* from = up ? &a.b1 : &a.b0;
+          if (elect_one()) {
+            if (!PAIR || w.rank == 0) mbar_expect(own + stage * 8, expect);
+            if constexpr (EPI == EPI_DX) {
+              load<PAIR>(to, &a.a, k, up, row, pa, full);
+            } else {
+              load<PAIR>(to, &a.a, row, second, k, pa, full);
+              load<PAIR>(to + 8192, &a.a, row + 64, second, k, pa, full);
+            }
+            // B's columns of this CTA: of each MMA's a pair's half
             uint32_t b = tb;
             for (int j = 0; j < a.n; j += kMostN) {
               const int some = min(kMostN, a.n - j) / (PAIR ? 2 : 1);
-              for (int k = 0; k < some; k += 64, b += 8192)
-                load<PAIR>(b, from, t.n * a.n + j + w.rank * some + k, 0, row, pb, full);
+              for (int c = 0; c < some; c += 64, b += 8192) load<PAIR>(b, from, column + j + w.rank * some + c, 0, k, pb, full);
             }
           }
         }
@@ -234,29 +245,29 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
     }
   }
   if (w.rank == 0) {
-  for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
+    for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
   } else if (!ok || sh.dead) {
     linger(a);  // the first CTA's barriers say nothing of copies that it did not ask for itself
   }
 }
 
 // The MMAs, by a CTA's second warp; a pair's by its first CTA's.
-template <bool PAIR, bool Q8>
+template <int EPI, bool PAIR, bool Q8>
 __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t ring, uint32_t tmem, const Worker& w, int items) {
   constexpr int kBlock = Q8 ? 128 : 64, kStep = Q8 ? 32 : 16;
+  constexpr bool kAlongA = EPI != EPI_DW, kAlongB = EPI == EPI_H || EPI == EPI_P;
+  constexpr uint32_t kStepA = kAlongA ? 32 >> 4 : 2048 >> 4, kStepB = kAlongB ? 32 >> 4 : 2048 >> 4;  // as desc_step()
   const uint32_t bytes = kABytes + a.b_bytes;
-  const bool a_along = a.load != LOAD_DW, b_along = a.load == LOAD_FWD;
-  const uint32_t step_a = desc_step(a_along), step_b = desc_step(b_along);
   const int products = a.parts == 1 ? 1 : 6;
   const bool wide = a.n > kMostN;
-  auto commit = [](uint64_t* bar) {
-    if constexpr (PAIR) mma_commit_pair(smem_addr(bar));
-    else mma_commit(smem_addr(bar));
+  auto commit = [](uint32_t bar) {
+    if constexpr (PAIR) mma_commit_pair(bar);
+    else mma_commit(bar);
   };
   uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
   bool ok = true;
   for (int i = w.first; ok && i < items; i += w.step) {
-    const int2 blocks = blocks_of(a, item_of(a, i).split);
+    const int2 blocks = a.splits == 1 ? make_int2(0, a.total) : blocks_of(a, divide(i, a.by_split));
     ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
     if (!ok) break;
     tc_fence_after();
@@ -264,33 +275,42 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
     uint32_t accumulate = 0;
     for (int q = 0; ok && q < products; ++q)
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
+        const int left = a.k - (EPI == EPI_DX && kb >= a.khalf ? kb - a.khalf : kb) * kBlock;
+        const uint32_t from = ring + stage * bytes, empty = smem_addr(&sh.empty[stage]);
+        const uint32_t la = desc_low(from, kAlongA), lb = desc_low(from + kABytes, kAlongB);
         ok = wait(sh, a, &sh.full[stage], phase);
         if (!ok) break;
         tc_fence_after();
-        const int left = a.k - (a.load == LOAD_DX && kb >= a.khalf ? kb - a.khalf : kb) * kBlock;
-        const int steps = left >= kBlock ? kBlock / kStep : (left + kStep - 1) / kStep;
-        const uint32_t from = ring + stage * bytes;
-        const uint32_t la = desc_low(from, a_along), lb = desc_low(from + kABytes, b_along);
-        if (elect_one()) {
-          for (int s = 0; s < steps; ++s) {
-            mma_step<PAIR, Q8>(d, la + s * step_a, lb + s * step_b, kDescHigh, a.idesc, accumulate);
-            if (wide)  // what lies beyond the first 256 columns
-              mma_step<PAIR, Q8>(d + kMostN, la + s * step_a, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * step_b, kDescHigh,
-                                 a.idesc2, accumulate);
-            accumulate = 1;
+        if (left >= kBlock && !wide) {
+          if (elect_one()) {
+            mma_step<PAIR, Q8>(d, la, lb, kDescHigh, a.idesc, accumulate);
+#pragma unroll
+            for (int s = 1; s < kBlock / kStep; ++s)
+              mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, 1);
+            commit(empty);
           }
-          commit(&sh.empty[stage]);
+        } else {
+          const int steps = min(kBlock / kStep, (left + kStep - 1) / kStep);
+          if (elect_one()) {
+            for (int s = 0; s < steps; ++s) {
+              mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, accumulate | s);
+              if (wide)  // what lies beyond the first 256 columns
+                mma_step<PAIR, Q8>(d + kMostN, la + s * kStepA, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * kStepB, kDescHigh,
+                                   a.idesc2, accumulate | s);
+            }
+            commit(empty);
+          }
         }
         accumulate = 1;
         __syncwarp();
         if (++stage == (uint32_t)a.stages) stage = 0, phase ^= 1;
       }
-    if (ok && elect_one()) commit(&sh.acc_full[acc]);
+    if (ok && elect_one()) commit(smem_addr(&sh.acc_full[acc]));
     __syncwarp();
     if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
   }
   if (elect_one()) {
-    commit(&sh.drain);
+    commit(smem_addr(&sh.drain));
     drain(a, &sh.drain, 0);
   }
   __syncwarp();
@@ -438,7 +458,8 @@ template <int EPI, typename T, bool PAIR>
 __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
   constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
-  const int width = EPI == EPI_OUT ? a.n : a.half;
+  constexpr bool kSums = EPI == EPI_DX || EPI == EPI_DW;
+  const int width = kSums ? a.n : a.half;
   const int quadrant = (warp + 2) & 3, sides = 4 / a.groups, side = (warp / 4) & (sides - 1), group = warp / 4 / sides;
   const int first = w.first + group * w.step, step = a.groups * w.step;
   Staging st = {staging + warp * kTilesStaged<EPI == EPI_P> * kTileBytes, 0};
@@ -489,11 +510,11 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
     got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
     tc_fence_after();
     const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * (kColumns / a.buffers);
-    if constexpr (EPI == EPI_OUT) {
+    if constexpr (kSums) {
       const int tiles = a.tiles_m / 2;
-      const bool second = a.load == LOAD_DW && t.m >= tiles;  // rows are hidden units, of up
+      const bool second = EPI == EPI_DW && t.m >= tiles;  // rows are hidden units, of up
       const long long m = second ? m0 - (long long)tiles * a.rows : m0;
-      const int left = a.load == LOAD_DW ? (int)max(0ll, min(32ll, a.H - m)) : rows;
+      const int left = EPI == EPI_DW ? (int)max(0ll, min(32ll, a.H - m)) : rows;
       const int n0 = t.n * a.n;
       auto sums = [&](auto zero, int c, auto store) {  // a stretch of TO
         typedef decltype(zero) TO;
@@ -652,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   if (warp == 0) {
-    produce<PAIR, Q8>(sh, a, base, w, items);
+    produce<EPI, PAIR, Q8>(sh, a, base, w, items);
   } else if (warp == 1) {
-    if (w.rank == 0) multiply<PAIR, Q8>(sh, a, base, tmem, w, items);
+    if (w.rank == 0) multiply<EPI, PAIR, Q8>(sh, a, base, tmem, w, items);
   } else {
     epilogue<EPI, T, PAIR>(sh, a, staging, tmem, w, items);
   }

@@ -98,22 +98,29 @@ struct Tiles {
   int n;           // columns (FWD: gate and up)
   int tiles_n, splits, kblocks;  // k blocks of a split
   int b_bytes, stages;
+  int resident;    // B's k blocks all stay in shared memory
 };
+
+// CTAs or pairs that share out the tiles; resident: as many for each column of them.
+int workers_of(bool pair, bool resident, int tiles_n, int sms) {
+  const int n = pair ? sms / 2 : sms;
+  return resident && tiles_n < n ? n / tiles_n * tiles_n : n;
+}
 
 // Time of a product in clocks, in round numbers: a k block takes its MMAs (a
 // column two clocks at 64 k) or its bytes at 55 a clock, and 1500 pass until the
 // first operands are there.  Epilogues run beside the next tile's products where
 // TMEM holds two tiles.
 double clocks(long long items, const Tiles& t, int sms, double iters, double epilogue) {
-  const double mma = 2.0 * t.n, load = (kABytes + t.b_bytes) / 55.0;
+  const double mma = 2.0 * t.n, load = (kABytes + (t.resident ? 0 : t.b_bytes)) / 55.0;
   const double tile = iters * (mma > load ? mma : load);
-  const int workers = t.pair ? sms / 2 : sms;
+  const int workers = workers_of(t.pair, t.resident, t.tiles_n, sms);
   const double rounds = (double)((items + workers - 1) / workers);
   if (t.n > kMostN) return rounds * (tile + epilogue) + 1500;
   return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
 }
 
-Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, bool p = false) {
+Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, int sms, bool whole = false, bool p = false) {
   Tiles t = {};
   t.pair = pair;
   t.rows = pair ? 2 * kRows : kRows;
@@ -122,7 +129,12 @@ Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, bool p = 
   t.splits = splits;
   t.kblocks = kblocks;
   t.b_bytes = n * (pair ? 64 : 128);
-  t.stages = (p ? kRing<true> : kRing<false>) / (kABytes + t.b_bytes);
+  const int ring = p ? kRing<true> : kRing<false>;
+  t.stages = ring / (kABytes + t.b_bytes);
+  if (whole && tiles_n <= (pair ? sms / 2 : sms) && kblocks * t.b_bytes + 4 * kABytes <= ring) {
+    t.resident = 1;
+    t.stages = (ring - kblocks * t.b_bytes) / kABytes;
+  }
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   return t;
 }
@@ -135,7 +147,7 @@ Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool gra
   double least = 0;
   for (int pair = 0; pair < 2; ++pair)
     for (int half = 32; half <= 128; half += 32) {
-      const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks, grad);
+      const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks, sms, products == 1, grad);
       const long long items = (d.M + t.rows - 1) / t.rows * t.tiles_n;
       const double c = clocks(items, t, sms, (double)kblocks * products, (half + stretch - 1) / stretch * (grad ? 3000. : 1500.));
       if (!best.n || c <= least) least = c, best = t;
@@ -156,7 +168,7 @@ Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products,
       for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
         const long long each = (kblocks + want - 1) / want;
         if (want > 1 && each < 4) break;
-        const Tiles t = tiles_of(pair, n, tn, (int)((kblocks + each - 1) / each), (int)each);
+        const Tiles t = tiles_of(pair, n, tn, (int)((kblocks + each - 1) / each), (int)each, sms);
         const long long tm = halves * ((M + t.rows - 1) / t.rows);
         double c = clocks(tm * tn * t.splits, t, sms, (double)each * products, (n + 127) / 128 * 700.);
         if (t.splits > 1)  // written and read at about 2500 bytes a clock, and a launch
@@ -266,7 +278,7 @@ cudaError_t launch_gemm(GemmArgs& a, cudaStream_t s) {
   const void* f = (const void*)gated_gemm<EPI, T, Q8, PAIR>;
   RET(wt::ensure_smem(f, kSmem));
   const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
-  const int workers = PAIR ? wt::sm_count() / 2 : wt::sm_count();
+  const int workers = workers_of(PAIR, a.resident, a.tiles_n, wt::sm_count());
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(items < workers ? items : workers) * (PAIR ? 2 : 1));
   c.blockDim = dim3(kThreads);
@@ -297,7 +309,8 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stre
   a.tiles_m = tiles_m;
   a.tiles_n = t.tiles_n;
   a.splits = t.splits;
-  a.group = 16;
+  a.resident = t.resident;
+  a.group = t.resident ? 1 : 16;  // resident: a CTA's tiles have the same columns
   a.buffers = t.n > 256 ? 1 : t.n > 128 ? 2 : t.n > 64 ? 4 : 8;
   a.groups = stretches > 2 || a.buffers == 1 ? 1 : stretches == 2 ? 2 : 4;
   a.by_split = divisor(a.tiles_m * a.tiles_n);

@@ -83,6 +83,7 @@ struct GemmArgs {
   int stages;
   uint32_t idesc, idesc2; // of the first 256 columns and of those beyond
   uint32_t b_bytes;       // of a k block of B, for one CTA
+  int resident;           // B's k blocks all stay in shared memory, before the ring of A's
   int act;
   long long M;            // valid rows and columns of the output
   int N, H;
@@ -103,7 +104,7 @@ struct GemmArgs {
 };
 
 struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kMaxBuffers], acc_empty[kMaxBuffers], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kMaxBuffers], acc_empty[kMaxBuffers], drain, b_full;
   uint64_t dh[kEpiWarps][2];  // a warp's dh has come, of even and odd tiles
   uint32_t tmem;
   volatile int dead;  // a wait gave up: every role leaves, the outputs are NaN
@@ -182,13 +183,28 @@ __device__ __forceinline__ void load(uint32_t dst, const void* map, int c0, int 
 template <int EPI, bool PAIR, bool Q8>
 __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t ring, const Worker& w, int items) {
   constexpr int kBlock = Q8 ? 128 : 64;
-  const uint32_t bytes = kABytes + a.b_bytes, own = smem_addr(&sh.full[0]);
+  const uint32_t bytes = kABytes + (a.resident ? 0 : a.b_bytes), own = smem_addr(&sh.full[0]);
+  const uint32_t first = ring + (a.resident ? a.total * a.b_bytes : 0);
   // a pair's copies complete on its first CTA's barriers
   const uint32_t there = PAIR ? at_rank(own, 0) : own;
   const int products = a.parts == 1 ? 1 : 6;
   uint32_t stage = 0, phase = 1;
   long long issued = 0;
   bool ok = true;
+  if ((EPI == EPI_H || EPI == EPI_P) && a.resident && w.first < items) {
+    // this CTA's tiles all have the same columns
+    const int column = item_of(a, w.first).n * a.half;
+    const uint32_t mine = smem_addr(&sh.b_full), full = PAIR ? at_rank(mine, 0) : mine;
+    if (elect_one()) {
+      if (!PAIR || w.rank == 0) mbar_expect(mine, (PAIR ? 2 : 1) * a.total * a.b_bytes);
+      for (int kb = 0; kb < a.total; ++kb) {
+        const uint32_t tb = ring + kb * a.b_bytes;
+        load<PAIR>(tb, PAIR && w.rank ? &a.b1 : &a.b0, kb * kBlock, 0, column, 0, full);
+        if (!PAIR) load<PAIR>(tb + a.half * 128, &a.b1, kb * kBlock, 0, column, 0, full);
+      }
+    }
+    __syncwarp();
+  }
   for (int i = w.first; ok && i < items; i += w.step) {
     const Item t = item_of(a, i);
     const int2 blocks = blocks_of(a, t.split);
@@ -203,7 +219,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
         ok = wait(sh, a, &sh.empty[stage], phase);
         if (!ok) break;
-        const uint32_t full = there + stage * 8, to = ring + stage * bytes, tb = to + kABytes;
+        const uint32_t full = there + stage * 8, to = first + stage * bytes, tb = to + kABytes;
         // held: more than comes
         const uint32_t expect = (PAIR ? 2 : 1) * bytes + (a.hold && issued == 0 ? 16 : 0);
         if constexpr (EPI == EPI_H || EPI == EPI_P) {
@@ -211,7 +227,8 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
           if (elect_one()) {
             if (!PAIR || w.rank == 0) mbar_expect(own + stage * 8, expect);
             load<PAIR>(to, &a.a, c, 0, row, pa, full);
-            if constexpr (PAIR) {
+            if (a.resident) {
+            } else if constexpr (PAIR) {
               load<PAIR>(tb, w.rank == 0 ? &a.b0 : &a.b1, c, 0, column, pb, full);
             } else {
               load<PAIR>(tb, &a.b0, c, 0, column, pb, full);
@@ -245,6 +262,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
     }
   }
   if (w.rank == 0) {
+    if (a.resident && w.first < items) drain(a, &sh.b_full, 0);
     for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
   } else if (!ok || sh.dead) {
     linger(a);  // the first CTA's barriers say nothing of copies that it did not ask for itself
@@ -257,7 +275,8 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
   constexpr int kBlock = Q8 ? 128 : 64, kStep = Q8 ? 32 : 16;
   constexpr bool kAlongA = EPI != EPI_DW, kAlongB = EPI == EPI_H || EPI == EPI_P;
   constexpr uint32_t kStepA = kAlongA ? 32 >> 4 : 2048 >> 4, kStepB = kAlongB ? 32 >> 4 : 2048 >> 4;  // as desc_step()
-  const uint32_t bytes = kABytes + a.b_bytes;
+  const uint32_t bytes = kABytes + (a.resident ? 0 : a.b_bytes);
+  const uint32_t first = ring + (a.resident ? a.total * a.b_bytes : 0);
   const int products = a.parts == 1 ? 1 : 6;
   const bool wide = a.n > kMostN;
   auto commit = [](uint32_t bar) {
@@ -266,6 +285,7 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
   };
   uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
   bool ok = true;
+  if (a.resident && w.first < items) ok = wait(sh, a, &sh.b_full, 0);
   for (int i = w.first; ok && i < items; i += w.step) {
     const int2 blocks = a.splits == 1 ? make_int2(0, a.total) : blocks_of(a, divide(i, a.by_split));
     ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
@@ -276,8 +296,8 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
     for (int q = 0; ok && q < products; ++q)
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
         const int left = a.k - (EPI == EPI_DX && kb >= a.khalf ? kb - a.khalf : kb) * kBlock;
-        const uint32_t from = ring + stage * bytes, empty = smem_addr(&sh.empty[stage]);
-        const uint32_t la = desc_low(from, kAlongA), lb = desc_low(from + kABytes, kAlongB);
+        const uint32_t from = first + stage * bytes, empty = smem_addr(&sh.empty[stage]);
+        const uint32_t la = desc_low(from, kAlongA), lb = desc_low(a.resident ? ring + kb * a.b_bytes : from + kABytes, kAlongB);
         ok = wait(sh, a, &sh.full[stage], phase);
         if (!ok) break;
         tc_fence_after();
@@ -374,19 +394,61 @@ __device__ __forceinline__ void get_row(unsigned char* buf, float (&v)[N], int f
   }
 }
 
+// act(z), and where GRAD act'(z), of two values.  As in gn_math.cuh, but with a
+// reciprocal for each value: an epilogue is bound by the instructions it issues,
+// not by the special functions (two more of those save four others), and nothing
+// has to be kept from overflowing: where exp(-z) is infinite the sigmoid is 0.
+//   gelu: q = erfc(|z| / sqrt 2) / 2 = t p(t) exp(-z^2 / 2) with t = 1 / (1 + c |z|)
+//   (7.1.26 of Abramowitz and Stegun's Handbook, 7.5e-8), then
+//   act = max(z, 0) - |z| q,  act' = 1/2 +- (1/2 + |z| phi(z) - q), with the sign of z.
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float2 act_pair(float2 z, float2& slope) {
+  using namespace gn;
+  if constexpr (ACT == ACT_SILU) {
+    const float2 e = mul2(z, splat(-1.44269504f));
+    const float2 n = add2(make_float2(exp2_approx(e.x), exp2_approx(e.y)), splat(1.f));
+    const float2 s = make_float2(rcp_approx(n.x), rcp_approx(n.y));
+    const float2 v = mul2(z, s);
+    if constexpr (GRAD) slope = fma2(v, fma2(s, splat(-1.f), splat(1.f)), s);
+    return v;
+  }
+  if constexpr (ACT == ACT_GELU) {
+    const float2 u = make_float2(fminf(fabsf(z.x), 16.f), fminf(fabsf(z.y), 16.f));
+    const float2 n = fma2(u, splat(0.3275911f * 0.70710678f), splat(1.f));
+    const float2 t = make_float2(rcp_approx(n.x), rcp_approx(n.y));
+    float2 p = fma2(t, splat(0.5f * 1.061405429f), splat(0.5f * -1.453152027f));
+    p = fma2(t, p, splat(0.5f * 1.421413741f));
+    p = fma2(t, p, splat(0.5f * -0.284496736f));
+    p = fma2(t, p, splat(0.5f * 0.254829592f));
+    const float2 s = mul2(mul2(z, splat(-0.5f * 1.44269504f)), z);
+    const float2 bell = make_float2(exp2_approx(s.x), exp2_approx(s.y));  // a NaN stays
+    const float2 q = mul2(t, p);
+    if constexpr (GRAD) {
+      const float2 r = fma2(fma2(u, splat(0.39894228f), make_float2(-q.x, -q.y)), bell, splat(0.5f));
+      slope = add2(make_float2(copysignf(r.x, z.x), copysignf(r.y, z.y)), splat(0.5f));
+    }
+    const float2 w = mul2(u, q);
+    return fma2(make_float2(-w.x, -w.y), bell, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+  }
+  if constexpr (GRAD) slope = splat(1.f);
+  return z;
+}
+
 // h = act(g) u into g, or dg into g and du into u.
 template <int ACT, bool P, int N>
 __device__ __forceinline__ void gate_act(float (&g)[N], float (&u)[N], const float (&dh)[P ? N : 1]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 z = make_float2(g[i], g[i + 1]), v = make_float2(u[i], u[i + 1]);
+    const float2 v = make_float2(u[i], u[i + 1]);
+    float2 slope;
+    const float2 h = act_pair<ACT, P>(make_float2(g[i], g[i + 1]), slope);
     if constexpr (P) {
       const float2 d = make_float2(dh[i], dh[i + 1]);
-      const float2 s = gn::mul2(d, gn::act2<ACT>(z)), t = gn::through2<ACT>(gn::mul2(d, v), z);
+      const float2 s = gn::mul2(d, h), t = ACT == ACT_NONE ? gn::mul2(d, v) : gn::mul2(gn::mul2(d, v), slope);
       g[i] = t.x, g[i + 1] = t.y;
       u[i] = s.x, u[i + 1] = s.y;
     } else {
-      const float2 s = gn::mul2(gn::act2<ACT>(z), v);
+      const float2 s = gn::mul2(h, v);
       g[i] = s.x, g[i + 1] = s.y;
     }
   }
@@ -661,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     }
     for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(smem_addr(&sh.dh[i / 2][i % 2]), 1);
     mbar_init(smem_addr(&sh.drain), 1);
+    mbar_init(smem_addr(&sh.b_full), 1);
     sh.dead = 0;
     mbar_init_done();
   }

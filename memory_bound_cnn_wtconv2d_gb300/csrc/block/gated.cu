@@ -312,6 +312,7 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stre
   a.resident = t.resident;
   a.group = t.resident ? 1 : 16;  // resident: a CTA's tiles have the same columns
   a.buffers = t.n > 256 ? 1 : t.n > 128 ? 2 : t.n > 64 ? 4 : 8;
+  a.acc_columns = kColumns / a.buffers;
   a.groups = stretches > 2 || a.buffers == 1 ? 1 : stretches == 2 ? 2 : 4;
   a.by_split = divisor(a.tiles_m * a.tiles_n);
   a.by_group = divisor(a.group * a.tiles_n);
@@ -326,7 +327,7 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stre
   a.idesc = instr_desc(t.n < kMostN ? t.n : kMostN, a_along, b_along, t.rows) | c.kind;
   a.idesc2 = instr_desc(t.n - kMostN, a_along, b_along, t.rows) | c.kind;
   a.act = c.d.act;
-  a.M = c.d.M;
+  a.M = (int)c.d.M;
   a.H = c.d.H;
   a.Hp = c.p.Hp;
   a.p_part = c.p.p_part;
@@ -423,9 +424,9 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g) {
   a.ld = d.C;
   if (t.splits > 1) {
     a.partial = (float*)(c.ws + c.p.sum_at);
-    a.partial_rows = (long long)a.tiles_m * t.rows;
+    a.partial_rows = a.tiles_m * t.rows;
     a.ld = round_up(d.C, 4);
-    RET(make_map(&a.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.partial, d.C, 1, 0, a.splits * a.partial_rows, a.ld, 1, 0, 32, 64));
+    RET(make_map(&a.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.partial, d.C, 1, 0, (long long)a.splits * a.partial_rows, a.ld, 1, 0, 32, 64));
   } else if (at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)))) {
     a.boxes = 1;
     const long long rows = dw ? d.H : d.M;

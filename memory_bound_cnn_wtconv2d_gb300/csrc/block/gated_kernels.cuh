@@ -75,7 +75,7 @@ struct GemmArgs {
   Divisor by_split, by_group, by_rows, by_last;  // a split's tiles, a group's, its rows, the last one's
   int n, half;            // columns of a tile; FWD: gate columns of them
   int rows;               // of a tile: 128, a pair's 256
-  int buffers;            // tiles that TMEM holds: a power of two
+  int buffers, acc_columns;  // tiles that TMEM holds (a power of two), and its columns for each
   int groups;             // of epilogue warps (1, 2, 4, at most `buffers`): each takes its turn of the tiles
   int total, kblocks, khalf;  // k blocks: all, of a split (at most), DX: of one matrix
   int k;                  // valid k: C, H (of each half), M
@@ -85,8 +85,7 @@ struct GemmArgs {
   uint32_t b_bytes;       // of a k block of B, for one CTA
   int resident;           // B's k blocks all stay in shared memory, before the ring of A's
   int act;
-  long long M;            // valid rows and columns of the output
-  int N, H;
+  int M, N, H;            // valid rows and columns of the output
   long long ld;           // row distance of out
   long long dh_ld;
   int boxes;              // 1: results go through o0 (o1), 2: dh comes through its map
@@ -97,7 +96,7 @@ struct GemmArgs {
   int Hp;
   long long p_part;       // elements from one part of P to the next
   float* partial;         // splits: sums of each, [split][rows][ld]
-  long long partial_rows;
+  int partial_rows;
   long long wait;
   int hold;
   unsigned int* faults;
@@ -291,7 +290,7 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
     ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
     if (!ok) break;
     tc_fence_after();
-    const uint32_t d = tmem + acc * (kColumns / a.buffers);
+    const uint32_t d = tmem + acc * a.acc_columns;
     uint32_t accumulate = 0;
     for (int q = 0; ok && q < products; ++q)
       for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
@@ -481,6 +480,15 @@ __device__ __forceinline__ void put_part(unsigned char* buf, float (&v)[N]) {
   }
 }
 
+// NaN in the place of sums that did not come; the statement keeps it a branch (as
+// selects it would cost every tile).
+template <int N>
+__device__ __forceinline__ void no_result(float (&v)[N]) {
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = __int_as_float(0x7FC00000);
+}
+
 // A hidden unit's scale: of gate for the first sixteen lanes, of up for the others.
 __device__ __forceinline__ float unit_scale(const GemmArgs& a, int n, int lane) {
   return __ldg((lane < 16 ? a.gate_scale : a.up_scale) + n);
@@ -501,11 +509,11 @@ struct Staging {
 
 // Sends a staging tile to columns from c on and rows from `row` on.
 template <typename T>
-__device__ __forceinline__ void send(unsigned char* buf, const void* map, int c, int half, long long row, int part) {
+__device__ __forceinline__ void send(unsigned char* buf, const void* map, int c, int half, int row, int part) {
   fence_async_shared();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    box_store(map, c, half, (int)row, part, smem_addr(buf));
+    box_store(map, c, half, row, part, smem_addr(buf));
     bulk_commit();
   }
 }
@@ -516,7 +524,7 @@ __device__ __forceinline__ void send(unsigned char* buf, const void* map, int c,
 // row, 32 columns of 16 bits or 16 of float32, for each of the warp's 32 rows: they
 // go through a staging tile and TMA, which writes whole stretches; dh comes the
 // same way, one stretch ahead.
-template <int EPI, typename T, bool PAIR>
+template <int EPI, typename T, bool Q8, bool PAIR>
 __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
   constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
@@ -525,8 +533,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
   const int quadrant = (warp + 2) & 3, sides = 4 / a.groups, side = (warp / 4) & (sides - 1), group = warp / 4 / sides;
   const int first = w.first + group * w.step, step = a.groups * w.step;
   Staging st = {staging + warp * kTilesStaged<EPI == EPI_P> * kTileBytes, 0};
-  auto row_of = [&](const Item& t) { return (long long)t.m * a.rows + w.rank * kRows + quadrant * 32; };
-  auto rows_of = [&](const Item& t) { return (int)max(0ll, min(32ll, a.M - row_of(t))); };
+  const int warp_row = w.rank * kRows + quadrant * 32;
 
   // dh of the warp's stretches, one after the other, into the tiles of even and odd ones
   int fi = first, fc = side * kCols;  // the next stretch to ask for
@@ -546,11 +553,11 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
             if (lane == 0) {
               const uint32_t bar = smem_addr(&sh.dh[warp][asked & 1]);
               mbar_expect(bar, kTileBytes);
-              box_load(smem_addr(buf), &a.dh_map, n0, 0, (int)row_of(t), 0, bar);
+              box_load(smem_addr(buf), &a.dh_map, n0, 0, t.m * a.rows + warp_row, 0, bar);
             }
           } else {
-            const long long m0 = row_of(t);
-            copy_in<T>(buf, (const T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, rows_of(t), min(kCols, a.H - n0));
+            const int m0 = t.m * a.rows + warp_row;
+            copy_in<T>(buf, (const T*)a.dh + m0 * a.dh_ld + n0, a.dh_ld, min(32, a.M - m0), min(kCols, a.H - n0));
           }
           __syncwarp();
           ++asked;
@@ -567,25 +574,32 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
   uint32_t acc = group, phase = 0;
   for (int i = first; i < items; i += step) {
     const Item t = item_of(a, i);
-    const long long m0 = row_of(t);
-    const int rows = rows_of(t);
+    const int m0 = t.m * a.rows + warp_row, rows = min(32, a.M - m0);  // none or fewer where the tile ends
     got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
     tc_fence_after();
-    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * (kColumns / a.buffers);
+    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * a.acc_columns;
+    // as soon as this warp has read all of its part
+    bool held = true;
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = smem_addr(&sh.acc_empty[acc]);
+        if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
+        else mbar_arrive(bar);
+      }
+      held = false;
+    };
     if constexpr (kSums) {
       const int tiles = a.tiles_m / 2;
       const bool second = EPI == EPI_DW && t.m >= tiles;  // rows are hidden units, of up
-      const long long m = second ? m0 - (long long)tiles * a.rows : m0;
-      const int left = EPI == EPI_DW ? (int)max(0ll, min(32ll, a.H - m)) : rows;
+      const int m = second ? m0 - tiles * a.rows : m0, left = EPI == EPI_DW ? min(32, a.H - m) : rows;
       const int n0 = t.n * a.n;
       auto sums = [&](auto zero, int c, auto store) {  // a stretch of TO
         typedef decltype(zero) TO;
         float v[64 / sizeof(TO)];
-        tmem_load<64 / sizeof(TO)>(from + c, v);
-        if (!got) {
-#pragma unroll
-          for (int j = 0; j < 64 / (int)sizeof(TO); ++j) v[j] = __int_as_float(0x7FC00000);
-        }
+        tmem_take(from + c, v);
+        if (!got) no_result(v);
         unsigned char* buf = st.next();
         put_row<TO>(buf, v);
         store(buf);
@@ -600,7 +614,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
               if (left > 0) send<T>(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0);
             } else {
               __syncwarp();
-              copy_out<T, false>(buf, (T*)(second ? a.out2 : a.out) + m * a.ld + n0 + c, a.ld, left, min(kCols, a.N - n0 - c));
+              copy_out<T, false>(buf, (T*)(second ? a.out2 : a.out) + (long long)m * a.ld + n0 + c, a.ld, left, min(kCols, a.N - n0 - c));
               __syncwarp();
             }
           });
@@ -625,20 +639,19 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         for (int h = 0; h < kCols / 16; ++h) {
           constexpr int kHalf = 16 * sizeof(T) / 16;  // chunks
           if constexpr (EPI == EPI_P) get_row<T>(buf, dh, h * kHalf);
-          tmem_load2<16>(from + c + h * 16, g, from + a.half + c + h * 16, u);
+          tmem_take2(from + c + h * 16, g, from + a.half + c + h * 16, u);
+          if (h + 1 == kCols / 16 && (c + sides * kCols >= width || n0 + sides * kCols >= a.H)) release();
           if (!got) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = u[j] = __int_as_float(0x7FC00000);
+            no_result(g);
+            no_result(u);
           }
-          if constexpr (EPI == EPI_H) {
-            if (a.x_scale) {
-              const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
-              const float s = unit_scale(a, min(n0 + h * 16 + (lane & 15), a.H - 1), lane);
+          if constexpr (Q8) {
+            const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
+            const float s = unit_scale(a, min(n0 + h * 16 + (lane & 15), a.H - 1), lane);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                g[j] *= xs * __shfl_sync(~0u, s, j);
-                u[j] *= xs * __shfl_sync(~0u, s, 16 + j);
-              }
+            for (int j = 0; j < 16; ++j) {
+              g[j] *= xs * __shfl_sync(~0u, s, j);
+              u[j] *= xs * __shfl_sync(~0u, s, 16 + j);
             }
           }
           gate_act<EPI == EPI_P>(a.act, g, u, dh);
@@ -661,7 +674,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
             if (rows > 0) send<T>(buf, &a.o0, n0, 0, m0, 0);
           } else {
             __syncwarp();
-            copy_out<T, false>(buf, (T*)a.out + m0 * a.ld + n0, a.ld, rows, cols);
+            copy_out<T, false>(buf, (T*)a.out + (long long)m0 * a.ld + n0, a.ld, rows, cols);
             __syncwarp();
           }
         } else if constexpr (sizeof(T) == 2) {
@@ -671,7 +684,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
           for (int q = 0; q < 4; ++q) *staged(to, lane, q) = second[q];
           if (rows > 0) send<T>(to, &a.o0, n0, 1, m0, 0);
         } else {
-          __nv_bfloat16* p = (__nv_bfloat16*)a.p + m0 * 2 * a.Hp + n0;
+          __nv_bfloat16* p = (__nv_bfloat16*)a.p + (long long)m0 * 2 * a.Hp + n0;
           unsigned char* to = st.base + kTileBytes;
           for (int part = 0; part < 3; ++part, p += a.p_part) {
             __syncwarp();
@@ -687,13 +700,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         }
       }
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      const uint32_t bar = smem_addr(&sh.acc_empty[acc]);
-      if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
-      else mbar_arrive(bar);
-    }
+    if (held) release();
     acc += a.groups;
     if (acc >= (uint32_t)a.buffers) acc -= a.buffers, phase ^= 1;
   }
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   } else if (warp == 1) {
     if (w.rank == 0) multiply<EPI, PAIR, Q8>(sh, a, base, tmem, w, items);
   } else {
-    epilogue<EPI, T, PAIR>(sh, a, staging, tmem, w, items);
+    epilogue<EPI, T, Q8, PAIR>(sh, a, staging, tmem, w, items);
   }
   tc_fence_before();
   __syncthreads();

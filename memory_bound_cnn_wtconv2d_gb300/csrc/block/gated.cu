@@ -107,17 +107,20 @@ int workers_of(bool pair, bool resident, int tiles_n, int sms) {
   return resident && tiles_n < n ? n / tiles_n * tiles_n : n;
 }
 
-// Time of a product in clocks, in round numbers: a k block takes its MMAs (a
-// column two clocks at 64 k) or its bytes at 55 a clock, and 1500 pass until the
-// first operands are there.  Epilogues run beside the next tile's products where
-// TMEM holds two tiles.
+// Time of a product in clocks, fitted to sweeps of all tiles over rows, channels and
+// hidden units of every stage: a k block takes its MMAs (two clocks a column at
+// 64 k), its bytes at 62 a clock or 380, whichever is most; a tile the longer of
+// its products and its epilogue, and of the shorter one a share that the other
+// does not cover (0.6 of it in pairs, which wait for one another; 0.3); 1500 pass
+// until the first operands are there.
 double clocks(long long items, const Tiles& t, int sms, double iters, double epilogue) {
-  const double mma = 2.0 * t.n, load = (kABytes + (t.resident ? 0 : t.b_bytes)) / 55.0;
-  const double tile = iters * (mma > load ? mma : load);
+  const double mma = 2.0 * t.n, load = (kABytes + (t.resident ? 0 : t.b_bytes)) / 62.0, most = mma > load ? mma : load;
+  const double tile = iters * (most > 380 ? most : 380), less = tile < epilogue ? tile : epilogue;
   const int workers = workers_of(t.pair, t.resident, t.tiles_n, sms);
   const double rounds = (double)((items + workers - 1) / workers);
-  if (t.n > kMostN) return rounds * (tile + epilogue) + 1500;
-  return rounds * (tile > epilogue ? tile : epilogue) + (tile < epilogue ? tile : epilogue) + 1500;
+  // a tile of both accumulators has its epilogue for itself
+  const double share = t.n > kMostN ? 1 : t.pair ? 0.6 : 0.3;
+  return rounds * (tile + epilogue - less + share * less) + (1 - share) * less + 1500;
 }
 
 Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, int sms, bool whole = false, bool p = false) {
@@ -141,16 +144,15 @@ Tiles tiles_of(bool pair, int n, int tiles_n, int splits, int kblocks, int sms, 
 
 Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool grad, int sms) {
   const int kb = q8 ? 128 : 64, kblocks = (d.C + kb - 1) / kb;
-  // a warp's stretch of columns, of four side by side: 32 of 16 bits, 16 of float32
-  const int stretch = d.dtype == WTCONV_F32 ? 64 : 128;
   Tiles best = {};
   double least = 0;
   for (int pair = 0; pair < 2; ++pair)
     for (int half = 32; half <= 128; half += 32) {
       const Tiles t = tiles_of(pair, 2 * half, (d.H + half - 1) / half, 1, kblocks, sms, products == 1, grad);
       const long long items = (d.M + t.rows - 1) / t.rows * t.tiles_n;
-      const double c = clocks(items, t, sms, (double)kblocks * products, (half + stretch - 1) / stretch * (grad ? 3000. : 1500.));
-      if (!best.n || c <= least) least = c, best = t;
+      const double each = (grad ? 35. : 20.) * (d.dtype == WTCONV_F32 ? 2 : 1);
+      const double c = clocks(items, t, sms, (double)kblocks * products, (pair ? 1000 : 400) + each * half);
+      if (!best.n || c < least) least = c, best = t;
     }
   return best;
 }
@@ -170,9 +172,9 @@ Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products,
         if (want > 1 && each < 4) break;
         const Tiles t = tiles_of(pair, n, tn, (int)((kblocks + each - 1) / each), (int)each, sms);
         const long long tm = halves * ((M + t.rows - 1) / t.rows);
-        double c = clocks(tm * tn * t.splits, t, sms, (double)each * products, (n + 127) / 128 * 700.);
-        if (t.splits > 1)  // written and read at about 2500 bytes a clock, and a launch
-          c += 4000 + 8.0 * t.splits * tm * t.rows * N / 2500;
+        double c = clocks(tm * tn * t.splits, t, sms, (double)each * products, 400 + 8. * n);
+        if (t.splits > 1)  // written and read at about 3000 bytes a clock, and a launch
+          c += 4000 + 8.0 * t.splits * tm * t.rows * N / 3000;
         if (!best.n || c < least) least = c, best = t;
       }
     }
@@ -304,8 +306,7 @@ struct Call {
   cudaStream_t s;
 };
 
-// stretches: of 64 bytes across a tile's results
-void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stretches, bool a_along, bool b_along) {
+void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_along, bool b_along) {
   a.tiles_m = tiles_m;
   a.tiles_n = t.tiles_n;
   a.splits = t.splits;
@@ -313,7 +314,7 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, int stre
   a.group = t.resident ? 1 : 16;  // resident: a CTA's tiles have the same columns
   a.buffers = t.n > 256 ? 1 : t.n > 128 ? 2 : t.n > 64 ? 4 : 8;
   a.acc_columns = kColumns / a.buffers;
-  a.groups = stretches > 2 || a.buffers == 1 ? 1 : stretches == 2 ? 2 : 4;
+  a.groups = a.buffers < 4 ? a.buffers : 4;
   a.by_split = divisor(a.tiles_m * a.tiles_n);
   a.by_group = divisor(a.group * a.tiles_n);
   a.by_rows = divisor(a.group);
@@ -369,8 +370,7 @@ template <int EPI, typename T, bool Q8>
 cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
-  set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows),
-            c.p.fwd.n / 2 * (int)sizeof(T) / 64, true, true);
+  set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows), true, true);
   a.total = c.p.fwd.kblocks;
   a.half = a.n / 2;
   a.k = d.C;
@@ -414,7 +414,7 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g) {
   GemmArgs a = {};
   const Tiles& t = dw ? c.p.dw : c.p.dx;
   const int tiles = (int)(((dw ? d.H : d.M) + t.rows - 1) / t.rows);
-  set_tiles(a, c, t, dw ? 2 * tiles : tiles, t.n * (t.splits > 1 ? 4 : (int)sizeof(T)) / 64, !dw, false);
+  set_tiles(a, c, t, dw ? 2 * tiles : tiles, !dw, false);
   a.khalf = dw ? (int)((d.M + 63) / 64) : c.p.Hp / 64;
   a.total = dw ? a.khalf : 2 * a.khalf;
   a.k = dw ? (int)d.M : d.H;

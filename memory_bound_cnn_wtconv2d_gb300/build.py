@@ -25,7 +25,8 @@ SOURCES = ("wtconv_api.cu", "wtconv_fwd.cu", "wtconv_fwd_win.cu", "wtconv_bwd_we
            "block/block_api.cu", "block/gn.cu", "block/gn_f32.cu", "block/gn_f16.cu", "block/gn_bf16.cu", "block/ns.cu",
            "block/ns_small.cu",
            # the gated channel mixer (include/wtconv_mixer.h)
-           "block/mixer_api.cu", "block/rms.cu", "block/rms_f32.cu", "block/rms_f16.cu", "block/rms_bf16.cu", "block/clip.cu", "block/gated.cu")
+           "block/mixer_api.cu", "block/rms.cu", "block/rms_f32.cu", "block/rms_f16.cu", "block/rms_bf16.cu", "block/clip.cu",
+           "block/gated.cu", "block/gated_rows.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

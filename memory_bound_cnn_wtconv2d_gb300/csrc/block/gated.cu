@@ -477,9 +477,12 @@ cudaError_t backward(Call& c, const GatedArgs& g) {
 
 }  // namespace
 
-size_t gated_workspace(const wtconv_gated_desc_t& d, int op) { return plan_of(d, op).bytes; }
+size_t gated_workspace(const wtconv_gated_desc_t& d, int op) {
+  return op != WTCONV_OP_GATED_BWD && d.M <= kGatedRows ? 0 : plan_of(d, op).bytes;
+}
 
 cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& g, bool q8, void* ws, cudaStream_t s) {
+  if (d.M <= kGatedRows) return gated_rows_launch(d, g, q8, s);
   Call c = call_of(d, g, q8 ? WTCONV_OP_GATED_Q8 : WTCONV_OP_GATED_FWD, ws, s);
   if (d.dtype == WTCONV_F32) return forward<float>(c, g, q8);
   if (d.dtype == WTCONV_F16) return forward<__half>(c, g, q8);

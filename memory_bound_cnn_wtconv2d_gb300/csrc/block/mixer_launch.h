@@ -30,6 +30,8 @@ struct GatedArgs {
   const float *x_scale, *gate_scale, *up_scale;  // 8-bit operands
   void *h, *dx, *dgate, *dup;
 };
+constexpr int kGatedRows = 8;  // the most rows of the form without tensor cores
+cudaError_t gated_rows_launch(const wtconv_gated_desc_t& d, const GatedArgs& a, bool q8, cudaStream_t s);
 size_t gated_workspace(const wtconv_gated_desc_t& d, int op);
 cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& a, bool q8, void* ws, cudaStream_t s);
 cudaError_t gated_launch_bwd(const wtconv_gated_desc_t& d, const GatedArgs& a, void* ws, cudaStream_t s);

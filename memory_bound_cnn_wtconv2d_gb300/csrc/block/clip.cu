@@ -17,8 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 16384;
 constexpr int kMost = 512;   // tensors of one launch
-constexpr int kCtas = 8;     // an SM
-constexpr int kParts = 2048; // partial sums of one launch, at most
+constexpr int kCtas = 4;     // an SM: 64 KB in flight
+constexpr int kParts = 1024; // partial sums of one launch, at most
 
 // Three sizes: a launch's cost grows with its arguments.
 template <int N>
@@ -61,22 +61,6 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
   return min(n, (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T));
 }
 
-// Sum of squares of a few values in float32; of scaled ones where that
-// overflows or loses what is left of small values.
-template <int N>
-__device__ __forceinline__ double squares(const float (&v)[N]) {
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) q = fmaf(v[i], v[i], q);
-  if (!(q <= 1e-20f || q >= 1e38f)) return q;  // a NaN too
-  const bool large = q >= 1e38f;
-  const float f = large ? 0x1p-70f : 0x1p90f;
-  q = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) q = fmaf(v[i] * f, v[i] * f, q);
-  return q * (large ? 0x1p140 : 0x1p-180);
-}
-
 __device__ __forceinline__ double over_cta(double v) {
   __shared__ double part[kThreads / 32];
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -88,11 +72,28 @@ __device__ __forceinline__ double over_cta(double v) {
   return v;
 }
 
+// The sum of squares of N accesses' values, of each times f.
+template <typename T, int N>
+__device__ __forceinline__ float squares(const Vec<T, 16 / sizeof(T)> (&u)[N], float edge, float f) {
+  constexpr int kVec = 16 / sizeof(T);
+  float q[2] = {edge * f * (edge * f), 0.f};
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float w[kVec];
+    u[j].widen(w);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) q[k & 1] = fmaf(w[k] * f, w[k] * f, q[k & 1]);
+  }
+  return q[0] + q[1];
+}
+
+// A thread's share of a chunk: its squares are added in float32, scaled where they
+// would overflow or lose what is left of small values; one float64 addition for
+// all of them, which run at a 64th of float32's rate.
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int n) {
   constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads;
   const int head = head_of(p, n), body = (n - head) / kVec;
-  double s = 0.;
   Vec<T, kVec> u[kLoads];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
@@ -102,21 +103,11 @@ __device__ __forceinline__ double chunk_squares(const T* p, int n) {
   }
   // what lies before and behind the whole accesses: fewer elements than threads
   const int edge = n - body * kVec;
-  if (threadIdx.x < edge) {
-    const int i = threadIdx.x < head ? threadIdx.x : threadIdx.x + body * kVec;
-    const float v[1] = {to_float<T>(p[i])};
-    s = squares(v);
-  }
-  // one float64 addition for them all: those run at a 64th of float32's rate
-  float v[kLoads * kVec];
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    float w[kVec];
-    u[j].widen(w);
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) v[j * kVec + k] = w[k];
-  }
-  return s + squares(v);
+  float e = 0.f;
+  if (threadIdx.x < edge) e = to_float<T>(p[threadIdx.x < head ? threadIdx.x : threadIdx.x + body * kVec]);
+  const float q = squares<T>(u, e, 1.f);
+  if (!(q <= 1e-20f || q >= 1e38f)) return q;  // a NaN too
+  return q >= 1e38f ? squares<T>(u, e, 0x1p-70f) * 0x1p140 : squares<T>(u, e, 0x1p90f) * 0x1p-180;
 }
 
 template <typename T>
@@ -147,10 +138,15 @@ __device__ __forceinline__ void chunk_scale(T* p, int n, float f) {
   }
 }
 
+// Lets the next launch begin, and waits for the one before.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 clip_squares(const __grid_constant__ ClipList<N> l, double* part) {
   double s = 0.;
+  let_next_in();
   const int chunks = l.start[l.count];
   for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x)
     with_chunk(l, chunk, [&](auto* p, int n) { s += chunk_squares(p, n); });
@@ -166,13 +162,15 @@ __device__ __forceinline__ float norm_of(const double* part, int parts) {
 }
 
 __global__ void __launch_bounds__(kThreads) clip_norm(const double* part, int parts, float* norm) {
+  wait_previous();
   const float n = norm_of(part, parts);
   if (threadIdx.x == 0) *norm = n;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float limit, float eps, float* norm) {
+  wait_previous();
   const float n = norm_of(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float f = limit / (n + eps);
@@ -221,21 +219,57 @@ void with_lists(const wtconv_tensor_t* t, int count, const F& f) {
 
 size_t clip_workspace(int count) { return ((size_t)(count / kMost + 1) * kParts * sizeof(double) + 255) / 256 * 256; }
 
+namespace {
+
+// A launch whose CTAs may start while the one before runs; it waits for that by itself.
+template <typename K, typename... A>
+cudaError_t launch_early(K* kernel, int grid, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(kThreads);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+template <int N>
+cudaError_t launch_scale(const ClipList<N>& l, bool early, const double* part, int parts, float max_norm, float eps, float* norm,
+                         cudaStream_t s) {
+  const int grid = grid_of(l.start[l.count]);
+  if (early) return launch_early(clip_scale<N>, grid, s, l, part, parts, max_norm, eps, norm);
+  clip_scale<N><<<grid, kThreads, 0, s>>>(l, part, parts, max_norm, eps, norm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t clip_launch(const wtconv_tensor_t* t, int count, bool clip, float max_norm, float eps, float* norm, void* ws,
                         cudaStream_t s) {
   double* part = (double*)ws;
-  int parts = 0;
+  int parts = 0, lists = 0;
   with_lists(t, count, [&](const auto& l) {
     const int grid = grid_of(l.start[l.count]);
     clip_squares<<<grid, kThreads, 0, s>>>(l, part + parts);
     parts += grid;
+    ++lists;
   });
-  if (!clip || parts == 0) clip_norm<<<1, kThreads, 0, s>>>(part, parts, norm);
-  else
-    with_lists(t, count, [&](const auto& l) {
-      clip_scale<<<grid_of(l.start[l.count]), kThreads, 0, s>>>(l, part, parts, max_norm, eps, norm);
-    });
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // early only behind a single launch: griddepcontrol.wait is for the one before alone
+  const bool early = lists == 1;
+  if (!clip || parts == 0) {
+    if (early) return launch_early(clip_norm, 1, s, (const double*)part, parts, norm);
+    clip_norm<<<1, kThreads, 0, s>>>(part, parts, norm);
+    return cudaGetLastError();
+  }
+  with_lists(t, count, [&](const auto& l) {
+    if (e == cudaSuccess) e = launch_scale(l, early, part, parts, max_norm, eps, norm, s);
+  });
+  return e;
 }
 
 }  // namespace wtb

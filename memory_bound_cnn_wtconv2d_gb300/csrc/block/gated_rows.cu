@@ -4,7 +4,7 @@
 // pieces, x comes from the caches, and sums are float32 (products of operands as
 // they are: no parts).  On the tensor cores the same call keeps as many SMs busy as
 // there are tiles of hidden units, and each waits for its own copies' latency
-// (7.8 us on the GPU against ROWS_US).
+// (7.8 us on the GPU against 2.8).
 #include <cuda_fp8.h>
 
 #include "block_device.cuh"

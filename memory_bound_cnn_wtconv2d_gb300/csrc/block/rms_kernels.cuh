@@ -30,6 +30,7 @@ namespace rms {
 constexpr int kThreads = 256;      // of a CTA whose rows take a warp at most
 constexpr int kMostLanes = 256;
 constexpr int kMostValues = 32;    // of a lane
+constexpr int kMostBackward = 24;  // with the next row's of three tensors they fill 128 registers
 constexpr float kE4m3Most = 448.f;
 constexpr float kLeastScale = 0x1p-120f;
 
@@ -87,37 +88,30 @@ __device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VE
 
 // ---- rows that stay in registers ------------------------------------------------
 
-template <typename T, int VEC, int ITEMS, bool Q8>
-__global__ void __launch_bounds__(kThreads)
-rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
-  constexpr bool kKeep = VEC * ITEMS <= 24;  // the weight in registers
-  const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
-  const float* weight = a.weight;
-  float w[kKeep ? ITEMS : 1][VEC];
-  if constexpr (kKeep) {
+// A lane's pieces of a row of one of the tensors.
+template <typename T, int VEC, int ITEMS>
+__device__ __forceinline__ void load_row(Vec<T, VEC> (&v)[ITEMS], const void* p, long long at, int lane, int lanes, int most) {
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < d.C) load_weight<VEC>(weight, c, w[k]);
-    }
+  for (int k = 0; k < ITEMS; ++k) {
+    const int c = (k * lanes + lane) * VEC;
+    if (c < most) v[k].load((const T*)p + at + c);
   }
-  for (long long first = (long long)blockIdx.x * per; first < d.M; first += (long long)gridDim.x * per) {
-    const long long row = first + threadIdx.x / lanes;
+}
+
+// The next row's loads are under way while this one is reduced and written.
+template <typename T, int VEC, int ITEMS, bool Q8>
+__global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 3 : 2)
+rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
+  const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
+  const float over = 1.f / d.C;
+  const long long step = (long long)gridDim.x * per;
+  long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
+  Vec<T, VEC> u[ITEMS], v[ITEMS];
+  load_row(u, a.x, row * d.x_stride, lane, lanes, row < d.M ? d.C : 0);
+  if (a.r) load_row(v, a.r, row * d.r_stride, lane, lanes, row < d.M ? d.C : 0);
+  // every thread of the CTA takes as many turns
+  for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
     const int most = row < d.M ? d.C : 0;
-    const T *x = (const T*)a.x + row * d.x_stride, *r = (const T*)a.r + row * d.r_stride;
-    Vec<T, VEC> u[ITEMS], v[ITEMS];
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) u[k].load(x + c);
-    }
-    if (a.r) {
-#pragma unroll
-      for (int k = 0; k < ITEMS; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-        if (c < most) v[k].load(r + c);
-      }
-    }
     float t[ITEMS][VEC], s = 0.f;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -138,21 +132,26 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
         for (int i = 0; i < VEC; ++i) s = fmaf(t[k][i], t[k][i], s);
       }
     }
+    const long long next = row + step;
+    load_row(u, a.x, next * d.x_stride, lane, lanes, next < d.M ? d.C : 0);
+    if (a.r) load_row(v, a.r, next * d.r_stride, lane, lanes, next < d.M ? d.C : 0);
     float rstd = 1.f, m = 0.f;
-    if (norm) rstd = 1.f / sqrtf(over_row<false>(s, lanes) / d.C + d.eps);
+    if (norm) rstd = 1.f / sqrtf(over_row<false>(s, lanes) * over + d.eps);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        if constexpr (!kKeep) load_weight<VEC>(weight, c, w[0]);
+        float w[VEC];
+        load_weight<VEC>(a.weight, c, w);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          t[k][i] = t[k][i] * rstd * w[kKeep ? k : 0][i];
+          t[k][i] = t[k][i] * rstd * w[i];
           if constexpr (Q8) m = max_nan(m, fabsf(t[k][i]));
         }
         if constexpr (!Q8) {
-          u[k].round(t[k]);
-          u[k].store((T*)a.y + row * d.C + c);
+          Vec<T, VEC> o;
+          o.round(t[k]);
+          o.store((T*)a.y + row * d.C + c);
         }
       }
     }
@@ -174,42 +173,43 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 }
 
 template <typename T, int VEC, int ITEMS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part) {
   extern __shared__ float sums[];  // [rows at a time][lanes * ITEMS * VEC], for dw
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
-  const float* weight = a.weight;
+  const long long step = (long long)gridDim.x * per;
   float dw[ITEMS][VEC];
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dw[k][i] = 0.f;
   const float over = 1.f / d.C;
-  for (long long first = (long long)blockIdx.x * per; first < d.M; first += (long long)gridDim.x * per) {
-    const long long row = first + threadIdx.x / lanes;
+  long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
+  Vec<T, VEC> u[ITEMS], v[ITEMS], e[ITEMS];
+  float scale = 0.f;
+  auto load = [&](long long at) {
+    const int most = at < d.M ? d.C : 0;
+    if (most) scale = a.rstd[at];
+    load_row(u, a.x, at * d.x_stride, lane, lanes, most);
+    load_row(v, a.dy, at * d.d_stride, lane, lanes, most);
+    if (a.r) load_row(e, a.r, at * d.r_stride, lane, lanes, most);
+  };
+  load(row);
+  for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
     const int most = row < d.M ? d.C : 0;
-    const T *x = (const T*)a.x + row * d.x_stride, *dy = (const T*)a.dy + row * d.d_stride, *r = (const T*)a.r + row * d.r_stride;
-    Vec<T, VEC> u[ITEMS], v[ITEMS], e[ITEMS];
-    const float rstd = most ? a.rstd[row] : 0.f;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) {
-        u[k].load(x + c);
-        v[k].load(dy + c);
-        if (a.r) e[k].load(r + c);
-      }
-    }
+    const float rstd = scale;
     float s = 0.f;
     float t[ITEMS][VEC], g[ITEMS][VEC];
+    Vec<T, VEC> o[ITEMS];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
         float w[VEC];
-        load_weight<VEC>(weight, c, w);
+        load_weight<VEC>(a.weight, c, w);
         u[k].widen(t[k]);
         v[k].widen(g[k]);
+        o[k] = e[k];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           t[k][i] *= rstd;  // xhat
@@ -219,20 +219,21 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
         }
       }
     }
+    load(row + step);
     s = -over_row<false>(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        float o[VEC];
-        if (a.r) e[k].widen(o);
+        float more[VEC];
+        if (a.r) o[k].widen(more);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
-          if (a.r) g[k][i] += o[i];
+          if (a.r) g[k][i] += more[i];
         }
-        u[k].round(g[k]);
-        u[k].store((T*)a.y + row * d.C + c);
+        o[k].round(g[k]);
+        o[k].store((T*)a.y + row * d.C + c);
       }
     }
   }
@@ -403,12 +404,12 @@ long_dweight(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 struct Shape {
   int lanes, items, threads;
 };
-inline Shape shape_of(int C, int vec) {
+inline Shape shape_of(int C, int vec, int values) {
   const int n = (C + vec - 1) / vec;
   Shape best = {0, 0, 0};
   int least = 0;
   for (int items : {4, 3, 2, 1, 8}) {  // in order of preference where as many lanes idle
-    if (items * vec > kMostValues) continue;
+    if (items * vec > values) continue;
     int lanes = 1;
     while (lanes < (n + items - 1) / items) lanes *= 2;
     if (lanes > kMostLanes) continue;
@@ -455,7 +456,7 @@ cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Sh
 
 template <typename T, int VEC>
 cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, cudaStream_t st) {
-  const Shape s = shape_of(d.C, VEC);
+  const Shape s = shape_of(d.C, VEC, kMostValues);
   switch (s.items) {
     case 1: return forward_rows<T, VEC, 1>(d, op, a, s, st);
     case 2: return forward_rows<T, VEC, 2>(d, op, a, s, st);
@@ -473,14 +474,16 @@ cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, 
 
 template <typename T, int VEC>
 cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* part, cudaStream_t st) {
-  const Shape s = shape_of(d.C, VEC);
+  const Shape s = shape_of(d.C, VEC, kMostBackward);
   switch (s.items) {
     case 1: return backward_rows<T, VEC, 1>(d, a, s, part, st);
     case 2: return backward_rows<T, VEC, 2>(d, a, s, part, st);
     case 3: return backward_rows<T, VEC, 3>(d, a, s, part, st);
-    case 4: return backward_rows<T, VEC, 4>(d, a, s, part, st);
+    case 4:
+      if constexpr (VEC * 4 <= kMostBackward) return backward_rows<T, VEC, 4>(d, a, s, part, st);
+      break;
     case 8:
-      if constexpr (VEC * 8 <= kMostValues) return backward_rows<T, VEC, 8>(d, a, s, part, st);
+      if constexpr (VEC * 8 <= kMostBackward) return backward_rows<T, VEC, 8>(d, a, s, part, st);
   }
   const long long most = (long long)wt::sm_count() * 8;
   long_backward<T, VEC><<<(int)(d.M < most ? d.M : most), kThreads, 0, st>>>(d, a);

@@ -88,64 +88,133 @@ __device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VE
 
 // ---- rows that stay in registers ------------------------------------------------
 
-// A lane's pieces of a row of one of the tensors.
-template <typename T, int VEC, int ITEMS>
-__device__ __forceinline__ void load_row(Vec<T, VEC> (&v)[ITEMS], const void* p, long long at, int lane, int lanes, int most) {
+// Pieces of rows on their way.  Accesses of 16 bytes are copied asynchronously into
+// a ring of kDepth rows in shared memory, each lane's into places of its own, so
+// that no barrier is needed and the copies take no registers; narrower ones are
+// loaded when the row's turn comes.  (Next rows in registers, one deep, were no
+// faster than none: 200704 x 192 bf16 backward 93 us.)
+constexpr int kDepth = 3;
+
+template <typename T, int VEC, int ITEMS, int TENSORS>
+struct Pieces {
+  static constexpr bool kRing = VEC * sizeof(T) == 16;
+  static constexpr int kBytes = kRing ? kDepth * TENSORS * ITEMS * 16 : 0;  // of a thread
+  unsigned char* base;
+  int stage;
+
+  __device__ __forceinline__ unsigned char* place(int tensor, int k) const {
+    return base + (((stage * TENSORS + tensor) * ITEMS + k) * blockDim.x + threadIdx.x) * 16;
+  }
+  // Asks for a tensor's part of the row that the current stage will hold.
+  __device__ __forceinline__ void ask(int tensor, const void* p, long long at, int lane, int lanes, int most) const {
+    if constexpr (kRing) {
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const int c = (k * lanes + lane) * VEC;
-    if (c < most) v[k].load((const T*)p + at + c);
+      for (int k = 0; k < ITEMS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c < most)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place(tensor, k))),
+                       "l"((const T*)p + at + c)
+                       : "memory");
+      }
+    }
+  }
+  __device__ __forceinline__ void asked() {  // one row
+    if constexpr (kRing) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (++stage == kDepth) stage = 0;
+    }
+  }
+  // Waits for the row asked for kDepth rows ago, which lies in the current stage.
+  __device__ __forceinline__ void arrived() const {
+    if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+  }
+  __device__ __forceinline__ void take(Vec<T, VEC>& v, int tensor, int k, const void* p, long long at) const {
+    if constexpr (kRing) v.r = *reinterpret_cast<const uint4*>(place(tensor, k));
+    else v.load((const T*)p + at);
+  }
+};
+
+// The weight in shared memory, ones where there is none.
+template <int VEC>
+__device__ __forceinline__ void keep_weight(float* w, const float* weight, int C) {
+  for (int c = threadIdx.x; c < C; c += blockDim.x) w[c] = weight ? __ldg(weight + c) : 1.f;
+  __syncthreads();
+}
+template <int VEC>
+__device__ __forceinline__ void kept_weight(const float* w, int c, float (&v)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(w + c + i);
+      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = w[c + i];
   }
 }
 
-// The next row's loads are under way while this one is reduced and written.
 template <typename T, int VEC, int ITEMS, bool Q8>
-__global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  typedef Pieces<T, VEC, ITEMS, 2> P;
+  P in = {raw, 0};
+  float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const float over = 1.f / d.C;
   const long long step = (long long)gridDim.x * per;
   long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
-  Vec<T, VEC> u[ITEMS], v[ITEMS];
-  load_row(u, a.x, row * d.x_stride, lane, lanes, row < d.M ? d.C : 0);
-  if (a.r) load_row(v, a.r, row * d.r_stride, lane, lanes, row < d.M ? d.C : 0);
+  auto ask = [&](long long at) {
+    const int most = at < d.M ? d.C : 0;
+    in.ask(0, a.x, at * d.x_stride, lane, lanes, most);
+    if (a.r) in.ask(1, a.r, at * d.r_stride, lane, lanes, most);
+    in.asked();
+  };
+  if constexpr (P::kRing) {
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) ask(row + i * step);
+  }
+  keep_weight<VEC>(w, a.weight, d.C);
   // every thread of the CTA takes as many turns
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
     const int most = row < d.M ? d.C : 0;
     float t[ITEMS][VEC], s = 0.f;
+    in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        u[k].widen(t[k]);
+        Vec<T, VEC> u;
+        in.take(u, 0, k, a.x, row * d.x_stride + c);
+        u.widen(t[k]);
         if (a.r) {
           float o[VEC];
-          v[k].widen(o);
+          in.take(u, 1, k, a.r, row * d.r_stride + c);
+          u.widen(o);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) t[k][i] += o[i];
           if (a.total) {
-            v[k].round(t[k]);
-            v[k].store((T*)a.total + row * d.C + c);
+            u.round(t[k]);
+            u.store((T*)a.total + row * d.C + c);
           }
         }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s = fmaf(t[k][i], t[k][i], s);
       }
     }
-    const long long next = row + step;
-    load_row(u, a.x, next * d.x_stride, lane, lanes, next < d.M ? d.C : 0);
-    if (a.r) load_row(v, a.r, next * d.r_stride, lane, lanes, next < d.M ? d.C : 0);
+    ask(row + kDepth * step);
     float rstd = 1.f, m = 0.f;
     if (norm) rstd = 1.f / sqrtf(over_row<false>(s, lanes) * over + d.eps);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        float w[VEC];
-        load_weight<VEC>(a.weight, c, w);
+        float f[VEC];
+        kept_weight<VEC>(w, c, f);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          t[k][i] = t[k][i] * rstd * w[i];
+          t[k][i] = t[k][i] * rstd * f[i];
           if constexpr (Q8) m = max_nan(m, fabsf(t[k][i]));
         }
         if constexpr (!Q8) {
@@ -175,7 +244,10 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 template <typename T, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kThreads, 2)
 rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part) {
-  extern __shared__ float sums[];  // [rows at a time][lanes * ITEMS * VEC], for dw
+  extern __shared__ __align__(16) unsigned char raw[];
+  typedef Pieces<T, VEC, ITEMS, 3> P;
+  P in = {raw, 0};
+  float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const long long step = (long long)gridDim.x * per;
   float dw[ITEMS][VEC];
@@ -185,57 +257,66 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     for (int i = 0; i < VEC; ++i) dw[k][i] = 0.f;
   const float over = 1.f / d.C;
   long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
-  Vec<T, VEC> u[ITEMS], v[ITEMS], e[ITEMS];
-  float scale = 0.f;
-  auto load = [&](long long at) {
+  auto ask = [&](long long at) {
     const int most = at < d.M ? d.C : 0;
-    if (most) scale = a.rstd[at];
-    load_row(u, a.x, at * d.x_stride, lane, lanes, most);
-    load_row(v, a.dy, at * d.d_stride, lane, lanes, most);
-    if (a.r) load_row(e, a.r, at * d.r_stride, lane, lanes, most);
+    in.ask(0, a.x, at * d.x_stride, lane, lanes, most);
+    in.ask(1, a.dy, at * d.d_stride, lane, lanes, most);
+    if (a.r) in.ask(2, a.r, at * d.r_stride, lane, lanes, most);
+    in.asked();
   };
-  load(row);
+  if constexpr (P::kRing) {
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) ask(row + i * step);
+  }
+  float next = row < d.M ? a.rstd[row] : 0.f;
+  keep_weight<VEC>(w, a.weight, d.C);
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
     const int most = row < d.M ? d.C : 0;
-    const float rstd = scale;
+    const float rstd = next;
+    if (row + step < d.M) next = a.rstd[row + step];
     float s = 0.f;
     float t[ITEMS][VEC], g[ITEMS][VEC];
-    Vec<T, VEC> o[ITEMS];
+    in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        float w[VEC];
-        load_weight<VEC>(a.weight, c, w);
-        u[k].widen(t[k]);
-        v[k].widen(g[k]);
-        o[k] = e[k];
+        Vec<T, VEC> u;
+        in.take(u, 0, k, a.x, row * d.x_stride + c);
+        u.widen(t[k]);
+        in.take(u, 1, k, a.dy, row * d.d_stride + c);
+        u.widen(g[k]);
+        float f[VEC];
+        kept_weight<VEC>(w, c, f);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           t[k][i] *= rstd;  // xhat
           dw[k][i] = fmaf(g[k][i], t[k][i], dw[k][i]);
-          g[k][i] *= w[i];
+          g[k][i] *= f[i];
           s = fmaf(g[k][i], t[k][i], s);
         }
       }
     }
-    load(row + step);
     s = -over_row<false>(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        float more[VEC];
-        if (a.r) o[k].widen(more);
+        Vec<T, VEC> o;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
-          if (a.r) g[k][i] += more[i];
+        for (int i = 0; i < VEC; ++i) g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
+        if (a.r) {
+          float more[VEC];
+          in.take(o, 2, k, a.r, row * d.r_stride + c);
+          o.widen(more);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) g[k][i] += more[i];
         }
-        o[k].round(g[k]);
-        o[k].store((T*)a.y + row * d.C + c);
+        o.round(g[k]);
+        o.store((T*)a.y + row * d.C + c);
       }
     }
+    ask(row + kDepth * step);
   }
   if (!a.dweight) return;
   float* out = part + (long long)blockIdx.x * d.C;
@@ -250,6 +331,9 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     return;
   }
   const int width = lanes * ITEMS * VEC;
+  float* sums = reinterpret_cast<float*>(raw);  // [rows at a time][width], where the ring was
+  if constexpr (P::kRing) asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
@@ -435,19 +519,25 @@ inline int grid_of(const void* f, long long M, const Shape& s, int smem) {
 
 template <typename T, int VEC, int ITEMS>
 cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, const Shape& s, cudaStream_t st) {
-  if (op == RMS_FWD) {
-    const int grid = grid_of((const void*)rows_forward<T, VEC, ITEMS, false>, d.M, s, 0);
-    rows_forward<T, VEC, ITEMS, false><<<grid, s.threads, 0, st>>>(d, a, s.lanes, 1);
-  } else {
-    const int grid = grid_of((const void*)rows_forward<T, VEC, ITEMS, true>, d.M, s, 0);
-    rows_forward<T, VEC, ITEMS, true><<<grid, s.threads, 0, st>>>(d, a, s.lanes, op == RMS_Q8);
-  }
-  return cudaGetLastError();
+  const int smem = s.threads * Pieces<T, VEC, ITEMS, 2>::kBytes + d.C * 4;
+  auto launch = [&](auto* f, int norm) {
+    const cudaError_t e = wt::ensure_smem((const void*)f, smem);
+    if (e != cudaSuccess) return e;
+    f<<<grid_of((const void*)f, d.M, s, smem), s.threads, smem, st>>>(d, a, s.lanes, norm);
+    return cudaGetLastError();
+  };
+  if (op == RMS_FWD) return launch(rows_forward<T, VEC, ITEMS, false>, 1);
+  return launch(rows_forward<T, VEC, ITEMS, true>, op == RMS_Q8);
 }
 template <typename T, int VEC, int ITEMS>
 cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Shape& s, float* part, cudaStream_t st) {
-  const int smem = a.dweight && s.threads > s.lanes ? s.threads * ITEMS * VEC * 4 : 0;
-  int grid = grid_of((const void*)rows_backward<T, VEC, ITEMS>, d.M, s, smem);
+  int smem = s.threads * Pieces<T, VEC, ITEMS, 3>::kBytes + d.C * 4;
+  const int sums = s.threads > s.lanes ? s.threads * ITEMS * VEC * 4 : 0;
+  if (sums > smem) smem = sums;
+  const void* f = (const void*)rows_backward<T, VEC, ITEMS>;
+  const cudaError_t e = wt::ensure_smem(f, smem);
+  if (e != cudaSuccess) return e;
+  int grid = grid_of(f, d.M, s, smem);
   if (grid > parts_most(d)) grid = parts_most(d);
   rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part);
   if (a.dweight) add_parts<<<(d.C + 31) / 32, 256, 0, st>>>(part, grid, d.C, a.dweight);

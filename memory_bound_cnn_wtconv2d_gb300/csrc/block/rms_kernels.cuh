@@ -41,22 +41,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Sum or maximum over a row's lanes: part of a warp, or the CTA.
+// Sum of s, and where MAX the maximum of m, over a row's lanes: part of a warp, or
+// the CTA.
 template <bool MAX>
-__device__ __forceinline__ float over_row(float v, int lanes) {
-  __shared__ float part[2][kMostLanes / 32];
+__device__ __forceinline__ void over_row(float& s, float& m, int lanes) {
+  __shared__ float2 part[kMostLanes / 32];
   for (int o = min(lanes, 32) / 2; o; o >>= 1) {
-    const float u = __shfl_xor_sync(~0u, v, o);
-    v = MAX ? max_nan(v, u) : v + u;
+    s += __shfl_xor_sync(~0u, s, o);
+    if (MAX) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
   }
   if (lanes > 32) {
-    __syncthreads();  // the last row's sums have been read
-    if ((threadIdx.x & 31) == 0) part[MAX][threadIdx.x / 32] = v;
+    __syncthreads();  // the last row's have been read
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = make_float2(s, m);
     __syncthreads();
-    v = part[MAX][0];
-    for (int i = 1; i < lanes / 32; ++i) v = MAX ? max_nan(v, part[MAX][i]) : v + part[MAX][i];
+    s = part[0].x, m = part[0].y;
+    for (int i = 1; i < lanes / 32; ++i) {
+      s += part[i].x;
+      if (MAX) m = max_nan(m, part[i].y);
+    }
   }
-  return v;
+}
+__device__ __forceinline__ float over_row(float s, int lanes) {
+  float m = 0.f;
+  over_row<false>(s, m, lanes);
+  return s;
 }
 
 template <int VEC>
@@ -179,7 +187,7 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
   // every thread of the CTA takes as many turns
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
     const int most = row < d.M ? d.C : 0;
-    float t[ITEMS][VEC], s = 0.f;
+    float t[ITEMS][VEC], s = 0.f, m = 0.f;
     in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -199,41 +207,49 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
             u.store((T*)a.total + row * d.C + c);
           }
         }
+        if constexpr (Q8) {
+          float f[VEC];
+          kept_weight<VEC>(w, c, f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s = fmaf(t[k][i], t[k][i], s);
+          for (int i = 0; i < VEC; ++i) {
+            s = fmaf(t[k][i], t[k][i], s);
+            t[k][i] *= f[i];
+            m = max_nan(m, fabsf(t[k][i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s = fmaf(t[k][i], t[k][i], s);
+        }
       }
     }
     ask(row + kDepth * step);
-    float rstd = 1.f, m = 0.f;
-    if (norm) rstd = 1.f / sqrtf(over_row<false>(s, lanes) * over + d.eps);
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) {
-        float f[VEC];
-        kept_weight<VEC>(w, c, f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          t[k][i] = t[k][i] * rstd * f[i];
-          if constexpr (Q8) m = max_nan(m, fabsf(t[k][i]));
-        }
-        if constexpr (!Q8) {
-          Vec<T, VEC> o;
-          o.round(t[k]);
-          o.store((T*)a.y + row * d.C + c);
-        }
-      }
-    }
+    // 8 bits: the largest |y| is rstd times the largest |t w|, so one exchange does
+    over_row<Q8>(s, m, lanes);
+    const float rstd = norm ? 1.f / sqrtf(s * over + d.eps) : 1.f;
     if constexpr (Q8) {
-      m = max_nan(over_row<true>(m, lanes), kLeastScale * kE4m3Most);
-      const float inv = kE4m3Most / m;
+      m = max_nan(m * rstd, kLeastScale * kE4m3Most);
+      const float f = kE4m3Most / m;
 #pragma unroll
       for (int k = 0; k < ITEMS; ++k) {
         const int c = (k * lanes + lane) * VEC;
         if (c < most) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) t[k][i] *= inv;
+          for (int i = 0; i < VEC; ++i) t[k][i] = t[k][i] * rstd * f;
           store_e4m3<VEC>(a.q + row * d.C + c, t[k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c < most) {
+          float f[VEC];
+          kept_weight<VEC>(w, c, f);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) t[k][i] = t[k][i] * rstd * f[i];
+          Vec<T, VEC> o;
+          o.round(t[k]);
+          o.store((T*)a.y + row * d.C + c);
         }
       }
     }
@@ -297,7 +313,7 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
         }
       }
     }
-    s = -over_row<false>(s, lanes) * over;
+    s = -over_row(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
@@ -397,7 +413,7 @@ long_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s = fmaf(t[i], t[i], s);
       }
-      rstd = 1.f / sqrtf(over_row<false>(s, kThreads) / d.C + d.eps);
+      rstd = 1.f / sqrtf(over_row(s, kThreads) / d.C + d.eps);
     }
     float m = 0.f, inv = 0.f;
     if constexpr (Q8) {
@@ -407,7 +423,9 @@ long_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < VEC; ++i) m = max_nan(m, fabsf(t[i] * rstd * w[i]));
       }
-      m = max_nan(over_row<true>(m, kThreads), kLeastScale * kE4m3Most);
+      float none = 0.f;
+      over_row<true>(none, m, kThreads);
+      m = max_nan(m, kLeastScale * kE4m3Most);
       inv = kE4m3Most / m;
     }
     for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
@@ -448,7 +466,7 @@ long_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s = fmaf(g[i] * w[i], t[i] * rstd, s);
     }
-    s = -over_row<false>(s, kThreads) / d.C;
+    s = -over_row(s, kThreads) / d.C;
     for (int c = threadIdx.x * VEC; c < d.C; c += kThreads * VEC) {
       u.load(x + c);
       u.widen(t);

@@ -96,33 +96,41 @@ __device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VE
 
 // ---- rows that stay in registers ------------------------------------------------
 
-// Pieces of rows on their way.  Accesses of 16 bytes are copied asynchronously into
-// a ring of kDepth rows in shared memory, each lane's into places of its own, so
-// that no barrier is needed and the copies take no registers; narrower ones are
-// loaded when the row's turn comes.  (Next rows in registers, one deep, were no
-// faster than none: 200704 x 192 bf16 backward 93 us.)
-constexpr int kDepth = 3;
-
+// Pieces of rows on their way.  They are copied asynchronously into a ring of kDepth
+// rows in shared memory, each lane's into places of its own, so that no barrier is
+// needed and the copies take no registers.  (Next rows in registers, one deep,
+// were no faster than none: 200704 x 192 bf16 backward 93 us, in the ring 56.)
+// Single 16-bit values are too small for such copies and do go through registers.
 template <typename T, int VEC, int ITEMS, int TENSORS>
 struct Pieces {
-  static constexpr bool kRing = VEC * sizeof(T) == 16;
-  static constexpr int kBytes = kRing ? kDepth * TENSORS * ITEMS * 16 : 0;  // of a thread
+  static constexpr int kSize = VEC * (int)sizeof(T);
+  static constexpr bool kRing = kSize >= 4;
+  static constexpr int kDepth = kRing ? 3 : 1;
+  static constexpr int kBytes = kRing ? kDepth * TENSORS * ITEMS * kSize : 0;  // of a thread
   unsigned char* base;
   int stage;
+  Vec<T, VEC> held[kRing ? 1 : TENSORS][kRing ? 1 : ITEMS];
 
+  __device__ __forceinline__ explicit Pieces(unsigned char* p) : base(p), stage(0) {}
   __device__ __forceinline__ unsigned char* place(int tensor, int k) const {
-    return base + (((stage * TENSORS + tensor) * ITEMS + k) * blockDim.x + threadIdx.x) * 16;
+    return base + (((stage * TENSORS + tensor) * ITEMS + k) * blockDim.x + threadIdx.x) * kSize;
   }
   // Asks for a tensor's part of the row that the current stage will hold.
-  __device__ __forceinline__ void ask(int tensor, const void* p, long long at, int lane, int lanes, int most) const {
-    if constexpr (kRing) {
+  __device__ __forceinline__ void ask(int tensor, const void* p, long long at, int lane, int lanes, int most) {
 #pragma unroll
-      for (int k = 0; k < ITEMS; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-        if (c < most)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place(tensor, k))),
-                       "l"((const T*)p + at + c)
-                       : "memory");
+    for (int k = 0; k < ITEMS; ++k) {
+      const int c = (k * lanes + lane) * VEC;
+      if (c >= most) continue;
+      const T* from = (const T*)p + at + c;
+      if constexpr (kSize == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place(tensor, k))), "l"(from)
+                     : "memory");
+      } else if constexpr (kRing) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(place(tensor, k))), "l"(from),
+                     "n"(kSize)
+                     : "memory");
+      } else {
+        held[tensor][k].load(from);
       }
     }
   }
@@ -136,9 +144,9 @@ struct Pieces {
   __device__ __forceinline__ void arrived() const {
     if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
   }
-  __device__ __forceinline__ void take(Vec<T, VEC>& v, int tensor, int k, const void* p, long long at) const {
-    if constexpr (kRing) v.r = *reinterpret_cast<const uint4*>(place(tensor, k));
-    else v.load((const T*)p + at);
+  __device__ __forceinline__ void take(Vec<T, VEC>& v, int tensor, int k) const {
+    if constexpr (kRing) v.load(reinterpret_cast<const T*>(place(tensor, k)));
+    else v = held[tensor][k];
   }
 };
 
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
   extern __shared__ __align__(16) unsigned char raw[];
   typedef Pieces<T, VEC, ITEMS, 2> P;
-  P in = {raw, 0};
+  P in(raw);
   float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const float over = 1.f / d.C;
@@ -179,10 +187,8 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
     if (a.r) in.ask(1, a.r, at * d.r_stride, lane, lanes, most);
     in.asked();
   };
-  if constexpr (P::kRing) {
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) ask(row + i * step);
-  }
+  for (int i = 0; i < P::kDepth; ++i) ask(row + i * step);
   keep_weight<VEC>(w, a.weight, d.C);
   // every thread of the CTA takes as many turns
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
@@ -194,11 +200,11 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
         Vec<T, VEC> u;
-        in.take(u, 0, k, a.x, row * d.x_stride + c);
+        in.take(u, 0, k);
         u.widen(t[k]);
         if (a.r) {
           float o[VEC];
-          in.take(u, 1, k, a.r, row * d.r_stride + c);
+          in.take(u, 1, k);
           u.widen(o);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) t[k][i] += o[i];
@@ -222,7 +228,7 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
         }
       }
     }
-    ask(row + kDepth * step);
+    ask(row + P::kDepth * step);
     // 8 bits: the largest |y| is rstd times the largest |t w|, so one exchange does
     over_row<Q8>(s, m, lanes);
     const float rstd = norm ? 1.f / sqrtf(s * over + d.eps) : 1.f;
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part) {
   extern __shared__ __align__(16) unsigned char raw[];
   typedef Pieces<T, VEC, ITEMS, 3> P;
-  P in = {raw, 0};
+  P in(raw);
   float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const long long step = (long long)gridDim.x * per;
@@ -280,10 +286,8 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     if (a.r) in.ask(2, a.r, at * d.r_stride, lane, lanes, most);
     in.asked();
   };
-  if constexpr (P::kRing) {
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) ask(row + i * step);
-  }
+  for (int i = 0; i < P::kDepth; ++i) ask(row + i * step);
   float next = row < d.M ? a.rstd[row] : 0.f;
   keep_weight<VEC>(w, a.weight, d.C);
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
@@ -292,16 +296,18 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     if (row + step < d.M) next = a.rstd[row + step];
     float s = 0.f;
     float t[ITEMS][VEC], g[ITEMS][VEC];
+    Vec<T, VEC> o[ITEMS];
     in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
         Vec<T, VEC> u;
-        in.take(u, 0, k, a.x, row * d.x_stride + c);
+        in.take(u, 0, k);
         u.widen(t[k]);
-        in.take(u, 1, k, a.dy, row * d.d_stride + c);
+        in.take(u, 1, k);
         u.widen(g[k]);
+        if (a.r) in.take(o[k], 2, k);
         float f[VEC];
         kept_weight<VEC>(w, c, f);
 #pragma unroll
@@ -313,27 +319,26 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
         }
       }
     }
+    ask(row + P::kDepth * step);
     s = -over_row(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
       const int c = (k * lanes + lane) * VEC;
       if (c < most) {
-        Vec<T, VEC> o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
         if (a.r) {
           float more[VEC];
-          in.take(o, 2, k, a.r, row * d.r_stride + c);
-          o.widen(more);
+          o[k].widen(more);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) g[k][i] += more[i];
         }
-        o.round(g[k]);
-        o.store((T*)a.y + row * d.C + c);
+        o[k].round(g[k]);
+        o[k].store((T*)a.y + row * d.C + c);
       }
     }
-    ask(row + kDepth * step);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.dweight) return;
   float* out = part + (long long)blockIdx.x * d.C;
   if (per == 1) {
@@ -362,26 +367,26 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
   }
 }
 
-// dw from the CTAs' parts: 32 columns a CTA, eight ranges of parts side by side.
-static __global__ void __launch_bounds__(256) add_parts(const float* part, int n, int C, float* out) {
-  __shared__ float sh[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x / 32;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+// dw from the CTAs' parts: 32 columns a CTA, 32 ranges of parts side by side, eight
+// loads of each under way.  It may begin while the parts are made.
+static __global__ void __launch_bounds__(1024) add_parts(const float* part, int n, int C, float* out) {
+  __shared__ float sh[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int x = threadIdx.x & 31, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
+  float s[8] = {};
   if (c < C) {
-    const int each = (n + 7) / 8, end = min(n, (y + 1) * each);
-    int i = y * each;
-    for (; i + 4 <= end; i += 4)
+    const int each = (n + 31) / 32, end = min(n, (y + 1) * each);
+    for (int i = y * each; i < end; i += 8)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] += __ldcg(part + (long long)(i + j) * C + c);
-    for (; i < end; ++i) s[0] += __ldcg(part + (long long)i * C + c);
+      for (int j = 0; j < 8; ++j)
+        if (i + j < end) s[j] += __ldcg(part + (long long)(i + j) * C + c);
   }
-  sh[y][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
+  sh[y][x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
-  if (y == 0 && c < C) {
-    float v = 0.f;
-    for (int i = 0; i < 8; ++i) v += sh[i][threadIdx.x];
-    out[c] = v;
-  }
+  // column y's ranges are now side by side in warp y
+  float v = sh[x][y];
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  if (x == 0 && blockIdx.x * 32 + y < C) out[blockIdx.x * 32 + y] = v;
 }
 
 // ---- rows that are read again ---------------------------------------------------
@@ -535,6 +540,19 @@ inline int grid_of(const void* f, long long M, const Shape& s, int smem) {
   return (int)(n < most ? n : most);
 }
 
+inline cudaError_t launch_add(const float* part, int n, int C, float* out, cudaStream_t s) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((C + 31) / 32);
+  c.blockDim = dim3(1024);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, add_parts, part, n, C, out);
+}
+
 template <typename T, int VEC, int ITEMS>
 cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, const Shape& s, cudaStream_t st) {
   const int smem = s.threads * Pieces<T, VEC, ITEMS, 2>::kBytes + d.C * 4;
@@ -558,8 +576,8 @@ cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Sh
   int grid = grid_of(f, d.M, s, smem);
   if (grid > parts_most(d)) grid = parts_most(d);
   rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part);
-  if (a.dweight) add_parts<<<(d.C + 31) / 32, 256, 0, st>>>(part, grid, d.C, a.dweight);
-  return cudaGetLastError();
+  if (!a.dweight) return cudaGetLastError();
+  return launch_add(part, grid, d.C, a.dweight, st);
 }
 
 template <typename T, int VEC>
@@ -598,7 +616,7 @@ cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* pa
   if (a.dweight) {
     const int n = parts_most(d);
     long_dweight<T><<<dim3((d.C + kThreads - 1) / kThreads, n), kThreads, 0, st>>>(d, a, part, (d.M + n - 1) / n);
-    add_parts<<<(d.C + 31) / 32, 256, 0, st>>>(part, n, d.C, a.dweight);
+    return launch_add(part, n, d.C, a.dweight, st);
   }
   return cudaGetLastError();
 }

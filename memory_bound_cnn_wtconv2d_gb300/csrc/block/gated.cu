@@ -164,7 +164,7 @@ Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products,
   Tiles best = {};
   double least = 0;
   for (int pair = 0; pair < 2; ++pair)
-    for (int n = pair ? 128 : 64; n <= (pair ? 512 : 256); n += pair ? 128 : 64) {
+    for (int n = pair ? 128 : 64; n <= (pair && products == 1 ? 512 : 256); n += pair ? 128 : 64) {
       const int tn = (N + n - 1) / n;
       if (best.n && best.pair == pair && n - (pair ? 128 : 64) >= N) break;
       for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
@@ -314,7 +314,12 @@ void set_tiles(GemmArgs& a, const Call& c, const Tiles& t, int tiles_m, bool a_a
   a.group = t.resident ? 1 : 16;  // resident: a CTA's tiles have the same columns
   a.buffers = t.n > 256 ? 1 : t.n > 128 ? 2 : t.n > 64 ? 4 : 8;
   a.acc_columns = kColumns / a.buffers;
-  a.groups = a.buffers < 4 ? a.buffers : 4;
+  // float32 results: sums of eight k blocks at a time leave TMEM, since the tensor
+  // core's additions truncate (1000 x 3000 -> 512 forward: error 6.4e-6 in one
+  // sum, 0.9e-6 in segments; plain float32 sums 1.5e-6); all warps share a tile
+  const bool keep = c.d.dtype == WTCONV_F32;
+  a.segment = keep ? 8 : 1 << 30;
+  a.groups = keep ? 1 : a.buffers < 4 ? a.buffers : 4;
   a.by_split = divisor(a.tiles_m * a.tiles_n);
   a.by_group = divisor(a.group * a.tiles_n);
   a.by_rows = divisor(a.group);

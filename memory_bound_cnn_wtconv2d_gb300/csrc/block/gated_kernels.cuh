@@ -80,6 +80,7 @@ struct GemmArgs {
   int total, kblocks, khalf;  // k blocks: all, of a split (at most), DX: of one matrix
   int k;                  // valid k: C, H (of each half), M
   int parts;              // 1, or 3 for float32
+  int segment;            // k blocks that are added up in TMEM before a float32 epilogue takes them
   int stages;
   uint32_t idesc, idesc2; // of the first 256 columns and of those beyond
   uint32_t b_bytes;       // of a k block of B, for one CTA
@@ -213,9 +214,10 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
       if (t.m >= tiles) row -= tiles * a.rows, second = 1;
     }
     const int column = EPI == EPI_H || EPI == EPI_P ? t.n * a.half : t.n * a.n;
-    for (int q = 0; ok && q < products; ++q) {
-      const int pa = products == 1 ? 0 : part_a(q), pb = products == 1 ? 0 : part_b(q);
-      for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
+    const int end = blocks.x + blocks.y, turns = products * ((blocks.y + a.segment - 1) / a.segment);
+    for (int turn = 0, q = 0, from = blocks.x; ok && turn < turns; ++turn) {
+      const int pa = products == 1 ? 0 : part_a(q), pb = products == 1 ? 0 : part_b(q), to_kb = min(end, from + a.segment);
+      for (int kb = from; kb < to_kb; ++kb) {
         ok = wait(sh, a, &sh.empty[stage], phase);
         if (!ok) break;
         const uint32_t full = there + stage * 8, to = first + stage * bytes, tb = to + kABytes;
@@ -237,7 +239,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
         } else {
           const bool up = EPI == EPI_DX && kb >= a.khalf;
           const int k = (up ? kb - a.khalf : kb) * 64;
-          const void* from = up ? &a.b1 : &a.b0;
+          const void* map = up ? &a.b1 : &a.b0;
           if (elect_one()) {
             if (!PAIR || w.rank == 0) mbar_expect(own + stage * 8, expect);
             if constexpr (EPI == EPI_DX) {
@@ -250,7 +252,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
             uint32_t b = tb;
             for (int j = 0; j < a.n; j += kMostN) {
               const int some = min(kMostN, a.n - j) / (PAIR ? 2 : 1);
-              for (int c = 0; c < some; c += 64, b += 8192) load<PAIR>(b, from, column + j + w.rank * some + c, 0, k, pb, full);
+              for (int c = 0; c < some; c += 64, b += 8192) load<PAIR>(b, map, column + j + w.rank * some + c, 0, k, pb, full);
             }
           }
         }
@@ -258,6 +260,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
         ++issued;
         if (++stage == (uint32_t)a.stages) stage = 0, phase ^= 1;
       }
+      if (++q == products) q = 0, from = to_kb;
     }
   }
   if (w.rank == 0) {
@@ -287,46 +290,50 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
   if (a.resident && w.first < items) ok = wait(sh, a, &sh.b_full, 0);
   for (int i = w.first; ok && i < items; i += w.step) {
     const int2 blocks = a.splits == 1 ? make_int2(0, a.total) : blocks_of(a, divide(i, a.by_split));
-    ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
-    if (!ok) break;
-    tc_fence_after();
-    const uint32_t d = tmem + acc * a.acc_columns;
-    uint32_t accumulate = 0;
-    for (int q = 0; ok && q < products; ++q)
-      for (int kb = blocks.x; kb < blocks.x + blocks.y; ++kb) {
-        const int left = a.k - (EPI == EPI_DX && kb >= a.khalf ? kb - a.khalf : kb) * kBlock;
-        const uint32_t from = first + stage * bytes, empty = smem_addr(&sh.empty[stage]);
-        const uint32_t la = desc_low(from, kAlongA), lb = desc_low(a.resident ? ring + kb * a.b_bytes : from + kABytes, kAlongB);
-        ok = wait(sh, a, &sh.full[stage], phase);
-        if (!ok) break;
-        tc_fence_after();
-        if (left >= kBlock && !wide) {
-          if (elect_one()) {
-            mma_step<PAIR, Q8>(d, la, lb, kDescHigh, a.idesc, accumulate);
+    const int end = blocks.x + blocks.y;
+    for (int from_kb = blocks.x; ok && from_kb < end; from_kb += a.segment) {
+      const int to_kb = min(end, from_kb + a.segment);
+      ok = wait(sh, a, &sh.acc_empty[acc], acc_phase);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * a.acc_columns;
+      uint32_t accumulate = 0;
+      for (int q = 0; ok && q < products; ++q)
+        for (int kb = from_kb; kb < to_kb; ++kb) {
+          const int left = a.k - (EPI == EPI_DX && kb >= a.khalf ? kb - a.khalf : kb) * kBlock;
+          const uint32_t from = first + stage * bytes, empty = smem_addr(&sh.empty[stage]);
+          const uint32_t la = desc_low(from, kAlongA), lb = desc_low(a.resident ? ring + kb * a.b_bytes : from + kABytes, kAlongB);
+          ok = wait(sh, a, &sh.full[stage], phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (left >= kBlock && !wide) {
+            if (elect_one()) {
+              mma_step<PAIR, Q8>(d, la, lb, kDescHigh, a.idesc, accumulate);
 #pragma unroll
-            for (int s = 1; s < kBlock / kStep; ++s)
-              mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, 1);
-            commit(empty);
-          }
-        } else {
-          const int steps = min(kBlock / kStep, (left + kStep - 1) / kStep);
-          if (elect_one()) {
-            for (int s = 0; s < steps; ++s) {
-              mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, accumulate | s);
-              if (wide)  // what lies beyond the first 256 columns
-                mma_step<PAIR, Q8>(d + kMostN, la + s * kStepA, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * kStepB, kDescHigh,
-                                   a.idesc2, accumulate | s);
+              for (int s = 1; s < kBlock / kStep; ++s)
+                mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, 1);
+              commit(empty);
             }
-            commit(empty);
+          } else {
+            const int steps = min(kBlock / kStep, (left + kStep - 1) / kStep);
+            if (elect_one()) {
+              for (int s = 0; s < steps; ++s) {
+                mma_step<PAIR, Q8>(d, la + s * kStepA, lb + s * kStepB, kDescHigh, a.idesc, accumulate | s);
+                if (wide)  // what lies beyond the first 256 columns
+                  mma_step<PAIR, Q8>(d + kMostN, la + s * kStepA, lb + (PAIR ? 16384 >> 4 : 32768 >> 4) + s * kStepB, kDescHigh,
+                                     a.idesc2, accumulate | s);
+              }
+              commit(empty);
+            }
           }
+          accumulate = 1;
+          __syncwarp();
+          if (++stage == (uint32_t)a.stages) stage = 0, phase ^= 1;
         }
-        accumulate = 1;
-        __syncwarp();
-        if (++stage == (uint32_t)a.stages) stage = 0, phase ^= 1;
-      }
-    if (ok && elect_one()) commit(smem_addr(&sh.acc_full[acc]));
-    __syncwarp();
-    if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
+      if (ok && elect_one()) commit(smem_addr(&sh.acc_full[acc]));
+      __syncwarp();
+      if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
+    }
   }
   if (elect_one()) {
     commit(smem_addr(&sh.drain));
@@ -490,7 +497,7 @@ template <int EPI, typename T, bool Q8, bool PAIR>
 __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned char* staging, uint32_t tmem, const Worker& w, int items) {
   constexpr int kCols = 64 / sizeof(T);
   const int warp = threadIdx.x / 32 - 2, lane = threadIdx.x & 31;
-  constexpr bool kSums = EPI == EPI_DX || EPI == EPI_DW;
+  constexpr bool kSums = EPI == EPI_DX || EPI == EPI_DW, kKeep = sizeof(T) == 4;
   const int width = kSums ? a.n : a.half;
   const int quadrant = (warp + 2) & 3, sides = 4 / a.groups, side = (warp / 4) & (sides - 1), group = warp / 4 / sides;
   const int first = w.first + group * w.step, step = a.groups * w.step;
@@ -534,57 +541,102 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
   fetch();
 
   uint32_t acc = group, phase = 0;
+  // as soon as this warp has read all of its part
+  auto release = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bar = smem_addr(&sh.acc_empty[acc]);
+      if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
+      else mbar_arrive(bar);
+    }
+    acc += a.groups;
+    if (acc >= (uint32_t)a.buffers) acc -= a.buffers, phase ^= 1;
+  };
   for (int i = first; i < items; i += step) {
     const Item t = item_of(a, i);
     const int m0 = t.m * a.rows + warp_row, rows = min(32, a.M - m0);  // none or fewer where the tile ends
-    got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
-    tc_fence_after();
-    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * a.acc_columns;
-    // as soon as this warp has read all of its part
-    bool held = true;
-    auto release = [&]() {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t bar = smem_addr(&sh.acc_empty[acc]);
-        if constexpr (PAIR) mbar_arrive_cluster(at_rank(bar, 0));
-        else mbar_arrive(bar);
+    // float32: the sums of the segments, added up here
+    float kept[kKeep ? 4 : 1][16];
+    if constexpr (kKeep) {
+      const int blocks = blocks_of(a, t.split).y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) kept[j][e] = 0.f;
+      for (int at = 0; at < blocks; at += a.segment) {
+        got = got && wait(sh, a, &sh.acc_full[acc], phase);  // after one that gave up the phases mean nothing
+        tc_fence_after();
+        const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * a.acc_columns;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // of gate and up in turn, or four stretches of sums
+          const int c = side * 16 + 64 * (kSums ? j : j / 2);
+          if (c < width) {
+            float v[16];
+            tmem_take(from + c + (kSums || j % 2 == 0 ? 0 : a.half), v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) kept[j][e] += v[e];
+          }
+        }
+        release();
       }
-      held = false;
-    };
+      if (!got) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) no_result(kept[j]);
+      }
+    } else {
+      got = got && wait(sh, a, &sh.acc_full[acc], phase);
+      tc_fence_after();
+    }
+    const uint32_t from = tmem + ((uint32_t)(quadrant * 32) << 16) + acc * a.acc_columns;
+    bool held = !kKeep;
     if constexpr (kSums) {
       const int tiles = a.tiles_m / 2;
       const bool second = EPI == EPI_DW && t.m >= tiles;  // rows are hidden units, of up
       const int m = second ? m0 - tiles * a.rows : m0, left = EPI == EPI_DW ? min(32, a.H - m) : rows;
       const int n0 = t.n * a.n;
-      auto sums = [&](auto zero, int c, auto store) {  // a stretch of TO
-        typedef decltype(zero) TO;
-        float v[64 / sizeof(TO)];
-        tmem_take(from + c, v);
-        if (!got) no_result(v);
+      auto stretch = [&](auto& v, int c) {  // of 64 bytes
+        typedef typename std::conditional<sizeof(v) == 64, float, T>::type TO;
         unsigned char* buf = st.next();
         put_row<TO>(buf, v);
-        store(buf);
+        if (sizeof(TO) == 4 && a.partial) {  // rows and columns are padded to whole tiles
+          send<float>(buf, &a.o0, n0 + c, 0, t.split * a.partial_rows + m0, 0);
+        } else if (a.boxes & 1) {
+          if (left > 0) send<TO>(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0);
+        } else {
+          __syncwarp();
+          copy_out<TO, false>(buf, (TO*)(second ? a.out2 : a.out) + (long long)m * a.ld + n0 + c, a.ld, left,
+                              min(64 / (int)sizeof(TO), a.N - n0 - c));
+          __syncwarp();
+        }
       };
-      if (a.partial) {  // rows and columns are padded to whole tiles
-        for (int c = side * 16; c < width && n0 + c < a.N; c += sides * 16)
-          sums(0.f, c, [&](unsigned char* buf) { send<float>(buf, &a.o0, n0 + c, 0, t.split * a.partial_rows + m0, 0); });
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = side * 16 + 64 * j;
+          if (c < width && n0 + c < a.N) stretch(kept[j], c);
+        }
+      } else if (a.partial) {
+        for (int c = side * 16; c < width && n0 + c < a.N; c += sides * 16) {
+          float v[16];
+          tmem_take(from + c, v);
+          if (!got) no_result(v);
+          stretch(v, c);
+        }
       } else {
-        for (int c = side * kCols; c < width && n0 + c < a.N; c += sides * kCols)
-          sums(T(), c, [&](unsigned char* buf) {
-            if (a.boxes & 1) {
-              if (left > 0) send<T>(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0);
-            } else {
-              __syncwarp();
-              copy_out<T, false>(buf, (T*)(second ? a.out2 : a.out) + (long long)m * a.ld + n0 + c, a.ld, left, min(kCols, a.N - n0 - c));
-              __syncwarp();
-            }
-          });
+        for (int c = side * kCols; c < width && n0 + c < a.N; c += sides * kCols) {
+          float v[kCols];
+          tmem_take(from + c, v);
+          if (!got) no_result(v);
+          stretch(v, c);
+        }
       }
     } else {
-      for (int c = side * kCols; c < width; c += sides * kCols) {
-        const int n0 = t.n * a.half + c, cols = min(kCols, a.H - n0);
-        if (cols <= 0) break;
+#pragma unroll(kKeep ? 2 : 1)
+      for (int j = 0; j < (kKeep ? 2 : 4); ++j) {
+        const int c = (side + j * sides) * kCols, n0 = t.n * a.half + c, cols = min(kCols, a.H - n0);
+        if (c >= width || cols <= 0) break;
         unsigned char* buf;
         if constexpr (EPI == EPI_P) {
           // the tiles of even and odd stretches' dh, and between them that of du
@@ -601,11 +653,19 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         for (int h = 0; h < kCols / 16; ++h) {
           constexpr int kHalf = 16 * sizeof(T) / 16;  // chunks
           if constexpr (EPI == EPI_P) get_row<T>(buf, dh, h * kHalf);
-          tmem_take2(from + c + h * 16, g, from + a.half + c + h * 16, u);
-          if (h + 1 == kCols / 16 && (c + sides * kCols >= width || n0 + sides * kCols >= a.H)) release();
-          if (!got) {
-            no_result(g);
-            no_result(u);
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[e] = kept[2 * j][e], u[e] = kept[2 * j + 1][e];
+          } else {
+            tmem_take2(from + c + h * 16, g, from + a.half + c + h * 16, u);
+            if (h + 1 == kCols / 16 && (c + sides * kCols >= width || n0 + sides * kCols >= a.H)) {
+              release();
+              held = false;
+            }
+            if (!got) {
+              no_result(g);
+              no_result(u);
+            }
           }
           if constexpr (Q8) {
             const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;
@@ -663,8 +723,6 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
       }
     }
     if (held) release();
-    acc += a.groups;
-    if (acc >= (uint32_t)a.buffers) acc -= a.buffers, phase ^= 1;
   }
   if (lane == 0) bulk_wait();
   if (EPI == EPI_P && !got) linger(a);  // dh that was asked for

@@ -153,7 +153,7 @@ wtconv_status_t wtconv_grad_norm(const wtconv_tensor_t* tensors, int count, floa
 /* The same norm, and every element times min(1, max_norm / (norm + eps)), in
  * place, rounded once; where that factor is 1 nothing is written.  A norm that
  * is infinite makes every finite element 0 and a NaN makes every element NaN,
- * as the factor says.  The tensors must not overlap. */
+ * as the factor says.  Tensors that overlap are refused. */
 wtconv_status_t wtconv_clip_grads(const wtconv_tensor_t* tensors, int count, float max_norm, float eps, float* norm,
                                   void* ws, size_t ws_bytes, void* stream);
 

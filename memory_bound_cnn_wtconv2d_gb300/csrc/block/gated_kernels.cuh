@@ -363,6 +363,7 @@ __device__ __forceinline__ void copy_out(unsigned char* buf, T* p, long long ld,
       if (i * 8 + (lane >> 2) < rows && q * kEach < cols)
         *reinterpret_cast<uint4*>(p) = *staged(buf, i * 8 + (lane >> 2), q);
   } else if (lane < cols) {
+#pragma unroll 8
     for (int row = 0; row < rows; ++row)
       p[row * ld + lane] = reinterpret_cast<const T*>(staged(buf, row, lane / kEach))[lane % kEach];
   }
@@ -372,6 +373,7 @@ __device__ __forceinline__ void copy_in(unsigned char* buf, const T* p, long lon
   constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   if (lane < cols)
+#pragma unroll 8
     for (int row = 0; row < rows; ++row)
       reinterpret_cast<T*>(staged(buf, row, lane / kEach))[lane % kEach] = p[row * ld + lane];
 }

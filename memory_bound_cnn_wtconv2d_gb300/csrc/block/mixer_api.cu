@@ -2,6 +2,10 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+#include <utility>
+#include <vector>
+
 #include "api_checks.h"
 #include "mixer_launch.h"
 
@@ -123,12 +127,28 @@ wtconv_status_t check_tensors(const wtconv_tensor_t* t, int count) {
   return WTCONV_OK;
 }
 
+// Tensors that a call writes share no memory.
+wtconv_status_t check_apart(const wtconv_tensor_t* t, int count) {
+  std::vector<std::pair<uintptr_t, int>> at;
+  at.reserve(count);
+  for (int i = 0; i < count; ++i)
+    if (t[i].numel) at.emplace_back((uintptr_t)t[i].data, i);
+  std::sort(at.begin(), at.end());
+  for (size_t i = 1; i < at.size(); ++i) {
+    const wtconv_tensor_t& before = t[at[i - 1].second];
+    if (at[i].first - at[i - 1].first < (uintptr_t)before.numel * esize(before.dtype))
+      return fail(WTCONV_ERR_INVALID_ARG, "tensors %d and %d overlap", at[i - 1].second, at[i].second);
+  }
+  return WTCONV_OK;
+}
+
 wtconv_status_t clip(const wtconv_tensor_t* t, int count, bool scale, float max_norm, float eps, float* norm, void* ws,
                      size_t ws_bytes, void* stream, const char* name) {
   try {
     TRY(check_tensors(t, count));
     if (scale && !(max_norm >= 0.f && isfinite(eps) && eps >= 0.f))
       return fail(WTCONV_ERR_INVALID_ARG, "max_norm and eps must not be negative, eps finite");
+    if (scale) TRY(check_apart(t, count));
     TRY(pointer(norm, "norm", 4));
     TRY(workspace(ws, ws_bytes, wtb::clip_workspace(count)));
     return cuda_status(wtb::clip_launch(t, count, scale, max_norm, eps, norm, ws, (cudaStream_t)stream), name);

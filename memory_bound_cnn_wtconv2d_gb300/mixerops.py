@@ -433,40 +433,40 @@ def _dense(t):
 
 
 def _list(tensors, name="tensors"):
-    """The tensors, and their entries for the library: three 64-bit words each."""
+    """The tensors, their entries for the library (three 64-bit words each), and their
+    device."""
     ts = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
     if not ts:
         raise ValueError(f"{name}: no tensors")
-    words, codes, device = [], _c.DTYPE_CODES, None
-    for t in ts:
-        if not (isinstance(t, torch.Tensor) and _c._on_cuda(t)) or t.layout is not torch.strided:
-            raise ValueError(f"{name} must be dense CUDA tensors")
-        code = codes.get(t.dtype)
-        if code is None:
-            raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name}: one device for all, got {device} and {t.device}")
-        if not (t.is_contiguous() or _dense(t)):
-            raise ValueError(f"{name}: the elements of a tensor must fill one stretch of memory, got strides {t.stride()}")
-        words += (t.data_ptr(), t.numel(), code)
-    return ts, words, (Tensor * len(ts)).from_buffer(array.array("q", words)), device
-
-
-def _apart(spans, name):
-    """Raises where two stretches of memory of one list overlap."""
-    spans.sort()
-    for (_, end), (start, _) in zip(spans, spans[1:]):
-        if start < end:
-            raise ValueError(f"{name}: the tensors overlap")
+    codes, words = _c.DTYPE_CODES, []
+    try:  # a list is as long as a model has parameters: few calls for each
+        device = ts[0].device
+        index = ts[0].get_device()
+        fine = index >= 0
+        for t in ts:
+            fine = fine and t.get_device() == index and (t.is_contiguous() or _dense(t))
+            words += (t.data_ptr(), t.numel(), codes[t.dtype])
+    except (AttributeError, KeyError, RuntimeError):  # sparse tensors have no address
+        fine = False
+    if not fine:
+        for t in ts:
+            if not (isinstance(t, torch.Tensor) and _c._on_cuda(t)) or t.layout is not torch.strided:
+                raise ValueError(f"{name} must be dense CUDA tensors")
+            if t.dtype not in codes:
+                raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+            if t.device != ts[0].device:
+                raise ValueError(f"{name}: one device for all, got {ts[0].device} and {t.device}")
+            if not _dense(t):
+                raise ValueError(f"{name}: the elements of a tensor must fill one stretch of memory, got strides {t.stride()}")
+        raise ValueError(f"{name} must be dense CUDA tensors")
+    return ts, (Tensor * len(ts)).from_buffer(array.array("q", words)), device
 
 
 def wtconv_grad_norm(tensors, norm=None, workspace=None, stream=None):
     """The root of the sum of squares of all elements of a list of tensors (of any
     of the three types, mixed if need be): a float32 tensor of no axes, on the
     GPU."""
-    ts, _, entries, device = _list(tensors)
+    ts, entries, device = _list(tensors)
     need = lib().wtconv_clip_workspace_size(len(ts))
     if norm is not None or workspace is not None:
         _check_out(norm, "norm", (), torch.float32, device)
@@ -485,10 +485,9 @@ def wtconv_grad_norm(tensors, norm=None, workspace=None, stream=None):
 def wtconv_clip_grads(tensors, max_norm, eps=1e-6, norm=None, workspace=None, stream=None):
     """Multiplies every tensor of a list in place by min(1, max_norm / (norm + eps)),
     with the norm of ``wtconv_grad_norm``, which it returns."""
-    ts, words, entries, device = _list(tensors)
+    ts, entries, device = _list(tensors)
     if not (max_norm >= 0 and math.isfinite(eps) and eps >= 0):
         raise ValueError("max_norm and eps must not be negative, eps finite")
-    _apart([(p, p + n * (2 if code else 4)) for p, n, code in zip(*[iter(words)] * 3) if n], "tensors")
     need = lib().wtconv_clip_workspace_size(len(ts))
     if norm is not None or workspace is not None:
         _check_out(norm, "norm", (), torch.float32, device)
@@ -500,6 +499,8 @@ def wtconv_clip_grads(tensors, max_norm, eps=1e-6, norm=None, workspace=None, st
         ws, n = _b._scratch(need, device, workspace)
         status = lib().wtconv_clip_grads(entries, len(ts), max_norm, eps, norm.data_ptr(), ws.data_ptr(), n,
                                          _b._stream_of(device))
+        if status == _c.WTCONV_ERR_INVALID_ARG:  # what is left of that: tensors that overlap
+            raise ValueError(_c.lib().wtconv_last_error().decode())
         if status:
             _c._check(status)
     _b._written(*ts)

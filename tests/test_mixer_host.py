@@ -139,6 +139,19 @@ def test_lists_refused(L):
         assert L.wtconv_clip_grads(entry(), 1, limit, eps, p, p, need, None) == INVALID
 
 
+def test_lists_that_overlap_refused(L):
+    p, need = P(FAKE), L.wtconv_clip_workspace_size(3)
+
+    def status(*spans):  # (start, bytes, type); norm = NULL is refused after the overlap
+        e = (mixerops.Tensor * len(spans))(*[mixerops.Tensor(a, n // (2 if t else 4), t) for a, n, t in spans])
+        s = L.wtconv_clip_grads(e, len(spans), 1.0, 0.0, None, p, need, None)
+        return s == INVALID and "overlap" in L.wtconv_last_error().decode()
+
+    assert status((4096, 64, 0), (8192, 64, 0), (4156, 8, 1)) and status((4096, 64, 0), (4096, 64, 0))
+    assert status((8192, 4, 0), (4096, 4098, 2)) and not status((4096, 64, 0), (4160, 64, 1), (4032, 64, 2))
+    assert not status((4096, 64, 0), (4096, 0, 0), (4100, 0, 1))
+
+
 def test_the_binding_knows_dense_tensors():
     t = torch.zeros(4, 6, 5)
     for d in (t, t.permute(2, 0, 1), t[1], t[:, :, :], t.view(-1)[7:19], torch.zeros(3, 1, 2).transpose(0, 1), torch.zeros(())):
@@ -158,6 +171,3 @@ def test_the_binding_refuses_before_the_device(monkeypatch):
             mixerops._row_stride(bad, "x")
     with pytest.raises(ValueError):
         mixerops._list([x, x[:, ::2]])
-    with pytest.raises(ValueError):
-        mixerops._apart([(0, 10), (20, 30), (9, 12)], "tensors")
-    mixerops._apart([(20, 30), (0, 10), (10, 20)], "tensors")

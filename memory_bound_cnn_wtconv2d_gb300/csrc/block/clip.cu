@@ -9,6 +9,7 @@
 // from the last one back: what the first one read last is still in the L2.
 #include "block_device.cuh"
 #include "mixer_launch.h"
+#include "tc_device.cuh"
 #include "../wtconv_launch.h"
 
 namespace wtb {
@@ -137,10 +138,6 @@ __device__ __forceinline__ void chunk_scale(T* p, int n, float f) {
     }
   }
 }
-
-// Lets the next launch begin, and waits for the one before.
-__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtas)

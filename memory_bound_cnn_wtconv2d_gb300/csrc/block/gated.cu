@@ -32,6 +32,7 @@ struct PackArgs {
 
 template <typename T>
 __global__ void __launch_bounds__(256) gated_pack(const __grid_constant__ PackArgs a) {
+  let_next_in();
   const PackOne& p = a.t[blockIdx.y];
   const int across = p.pitch / 8;
   const long long total = p.rows * across;
@@ -64,6 +65,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 gated_sum(const float* part, int splits, long long part_rows, long long ld, long long rows, int cols, long long second,
           long long second_at, T* out, T* out2) {
+  wait_previous();  // it may have begun early
   const int across = (cols + 3) / 4;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < rows * across; i += gridDim.x * 256ll) {
     const long long row = i / across;
@@ -270,8 +272,17 @@ int map_type() {
          : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
+// The attribute that lets a launch begin while the one before runs.
+cudaLaunchAttribute early_launch() {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return at;
+}
+
 template <int EPI, typename T, bool Q8, bool PAIR>
-cudaError_t launch_gemm(GemmArgs& a, cudaStream_t s) {
+cudaError_t launch_gemm(GemmArgs& a, Order order, cudaStream_t s) {
+  a.order = order;
   const bool hook = wt::wait_hook_on();
   a.wait = hook ? 1ll << 20 : kWaitCycles;
   a.hold = hook;
@@ -286,12 +297,17 @@ cudaError_t launch_gemm(GemmArgs& a, cudaStream_t s) {
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
   c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (PAIR) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = 2;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (order != AFTER) at[n++] = early_launch();
   c.attrs = at;
-  c.numAttrs = PAIR ? 1 : 0;
+  c.numAttrs = n;
   return cudaLaunchKernelEx(&c, gated_gemm<EPI, T, Q8, PAIR>, (const GemmArgs)a);
 }
 
@@ -372,7 +388,7 @@ cudaError_t pack(Call& c, const GatedArgs& g) {
 bool at16(const void* p, long long ld, int es) { return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0; }
 
 template <int EPI, typename T, bool Q8>
-cudaError_t product_forward(const Call& c, const GatedArgs& g) {
+cudaError_t product_forward(const Call& c, const GatedArgs& g, Order order) {
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
   set_tiles(a, c, c.p.fwd, (int)((d.M + c.p.fwd.rows - 1) / c.p.fwd.rows), true, true);
@@ -401,19 +417,25 @@ cudaError_t product_forward(const Call& c, const GatedArgs& g) {
   RET(make_map(&a.a, c.type, c.x.p, d.C, 1, 0, d.M, c.x.ld, c.p.parts, c.x.part, kRows));
   RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, a.half));
   RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, a.half));
-  return c.p.fwd.pair ? launch_gemm<EPI, T, Q8, true>(a, c.s) : launch_gemm<EPI, T, Q8, false>(a, c.s);
+  return c.p.fwd.pair ? launch_gemm<EPI, T, Q8, true>(a, order, c.s) : launch_gemm<EPI, T, Q8, false>(a, order, c.s);
 }
 
 template <typename T>
 cudaError_t sum_up(const Call& c, const GemmArgs& a, long long rows, long long second, long long second_at) {
   const long long n = (rows * ((c.d.C + 3) / 4) + 255) / 256, limit = 8ll * wt::sm_count();
-  gated_sum<T><<<(unsigned)(n < limit ? n : limit), 256, 0, c.s>>>(a.partial, a.splits, a.partial_rows, a.ld, rows, c.d.C, second,
-                                                                 second_at, (T*)a.out, (T*)a.out2);
-  return cudaGetLastError();
+  cudaLaunchConfig_t l = {};
+  l.gridDim = dim3((unsigned)(n < limit ? n : limit));
+  l.blockDim = dim3(256);
+  l.stream = c.s;
+  cudaLaunchAttribute at = early_launch();
+  l.attrs = &at;
+  l.numAttrs = 1;
+  return cudaLaunchKernelEx(&l, gated_sum<T>, (const float*)a.partial, a.splits, (long long)a.partial_rows, a.ld, rows, c.d.C, second,
+                            second_at, (T*)a.out, (T*)a.out2);
 }
 
 template <int EPI, typename T>
-cudaError_t product_sums(const Call& c, const GatedArgs& g) {
+cudaError_t product_sums(const Call& c, const GatedArgs& g, Order order) {
   constexpr bool dw = EPI == EPI_DW;
   const wtconv_gated_desc_t& d = c.d;
   GemmArgs a = {};
@@ -445,7 +467,7 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g) {
     RET(make_map(&a.b0, c.type, c.gate.p, d.C, 1, 0, d.H, c.gate.ld, c.p.parts, c.gate.part, 64));
     RET(make_map(&a.b1, c.type, c.up.p, d.C, 1, 0, d.H, c.up.ld, c.p.parts, c.up.part, 64));
   }
-  RET((t.pair ? launch_gemm<EPI, T, false, true>(a, c.s) : launch_gemm<EPI, T, false, false>(a, c.s)));
+  RET((t.pair ? launch_gemm<EPI, T, false, true>(a, order, c.s) : launch_gemm<EPI, T, false, false>(a, order, c.s)));
   if (t.splits == 1) return cudaSuccess;
   return dw ? sum_up<T>(c, a, 2ll * d.H, d.H, (long long)tiles * t.rows) : sum_up<T>(c, a, d.M, d.M, 0);
 }
@@ -466,17 +488,18 @@ Call call_of(const wtconv_gated_desc_t& d, const GatedArgs& g, int op, void* ws,
 
 template <typename T>
 cudaError_t forward(Call& c, const GatedArgs& g, bool q8) {
-  if (q8) return product_forward<EPI_H, T, true>(c, g);
+  if (q8) return product_forward<EPI_H, T, true>(c, g, AFTER);
   RET(pack<T>(c, g));
-  return product_forward<EPI_H, T, false>(c, g);
+  return product_forward<EPI_H, T, false>(c, g, c.p.copy_x || c.p.copy_w ? EARLY : AFTER);
 }
 
 template <typename T>
 cudaError_t backward(Call& c, const GatedArgs& g) {
   RET(pack<T>(c, g));
-  RET((product_forward<EPI_P, T, false>(c, g)));
-  if (g.dx) RET((product_sums<EPI_DX, T>(c, g)));
-  if (g.dgate) RET((product_sums<EPI_DW, T>(c, g)));
+  RET((product_forward<EPI_P, T, false>(c, g, c.p.copy_x || c.p.copy_w ? EARLY : AFTER)));
+  if (g.dx) RET((product_sums<EPI_DX, T>(c, g, EARLY)));
+  // both read P; where dx takes no partial sums, whose place dW's would take, it runs beside
+  if (g.dgate) RET((product_sums<EPI_DW, T>(c, g, g.dx && c.p.dx.splits == 1 ? BESIDE : EARLY)));
   return cudaSuccess;
 }
 

@@ -67,6 +67,12 @@ __device__ __forceinline__ int divide(int n, const Divisor& d) {
   return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
 }
 
+// When a launch may begin: after the one before; while that runs, which it waits for
+// behind its own preparations; or while that runs, of which it needs nothing (what
+// both read was there before either), so that it takes the SMs as they fall free,
+// and waits for it at its end, so that who waits for this one waits for both.
+enum Order { AFTER, EARLY, BESIDE };
+
 struct GemmArgs {
   CUtensorMap a, b0, b1;  // operands: (column, 0 or which half, row, part)
   CUtensorMap o0, o1, dh_map;  // results and dh, in staging tiles
@@ -101,6 +107,7 @@ struct GemmArgs {
   long long wait;
   int hold;
   unsigned int* faults;
+  int order;              // an Order
 };
 
 struct Shared {
@@ -763,6 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   if constexpr (PAIR) cluster_meet();
   __syncthreads();
   tc_fence_after();
+  // in this order: a launch BESIDE this one relies on what this one has waited for
+  if (a.order == EARLY) wait_previous();
+  let_next_in();
   const uint32_t tmem = sh.tmem;
   if (warp == 0) {
     produce<EPI, PAIR, Q8>(sh, a, base, w, items);
@@ -779,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     if constexpr (PAIR) tmem_free_pair(tmem, kColumns);
     else tmem_free(tmem, kColumns);
   }
+  if (a.order == BESIDE) wait_previous();
 }
 
 }  // namespace gated

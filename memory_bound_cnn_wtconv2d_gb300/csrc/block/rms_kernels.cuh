@@ -22,6 +22,7 @@
 
 #include "gn_math.cuh"
 #include "mixer_launch.h"
+#include "tc_device.cuh"
 #include "../wtconv_launch.h"
 
 namespace wtb {
@@ -338,7 +339,7 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
       }
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_in();
   if (!a.dweight) return;
   float* out = part + (long long)blockIdx.x * d.C;
   if (per == 1) {
@@ -371,7 +372,7 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
 // loads of each under way.  It may begin while the parts are made.
 static __global__ void __launch_bounds__(1024) add_parts(const float* part, int n, int C, float* out) {
   __shared__ float sh[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_previous();
   const int x = threadIdx.x & 31, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
   float s[8] = {};
   if (c < C) {

@@ -31,7 +31,7 @@ namespace wtb {
 namespace gated {
 
 constexpr int kRows = 128;         // of a tile
-constexpr int kEpiWarps = 16;    // four for each quarter of the rows
+constexpr int kEpiWarps = 16;      // four for each quarter of the rows
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kABytes = 16384;     // 128 rows (or two times 64 k) of 128 bytes
 constexpr int kMaxStages = 8;

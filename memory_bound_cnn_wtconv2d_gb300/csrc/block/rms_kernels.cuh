@@ -97,8 +97,8 @@ __device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VE
 
 // ---- rows that stay in registers ------------------------------------------------
 
-// Pieces of rows on their way.  They are copied asynchronously into a ring of kDepth
-// rows in shared memory, each lane's into places of its own, so that no barrier is
+// Pieces of rows on their way.  They are copied asynchronously into a ring of three
+// rows (or two) in shared memory, each lane's into places of its own, so that no barrier is
 // needed and the copies take no registers.  (Next rows in registers, one deep,
 // were no faster than none: 200704 x 192 bf16 backward 93 us, in the ring 56.)
 // Single 16-bit values are too small for such copies and do go through registers.
@@ -106,13 +106,12 @@ template <typename T, int VEC, int ITEMS, int TENSORS>
 struct Pieces {
   static constexpr int kSize = VEC * (int)sizeof(T);
   static constexpr bool kRing = kSize >= 4;
-  static constexpr int kDepth = kRing ? 3 : 1;
-  static constexpr int kBytes = kRing ? kDepth * TENSORS * ITEMS * kSize : 0;  // of a thread
+  static constexpr int kRow = kRing ? TENSORS * ITEMS * kSize : 0;  // bytes of a thread for a row
   unsigned char* base;
-  int stage;
+  int stage, depth;
   Vec<T, VEC> held[kRing ? 1 : TENSORS][kRing ? 1 : ITEMS];
 
-  __device__ __forceinline__ explicit Pieces(unsigned char* p) : base(p), stage(0) {}
+  __device__ __forceinline__ Pieces(unsigned char* p, int d) : base(p), stage(0), depth(kRing ? d : 1) {}
   __device__ __forceinline__ unsigned char* place(int tensor, int k) const {
     return base + (((stage * TENSORS + tensor) * ITEMS + k) * blockDim.x + threadIdx.x) * kSize;
   }
@@ -138,12 +137,15 @@ struct Pieces {
   __device__ __forceinline__ void asked() {  // one row
     if constexpr (kRing) {
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (++stage == kDepth) stage = 0;
+      if (++stage == depth) stage = 0;
     }
   }
-  // Waits for the row asked for kDepth rows ago, which lies in the current stage.
+  // Waits for the row asked for `depth` rows ago, which lies in the current stage.
   __device__ __forceinline__ void arrived() const {
-    if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    if constexpr (kRing) {
+      if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
   }
   __device__ __forceinline__ void take(Vec<T, VEC>& v, int tensor, int k) const {
     if constexpr (kRing) v.load(reinterpret_cast<const T*>(place(tensor, k)));
@@ -173,11 +175,11 @@ __device__ __forceinline__ void kept_weight(const float* w, int c, float (&v)[VE
 
 template <typename T, int VEC, int ITEMS, bool Q8>
 __global__ void __launch_bounds__(kThreads, 2)
-rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm) {
+rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm, int depth) {
   extern __shared__ __align__(16) unsigned char raw[];
   typedef Pieces<T, VEC, ITEMS, 2> P;
-  P in(raw);
-  float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
+  P in(raw, depth);
+  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const float over = 1.f / d.C;
   const long long step = (long long)gridDim.x * per;
@@ -188,8 +190,7 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
     if (a.r) in.ask(1, a.r, at * d.r_stride, lane, lanes, most);
     in.asked();
   };
-#pragma unroll
-  for (int i = 0; i < P::kDepth; ++i) ask(row + i * step);
+  for (int i = 0; i < in.depth; ++i) ask(row + i * step);
   keep_weight<VEC>(w, a.weight, d.C);
   // every thread of the CTA takes as many turns
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
@@ -229,7 +230,7 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
         }
       }
     }
-    ask(row + P::kDepth * step);
+    ask(row + in.depth * step);
     // 8 bits: the largest |y| is rstd times the largest |t w|, so one exchange does
     over_row<Q8>(s, m, lanes);
     const float rstd = norm ? 1.f / sqrtf(s * over + d.eps) : 1.f;
@@ -266,11 +267,11 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 
 template <typename T, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kThreads, 2)
-rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part) {
+rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part, int depth) {
   extern __shared__ __align__(16) unsigned char raw[];
   typedef Pieces<T, VEC, ITEMS, 3> P;
-  P in(raw);
-  float* w = reinterpret_cast<float*>(raw + P::kBytes * blockDim.x);
+  P in(raw, depth);
+  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x);
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const long long step = (long long)gridDim.x * per;
   float dw[ITEMS][VEC];
@@ -287,8 +288,7 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     if (a.r) in.ask(2, a.r, at * d.r_stride, lane, lanes, most);
     in.asked();
   };
-#pragma unroll
-  for (int i = 0; i < P::kDepth; ++i) ask(row + i * step);
+  for (int i = 0; i < in.depth; ++i) ask(row + i * step);
   float next = row < d.M ? a.rstd[row] : 0.f;
   keep_weight<VEC>(w, a.weight, d.C);
   for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
@@ -320,7 +320,7 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
         }
       }
     }
-    ask(row + P::kDepth * step);
+    ask(row + in.depth * step);
     s = -over_row(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -521,8 +521,9 @@ inline Shape shape_of(int C, int vec, int values) {
     int lanes = 1;
     while (lanes < (n + items - 1) / items) lanes *= 2;
     if (lanes > kMostLanes) continue;
-    // lanes beyond a warp cost a barrier, worth a quarter of idle lanes
-    const int cost = lanes * items * (lanes > 32 ? 5 : 4);
+    // lanes beyond a warp cost a barrier, worth a quarter of idle lanes; 32 values a
+    // lane there leave the SM few warps (16384 x 2048 16-bit: 57 us, 16 values 54)
+    const int cost = lanes * items * (lanes <= 32 ? 8 : items * vec == 32 ? 12 : 10);
     if (!best.items || cost < least) least = cost, best = {lanes, items, lanes > 32 ? lanes : kThreads};
   }
   return best;
@@ -554,13 +555,19 @@ inline cudaError_t launch_add(const float* part, int n, int C, float* out, cudaS
   return cudaLaunchKernelEx(&c, add_parts, part, n, C, out);
 }
 
+// Rows of the ring: three, or two where that lets a second CTA onto the SM.
+inline int depth_of(const Shape& s, int row_bytes, int C) {
+  return s.threads * row_bytes * 3 + C * 4 > 113 * 1024 ? 2 : 3;
+}
+
 template <typename T, int VEC, int ITEMS>
 cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, const Shape& s, cudaStream_t st) {
-  const int smem = s.threads * Pieces<T, VEC, ITEMS, 2>::kBytes + d.C * 4;
+  typedef Pieces<T, VEC, ITEMS, 2> P;
+  const int depth = depth_of(s, P::kRow, d.C), smem = s.threads * P::kRow * depth + d.C * 4;
   auto launch = [&](auto* f, int norm) {
     const cudaError_t e = wt::ensure_smem((const void*)f, smem);
     if (e != cudaSuccess) return e;
-    f<<<grid_of((const void*)f, d.M, s, smem), s.threads, smem, st>>>(d, a, s.lanes, norm);
+    f<<<grid_of((const void*)f, d.M, s, smem), s.threads, smem, st>>>(d, a, s.lanes, norm, depth);
     return cudaGetLastError();
   };
   if (op == RMS_FWD) return launch(rows_forward<T, VEC, ITEMS, false>, 1);
@@ -568,7 +575,9 @@ cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a,
 }
 template <typename T, int VEC, int ITEMS>
 cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Shape& s, float* part, cudaStream_t st) {
-  int smem = s.threads * Pieces<T, VEC, ITEMS, 3>::kBytes + d.C * 4;
+  typedef Pieces<T, VEC, ITEMS, 3> P;
+  const int depth = depth_of(s, P::kRow, d.C);
+  int smem = s.threads * P::kRow * depth + d.C * 4;
   const int sums = s.threads > s.lanes ? s.threads * ITEMS * VEC * 4 : 0;
   if (sums > smem) smem = sums;
   const void* f = (const void*)rows_backward<T, VEC, ITEMS>;
@@ -576,7 +585,7 @@ cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Sh
   if (e != cudaSuccess) return e;
   int grid = grid_of(f, d.M, s, smem);
   if (grid > parts_most(d)) grid = parts_most(d);
-  rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part);
+  rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part, depth);
   if (!a.dweight) return cudaGetLastError();
   return launch_add(part, grid, d.C, a.dweight, st);
 }

@@ -36,22 +36,26 @@ wtconv_status_t check_rms(const wtconv_rms_desc_t* d, int need) {
   return WTCONV_OK;
 }
 
-// The widest access that C, the addresses and the strides (0: contiguous rows)
-// allow; NULL allows any.
-struct Width {
+// How the rows of a call's tensors can be read; NULL tensors do not count.
+struct Rows {
   const wtconv_rms_desc_t* d;
-  int es, v;
-  explicit Width(const wtconv_rms_desc_t* d) : d(d), es(esize(d->dtype)), v(16 / es) {
-    while (v > 1 && d->C % v) v >>= 1;
-  }
+  int es, vec, begin = -1;
+  bool aligned, shifted = true;
+  explicit Rows(const wtconv_rms_desc_t* d) : d(d), es(esize(d->dtype)), vec(16 / es), aligned(d->C % vec == 0) {}
   void with(const void* p, long long stride) {
     if (!p) return;
-    const int w = widest(es, p, 0, stride, 1, d->M);
-    if (w < v) v = w;
+    const int at = (int)((uintptr_t)p % 16) / es;
+    if (begin < 0) begin = at;
+    // a row and the next of every tensor as those of contiguous rows lie
+    shifted = shifted && at == begin && (d->M == 1 || stride % vec == d->C % vec);
+    aligned = aligned && at == 0 && (d->M == 1 || stride % vec == 0);
   }
-  void with_bytes(const void* p) {
-    while (v > 1 && (uintptr_t)p % v) v >>= 1;
+  void with_bytes(const void* p) {  // of one byte a value, where `with` has seen another
+    if (!p) return;
+    shifted = shifted && (int)((uintptr_t)p % vec) == begin;
+    aligned = aligned && (uintptr_t)p % vec == 0;
   }
+  wtb::RowAccess how() const { return aligned ? wtb::ROWS_ALIGNED : shifted ? wtb::ROWS_SHIFTED : wtb::ROWS_SINGLE; }
 };
 
 wtconv_status_t rms_forward(const wtconv_rms_desc_t* d, wtb::RmsOp op, const void* x, const void* r, const float* w,
@@ -70,13 +74,14 @@ wtconv_status_t rms_forward(const wtconv_rms_desc_t* d, wtb::RmsOp op, const voi
     if (!r) total = nullptr;
     wtb::RmsArgs a = {};
     a.x = x; a.r = r; a.weight = w; a.y = y; a.q = (unsigned char*)q; a.total = total; a.rstd = stat;
-    Width v(d);
+    Rows v(d);
     v.with(x, d->x_stride);
     v.with(r, d->r_stride);
     v.with(y, d->C);
     v.with(total, d->C);
     v.with_bytes(q);
-    return cuda_status(wtb::rms_launch(*d, op, a, v.v, (cudaStream_t)stream), name);
+    a.begin = v.begin;
+    return cuda_status(wtb::rms_launch(*d, op, a, v.how(), (cudaStream_t)stream), name);
   } catch (...) {
     return fail(WTCONV_ERR_CUDA, "%s: out of host memory", name);
   }
@@ -203,12 +208,13 @@ wtconv_status_t wtconv_rms_norm_bwd(const wtconv_rms_desc_t* d, const void* dy, 
     if (dw) TRY(workspace(ws, ws_bytes, wtb::rms_bwd_workspace(*d)));
     wtb::RmsArgs a = {};
     a.x = total; a.r = dtotal; a.dy = dy; a.weight = w; a.y = dx; a.rstd = const_cast<float*>(rstd); a.dweight = dw;
-    Width v(d);
+    Rows v(d);
     v.with(total, d->x_stride);
     v.with(dtotal, d->r_stride);
     v.with(dy, d->d_stride);
     v.with(dx, d->C);
-    return cuda_status(wtb::rms_bwd_launch(*d, a, v.v, ws, s), "wtconv_rms_norm_bwd");
+    a.begin = v.begin;
+    return cuda_status(wtb::rms_bwd_launch(*d, a, v.how(), ws, s), "wtconv_rms_norm_bwd");
   } catch (...) {
     return fail(WTCONV_ERR_CUDA, "wtconv_rms_norm_bwd: out of host memory");
   }

@@ -8,8 +8,10 @@
 
 namespace wtb {
 
-// Root-mean-square norm.  `vec` is the number of elements of the widest access
-// that every pointer, stride and C allow (16 bytes at most).
+// Root-mean-square norm.  How rows can be read: every one begins on a 16-byte
+// boundary and ends on one; every tensor's rows begin as many elements behind one
+// (`begin` for the first row); neither.
+enum RowAccess { ROWS_ALIGNED, ROWS_SHIFTED, ROWS_SINGLE };
 struct RmsArgs {
   const void *x, *r, *dy;  // backward: x is t, r is what reaches t by itself
   const float* weight;
@@ -18,11 +20,12 @@ struct RmsArgs {
   void* total;
   float* rstd;             // 8-bit output: the scales
   float* dweight;
+  int begin;
 };
 enum RmsOp { RMS_FWD, RMS_Q8, RMS_QUANTIZE };
-cudaError_t rms_launch(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, int vec, cudaStream_t s);
+cudaError_t rms_launch(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, RowAccess how, cudaStream_t s);
 size_t rms_bwd_workspace(const wtconv_rms_desc_t& d);
-cudaError_t rms_bwd_launch(const wtconv_rms_desc_t& d, const RmsArgs& a, int vec, void* ws, cudaStream_t s);
+cudaError_t rms_bwd_launch(const wtconv_rms_desc_t& d, const RmsArgs& a, RowAccess how, void* ws, cudaStream_t s);
 
 // Gated product.
 struct GatedArgs {

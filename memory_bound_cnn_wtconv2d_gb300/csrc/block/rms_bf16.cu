@@ -2,10 +2,10 @@
 #include "rms_kernels.cuh"
 
 namespace wtb {
-cudaError_t rms_forward_bf16(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, int vec, cudaStream_t s) {
-  return rms::forward_typed<__nv_bfloat16>(d, op, a, vec, s);
+cudaError_t rms_forward_bf16(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, RowAccess how, cudaStream_t s) {
+  return rms::forward_typed<__nv_bfloat16>(d, op, a, how, s);
 }
-cudaError_t rms_backward_bf16(const wtconv_rms_desc_t& d, const RmsArgs& a, int vec, float* part, cudaStream_t s) {
-  return rms::backward_typed<__nv_bfloat16>(d, a, vec, part, s);
+cudaError_t rms_backward_bf16(const wtconv_rms_desc_t& d, const RmsArgs& a, RowAccess how, float* part, cudaStream_t s) {
+  return rms::backward_typed<__nv_bfloat16>(d, a, how, part, s);
 }
 }  // namespace wtb

@@ -10,8 +10,15 @@
 // of a warp for short rows (several rows a warp, no barrier), a CTA of 64 to 256
 // threads for long ones.  Values a lane and lanes are chosen so that few lanes
 // idle (96 channels of 16 bits: 4 lanes of three 16-byte accesses).  Rows that no
-// CTA holds (above 8192 channels, or long ones of odd width) are read twice or
-// three times, the later times from the caches.
+// CTA holds (above 8192 channels, backward 6144) are read twice or three times,
+// the later times from the caches.
+//
+// Rows of 90 or 1001 channels begin between two 16-byte boundaries, and not all at
+// the same place.  They are taken from the boundary before on: a lane's pieces are
+// shifted by what the row begins behind it, pieces that hang over are masked and
+// written value by value.  A lane's rows lie a multiple of eight apart, so that its
+// shift, and with it its columns of dw, stay.  Only where the tensors' rows do not
+// all begin at the same place are they read value by value.
 //
 // CTAs stay and take rows in turn: the weight is read once where it fits the
 // registers, and the backward adds up its part of dw on the way, so that dy and t
@@ -102,7 +109,7 @@ __device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&v)[VE
 // needed and the copies take no registers.  (Next rows in registers, one deep,
 // were no faster than none: 200704 x 192 bf16 backward 93 us, in the ring 56.)
 // Single 16-bit values are too small for such copies and do go through registers.
-template <typename T, int VEC, int ITEMS, int TENSORS>
+template <typename T, int VEC, int ITEMS, int TENSORS, bool SHIFT>
 struct Pieces {
   static constexpr int kSize = VEC * (int)sizeof(T);
   static constexpr bool kRing = kSize >= 4;
@@ -115,13 +122,23 @@ struct Pieces {
   __device__ __forceinline__ unsigned char* place(int tensor, int k) const {
     return base + (((stage * TENSORS + tensor) * ITEMS + k) * blockDim.x + threadIdx.x) * kSize;
   }
-  // Asks for a tensor's part of the row that the current stage will hold.
-  __device__ __forceinline__ void ask(int tensor, const void* p, long long at, int lane, int lanes, int most) {
+  // Asks for a tensor's part of the row that the current stage will hold; `first` is
+  // the column of the lane's first piece.  edge: a row at the tensor's beginning or
+  // end, where pieces that hang over are not read whole.
+  __device__ __forceinline__ void ask(int tensor, const void* p, long long at, int first, int lanes, int most, bool edge) {
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c >= most) continue;
+      const int c = first + k * lanes * VEC;
+      if (c >= most || c <= -VEC) continue;  // a row that does not exist has less than -VEC + 1
       const T* from = (const T*)p + at + c;
+      if constexpr (SHIFT) {
+        if (edge && (c < 0 || c + VEC > most)) {
+          T* to = reinterpret_cast<T*>(place(tensor, k));
+          for (int i = 0; i < VEC; ++i)
+            if (c + i >= 0 && c + i < most) to[i] = from[i];
+          continue;
+        }
+      }
       if constexpr (kSize == 16) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place(tensor, k))), "l"(from)
                      : "memory");
@@ -153,15 +170,18 @@ struct Pieces {
   }
 };
 
-// The weight in shared memory, ones where there is none.
-template <int VEC>
+// The weight in shared memory (ones where there is none), and room on both sides for
+// pieces that hang over.
+constexpr int kMargin = 8;
+constexpr int kNone = -kMargin;  // columns of a row that does not exist: before any piece's first
 __device__ __forceinline__ void keep_weight(float* w, const float* weight, int C) {
-  for (int c = threadIdx.x; c < C; c += blockDim.x) w[c] = weight ? __ldg(weight + c) : 1.f;
+  for (int c = (int)threadIdx.x - kMargin; c < C + kMargin; c += blockDim.x)
+    w[c] = c < 0 || c >= C ? 0.f : weight ? __ldg(weight + c) : 1.f;
   __syncthreads();
 }
-template <int VEC>
+template <int VEC, bool SHIFT>
 __device__ __forceinline__ void kept_weight(const float* w, int c, float (&v)[VEC]) {
-  if constexpr (VEC % 4 == 0) {
+  if constexpr (VEC % 4 == 0 && !SHIFT) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4) {
       const float4 f = *reinterpret_cast<const float4*>(w + c + i);
@@ -173,51 +193,86 @@ __device__ __forceinline__ void kept_weight(const float* w, int c, float (&v)[VE
   }
 }
 
-template <typename T, int VEC, int ITEMS, bool Q8>
+// A piece's values, 0 for those that lie outside of the row.
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void widen_piece(const Vec<T, VEC>& u, int c, int C, float (&v)[VEC]) {
+  u.widen(v);
+  if constexpr (SHIFT) {
+    if (c < 0 || c + VEC > C) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (c + i < 0 || c + i >= C) v[i] = 0.f;
+    }
+  }
+}
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void store_piece(T* row, int c, int C, const float (&v)[VEC]) {
+  Vec<T, VEC> o;
+  o.round(v);
+  if (!SHIFT || (c >= 0 && c + VEC <= C)) {
+    o.store(row + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c + i >= 0 && c + i < C) row[c + i] = o.e[i];
+  }
+}
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void store_piece_e4m3(unsigned char* row, int c, int C, const float (&v)[VEC]) {
+  if (!SHIFT || (c >= 0 && c + VEC <= C)) {
+    store_e4m3<VEC>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c + i >= 0 && c + i < C) row[c + i] = __nv_cvt_float_to_fp8(v[i], __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+template <typename T, int VEC, int ITEMS, bool Q8, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 2)
 rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, int norm, int depth) {
   extern __shared__ __align__(16) unsigned char raw[];
-  typedef Pieces<T, VEC, ITEMS, 2> P;
+  typedef Pieces<T, VEC, ITEMS, 2, SHIFT> P;
   P in(raw, depth);
-  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x);
+  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x) + kMargin;
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const float over = 1.f / d.C;
   const long long step = (long long)gridDim.x * per;
   long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
+  const int first = lane * VEC - (SHIFT ? (int)((a.begin + row * d.C) % VEC) : 0);  // the column of the first piece
   auto ask = [&](long long at) {
-    const int most = at < d.M ? d.C : 0;
-    in.ask(0, a.x, at * d.x_stride, lane, lanes, most);
-    if (a.r) in.ask(1, a.r, at * d.r_stride, lane, lanes, most);
+    const int most = at < d.M ? d.C : kNone;
+    // fewer than VEC values of the tensor before or behind the row
+    const bool edge = SHIFT && (at * d.C < VEC || (d.M - 1 - at) * d.C < VEC);
+    in.ask(0, a.x, at * d.x_stride, first, lanes, most, edge);
+    if (a.r) in.ask(1, a.r, at * d.r_stride, first, lanes, most, edge);
     in.asked();
   };
   for (int i = 0; i < in.depth; ++i) ask(row + i * step);
-  keep_weight<VEC>(w, a.weight, d.C);
+  keep_weight(w, a.weight, d.C);
   // every thread of the CTA takes as many turns
-  for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
-    const int most = row < d.M ? d.C : 0;
+  for (long long turn = (long long)blockIdx.x * per; turn < d.M; turn += step, row += step) {
+    const int most = row < d.M ? d.C : kNone;
     float t[ITEMS][VEC], s = 0.f, m = 0.f;
     in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) {
+      const int c = first + k * lanes * VEC;
+      if (c < most && c > -VEC) {
         Vec<T, VEC> u;
         in.take(u, 0, k);
-        u.widen(t[k]);
+        widen_piece<T, VEC, SHIFT>(u, c, d.C, t[k]);
         if (a.r) {
           float o[VEC];
           in.take(u, 1, k);
-          u.widen(o);
+          widen_piece<T, VEC, SHIFT>(u, c, d.C, o);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) t[k][i] += o[i];
-          if (a.total) {
-            u.round(t[k]);
-            u.store((T*)a.total + row * d.C + c);
-          }
+          if (a.total) store_piece<T, VEC, SHIFT>((T*)a.total + row * d.C, c, d.C, t[k]);
         }
         if constexpr (Q8) {
           float f[VEC];
-          kept_weight<VEC>(w, c, f);
+          kept_weight<VEC, SHIFT>(w, c, f);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             s = fmaf(t[k][i], t[k][i], s);
@@ -239,39 +294,37 @@ rows_forward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
       const float f = kE4m3Most / m;
 #pragma unroll
       for (int k = 0; k < ITEMS; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-        if (c < most) {
+        const int c = first + k * lanes * VEC;
+        if (c < most && c > -VEC) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) t[k][i] = t[k][i] * rstd * f;
-          store_e4m3<VEC>(a.q + row * d.C + c, t[k]);
+          store_piece_e4m3<VEC, SHIFT>(a.q + row * d.C, c, d.C, t[k]);
         }
       }
     } else {
 #pragma unroll
       for (int k = 0; k < ITEMS; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-        if (c < most) {
+        const int c = first + k * lanes * VEC;
+        if (c < most && c > -VEC) {
           float f[VEC];
-          kept_weight<VEC>(w, c, f);
+          kept_weight<VEC, SHIFT>(w, c, f);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) t[k][i] = t[k][i] * rstd * f[i];
-          Vec<T, VEC> o;
-          o.round(t[k]);
-          o.store((T*)a.y + row * d.C + c);
+          store_piece<T, VEC, SHIFT>((T*)a.y + row * d.C, c, d.C, t[k]);
         }
       }
     }
-    if (lane == 0 && most) a.rstd[row] = Q8 ? m / kE4m3Most : rstd;
+    if (lane == 0 && most > 0) a.rstd[row] = Q8 ? m / kE4m3Most : rstd;
   }
 }
 
-template <typename T, int VEC, int ITEMS>
+template <typename T, int VEC, int ITEMS, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 2)
 rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant__ RmsArgs a, int lanes, float* part, int depth) {
   extern __shared__ __align__(16) unsigned char raw[];
-  typedef Pieces<T, VEC, ITEMS, 3> P;
+  typedef Pieces<T, VEC, ITEMS, 3, SHIFT> P;
   P in(raw, depth);
-  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x);
+  float* w = reinterpret_cast<float*>(raw + P::kRow * depth * blockDim.x) + kMargin;
   const int lane = threadIdx.x & (lanes - 1), per = blockDim.x / lanes;
   const long long step = (long long)gridDim.x * per;
   float dw[ITEMS][VEC];
@@ -281,18 +334,21 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     for (int i = 0; i < VEC; ++i) dw[k][i] = 0.f;
   const float over = 1.f / d.C;
   long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;
+  const int first = lane * VEC - (SHIFT ? (int)((a.begin + row * d.C) % VEC) : 0);
   auto ask = [&](long long at) {
-    const int most = at < d.M ? d.C : 0;
-    in.ask(0, a.x, at * d.x_stride, lane, lanes, most);
-    in.ask(1, a.dy, at * d.d_stride, lane, lanes, most);
-    if (a.r) in.ask(2, a.r, at * d.r_stride, lane, lanes, most);
+    const int most = at < d.M ? d.C : kNone;
+    // fewer than VEC values of the tensor before or behind the row
+    const bool edge = SHIFT && (at * d.C < VEC || (d.M - 1 - at) * d.C < VEC);
+    in.ask(0, a.x, at * d.x_stride, first, lanes, most, edge);
+    in.ask(1, a.dy, at * d.d_stride, first, lanes, most, edge);
+    if (a.r) in.ask(2, a.r, at * d.r_stride, first, lanes, most, edge);
     in.asked();
   };
   for (int i = 0; i < in.depth; ++i) ask(row + i * step);
   float next = row < d.M ? a.rstd[row] : 0.f;
-  keep_weight<VEC>(w, a.weight, d.C);
-  for (long long first = (long long)blockIdx.x * per; first < d.M; first += step, row += step) {
-    const int most = row < d.M ? d.C : 0;
+  keep_weight(w, a.weight, d.C);
+  for (long long turn = (long long)blockIdx.x * per; turn < d.M; turn += step, row += step) {
+    const int most = row < d.M ? d.C : kNone;
     const float rstd = next;
     if (row + step < d.M) next = a.rstd[row + step];
     float s = 0.f;
@@ -301,16 +357,16 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     in.arrived();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) {
+      const int c = first + k * lanes * VEC;
+      if (c < most && c > -VEC) {
         Vec<T, VEC> u;
         in.take(u, 0, k);
-        u.widen(t[k]);
+        widen_piece<T, VEC, SHIFT>(u, c, d.C, t[k]);
         in.take(u, 1, k);
-        u.widen(g[k]);
+        widen_piece<T, VEC, SHIFT>(u, c, d.C, g[k]);
         if (a.r) in.take(o[k], 2, k);
         float f[VEC];
-        kept_weight<VEC>(w, c, f);
+        kept_weight<VEC, SHIFT>(w, c, f);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           t[k][i] *= rstd;  // xhat
@@ -324,8 +380,8 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
     s = -over_row(s, lanes) * over;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-      if (c < most) {
+      const int c = first + k * lanes * VEC;
+      if (c < most && c > -VEC) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) g[k][i] = rstd * fmaf(s, t[k][i], g[k][i]);
         if (a.r) {
@@ -334,36 +390,30 @@ rows_backward(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant
 #pragma unroll
           for (int i = 0; i < VEC; ++i) g[k][i] += more[i];
         }
-        o[k].round(g[k]);
-        o[k].store((T*)a.y + row * d.C + c);
+        store_piece<T, VEC, SHIFT>((T*)a.y + row * d.C, c, d.C, g[k]);
       }
     }
   }
   let_next_in();
   if (!a.dweight) return;
   float* out = part + (long long)blockIdx.x * d.C;
-  if (per == 1) {
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int c = (k * lanes + lane) * VEC;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (c < d.C) out[c + i] = dw[k][i];
-    }
-    return;
+  float* sums = reinterpret_cast<float*>(raw);  // [rows at a time][C], where the ring was
+  if (per > 1) {
+    if constexpr (P::kRing) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
   }
-  const int width = lanes * ITEMS * VEC;
-  float* sums = reinterpret_cast<float*>(raw);  // [rows at a time][width], where the ring was
-  if constexpr (P::kRing) asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k)
+  for (int k = 0; k < ITEMS; ++k) {
+    const int c = first + k * lanes * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sums[threadIdx.x / lanes * width + (k * lanes + lane) * VEC + i] = dw[k][i];
+    for (int i = 0; i < VEC; ++i)
+      if (c + i >= 0 && c + i < d.C) (per == 1 ? out : sums + threadIdx.x / lanes * d.C)[c + i] = dw[k][i];
+  }
+  if (per == 1) return;
   __syncthreads();
   for (int c = threadIdx.x; c < d.C; c += blockDim.x) {
     float v = 0.f;
-    for (int i = 0; i < per; ++i) v += sums[i * width + c];
+    for (int i = 0; i < per; ++i) v += sums[i * d.C + c];
     out[c] = v;
   }
 }
@@ -535,11 +585,14 @@ inline int parts_most(const wtconv_rms_desc_t& d) {
   return (int)(d.M < most ? d.M : most);
 }
 
-inline int grid_of(const void* f, long long M, const Shape& s, int smem) {
+// SHIFT: rows that a group of lanes takes lie a multiple of VEC apart.
+inline int grid_of(const void* f, long long M, const Shape& s, int smem, int vec) {
   const long long per = s.threads / s.lanes, n = (M + per - 1) / per;
   const int fit = wt::occupancy(f, s.threads, smem);
-  const long long most = (long long)wt::sm_count() * (fit < 1 ? 1 : fit);
-  return (int)(n < most ? n : most);
+  long long most = (long long)wt::sm_count() * (fit < 1 ? 1 : fit < 8 ? fit : 8);
+  if (n <= most) return (int)n;  // one turn
+  if (per < vec) most = most / (vec / per) * (vec / per);
+  return (int)most;
 }
 
 inline cudaError_t launch_add(const float* part, int n, int C, float* out, cudaStream_t s) {
@@ -560,69 +613,70 @@ inline int depth_of(const Shape& s, int row_bytes, int C) {
   return s.threads * row_bytes * 3 + C * 4 > 113 * 1024 ? 2 : 3;
 }
 
-template <typename T, int VEC, int ITEMS>
+template <typename T, int VEC, int ITEMS, bool SHIFT>
 cudaError_t forward_rows(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, const Shape& s, cudaStream_t st) {
-  typedef Pieces<T, VEC, ITEMS, 2> P;
-  const int depth = depth_of(s, P::kRow, d.C), smem = s.threads * P::kRow * depth + d.C * 4;
+  typedef Pieces<T, VEC, ITEMS, 2, SHIFT> P;
+  const int depth = depth_of(s, P::kRow, d.C), smem = s.threads * P::kRow * depth + (d.C + 2 * kMargin) * 4;
   auto launch = [&](auto* f, int norm) {
     const cudaError_t e = wt::ensure_smem((const void*)f, smem);
     if (e != cudaSuccess) return e;
-    f<<<grid_of((const void*)f, d.M, s, smem), s.threads, smem, st>>>(d, a, s.lanes, norm, depth);
+    f<<<grid_of((const void*)f, d.M, s, smem, SHIFT ? VEC : 1), s.threads, smem, st>>>(d, a, s.lanes, norm, depth);
     return cudaGetLastError();
   };
-  if (op == RMS_FWD) return launch(rows_forward<T, VEC, ITEMS, false>, 1);
-  return launch(rows_forward<T, VEC, ITEMS, true>, op == RMS_Q8);
+  if (op == RMS_FWD) return launch(rows_forward<T, VEC, ITEMS, false, SHIFT>, 1);
+  return launch(rows_forward<T, VEC, ITEMS, true, SHIFT>, op == RMS_Q8);
 }
-template <typename T, int VEC, int ITEMS>
+template <typename T, int VEC, int ITEMS, bool SHIFT>
 cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Shape& s, float* part, cudaStream_t st) {
-  typedef Pieces<T, VEC, ITEMS, 3> P;
+  typedef Pieces<T, VEC, ITEMS, 3, SHIFT> P;
   const int depth = depth_of(s, P::kRow, d.C);
-  int smem = s.threads * P::kRow * depth + d.C * 4;
-  const int sums = s.threads > s.lanes ? s.threads * ITEMS * VEC * 4 : 0;
+  int smem = s.threads * P::kRow * depth + (d.C + 2 * kMargin) * 4;
+  const int sums = s.threads > s.lanes ? s.threads / s.lanes * d.C * 4 : 0;
   if (sums > smem) smem = sums;
-  const void* f = (const void*)rows_backward<T, VEC, ITEMS>;
+  const void* f = (const void*)rows_backward<T, VEC, ITEMS, SHIFT>;
   const cudaError_t e = wt::ensure_smem(f, smem);
   if (e != cudaSuccess) return e;
-  int grid = grid_of(f, d.M, s, smem);
-  if (grid > parts_most(d)) grid = parts_most(d);
-  rows_backward<T, VEC, ITEMS><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part, depth);
+  const int grid = grid_of(f, d.M, s, smem, SHIFT ? VEC : 1);  // at most parts_most()
+  rows_backward<T, VEC, ITEMS, SHIFT><<<grid, s.threads, smem, st>>>(d, a, s.lanes, part, depth);
   if (!a.dweight) return cudaGetLastError();
   return launch_add(part, grid, d.C, a.dweight, st);
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool SHIFT>
 cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, cudaStream_t st) {
-  const Shape s = shape_of(d.C, VEC, kMostValues);
+  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostValues);
   switch (s.items) {
-    case 1: return forward_rows<T, VEC, 1>(d, op, a, s, st);
-    case 2: return forward_rows<T, VEC, 2>(d, op, a, s, st);
-    case 3: return forward_rows<T, VEC, 3>(d, op, a, s, st);
-    case 4: return forward_rows<T, VEC, 4>(d, op, a, s, st);
+    case 1: return forward_rows<T, VEC, 1, SHIFT>(d, op, a, s, st);
+    case 2: return forward_rows<T, VEC, 2, SHIFT>(d, op, a, s, st);
+    case 3: return forward_rows<T, VEC, 3, SHIFT>(d, op, a, s, st);
+    case 4: return forward_rows<T, VEC, 4, SHIFT>(d, op, a, s, st);
     case 8:
-      if constexpr (VEC * 8 <= kMostValues) return forward_rows<T, VEC, 8>(d, op, a, s, st);
+      if constexpr (VEC * 8 <= kMostValues) return forward_rows<T, VEC, 8, SHIFT>(d, op, a, s, st);
   }
+  constexpr int kLong = SHIFT ? 1 : VEC;
   const long long most = (long long)wt::sm_count() * 8;
   const int grid = (int)(d.M < most ? d.M : most);
-  if (op == RMS_FWD) long_forward<T, VEC, false><<<grid, kThreads, 0, st>>>(d, a, 1);
-  else long_forward<T, VEC, true><<<grid, kThreads, 0, st>>>(d, a, op == RMS_Q8);
+  if (op == RMS_FWD) long_forward<T, kLong, false><<<grid, kThreads, 0, st>>>(d, a, 1);
+  else long_forward<T, kLong, true><<<grid, kThreads, 0, st>>>(d, a, op == RMS_Q8);
   return cudaGetLastError();
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool SHIFT>
 cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* part, cudaStream_t st) {
-  const Shape s = shape_of(d.C, VEC, kMostBackward);
+  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostBackward);
   switch (s.items) {
-    case 1: return backward_rows<T, VEC, 1>(d, a, s, part, st);
-    case 2: return backward_rows<T, VEC, 2>(d, a, s, part, st);
-    case 3: return backward_rows<T, VEC, 3>(d, a, s, part, st);
+    case 1: return backward_rows<T, VEC, 1, SHIFT>(d, a, s, part, st);
+    case 2: return backward_rows<T, VEC, 2, SHIFT>(d, a, s, part, st);
+    case 3: return backward_rows<T, VEC, 3, SHIFT>(d, a, s, part, st);
     case 4:
-      if constexpr (VEC * 4 <= kMostBackward) return backward_rows<T, VEC, 4>(d, a, s, part, st);
+      if constexpr (VEC * 4 <= kMostBackward) return backward_rows<T, VEC, 4, SHIFT>(d, a, s, part, st);
       break;
     case 8:
-      if constexpr (VEC * 8 <= kMostBackward) return backward_rows<T, VEC, 8>(d, a, s, part, st);
+      if constexpr (VEC * 8 <= kMostBackward) return backward_rows<T, VEC, 8, SHIFT>(d, a, s, part, st);
   }
+  constexpr int kLong = SHIFT ? 1 : VEC;
   const long long most = (long long)wt::sm_count() * 8;
-  long_backward<T, VEC><<<(int)(d.M < most ? d.M : most), kThreads, 0, st>>>(d, a);
+  long_backward<T, kLong><<<(int)(d.M < most ? d.M : most), kThreads, 0, st>>>(d, a);
   if (a.dweight) {
     const int n = parts_most(d);
     long_dweight<T><<<dim3((d.C + kThreads - 1) / kThreads, n), kThreads, 0, st>>>(d, a, part, (d.M + n - 1) / n);
@@ -631,15 +685,17 @@ cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* pa
   return cudaGetLastError();
 }
 
+// 16-byte accesses at the rows' beginnings, or from the boundaries before them, or
+// single values.
 template <typename T>
-cudaError_t forward_typed(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, int vec, cudaStream_t s) {
-  if (vec >= 16 / (int)sizeof(T)) return forward_vec<T, 16 / sizeof(T)>(d, op, a, s);
-  return vec >= 2 ? forward_vec<T, 2>(d, op, a, s) : forward_vec<T, 1>(d, op, a, s);
+cudaError_t forward_typed(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, RowAccess how, cudaStream_t s) {
+  if (how == ROWS_ALIGNED) return forward_vec<T, 16 / sizeof(T), false>(d, op, a, s);
+  return how == ROWS_SHIFTED ? forward_vec<T, 16 / sizeof(T), true>(d, op, a, s) : forward_vec<T, 1, false>(d, op, a, s);
 }
 template <typename T>
-cudaError_t backward_typed(const wtconv_rms_desc_t& d, const RmsArgs& a, int vec, float* part, cudaStream_t s) {
-  if (vec >= 16 / (int)sizeof(T)) return backward_vec<T, 16 / sizeof(T)>(d, a, part, s);
-  return vec >= 2 ? backward_vec<T, 2>(d, a, part, s) : backward_vec<T, 1>(d, a, part, s);
+cudaError_t backward_typed(const wtconv_rms_desc_t& d, const RmsArgs& a, RowAccess how, float* part, cudaStream_t s) {
+  if (how == ROWS_ALIGNED) return backward_vec<T, 16 / sizeof(T), false>(d, a, part, s);
+  return how == ROWS_SHIFTED ? backward_vec<T, 16 / sizeof(T), true>(d, a, part, s) : backward_vec<T, 1, false>(d, a, part, s);
 }
 
 }  // namespace rms

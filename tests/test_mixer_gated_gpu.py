@@ -241,6 +241,27 @@ def test_what_lies_behind_the_last_row_stays(ops):
         assert (bx[131:] == 7).all() and (bw[:, 72:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_tensors_that_begin_anywhere(ops, dtype):
+    for M, C, H in ((3, 24, 40), (140, 64, 96), (129, 33, 57)):
+        dh0, x0, gate0, up0 = inputs(M, C, H, dtype)
+        for offsets in ((1, 0, 0, 0), (0, 1, 3, 5), (3, 3, 3, 3), (8, 8, 8, 8)):
+            def place(t, o):
+                flat = torch.full((t.numel() + 40,), 7.0, device="cuda", dtype=dtype)
+                flat[16 + o:16 + o + t.numel()] = t.flatten()
+                return flat[16 + o:16 + o + t.numel()].view(t.shape), flat
+
+            dh, x, gate, up = (place(t, o)[0] for t, o in zip((dh0, x0, gate0, up0), offsets))
+            outs = [place(t * 0, o) for t, o in zip((dh0, x0, gate0, up0), offsets)]
+            ops.wtconv_gated_fwd(x, gate, up, h=outs[0][0])
+            check_forward(outs[0][0], x0, gate0, up0, "silu")
+            ops.wtconv_gated_bwd(dh, x, gate, up, dx=outs[1][0], dgate=outs[2][0], dup=outs[3][0])
+            check_backward(tuple(o[0] for o in outs[1:]), dh0, x0, gate0, up0, "silu", dtype)
+            for t, flat in outs:
+                at = t.storage_offset()
+                assert (flat[:at] == 7).all() and (flat[at + t.numel():] == 7).all()
+
+
 def test_refusals(ops):
     dh, x, gate, up = inputs(4, 32, 16, F32)
     q, s = ops.wtconv_quantize_rows(x)

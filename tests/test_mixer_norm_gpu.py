@@ -137,6 +137,43 @@ def test_slices_and_leading_axes(ops, dtype):
     near(ops.wtconv_rms_norm_fwd(row)[0], forward64(row, None, None, 1e-6)[0], dtype)
 
 
+def at_offset(shape, offset, dtype, fill=None):
+    """A contiguous tensor that begins `offset` elements behind a 16-byte boundary, and
+    the buffer around it."""
+    n = 1
+    for v in shape:
+        n *= v
+    flat = torch.full((n + 64,), 7.0, device="cuda").to(dtype)
+    t = flat[32 + offset:32 + offset + n].view(shape)
+    if fill is not None:
+        t.copy_(fill)
+    return t, flat
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,C", [(1, 1), (2, 3), (9, 5), (40, 7), (100, 90), (33, 91), (300, 257), (3, 1001), (1000, 13), (7, 8), (64, 96)])
+def test_rows_that_begin_anywhere(ops, M, C, dtype):
+    x0, r0, w, dy0, dt0 = inputs(M, C, dtype, C)
+    q8 = torch.float8_e4m3fn
+    for offsets in ((0, 0, 0, 0), (1, 1, 1, 1), (3, 3, 3, 3), (0, 1, 2, 3), (5, 5, 5, 0), (7, 7, 7, 7)):
+        x, r, dy, dt = (at_offset((M, C), o, dtype, v)[0] for o, v in zip(offsets, (x0, r0, dy0, dt0)))
+        outs = [at_offset((M, C), o, t) for o, t in zip((offsets[0], offsets[1], offsets[0], offsets[3]), (dtype, dtype, q8, dtype))]
+        y, total, rstd = ops.wtconv_rms_norm_fwd(x, w, residual=r, y=outs[0][0], total=outs[1][0])
+        y64, t64, _ = forward64(x0, r0, w, 1e-6)
+        near(y, y64, dtype)
+        near(total, t64, dtype, 1e-6)
+        q, scale, _ = ops.wtconv_rms_norm_q8(x, w, residual=r, q=outs[2][0])
+        in_8_bits(q, scale, y64)
+        dx, dw = ops.wtconv_rms_norm_bwd(dy, x, rstd, w, dtotal=dt, dx=outs[3][0])
+        dx64, terms, first = backward64(dy0, x0, rstd, w, dt0)
+        near(dx, dx64, dtype, terms=torch.maximum(first.abs(), dx64.abs()))
+        assert float(((dw.double() - terms.sum(0)).abs() - 1e-5 * terms.square().sum(0).sqrt()).max()) <= 0
+        for t, flat in outs:  # nothing around the outputs is touched
+            at = t.storage_offset()
+            around = torch.cat([flat[:at].float(), flat[at + M * C:].float()])
+            assert (around == 7).all()
+
+
 def test_rows_of_zeros_and_of_extremes(ops):
     x = torch.randn(9, 320, device="cuda")
     x[2] = 0

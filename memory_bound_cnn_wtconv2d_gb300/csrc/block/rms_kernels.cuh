@@ -562,8 +562,12 @@ long_dweight(const __grid_constant__ wtconv_rms_desc_t d, const __grid_constant_
 struct Shape {
   int lanes, items, threads;
 };
-inline Shape shape_of(int C, int vec, int values) {
+inline Shape shape_of(int C, int vec, int values, long long M) {
   const int n = (C + vec - 1) / vec;
+  // few rows: a lane for each piece, as long as two CTAs an SM hold them all
+  int one = 1;
+  while (one < n) one *= 2;
+  if (one <= kMostLanes && M * one <= 2ll * kThreads * wt::sm_count()) return {one, 1, one > 32 ? one : kThreads};
   Shape best = {0, 0, 0};
   int least = 0;
   for (int items : {4, 3, 2, 1, 8}) {  // in order of preference where as many lanes idle
@@ -644,7 +648,7 @@ cudaError_t backward_rows(const wtconv_rms_desc_t& d, const RmsArgs& a, const Sh
 
 template <typename T, int VEC, bool SHIFT>
 cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, cudaStream_t st) {
-  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostValues);
+  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostValues, d.M);
   switch (s.items) {
     case 1: return forward_rows<T, VEC, 1, SHIFT>(d, op, a, s, st);
     case 2: return forward_rows<T, VEC, 2, SHIFT>(d, op, a, s, st);
@@ -663,7 +667,7 @@ cudaError_t forward_vec(const wtconv_rms_desc_t& d, RmsOp op, const RmsArgs& a, 
 
 template <typename T, int VEC, bool SHIFT>
 cudaError_t backward_vec(const wtconv_rms_desc_t& d, const RmsArgs& a, float* part, cudaStream_t st) {
-  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostBackward);
+  const Shape s = shape_of(d.C + (SHIFT ? VEC - 1 : 0), VEC, kMostBackward, d.M);
   switch (s.items) {
     case 1: return backward_rows<T, VEC, 1, SHIFT>(d, a, s, part, st);
     case 2: return backward_rows<T, VEC, 2, SHIFT>(d, a, s, part, st);

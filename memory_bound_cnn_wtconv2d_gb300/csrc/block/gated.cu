@@ -5,6 +5,10 @@
 // C operations of 12 in all), which costs less than writing and reading them
 // where C is below about 560, and no memory.  Three products: P = [dg du] with
 // its epilogue, dx = P [Wg; Wu], dW = P^T x.
+#include <string.h>
+
+#include <atomic>
+
 #include "gated_kernels.cuh"
 
 #include "block_launch.h"
@@ -193,9 +197,8 @@ struct Plan {
   long long p_part;
 };
 
-Plan plan_of(const wtconv_gated_desc_t& d, int op) {
+Plan make_plan(const wtconv_gated_desc_t& d, int op, int sms) {
   Plan p = {};
-  const int sms = wt::sm_count() > 0 ? wt::sm_count() : 152;  // a size may be asked for without a GPU
   const bool f32 = d.dtype == WTCONV_F32 && op != WTCONV_OP_GATED_Q8;
   p.parts = f32 ? 3 : 1;
   p.products = f32 ? 6 : 1;
@@ -238,6 +241,26 @@ Plan plan_of(const wtconv_gated_desc_t& d, int op) {
   return p;
 }
 
+// The thread's last few plans by description: a call asks for its plan twice, and a
+// step makes the same few calls again and again.
+Plan plan_of(const wtconv_gated_desc_t& d, int op) {
+  struct Kept {
+    wtconv_gated_desc_t d;
+    int op, sms;
+    Plan p;
+  };
+  static thread_local Kept kept[4] = {};
+  static thread_local unsigned next = 0;
+  const int n = wt::sm_count(), sms = n > 0 ? n : 152;  // a size may be asked for without a GPU
+  for (const Kept& k : kept)
+    if (k.sms == sms && k.op == op && memcmp(&k.d, &d, sizeof(d)) == 0) return k.p;
+  Kept& k = kept[next++ % 4];
+  memcpy(&k.d, &d, sizeof(d));
+  k.op = op;
+  k.sms = sms;
+  return k.p = make_plan(d, op, sms);
+}
+
 // ---- launches --------------------------------------------------------------------
 
 #define RET(e)                               \
@@ -272,6 +295,21 @@ int map_type() {
          : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
+// Where waits that gave up are counted, on the current device.
+cudaError_t fault_count(unsigned int** p) {
+  static std::atomic<unsigned int*> kept[64];
+  int device = 0;
+  RET(cudaGetDevice(&device));
+  *p = device < 64 ? kept[device].load() : nullptr;
+  if (*p) return cudaSuccess;
+  if (!(*p = ns_fault_count())) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? cudaErrorUnknown : e;
+  }
+  if (device < 64) kept[device].store(*p);
+  return cudaSuccess;
+}
+
 // The attribute that lets a launch begin while the one before runs.
 cudaLaunchAttribute early_launch() {
   cudaLaunchAttribute at = {};
@@ -286,8 +324,7 @@ cudaError_t launch_gemm(GemmArgs& a, Order order, cudaStream_t s) {
   const bool hook = wt::wait_hook_on();
   a.wait = hook ? 1ll << 20 : kWaitCycles;
   a.hold = hook;
-  a.faults = ns_fault_count();
-  if (!a.faults) return cudaGetLastError();
+  RET(fault_count(&a.faults));
   const void* f = (const void*)gated_gemm<EPI, T, Q8, PAIR>;
   RET(wt::ensure_smem(f, kSmem));
   const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;

@@ -483,13 +483,14 @@ struct Staging {
   }
 };
 
-// Sends a staging tile to columns from c on and rows from `row` on.
-template <typename T>
-__device__ __forceinline__ void send(unsigned char* buf, const void* map, int c, int half, int row, int part) {
+// Sends a staging tile to columns from c on and rows from `row` on, of which `rows`
+// exist.  Without one it still closes a group, an empty one: who waits for all
+// groups but the last counts one for each tile.
+__device__ __forceinline__ void send(unsigned char* buf, const void* map, int c, int half, int row, int part, int rows = 32) {
   fence_async_shared();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    box_store(map, c, half, row, part, smem_addr(buf));
+    if (rows > 0) box_store(map, c, half, row, part, smem_addr(buf));
     bulk_commit();
   }
 }
@@ -610,9 +611,9 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         unsigned char* buf = st.next();
         put_row<TO>(buf, v);
         if (sizeof(TO) == 4 && a.partial) {  // rows and columns are padded to whole tiles
-          send<float>(buf, &a.o0, n0 + c, 0, t.split * a.partial_rows + m0, 0);
+          send(buf, &a.o0, n0 + c, 0, t.split * a.partial_rows + m0, 0);
         } else if (a.boxes & 1) {
-          if (left > 0) send<TO>(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0);
+          send(buf, second ? &a.o1 : &a.o0, n0 + c, 0, m, 0, left);
         } else {
           __syncwarp();
           copy_out<TO, false>(buf, (TO*)(second ? a.out2 : a.out) + (long long)m * a.ld + n0 + c, a.ld, left,
@@ -702,7 +703,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         }
         if constexpr (EPI == EPI_H) {
           if (a.boxes & 1) {
-            if (rows > 0) send<T>(buf, &a.o0, n0, 0, m0, 0);
+            send(buf, &a.o0, n0, 0, m0, 0, rows);
           } else {
             __syncwarp();
             copy_out<T, false>(buf, (T*)a.out + (long long)m0 * a.ld + n0, a.ld, rows, cols);
@@ -710,10 +711,10 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
           }
         } else if constexpr (sizeof(T) == 2) {
           unsigned char* to = st.base + kTileBytes;
-          if (rows > 0) send<T>(buf, &a.o0, n0, 0, m0, 0);
+          send(buf, &a.o0, n0, 0, m0, 0, rows);
 #pragma unroll
           for (int q = 0; q < 4; ++q) *staged(to, lane, q) = second[q];
-          if (rows > 0) send<T>(to, &a.o0, n0, 1, m0, 0);
+          send(to, &a.o0, n0, 1, m0, 0, rows);
         } else {
           __nv_bfloat16* p = (__nv_bfloat16*)a.p + (long long)m0 * 2 * a.Hp + n0;
           unsigned char* to = st.base + kTileBytes;

@@ -102,8 +102,9 @@ typedef enum { WTCONV_OP_GATED_FWD = 0, WTCONV_OP_GATED_BWD = 1, WTCONV_OP_GATED
 size_t wtconv_gated_workspace_size(const wtconv_gated_desc_t* desc, int op);
 
 /* h = act(x gate^T) * (x up^T).  Products of 16-bit operands are exact and
- * added in float32; those of float32 operands keep 24 bits (three bfloat16
- * parts each, six products).  An infinite or NaN value of a float32 operand
+ * added in float32, sixteen at a time by additions that truncate (up to 8 rows:
+ * that round); those of float32 operands keep 24 bits (three bfloat16 parts
+ * each, six products), and no more than 512 products in a row are added so.  An infinite or NaN value of a float32 operand
  * makes the results that it enters NaN or infinite. */
 wtconv_status_t wtconv_gated_fwd(const wtconv_gated_desc_t* desc, const void* x, const void* gate, const void* up,
                                  void* h, void* ws, size_t ws_bytes, void* stream);
@@ -152,8 +153,9 @@ wtconv_status_t wtconv_grad_norm(const wtconv_tensor_t* tensors, int count, floa
 
 /* The same norm, and every element times min(1, max_norm / (norm + eps)), in
  * place, rounded once; where that factor is 1 nothing is written.  A norm that
- * is infinite makes every finite element 0 and a NaN makes every element NaN,
- * as the factor says.  Tensors that overlap are refused. */
+ * is infinite makes every finite element 0 (with a max_norm that is infinite too,
+ * NaN) and a NaN makes every element NaN, as the factor says.  Tensors that
+ * overlap are refused. */
 wtconv_status_t wtconv_clip_grads(const wtconv_tensor_t* tensors, int count, float max_norm, float eps, float* norm,
                                   void* ws, size_t ws_bytes, void* stream);
 

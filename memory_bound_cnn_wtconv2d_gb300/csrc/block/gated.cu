@@ -276,15 +276,16 @@ cudaError_t make_map(CUtensorMap* m, int type, const void* p, long long cols, in
   wt::EncodeTiledFn fn = wt::encode_tiled();
   if (!fn) return cudaErrorNotSupported;
   const int es = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
-  if (halves == 1) half_ld = ld;
   if (rows == 1) ld = round_up(cols, 16 / es);
   if (parts == 1) part_ld = ld;
   const cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)halves, (cuuint64_t)rows, (cuuint64_t)parts};
-  const cuuint64_t strides[3] = {(cuuint64_t)((halves == 1 ? ld : half_ld) * es), (cuuint64_t)(ld * es), (cuuint64_t)(part_ld * es)};
+  const cuuint64_t strides[3] = {(cuuint64_t)((halves == 1 ? ld : half_ld) * es), (cuuint64_t)(ld * es),
+                                 (cuuint64_t)(part_ld * es)};
   const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / es), 1u, (cuuint32_t)box_rows, 1u};
   const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
   return fn(m, (CUtensorMapDataType)type, 4, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
@@ -467,8 +468,8 @@ cudaError_t sum_up(const Call& c, const GemmArgs& a, long long rows, long long s
   cudaLaunchAttribute at = early_launch();
   l.attrs = &at;
   l.numAttrs = 1;
-  return cudaLaunchKernelEx(&l, gated_sum<T>, (const float*)a.partial, a.splits, (long long)a.partial_rows, a.ld, rows, c.d.C, second,
-                            second_at, (T*)a.out, (T*)a.out2);
+  return cudaLaunchKernelEx(&l, gated_sum<T>, (const float*)a.partial, a.splits, (long long)a.partial_rows, a.ld, rows, c.d.C,
+                            second, second_at, (T*)a.out, (T*)a.out2);
 }
 
 template <int EPI, typename T>
@@ -490,7 +491,8 @@ cudaError_t product_sums(const Call& c, const GatedArgs& g, Order order) {
     a.partial = (float*)(c.ws + c.p.sum_at);
     a.partial_rows = a.tiles_m * t.rows;
     a.ld = round_up(d.C, 4);
-    RET(make_map(&a.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.partial, d.C, 1, 0, (long long)a.splits * a.partial_rows, a.ld, 1, 0, 32, 64));
+    RET(make_map(&a.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.partial, d.C, 1, 0, (long long)a.splits * a.partial_rows, a.ld, 1, 0,
+                 32, 64));
   } else if (at16(a.out, d.C, sizeof(T)) && (!dw || at16(a.out2, d.C, sizeof(T)))) {
     a.boxes = 1;
     const long long rows = dw ? d.H : d.M;

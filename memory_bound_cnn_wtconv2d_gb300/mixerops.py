@@ -132,7 +132,7 @@ def _cached(key, make):
 
 
 class _RmsLayout:
-    __slots__ = ("desc", "ref", "M", "C", "device", "rows", "contiguous", "ws")
+    __slots__ = ("desc", "ref", "M", "C", "device", "rows", "ws")
 
     def __init__(self, x, r, dy, eps, names):
         stride = _row_stride(x, names[0])
@@ -150,7 +150,6 @@ class _RmsLayout:
         self.rows = x.shape[:-1]
         self.M = math.prod(self.rows)
         self.device = x.device
-        self.contiguous = x.is_contiguous()
         self.desc = RmsDesc(self.M, self.C, _c.DTYPE_CODES[x.dtype], eps, stride, rs, ds)
         self.ref = ctypes.byref(self.desc)
         self.ws = 0

@@ -3,14 +3,15 @@
 //   n = (sum of all g^2)^1/2, g <- g min(1, limit / (n + eps))
 //
 // Bound by memory: the elements are read, and where the norm is above the
-// limit read and written again.  The list of tensors is cut into chunks of 64 KB,
+// limit read and written again.  The list of tensors is cut into chunks of 48 KB,
 // which the CTAs share out; the list itself comes as a kernel argument, so that a
 // call copies nothing and can be captured.  The second launch walks the chunks
 // from the last one back: what the first one read last is still in the L2.
 // Few CTAs of large chunks: each adds up all partial sums in the second launch, and has
-// its loads of a chunk under way together.  81 float32 tensors of 47 MB, clipped: 14.6 us on
+// its loads of a chunk under way together.  81 float32 tensors of 47 MB, clipped: 15.2 us on
 // the GPU (of inputs that the L2 partly holds; 16 KB and four CTAs an SM 20, 32 KB and three 16.7);
-// 12 bfloat16 matrices of 277 MB below the limit 49 us (5.8 TB/s; 58, 49.6).
+// 12 bfloat16 matrices of 277 MB below the limit 48.8 us (5.8 TB/s; 58, 49.6; 64 KB and
+// two 55, whose loads and sums no longer fit the registers).
 #include "block_device.cuh"
 #include "mixer_launch.h"
 #include "tc_device.cuh"
@@ -20,9 +21,9 @@ namespace wtb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunkBytes = 65536;
+constexpr int kChunkBytes = 49152;
 constexpr int kMost = 512;   // tensors of one launch
-constexpr int kCtas = 2;     // an SM: 128 KB in flight
+constexpr int kCtas = 2;     // an SM: 96 KB in flight
 constexpr int kHalves = 2;   // of a chunk that is scaled
 constexpr int kParts = 1024; // partial sums of one launch, at most
 

@@ -125,9 +125,10 @@ wtconv_status_t wtconv_muon_step(const wtconv_ns_desc_t* desc, void* const* weig
                                  long long m_ld, float mu, int nesterov, float decay, float rate, void* ws,
                                  size_t ws_bytes, void* stream);
 
-/* In-kernel waits of the matrix operators that gave up (after about a second)
- * since the previous call on the current device (0 in normal operation), then
- * resets the count; see wtconv_device_faults.  Synchronises the current
+/* In-kernel waits of the matrix operators, and of the gated product (see
+ * wtconv_mixer.h), that gave up (after about a second) since the previous call
+ * on the current device (0 in normal operation), then resets the count; see
+ * wtconv_device_faults.  Synchronises the current
  * device.  After such a wait the kernel leaves early, the device stays
  * usable, and no matrix of that call gets a result: wtconv_orthogonalize
  * writes NaN, wtconv_muon_step leaves the weights as they are (the momentum

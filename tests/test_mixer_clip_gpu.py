@@ -1,8 +1,9 @@
 """The global gradient norm and clipping by it, against float64.
 
-Tolerances, derived before any run.  Squares of a few values are added in
-float32 (a handful of roundings, 2^-24 relative each) and carried on in
-float64; the root halves a relative error and is rounded once: 1e-6.  A clipped
+Tolerances, derived before any run.  Squares of a few values (24 in a row at
+most) are added in float32 (roundings of 2^-24 relative each, half of them on
+average) and carried on in float64; the root halves a relative error and is
+rounded once: 1e-6.  A clipped
 element is one float32 product with a factor of that error and one rounding.
 """
 import math

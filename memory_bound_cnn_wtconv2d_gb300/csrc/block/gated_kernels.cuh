@@ -181,7 +181,8 @@ __device__ __forceinline__ void drain(const GemmArgs& a, uint64_t* bar, uint32_t
   }
 }
 
-// Copies that nobody waits for after a wait gave up land in a fraction of this time.
+// Copies and arrivals that nobody waits for after a wait gave up land in a fraction of
+// this time.
 __device__ __forceinline__ void linger(const GemmArgs& a) {
   const long long t0 = clock64();
   while (clock64() - t0 < a.wait) {
@@ -283,9 +284,13 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
   if (w.rank == 0) {
     if (a.resident && w.first < items) drain(a, &sh.b_full, 0);
     for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
-  } else if (!ok || sh.dead) {
-    linger(a);  // the first CTA's barriers say nothing of copies that it did not ask for itself
   }
+  // the MMAs' last arrivals at `empty`, a pair's at both CTAs' barriers
+  for (int s = 0; ok && !sh.dead && s < a.stages && s < issued; ++s)
+    drain(a, &sh.empty[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
+  // not all of them come, and the first CTA's barriers say nothing of copies that it did
+  // not ask for itself
+  if (!ok || sh.dead) linger(a);
 }
 
 // The MMAs, by a CTA's second warp; a pair's by its first CTA's.
@@ -352,10 +357,7 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
       if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
     }
   }
-  if (elect_one()) {
-    commit(smem_addr(&sh.drain));
-    drain(a, &sh.drain, 0);
-  }
+  if (elect_one()) commit(smem_addr(&sh.drain));
   __syncwarp();
 }
 
@@ -794,6 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
+  // A pair's last commit arrives at both CTAs' barriers: each waits for its own, from
+  // here on, where the products have been read, so that the limit counts from there.
+  if (warp == 1) drain(a, &sh.drain, 0);
   if constexpr (PAIR) cluster_meet();  // the other CTA's MMAs, copies and arrivals touch this one
   tc_fence_after();
   if (warp == 1) {

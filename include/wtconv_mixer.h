@@ -132,7 +132,14 @@ wtconv_status_t wtconv_gated_bwd(const wtconv_gated_desc_t* desc, const void* dh
 
 /* Waits inside the gated kernels are bounded (about a second).  After one that
  * gave up the outputs that it held up are NaN, the device stays usable, and
- * the wait counts in wtconv_block_device_faults(). */
+ * the wait counts in wtconv_block_device_faults().  wtconv_test_copy_timeout
+ * makes the first wait for operands of every product run out. */
+
+/* Test support, off by default: with enable nonzero, every later backward on
+ * any thread lets the waits for its first copies of dh run out, where TMA brings
+ * them (dh on a 16-byte boundary, its row distance a multiple of 16 bytes);
+ * enable = 0 restores normal operation. */
+void wtconv_test_dh_timeout(int enable);
 
 /* One tensor of a list: numel elements of dtype, contiguous. */
 typedef struct {

@@ -311,6 +311,8 @@ cudaError_t fault_count(unsigned int** p) {
   return cudaSuccess;
 }
 
+std::atomic<bool> dh_hook{false};  // wtconv_test_dh_timeout
+
 // The attribute that lets a launch begin while the one before runs.
 cudaLaunchAttribute early_launch() {
   cudaLaunchAttribute at = {};
@@ -322,9 +324,8 @@ cudaLaunchAttribute early_launch() {
 template <int EPI, typename T, bool Q8, bool PAIR>
 cudaError_t launch_gemm(GemmArgs& a, Order order, cudaStream_t s) {
   a.order = order;
-  const bool hook = wt::wait_hook_on();
-  a.wait = hook ? 1ll << 20 : kWaitCycles;
-  a.hold = hook;
+  a.hold = wt::wait_hook_on() ? HOLD_FIRST : EPI == EPI_P && dh_hook ? HOLD_DH : HOLD_NONE;
+  a.wait = a.hold ? 1ll << 20 : kWaitCycles;
   RET(fault_count(&a.faults));
   const void* f = (const void*)gated_gemm<EPI, T, Q8, PAIR>;
   RET(wt::ensure_smem(f, kSmem));
@@ -543,6 +544,8 @@ cudaError_t backward(Call& c, const GatedArgs& g) {
 }
 
 }  // namespace
+
+void gated_hold_dh(bool on) { dh_hook = on; }
 
 size_t gated_workspace(const wtconv_gated_desc_t& d, int op) {
   return op != WTCONV_OP_GATED_BWD && d.M <= kGatedRows ? 0 : plan_of(d, op).bytes;

@@ -83,6 +83,10 @@ __device__ __forceinline__ int divide(int n, const Divisor& d) {
 // and waits for it at its end, so that who waits for this one waits for both.
 enum Order { AFTER, EARLY, BESIDE };
 
+// Which wait a test makes run out: none, that for a product's first k block, or each
+// warp's for its first dh.
+enum Hold { HOLD_NONE, HOLD_FIRST, HOLD_DH };
+
 struct GemmArgs {
   CUtensorMap a, b0, b1;  // operands: (column, 0 or which half, row, part)
   CUtensorMap o0, o1, dh_map;  // results and dh, in staging tiles
@@ -115,7 +119,7 @@ struct GemmArgs {
   float* partial;         // splits: sums of each, [split][rows][ld]
   int partial_rows;
   long long wait;
-  int hold;
+  int hold;               // a Hold
   unsigned int* faults;
   int order;              // an Order
 };
@@ -240,7 +244,7 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
         if (!ok) break;
         const uint32_t full = there + stage * 8, to = first + stage * bytes, tb = to + kABytes;
         // held: more than comes
-        const uint32_t expect = (PAIR ? 2 : 1) * bytes + (a.hold && issued == 0 ? 16 : 0);
+        const uint32_t expect = (PAIR ? 2 : 1) * bytes + (a.hold == HOLD_FIRST && issued == 0 ? 16 : 0);
         if constexpr (EPI == EPI_H || EPI == EPI_P) {
           const int c = kb * kBlock;
           if (elect_one()) {
@@ -543,7 +547,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
           if (a.boxes & 2) {
             if (lane == 0) {
               const uint32_t bar = smem_addr(&sh.dh[warp][asked & 1]);
-              mbar_expect(bar, kTileBytes);
+              mbar_expect(bar, kTileBytes + (a.hold == HOLD_DH && asked == 0 ? 16 : 0));
               box_load(smem_addr(buf), &a.dh_map, n0, 0, t.m * a.rows + warp_row, 0, bar);
             }
           } else {
@@ -603,7 +607,7 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
         }
         release();
       }
-      if (!got) {
+      if (kSums && !got) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) no_result(kept[j]);
       }
@@ -684,10 +688,10 @@ __device__ __forceinline__ void epilogue(Shared& sh, const GemmArgs& a, unsigned
               release();
               held = false;
             }
-            if (!got) {
-              no_result(g);
-              no_result(u);
-            }
+          }
+          if (!got) {  // the sums, or this stretch's dh
+            no_result(g);
+            no_result(u);
           }
           if constexpr (Q8) {
             const float xs = lane < rows ? a.x_scale[m0 + lane] : 0.f;

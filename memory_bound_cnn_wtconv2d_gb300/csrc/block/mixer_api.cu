@@ -296,6 +296,8 @@ wtconv_status_t wtconv_gated_bwd(const wtconv_gated_desc_t* d, const void* dh, c
   }
 }
 
+void wtconv_test_dh_timeout(int enable) { wtb::gated_hold_dh(enable != 0); }
+
 size_t wtconv_clip_workspace_size(int count) { return count < 0 ? 0 : wtb::clip_workspace(count); }
 
 wtconv_status_t wtconv_grad_norm(const wtconv_tensor_t* t, int count, float* norm, void* ws, size_t ws_bytes,

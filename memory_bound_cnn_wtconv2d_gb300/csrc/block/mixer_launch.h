@@ -38,6 +38,7 @@ cudaError_t gated_rows_launch(const wtconv_gated_desc_t& d, const GatedArgs& a, 
 size_t gated_workspace(const wtconv_gated_desc_t& d, int op);
 cudaError_t gated_launch_fwd(const wtconv_gated_desc_t& d, const GatedArgs& a, bool q8, void* ws, cudaStream_t s);
 cudaError_t gated_launch_bwd(const wtconv_gated_desc_t& d, const GatedArgs& a, void* ws, cudaStream_t s);
+void gated_hold_dh(bool on);
 
 // Gradient norm.
 size_t clip_workspace(int count);

@@ -26,7 +26,8 @@ E4M3 = torch.float8_e4m3fn
 # entry points declared in include/wtconv_mixer.h
 EXPORTS = ("wtconv_rms_norm_fwd", "wtconv_rms_norm_q8", "wtconv_quantize_rows", "wtconv_rms_workspace_size",
            "wtconv_rms_norm_bwd", "wtconv_gated_workspace_size", "wtconv_gated_fwd", "wtconv_gated_q8",
-           "wtconv_gated_bwd", "wtconv_clip_workspace_size", "wtconv_grad_norm", "wtconv_clip_grads")
+           "wtconv_gated_bwd", "wtconv_test_dh_timeout", "wtconv_clip_workspace_size", "wtconv_grad_norm",
+           "wtconv_clip_grads")
 
 
 class RmsDesc(ctypes.Structure):
@@ -63,6 +64,7 @@ def lib() -> ctypes.CDLL:
                 ("wtconv_gated_fwd", i, [gd, vp, vp, vp, vp, vp, sz, vp]),
                 ("wtconv_gated_q8", i, [gd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
                 ("wtconv_gated_bwd", i, [gd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                ("wtconv_test_dh_timeout", None, [i]),
                 ("wtconv_clip_workspace_size", sz, [i]),
                 ("wtconv_grad_norm", i, [td, i, vp, vp, sz, vp]),
                 ("wtconv_clip_grads", i, [td, i, f, f, vp, vp, sz, vp])):
@@ -417,6 +419,12 @@ def wtconv_gated_bwd(dh, x, gate, up, activation="silu", dx=None, dgate=None, du
         if status:
             _c._check(status)
     return dx, dgate, dup
+
+
+def wtconv_test_dh_timeout(enable: bool) -> None:
+    """Test support: while on, a backward's waits for its first copies of dh run out
+    (see include/wtconv_mixer.h); off restores normal operation."""
+    lib().wtconv_test_dh_timeout(1 if enable else 0)
 
 
 def _dense(t):

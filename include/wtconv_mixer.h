@@ -125,7 +125,9 @@ wtconv_status_t wtconv_gated_q8(const wtconv_gated_desc_t* desc, const void* x, 
  * du are held in desc->dtype between the products (float32: in 24 bits), as
  * the gradient of g and u would be by a chain of products in that type: in
  * float16, values beyond 65504 there are infinite.  Sums over rows are made in
- * a fixed order.  M = 0: dgate and dup are 0. */
+ * a fixed order.  Of 16-bit operands at most 16384 rows (dx: hidden units) are
+ * added up by additions that truncate, as in the forward; such sums are added
+ * by additions that round.  M = 0: dgate and dup are 0. */
 wtconv_status_t wtconv_gated_bwd(const wtconv_gated_desc_t* desc, const void* dh, const void* x, const void* gate,
                                  const void* up, void* dx, void* dgate, void* dup, void* ws, size_t ws_bytes,
                                  void* stream);

@@ -77,7 +77,7 @@ gated_sum(const float* part, int splits, long long part_rows, long long ld, long
     // rows from `second` on are of the second matrix, whose sums begin at row second_at
     const float* p = part + (row < second ? row : row - second + second_at) * ld + col;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < splits; ++k) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p + k * part_rows * ld));
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
@@ -163,9 +163,19 @@ Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool gra
   return best;
 }
 
+// The longest sum of 16-bit operands that stays in TMEM, in k blocks of 64.  Adding
+// sixteen products there cuts each off below 2^-25 of the largest term or the sum so
+// far, and the result below 2^-23: 5 * 2^-23 of the sum at most, always towards zero.
+// Over the 1024 additions of 256 blocks, while the sum grows to what it comes to, that is
+// 2^-11.7 of it at most (terms of one sign; 2^-13.4 measured), less than the rounding
+// to float16 that follows.  Without a bound sums over 2^24 rows were off by 2.8e-3.  It
+// costs nothing up to 800,000 rows and 4 to 6 % of the backward beyond (1048576 x 64 ->
+// 512: 1242 us without, 1309).
+constexpr long long kMostBlocks = 256;
+
 // Sums alone: M rows (of each of `halves` matrices) of N columns over k blocks; few
 // tiles share out k, at least four blocks each, and a second launch adds their sums
-// up.
+// up.  float32 operands' sums leave TMEM sooner in any case.
 Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products, int sms) {
   Tiles best = {};
   double least = 0;
@@ -173,9 +183,11 @@ Tiles plan_sums(long long M, int halves, int N, long long kblocks, int products,
     for (int n = pair ? 128 : 64; n <= (pair && products == 1 ? 512 : 256); n += pair ? 128 : 64) {
       const int tn = (N + n - 1) / n;
       if (best.n && best.pair == pair && n - (pair ? 128 : 64) >= N) break;
-      for (int want = 1; want <= 64; want += want < 8 ? 1 : want / 4) {
+      const long long least_splits = products == 1 ? (kblocks + kMostBlocks - 1) / kMostBlocks : 1;
+      for (long long want = 1; want <= 64 || want <= 2 * least_splits; want += want < 8 ? 1 : want / 4) {
+        if (want < least_splits) continue;
         const long long each = (kblocks + want - 1) / want;
-        if (want > 1 && each < 4) break;
+        if (want > least_splits && each < 4) break;
         const Tiles t = tiles_of(pair, n, tn, (int)((kblocks + each - 1) / each), (int)each, sms);
         const long long tm = halves * ((M + t.rows - 1) / t.rows);
         double c = clocks(tm * tn * t.splits, t, sms, (double)each * products, 400 + 8. * n);

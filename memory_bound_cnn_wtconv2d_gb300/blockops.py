@@ -164,6 +164,7 @@ _LAYOUTS = {}
 
 
 def _gn_layout(x, dy, num_groups, eps, activation):
+    eps = float(eps)  # a tensor would be found again by its identity, whatever it holds by then
     try:
         # with the type: 4.0 and 4 are equal, but only one of them is taken
         key = (x.shape, x.stride(), x.dtype, x.device, num_groups, type(num_groups), eps, activation,
@@ -393,8 +394,10 @@ _NS_DESCS = {}
 
 
 def _ns_desc(s, count, steps, coefficients, eps):
+    eps = float(eps)
     try:
-        key = (count, s.m, s.n, s.dtype, s.device, steps, type(steps), tuple(coefficients), eps)
+        coefficients = tuple(float(v) for v in coefficients)
+        key = (count, s.m, s.n, s.dtype, s.device, steps, type(steps), coefficients, eps)
         got = _NS_DESCS.get(key)
     except TypeError:
         key = got = None

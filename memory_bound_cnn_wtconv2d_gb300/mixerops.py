@@ -161,6 +161,8 @@ class _RmsLayout:
 
 
 def _rms_layout(x, r, dy, eps, names):
+    eps = float(eps)  # a tensor would be found again by its identity, whatever it holds by then
+
     def make():
         return _RmsLayout(x, r, dy, eps, names)
     try:

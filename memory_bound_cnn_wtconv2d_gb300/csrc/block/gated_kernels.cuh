@@ -285,16 +285,20 @@ __device__ __forceinline__ void produce(Shared& sh, const GemmArgs& a, uint32_t 
       if (++q == products) q = 0, from = to_kb;
     }
   }
+  // A stage's last turn was in this lap of the ring, or in the one before.
+  auto last = [&](uint32_t s) { return s < stage ? phase ^ 1 : phase; };
+  const uint32_t used = issued < a.stages ? (uint32_t)issued : (uint32_t)a.stages;
   if (w.rank == 0) {
     if (a.resident && w.first < items) drain(a, &sh.b_full, 0);
-    for (int s = 0; s < a.stages && s < issued; ++s) drain(a, &sh.full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
+    for (uint32_t s = 0; s < used; ++s) drain(a, &sh.full[s], last(s));
   }
   // the MMAs' last arrivals at `empty`, a pair's at both CTAs' barriers
-  for (int s = 0; ok && !sh.dead && s < a.stages && s < issued; ++s)
-    drain(a, &sh.empty[s], (uint32_t)((issued - 1 - s) / a.stages) & 1);
+  for (uint32_t s = 0; ok && !sh.dead && s < used; ++s) drain(a, &sh.empty[s], last(s));
   // not all of them come, and the first CTA's barriers say nothing of copies that it did
   // not ask for itself
   if (!ok || sh.dead) linger(a);
+  // the last commit, of whose arrivals the MMAs' warp waits for the first CTA's
+  if (w.rank) drain(a, &sh.drain, 0);
 }
 
 // The MMAs, by a CTA's second warp; a pair's by its first CTA's.
@@ -361,7 +365,10 @@ __device__ __forceinline__ void multiply(Shared& sh, const GemmArgs& a, uint32_t
       if (++acc == (uint32_t)a.buffers) acc = 0, acc_phase ^= 1;
     }
   }
-  if (elect_one()) commit(smem_addr(&sh.drain));
+  if (elect_one()) {
+    commit(smem_addr(&sh.drain));
+    drain(a, &sh.drain, 0);
+  }
   __syncwarp();
 }
 
@@ -800,9 +807,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
-  // A pair's last commit arrives at both CTAs' barriers: each waits for its own, from
-  // here on, where the products have been read, so that the limit counts from there.
-  if (warp == 1) drain(a, &sh.drain, 0);
   if constexpr (PAIR) cluster_meet();  // the other CTA's MMAs, copies and arrivals touch this one
   tc_fence_after();
   if (warp == 1) {

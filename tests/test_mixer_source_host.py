@@ -36,9 +36,11 @@ def test_every_barrier_that_a_commit_arrives_at_is_waited_for_in_both_ctas():
     end = end[end.index("}") + 1:]  # behind what is the first CTA's alone
     assert re.search(r"for \([^)]*\)\s*drain\(a, &sh\.empty\[s\]", end)
     assert "else" not in end and re.search(r"if \(!ok \|\| sh\.dead\) linger\(a\);", end)
+    # the last commit: the second CTA's by that warp too, the first one's by the MMAs' warp
+    assert re.search(r"linger\(a\);\s*if \(w\.rank\) drain\(a, &sh\.drain, 0\);\s*$", end)
+    assert re.search(r"commit\(smem_addr\(&sh\.drain\)\);\s*drain\(a, &sh\.drain, 0\);\s*\}\s*__syncwarp\(\);\s*$", multiply)
     # the tiles: by every epilogue warp
     assert "wait(sh, a, &sh.acc_full[acc], phase)" in body(src, "epilogue")
-    # the last commit: between the roles and the pair's parting
+    # and the two meet before either leaves
     kernel = body(src, "gated_gemm")
-    last = kernel[kernel.index("epilogue<"):kernel.rindex("cluster_meet()")]
-    assert re.search(r"__syncthreads\(\);\s*if \(warp == 1\) drain\(a, &sh\.drain, 0\);\s*if constexpr \(PAIR\)", last)
+    assert re.search(r"__syncthreads\(\);\s*if constexpr \(PAIR\) cluster_meet\(\);", kernel[kernel.index("epilogue<"):])

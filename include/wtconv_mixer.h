@@ -102,17 +102,22 @@ typedef enum { WTCONV_OP_GATED_FWD = 0, WTCONV_OP_GATED_BWD = 1, WTCONV_OP_GATED
 size_t wtconv_gated_workspace_size(const wtconv_gated_desc_t* desc, int op);
 
 /* h = act(x gate^T) * (x up^T).  Products of 16-bit operands are exact and
- * added in float32, sixteen at a time by additions that truncate (up to 8 rows:
- * that round); those of float32 operands keep 24 bits (three bfloat16 parts
- * each, six products), and no more than 512 products in a row are added so.  An infinite or NaN value of a float32 operand
- * makes the results that it enters NaN or infinite. */
+ * added in float32, sixteen at a time by additions that truncate, each of which
+ * loses less than 5 * 2^-23 of its largest term or the sum so far (up to 8 rows:
+ * by additions that round); C / 16 of them follow one another.  Those of float32
+ * operands keep 24 bits (three bfloat16 parts each, six products), and after
+ * 512 values of C (six products each) a sum is carried on by additions that
+ * round.  An infinite or NaN value of a float32 operand makes the results that
+ * it enters NaN or infinite. */
 wtconv_status_t wtconv_gated_fwd(const wtconv_gated_desc_t* desc, const void* x, const void* gate, const void* up,
                                  void* h, void* ws, size_t ws_bytes, void* stream);
 
 /* The same from 8-bit operands (e4m3): x[M, C] with x_scale[M], gate and up
  * [H, C] with gate_scale[H], up_scale[H]; the scales are float32.  h in
  * desc->dtype.  C and the strides are multiples of 16, the 8-bit pointers
- * 16-byte aligned. */
+ * 16-byte aligned.  Products are exact and added 32 at a time by additions that
+ * truncate (each loses less than 9 * 2^-23, as above): all C of them for a 16-bit
+ * h, 1024 in a row for a float32 one. */
 wtconv_status_t wtconv_gated_q8(const wtconv_gated_desc_t* desc, const void* x, const float* x_scale,
                                 const void* gate, const float* gate_scale, const void* up, const float* up_scale,
                                 void* h, void* ws, size_t ws_bytes, void* stream);
@@ -124,7 +129,11 @@ wtconv_status_t wtconv_gated_q8(const wtconv_gated_desc_t* desc, const void* x, 
  * each contiguous in desc->dtype; dx, or dgate and dup, may be NULL.  dg and
  * du are held in desc->dtype between the products (float32: in 24 bits), as
  * the gradient of g and u would be by a chain of products in that type: in
- * float16, values beyond 65504 there are infinite.  Sums over rows are made in
+ * float16, values beyond 65504 there are infinite and those below 2^-25 zero
+ * (below 2^-14 they keep fewer bits), even where dx would be neither.  The
+ * workspace holds them: 4 M Hp bytes (float32 12 M Hp), Hp being H to a multiple
+ * of 64, beside copies of operands (float32: 6 bytes for each of their elements)
+ * and partial sums.  Sums over rows are made in
  * a fixed order.  Of 16-bit operands at most 16384 rows (dx: hidden units) are
  * added up by additions that truncate, as in the forward; such sums are added
  * by additions that round.  M = 0: dgate and dup are 0. */

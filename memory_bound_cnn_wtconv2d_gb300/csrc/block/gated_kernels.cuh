@@ -18,15 +18,16 @@
 // float32 operands come as three bfloat16 parts (24 bits); six of their nine
 // products count (the others lie below 2^-25), least first, since the tensor
 // core's additions truncate; for the same reason their sums leave TMEM after every
-// eight k blocks.
+// eight k blocks, and those of 16-bit operands in dx and dW after 256 (kMostBlocks in
+// gated.cu).
 //
 // What bounds it, and what it takes (GPU time in a captured graph):
 //   8192 x 2048 -> 5632   the MMAs, at the clock that the power limit leaves: bfloat16
-//       forward 192 us (1.97 PFLOP/s), backward 643 us (1.76), e4m3 forward 108 us (3.5)
-//   25088 x 384 -> 1024   bfloat16 backward 122 us: P 50 us by its epilogue (tensor cores
+//       forward 192 us (1.97 PFLOP/s), backward 650 us (1.74), e4m3 forward 108 us (3.5)
+//   25088 x 384 -> 1024   bfloat16 backward 126 us: P 50 us by its epilogue (tensor cores
 //       32 % busy), dx 43 us by two rounds of tiles that fill 64 % of the SMs and
 //       by operands from the L2, dW, which fills the gaps, 33 us
-//   200704 x 96 -> 256    bfloat16 forward 39 us: 16.5 instructions an element of the
+//   200704 x 96 -> 256    bfloat16 forward 40 us: 16.5 instructions an element of the
 //       epilogue, two special functions among them (issue slots 60 % busy, 37 % of DRAM's rate)
 #pragma once
 

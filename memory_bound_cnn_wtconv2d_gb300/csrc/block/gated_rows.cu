@@ -3,8 +3,17 @@
 // makes a hidden unit for all rows: its lanes read the two weight rows in 16-byte
 // pieces, x comes from the caches, and sums are float32 (products of operands as
 // they are: no parts).  On the tensor cores the same call keeps as many SMs busy as
-// there are tiles of hidden units, and each waits for its own copies' latency
-// (7.8 us on the GPU against 2.8).
+// there are tiles of hidden units, and each waits for its own copies' latency.
+// Rows are given by kGatedRows: with eight of them the two forms meet at the sizes that a
+// pooled image brings.  GPU time of a call, here and on the tensor cores, us (the weights
+// of four calls in turn, partly from the L2):
+//                      float16                    float32      e4m3
+//   rows               1          4        8      8            8
+//   96 -> 256     1.5, 4.7   2.5, 4.9   3.5, 4.9    2.3, 9.9   3.9, 5.3
+//   768 -> 2048   2.4, 8.0   4.8, 8.1   7.7, 7.9    6.2, 32    8.9, 7.5
+//   2048 -> 5632  10.1, 23   20, 20     29, 19      45, 111    21, 14
+// Each row reads x anew from the L1, which bounds five to eight rows of wide matrices
+// of 16 and 8 bits: there the tensor cores would be up to 1.5 times faster.
 #include <cuda_fp8.h>
 
 #include "block_device.cuh"

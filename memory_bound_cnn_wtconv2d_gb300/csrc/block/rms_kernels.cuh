@@ -10,8 +10,9 @@
 // of a warp for short rows (several rows a warp, no barrier), a CTA of 64 to 256
 // threads for long ones.  Values a lane and lanes are chosen so that few lanes
 // idle (96 channels of 16 bits: 4 lanes of three 16-byte accesses).  Rows that no
-// CTA holds (above 8192 channels, backward 6144) are read twice or three times,
-// the later times from the caches.
+// CTA holds are read twice or three times, the later times from the caches: those
+// above 8192 channels, in the backward above 6144 (24 values a lane; float32: 4096, of
+// four 16-byte accesses), and above 2048 where they are read value by value.
 //
 // Rows of 90 or 1001 channels begin between two 16-byte boundaries, and not all at
 // the same place.  They are taken from the boundary before on: a lane's pieces are
@@ -26,7 +27,9 @@
 //
 // GPU time and the rate of the bytes that count: 200704 x 96 bfloat16 forward 26 us
 // (6.0 TB/s), 16384 x 2048 float16 to 8 bits 46 us (5.1), 200704 x 192 bfloat16 backward
-// 56 us (5.5), 1961 x 90 float32 forward 3.4 us (latency).
+// 56 us (5.5), 1961 x 90 float32 forward 3.4 us (latency).  Rows read again: 2048 x 16384
+// bfloat16 forward 62 us (4.3 TB/s), backward 182 (1.5); 8192 x 4100 float32 backward 149
+// (3.6), where 4096 channels take 96 (5.6).
 #pragma once
 
 #include <cuda_fp8.h>

@@ -77,7 +77,7 @@ gated_sum(const float* part, int splits, long long part_rows, long long ld, long
     // rows from `second` on are of the second matrix, whose sums begin at row second_at
     const float* p = part + (row < second ? row : row - second + second_at) * ld + col;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < splits; ++k) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p + k * part_rows * ld));
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
@@ -170,7 +170,7 @@ Tiles plan_forward(const wtconv_gated_desc_t& d, int products, bool q8, bool gra
 // 2^-11.7 of it at most (terms of one sign; 2^-13.4 measured), less than the rounding
 // to float16 that follows.  Without a bound sums over 2^24 rows were off by 2.8e-3.  It
 // costs nothing up to 800,000 rows and 4 to 6 % of the backward beyond (1048576 x 64 ->
-// 512: 1242 us without, 1309).
+// 512: 1242 us without, 1315).
 constexpr long long kMostBlocks = 256;
 
 // Sums alone: M rows (of each of `halves` matrices) of N columns over k blocks; few

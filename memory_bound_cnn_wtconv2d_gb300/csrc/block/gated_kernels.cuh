@@ -27,7 +27,7 @@
 //   25088 x 384 -> 1024   bfloat16 backward 126 us: P 50 us by its epilogue (tensor cores
 //       32 % busy), dx 43 us by two rounds of tiles that fill 64 % of the SMs and
 //       by operands from the L2, dW, which fills the gaps, 33 us
-//   200704 x 96 -> 256    bfloat16 forward 40 us: 16.5 instructions an element of the
+//   200704 x 96 -> 256    bfloat16 forward 40 us: 16.7 instructions an element of the
 //       epilogue, two special functions among them (issue slots 60 % busy, 37 % of DRAM's rate)
 #pragma once
 

@@ -133,10 +133,10 @@ wtconv_status_t wtconv_gated_q8(const wtconv_gated_desc_t* desc, const void* x, 
  * (below 2^-14 they keep fewer bits), even where dx would be neither.  The
  * workspace holds them: 4 M Hp bytes (float32 12 M Hp), Hp being H to a multiple
  * of 64, beside copies of operands (float32: 6 bytes for each of their elements)
- * and partial sums.  Sums over rows are made in
- * a fixed order.  Of 16-bit operands at most 16384 products in a row (of as
- * many rows; dx: of dg and du of 8192 hidden units) are added by additions that
- * truncate, as in the forward, and what they come to by additions that round.  M = 0: dgate and dup are 0. */
+ * and partial sums.  Sums over rows are made in a fixed order.  Of 16-bit
+ * operands at most 16384 products in a row (of as many rows; dx: of dg and du of
+ * 8192 hidden units) are added by additions that truncate, as in the forward,
+ * and what they come to by additions that round.  M = 0: dgate and dup are 0. */
 wtconv_status_t wtconv_gated_bwd(const wtconv_gated_desc_t* desc, const void* dh, const void* x, const void* gate,
                                  const void* up, void* dx, void* dgate, void* dup, void* ws, size_t ws_bytes,
                                  void* stream);
